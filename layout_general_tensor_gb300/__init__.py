@@ -1,5 +1,7 @@
-"""Python binding of the any-layout GEMM C ABI (``include/gemm.h``) and the
-fp32 row reduction (``include/reduce.h``).
+"""Python binding of the any-layout GEMM C ABI (``include/gemm.h``), the fp32
+row reduction (``include/reduce.h``), the fused attention
+(``include/attention.h``) and the operators of a serving attention layer
+(``include/attn_rope.h``, ``include/attn_prompt.h``, ``include/attn_cache.h``).
 
 Argument marshalling only: every function forwards to the entry point of the
 same name in ``_lib/libgemm.so``; all arithmetic runs in the library's CUDA
@@ -34,7 +36,10 @@ GEMM_BF16 = 1
 GEMM_INT4 = 2
 GEMM_F32 = 3
 
-# Every entry point include/gemm.h and include/reduce.h declare.
+ATTN_ROPE_HALF = 0
+ATTN_ROPE_INTERLEAVED = 1
+
+# Every entry point the headers under include/ declare.
 EXPORTS = (
     "gemm_create", "gemm_workspace_size", "gemm_query", "gemm_run", "gemm_run_static_scratch",
     "gemm_sync_status", "gemm_destroy",
@@ -42,6 +47,9 @@ EXPORTS = (
     "gemm_magic_divmod_device", "gemm_status_string", "gemm_int4_prepack_bytes", "gemm_int4_prepack",
     "reduce_rows_workspace_size", "reduce_rows_f32",
     "attn_create", "attn_run", "attn_sync_status", "attn_destroy",
+    "attn_rope_frequencies", "attn_rope_create", "attn_rope_run", "attn_rope_destroy",
+    "attn_prompt_create", "attn_prompt_run", "attn_prompt_sync_status", "attn_prompt_destroy",
+    "attn_cache_write", "attn_cache_read", "attn_cache_attend_workspace_size", "attn_cache_attend",
 )
 
 
@@ -63,6 +71,31 @@ class attn_desc_t(ctypes.Structure):
     ]
 
 
+class attn_rope_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("magnitude", ctypes.c_float),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("context", ctypes.c_double),
+        ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double),
+    ]
+
+
+class attn_prompt_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class attn_cache_t(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+        ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+    ]
+
+
 class gemm_info_t(ctypes.Structure):
     _fields_ = [
         ("split_k", ctypes.c_int32), ("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32),
@@ -79,7 +112,7 @@ def _load():
         raise ImportError(f"{LIB_PATH} is missing: build it with `python layout_general_tensor_gb300/build.py` "
                           "(there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
-    P = ctypes.c_void_p
+    P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     sig = {
         "gemm_create": (ctypes.c_int, [ctypes.POINTER(gemm_desc_t), ctypes.POINTER(P)]),
         "gemm_workspace_size": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_size_t)]),
@@ -108,6 +141,19 @@ def _load():
         "attn_run": (ctypes.c_int, [P, P, P, P, P, P]),
         "attn_sync_status": (ctypes.c_int, [P, P]),
         "attn_destroy": (ctypes.c_int, [P]),
+        "attn_rope_frequencies": (ctypes.c_int, [ctypes.POINTER(attn_rope_desc_t), P]),
+        "attn_rope_create": (ctypes.c_int, [ctypes.POINTER(attn_rope_desc_t), P, ctypes.POINTER(P)]),
+        "attn_rope_run": (ctypes.c_int, [P, P, I64, P, I64, P, P, P, I64, P, I64, P, I64, P]),
+        "attn_rope_destroy": (ctypes.c_int, [P]),
+        "attn_prompt_create": (ctypes.c_int, [ctypes.POINTER(attn_prompt_desc_t), ctypes.POINTER(P)]),
+        "attn_prompt_run": (ctypes.c_int, [P, P, I64, P, I64, P, I64, P, P, I32, I64, I64, P, I64, P]),
+        "attn_prompt_sync_status": (ctypes.c_int, [P, P]),
+        "attn_prompt_destroy": (ctypes.c_int, [P]),
+        "attn_cache_write": (ctypes.c_int, [ctypes.POINTER(attn_cache_t), P, I64, P, I64, P, I64, I32, P]),
+        "attn_cache_read": (ctypes.c_int, [ctypes.POINTER(attn_cache_t), P, I64, P, I64, P, I64, I32, P]),
+        "attn_cache_attend_workspace_size": (ctypes.c_int, [I32, I32, I32, I32, ctypes.POINTER(ctypes.c_size_t)]),
+        "attn_cache_attend": (ctypes.c_int, [ctypes.POINTER(attn_cache_t), P, I64, I32, P, I64, I32, P, I32,
+                                             ctypes.c_float, I32, P, I64, P, ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -383,3 +429,253 @@ class Attention:
             self.close()
         except Exception:
             pass
+
+
+def _torch_dtype(dtype):
+    import torch
+    return torch.bfloat16 if dtype == GEMM_BF16 else torch.float16
+
+
+def _rows(what, name, t, heads, head_dim, dtype, rows=None):
+    """Check a [rows][heads][head_dim] device tensor of 16-bit values whose
+    heads are contiguous; returns its row stride in elements."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{what}: {name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if t.dtype != _torch_dtype(dtype) or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or \
+            (rows is not None and shape[0] != rows):
+        raise ValueError(f"{what}: {name} must be [{'rows' if rows is None else rows}][{heads}][{head_dim}] of "
+                         f"{_torch_dtype(dtype)}, got {tuple(shape)} of {t.dtype}")
+    if t.numel() == 0 or shape[0] == 1:
+        if t.numel() and (stride[2] != 1 or (heads > 1 and stride[1] != head_dim)):
+            raise ValueError(f"{what}: the heads of {name} must be contiguous")
+        return heads * head_dim
+    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
+        raise ValueError(f"{what}: the heads of {name} must be contiguous")
+    if stride[0] < heads * head_dim:  # (0 would ask the library for its default)
+        raise ValueError(f"{what}: the rows of {name} overlap")
+    return stride[0]
+
+
+def _int32s(what, name, t, count):
+    """Check a contiguous device vector of `count` int32."""
+    import torch
+    if not getattr(t, "is_cuda", False) or t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != count or \
+            not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous CUDA vector of {count} int32")
+
+
+def _stream(stream):
+    import torch
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+
+
+def attn_rope_frequencies(desc: attn_rope_desc_t):
+    """The frequencies (radians a position) `desc` stands for, as a list."""
+    out = (ctypes.c_double * max(desc.rot_dim // 2, 1))()
+    _check(_lib.attn_rope_frequencies(ctypes.byref(desc), out), "attn_rope_frequencies")
+    return list(out)[: desc.rot_dim // 2]
+
+
+def attn_rope_create_status(desc: attn_rope_desc_t, frequencies=None):
+    """attn_rope_create returning (status, handle or None) without raising."""
+    h = ctypes.c_void_p()
+    f = None if frequencies is None else (ctypes.c_double * max(len(frequencies), 1))(*frequencies)
+    return _lib.attn_rope_create(ctypes.byref(desc), f, ctypes.byref(h)), h.value
+
+
+class QKNormRope:
+    """The RMS norm of every query and key head and its rotation by position,
+    in one pass over [token][head][head_dim] tensors, which may be slices of
+    one projection's output (include/attn_rope.h).  Without weights there is
+    no norm.  `frequencies` (rot_dim / 2 radians a position) takes the place
+    of base, factor, context, low_turns and high_turns."""
+
+    def __init__(self, q_heads, k_heads, head_dim, rot_dim=None, layout=ATTN_ROPE_HALF, dtype=GEMM_BF16, eps=1e-6,
+                 base=10000.0, factor=1.0, context=0.0, low_turns=0.0, high_turns=0.0, magnitude=1.0,
+                 frequencies=None):
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        self.plan = None
+        self.desc = attn_rope_desc_t(q_heads, k_heads, head_dim, rot_dim, layout, dtype, eps, magnitude, base, factor,
+                                     context, low_turns, high_turns)
+        if frequencies is not None and len(frequencies) != rot_dim // 2:
+            raise ValueError(f"QKNormRope: {rot_dim // 2} frequencies are wanted, got {len(frequencies)}")
+        st, h = attn_rope_create_status(self.desc, frequencies)
+        _check(st, "attn_rope_create")
+        self.plan = h
+
+    def run(self, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, stream=None):
+        """q_out, k_out: may be q and k themselves.  positions: int32."""
+        d, what = self.desc, "QKNormRope.run"
+        n = q.shape[0]
+        strides = [_rows(what, name, t, heads, d.head_dim, d.dtype, n)
+                   for name, t, heads in (("q", q, d.q_heads), ("k", k, d.k_heads), ("q_out", q_out, d.q_heads),
+                                          ("k_out", k_out, d.k_heads))]
+        _int32s(what, "positions", positions, n)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None and (not w.is_cuda or w.dtype != q.dtype or tuple(w.shape) != (d.head_dim,) or
+                                  not w.is_contiguous()):
+                raise ValueError(f"{what}: {name} must be a contiguous CUDA vector of {d.head_dim} {q.dtype}")
+        _check(_lib.attn_rope_run(self.plan, q.data_ptr() or None, strides[0], k.data_ptr() or None, strides[1],
+                                  q_weight.data_ptr() if q_weight is not None else None,
+                                  k_weight.data_ptr() if k_weight is not None else None,
+                                  positions.data_ptr() or None, n, q_out.data_ptr() or None, strides[2],
+                                  k_out.data_ptr() or None, strides[3], _stream(stream) or None), "attn_rope_run")
+
+    def close(self):
+        if self.plan:
+            _lib.attn_rope_destroy(self.plan)
+            self.plan = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def attn_prompt_create_status(desc: attn_prompt_desc_t):
+    """attn_prompt_create returning (status, handle or None) without raising."""
+    h = ctypes.c_void_p()
+    return _lib.attn_prompt_create(ctypes.byref(desc), ctypes.byref(h)), h.value
+
+
+class PromptAttention:
+    """Attention over packed sequences of different lengths, causal or not,
+    with grouped heads (include/attn_prompt.h), on [row][head][head_dim]
+    tensors and cumulative lengths (batch + 1 int32 on the device)."""
+
+    def __init__(self, q_heads, k_heads, head_dim, dtype=GEMM_BF16, causal=True, scale=0.0):
+        self.plan = None
+        self.desc = attn_prompt_desc_t(q_heads, k_heads, head_dim, dtype, int(causal), scale)
+        st, h = attn_prompt_create_status(self.desc)
+        _check(st, "attn_prompt_create")
+        self.plan = h
+
+    def run(self, q, k, v, cu_q, cu_k, out, stream=None):
+        d, what = self.desc, "PromptAttention.run"
+        nq, nk = q.shape[0], k.shape[0]
+        sq = _rows(what, "q", q, d.q_heads, d.head_dim, d.dtype)
+        so = _rows(what, "out", out, d.q_heads, d.head_dim, d.dtype, nq)
+        sk = _rows(what, "k", k, d.k_heads, d.head_dim, d.dtype)
+        sv = _rows(what, "v", v, d.k_heads, d.head_dim, d.dtype, nk)
+        _int32s(what, "cu_q", cu_q, cu_q.shape[0])
+        _int32s(what, "cu_k", cu_k, cu_q.shape[0])
+        if cu_q.shape[0] < 1:
+            raise ValueError(f"{what}: cu_q and cu_k hold batch + 1 values")
+        _check(_lib.attn_prompt_run(self.plan, q.data_ptr() or None, sq, k.data_ptr() or None, sk,
+                                    v.data_ptr() or None, sv, cu_q.data_ptr(), cu_k.data_ptr(), cu_q.shape[0] - 1, nq,
+                                    nk, out.data_ptr() or None, so, _stream(stream) or None), "attn_prompt_run")
+
+    def sync_status(self, stream=None) -> int:
+        return _lib.attn_prompt_sync_status(self.plan, _stream(stream) or None)
+
+    def close(self):
+        if self.plan:
+            _lib.attn_prompt_destroy(self.plan)
+            self.plan = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """A paged cache of keys and values in 8 bits (include/attn_cache.h), on
+    four uint8 tensors: codes [pages][k_heads][page_size][head_dim] and
+    exponents [pages][k_heads][page_size]."""
+
+    def __init__(self, k, v, k_exp, v_exp):
+        import torch
+        for name, t in (("k", k), ("v", v), ("k_exp", k_exp), ("v_exp", v_exp)):
+            if not getattr(t, "is_cuda", False) or t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError(f"KVCache: {name} must be a contiguous CUDA tensor of uint8")
+        if k.dim() != 4 or v.shape != k.shape or k_exp.shape != k.shape[:3] or v_exp.shape != k.shape[:3]:
+            raise ValueError("KVCache: codes are [pages][k_heads][page_size][head_dim], exponents one dimension less")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.pages, self.k_heads, self.page_size, self.head_dim = k.shape
+        self.c = attn_cache_t(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), self.pages,
+                              self.page_size, self.k_heads, self.head_dim)
+        self._ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, pages, page_size, k_heads, head_dim, device="cuda"):
+        import torch
+        made = [torch.zeros(pages, k_heads, page_size, head_dim, dtype=torch.uint8, device=device) for _ in range(2)]
+        made += [torch.zeros(pages, k_heads, page_size, dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(*made)
+
+    def _dtype(self, what, t):
+        import torch
+        if t.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"{what}: k and v must be float16 or bfloat16, got {t.dtype}")
+        return GEMM_BF16 if t.dtype == torch.bfloat16 else GEMM_F16
+
+    def write(self, k, v, slots, stream=None):
+        """Quantise [token][k_heads][head_dim] keys and values into their slots (int32; negative: left out)."""
+        what = "KVCache.write"
+        dtype, n = self._dtype(what, k), k.shape[0]
+        sk = _rows(what, "k", k, self.k_heads, self.head_dim, dtype)
+        sv = _rows(what, "v", v, self.k_heads, self.head_dim, dtype, n)
+        _int32s(what, "slots", slots, n)
+        _check(_lib.attn_cache_write(self._ref, k.data_ptr() or None, sk, v.data_ptr() or None, sv,
+                                     slots.data_ptr() or None, n, dtype, _stream(stream) or None), "attn_cache_write")
+
+    def read(self, slots, k, v, stream=None):
+        """The values of the slots into [token][k_heads][head_dim] tensors (zeros for a negative slot)."""
+        what = "KVCache.read"
+        dtype, n = self._dtype(what, k), k.shape[0]
+        sk = _rows(what, "k", k, self.k_heads, self.head_dim, dtype)
+        sv = _rows(what, "v", v, self.k_heads, self.head_dim, dtype, n)
+        _int32s(what, "slots", slots, n)
+        _check(_lib.attn_cache_read(self._ref, slots.data_ptr() or None, n, k.data_ptr() or None, sk,
+                                    v.data_ptr() or None, sv, dtype, _stream(stream) or None), "attn_cache_read")
+
+
+class CacheAttention:
+    """Attention of one query a sequence over a KVCache (include/attn_cache.h),
+    with its (zero-filled) device workspace for `batch` sequences; a larger batch
+    waits for the device and makes a larger one.  Runs that may be under way at the same time need objects of their own."""
+
+    def __init__(self, q_heads, k_heads, head_dim, page_size, dtype=GEMM_BF16, scale=0.0, batch=64):
+        self.q_heads, self.k_heads, self.head_dim, self.page_size = q_heads, k_heads, head_dim, page_size
+        self.dtype, self.scale = dtype, scale
+        self.workspace, self.ws_bytes, self.batch = None, 0, 0
+        self._grow(batch)
+
+    def _grow(self, batch):
+        import torch
+        n = ctypes.c_size_t()
+        _check(_lib.attn_cache_attend_workspace_size(self.q_heads, self.k_heads, self.head_dim, batch,
+                                                     ctypes.byref(n)), "attn_cache_attend_workspace_size")
+        # (the old one may be in use and the new one is used on any stream)
+        torch.cuda.synchronize()
+        self.workspace = torch.zeros(n.value, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        self.ws_bytes, self.batch = n.value, batch
+
+    def run(self, q, cache, page_table, lengths, out, stream=None):
+        """q, out: [batch][q_heads][head_dim]; page_table: [batch][pages a sequence] int32; lengths: batch int32."""
+        import torch
+        what = "CacheAttention.run"
+        n = q.shape[0]
+        if (cache.k_heads, cache.head_dim, cache.page_size) != (self.k_heads, self.head_dim, self.page_size):
+            raise ValueError(f"{what}: the cache has another shape than this was made for")
+        sq = _rows(what, "q", q, self.q_heads, self.head_dim, self.dtype)
+        so = _rows(what, "out", out, self.q_heads, self.head_dim, self.dtype, n)
+        _int32s(what, "lengths", lengths, n)
+        if not page_table.is_cuda or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+                page_table.shape[0] != n or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError(f"{what}: page_table must be a CUDA tensor [{n}][pages] of int32 with contiguous rows")
+        if n > self.batch:
+            self._grow(n)
+        most = page_table.shape[1]
+        pitch = page_table.stride(0) if n > 1 else most
+        if pitch < most:
+            raise ValueError(f"{what}: the rows of page_table overlap")
+        _check(_lib.attn_cache_attend(cache._ref, q.data_ptr() or None, sq, self.q_heads, page_table.data_ptr() or None,
+                                      pitch, most, lengths.data_ptr() or None, n, self.scale, self.dtype,
+                                      out.data_ptr() or None, so, self.workspace.data_ptr(), self.ws_bytes,
+                                      _stream(stream) or None), "attn_cache_attend")

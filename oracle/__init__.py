@@ -279,6 +279,107 @@ def attention_rows(heads_idx, rows, Q, K, V, heads, sq, sk, d, dtype, scale=None
 
 
 # ---------------------------------------------------------------------------
+# the operators of a serving attention layer
+# ---------------------------------------------------------------------------
+
+def rope_frequencies(rot, base, factor=1.0, context=0.0, low=0.0, high=0.0) -> np.ndarray:
+    """Radians a position for each of rot / 2 pairs; with factor > 1 a pair
+    that turns at most `low` times in `context` positions is slowed by the
+    factor, one that turns at least `high` times is kept, and the share kept
+    grows linearly between."""
+    f = np.array([base ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=np.float64)
+    if factor <= 1.0:
+        return f
+    out = []
+    for x in f:
+        turns = context * x / (2 * np.pi)
+        if high == 0.0 or turns <= low and turns < high:
+            keep = 0.0
+        elif turns >= high:
+            keep = 1.0
+        else:
+            keep = (turns - low) / (high - low)
+        out.append(x * keep + x / factor * (1 - keep))
+    return np.array(out)
+
+
+def qk_norm_rope(x, positions, frequencies, half, weight=None, eps=0.0, magnitude=1.0) -> np.ndarray:
+    """fp64 norm and rotation of x [tokens][heads][d] (fp64 values): the first
+    2 * len(frequencies) values of each head are turned, as complex numbers."""
+    y = np.array(x, dtype=np.float64)
+    if weight is not None:
+        y = y / np.sqrt((y * y).mean(axis=-1, keepdims=True) + eps) * weight
+    n = len(frequencies)
+    z = magnitude * np.exp(1j * np.outer(np.asarray(positions, dtype=np.float64), frequencies))[:, None, :]
+    a, b = (slice(0, n), slice(n, 2 * n)) if half else (slice(0, 2 * n, 2), slice(1, 2 * n, 2))
+    t = (y[..., a] + 1j * y[..., b]) * z
+    y[..., a], y[..., b] = t.real, t.imag
+    return y
+
+
+def prompt_attention(q, k, v, cu_q, cu_k, causal=True, scale=None):
+    """fp64 attention of packed sequences: q [rows][hq][d], k and v
+    [rows][hk][d] (fp64 values).  Returns (out, the same with |v|, which the
+    error bounds need); rows of no sequence, and rows without a visible key,
+    are zero.  One row at a time, over its visible keys only."""
+    hq, d = q.shape[1:]
+    group = hq // k.shape[1]
+    scale = 1.0 / np.sqrt(d) if scale is None else scale
+    out, mag = np.zeros(q.shape), np.zeros(q.shape)
+    for b in range(len(cu_q) - 1):
+        nq, nk = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
+        for i in range(nq):
+            vis = min(max(i + nk - nq + 1, 0), nk) if causal else nk
+            if vis == 0:
+                continue
+            rows = slice(cu_k[b], cu_k[b] + vis)
+            for h in range(hq):
+                s = k[rows, h // group] @ q[cu_q[b] + i, h] * scale
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                out[cu_q[b] + i, h] = p @ v[rows, h // group]
+                mag[cu_q[b] + i, h] = p @ np.abs(v[rows, h // group])
+    return out, mag
+
+
+def _e4m3_values() -> np.ndarray:
+    """The finite values of the 128 codes without a sign bit (code 127 is NaN)."""
+    e, m = np.arange(127) >> 3, np.arange(127) & 7
+    return np.where(e == 0, m / 8.0 * 2.0 ** -6, (1 + m / 8.0) * 2.0 ** (e - 7.0))
+
+
+def cache_encode(x):
+    """Codes and exponent bytes of rows x [...][d] (fp64 values): the least
+    power of two, at least 2^-126, that keeps the row's largest finite
+    magnitude within 448, and each quotient's nearest e4m3 value, ties to the
+    even code; infinities take the largest code, NaN code 127."""
+    x = np.asarray(x, dtype=np.float64)
+    mag = np.where(np.isfinite(x), np.abs(x), 0.0)
+    amax = mag.max(axis=-1)
+    power = np.zeros(amax.shape, dtype=np.int64)
+    nz = amax > 0
+    m, e = np.frexp(amax[nz] / 448.0)
+    power[nz] = np.maximum(np.where(m == 0.5, e - 1, e), -126)
+    grid = _e4m3_values()
+    y = np.ldexp(mag, -power[..., None])
+    hi = np.clip(np.searchsorted(grid, y), 0, 126)
+    lo = np.maximum(hi - 1, 0)
+    up = grid[hi] - y
+    down = y - grid[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = np.where(np.isinf(x), 126, code)
+    code = np.where(np.isnan(x), 127, code | (np.signbit(x).astype(np.int64) << 7))
+    return code.astype(np.uint8), (power + 127).astype(np.uint8)
+
+
+def cache_decode(codes, exponents) -> np.ndarray:
+    """fp64 values of codes [...][d] with exponent bytes [...]."""
+    grid = np.concatenate([_e4m3_values(), [np.nan]])
+    x = grid[codes & 127] * np.where(codes >> 7, -1.0, 1.0)
+    return np.ldexp(x, exponents[..., None].astype(np.int64) - 127)
+
+
+# ---------------------------------------------------------------------------
 # split-K factor (SM-waste rule)
 # ---------------------------------------------------------------------------
 
