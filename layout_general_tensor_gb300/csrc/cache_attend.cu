@@ -6,14 +6,18 @@
 // instructions on registers carry it and nothing goes through shared memory
 // on the way.
 //
-// Work.  A tile is 64 keys of one sequence and key head.  The tiles of the
-// whole batch, in the order (sequence, head, key), are cut into as many equal
-// runs as there are CTAs, so a long sequence among short ones spreads over
-// the GPU and every CTA reads the same number of bytes.  Each CTA finds its
-// run from the lengths by a prefix sum in shared memory.  Only the first and
-// the last sequence-head of a run can be shared with other CTAs; their
-// unnormalised results go to the workspace, and the CTA that arrives last
-// on the sequence-head's counter joins them, in the order of the keys.
+// Work.  A pass is one sequence, key head and group of up to 8 (16) query
+// heads; its units are its blocks of 16 keys and one more for what a pass
+// costs whatever its length.  The units of the whole batch, pass after pass,
+// are cut into as many equal runs as there are CTAs, and a CTA's run into one
+// for each warp, so a long sequence among short ones spreads over the GPU and
+// every warp reads about the same number of bytes, without meeting another
+// before the end of its run.  A pass that lies in one warp's run goes straight
+// to the output.  Of the others each warp leaves its unnormalised share (at
+// most two: its first and its last) in shared memory, where the CTA joins
+// them; the shares of passes that cross CTAs go on to the workspace, and the
+// CTA that arrives last on the pass's counter joins those.  All are joined in
+// the order of the keys.
 //
 // A warp takes 16 keys at a time (always inside one page).  With G <= 8 query
 // heads to a key head (NT = 1; 16 with NT = 2):
@@ -43,10 +47,10 @@
 namespace lgt {
 namespace {
 
-constexpr int kAtWarps = 8;
-constexpr int kAtThreads = kAtWarps * 32;
-constexpr int kAtTile = 64;         // keys
-constexpr int kAtMaxBatch = 8192;   // prefix sums in shared memory
+constexpr int kAtKeys = 16;         // a unit
+constexpr int kAtMaxBatch = 8192;   // lengths and prefix sums in shared memory
+constexpr uint32_t kAtJoin = 32;    // CTAs' parts joined in one step; their number is at most its square
+constexpr uint32_t kAtNone = 0xffffffffu;
 constexpr float kAtLazy = 8.0f;
 
 struct AttendArgs {
@@ -55,7 +59,7 @@ struct AttendArgs {
   uint16_t* out;
   const int32_t *table, *lengths;
   float* part;        // [cta][2][heads][D + 4]: sums, then l, m, R
-  int32_t* counters;  // one per (sequence, key head, head group)
+  int32_t* counters;  // one per pass, then one per part
   int64_t qs, os, table_stride;
   uint32_t pages;
   int32_t max_pages, batch, hk, group, hgroups;  // hgroups: groups of 8 * NT query heads of a key head
@@ -105,46 +109,114 @@ __device__ __forceinline__ float ex2f(float x) {
 
 // Joining partial results {l, m, R}: R against the common m, and the factors
 // of l and of the sum.  A part that saw no keys (m never set) counts nothing.
-template <typename P>
-__device__ __forceinline__ float ref_at(P s, float m) {
+__device__ __forceinline__ float ref_at(const float* s, float m) {
   return s[1] == -INFINITY ? -INFINITY : s[1] - m + s[2];
 }
-template <typename P>
-__device__ __forceinline__ float l_scale(P s, float m) {
-  return s[1] == -INFINITY ? 0.0f : ex2f(s[1] - m);
-}
-template <typename P>
-__device__ __forceinline__ float sum_scale(P s, float m, float R) {
+__device__ __forceinline__ float l_scale(const float* s, float m) { return s[1] == -INFINITY ? 0.0f : ex2f(s[1] - m); }
+__device__ __forceinline__ float sum_scale(const float* s, float m, float R) {
   return s[1] == -INFINITY ? 0.0f : ex2f(s[1] - m + s[2] - R);
 }
 
+// Whether this CTA is the last of `n` to arrive here with its results written;
+// then the others' are visible to it and the counter is 0 again.
+__device__ __forceinline__ bool arrive_last(int32_t* counter, uint32_t n, int* flag) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) *flag = atomicAdd(counter, 1) == static_cast<int>(n - 1);
+  __syncthreads();
+  const bool last = *flag != 0;
+  if (last) {
+    __threadfence();
+    if (threadIdx.x == 0) *counter = 0;
+  }
+  return last;
+}
+
+// Join n parts (rows of `heads` heads at their slots), by the
+// whole CTA: their {l, m, R} through shared memory, then each thread four
+// values of d over the parts in order, eight loads at a time.
+template <int D, int HP, int THREADS, typename SlotOf, typename Put>
+__device__ __forceinline__ void join_parts(const float* part, uint32_t* smem, uint32_t n, SlotOf slot_of, int heads, Put put) {
+  constexpr int ROW = D + 4;
+  float* stats = reinterpret_cast<float*>(smem);  // [part][HP][4]
+  for (uint32_t i = threadIdx.x; i < n * HP; i += THREADS) {
+    const uint32_t p = i / HP, head = i % HP;
+    float4 x = make_float4(0.0f, -INFINITY, -INFINITY, 0.0f);
+    if (static_cast<int>(head) < heads)
+      x = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p) * HP + head) * ROW + D));
+    *reinterpret_cast<float4*>(stats + i * 4) = x;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * (D / 4); i += THREADS) {
+    const int head = i / (D / 4), d = i % (D / 4) * 4;
+    const float* st = stats + head * 4;
+    float mt = -INFINITY, Rt = -INFINITY;
+    for (uint32_t p = 0; p < n; ++p) mt = fmaxf(mt, st[p * HP * 4 + 1]);
+    for (uint32_t p = 0; p < n; ++p) Rt = fmaxf(Rt, ref_at(st + p * HP * 4, mt));
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float lt = 0.0f;
+    for (uint32_t p0 = 0; p0 < n; p0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = p0 + e < n ? __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p0 + e) * HP + head) * ROW + d))
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (p0 + e < n) {
+          const float* s = st + (p0 + e) * HP * 4;
+          const float f = sum_scale(s, mt, Rt);
+          acc.x += x[e].x * f;
+          acc.y += x[e].y * f;
+          acc.z += x[e].z * f;
+          acc.w += x[e].w * f;
+          lt += s[0] * l_scale(s, mt);
+        }
+    }
+    put(head, d, acc, lt, mt, Rt);
+  }
+  __syncthreads();  // the shared memory is used again
+}
+
+template <int NT>
+struct AttendCfg {
+  // registers: 16 warps of 128 (NT = 1) or 8 of 255 fill an SM
+  static constexpr int W = NT == 1 ? 16 : 8;
+  static constexpr int THREADS = W * 32;
+  static constexpr int HP = 8 * NT;  // query heads of a pass
+};
+
 template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(kAtThreads, NT == 1 ? 2 : 1) cache_attend_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int HP = 8 * NT;       // query heads of a pass
-  constexpr int ROW = D + 4;       // floats of a partial row
+__global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int W = AttendCfg<NT>::W, THREADS = AttendCfg<NT>::THREADS, HP = AttendCfg<NT>::HP;
+  constexpr int ROW = D + 4;       // floats of a part's row
   constexpr int KP = D / 64;       // 16-byte pieces of a key a lane loads
   constexpr int VW = D / 32;       // words of a value row a lane loads (D / 8 bytes)
   constexpr int MT = D / 16;       // m-tiles of O^T
-  extern __shared__ uint32_t smem_u[];
-  float* red = reinterpret_cast<float*>(smem_u);             // [warp][HP][ROW]
-  uint32_t* prefix = smem_u + kAtWarps * HP * ROW;           // batch + 1
-  __shared__ uint32_t scan[kAtWarps];
-  __shared__ int last_flag;
+  extern __shared__ __align__(16) uint32_t smem_u[];
+  float* parts = reinterpret_cast<float*>(smem_u);           // [warp][2][HP][ROW]
+  uint32_t* prefix = smem_u + W * 2 * HP * ROW;              // batch + 1
+  int32_t* lens = reinterpret_cast<int32_t*>(prefix + a.batch + 1);
+  __shared__ uint32_t scan[W], pass_of[2 * W], leader_of[2 * W];
+  __shared__ int flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   pdl_launch_dependents();
+  if (threadIdx.x < 2 * W) pass_of[threadIdx.x] = kAtNone;
   pdl_wait();
 
-  // ---- prefix sums of the sequences' tiles (at least one each: somebody writes the zeros)
+  // ---- lengths and prefix sums of the sequences' units
   const uint32_t per_seq = static_cast<uint32_t>(a.hk * a.hgroups);
+  auto units_of = [](int len) { return static_cast<uint32_t>((len + kAtKeys - 1) / kAtKeys + 1); };
   {
     uint32_t carry = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kAtThreads) {
+    for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
       const int b = b0 + static_cast<int>(threadIdx.x);
       uint32_t n = 0;
       if (b < a.batch) {
         const int len = min(max(a.lengths[b], 0), a.max_len);
-        n = static_cast<uint32_t>(max((len + kAtTile - 1) / kAtTile, 1)) * per_seq;
+        lens[b] = len;
+        n = units_of(len) * per_seq;
       }
       uint32_t x = n;
 #pragma unroll
@@ -156,7 +228,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 2 : 1) cache_attend_kern
       __syncthreads();
       uint32_t before = carry, all = 0;
 #pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         before += w < warp ? scan[w] : 0u;
         all += scan[w];
       }
@@ -167,37 +239,90 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 2 : 1) cache_attend_kern
     if (threadIdx.x == 0) prefix[a.batch] = carry;
     __syncthreads();
   }
-  // (never more CTAs than tiles: every run has a tile, so every CTA between a
-  // sequence-head's first and last takes part in it)
-  const uint32_t total = prefix[a.batch], ctas = min(gridDim.x, total);
+  // (a unit for every warp at least, where there are that many in all; so no
+  // run is empty, and every CTA between a pass's first and last takes part)
+  const uint32_t total = prefix[a.batch], ctas = min(gridDim.x, max(total / W, 1u));
   if (blockIdx.x >= ctas) return;
   auto run_start = [&](uint32_t cta) { return static_cast<uint32_t>(static_cast<uint64_t>(cta) * total / ctas); };
-  auto owner = [&](uint32_t tile) {
-    return static_cast<uint32_t>((static_cast<uint64_t>(tile + 1) * ctas - 1) / total);
+  auto owner = [&](uint32_t unit) {
+    return static_cast<uint32_t>((static_cast<uint64_t>(unit + 1) * ctas - 1) / total);
   };
   const uint32_t t0 = run_start(blockIdx.x), t1 = run_start(blockIdx.x + 1);
+  const uint32_t s0 = t0 + static_cast<uint32_t>(static_cast<uint64_t>(t1 - t0) * warp / W);
+  const uint32_t s1 = t0 + static_cast<uint32_t>(static_cast<uint64_t>(t1 - t0) * (warp + 1) / W);
   int b = 0;
   {
-    int lo = 0, hi = a.batch - 1;  // the last sequence whose prefix is <= t0
+    int lo = 0, hi = a.batch - 1;  // the last sequence whose prefix is <= s0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= t0) lo = mid; else hi = mid - 1;
+      if (prefix[mid] <= s0) lo = mid; else hi = mid - 1;
     }
     b = lo;
   }
+  auto put4 = [&](int seq, int head_at, int d, float4 acc, float lt, float Rt) {
+    const float f = ex2f(Rt) / lt;
+    uint16_t* dst = a.out + static_cast<int64_t>(seq) * a.os + static_cast<int64_t>(head_at) * D + d;
+    if (lt == 0.0f)
+      st_global_v2(dst, 0u, 0u);
+    else
+      st_global_v2(dst, pack_pair16<BF16>(acc.x * f, acc.y * f), pack_pair16<BF16>(acc.z * f, acc.w * f));
+  };
 
-  for (uint32_t t = t0; t < t1;) {
+  for (uint32_t t = s0; t < s1;) {
     while (t >= prefix[b + 1]) ++b;
-    const int len = min(max(a.lengths[b], 0), a.max_len);
-    const uint32_t tiles = (prefix[b + 1] - prefix[b]) / per_seq;  // of one pass over the keys
-    const uint32_t in_seq = t - prefix[b];
-    const uint32_t hh = in_seq / tiles, tile = in_seq - hh * tiles;
+    const int len = lens[b];
+    const uint32_t units = units_of(len);
+    const uint32_t hh = (t - prefix[b]) / units, in = t - prefix[b] - hh * units;
+    const uint32_t stop = min(units, in + (s1 - t));  // the share: units [in, stop) of the pass
     const int h = static_cast<int>(hh) / a.hgroups, hg = static_cast<int>(hh) - h * a.hgroups;
-    const uint32_t seg_end = min(t1, prefix[b] + (hh + 1) * tiles);
-    const int key0 = static_cast<int>(tile) * kAtTile;
-    const int key1 = min(len, static_cast<int>(tile + (seg_end - t)) * kAtTile);
+    const int key1 = min(len, static_cast<int>(stop) * kAtKeys);
     const int heads = min(HP, a.group - hg * HP);  // of this pass
     const int hq0 = h * a.group + hg * HP;
+    int key = static_cast<int>(in) * kAtKeys;
+
+    // ---- the first keys on their way
+    uint4 kw[2][KP];
+    uint32_t vw[4][VW];
+    int kx[2], vx[2];
+    auto page_of = [&](int at) -> uint32_t {
+      if (at >= key1) return kAtNone;
+      return static_cast<uint32_t>(
+          a.table[static_cast<int64_t>(b) * a.table_stride + magic_div(static_cast<uint32_t>(at), a.div_page)]);
+    };
+    auto row_of = [&](int at, uint32_t page) -> int64_t {
+      const int off = at - static_cast<int>(magic_div(static_cast<uint32_t>(at), a.div_page)) * a.page;
+      return (static_cast<int64_t>(page) * a.hk + h) * a.page + off;
+    };
+    auto load_k = [&](int at, uint32_t page) {
+      if (page >= a.pages) return;
+      const int64_t row = row_of(at, page);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int p = 0; p < KP; ++p) kw[i][p] = ld_stream_v4(a.k + (row + r + 8 * i) * D + p * 64 + c * 16);
+        kx[i] = a.ke[row + r + 8 * i];
+      }
+    };
+    auto load_v = [&](int at, uint32_t page) {
+      if (page >= a.pages) return;
+      const int64_t row = row_of(at, page);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = a.v + (row + 2 * c + (i & 1) + 8 * (i >> 1)) * D + r * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 x = ld_stream_v4(p);
+          vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
+        } else {
+          const uint2 x = ld_stream_v2(p);
+          vw[i][0] = x.x; vw[i][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) vx[i] = a.ve[row + r + 8 * i];
+    };
+    uint32_t page = page_of(key), next_page = page_of(key + kAtKeys);
+    load_k(key, page);
+    load_v(key, page);
 
     // ---- the queries as B fragments: lane (r, c) has head r's values
     // p*64 + c*16 + 4j + {0, 1 | 2, 3} for step (p, j), in fp16 (bf16 ones
@@ -269,55 +394,9 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 2 : 1) cache_attend_kern
     }
 
     // ---- the keys, 16 at a time
-    uint4 kw[2][KP];
-    uint32_t vw[4][VW];
-    int kx[2], vx[2];
-    auto page_of = [&](int key) -> uint32_t {
-      if (key >= key1) return 0xffffffffu;
-      return static_cast<uint32_t>(
-          a.table[static_cast<int64_t>(b) * a.table_stride + magic_div(static_cast<uint32_t>(key), a.div_page)]);
-    };
-    auto row_of = [&](int key, uint32_t page) -> int64_t {
-      const int off = key - static_cast<int>(magic_div(static_cast<uint32_t>(key), a.div_page)) * a.page;
-      return (static_cast<int64_t>(page) * a.hk + h) * a.page + off;
-    };
-    auto load_k = [&](int key, uint32_t page) {
-      if (page >= a.pages) return;
-      const int64_t row = row_of(key, page);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int p = 0; p < KP; ++p) kw[i][p] = ld_stream_v4(a.k + (row + r + 8 * i) * D + p * 64 + c * 16);
-        kx[i] = a.ke[row + r + 8 * i];
-      }
-    };
-    auto load_v = [&](int key, uint32_t page) {
-      if (page >= a.pages) return;
-      const int64_t row = row_of(key, page);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* p = a.v + (row + 2 * c + (i & 1) + 8 * (i >> 1)) * D + r * (D / 8);
-        if constexpr (D == 128) {
-          const uint4 x = ld_stream_v4(p);
-          vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
-        } else {
-          const uint2 x = ld_stream_v2(p);
-          vw[i][0] = x.x; vw[i][1] = x.y;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) vx[i] = a.ve[row + r + 8 * i];
-    };
-
-    int key = key0 + warp * 16;
-    uint32_t page = page_of(key), next_page = page_of(key + kAtWarps * 16);
-    if (key < key1) {
-      load_k(key, page);
-      load_v(key, page);
-    }
-    for (; key < key1; key += kAtWarps * 16) {
-      const int next = key + kAtWarps * 16;
-      const uint32_t page2 = page_of(next + kAtWarps * 16);
+    for (; key < key1; key += kAtKeys) {
+      const int next = key + kAtKeys;
+      const uint32_t page2 = page_of(next + kAtKeys);
       const int valid = page < a.pages ? min(16, key1 - key) : 0;  // a page that is none holds no keys
       if (valid > 0) {
         float s[NT][4];
@@ -424,90 +503,128 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 2 : 1) cache_attend_kern
       next_page = page2;
     }
 
-    // ---- the warps' results together, in the order of the warps
+    // ---- a whole pass to the output, a share to shared memory
+    const bool whole = in == 0 && stop == units;
+    const int part = warp * 2 + (t == s0 ? 0 : 1);
+    if (!whole && lane == 0) pass_of[part] = static_cast<uint32_t>(b) * per_seq + hh;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], sh);
-        float* row = red + (warp * HP + n * 8 + 2 * c + e) * ROW;
-        if (r == 0) {
-          row[D] = l[n][e];
-          row[D + 1] = m[n][e];
-          row[D + 2] = R[n][e];
-        }
+        const int head = n * 8 + 2 * c + e;
+        if (head < heads) {
+          float* row = parts + (part * HP + head) * ROW;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          row[r * (D / 8) + 2 * i] = o[i][n][e];
-          row[r * (D / 8) + 2 * i + 1] = o[i][n][2 + e];
-        }
-      }
-    __syncthreads();
-    const uint32_t first_tile = prefix[b] + hh * tiles, last_tile = first_tile + tiles - 1;
-    const uint32_t c0 = owner(first_tile), c1 = owner(last_tile);
-    auto write_out = [&](int head, int d, float acc, float lt, float Rt) {
-      const float y = lt == 0.0f ? 0.0f : acc * (ex2f(Rt) / lt);
-      uint16_t* dst = a.out + static_cast<int64_t>(b) * a.os + static_cast<int64_t>(hq0 + head) * D + d;
-      *dst = static_cast<uint16_t>(pack_pair16<BF16>(y, 0.0f));
-    };
-    for (int i = threadIdx.x; i < heads * D; i += kAtThreads) {
-      const int head = i / D, d = i - head * D;
-      const float* rows = red + head * ROW;
-      float mt = -INFINITY, Rt = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) mt = fmaxf(mt, rows[w * HP * ROW + D + 1]);
-#pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) Rt = fmaxf(Rt, ref_at(rows + w * HP * ROW + D, mt));
-      float acc = 0.0f, lt = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) {
-        const float* row = rows + w * HP * ROW;
-        acc += row[d] * sum_scale(row + D, mt, Rt);
-        lt += row[D] * l_scale(row + D, mt);
-      }
-      if (c0 == c1) {
-        write_out(head, d, acc, lt, Rt);
-      } else {
-        float* row = a.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (t == t0 ? 0 : 1)) * HP + head) * ROW;
-        row[d] = acc;
-        if (d == 0) {
-          row[D] = lt;
-          row[D + 1] = mt;
-          row[D + 2] = Rt;
-        }
-      }
-    }
-    if (c0 != c1) {
-      __threadfence();
-      __syncthreads();
-      int32_t* counter = a.counters + static_cast<int64_t>(b) * per_seq + hh;
-      if (threadIdx.x == 0) last_flag = atomicAdd(counter, 1) == static_cast<int>(c1 - c0);
-      __syncthreads();
-      if (last_flag) {
-        __threadfence();
-        if (threadIdx.x == 0) *counter = 0;
-        for (int i = threadIdx.x; i < heads * D; i += kAtThreads) {
-          const int head = i / D, d = i - head * D;
-          auto row_at = [&](uint32_t cta) -> const volatile float* {  // (other CTAs wrote it: not through L1)
-            const int slot = cta == c0 && run_start(c0) != first_tile ? 1 : 0;
-            return a.part + ((static_cast<int64_t>(cta) * 2 + slot) * HP + head) * ROW;
-          };
-          float mt = -INFINITY, Rt = -INFINITY;
-          for (uint32_t x = c0; x <= c1; ++x) mt = fmaxf(mt, row_at(x)[D + 1]);
-          for (uint32_t x = c0; x <= c1; ++x) Rt = fmaxf(Rt, ref_at(row_at(x) + D, mt));
-          float acc = 0.0f, lt = 0.0f;
-          for (uint32_t x = c0; x <= c1; ++x) {
-            const volatile float* row = row_at(x);
-            acc += row[d] * sum_scale(row + D, mt, Rt);
-            lt += row[D] * l_scale(row + D, mt);
+          for (int i = 0; i < MT; i += 2) {
+            const float4 x = make_float4(o[i][n][e], o[i][n][2 + e], o[i + 1][n][e], o[i + 1][n][2 + e]);
+            const int d = r * (D / 8) + 2 * i;
+            if (whole)
+              put4(b, hq0 + head, d, x, l[n][e], R[n][e]);
+            else
+              *reinterpret_cast<float4*>(row + d) = x;
           }
-          write_out(head, d, acc, lt, Rt);
+          if (!whole && r == 0) *reinterpret_cast<float4*>(row + D) = make_float4(l[n][e], m[n][e], R[n][e], 0.0f);
         }
       }
+    t += stop - in;
+  }
+  __syncthreads();
+
+  // ---- the warps' shares together: neighbouring ones of the same pass
+  struct Pass {
+    int b, heads, hq0;
+    uint32_t hh, first, c0, c1;  // its first unit, its first and last CTA
+  };
+  auto pass_at = [&](uint32_t p) {
+    Pass x;
+    x.b = static_cast<int>(p / per_seq);
+    x.hh = p - static_cast<uint32_t>(x.b) * per_seq;
+    const int h = static_cast<int>(x.hh) / a.hgroups, hg = static_cast<int>(x.hh) - h * a.hgroups;
+    x.heads = min(HP, a.group - hg * HP);
+    x.hq0 = h * a.group + hg * HP;
+    const uint32_t units = units_of(lens[x.b]);
+    x.first = prefix[x.b] + x.hh * units;
+    x.c0 = owner(x.first);
+    x.c1 = owner(x.first + units - 1);
+    return x;
+  };
+  // where a CTA's share of a pass is in the workspace
+  auto slot_of = [](const Pass& x, uint32_t cta) -> int64_t { return static_cast<int64_t>(cta) * 2 + (cta == x.c0 ? 1 : 0); };
+  const uint32_t mine = lane < 2 * W ? pass_of[lane] : kAtNone;
+  uint32_t used = __ballot_sync(0xffffffffu, mine != kAtNone);
+  const uint32_t below = used & ((1u << lane) - 1u);
+  const uint32_t previous = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
+  const bool leads = mine != kAtNone && (!below || previous != mine);
+  const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+  if (warp == 0 && leads) leader_of[__popc(leaders & ((1u << lane) - 1u))] = lane;
+  __syncthreads();
+  constexpr int kItems = HP * (D / 4);
+  for (int i = threadIdx.x; i < __popc(leaders) * kItems; i += THREADS) {
+    const uint32_t e0 = leader_of[i / kItems];
+    const int head = i % kItems / (D / 4), d = i % (D / 4) * 4;
+    const Pass x = pass_at(pass_of[e0]);
+    if (head >= x.heads) continue;
+    uint32_t own = used & ~((1u << e0) - 1u);  // its shares: from e0 up to the next leader
+    const uint32_t later = leaders & ~((2u << e0) - 1u);
+    if (later) own &= (later & (0u - later)) - 1u;
+    float mt = -INFINITY, Rt = -INFINITY, lt = 0.0f;
+    for (uint32_t q = own; q; q &= q - 1) mt = fmaxf(mt, parts[((__ffs(q) - 1) * HP + head) * ROW + D + 1]);
+    for (uint32_t q = own; q; q &= q - 1) Rt = fmaxf(Rt, ref_at(parts + ((__ffs(q) - 1) * HP + head) * ROW + D, mt));
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (uint32_t q = own; q; q &= q - 1) {
+      const float* row = parts + ((__ffs(q) - 1) * HP + head) * ROW;
+      const float4 y = *reinterpret_cast<const float4*>(row + d);
+      const float f = sum_scale(row + D, mt, Rt);
+      acc.x += y.x * f;
+      acc.y += y.y * f;
+      acc.z += y.z * f;
+      acc.w += y.w * f;
+      lt += row[D] * l_scale(row + D, mt);
     }
-    __syncthreads();  // red and last_flag are used again by the next segment
-    t = seg_end;
+    if (x.c0 == x.c1) {
+      put4(x.b, x.hq0 + head, d, acc, lt, Rt);
+    } else {
+      float* row = a.part + (slot_of(x, blockIdx.x) * HP + head) * ROW;
+      *reinterpret_cast<float4*>(row + d) = acc;
+      if (d == 0) *reinterpret_cast<float4*>(row + D) = make_float4(lt, mt, Rt, 0.0f);
+    }
+  }
+
+  // ---- the CTAs' shares, of the first and the last pass of this run
+  uint32_t done = kAtNone;
+#pragma unroll 1
+  for (int k = 0; k < 2 && used; ++k) {
+    const uint32_t e = k == 0 ? __ffs(used) - 1 : 31 - __clz(used);
+    const uint32_t p = pass_of[e];
+    const Pass x = pass_at(p);
+    if (p == done || x.c0 == x.c1) continue;
+    done = p;
+    // in two steps where there are many parts: kAtJoin neighbours by the last
+    // of them to arrive, then those by the last of all
+    const uint32_t n = x.c1 - x.c0 + 1, lo = (blockIdx.x - x.c0) / kAtJoin * kAtJoin, group = min(kAtJoin, n - lo);
+    const bool all = n <= kAtJoin;
+    int32_t* pass_counter = a.counters + p;
+    int32_t* group_counter = a.counters + static_cast<int64_t>(a.batch) * per_seq + slot_of(x, x.c0 + lo);
+    if (!arrive_last(all ? pass_counter : group_counter, group, &flag)) continue;
+    join_parts<D, HP, THREADS>(a.part, smem_u, group, [&](uint32_t i) { return slot_of(x, x.c0 + lo + i); }, x.heads,
+                               [&](int head, int d, float4 acc, float lt, float mt, float Rt) {
+                                 if (all) {
+                                   put4(x.b, x.hq0 + head, d, acc, lt, Rt);
+                                 } else {
+                                   float* row = a.part + (slot_of(x, x.c0 + lo) * HP + head) * ROW;
+                                   *reinterpret_cast<float4*>(row + d) = acc;
+                                   if (d == 0) *reinterpret_cast<float4*>(row + D) = make_float4(lt, mt, Rt, 0.0f);
+                                 }
+                               });
+    if (all) continue;
+    const uint32_t groups = (n + kAtJoin - 1) / kAtJoin;
+    if (!arrive_last(pass_counter, groups, &flag)) continue;
+    join_parts<D, HP, THREADS>(a.part, smem_u, groups, [&](uint32_t i) { return slot_of(x, x.c0 + i * kAtJoin); }, x.heads,
+                               [&](int head, int d, float4 acc, float lt, float mt, float Rt) {
+                                 put4(x.b, x.hq0 + head, d, acc, lt, Rt);
+                               });
   }
 }
 
@@ -516,7 +633,6 @@ struct AttendPlan {
   size_t part_bytes, bytes;
 };
 
-// CTAs: two an SM where the registers allow it (up to eight heads a pass).
 bool plan_attend(int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t batch, AttendPlan* p) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -527,19 +643,22 @@ bool plan_attend(int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t bat
   const int group = q_heads / k_heads;
   p->nt = group <= 8 ? 1 : 2;
   p->hgroups = (group + 8 * p->nt - 1) / (8 * p->nt);
-  p->ctas = sms * (p->nt == 1 ? 2 : 1);
+  p->ctas = sms;
   p->part_bytes = static_cast<size_t>(p->ctas) * 2 * 8 * p->nt * (head_dim + 4) * sizeof(float);
-  p->bytes = p->part_bytes + static_cast<size_t>(batch) * k_heads * p->hgroups * sizeof(int32_t);
+  p->bytes = p->part_bytes + (static_cast<size_t>(batch) * k_heads * p->hgroups + 2 * p->ctas) * sizeof(int32_t);
   return true;
 }
 
 template <int D, int NT, bool BF16>
 cudaError_t launch_attend(const AttendArgs& a, int ctas, cudaStream_t stream) {
-  const size_t smem = sizeof(uint32_t) * (static_cast<size_t>(kAtWarps) * 8 * NT * (D + 4) + a.batch + 1);
-  constexpr size_t most = sizeof(uint32_t) * (static_cast<size_t>(kAtWarps) * 8 * NT * (D + 4) + kAtMaxBatch + 1);
+  using C = AttendCfg<NT>;
+  constexpr size_t parts = sizeof(float) * C::W * 2 * C::HP * (D + 4);
+  constexpr size_t most = parts + sizeof(uint32_t) * (2 * kAtMaxBatch + 1);
+  static_assert(most <= 227 * 1024 - 1024, "shared memory");
   const cudaError_t e = set_smem_once<cache_attend_kernel<D, NT, BF16>>(static_cast<int>(most));
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attend_kernel<D, NT, BF16>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), smem, stream, a);
+  return launch_pdl(cache_attend_kernel<D, NT, BF16>, dim3(static_cast<unsigned>(ctas)), dim3(C::THREADS),
+                    parts + sizeof(uint32_t) * (2 * static_cast<size_t>(a.batch) + 1), stream, a);
 }
 
 bool attend_shape_ok(int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t batch) {
@@ -580,12 +699,12 @@ extern "C" gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void
   for (const void* p : {Q, static_cast<const void*>(out), static_cast<const void*>(c.k), static_cast<const void*>(c.v)})
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return GEMM_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(lengths) | reinterpret_cast<uintptr_t>(page_table)) % 4 != 0) return GEMM_ERR_ALIGNMENT;
-  // (tiles are counted in 32 bits, keys in 31)
+  // (units are counted in 32 bits, keys in 31)
   const int64_t max_len = static_cast<int64_t>(max_pages) * c.page_size;
   if (batch > lgt::kAtMaxBatch || max_len > (int64_t{1} << 30)) return GEMM_ERR_UNSUPPORTED;
   lgt::AttendPlan p;
   if (!lgt::plan_attend(q_heads, c.k_heads, c.head_dim, batch, &p)) return GEMM_ERR_CUDA;
-  if ((max_len / lgt::kAtTile + 1) * batch * c.k_heads * p.hgroups >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
+  if ((max_len / lgt::kAtKeys + 2) * batch * c.k_heads * p.hgroups >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
     return GEMM_ERR_WORKSPACE;
   lgt::AttendArgs a;

@@ -1,12 +1,13 @@
 // Norm and position rotation of queries and keys in one pass
 // (include/attn_rope.h).
 //
-// A head's d values belong to a group of LG lanes (the least power of two
-// with LG * 8 >= d), eight values a lane: in the half layout two runs of
-// four, [4u, 4u + 4) of the first half of the rotated part and the same of
-// the second, so that both values of each of the lane's four pairs are its
-// own; otherwise eight neighbours.  The head's sum of squares goes around
-// the group by a shuffle butterfly; everything is fp32 and is rounded once.
+// A head's d values belong to a group of LG lanes, two runs of R = 8 (16
+// bytes) or 4 values a lane: in the half layout R of the first half of the
+// rotated part and the same R of the second, so that both values of each of
+// the lane's R pairs are its own; otherwise 2R neighbours.  LG is the least
+// power of two with LG * 2R >= d.  R is 8 where rot_dim and d are multiples of
+// 16, which all common sizes are.  The head's sum of squares goes around the
+// group by a shuffle butterfly; everything is fp32 and is rounded once.
 //
 // The angle.  f_i / (2 pi), the turns a position, is held as a 64-bit binary
 // fraction.  position * fraction modulo 2^64 is the phase modulo one turn,
@@ -16,10 +17,9 @@
 // taken of an angle in [-pi, pi], where the hardware's approximations are
 // within 2^-20.9 absolute, a thousandth of an fp16 rounding.
 //
-// Bound: memory, each value read and written once.  A group takes kItems
-// neighbouring heads and loads all of them before it works on the first
-// (16 bytes a lane each), and computes the sines again only where the token
-// changes.
+// Bound: memory, each value read and written once.  A group takes a chunk of
+// neighbouring heads, two at a time with the next two on their way, and
+// computes the sines again only where the token changes.
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxPairs = 128;  // head_dim 256
+constexpr uint32_t kRopeBlocks = 8;  // blocks an SM the chunks are cut for
 
 struct RopeArgs {
   const uint16_t *q, *k, *wq, *wk;
@@ -41,149 +42,203 @@ struct RopeArgs {
   const int32_t* pos;
   int64_t qs, ks, qos, kos;
   uint32_t items;  // tokens * heads
+  uint32_t chunk;  // of a group
   MagicDiv div_heads;
-  int32_t hq, d, rot;
+  int32_t hq, heads, d, rot;
   float eps, inv_d, magnitude;
   uint64_t turns[kRopeMaxPairs];  // of pair i a position, as a fraction of 2^64
 };
 
-// One lane's part of one head: where its two runs of four values are.
-template <bool HALF>
-__device__ __forceinline__ void run_offsets(int u, int rot, int& o0, int& o1) {
-  if (HALF && 8 * u < rot) {
-    o0 = 4 * u;
-    o1 = rot / 2 + 4 * u;
+template <int R>
+struct Run {  // R 16-bit values
+  uint32_t w[R / 2];
+};
+
+template <int R>
+__device__ __forceinline__ Run<R> load_run(const uint16_t* p) {
+  Run<R> r;
+  if constexpr (R == 8) {
+    const uint4 v = ld_stream_v4(p);
+    r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
   } else {
-    o0 = 8 * u;
-    o1 = 8 * u + 4;
+    const uint2 v = ld_stream_v2(p);
+    r.w[0] = v.x; r.w[1] = v.y;
+  }
+  return r;
+}
+
+template <int R>
+__device__ __forceinline__ void store_run(uint16_t* p, const Run<R>& r) {
+  if constexpr (R == 8)
+    st_global_v4(p, r.w[0], r.w[1], r.w[2], r.w[3]);
+  else
+    st_global_v2(p, r.w[0], r.w[1]);
+}
+
+template <int R, bool BF16>
+__device__ __forceinline__ void widen_run(const Run<R>& r, float* x) {
+#pragma unroll
+  for (int i = 0; i < R / 2; ++i) {
+    const float2 p = unpack_pair16<BF16>(r.w[i]);
+    x[2 * i] = p.x;
+    x[2 * i + 1] = p.y;
   }
 }
 
-template <int LG, bool BF16, bool HALF, int ITEMS>
+template <int R, bool BF16>
+__device__ __forceinline__ Run<R> narrow_run(const float* x) {
+  Run<R> r;
+#pragma unroll
+  for (int i = 0; i < R / 2; ++i) r.w[i] = pack_pair16<BF16>(x[2 * i], x[2 * i + 1]);
+  return r;
+}
+
+template <int R, int LG, bool BF16, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   pdl_launch_dependents();
-  pdl_wait();
   const int u = threadIdx.x % LG;
-  const uint32_t first = (blockIdx.x * (kRopeThreads / LG) + threadIdx.x / LG) * ITEMS;
-  const bool mine = 8 * u < a.d;
-  const bool turned = 8 * u < a.rot;
+  const uint32_t group = blockIdx.x * (kRopeThreads / LG) + threadIdx.x / LG;
+  const uint32_t first = min(group * a.chunk, a.items), end = min(first + a.chunk, a.items);
+  const bool mine = 2 * R * u < a.d;
+  const bool turned = 2 * R * u < a.rot;
   const bool norms = a.wq != nullptr || a.wk != nullptr;
-  int o0, o1;
-  run_offsets<HALF>(u, a.rot, o0, o1);
-
-  uint2 x0[ITEMS], x1[ITEMS];
+  const int o0 = HALF && turned ? R * u : 2 * R * u, o1 = HALF && turned ? a.rot / 2 + R * u : 2 * R * u + R;
+  uint32_t turns_lo[R], turns_hi[R];
 #pragma unroll
-  for (int j = 0; j < ITEMS; ++j) {
-    x0[j] = x1[j] = make_uint2(0u, 0u);
-    if (first + j < a.items && mine) {
-      uint32_t t, h;
-      magic_divmod(first + j, a.div_heads, t, h);
-      const bool is_q = h < static_cast<uint32_t>(a.hq);
-      const uint16_t* src = is_q ? a.q + static_cast<int64_t>(t) * a.qs + static_cast<int64_t>(h) * a.d
-                                 : a.k + static_cast<int64_t>(t) * a.ks + static_cast<int64_t>(h - a.hq) * a.d;
-      if constexpr (HALF) {
-        x0[j] = ld_stream_v2(src + o0);
-        x1[j] = ld_stream_v2(src + o1);
-      } else {
-        const uint4 v = ld_stream_v4(src + o0);
-        x0[j] = make_uint2(v.x, v.y);
-        x1[j] = make_uint2(v.z, v.w);
+  for (int e = 0; e < R; ++e) {
+    const uint64_t f = turned ? a.turns[R * u + e] : 0u;
+    turns_lo[e] = static_cast<uint32_t>(f);
+    turns_hi[e] = static_cast<uint32_t>(f >> 32);
+  }
+  uint32_t t, h;  // of the head that is loaded next
+  magic_divmod(min(first, a.items - 1u), a.div_heads, t, h);
+  auto is_query = [&](uint32_t hh) { return hh < static_cast<uint32_t>(a.hq); };
+  pdl_wait();
+
+  Run<R> x0[2], x1[2];
+  uint32_t lt[2], lh[2];
+  auto load = [&](uint32_t item) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      lt[j] = t;
+      lh[j] = h;
+#pragma unroll
+      for (int i = 0; i < R / 2; ++i) x0[j].w[i] = x1[j].w[i] = 0u;
+      if (item + j < end) {
+        if (mine) {
+          const uint16_t* src = is_query(h) ? a.q + static_cast<int64_t>(t) * a.qs + h * a.d
+                                            : a.k + static_cast<int64_t>(t) * a.ks + (h - a.hq) * a.d;
+          x0[j] = load_run<R>(src + o0);
+          x1[j] = load_run<R>(src + o1);
+        }
+        if (++h == static_cast<uint32_t>(a.heads)) {
+          h = 0;
+          ++t;
+        }
       }
     }
-  }
+  };
+  load(first);
 
-  float cs[4], sn[4], w[8];
+  float cs[R], sn[R], w[2 * R];
   uint32_t have_t = 0xffffffffu;
   int have_w = -1;
+  // (every lane of a warp goes round as often: the butterflies are of all)
+  for (uint32_t step = 0; step < a.chunk; step += 2) {
+    float y[2][2 * R];
+    uint32_t ct[2], ch[2];
 #pragma unroll
-  for (int j = 0; j < ITEMS; ++j) {
-    uint32_t t, h;
-    magic_divmod(first + j < a.items ? first + j : a.items - 1, a.div_heads, t, h);
-    const bool is_q = h < static_cast<uint32_t>(a.hq);
-    float y[8];
-    {
-      const float2 p0 = unpack_pair16<BF16>(x0[j].x), p1 = unpack_pair16<BF16>(x0[j].y);
-      const float2 p2 = unpack_pair16<BF16>(x1[j].x), p3 = unpack_pair16<BF16>(x1[j].y);
-      y[0] = p0.x; y[1] = p0.y; y[2] = p1.x; y[3] = p1.y;
-      y[4] = p2.x; y[5] = p2.y; y[6] = p3.x; y[7] = p3.y;
+    for (int j = 0; j < 2; ++j) {
+      ct[j] = lt[j];
+      ch[j] = lh[j];
+      widen_run<R, BF16>(x0[j], y[j]);
+      widen_run<R, BF16>(x1[j], y[j] + R);
     }
-    const uint16_t* wt = is_q ? a.wq : a.wk;
-    if (norms) {  // (the same for every lane: the groups of a warp may be at heads with and without a norm)
-      float ss = 0.0f;
+    const uint32_t item = first + step;
+    load(item + 2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+    for (int j = 0; j < 2; ++j) {
+      const bool is_q = is_query(ch[j]);
+      if (norms) {
+        float ss[2] = {};
 #pragma unroll
-      for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (wt && mine) {
-        const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
-        if (have_w != static_cast<int>(is_q)) {
-          have_w = is_q;
-          const uint2 w0 = *reinterpret_cast<const uint2*>(wt + o0), w1 = *reinterpret_cast<const uint2*>(wt + o1);
-          const float2 p0 = unpack_pair16<BF16>(w0.x), p1 = unpack_pair16<BF16>(w0.y);
-          const float2 p2 = unpack_pair16<BF16>(w1.x), p3 = unpack_pair16<BF16>(w1.y);
-          w[0] = p0.x; w[1] = p0.y; w[2] = p1.x; w[3] = p1.y;
-          w[4] = p2.x; w[5] = p2.y; w[6] = p3.x; w[7] = p3.y;
-        }
+        for (int e = 0; e < 2 * R; ++e) ss[e & 1] = fmaf(y[j][e], y[j][e], ss[e & 1]);
+        ss[0] += ss[1];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
-      }
-    }
-    if (turned) {
-      if (t != have_t) {
-        have_t = t;
-        const uint64_t p = static_cast<uint64_t>(static_cast<int64_t>(a.pos[t]));
+        for (int o = LG / 2; o > 0; o >>= 1) ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], o);
+        const uint16_t* wt = is_q ? a.wq : a.wk;
+        if (wt && mine) {
+          const float r = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+          if (have_w != static_cast<int>(is_q)) {
+            have_w = is_q;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint64_t phase = p * a.turns[4 * u + e];
-          const float ang = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
-          sn[e] = __sinf(ang) * a.magnitude;
-          cs[e] = __cosf(ang) * a.magnitude;
+            for (int e = 0; e < 2; ++e) {
+              Run<R> v;
+#pragma unroll
+              for (int i = 0; i < R / 2; ++i) v.w[i] = __ldg(reinterpret_cast<const uint32_t*>(wt + (e ? o1 : o0)) + i);
+              widen_run<R, BF16>(v, w + e * R);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2 * R; ++e) y[j][e] = y[j][e] * r * w[e];
         }
       }
+      if (turned) {
+        if (ct[j] != have_t && item + j < end) {
+          have_t = ct[j];
+          const int32_t p = __ldg(a.pos + ct[j]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float& lo = HALF ? y[e] : y[2 * e];
-        float& hi = HALF ? y[4 + e] : y[2 * e + 1];
-        const float c = lo * cs[e] - hi * sn[e], s = hi * cs[e] + lo * sn[e];
-        lo = c;
-        hi = s;
+          for (int e = 0; e < R; ++e) {
+            // bits 32 .. 63 of position * turns
+            const uint32_t phase = __umulhi(static_cast<uint32_t>(p), turns_lo[e]) + static_cast<uint32_t>(p) * turns_hi[e] -
+                                   (p < 0 ? turns_lo[e] : 0u);
+            const float ang = static_cast<float>(static_cast<int32_t>(phase)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+            sn[e] = __sinf(ang) * a.magnitude;
+            cs[e] = __cosf(ang) * a.magnitude;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < R; ++e) {
+          float& lo = HALF ? y[j][e] : y[j][2 * e];
+          float& hi = HALF ? y[j][R + e] : y[j][2 * e + 1];
+          const float c = lo * cs[e] - hi * sn[e], s = hi * cs[e] + lo * sn[e];
+          lo = c;
+          hi = s;
+        }
       }
-    }
-    if (first + j < a.items && mine) {
-      uint16_t* dst = is_q ? a.qo + static_cast<int64_t>(t) * a.qos + static_cast<int64_t>(h) * a.d
-                           : a.ko + static_cast<int64_t>(t) * a.kos + static_cast<int64_t>(h - a.hq) * a.d;
-      const uint32_t p0 = pack_pair16<BF16>(y[0], y[1]), p1 = pack_pair16<BF16>(y[2], y[3]);
-      const uint32_t p2 = pack_pair16<BF16>(y[4], y[5]), p3 = pack_pair16<BF16>(y[6], y[7]);
-      if constexpr (HALF) {
-        st_global_v2(dst + o0, p0, p1);
-        st_global_v2(dst + o1, p2, p3);
-      } else {
-        st_global_v4(dst + o0, p0, p1, p2, p3);
+      if (item + j < end && mine) {
+        uint16_t* dst = is_q ? a.qo + static_cast<int64_t>(ct[j]) * a.qos + ch[j] * a.d
+                             : a.ko + static_cast<int64_t>(ct[j]) * a.kos + (ch[j] - a.hq) * a.d;
+        store_run<R>(dst + o0, narrow_run<R, BF16>(y[j]));
+        store_run<R>(dst + o1, narrow_run<R, BF16>(y[j] + R));
       }
     }
   }
 }
 
-template <int LG, bool BF16, bool HALF>
-cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t stream) {
+template <int R, int LG, bool BF16, bool HALF>
+cudaError_t launch_rope(RopeArgs& a, int sms, cudaStream_t stream) {
   constexpr uint32_t groups = kRopeThreads / LG;
-  // four heads a group where that still gives every SM two blocks of them
-  if (a.items >= groups * 4u * 2u * static_cast<uint32_t>(sms)) {
-    const uint32_t blocks = (a.items + groups * 4u - 1u) / (groups * 4u);
-    return launch_pdl(rope_kernel<LG, BF16, HALF, 4>, dim3(blocks), dim3(kRopeThreads), 0, stream, a);
-  }
-  const uint32_t blocks = (a.items + groups - 1u) / groups;
-  return launch_pdl(rope_kernel<LG, BF16, HALF, 1>, dim3(blocks), dim3(kRopeThreads), 0, stream, a);
+  // Chunks that give every SM kRopeBlocks blocks, whole pairs of heads; one
+  // head a group where there are fewer than that.
+  const uint32_t most = static_cast<uint32_t>(sms) * kRopeBlocks * groups;
+  a.chunk = a.items <= most ? 1u : ((a.items + most - 1u) / most + 1u) & ~1u;
+  const uint32_t per_block = groups * a.chunk, blocks = a.items / per_block + (a.items % per_block ? 1u : 0u);
+  return launch_pdl(rope_kernel<R, LG, BF16, HALF>, dim3(blocks), dim3(kRopeThreads), 0, stream, a);
 }
 
 template <bool BF16, bool HALF>
-cudaError_t launch_rope_lg(const RopeArgs& a, int sms, cudaStream_t stream) {
-  if (a.d <= 8) return launch_rope<1, BF16, HALF>(a, sms, stream);
-  if (a.d <= 16) return launch_rope<2, BF16, HALF>(a, sms, stream);
-  if (a.d <= 32) return launch_rope<4, BF16, HALF>(a, sms, stream);
-  if (a.d <= 64) return launch_rope<8, BF16, HALF>(a, sms, stream);
-  if (a.d <= 128) return launch_rope<16, BF16, HALF>(a, sms, stream);
-  return launch_rope<32, BF16, HALF>(a, sms, stream);
+cudaError_t launch_rope_lg(RopeArgs& a, int sms, cudaStream_t stream) {
+  if (a.d % 16 == 0 && a.rot % 16 == 0) {
+    if (a.d <= 16) return launch_rope<8, 1, BF16, HALF>(a, sms, stream);
+    if (a.d <= 32) return launch_rope<8, 2, BF16, HALF>(a, sms, stream);
+    if (a.d <= 64) return launch_rope<8, 4, BF16, HALF>(a, sms, stream);
+    if (a.d <= 128) return launch_rope<8, 8, BF16, HALF>(a, sms, stream);
+    return launch_rope<8, 16, BF16, HALF>(a, sms, stream);
+  }
+  if (a.d <= 64) return launch_rope<4, 8, BF16, HALF>(a, sms, stream);
+  if (a.d <= 128) return launch_rope<4, 16, BF16, HALF>(a, sms, stream);
+  return launch_rope<4, 32, BF16, HALF>(a, sms, stream);
 }
 
 bool rope_desc_ok(const attn_rope_desc_t& d, bool own_frequencies) {
@@ -302,6 +357,7 @@ gemm_status_t attn_rope_run(const attn_rope_plan_t* plan, const void* Q, int64_t
   a.items = static_cast<uint32_t>(tokens * heads);
   a.div_heads = lgt::magic_encode(static_cast<uint32_t>(heads));
   a.hq = d.q_heads;
+  a.heads = static_cast<int32_t>(heads);
   a.d = d.head_dim;
   a.rot = d.rot_dim;
   a.eps = d.eps;

@@ -162,16 +162,19 @@ def test_oracle_attention_is_the_dense_one():
     assert not out[:2].any() and np.allclose(out[2, 0], v[0, 0])
 
 
-def test_cache_attention_split_covers_every_tile_once():
-    """The runs of tiles partition them, no run is empty, and the CTAs that
-    take part in a range of tiles are exactly those between the owners of its
-    first and last."""
+def test_cache_attention_split_covers_every_unit_once():
+    """The CTAs' runs of units partition them and none is empty, the warps'
+    runs partition a CTA's, and the CTAs that take part in a range of units
+    are exactly those between the owners of its first and last."""
     rng = np.random.default_rng(1)
     for _ in range(300):
-        total, grid = int(rng.integers(1, 5000)), int(rng.integers(1, 400))
-        ctas = min(grid, total)
+        total, grid, warps = int(rng.integers(1, 5000)), int(rng.integers(1, 400)), int(rng.choice([8, 16]))
+        ctas = min(grid, max(total // warps, 1))
         start = [c * total // ctas for c in range(ctas + 1)]
         assert start[0] == 0 and start[-1] == total and all(a < b for a, b in zip(start, start[1:]))
+        for t0, t1 in zip(start, start[1:]):
+            runs = [t0 + (t1 - t0) * w // warps for w in range(warps + 1)]
+            assert runs[0] == t0 and runs[-1] == t1 and (total < warps or all(a < b for a, b in zip(runs, runs[1:])))
         owner = [((t + 1) * ctas - 1) // total for t in range(total)]
         for t in range(total):
             assert start[owner[t]] <= t < start[owner[t] + 1]
