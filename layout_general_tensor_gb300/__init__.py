@@ -431,27 +431,44 @@ class Attention:
             pass
 
 
-def _torch_dtype(dtype):
+_torch = None
+_raw_stream = None
+
+
+def _with_torch():
+    """The torch module and its function for a device's current stream
+    (imported at the first use: the rest of the binding does without)."""
+    global _torch, _raw_stream
     import torch
+    # (the plain way to the current stream costs 3.5 us a call on the host, a
+    # third of a small operator's whole call)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _torch_dtype(dtype):
+    torch = _torch or _with_torch()
     return torch.bfloat16 if dtype == GEMM_BF16 else torch.float16
 
 
 def _rows(what, name, t, heads, head_dim, dtype, rows=None):
-    """Check a [rows][heads][head_dim] device tensor of 16-bit values whose
-    heads are contiguous; returns its row stride in elements."""
+    """Check a [rows][heads][head_dim] device tensor of 16-bit values (dtype:
+    torch's) whose heads are contiguous; returns its row stride in elements."""
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{what}: {name} must be a CUDA tensor")
     shape, stride = t.shape, t.stride()
-    if t.dtype != _torch_dtype(dtype) or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or \
+    if t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or \
             (rows is not None and shape[0] != rows):
-        raise ValueError(f"{what}: {name} must be [{'rows' if rows is None else rows}][{heads}][{head_dim}] of "
-                         f"{_torch_dtype(dtype)}, got {tuple(shape)} of {t.dtype}")
-    if t.numel() == 0 or shape[0] == 1:
-        if t.numel() and (stride[2] != 1 or (heads > 1 and stride[1] != head_dim)):
-            raise ValueError(f"{what}: the heads of {name} must be contiguous")
+        raise ValueError(f"{what}: {name} must be [{'rows' if rows is None else rows}][{heads}][{head_dim}] of {dtype}, "
+                         f"got {tuple(shape)} of {t.dtype}")
+    if shape[0] == 0:
         return heads * head_dim
     if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
         raise ValueError(f"{what}: the heads of {name} must be contiguous")
+    if shape[0] == 1:
+        return heads * head_dim
     if stride[0] < heads * head_dim:  # (0 would ask the library for its default)
         raise ValueError(f"{what}: the rows of {name} overlap")
     return stride[0]
@@ -459,15 +476,18 @@ def _rows(what, name, t, heads, head_dim, dtype, rows=None):
 
 def _int32s(what, name, t, count):
     """Check a contiguous device vector of `count` int32."""
-    import torch
-    if not getattr(t, "is_cuda", False) or t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != count or \
+    if not getattr(t, "is_cuda", False) or t.dtype is not (_torch or _with_torch()).int32 or t.shape != (count,) or \
             not t.is_contiguous():
         raise ValueError(f"{what}: {name} must be a contiguous CUDA vector of {count} int32")
 
 
-def _stream(stream):
-    import torch
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+def _stream(stream, t):
+    """`stream`, or the current one of the device of tensor `t`."""
+    if stream is not None:
+        return stream
+    if _raw_stream is None:
+        _with_torch()
+    return _raw_stream(t.get_device())
 
 
 def attn_rope_frequencies(desc: attn_rope_desc_t):
@@ -503,24 +523,31 @@ class QKNormRope:
         st, h = attn_rope_create_status(self.desc, frequencies)
         _check(st, "attn_rope_create")
         self.plan = h
+        self.dtype = _torch_dtype(dtype)
 
     def run(self, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, stream=None):
         """q_out, k_out: may be q and k themselves.  positions: int32."""
         d, what = self.desc, "QKNormRope.run"
-        n = q.shape[0]
-        strides = [_rows(what, name, t, heads, d.head_dim, d.dtype, n)
-                   for name, t, heads in (("q", q, d.q_heads), ("k", k, d.k_heads), ("q_out", q_out, d.q_heads),
-                                          ("k_out", k_out, d.k_heads))]
+        dim, dtype, hq, hk, n = d.head_dim, self.dtype, d.q_heads, d.k_heads, q.shape[0]
+        qs = _rows(what, "q", q, hq, dim, dtype)
+        ks = _rows(what, "k", k, hk, dim, dtype, n)
+        qos = qs if q_out is q else _rows(what, "q_out", q_out, hq, dim, dtype, n)
+        kos = ks if k_out is k else _rows(what, "k_out", k_out, hk, dim, dtype, n)
         _int32s(what, "positions", positions, n)
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None and (not w.is_cuda or w.dtype != q.dtype or tuple(w.shape) != (d.head_dim,) or
-                                  not w.is_contiguous()):
-                raise ValueError(f"{what}: {name} must be a contiguous CUDA vector of {d.head_dim} {q.dtype}")
-        _check(_lib.attn_rope_run(self.plan, q.data_ptr() or None, strides[0], k.data_ptr() or None, strides[1],
-                                  q_weight.data_ptr() if q_weight is not None else None,
-                                  k_weight.data_ptr() if k_weight is not None else None,
-                                  positions.data_ptr() or None, n, q_out.data_ptr() or None, strides[2],
-                                  k_out.data_ptr() or None, strides[3], _stream(stream) or None), "attn_rope_run")
+        wq = wk = None
+        if q_weight is not None:
+            wq = self._weight("q_weight", q_weight)
+        if k_weight is not None:
+            wk = self._weight("k_weight", k_weight)
+        st = _lib.attn_rope_run(self.plan, q.data_ptr(), qs, k.data_ptr(), ks, wq, wk, positions.data_ptr(), n,
+                                q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream(stream, q))
+        if st:
+            _check(st, "attn_rope_run")
+
+    def _weight(self, name, w):
+        if not w.is_cuda or w.dtype is not self.dtype or w.shape != (self.desc.head_dim,) or not w.is_contiguous():
+            raise ValueError(f"QKNormRope.run: {name} must be a contiguous CUDA vector of {self.desc.head_dim} {self.dtype}")
+        return w.data_ptr()
 
     def close(self):
         if self.plan:
@@ -551,24 +578,28 @@ class PromptAttention:
         st, h = attn_prompt_create_status(self.desc)
         _check(st, "attn_prompt_create")
         self.plan = h
+        self.dtype = _torch_dtype(dtype)
 
     def run(self, q, k, v, cu_q, cu_k, out, stream=None):
         d, what = self.desc, "PromptAttention.run"
-        nq, nk = q.shape[0], k.shape[0]
-        sq = _rows(what, "q", q, d.q_heads, d.head_dim, d.dtype)
-        so = _rows(what, "out", out, d.q_heads, d.head_dim, d.dtype, nq)
-        sk = _rows(what, "k", k, d.k_heads, d.head_dim, d.dtype)
-        sv = _rows(what, "v", v, d.k_heads, d.head_dim, d.dtype, nk)
-        _int32s(what, "cu_q", cu_q, cu_q.shape[0])
-        _int32s(what, "cu_k", cu_k, cu_q.shape[0])
-        if cu_q.shape[0] < 1:
+        dim, dtype, hq, hk = d.head_dim, self.dtype, d.q_heads, d.k_heads
+        nq, nk, cus = q.shape[0], k.shape[0], cu_q.shape[0]
+        sq = _rows(what, "q", q, hq, dim, dtype)
+        so = _rows(what, "out", out, hq, dim, dtype, nq)
+        sk = _rows(what, "k", k, hk, dim, dtype)
+        sv = _rows(what, "v", v, hk, dim, dtype, nk)
+        _int32s(what, "cu_q", cu_q, cus)
+        _int32s(what, "cu_k", cu_k, cus)
+        if cus < 1:
             raise ValueError(f"{what}: cu_q and cu_k hold batch + 1 values")
-        _check(_lib.attn_prompt_run(self.plan, q.data_ptr() or None, sq, k.data_ptr() or None, sk,
-                                    v.data_ptr() or None, sv, cu_q.data_ptr(), cu_k.data_ptr(), cu_q.shape[0] - 1, nq,
-                                    nk, out.data_ptr() or None, so, _stream(stream) or None), "attn_prompt_run")
+        st = _lib.attn_prompt_run(self.plan, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, cu_q.data_ptr(),
+                                  cu_k.data_ptr(), cus - 1, nq, nk, out.data_ptr(), so, _stream(stream, q))
+        if st:
+            _check(st, "attn_prompt_run")
 
     def sync_status(self, stream=None) -> int:
-        return _lib.attn_prompt_sync_status(self.plan, _stream(stream) or None)
+        torch = _torch or _with_torch()
+        return _lib.attn_prompt_sync_status(self.plan, torch.cuda.current_stream().cuda_stream if stream is None else stream)
 
     def close(self):
         if self.plan:
@@ -607,31 +638,32 @@ class KVCache:
         made += [torch.zeros(pages, k_heads, page_size, dtype=torch.uint8, device=device) for _ in range(2)]
         return cls(*made)
 
-    def _dtype(self, what, t):
-        import torch
-        if t.dtype not in (torch.float16, torch.bfloat16):
-            raise ValueError(f"{what}: k and v must be float16 or bfloat16, got {t.dtype}")
-        return GEMM_BF16 if t.dtype == torch.bfloat16 else GEMM_F16
+    def _rows(self, what, k, v, slots):
+        """Check keys, values and slots; returns their count, row strides and type."""
+        torch = _torch or _with_torch()
+        dtype, n = k.dtype, k.shape[0]
+        if dtype is not torch.bfloat16 and dtype is not torch.float16:
+            raise ValueError(f"{what}: k and v must be float16 or bfloat16, got {dtype}")
+        sk = _rows(what, "k", k, self.k_heads, self.head_dim, dtype)
+        sv = _rows(what, "v", v, self.k_heads, self.head_dim, dtype, n)
+        _int32s(what, "slots", slots, n)
+        return n, sk, sv, GEMM_BF16 if dtype is torch.bfloat16 else GEMM_F16
 
     def write(self, k, v, slots, stream=None):
         """Quantise [token][k_heads][head_dim] keys and values into their slots (int32; negative: left out)."""
-        what = "KVCache.write"
-        dtype, n = self._dtype(what, k), k.shape[0]
-        sk = _rows(what, "k", k, self.k_heads, self.head_dim, dtype)
-        sv = _rows(what, "v", v, self.k_heads, self.head_dim, dtype, n)
-        _int32s(what, "slots", slots, n)
-        _check(_lib.attn_cache_write(self._ref, k.data_ptr() or None, sk, v.data_ptr() or None, sv,
-                                     slots.data_ptr() or None, n, dtype, _stream(stream) or None), "attn_cache_write")
+        n, sk, sv, dtype = self._rows("KVCache.write", k, v, slots)
+        st = _lib.attn_cache_write(self._ref, k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(), n, dtype,
+                                   _stream(stream, k))
+        if st:
+            _check(st, "attn_cache_write")
 
     def read(self, slots, k, v, stream=None):
         """The values of the slots into [token][k_heads][head_dim] tensors (zeros for a negative slot)."""
-        what = "KVCache.read"
-        dtype, n = self._dtype(what, k), k.shape[0]
-        sk = _rows(what, "k", k, self.k_heads, self.head_dim, dtype)
-        sv = _rows(what, "v", v, self.k_heads, self.head_dim, dtype, n)
-        _int32s(what, "slots", slots, n)
-        _check(_lib.attn_cache_read(self._ref, slots.data_ptr() or None, n, k.data_ptr() or None, sk,
-                                    v.data_ptr() or None, sv, dtype, _stream(stream) or None), "attn_cache_read")
+        n, sk, sv, dtype = self._rows("KVCache.read", k, v, slots)
+        st = _lib.attn_cache_read(self._ref, slots.data_ptr(), n, k.data_ptr(), sk, v.data_ptr(), sv, dtype,
+                                  _stream(stream, k))
+        if st:
+            _check(st, "attn_cache_read")
 
 
 class CacheAttention:
@@ -641,12 +673,13 @@ class CacheAttention:
 
     def __init__(self, q_heads, k_heads, head_dim, page_size, dtype=GEMM_BF16, scale=0.0, batch=64):
         self.q_heads, self.k_heads, self.head_dim, self.page_size = q_heads, k_heads, head_dim, page_size
-        self.dtype, self.scale = dtype, scale
+        self.dtype, self.scale, self.code = _torch_dtype(dtype), scale, dtype
+        self.shape = (k_heads, page_size, head_dim)
         self.workspace, self.ws_bytes, self.batch = None, 0, 0
         self._grow(batch)
 
     def _grow(self, batch):
-        import torch
+        torch = _torch
         n = ctypes.c_size_t()
         _check(_lib.attn_cache_attend_workspace_size(self.q_heads, self.k_heads, self.head_dim, batch,
                                                      ctypes.byref(n)), "attn_cache_attend_workspace_size")
@@ -658,24 +691,24 @@ class CacheAttention:
 
     def run(self, q, cache, page_table, lengths, out, stream=None):
         """q, out: [batch][q_heads][head_dim]; page_table: [batch][pages a sequence] int32; lengths: batch int32."""
-        import torch
-        what = "CacheAttention.run"
-        n = q.shape[0]
-        if (cache.k_heads, cache.head_dim, cache.page_size) != (self.k_heads, self.head_dim, self.page_size):
+        what, n, dim, hq = "CacheAttention.run", q.shape[0], self.head_dim, self.q_heads
+        if cache.k.shape[1:] != self.shape:
             raise ValueError(f"{what}: the cache has another shape than this was made for")
-        sq = _rows(what, "q", q, self.q_heads, self.head_dim, self.dtype)
-        so = _rows(what, "out", out, self.q_heads, self.head_dim, self.dtype, n)
+        sq = _rows(what, "q", q, hq, dim, self.dtype)
+        so = _rows(what, "out", out, hq, dim, self.dtype, n)
         _int32s(what, "lengths", lengths, n)
-        if not page_table.is_cuda or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
-                page_table.shape[0] != n or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        shape, pitch = page_table.shape, page_table.stride()
+        if not page_table.is_cuda or page_table.dtype is not _torch.int32 or len(shape) != 2 or shape[0] != n or \
+                (shape[1] > 1 and pitch[1] != 1):
             raise ValueError(f"{what}: page_table must be a CUDA tensor [{n}][pages] of int32 with contiguous rows")
         if n > self.batch:
             self._grow(n)
-        most = page_table.shape[1]
-        pitch = page_table.stride(0) if n > 1 else most
+        most = shape[1]
+        pitch = pitch[0] if n > 1 else most
         if pitch < most:
             raise ValueError(f"{what}: the rows of page_table overlap")
-        _check(_lib.attn_cache_attend(cache._ref, q.data_ptr() or None, sq, self.q_heads, page_table.data_ptr() or None,
-                                      pitch, most, lengths.data_ptr() or None, n, self.scale, self.dtype,
-                                      out.data_ptr() or None, so, self.workspace.data_ptr(), self.ws_bytes,
-                                      _stream(stream) or None), "attn_cache_attend")
+        st = _lib.attn_cache_attend(cache._ref, q.data_ptr(), sq, hq, page_table.data_ptr(), pitch, most,
+                                    lengths.data_ptr(), n, self.scale, self.code, out.data_ptr(), so,
+                                    self.workspace.data_ptr(), self.ws_bytes, _stream(stream, q))
+        if st:
+            _check(st, "attn_cache_attend")
