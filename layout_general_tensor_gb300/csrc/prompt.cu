@@ -79,8 +79,8 @@ struct PromptCfg {
   static constexpr uint32_t Q_OFF = 0;                // two tiles
   static constexpr uint32_t RING_OFF = 2 * TILE;
   static constexpr uint32_t BAR_OFF = RING_OFF + NS * TILE;
-  // full[NS], empty[NS], q_full[2], s_full[2], p_full[2], o_full[2], v_go[3], v_clean[3], teardown
-  static constexpr int NBARS = 2 * NS + 15;
+  // full[NS], empty[NS], q_full[2], s_full[2], p_full[2][2], o_full[2], v_go[3], v_clean[3], teardown
+  static constexpr int NBARS = 2 * NS + 17;
   static constexpr uint32_t MISC_OFF = BAR_OFF + ((NBARS * 8 + 15) & ~15);
   static constexpr uint32_t SMEM = MISC_OFF + 16 + 1024;  // slack for the 1024-byte alignment
   static constexpr uint32_t S_COL = 128;                  // between the tiles' S
@@ -226,7 +226,7 @@ __device__ __forceinline__ uint32_t spread_halves(uint32_t signs) { return (sign
 // Add the values of keys [from, to) that are not finite, columns col and
 // col + 1 of V, to a query's results.
 template <bool BF16>
-__device__ __noinline__ void add_odd(const PromptArgs& a, int key_row, int from, int to, int col, float& lo, float& hi) {
+__device__ __forceinline__ void add_odd(const PromptArgs& a, int key_row, int from, int to, int col, float& lo, float& hi) {
   for (int k = from; k < to; ++k) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(a.v + static_cast<int64_t>(key_row + k) * a.vs + col);
     const uint32_t bad = odd_halves<BF16>(w);
@@ -250,11 +250,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   auto empty = [&](int s) { return bar0 + 8u * (C::NS + s); };
   auto q_full = [&](int t) { return bar0 + 8u * (2 * C::NS + t); };
   auto s_full = [&](int t) { return bar0 + 8u * (2 * C::NS + 2 + t); };
-  auto p_full = [&](int t) { return bar0 + 8u * (2 * C::NS + 4 + t); };
-  auto o_full = [&](int t) { return bar0 + 8u * (2 * C::NS + 6 + t); };
-  auto v_go = [&](int i) { return bar0 + 8u * (2 * C::NS + 8 + i); };
-  auto v_clean = [&](int i) { return bar0 + 8u * (2 * C::NS + 11 + i); };
-  const uint32_t teardown = bar0 + 8u * (2 * C::NS + 14);
+  auto p_full = [&](int t, int half) { return bar0 + 8u * (2 * C::NS + 4 + 2 * t + half); };
+  auto o_full = [&](int t) { return bar0 + 8u * (2 * C::NS + 8 + t); };
+  auto v_go = [&](int i) { return bar0 + 8u * (2 * C::NS + 10 + i); };
+  auto v_clean = [&](int i) { return bar0 + 8u * (2 * C::NS + 13 + i); };
+  const uint32_t teardown = bar0 + 8u * (2 * C::NS + 16);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   volatile int* odd_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);  // V held values that are not finite
@@ -268,7 +268,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);  // the tile's softmax warps
+      mbar_init(p_full(t, 0), 4);  // the tile's softmax warps
+      mbar_init(p_full(t, 1), 4);
       mbar_init(o_full(t), 1);
     }
     for (int i = 0; i < 3; ++i) {
@@ -373,14 +374,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int t, int n, bool first, bool last) {
+    auto issue_pv = [&](int t, int n, int half, bool first, bool last) {
       if (leader) {
         const uint64_t vd = sw128_desc(base + C::RING_OFF + (n % C::NS) * C::TILE, C::CHUNK, 1024u);
         const uint32_t dst = tmem + C::O_COL + t * D, pa = tmem + C::P_COL + t * C::P_STEP;
         // 16 keys are 2 KiB of V and 8 columns of P
 #pragma unroll
-        for (int k = 0; k < kPrKeys / 16; ++k)
-          mma_ts(dst, pa + k * 8, vd + static_cast<uint64_t>(k * 2048u >> 4), a.idesc_pv, (first && k == 0) ? 0u : 1u);
+        for (int i = 0; i < kPrKeys / 32; ++i) {
+          const uint32_t k = half * (kPrKeys / 32) + i;
+          mma_ts(dst, pa + k * 8, vd + static_cast<uint64_t>(k * 2048u >> 4), a.idesc_pv, (first && i == 0) ? 0u : 1u);
+        }
         if (last) tc_commit(o_full(t));
       }
       __syncwarp();
@@ -407,9 +410,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (j < blocks[t]) {
-          if (!wait(p_full(t), j & 1)) break;
+          if (!wait(p_full(t, 0), j & 1)) break;
           tc_fence_after();
-          issue_pv(t, vn, j == 0, j + 1 == blocks[t]);
+          issue_pv(t, vn, 0, j == 0, false);
+          if (!wait(p_full(t, 1), j & 1)) break;
+          tc_fence_after();
+          issue_pv(t, vn, 1, false, j + 1 == blocks[t]);
         }
         if (t == 1) commit(empty(vn % C::NS));
         if (j + 1 < blocks[t]) issue_s(t, kn);
@@ -472,70 +478,85 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         break;
       }
       tc_fence_after();
-      uint32_t sv[128];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        tc_ld_32x32b_x32(s_addr + 32u * i, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * i));
-      tc_wait_ld_regs(sv);
+      // The first half of P against the reference as it stands, while the
+      // block's maximum is found; in the rare block that exceeds the
+      // reference by 2^kPrLazy in some row (and the first), the reference
+      // moves and the half is made again.
       const int valid = vis - j * kPrKeys;
-      if (__any_sync(0xffffffffu, valid < kPrKeys)) {
+      const bool masked = __any_sync(0xffffffffu, valid < kPrKeys);
+      const float2 cs2 = make_float2(a.cs, a.cs);
+      float2 sum[4];
+      uint32_t sv[128], pk[32];
+      while (true) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (i >= valid) sv[i] = __float_as_uint(-INFINITY);
-      }
-      float mp[4];
+        for (int i = 0; i < 4; ++i)
+          tc_ld_32x32b_x32(s_addr + 32u * i, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * i));
+        tc_wait_ld_regs(sv);
+        if (masked) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) mp[u] = __uint_as_float(sv[u]);
-#pragma unroll
-      for (int i = 4; i + 7 < 128; i += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          mp[u] = max3(mp[u], __uint_as_float(sv[i + 2 * u]), __uint_as_float(sv[i + 2 * u + 1]));
-#pragma unroll
-      for (int u = 0; u < 4; ++u) mp[u] = fmaxf(mp[u], __uint_as_float(sv[124 + u]));
-      const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * a.cs;
-      float alpha = 1.0f;
-      if (mx > m + kPrLazy) {  // always at the first block with a visible key
-        alpha = ex2(m - mx);
-        m = mx;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, alpha < 1.0f)) {
-        // the product before has completed: this S was issued after it by
-        // the same thread, and its barrier covers all that was issued before
-        l *= alpha;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          tc_ld_32x32b_x32(o_addr + c, v);
-          tc_wait_ld_regs(v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-          st_tmem_x32(o_addr + c, v);
+          for (int i = 0; i < 128; ++i)
+            if (i >= valid) sv[i] = __float_as_uint(-INFINITY);
         }
-        st_tmem_wait();
-      }
-      // (a row that has seen no key keeps weights of 2^-inf = 0)
-      const float ref = m == -INFINITY ? 0.0f : m;
-      const float2 cs2 = make_float2(a.cs, a.cs), neg = make_float2(-ref, -ref);
-      float2 sum[4] = {};
-      uint32_t pk[32];
+        // (a row that has seen no key keeps weights of 2^-inf = 0)
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const float2 neg = make_float2(-ref, -ref);
+        float mp[4];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
+        for (int u = 0; u < 4; ++u) {
+          sum[u] = make_float2(0.0f, 0.0f);
+          mp[u] = -INFINITY;
+        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float2 x = fma2(make_float2(__uint_as_float(sv[64 * hh + 2 * i]), __uint_as_float(sv[64 * hh + 2 * i + 1])), cs2, neg);
+          const float2 x = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), cs2, neg);
           const float2 e = make_float2(ex2(x.x), ex2(x.y));
           sum[i & 3] = add2(sum[i & 3], e);
           pk[i] = pack_pair16<BF16>(e.x, e.y);
+          mp[i & 3] = max3(mp[i & 3], __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+          mp[i & 3] = max3(mp[i & 3], __uint_as_float(sv[64 + 2 * i]), __uint_as_float(sv[64 + 2 * i + 1]));
         }
-        st_tmem_x32(p_addr + 32u * hh, pk);
+        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * a.cs;
+        const bool over = mx > m + kPrLazy;
+        if (!__any_sync(0xffffffffu, over)) break;
+        const float alpha = over ? ex2(m - mx) : 1.0f;  // 0 at the first block with a visible key
+        if (over) m = mx;
+        l *= alpha;
+        if (j > 0) {
+          // the product before has completed: this S was issued after it by
+          // the same thread, and its barrier covers all that was issued before
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            tc_ld_32x32b_x32(o_addr + c, v);
+            tc_wait_ld_regs(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            st_tmem_x32(o_addr + c, v);
+          }
+          st_tmem_wait();
+        }
       }
-      const float2 s4 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-      l += s4.x + s4.y;
+      st_tmem_x32(p_addr, pk);
       st_tmem_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(t));
+      if (lane == 0) mbar_arrive(p_full(t, 0));
+      const float ref = m == -INFINITY ? 0.0f : m;
+      const float2 neg = make_float2(-ref, -ref);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 x = fma2(make_float2(__uint_as_float(sv[64 + 2 * i]), __uint_as_float(sv[64 + 2 * i + 1])), cs2, neg);
+        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+        sum[i & 3] = add2(sum[i & 3], e);
+        pk[i] = pack_pair16<BF16>(e.x, e.y);
+      }
+      st_tmem_x32(p_addr + 32u, pk);
+      st_tmem_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(t, 1));
+      const float2 s4 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+      l += s4.x + s4.y;
     }
     if (ok && my_blocks > 0) ok = warp_wait(o_full(t), 0, a.wait_limit_ns, abort_flag);
     if (ok) {
