@@ -353,14 +353,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 0);
   } else if (warp == 9) {
     // ----------------------------------------------------------- products
-    const bool leader = elect_one();
-    bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = warp_wait(bar, parity, a.wait_limit_ns, abort_flag);
-      return ok;
-    };
-    auto issue_s = [&](int t, int n) {
-      if (leader) {
+    // One thread does it all.  The tensor core takes the products in the
+    // order of their issue, so the order is the schedule: P V of a tile as
+    // its halves of P come, then the tile's next S, then the other tile's.
+    // Waits on loads stand before products that queue up anyway.
+    if (elect_one()) {
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = mbar_wait_bounded(bar, parity, a.wait_limit_ns, abort_flag);
+        return ok;
+      };
+      auto wait_full = [&](int n) { return wait(full(n % C::NS), (n / C::NS) & 1); };
+      auto issue_s = [&](int t, int n) {
         const uint32_t kb = base + C::RING_OFF + (n % C::NS) * C::TILE, qb = base + C::Q_OFF + t * C::TILE;
         // 16 values of d are 32 bytes further in a 64-value chunk
         const uint64_t qd = sw128_desc(qb, 16u, 1024u), kd = sw128_desc(kb, 16u, 1024u);
@@ -371,11 +375,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           tc_mma_f16_ss(dst, qd + off, kd + off, a.idesc_s, k > 0 ? 1u : 0u);
         }
         tc_commit(s_full(t));
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int t, int n, int half, bool first, bool last) {
-      if (leader) {
+      };
+      auto issue_pv = [&](int t, int n, int half, bool first) {
         const uint64_t vd = sw128_desc(base + C::RING_OFF + (n % C::NS) * C::TILE, C::CHUNK, 1024u);
         const uint32_t dst = tmem + C::O_COL + t * D, pa = tmem + C::P_COL + t * C::P_STEP;
         // 16 keys are 2 KiB of V and 8 columns of P
@@ -384,46 +385,44 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           const uint32_t k = half * (kPrKeys / 32) + i;
           mma_ts(dst, pa + k * 8, vd + static_cast<uint64_t>(k * 2048u >> 4), a.idesc_pv, (first && i == 0) ? 0u : 1u);
         }
-        if (last) tc_commit(o_full(t));
-      }
-      __syncwarp();
-    };
-    auto commit = [&](uint32_t bar) {
-      if (leader) tc_commit(bar);
-      __syncwarp();
-    };
-    if (nb > 0 && wait(full(0), 0)) {
+      };
+      if (nb > 0 && wait_full(0)) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (blocks[t] > 0 && wait(q_full(t), 0)) {
-          tc_fence_after();
-          issue_s(t, 0);
-        }
-      if (ok) commit(empty(0));
-    }
-    for (int j = 0; ok && j < nb; ++j) {
-      const int vn = 2 * j + 1, kn = 2 * j + 2;
-      if (!wait(full(vn % C::NS), (vn / C::NS) & 1)) break;
-      if (j >= mixed && !wait(v_clean(j - mixed), 0)) break;
-      if (j + 1 < nb && !wait(full(kn % C::NS), (kn / C::NS) & 1)) break;
-      tc_fence_after();
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (j < blocks[t]) {
-          if (!wait(p_full(t, 0), j & 1)) break;
-          tc_fence_after();
-          issue_pv(t, vn, 0, j == 0, false);
-          if (!wait(p_full(t, 1), j & 1)) break;
-          tc_fence_after();
-          issue_pv(t, vn, 1, false, j + 1 == blocks[t]);
-        }
-        if (t == 1) commit(empty(vn % C::NS));
-        if (j + 1 < blocks[t]) issue_s(t, kn);
+        for (int t = 0; t < 2; ++t)
+          if (blocks[t] > 0 && wait(q_full(t), 0)) {
+            tc_fence_after();
+            issue_s(t, 0);
+          }
+        if (ok) tc_commit(empty(0));
+        wait_full(1);
       }
-      if (ok && j + 1 < nb) commit(empty(kn % C::NS));
+      for (int j = 0; ok && j < nb; ++j) {
+        const int vn = 2 * j + 1, kn = 2 * j + 2;
+        if (j >= mixed && !wait(v_clean(j - mixed), 0)) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j < blocks[t]) {
+            if (!wait(p_full(t, 0), j & 1)) break;
+            tc_fence_after();
+            issue_pv(t, vn, 0, j == 0);
+            if (t == 0 && j + 1 < nb && !wait_full(kn)) break;
+            if (!wait(p_full(t, 1), j & 1)) break;
+            tc_fence_after();
+            issue_pv(t, vn, 1, false);
+            if (j + 1 == blocks[t]) tc_commit(o_full(t));
+          } else if (t == 0 && j + 1 < nb && !wait_full(kn)) {
+            break;
+          }
+          if (t == 1) tc_commit(empty(vn % C::NS));
+          if (t == 1 && j + 1 < nb && !wait_full(vn + 2)) break;
+          if (j + 1 < blocks[t]) issue_s(t, kn);
+        }
+        if (ok && j + 1 < nb) tc_commit(empty(kn % C::NS));
+      }
+      if (!ok && !*abort_flag) prompt_timeout(a, abort_flag, 1);
+      tc_commit(teardown);  // every product is done before the tensor memory is freed
     }
-    if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 1);
-    commit(teardown);  // every product is done before the tensor memory is freed
+    __syncwarp();
   } else if (warp >= 10) {
     // ------------------------------------------- rows of V that not all see
     for (int j = mixed; j < nb; ++j) {
