@@ -14,15 +14,22 @@
 //   P = 2^(s - m)  one row a thread, the 128 logits of a block in registers,
 //                  so no maximum or sum crosses threads; m is a reference
 //                  that is moved (and O rescaled) only when a block exceeds
-//                  it by 2^8; P goes back to tensor memory in 16 bits.
+//                  it by 2^8; P goes back to tensor memory in 16 bits, each
+//                  half as soon as it is made.
 //   O += P V       tcgen05, A = P from tensor memory, B = V as it lies
 //                  (MN-major).
 // The two tiles alternate: while the tensor core works on one tile's
 // products, the other tile's softmax runs.
 //
+// Work.  A unit is 2T tokens of a sequence and a key head.  The grid has a
+// block for every unit, the ones with the most keys of a sequence first; a
+// running CTA takes over blocks that have not started (cluster launch
+// control), so that it loads the next unit's tiles and issues their first
+// products while the softmax warps still write the last unit's result.
+//
 // Warps (384 threads): 0-3 softmax of tile 0, 4-7 of tile 1, 8 loads, 9 issues
-// the products, 10 and 11 look over the rows of V that some query of the CTA
-// must not see, since a weight of 0 does not cancel an infinity or a NaN: rows
+// the products, 11 finds the units, 10 looks over the rows of V that some
+// query of the CTA must not see, since a weight of 0 does not cancel an infinity or a NaN: rows
 // that no query sees (later ones, or the next sequence's) are cleared; in the
 // others (2T at most) values that are not finite are, and are added to the
 // results of the queries that do see them at the end, where a sum with a
@@ -38,6 +45,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <new>
+#include <type_traits>
 
 #include "attn_prompt.h"
 #include "half_types.cuh"
@@ -48,7 +56,7 @@
 namespace lgt {
 namespace {
 
-constexpr int kPrThreads = 384;
+constexpr int kPrThreads = 384;  // 168 registers each
 constexpr int kPrRows = 128;   // rows of a tile
 constexpr int kPrKeys = 128;   // keys of a block
 constexpr int kPrTimeout = GEMM_ERR_TIMEOUT;
@@ -71,17 +79,51 @@ struct PromptArgs {
   uint32_t idesc_s, idesc_pv;
 };
 
+// What a CTA works on, 2T tokens of one sequence and key head, and what
+// follows from that for its tiles and blocks of keys.
+struct PromptUnit {
+  int row0, tokens;        // first row of Q, tokens (1 .. 2T); 0: nothing, -1: no more units
+  int key_row, nk;         // first row of K and V, keys
+  int shift;               // token i of the unit sees keys <= i + shift
+  int h;                   // key head
+  int toks[2], blocks[2];  // tokens of the tiles, blocks with keys that they see
+  int nb;                  // blocks of the unit
+  // keys that every token sees, and that any does; the blocks from `mixed` on
+  // (three at most: they span 2T keys) hold some that not all see
+  int all_see, any_sees, mixed;
+  int odd;                 // V held values that are not finite
+  int pad;
+};
+static_assert(sizeof(PromptUnit) == 64, "two of them in shared memory");
+
+__device__ __forceinline__ void shape_unit(const PromptArgs& a, PromptUnit& x) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    x.toks[t] = min(max(x.tokens - t * a.tok, 0), a.tok);
+    const int last = t * a.tok + x.toks[t] - 1;
+    const int vis = x.toks[t] == 0 ? 0 : a.causal ? min(max(last + x.shift + 1, 0), x.nk) : x.nk;
+    x.blocks[t] = (vis + kPrKeys - 1) / kPrKeys;
+  }
+  x.nb = max(x.blocks[0], x.blocks[1]);
+  x.all_see = a.causal ? min(max(x.shift + 1, 0), x.nk) : x.nk;
+  x.any_sees = a.causal ? min(max(x.tokens + x.shift, 0), x.nk) : x.nk;
+  x.mixed = x.all_see / kPrKeys;
+}
+
 template <int D>
 struct PromptCfg {
   static constexpr uint32_t CHUNK = 128u * 128u;      // 64 values of 128 rows
   static constexpr uint32_t TILE = (D / 64) * CHUNK;  // a tile of Q, K or V
-  static constexpr int NS = D == 128 ? 5 : 9;         // ring of K and V tiles, in the order they are used
+  static constexpr int NS = 4;                        // ring of K and V tiles, in the order they are used
   static constexpr uint32_t Q_OFF = 0;                // two tiles
   static constexpr uint32_t RING_OFF = 2 * TILE;
   static constexpr uint32_t BAR_OFF = RING_OFF + NS * TILE;
-  // full[NS], empty[NS], q_full[2], s_full[2], p_full[2][2], o_full[2], v_go[3], v_clean[3], teardown
-  static constexpr int NBARS = 2 * NS + 17;
-  static constexpr uint32_t MISC_OFF = BAR_OFF + ((NBARS * 8 + 15) & ~15);
+  // full[NS], empty[NS], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], v_go[2][3], v_clean[2][3],
+  // unit_full[2], unit_empty[2], taken, teardown
+  static constexpr int NBARS = 2 * NS + 30;
+  static constexpr uint32_t TAKEN_OFF = BAR_OFF + ((NBARS * 8 + 15) & ~15);  // 16 bytes: a block taken over
+  static constexpr uint32_t UNIT_OFF = TAKEN_OFF + 16;                       // two PromptUnit
+  static constexpr uint32_t MISC_OFF = UNIT_OFF + 2 * sizeof(PromptUnit);
   static constexpr uint32_t SMEM = MISC_OFF + 16 + 1024;  // slack for the 1024-byte alignment
   static constexpr uint32_t S_COL = 128;                  // between the tiles' S
   static constexpr uint32_t O_COL = 256;
@@ -158,24 +200,49 @@ __device__ __forceinline__ void prompt_timeout(const PromptArgs& a, volatile int
   if (atomicCAS(&a.status->code, 0, kPrTimeout) == 0) a.status->where = where;
 }
 
+// The bounded wait, all but its first try out of line: it stands at many
+// places, in code that several warps run through at once.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+  return mbar_wait_bounded(bar, parity, limit_ns, abort_flag);
+}
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || wait_on(bar, parity, limit_ns, abort_flag);
+}
+
 // A bounded wait whose outcome is the whole warp's: a lane that gave up while
 // another saw the phase complete would part from it at the next warp barrier.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns, abort_flag));
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, limit_ns, abort_flag));
 }
 
-// What a CTA works on: 2T tokens of one sequence and key head.
-struct PromptUnit {
-  int row0, tokens;     // first row of Q, tokens (1 .. 2T); 0: nothing
-  int key_row, nk;      // first row of K and V, keys
-  int shift;            // token i of the unit sees keys <= i + shift
-};
+// Ask for a block of the grid that has not started; the answer's 16 bytes
+// arrive at `dst` and complete on `bar`.
+__device__ __forceinline__ void take_block(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+               "r"(bar)
+               : "memory");
+}
+// Its index, or -1 where there is none.
+__device__ __forceinline__ int64_t taken_block(uint32_t src) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(src)
+      : "memory");
+  return ok ? static_cast<int64_t>(x) : -1;
+}
 
 // Unit `u` of the list (sequences in order, each one's last tokens -- the
 // most keys -- first); every lane of the warp returns the same.
 __device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u) {
   const int lane = threadIdx.x & 31;
-  PromptUnit r{0, 0, 0, 0, 0};
+  PromptUnit r{};
   uint32_t before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const int b = b0 + lane;
@@ -223,17 +290,37 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
 // All bits of the halves whose sign bits are set.
 __device__ __forceinline__ uint32_t spread_halves(uint32_t signs) { return (signs >> 15) * 0xffffu; }
 
-// Add the values of keys [from, to) that are not finite, columns col and
-// col + 1 of V, to a query's results.
+// Add the values of 32 columns of V (at `p`) that are not finite to a row's
+// sums.  (They stay what they are, or become NaN, in the division by the
+// row's sum of weights.)
 template <bool BF16>
-__device__ __forceinline__ void add_odd(const PromptArgs& a, int key_row, int from, int to, int col, float& lo, float& hi) {
-  for (int k = from; k < to; ++k) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(a.v + static_cast<int64_t>(key_row + k) * a.vs + col);
-    const uint32_t bad = odd_halves<BF16>(w);
-    const float2 x = unpack_pair16<BF16>(w);
-    if (bad & 0x8000u) lo += x.x;
-    if (bad & 0x80000000u) hi += x.y;
+__device__ __forceinline__ void add_odd(const uint16_t* p, uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t x = reinterpret_cast<const uint32_t*>(p)[i];
+    const uint32_t bad = odd_halves<BF16>(x);
+    const float2 y = unpack_pair16<BF16>(x);
+    if (bad & 0x8000u) v[2 * i] = __float_as_uint(__uint_as_float(v[2 * i]) + y.x);
+    if (bad & 0x80000000u) v[2 * i + 1] = __float_as_uint(__uint_as_float(v[2 * i + 1]) + y.y);
   }
+}
+
+// Four lanes' 16-byte pieces (four of four words each) transposed: lane q
+// gets piece q of its neighbours' rows 0 .. 3.
+__device__ __forceinline__ void exchange4(uint32_t (&y)[16], int lane) {
+  const bool up2 = lane & 2, up1 = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, up2 ? y[i] : y[i + 8], 2);
+    if (up2) y[i] = got; else y[i + 8] = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up1 ? y[i + e] : y[i + 4 + e], 1);
+      if (up1) y[i + e] = got; else y[i + 4 + e] = got;
+    }
 }
 
 template <int D, bool BF16>
@@ -248,16 +335,23 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   const uint32_t bar0 = base + C::BAR_OFF;
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (C::NS + s); };
-  auto q_full = [&](int t) { return bar0 + 8u * (2 * C::NS + t); };
-  auto s_full = [&](int t) { return bar0 + 8u * (2 * C::NS + 2 + t); };
-  auto p_full = [&](int t, int half) { return bar0 + 8u * (2 * C::NS + 4 + 2 * t + half); };
-  auto o_full = [&](int t) { return bar0 + 8u * (2 * C::NS + 8 + t); };
-  auto v_go = [&](int i) { return bar0 + 8u * (2 * C::NS + 10 + i); };
-  auto v_clean = [&](int i) { return bar0 + 8u * (2 * C::NS + 13 + i); };
-  const uint32_t teardown = bar0 + 8u * (2 * C::NS + 16);
+  constexpr int kB = 2 * C::NS;
+  auto q_full = [&](int t) { return bar0 + 8u * (kB + t); };
+  auto q_empty = [&](int t) { return bar0 + 8u * (kB + 2 + t); };
+  auto s_full = [&](int t) { return bar0 + 8u * (kB + 4 + t); };
+  auto p_full = [&](int t, int half) { return bar0 + 8u * (kB + 6 + 2 * t + half); };
+  auto o_full = [&](int t) { return bar0 + 8u * (kB + 10 + t); };
+  // (of even and odd units: a unit is taken up only when nobody is at the one
+  // before the last, so no wait can be two phases behind)
+  auto v_go = [&](int i) { return bar0 + 8u * (kB + 12 + i); };
+  auto v_clean = [&](int i) { return bar0 + 8u * (kB + 18 + i); };
+  auto unit_full = [&](int i) { return bar0 + 8u * (kB + 24 + i); };
+  auto unit_empty = [&](int i) { return bar0 + 8u * (kB + 26 + i); };
+  const uint32_t taken = bar0 + 8u * (kB + 28);
+  const uint32_t teardown = bar0 + 8u * (kB + 29);
+  PromptUnit* units = reinterpret_cast<PromptUnit*>(smem + C::UNIT_OFF);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
-  volatile int* odd_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);  // V held values that are not finite
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -267,18 +361,21 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
+      mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t, 0), 4);  // the tile's softmax warps
       mbar_init(p_full(t, 1), 4);
       mbar_init(o_full(t), 1);
+      mbar_init(unit_full(t), 1);
+      mbar_init(unit_empty(t), 11);  // eight softmax warps, loads, products, V
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 6; ++i) {
       mbar_init(v_go(i), 1);
-      mbar_init(v_clean(i), 2);  // both looking warps
+      mbar_init(v_clean(i), 1);
     }
+    mbar_init(taken, 1);
     mbar_init(teardown, 1);
     *abort_flag = 0;
-    *odd_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&a.tm_q);
@@ -295,61 +392,56 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
-  uint32_t unit, h;
-  magic_divmod(blockIdx.x, a.div_hk, unit, h);
-  const PromptUnit w = find_unit(a, unit);
-  // tokens, visible keys and blocks of the two tiles
-  int toks[2], blocks[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    toks[t] = min(max(w.tokens - t * a.tok, 0), a.tok);
-    const int last = t * a.tok + toks[t] - 1;
-    const int vis = toks[t] == 0 ? 0 : a.causal ? min(max(last + w.shift + 1, 0), w.nk) : w.nk;
-    blocks[t] = (vis + kPrKeys - 1) / kPrKeys;
-  }
-  const int nb = max(blocks[0], blocks[1]);
-  // keys that every token of the CTA sees, and that any does; the blocks from
-  // `mixed` on (three at most: they span 2T keys) hold some that not all see
-  const int all_see = a.causal ? min(max(w.shift + 1, 0), w.nk) : w.nk;
-  const int any_sees = a.causal ? min(max(w.tokens + w.shift, 0), w.nk) : w.nk;
-  const int mixed = all_see / kPrKeys;
-
-  int issued = 0;  // loads of the ring that were issued (warp 8)
-  bool q_issued = false;
+  // Every role walks the same list of units; it and every ring and barrier go
+  // on from one unit to the next, so each role counts its own uses of them.
+  const uint64_t limit = a.wait_limit_ns;
+  auto unit_ready = [&](int it) { return warp_wait(unit_full(it & 1), (it >> 1) & 1, limit, abort_flag); };
+  int issued = 0;                 // loads of the ring (warp 8)
+  int q_uses[2] = {0, 0};         // loads of Q (warp 8)
+  int asked = 0;                  // blocks asked for (warp 11)
 
   if (warp == 8) {
     // -------------------------------------------------------------- loads
     const bool leader = elect_one();
     bool ok = true;
-    auto load_q = [&](int t) {
-      if (!leader || blocks[t] == 0) return;
-      mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tok * a.group) * 128u * (D / 64));
+    for (int it = 0; ok; ++it) {
+      if (!(ok = unit_ready(it))) break;
+      const PromptUnit w = units[it & 1];
+      if (w.tokens < 0) break;
+      for (int n = 0; ok && n < 2 * w.nb; ++n) {
+        const int s = issued % C::NS;
+        if (issued >= C::NS && !(ok = warp_wait(empty(s), ((issued / C::NS) - 1) & 1, limit, abort_flag))) break;
+        if (leader) {
+          mbar_arrive_expect_tx(full(s), C::TILE);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_3d(base + C::Q_OFF + t * C::TILE + c * C::CHUNK, &a.tm_q, q_full(t), c * 64,
-                    static_cast<int32_t>(h) * a.group, w.row0 + t * a.tok);
-    };
-    load_q(0);
-    for (int n = 0; ok && n < 2 * nb; ++n) {
-      const int s = n % C::NS;
-      if (n >= C::NS && !warp_wait(empty(s), ((n / C::NS) - 1) & 1, a.wait_limit_ns, abort_flag)) {
-        ok = false;
-        break;
-      }
-      if (leader) {
-        mbar_arrive_expect_tx(full(s), C::TILE);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(base + C::RING_OFF + s * C::TILE + c * C::CHUNK, (n & 1) ? &a.tm_v : &a.tm_k, full(s), c * 64,
+                        w.h, w.key_row + (n >> 1) * kPrKeys);
+        }
+        __syncwarp();
+        ++issued;
+        // (only now, so that the looker waits for this load's phase and no earlier one)
+        if (const int i = (n >> 1) - w.mixed; (n & 1) && i >= 0 && leader) mbar_arrive(v_go((it & 1) * 3 + i));
+        if (n == 0) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(base + C::RING_OFF + s * C::TILE + c * C::CHUNK, (n & 1) ? &a.tm_v : &a.tm_k, full(s), c * 64,
-                      static_cast<int32_t>(h), w.key_row + (n >> 1) * kPrKeys);
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || w.blocks[t] == 0) continue;
+            // (the last products that read this tile of Q are done)
+            if (q_uses[t] > 0 && !(ok = warp_wait(q_empty(t), (q_uses[t] - 1) & 1, limit, abort_flag))) continue;
+            if (leader) {
+              mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tok * a.group) * 128u * (D / 64));
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(base + C::Q_OFF + t * C::TILE + c * C::CHUNK, &a.tm_q, q_full(t), c * 64, w.h * a.group,
+                            w.row0 + t * a.tok);
+            }
+            __syncwarp();
+            ++q_uses[t];
+          }
+        }
       }
-      __syncwarp();
-      issued = n + 1;
-      // (only now, so that the lookers wait for this load's phase and no earlier one)
-      if ((n & 1) && (n >> 1) >= mixed && leader) mbar_arrive(v_go((n >> 1) - mixed));
-      if (n == 0) load_q(1);
+      if (lane == 0) mbar_arrive(unit_empty(it & 1));
     }
-    q_issued = true;
     if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 0);
   } else if (warp == 9) {
     // ----------------------------------------------------------- products
@@ -360,103 +452,196 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     if (elect_one()) {
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = mbar_wait_bounded(bar, parity, a.wait_limit_ns, abort_flag);
+        if (ok) ok = wait_bounded(bar, parity, limit, abort_flag);
         return ok;
       };
-      auto wait_full = [&](int n) { return wait(full(n % C::NS), (n / C::NS) & 1); };
-      auto issue_s = [&](int t, int n) {
-        const uint32_t kb = base + C::RING_OFF + (n % C::NS) * C::TILE, qb = base + C::Q_OFF + t * C::TILE;
-        // 16 values of d are 32 bytes further in a 64-value chunk
-        const uint64_t qd = sw128_desc(qb, 16u, 1024u), kd = sw128_desc(kb, 16u, 1024u);
+      // (this thread is the pace of the CTA: blocks are taken by turns with the
+      // ring's two places for K and for V, so that every address is a constant
+      // in the code of its turn)
+      auto wait_full = [&](int slot, uint32_t block) { return wait(full(slot), (block >> 1) & 1u); };
+      // 16 values of d are 32 bytes further in a 64-value chunk
+      const uint64_t q_desc = sw128_desc(base + C::Q_OFF, 16u, 1024u), k_desc = sw128_desc(base + C::RING_OFF, 16u, 1024u);
+      const uint64_t v_desc = sw128_desc(base + C::RING_OFF, C::CHUNK, 1024u);
+      const uint32_t idesc_s = a.idesc_s, idesc_pv = a.idesc_pv;
+      auto issue_s = [&](int t, int slot) {
+        const uint64_t qd = q_desc + t * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
         const uint32_t dst = tmem + t * C::S_COL;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32u) >> 4;
-          tc_mma_f16_ss(dst, qd + off, kd + off, a.idesc_s, k > 0 ? 1u : 0u);
+          tc_mma_f16_ss(dst, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
         }
         tc_commit(s_full(t));
       };
-      auto issue_pv = [&](int t, int n, int half, bool first) {
-        const uint64_t vd = sw128_desc(base + C::RING_OFF + (n % C::NS) * C::TILE, C::CHUNK, 1024u);
+      auto issue_pv = [&](int t, int slot, int half, bool first) {
+        const uint64_t vd = v_desc + slot * (C::TILE >> 4);
         const uint32_t dst = tmem + C::O_COL + t * D, pa = tmem + C::P_COL + t * C::P_STEP;
         // 16 keys are 2 KiB of V and 8 columns of P
 #pragma unroll
         for (int i = 0; i < kPrKeys / 32; ++i) {
           const uint32_t k = half * (kPrKeys / 32) + i;
-          mma_ts(dst, pa + k * 8, vd + static_cast<uint64_t>(k * 2048u >> 4), a.idesc_pv, (first && i == 0) ? 0u : 1u);
+          mma_ts(dst, pa + k * 8, vd + static_cast<uint64_t>(k * 2048u >> 4), idesc_pv, (first && i == 0) ? 0u : 1u);
         }
       };
-      if (nb > 0 && wait_full(0)) {
+      uint32_t p_parity[2] = {0, 0}, q_parity[2] = {0, 0};
+      uint32_t v_parity = 0;      // of the uses of v_clean
+      uint32_t block = 0;         // of the CTA's, counted through
+      int nb = 0, mixed = 0, blocks[2] = {0, 0}, it = 0;
+      auto first_s = [&](auto turn) {
+        constexpr int ks = 2 * decltype(turn)::value;
+        if (!wait_full(ks, block)) return;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (blocks[t] > 0 && wait(q_full(t), 0)) {
+          if (blocks[t] > 0 && wait(q_full(t), q_parity[t])) {
+            q_parity[t] ^= 1u;
             tc_fence_after();
-            issue_s(t, 0);
+            issue_s(t, ks);
+            if (blocks[t] == 1) tc_commit(q_empty(t));
           }
-        if (ok) tc_commit(empty(0));
-        wait_full(1);
-      }
-      for (int j = 0; ok && j < nb; ++j) {
-        const int vn = 2 * j + 1, kn = 2 * j + 2;
-        if (j >= mixed && !wait(v_clean(j - mixed), 0)) break;
+        if (ok) tc_commit(empty(ks));
+        wait_full(ks + 1, block);
+      };
+      auto step = [&](auto turn, int j) {
+        constexpr int vs = 2 * decltype(turn)::value + 1, ks = 2 * (1 - decltype(turn)::value);
+        const bool more = j + 1 < nb;
+        if (j >= mixed) {
+          const int i = (it & 1) * 3 + j - mixed;
+          if (!wait(v_clean(i), (v_parity >> i) & 1u)) return;
+          v_parity ^= 1u << i;
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (j < blocks[t]) {
-            if (!wait(p_full(t, 0), j & 1)) break;
+            if (!wait(p_full(t, 0), p_parity[t])) return;
             tc_fence_after();
-            issue_pv(t, vn, 0, j == 0);
-            if (t == 0 && j + 1 < nb && !wait_full(kn)) break;
-            if (!wait(p_full(t, 1), j & 1)) break;
+            issue_pv(t, vs, 0, j == 0);
+            if (t == 0 && more && !wait_full(ks, block + 1)) return;
+            if (!wait(p_full(t, 1), p_parity[t])) return;
             tc_fence_after();
-            issue_pv(t, vn, 1, false);
+            issue_pv(t, vs, 1, false);
+            p_parity[t] ^= 1u;
             if (j + 1 == blocks[t]) tc_commit(o_full(t));
-          } else if (t == 0 && j + 1 < nb && !wait_full(kn)) {
-            break;
+          } else if (t == 0 && more && !wait_full(ks, block + 1)) {
+            return;
           }
-          if (t == 1) tc_commit(empty(vn % C::NS));
-          if (t == 1 && j + 1 < nb && !wait_full(vn + 2)) break;
-          if (j + 1 < blocks[t]) issue_s(t, kn);
+          if (t == 1) tc_commit(empty(vs));
+          if (t == 1 && more && !wait_full(ks + 1, block + 1)) return;
+          if (j + 1 < blocks[t]) {
+            issue_s(t, ks);
+            if (j + 2 == blocks[t]) tc_commit(q_empty(t));
+          }
         }
-        if (ok && j + 1 < nb) tc_commit(empty(kn % C::NS));
+        if (more) tc_commit(empty(ks));
+      };
+      for (; ok; ++it) {
+        if (!wait(unit_full(it & 1), (it >> 1) & 1)) break;
+        nb = units[it & 1].nb;
+        mixed = units[it & 1].mixed;
+        blocks[0] = units[it & 1].blocks[0];
+        blocks[1] = units[it & 1].blocks[1];
+        if (units[it & 1].tokens < 0) break;
+        if (nb > 0) {
+          if (block & 1u)
+            first_s(std::integral_constant<int, 1>{});
+          else
+            first_s(std::integral_constant<int, 0>{});
+        }
+        for (int j = 0; ok && j < nb; ++j, ++block) {
+          if (block & 1u)
+            step(std::integral_constant<int, 1>{}, j);
+          else
+            step(std::integral_constant<int, 0>{}, j);
+        }
+        mbar_arrive(unit_empty(it & 1));
       }
       if (!ok && !*abort_flag) prompt_timeout(a, abort_flag, 1);
       tc_commit(teardown);  // every product is done before the tensor memory is freed
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp == 10) {
     // ------------------------------------------- rows of V that not all see
-    for (int j = mixed; j < nb; ++j) {
-      const int n = 2 * j + 1, s = n % C::NS;
-      if (!warp_wait(v_go(j - mixed), 0, a.wait_limit_ns, abort_flag) ||
-          !warp_wait(full(s), (n / C::NS) & 1, a.wait_limit_ns, abort_flag)) {
-        if (lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 3);
-        break;
-      }
-      const uint32_t vb = base + C::RING_OFF + s * C::TILE;
-      const int look = max(all_see - j * kPrKeys, 0), clear = min(any_sees - j * kPrKeys, kPrKeys);
-      uint32_t odd = 0;
-      for (int i = look * 8 + (warp - 10) * 32 + lane; i < clear * 8; i += 64) {
+    int n0 = 0;
+    uint32_t v_parity = 0;  // of the uses of v_go
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      if (!(ok = unit_ready(it))) break;
+      PromptUnit* unit = &units[it & 1];
+      const PromptUnit w = *unit;
+      for (int j = w.mixed; ok && j < w.nb; ++j) {
+        const int i = (it & 1) * 3 + j - w.mixed, n = n0 + 2 * j + 1, s = n % C::NS;
+        ok = warp_wait(v_go(i), (v_parity >> i) & 1u, limit, abort_flag) &&
+             warp_wait(full(s), (n / C::NS) & 1, limit, abort_flag);
+        if (!ok) break;
+        v_parity ^= 1u << i;
+        const uint32_t vb = base + C::RING_OFF + s * C::TILE;
+        const int look = max(w.all_see - j * kPrKeys, 0), clear = min(w.any_sees - j * kPrKeys, kPrKeys);
+        uint32_t odd = 0;
+        for (int r = look * 8 + lane; r < clear * 8; r += 32) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint4 x = ld_shared_v4(vb + c * C::CHUNK + i * 16);
-          const uint32_t y = odd_halves<BF16>(x.x) | odd_halves<BF16>(x.y) | odd_halves<BF16>(x.z) | odd_halves<BF16>(x.w);
-          if (y) {
-            odd = 1;
-            st_shared_v4(vb + c * C::CHUNK + i * 16, x.x & ~spread_halves(odd_halves<BF16>(x.x)),
-                         x.y & ~spread_halves(odd_halves<BF16>(x.y)), x.z & ~spread_halves(odd_halves<BF16>(x.z)),
-                         x.w & ~spread_halves(odd_halves<BF16>(x.w)));
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t at = vb + c * C::CHUNK + r * 16;
+            const uint4 v = ld_shared_v4(at);
+            const uint32_t o0 = odd_halves<BF16>(v.x), o1 = odd_halves<BF16>(v.y), o2 = odd_halves<BF16>(v.z),
+                           o3 = odd_halves<BF16>(v.w);
+            if (o0 | o1 | o2 | o3) {
+              odd = 1;
+              st_shared_v4(at, v.x & ~spread_halves(o0), v.y & ~spread_halves(o1), v.z & ~spread_halves(o2),
+                           v.w & ~spread_halves(o3));
+            }
           }
         }
-      }
-      for (int i = clear * 8 + (warp - 10) * 32 + lane; i < kPrKeys * 8; i += 64)
+        for (int r = clear * 8 + lane; r < kPrKeys * 8; r += 32)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) st_shared_v4(vb + c * C::CHUNK + i * 16, 0u, 0u, 0u, 0u);
-      if (odd) *odd_flag = 1;
-      fence_proxy_async_smem();
+          for (int c = 0; c < D / 64; ++c) st_shared_v4(vb + c * C::CHUNK + r * 16, 0u, 0u, 0u, 0u);
+        if (odd) *const_cast<volatile int*>(&unit->odd) = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_clean(i));
+      }
+      n0 += 2 * w.nb;
+      if (w.tokens < 0) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(v_clean(j - mixed));
+      if (lane == 0) mbar_arrive(unit_empty(it & 1));
     }
-  } else if (warp < 8) {
+    if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 3);
+  } else if (warp == 11) {
+    // -------------------------------------------------------------- units
+    int64_t block = blockIdx.x;
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      if (it >= 2 && !(ok = warp_wait(unit_empty(it & 1), ((it >> 1) - 1) & 1, limit, abort_flag))) break;
+      PromptUnit w{};
+      w.tokens = -1;
+      // (blocks past the last unit hold nothing)
+      while (block >= 0) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(taken, 16);
+          take_block(base + C::TAKEN_OFF, taken);
+        }
+        __syncwarp();
+        uint32_t unit, h;
+        magic_divmod(static_cast<uint32_t>(block), a.div_hk, unit, h);
+        w = find_unit(a, unit);
+        w.h = static_cast<int>(h);
+        shape_unit(a, w);
+        ++asked;
+        if (!(ok = warp_wait(taken, (asked - 1) & 1, limit, abort_flag))) break;
+        block = taken_block(base + C::TAKEN_OFF);
+        fence_proxy_async_smem();  // (read before the next answer is written)
+        __syncwarp();
+        if (w.tokens > 0) break;
+        w.tokens = -1;
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        units[it & 1] = w;
+        mbar_arrive(unit_full(it & 1));
+      }
+      __syncwarp();
+      if (w.tokens < 0) break;
+    }
+    if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 4);
+  } else {
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -466,104 +651,116 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     const uint32_t o_addr = tmem + lanes + C::O_COL + t * D;
     uint32_t tok, g;
     magic_divmod(static_cast<uint32_t>(row), a.div_group, tok, g);
-    const bool live = static_cast<int>(tok) < toks[t];
-    const int vis = a.causal ? min(static_cast<int>(tok) + t * a.tok + w.shift + 1, w.nk) : w.nk;
-    float m = -INFINITY, l = 0.0f;
     bool ok = true;
-    const int my_blocks = blocks[t];
-    for (int j = 0; j < my_blocks; ++j) {
-      if (!warp_wait(s_full(t), j & 1, a.wait_limit_ns, abort_flag)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      // The first half of P against the reference as it stands, while the
-      // block's maximum is found; in the rare block that exceeds the
-      // reference by 2^kPrLazy in some row (and the first), the reference
-      // moves and the half is made again.
-      const int valid = vis - j * kPrKeys;
-      const bool masked = __any_sync(0xffffffffu, valid < kPrKeys);
-      const float2 cs2 = make_float2(a.cs, a.cs);
-      float2 sum[4];
-      uint32_t sv[128], pk[32];
-      while (true) {
+    int s_uses = 0, o_uses = 0;
+    for (int it = 0; ok; ++it) {
+      if (!(ok = unit_ready(it))) break;
+      const PromptUnit* w = &units[it & 1];
+      if (w->tokens < 0) break;
+      const int my_blocks = w->blocks[t];
+      const bool live = static_cast<int>(tok) < w->toks[t];
+      const int vis = a.causal ? min(static_cast<int>(tok) + t * a.tok + w->shift + 1, w->nk) : w->nk;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < my_blocks; ++j, ++s_uses) {
+        if (!(ok = warp_wait(s_full(t), s_uses & 1, limit, abort_flag))) break;
+        tc_fence_after();
+        // The first half of P against the reference as it stands, while the
+        // block's maximum is found; in the rare block that exceeds the
+        // reference by 2^kPrLazy in some row (and the first), the reference
+        // moves and the half is made again.
+        const int valid = vis - j * kPrKeys;
+        const bool masked = __any_sync(0xffffffffu, valid < kPrKeys);
+        const float2 cs2 = make_float2(a.cs, a.cs);
+        float2 sum[4];
+        uint32_t sv[128], pk[32];
+        while (true) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          tc_ld_32x32b_x32(s_addr + 32u * i, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * i));
-        tc_wait_ld_regs(sv);
-        if (masked) {
+          for (int i = 0; i < 4; ++i)
+            tc_ld_32x32b_x32(s_addr + 32u * i, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * i));
+          tc_wait_ld_regs(sv);
+          if (masked) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= valid) sv[i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 128; ++i)
+              if (i >= valid) sv[i] = __float_as_uint(-INFINITY);
+          }
+          // (a row that has seen no key keeps weights of 2^-inf = 0)
+          const float ref = m == -INFINITY ? 0.0f : m;
+          const float2 neg = make_float2(-ref, -ref);
+          float mp[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            sum[u] = make_float2(0.0f, 0.0f);
+            mp[u] = -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 x = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), cs2, neg);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum[i & 3] = add2(sum[i & 3], e);
+            pk[i] = pack_pair16<BF16>(e.x, e.y);
+            mp[i & 3] = max3(mp[i & 3], __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+            mp[i & 3] = max3(mp[i & 3], __uint_as_float(sv[64 + 2 * i]), __uint_as_float(sv[64 + 2 * i + 1]));
+          }
+          const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * a.cs;
+          const bool over = mx > m + kPrLazy;
+          if (!__any_sync(0xffffffffu, over)) break;
+          const float alpha = over ? ex2(m - mx) : 1.0f;  // 0 at the first block with a visible key
+          if (over) m = mx;
+          l *= alpha;
+          if (j > 0) {
+            // the product before has completed: this S was issued after it by
+            // the same thread, and its barrier covers all that was issued before
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t v[32];
+              tc_ld_32x32b_x32(o_addr + c, v);
+              tc_wait_ld_regs(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+              st_tmem_x32(o_addr + c, v);
+            }
+            st_tmem_wait();
+          }
         }
-        // (a row that has seen no key keeps weights of 2^-inf = 0)
+        st_tmem_x32(p_addr, pk);
+        st_tmem_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t, 0));
         const float ref = m == -INFINITY ? 0.0f : m;
         const float2 neg = make_float2(-ref, -ref);
-        float mp[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          sum[u] = make_float2(0.0f, 0.0f);
-          mp[u] = -INFINITY;
-        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float2 x = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), cs2, neg);
+          const float2 x = fma2(make_float2(__uint_as_float(sv[64 + 2 * i]), __uint_as_float(sv[64 + 2 * i + 1])), cs2, neg);
           const float2 e = make_float2(ex2(x.x), ex2(x.y));
           sum[i & 3] = add2(sum[i & 3], e);
           pk[i] = pack_pair16<BF16>(e.x, e.y);
-          mp[i & 3] = max3(mp[i & 3], __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-          mp[i & 3] = max3(mp[i & 3], __uint_as_float(sv[64 + 2 * i]), __uint_as_float(sv[64 + 2 * i + 1]));
         }
-        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * a.cs;
-        const bool over = mx > m + kPrLazy;
-        if (!__any_sync(0xffffffffu, over)) break;
-        const float alpha = over ? ex2(m - mx) : 1.0f;  // 0 at the first block with a visible key
-        if (over) m = mx;
-        l *= alpha;
-        if (j > 0) {
-          // the product before has completed: this S was issued after it by
-          // the same thread, and its barrier covers all that was issued before
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t v[32];
-            tc_ld_32x32b_x32(o_addr + c, v);
-            tc_wait_ld_regs(v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-            st_tmem_x32(o_addr + c, v);
-          }
-          st_tmem_wait();
-        }
+        st_tmem_x32(p_addr + 32u, pk);
+        st_tmem_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t, 1));
+        const float2 s4 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += s4.x + s4.y;
       }
-      st_tmem_x32(p_addr, pk);
-      st_tmem_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(t, 0));
-      const float ref = m == -INFINITY ? 0.0f : m;
-      const float2 neg = make_float2(-ref, -ref);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 x = fma2(make_float2(__uint_as_float(sv[64 + 2 * i]), __uint_as_float(sv[64 + 2 * i + 1])), cs2, neg);
-        const float2 e = make_float2(ex2(x.x), ex2(x.y));
-        sum[i & 3] = add2(sum[i & 3], e);
-        pk[i] = pack_pair16<BF16>(e.x, e.y);
+      if (!ok) break;
+      if (my_blocks > 0) {
+        if (!(ok = warp_wait(o_full(t), o_uses & 1, limit, abort_flag))) break;
+        ++o_uses;
       }
-      st_tmem_x32(p_addr + 32u, pk);
-      st_tmem_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(t, 1));
-      const float2 s4 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-      l += s4.x + s4.y;
-    }
-    if (ok && my_blocks > 0) ok = warp_wait(o_full(t), 0, a.wait_limit_ns, abort_flag);
-    if (ok) {
       tc_fence_after();
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const bool odd = *odd_flag != 0;  // (set before the last product was let go)
-      uint16_t* dst = a.out + static_cast<int64_t>(w.row0 + t * a.tok + static_cast<int>(tok)) * a.os +
-                      static_cast<int64_t>(h * a.group + g) * D;
+      const bool odd = *const_cast<volatile int*>(&w->odd) != 0;  // (set before the last product was let go)
+      // Four lanes exchange 16-byte pieces of their rows, so that a store
+      // writes 64 bytes of each of eight rows (a row a lane, 16 bytes of 32
+      // rows a store, took 5,500 cycles a unit).
+      const int64_t at = live ? static_cast<int64_t>(w->row0 + t * a.tok + static_cast<int>(tok)) * a.os +
+                                    static_cast<int64_t>(w->h * a.group + static_cast<int>(g)) * D
+                              : -1;
+      int64_t row_at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) row_at[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
@@ -574,23 +771,26 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
-        if (live) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo = __uint_as_float(v[8 * q + 2 * e]) * inv, hi = __uint_as_float(v[8 * q + 2 * e + 1]) * inv;
-              if (odd) add_odd<BF16>(a, w.key_row, all_see, vis, static_cast<int>(h) * D + c + 8 * q + 2 * e, lo, hi);
-              x[e] = l == 0.0f ? 0u : pack_pair16<BF16>(lo, hi);
-            }
-            st_global_v4(dst + c + 8 * q, x[0], x[1], x[2], x[3]);
-          }
+        if (odd && live) {
+#pragma unroll 1
+          for (int k = w->all_see; k < vis; ++k)
+            add_odd<BF16>(a.v + static_cast<int64_t>(w->key_row + k) * a.vs + w->h * D + c, v);
         }
+        uint32_t y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          y[i] = l == 0.0f ? 0u : pack_pair16<BF16>(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+        exchange4(y, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (row_at[k] >= 0)
+            st_global_v4(a.out + row_at[k] + c + (lane & 3) * 8, y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       }
-    } else if (lane == 0 && !*abort_flag) {
-      prompt_timeout(a, abort_flag, 2);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(unit_empty(it & 1));
     }
+    if (!ok && lane == 0) prompt_timeout(a, abort_flag, 2);
   }
 
   // ------------------------------------------------------------ teardown
@@ -598,15 +798,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   if (warp == 8 && *abort_flag) {
     // let the loads still in flight land before the CTA exits
     volatile int no_abort = 0;
-    if (q_issued)
-      for (int t = 0; t < 2; ++t)
-        if (blocks[t] > 0) mbar_wait_bounded(q_full(t), 0, a.wait_limit_ns, &no_abort);
+    for (int t = 0; t < 2; ++t)
+      if (q_uses[t] > 0) mbar_wait_bounded(q_full(t), (q_uses[t] - 1) & 1, limit, &no_abort);
     for (int n = issued > C::NS ? issued - C::NS : 0; n < issued; ++n)
-      mbar_wait_bounded(full(n % C::NS), (n / C::NS) & 1, a.wait_limit_ns, &no_abort);
+      mbar_wait_bounded(full(n % C::NS), (n / C::NS) & 1, limit, &no_abort);
+  }
+  if (warp == 11 && *abort_flag && asked > 0) {
+    volatile int no_abort = 0;
+    mbar_wait_bounded(taken, (asked - 1) & 1, limit, &no_abort);
   }
   if (warp == 9) {
     volatile int no_abort = 0;
-    mbar_wait_bounded(teardown, 0, a.wait_limit_ns, &no_abort);
+    mbar_wait_bounded(teardown, 0, limit, &no_abort);
   }
   tc_fence_before();
   __syncthreads();
