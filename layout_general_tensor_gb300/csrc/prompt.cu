@@ -21,15 +21,23 @@
 // The two tiles alternate: while the tensor core works on one tile's
 // products, the other tile's softmax runs.
 //
-// Work.  A unit is 2T tokens of a sequence and a key head.  The grid has a
+// Few rows.  Where a unit's tokens fit one tile, both tiles take them, each
+// every other block of the keys, and the two results are joined at the end:
+// the walk over the keys, which is what such a unit takes, is half as long.
+// Where there are few units, a sequence whose walk over its keys is longer than
+// twice what each SM would have to do is cut into units of T tokens, so that
+// all of them are of this kind.  (A kernel of its own, FEW: in the other the
+// code that no unit uses costs 2 %.)
+//
+// Work.  A unit is 2T tokens (or T) of a sequence and a key head.  The grid has a
 // block for every unit, the ones with the most keys of a sequence first; a
 // running CTA takes over blocks that have not started (cluster launch
 // control), so that it loads the next unit's tiles and issues their first
 // products while the softmax warps still write the last unit's result.
 //
-// Warps (384 threads): 0-3 softmax of tile 0, 4-7 of tile 1, 8 loads, 9 issues
-// the products, 11 finds the units, 10 looks over the rows of V that some
-// query of the CTA must not see, since a weight of 0 does not cancel an infinity or a NaN: rows
+// Warps (384 threads): 0-3 softmax of tile 0, 4-7 of tile 1, 8 loads Q and K,
+// 9 issues the products, 11 finds the units, 10 loads V and looks over the
+// rows of it that some query of the CTA must not see, since a weight of 0 does not cancel an infinity or a NaN: rows
 // that no query sees (later ones, or the next sequence's) are cleared; in the
 // others (2T at most) values that are not finite are, and are added to the
 // results of the queries that do see them at the end, where a sum with a
@@ -61,6 +69,7 @@ constexpr int kPrRows = 128;   // rows of a tile
 constexpr int kPrKeys = 128;   // keys of a block
 constexpr int kPrTimeout = GEMM_ERR_TIMEOUT;
 constexpr float kPrLazy = 8.0f;
+constexpr int kPrFill = 2;     // units an SM below which the kernel for few is taken
 
 struct PromptArgs {
   CUtensorMap tm_q;        // {head_dim, q_heads, rows}, box {64, group, T}
@@ -73,8 +82,9 @@ struct PromptArgs {
   int64_t vs, os;
   int32_t batch, total_q, total_k;
   int32_t hk, group, tok;  // tok: T
+  int32_t sms;
   int32_t causal;
-  MagicDiv div_hk, div_group, div_pair;  // div_pair: by 2T
+  MagicDiv div_hk, div_group, div_tok, div_pair;  // by T, by 2T
   float cs;  // scale * log2(e)
   uint32_t idesc_s, idesc_pv;
 };
@@ -86,17 +96,21 @@ struct PromptUnit {
   int key_row, nk;         // first row of K and V, keys
   int shift;               // token i of the unit sees keys <= i + shift
   int h;                   // key head
-  int toks[2], blocks[2];  // tokens of the tiles, blocks with keys that they see
-  int nb;                  // blocks of the unit
+  // tokens of the tiles, and blocks with keys that they see; with split = 1
+  // the tokens are both tiles' and the blocks are dealt in turns, the first
+  // one to tile `start`
+  int toks[2], blocks[2];
+  int nb, split, start;    // nb: blocks of the unit
   // keys that every token sees, and that any does; the blocks from `mixed` on
   // (three at most: they span 2T keys) hold some that not all see
   int all_see, any_sees, mixed;
   int odd;                 // V held values that are not finite
-  int pad;
+  int pad[15];
 };
-static_assert(sizeof(PromptUnit) == 64, "two of them in shared memory");
+static_assert(sizeof(PromptUnit) == 128, "two of them in shared memory");
 
-__device__ __forceinline__ void shape_unit(const PromptArgs& a, PromptUnit& x) {
+template <bool FEW>
+__device__ __forceinline__ void shape_unit(const PromptArgs& a, PromptUnit& x, int turn) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     x.toks[t] = min(max(x.tokens - t * a.tok, 0), a.tok);
@@ -105,6 +119,13 @@ __device__ __forceinline__ void shape_unit(const PromptArgs& a, PromptUnit& x) {
     x.blocks[t] = (vis + kPrKeys - 1) / kPrKeys;
   }
   x.nb = max(x.blocks[0], x.blocks[1]);
+  x.split = FEW && x.tokens <= a.tok;
+  x.start = turn;
+  if (x.split) {
+    x.toks[1] = x.toks[0];
+    x.blocks[0] = (x.nb + (turn ^ 1)) / 2;
+    x.blocks[1] = (x.nb + turn) / 2;
+  }
   x.all_see = a.causal ? min(max(x.shift + 1, 0), x.nk) : x.nk;
   x.any_sees = a.causal ? min(max(x.tokens + x.shift, 0), x.nk) : x.nk;
   x.mixed = x.all_see / kPrKeys;
@@ -114,16 +135,17 @@ template <int D>
 struct PromptCfg {
   static constexpr uint32_t CHUNK = 128u * 128u;      // 64 values of 128 rows
   static constexpr uint32_t TILE = (D / 64) * CHUNK;  // a tile of Q, K or V
-  static constexpr int NS = 4;                        // ring of K and V tiles, in the order they are used
+  static constexpr int NS = 4;                        // places: K, V, K, V, two blocks of each
   static constexpr uint32_t Q_OFF = 0;                // two tiles
   static constexpr uint32_t RING_OFF = 2 * TILE;
   static constexpr uint32_t BAR_OFF = RING_OFF + NS * TILE;
-  // full[NS], empty[NS], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], v_go[2][3], v_clean[2][3],
-  // unit_full[2], unit_empty[2], taken, teardown
-  static constexpr int NBARS = 2 * NS + 30;
+  // full[NS], empty[NS], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], v_clean[2][3],
+  // unit_full[2], unit_empty[2], taken, teardown, join_ready[2][4], join_done[2][4]
+  static constexpr int NBARS = 2 * NS + 40;
   static constexpr uint32_t TAKEN_OFF = BAR_OFF + ((NBARS * 8 + 15) & ~15);  // 16 bytes: a block taken over
   static constexpr uint32_t UNIT_OFF = TAKEN_OFF + 16;                       // two PromptUnit
-  static constexpr uint32_t MISC_OFF = UNIT_OFF + 2 * sizeof(PromptUnit);
+  static constexpr uint32_t XCH_OFF = UNIT_OFF + 2 * sizeof(PromptUnit);     // {m, l} of both tiles' rows
+  static constexpr uint32_t MISC_OFF = XCH_OFF + 2 * kPrRows * 8;
   static constexpr uint32_t SMEM = MISC_OFF + 16 + 1024;  // slack for the 1024-byte alignment
   static constexpr uint32_t S_COL = 128;                  // between the tiles' S
   static constexpr uint32_t O_COL = 256;
@@ -153,6 +175,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -238,20 +266,50 @@ __device__ __forceinline__ int64_t taken_block(uint32_t src) {
   return ok ? static_cast<int64_t>(x) : -1;
 }
 
+// Query and key rows of sequence b.
+struct PromptSeq {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ PromptSeq seq_at(const PromptArgs& a, int b) {
+  PromptSeq s{0, 0, 0, 0};
+  if (b < a.batch) {
+    s.q0 = min(max(a.cu_q[b], 0), a.total_q);
+    s.nq = max(min(a.cu_q[b + 1], a.total_q) - s.q0, 0);
+    s.k0 = min(max(a.cu_k[b], 0), a.total_k);
+    s.nk = max(min(a.cu_k[b + 1], a.total_k) - s.k0, 0);
+  }
+  return s;
+}
+
+// Blocks of keys above which a sequence is cut into units of one tile: twice
+// the blocks that each SM would walk if all units were of two.  (Measured,
+// 32 / 8 heads of 128: one prompt of 512 tokens 10.7 us so cut, 12.0 not; one
+// of 64 after 8192 keys 35 and 58; four of 256, which it leaves alone, 13.0
+// and 9.8.)  The whole warp returns the same.
+__device__ __forceinline__ int narrow_above(const PromptArgs& a) {
+  float sum = 0.0f;
+  for (int b = threadIdx.x & 31; b < a.batch; b += 32) {
+    const PromptSeq s = seq_at(a, b);
+    const float walk = static_cast<float>(s.nk) - (a.causal ? 0.5f * static_cast<float>(s.nq) : 0.0f);
+    sum += static_cast<float>(magic_div(static_cast<uint32_t>(s.nq + 2 * a.tok) - 1u, a.div_pair)) *
+           (fmaxf(walk, 0.0f) * (1.0f / kPrKeys) + 0.5f);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return static_cast<int>(fminf(2.0f * sum * static_cast<float>(a.hk) / static_cast<float>(a.sms), 1e9f));
+}
+
 // Unit `u` of the list (sequences in order, each one's last tokens -- the
 // most keys -- first); every lane of the warp returns the same.
-__device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u) {
+__device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u, int narrow) {
   const int lane = threadIdx.x & 31;
   PromptUnit r{};
   uint32_t before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane;
-    int q0 = 0, nq = 0;
-    if (b < a.batch) {
-      q0 = min(max(a.cu_q[b], 0), a.total_q);
-      nq = max(min(a.cu_q[b + 1], a.total_q) - q0, 0);
-    }
-    const uint32_t n = magic_div(static_cast<uint32_t>(nq) + 2u * a.tok - 1u, a.div_pair);
+    const PromptSeq q = seq_at(a, b0 + lane);
+    const bool cut = (q.nk + kPrKeys - 1) / kPrKeys > narrow;
+    const int my_span = cut ? a.tok : 2 * a.tok;
+    const uint32_t n = magic_div(static_cast<uint32_t>(q.nq + my_span) - 1u, cut ? a.div_tok : a.div_pair);
     uint32_t x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -263,17 +321,15 @@ __device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u)
       const uint32_t in = u - before;
       const unsigned hit = __ballot_sync(0xffffffffu, x > in);
       const int src = __ffs(hit) - 1;
-      const int sq0 = __shfl_sync(0xffffffffu, q0, src), snq = __shfl_sync(0xffffffffu, nq, src);
+      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
       const uint32_t units = __shfl_sync(0xffffffffu, n, src), first = __shfl_sync(0xffffffffu, x - n, src);
-      const int i0 = static_cast<int>(units - 1u - (in - first)) * 2 * a.tok;
-      const int sb = b0 + src;
-      const int k0 = min(max(a.cu_k[sb], 0), a.total_k);
-      const int nk = max(min(a.cu_k[sb + 1], a.total_k) - k0, 0);
-      r.row0 = sq0 + i0;
-      r.tokens = min(2 * a.tok, snq - i0);
-      r.key_row = k0;
-      r.nk = nk;
-      r.shift = i0 + nk - snq;
+      const int span = of(my_span), nq = of(q.nq);
+      const int i0 = static_cast<int>(units - 1u - (in - first)) * span;
+      r.row0 = of(q.q0) + i0;
+      r.tokens = min(span, nq - i0);
+      r.key_row = of(q.k0);
+      r.nk = of(q.nk);
+      r.shift = i0 + r.nk - nq;
       return r;
     }
     before += all;
@@ -323,7 +379,7 @@ __device__ __forceinline__ void exchange4(uint32_t (&y)[16], int lane) {
     }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool FEW>
 __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_constant__ PromptArgs a) {
   using C = PromptCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -343,12 +399,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   auto o_full = [&](int t) { return bar0 + 8u * (kB + 10 + t); };
   // (of even and odd units: a unit is taken up only when nobody is at the one
   // before the last, so no wait can be two phases behind)
-  auto v_go = [&](int i) { return bar0 + 8u * (kB + 12 + i); };
-  auto v_clean = [&](int i) { return bar0 + 8u * (kB + 18 + i); };
-  auto unit_full = [&](int i) { return bar0 + 8u * (kB + 24 + i); };
-  auto unit_empty = [&](int i) { return bar0 + 8u * (kB + 26 + i); };
-  const uint32_t taken = bar0 + 8u * (kB + 28);
-  const uint32_t teardown = bar0 + 8u * (kB + 29);
+  auto v_clean = [&](int i) { return bar0 + 8u * (kB + 12 + i); };
+  auto unit_full = [&](int i) { return bar0 + 8u * (kB + 18 + i); };
+  auto unit_empty = [&](int i) { return bar0 + 8u * (kB + 20 + i); };
+  const uint32_t taken = bar0 + 8u * (kB + 22);
+  const uint32_t teardown = bar0 + 8u * (kB + 23);
+  auto join_ready = [&](int t, int q) { return bar0 + 8u * (kB + 24 + t * 4 + q); };
+  auto join_done = [&](int t, int q) { return bar0 + 8u * (kB + 32 + t * 4 + q); };
   PromptUnit* units = reinterpret_cast<PromptUnit*>(smem + C::UNIT_OFF);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
@@ -369,9 +426,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       mbar_init(unit_full(t), 1);
       mbar_init(unit_empty(t), 11);  // eight softmax warps, loads, products, V
     }
-    for (int i = 0; i < 6; ++i) {
-      mbar_init(v_go(i), 1);
-      mbar_init(v_clean(i), 1);
+    for (int i = 0; i < 6; ++i) mbar_init(v_clean(i), 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(join_ready(i >> 2, i & 3), 1);
+      mbar_init(join_done(i >> 2, i & 3), 1);
     }
     mbar_init(taken, 1);
     mbar_init(teardown, 1);
@@ -396,48 +454,50 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   // on from one unit to the next, so each role counts its own uses of them.
   const uint64_t limit = a.wait_limit_ns;
   auto unit_ready = [&](int it) { return warp_wait(unit_full(it & 1), (it >> 1) & 1, limit, abort_flag); };
-  int issued = 0;                 // loads of the ring (warp 8)
+  int issued = 0;                 // loads of K (warp 8), of V (warp 10)
   int q_uses[2] = {0, 0};         // loads of Q (warp 8)
   int asked = 0;                  // blocks asked for (warp 11)
 
+  // Load block j of K (which = 0) or V (1) of unit w into its next place.
+  auto load = [&](int which, int j, const PromptUnit& w, const CUtensorMap* map, bool leader) {
+    const int s = 2 * (issued & 1) + which;
+    if (issued >= 2 && !warp_wait(empty(s), ((issued >> 1) - 1) & 1, limit, abort_flag)) return false;
+    if (leader) {
+      mbar_arrive_expect_tx(full(s), C::TILE);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(base + C::RING_OFF + s * C::TILE + c * C::CHUNK, map, full(s), c * 64, w.h, w.key_row + j * kPrKeys);
+    }
+    __syncwarp();
+    ++issued;
+    return true;
+  };
+
   if (warp == 8) {
-    // -------------------------------------------------------------- loads
+    // --------------------------------------------------- loads of Q and K
     const bool leader = elect_one();
     bool ok = true;
     for (int it = 0; ok; ++it) {
       if (!(ok = unit_ready(it))) break;
       const PromptUnit w = units[it & 1];
       if (w.tokens < 0) break;
-      for (int n = 0; ok && n < 2 * w.nb; ++n) {
-        const int s = issued % C::NS;
-        if (issued >= C::NS && !(ok = warp_wait(empty(s), ((issued / C::NS) - 1) & 1, limit, abort_flag))) break;
-        if (leader) {
-          mbar_arrive_expect_tx(full(s), C::TILE);
+      for (int j = 0; ok && j < w.nb; ++j) {
+        if (!(ok = load(0, j, w, &a.tm_k, leader))) break;
+        if (j > 0) continue;
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(base + C::RING_OFF + s * C::TILE + c * C::CHUNK, (n & 1) ? &a.tm_v : &a.tm_k, full(s), c * 64,
-                        w.h, w.key_row + (n >> 1) * kPrKeys);
-        }
-        __syncwarp();
-        ++issued;
-        // (only now, so that the looker waits for this load's phase and no earlier one)
-        if (const int i = (n >> 1) - w.mixed; (n & 1) && i >= 0 && leader) mbar_arrive(v_go((it & 1) * 3 + i));
-        if (n == 0) {
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (w.split ? t != 0 : w.blocks[t] == 0)) continue;
+          // (the last products that read this tile of Q are done)
+          if (q_uses[t] > 0 && !(ok = warp_wait(q_empty(t), (q_uses[t] - 1) & 1, limit, abort_flag))) continue;
+          if (leader) {
+            mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tok * a.group) * 128u * (D / 64));
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || w.blocks[t] == 0) continue;
-            // (the last products that read this tile of Q are done)
-            if (q_uses[t] > 0 && !(ok = warp_wait(q_empty(t), (q_uses[t] - 1) & 1, limit, abort_flag))) continue;
-            if (leader) {
-              mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tok * a.group) * 128u * (D / 64));
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(base + C::Q_OFF + t * C::TILE + c * C::CHUNK, &a.tm_q, q_full(t), c * 64, w.h * a.group,
-                            w.row0 + t * a.tok);
-            }
-            __syncwarp();
-            ++q_uses[t];
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(base + C::Q_OFF + t * C::TILE + c * C::CHUNK, &a.tm_q, q_full(t), c * 64, w.h * a.group,
+                          w.row0 + t * a.tok);
           }
+          __syncwarp();
+          ++q_uses[t];
         }
       }
       if (lane == 0) mbar_arrive(unit_empty(it & 1));
@@ -463,8 +523,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       const uint64_t q_desc = sw128_desc(base + C::Q_OFF, 16u, 1024u), k_desc = sw128_desc(base + C::RING_OFF, 16u, 1024u);
       const uint64_t v_desc = sw128_desc(base + C::RING_OFF, C::CHUNK, 1024u);
       const uint32_t idesc_s = a.idesc_s, idesc_pv = a.idesc_pv;
-      auto issue_s = [&](int t, int slot) {
-        const uint64_t qd = q_desc + t * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
+      auto issue_s = [&](int t, int q_tile, int slot) {
+        const uint64_t qd = q_desc + q_tile * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
         const uint32_t dst = tmem + t * C::S_COL;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -495,7 +555,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           if (blocks[t] > 0 && wait(q_full(t), q_parity[t])) {
             q_parity[t] ^= 1u;
             tc_fence_after();
-            issue_s(t, ks);
+            issue_s(t, t, ks);
             if (blocks[t] == 1) tc_commit(q_empty(t));
           }
         if (ok) tc_commit(empty(ks));
@@ -527,12 +587,48 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           if (t == 1) tc_commit(empty(vs));
           if (t == 1 && more && !wait_full(ks + 1, block + 1)) return;
           if (j + 1 < blocks[t]) {
-            issue_s(t, ks);
+            issue_s(t, t, ks);
             if (j + 2 == blocks[t]) tc_commit(q_empty(t));
           }
         }
         if (more) tc_commit(empty(ks));
       };
+      // The same for units whose tiles share their rows: blocks go to the tile
+      // of their place in the ring, so the tile is the turn.
+      auto first_s_split = [&](auto turn, int j) {
+        constexpr int t = decltype(turn)::value, ks = 2 * t;
+        if (!wait_full(ks, block + j)) return;
+        tc_fence_after();
+        issue_s(t, 0, ks);
+        tc_commit(empty(ks));
+        if (j + 1 == nb) tc_commit(q_empty(0));
+      };
+      auto step_split = [&](auto turn, int j) {
+        constexpr int t = decltype(turn)::value, ks = 2 * t, vs = ks + 1;
+        if (!wait_full(vs, block)) return;
+        if (j >= mixed) {
+          const int i = (it & 1) * 3 + j - mixed;
+          if (!wait(v_clean(i), (v_parity >> i) & 1u)) return;
+          v_parity ^= 1u << i;
+        }
+        if (!wait(p_full(t, 0), p_parity[t])) return;
+        tc_fence_after();
+        issue_pv(t, vs, 0, j < 2);
+        if (j + 2 < nb && !wait_full(ks, block + 2)) return;
+        if (!wait(p_full(t, 1), p_parity[t])) return;
+        tc_fence_after();
+        issue_pv(t, vs, 1, false);
+        p_parity[t] ^= 1u;
+        if (j + 2 >= nb) tc_commit(o_full(t));
+        tc_commit(empty(vs));
+        if (j + 2 < nb) {
+          issue_s(t, 0, ks);
+          tc_commit(empty(ks));
+          if (j + 3 == nb) tc_commit(q_empty(0));
+        }
+      };
+      constexpr std::integral_constant<int, 0> even{};
+      constexpr std::integral_constant<int, 1> odd{};
       for (; ok; ++it) {
         if (!wait(unit_full(it & 1), (it >> 1) & 1)) break;
         nb = units[it & 1].nb;
@@ -540,17 +636,35 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         blocks[0] = units[it & 1].blocks[0];
         blocks[1] = units[it & 1].blocks[1];
         if (units[it & 1].tokens < 0) break;
-        if (nb > 0) {
-          if (block & 1u)
-            first_s(std::integral_constant<int, 1>{});
-          else
-            first_s(std::integral_constant<int, 0>{});
-        }
-        for (int j = 0; ok && j < nb; ++j, ++block) {
-          if (block & 1u)
-            step(std::integral_constant<int, 1>{}, j);
-          else
-            step(std::integral_constant<int, 0>{}, j);
+        if (FEW && units[it & 1].split) {
+          if (nb > 0 && wait(q_full(0), q_parity[0])) {
+            q_parity[0] ^= 1u;
+            for (int j = 0; ok && j < min(nb, 2); ++j) {
+              if ((block + j) & 1u)
+                first_s_split(odd, j);
+              else
+                first_s_split(even, j);
+            }
+          }
+          for (int j = 0; ok && j < nb; ++j, ++block) {
+            if (block & 1u)
+              step_split(odd, j);
+            else
+              step_split(even, j);
+          }
+        } else {
+          if (nb > 0) {
+            if (block & 1u)
+              first_s(odd);
+            else
+              first_s(even);
+          }
+          for (int j = 0; ok && j < nb; ++j, ++block) {
+            if (block & 1u)
+              step(odd, j);
+            else
+              step(even, j);
+          }
         }
         mbar_arrive(unit_empty(it & 1));
       }
@@ -559,22 +673,23 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ------------------------------------------- rows of V that not all see
-    int n0 = 0;
-    uint32_t v_parity = 0;  // of the uses of v_go
+    // ------------------- loads of V, and its rows that not all queries see
+    const bool leader = elect_one();
     bool ok = true;
     for (int it = 0; ok; ++it) {
       if (!(ok = unit_ready(it))) break;
       PromptUnit* unit = &units[it & 1];
       const PromptUnit w = *unit;
-      for (int j = w.mixed; ok && j < w.nb; ++j) {
-        const int i = (it & 1) * 3 + j - w.mixed, n = n0 + 2 * j + 1, s = n % C::NS;
-        ok = warp_wait(v_go(i), (v_parity >> i) & 1u, limit, abort_flag) &&
-             warp_wait(full(s), (n / C::NS) & 1, limit, abort_flag);
-        if (!ok) break;
-        v_parity ^= 1u << i;
+      if (w.tokens < 0) break;
+      // (block j is looked over after j + 1 is asked for)
+      for (int j = 0; ok && j <= w.nb; ++j) {
+        if (j < w.nb && !(ok = load(1, j, w, &a.tm_v, leader))) break;
+        const int jj = j - 1;
+        if (jj < w.mixed || jj < 0) continue;
+        const int n = issued - (j < w.nb ? 2 : 1), s = 2 * (n & 1) + 1;
+        if (!(ok = warp_wait(full(s), (n >> 1) & 1, limit, abort_flag))) break;
         const uint32_t vb = base + C::RING_OFF + s * C::TILE;
-        const int look = max(w.all_see - j * kPrKeys, 0), clear = min(w.any_sees - j * kPrKeys, kPrKeys);
+        const int look = max(w.all_see - jj * kPrKeys, 0), clear = min(w.any_sees - jj * kPrKeys, kPrKeys);
         uint32_t odd = 0;
         for (int r = look * 8 + lane; r < clear * 8; r += 32) {
 #pragma unroll
@@ -596,10 +711,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         if (odd) *const_cast<volatile int*>(&unit->odd) = 1;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_clean(i));
+        if (lane == 0) mbar_arrive(v_clean((it & 1) * 3 + jj - w.mixed));
       }
-      n0 += 2 * w.nb;
-      if (w.tokens < 0) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(unit_empty(it & 1));
     }
@@ -607,6 +720,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   } else if (warp == 11) {
     // -------------------------------------------------------------- units
     int64_t block = blockIdx.x;
+    int turn = 0;  // of the next unit's first block at the ring's places
+    const int narrow = FEW ? narrow_above(a) : 0x7fffffff;
     bool ok = true;
     for (int it = 0; ok; ++it) {
       if (it >= 2 && !(ok = warp_wait(unit_empty(it & 1), ((it >> 1) - 1) & 1, limit, abort_flag))) break;
@@ -621,9 +736,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         __syncwarp();
         uint32_t unit, h;
         magic_divmod(static_cast<uint32_t>(block), a.div_hk, unit, h);
-        w = find_unit(a, unit);
+        w = find_unit(a, unit, narrow);
         w.h = static_cast<int>(h);
-        shape_unit(a, w);
+        shape_unit<FEW>(a, w, turn);
         ++asked;
         if (!(ok = warp_wait(taken, (asked - 1) & 1, limit, abort_flag))) break;
         block = taken_block(base + C::TAKEN_OFF);
@@ -633,6 +748,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         w.tokens = -1;
       }
       if (!ok) break;
+      if (w.tokens > 0) turn ^= w.nb & 1;
       if (lane == 0) {
         units[it & 1] = w;
         mbar_arrive(unit_full(it & 1));
@@ -652,14 +768,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     uint32_t tok, g;
     magic_divmod(static_cast<uint32_t>(row), a.div_group, tok, g);
     bool ok = true;
-    int s_uses = 0, o_uses = 0;
+    int s_uses = 0, o_uses = 0, joins = 0;
     for (int it = 0; ok; ++it) {
       if (!(ok = unit_ready(it))) break;
       const PromptUnit* w = &units[it & 1];
       if (w->tokens < 0) break;
-      const int my_blocks = w->blocks[t];
+      const int my_blocks = w->blocks[t], split = FEW ? w->split : 0;
       const bool live = static_cast<int>(tok) < w->toks[t];
-      const int vis = a.causal ? min(static_cast<int>(tok) + t * a.tok + w->shift + 1, w->nk) : w->nk;
+      const int my_tok = static_cast<int>(tok) + (split ? 0 : t * a.tok);
+      const int vis = a.causal ? min(my_tok + w->shift + 1, w->nk) : w->nk;
+      // keys of the tile's first block, and between its blocks
+      const int key0 = split ? (t ^ w->start) * kPrKeys : 0, key_step = split ? 2 * kPrKeys : kPrKeys;
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < my_blocks; ++j, ++s_uses) {
         if (!(ok = warp_wait(s_full(t), s_uses & 1, limit, abort_flag))) break;
@@ -668,7 +787,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         // block's maximum is found; in the rare block that exceeds the
         // reference by 2^kPrLazy in some row (and the first), the reference
         // moves and the half is made again.
-        const int valid = vis - j * kPrKeys;
+        const int valid = vis - key0 - j * key_step;
         const bool masked = __any_sync(0xffffffffu, valid < kPrKeys);
         const float2 cs2 = make_float2(a.cs, a.cs);
         float2 sum[4];
@@ -744,32 +863,72 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         const float2 s4 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += s4.x + s4.y;
       }
-      if (!ok) break;
-      if (my_blocks > 0) {
-        if (!(ok = warp_wait(o_full(t), o_uses & 1, limit, abort_flag))) break;
+      if (ok && my_blocks > 0) {
+        ok = warp_wait(o_full(t), o_uses & 1, limit, abort_flag);
         ++o_uses;
       }
+      // f0, f1: what the tiles' sums are multiplied by (f1 only where two are
+      // joined), 0 for one that has none
+      float f0 = l == 0.0f ? 0.0f : 1.0f / l, f1 = 0.0f;
+      bool use0 = my_blocks > 0, use1 = false;
+      uint32_t o0 = o_addr, o1 = o_addr;
+      int c0 = 0, c1 = D;
+      if (split) {
+        // The warp of the other tile has the same rows: the two exchange their
+        // {m, l} and each writes half of the columns.
+        const int q = warp & 3;
+        const uint32_t xch = base + C::XCH_OFF + row * 8;
+        st_shared_f32(xch + t * kPrRows * 8, m);
+        st_shared_f32(xch + t * kPrRows * 8 + 4, l);
+        tc_fence_before();
+        __syncwarp();
+        if (ok) {
+          if (lane == 0) mbar_arrive(join_ready(t, q));
+          ok = warp_wait(join_ready(t ^ 1, q), joins & 1, limit, abort_flag);
+        }
+        if (ok) {
+          const float om = ld_shared_f32(xch + (t ^ 1) * kPrRows * 8), ol = ld_shared_f32(xch + (t ^ 1) * kPrRows * 8 + 4);
+          const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.0f : top;
+          const float g0 = ex2(m - ref), g1 = ex2(om - ref);
+          l = l * g0 + ol * g1;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          f0 = g0 * inv;
+          f1 = g1 * inv;
+          use1 = w->blocks[t ^ 1] > 0;
+          o1 = tmem + lanes + C::O_COL + (t ^ 1) * D;
+          c0 = t * (D / 2);
+          c1 = c0 + D / 2;
+        }
+      }
+      if (!ok) break;
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const bool odd = *const_cast<volatile int*>(&w->odd) != 0;  // (set before the last product was let go)
       // Four lanes exchange 16-byte pieces of their rows, so that a store
       // writes 64 bytes of each of eight rows (a row a lane, 16 bytes of 32
       // rows a store, took 5,500 cycles a unit).
-      const int64_t at = live ? static_cast<int64_t>(w->row0 + t * a.tok + static_cast<int>(tok)) * a.os +
+      const int64_t at = live ? static_cast<int64_t>(w->row0 + my_tok) * a.os +
                                     static_cast<int64_t>(w->h * a.group + static_cast<int>(g)) * D
                               : -1;
       int64_t row_at[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) row_at[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = c0; c < c1; c += 32) {
         uint32_t v[32];
-        if (my_blocks > 0) {
-          tc_ld_32x32b_x32(o_addr + c, v);
-          tc_wait_ld_regs(v);
-        } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+        if (use0) {
+          tc_ld_32x32b_x32(o0 + c, v);
+          tc_wait_ld_regs(v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f0);
+        }
+        if (use1) {
+          uint32_t u[32];
+          tc_ld_32x32b_x32(o1 + c, u);
+          tc_wait_ld_regs(u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), f1, __uint_as_float(v[i])));
         }
         if (odd && live) {
 #pragma unroll 1
@@ -779,7 +938,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         uint32_t y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          y[i] = l == 0.0f ? 0u : pack_pair16<BF16>(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+          y[i] = l == 0.0f ? 0u : pack_pair16<BF16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
         exchange4(y, lane);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -788,6 +947,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       }
       tc_fence_before();
       __syncwarp();
+      if (split) {
+        // (the other warp has read this tile's sums too, before they are written again)
+        if (lane == 0) mbar_arrive(join_done(t, warp & 3));
+        if (!(ok = warp_wait(join_done(t ^ 1, warp & 3), joins & 1, limit, abort_flag))) break;
+        ++joins;
+      }
       if (lane == 0) mbar_arrive(unit_empty(it & 1));
     }
     if (!ok && lane == 0) prompt_timeout(a, abort_flag, 2);
@@ -795,13 +960,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   // ------------------------------------------------------------ teardown
   __syncthreads();
-  if (warp == 8 && *abort_flag) {
+  if ((warp == 8 || warp == 10) && *abort_flag) {
     // let the loads still in flight land before the CTA exits
     volatile int no_abort = 0;
     for (int t = 0; t < 2; ++t)
       if (q_uses[t] > 0) mbar_wait_bounded(q_full(t), (q_uses[t] - 1) & 1, limit, &no_abort);
-    for (int n = issued > C::NS ? issued - C::NS : 0; n < issued; ++n)
-      mbar_wait_bounded(full(n % C::NS), (n / C::NS) & 1, limit, &no_abort);
+    for (int n = issued > 2 ? issued - 2 : 0; n < issued; ++n)
+      mbar_wait_bounded(full(2 * (n & 1) + (warp == 10)), (n >> 1) & 1, limit, &no_abort);
   }
   if (warp == 11 && *abort_flag && asked > 0) {
     volatile int no_abort = 0;
@@ -817,12 +982,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool BF16>
-cudaError_t launch_prompt(const PromptArgs& a, unsigned grid, cudaStream_t stream) {
+template <int D, bool BF16, bool FEW>
+cudaError_t launch_prompt_as(const PromptArgs& a, unsigned grid, cudaStream_t stream) {
   using C = PromptCfg<D>;
-  const cudaError_t e = set_smem_once<prompt_kernel<D, BF16>>(static_cast<int>(C::SMEM));
+  const cudaError_t e = set_smem_once<prompt_kernel<D, BF16, FEW>>(static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
-  return launch_pdl(prompt_kernel<D, BF16>, dim3(grid), dim3(kPrThreads), C::SMEM, stream, a);
+  return launch_pdl(prompt_kernel<D, BF16, FEW>, dim3(grid), dim3(kPrThreads), C::SMEM, stream, a);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_prompt(const PromptArgs& a, bool few, unsigned grid, cudaStream_t stream) {
+  return few ? launch_prompt_as<D, BF16, true>(a, grid, stream) : launch_prompt_as<D, BF16, false>(a, grid, stream);
 }
 
 // Rows of `heads` heads, pitch `stride` elements: boxes of 64 values, `box_heads` heads, `box_rows` rows.
@@ -908,8 +1078,17 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return GEMM_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) % 4 != 0) return GEMM_ERR_ALIGNMENT;
   const int group = d.q_heads / d.k_heads, tok = lgt::kPrRows / group;
-  // a sequence of n tokens has at most n / 2T + 1 units
-  const int64_t units = (total_q / (2 * tok) + batch) * d.k_heads;
+  // A sequence of n tokens has at most n / 2T + 1 units of 2T, n / T + 1 of T.
+  // (At most: what is past the last unit is found out by the CTAs.)
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  const int64_t wide = (total_q / (2 * tok) + batch) * d.k_heads;
+  const bool few = wide < static_cast<int64_t>(lgt::kPrFill) * sms;
+  const int64_t units = few ? (total_q / tok + batch) * d.k_heads : wide;
   if (total_q > (int64_t{1} << 30) || total_k > (int64_t{1} << 30) || units >= (int64_t{1} << 31))
     return GEMM_ERR_UNSUPPORTED;
   lgt::PromptArgs a;
@@ -937,6 +1116,8 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
   a.causal = d.causal;
   a.div_hk = lgt::magic_encode(static_cast<uint32_t>(d.k_heads));
   a.div_group = lgt::magic_encode(static_cast<uint32_t>(group));
+  a.sms = sms;
+  a.div_tok = lgt::magic_encode(static_cast<uint32_t>(tok));
   a.div_pair = lgt::magic_encode(static_cast<uint32_t>(2 * tok));
   a.cs = (d.scale > 0.0f ? d.scale : 1.0f / std::sqrt(static_cast<float>(d.head_dim))) * 1.4426950408889634f;
   const bool bf16 = d.dtype == GEMM_BF16;
@@ -945,8 +1126,8 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(units);
   const cudaError_t e = d.head_dim == 128
-                            ? (bf16 ? lgt::launch_prompt<128, true>(a, grid, s) : lgt::launch_prompt<128, false>(a, grid, s))
-                            : (bf16 ? lgt::launch_prompt<64, true>(a, grid, s) : lgt::launch_prompt<64, false>(a, grid, s));
+                            ? (bf16 ? lgt::launch_prompt<128, true>(a, few, grid, s) : lgt::launch_prompt<128, false>(a, few, grid, s))
+                            : (bf16 ? lgt::launch_prompt<64, true>(a, few, grid, s) : lgt::launch_prompt<64, false>(a, few, grid, s));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
