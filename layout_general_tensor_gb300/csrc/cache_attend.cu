@@ -117,63 +117,76 @@ __device__ __forceinline__ float sum_scale(const float* s, float m, float R) {
   return s[1] == -INFINITY ? 0.0f : ex2f(s[1] - m + s[2] - R);
 }
 
-// Whether this CTA is the last of `n` to arrive here with its results written;
-// then the others' are visible to it and the counter is 0 again.
-__device__ __forceinline__ bool arrive_last(int32_t* counter, uint32_t n, int* flag) {
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) *flag = atomicAdd(counter, 1) == static_cast<int>(n - 1);
-  __syncthreads();
-  const bool last = *flag != 0;
-  if (last) {
-    __threadfence();
-    if (threadIdx.x == 0) *counter = 0;
-  }
-  return last;
+// Count this CTA in at `counter`, whose `n`-th arrival sets it back to 0; true
+// for that one.  One thread does it after a barrier of the CTA: what the CTA
+// wrote before is visible to whoever arrives later, and what the earlier ones
+// wrote to it after the next barrier (read past L1).
+__device__ __forceinline__ bool arrive_last(int32_t* counter, uint32_t n) {
+  int32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  if (old != static_cast<int32_t>(n) - 1) return false;
+  *counter = 0;
+  return true;
 }
 
-// Join n parts (rows of `heads` heads at their slots), by the
-// whole CTA: their {l, m, R} through shared memory, then each thread four
-// values of d over the parts in order, eight loads at a time.
-template <int D, int HP, int THREADS, typename SlotOf, typename Put>
-__device__ __forceinline__ void join_parts(const float* part, uint32_t* smem, uint32_t n, SlotOf slot_of, int heads, Put put) {
-  constexpr int ROW = D + 4;
-  float* stats = reinterpret_cast<float*>(smem);  // [part][HP][4]
-  for (uint32_t i = threadIdx.x; i < n * HP; i += THREADS) {
-    const uint32_t p = i / HP, head = i % HP;
-    float4 x = make_float4(0.0f, -INFINITY, -INFINITY, 0.0f);
-    if (static_cast<int>(head) < heads)
-      x = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p) * HP + head) * ROW + D));
-    *reinterpret_cast<float4*>(stats + i * 4) = x;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < heads * (D / 4); i += THREADS) {
-    const int head = i / (D / 4), d = i % (D / 4) * 4;
-    const float* st = stats + head * 4;
-    float mt = -INFINITY, Rt = -INFINITY;
-    for (uint32_t p = 0; p < n; ++p) mt = fmaxf(mt, st[p * HP * 4 + 1]);
-    for (uint32_t p = 0; p < n; ++p) Rt = fmaxf(Rt, ref_at(st + p * HP * 4, mt));
+// Join n <= kAtJoin parts (rows of `heads` heads at their slots) by the whole
+// CTA: each thread four values of d of every SEGS-th part, all on their way at
+// once, with the parts' {l, m, R} through shared memory meanwhile.
+template <int D, int THREADS, typename SlotOf, typename Put>
+__device__ __forceinline__ void join_parts(const float* part, int hp, float* smem, uint32_t n, SlotOf slot_of, int heads,
+                                           Put put) {
+  constexpr int ROW = D + 4, MOST = 8;
+  const int items = heads * (D / 4);
+  const int segs = max(THREADS / items, 1);
+  float4* stats = reinterpret_cast<float4*>(smem);  // [part][heads]
+  float4* sums = stats + n * heads;                 // [seg][items]
+  for (uint32_t i = threadIdx.x; i < n * heads; i += THREADS)
+    stats[i] = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(i / heads) * hp + i % heads) * ROW + D));
+  for (int i0 = 0; i0 < items * segs; i0 += THREADS) {  // (once, but for 16 heads of 128 by 256 threads)
+    const int i = i0 + static_cast<int>(threadIdx.x), seg = i / items, it = i - seg * items;
+    const int head = it / (D / 4), d = it % (D / 4) * 4;
+    const bool mine = seg < segs;
+    float mt = -INFINITY, Rt = -INFINITY, lt = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float lt = 0.0f;
-    for (uint32_t p0 = 0; p0 < n; p0 += 8) {
-      float4 x[8];
+    for (uint32_t p0 = seg; p0 < n || p0 == static_cast<uint32_t>(seg); p0 += MOST * segs) {
+      float4 x[MOST];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = p0 + e < n ? __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p0 + e) * HP + head) * ROW + d))
-                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int e = 0; e < MOST; ++e) {
+        x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (const uint32_t p = p0 + e * segs; mine && p < n)
+          x[e] = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p) * hp + head) * ROW + d));
+      }
+      if (p0 == static_cast<uint32_t>(seg)) {
+        if (i0 == 0) __syncthreads();  // the {l, m, R}
+        if (mine) {
+          for (uint32_t p = 0; p < n; ++p) mt = fmaxf(mt, stats[p * heads + head].y);
+          for (uint32_t p = 0; p < n; ++p) Rt = fmaxf(Rt, ref_at(&stats[p * heads + head].x, mt));
+          for (uint32_t p = 0; p < n; ++p) lt += stats[p * heads + head].x * l_scale(&stats[p * heads + head].x, mt);
+        }
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (p0 + e < n) {
-          const float* s = st + (p0 + e) * HP * 4;
-          const float f = sum_scale(s, mt, Rt);
+      for (int e = 0; e < MOST; ++e)
+        if (const uint32_t p = p0 + e * segs; mine && p < n) {
+          const float f = sum_scale(&stats[p * heads + head].x, mt, Rt);
           acc.x += x[e].x * f;
           acc.y += x[e].y * f;
           acc.z += x[e].z * f;
           acc.w += x[e].w * f;
-          lt += s[0] * l_scale(s, mt);
         }
     }
-    put(head, d, acc, lt, mt, Rt);
+    if (segs > 1) {
+      if (mine) sums[i] = acc;
+      __syncthreads();
+      if (seg == 0)
+        for (int q = 1; q < segs; ++q) {
+          const float4 y = sums[q * items + it];
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+        }
+    }
+    if (seg == 0) put(head, d, acc, lt, mt, Rt);
   }
   __syncthreads();  // the shared memory is used again
 }
@@ -197,8 +210,20 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
   float* parts = reinterpret_cast<float*>(smem_u);           // [warp][2][HP][ROW]
   uint32_t* prefix = smem_u + W * 2 * HP * ROW;              // batch + 1
   int32_t* lens = reinterpret_cast<int32_t*>(prefix + a.batch + 1);
+  // of the warps' shares: their pass, and what the pass is
+  struct Share {
+    int b, hq0, heads;
+    uint32_t first, units;  // the pass's units
+  };
+  // of the first and the last pass of this CTA, where they cross its ends
+  struct Cross {
+    uint32_t pass, c0, c1;  // its first and last CTA
+    int last;               // whether this CTA arrived last
+  };
   __shared__ uint32_t scan[W], pass_of[2 * W], leader_of[2 * W];
-  __shared__ int flag;
+  __shared__ Share share_of[2 * W];
+  __shared__ Cross cross[2];
+  __shared__ float4 group_stats[2 * W][HP];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   pdl_launch_dependents();
@@ -506,7 +531,10 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
     // ---- a whole pass to the output, a share to shared memory
     const bool whole = in == 0 && stop == units;
     const int part = warp * 2 + (t == s0 ? 0 : 1);
-    if (!whole && lane == 0) pass_of[part] = static_cast<uint32_t>(b) * per_seq + hh;
+    if (!whole && lane == 0) {
+      pass_of[part] = static_cast<uint32_t>(b) * per_seq + hh;
+      share_of[part] = Share{b, hq0, heads, prefix[b] + hh * units, units};
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -533,98 +561,114 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
   __syncthreads();
 
   // ---- the warps' shares together: neighbouring ones of the same pass
-  struct Pass {
-    int b, heads, hq0;
-    uint32_t hh, first, c0, c1;  // its first unit, its first and last CTA
-  };
-  auto pass_at = [&](uint32_t p) {
-    Pass x;
-    x.b = static_cast<int>(p / per_seq);
-    x.hh = p - static_cast<uint32_t>(x.b) * per_seq;
-    const int h = static_cast<int>(x.hh) / a.hgroups, hg = static_cast<int>(x.hh) - h * a.hgroups;
-    x.heads = min(HP, a.group - hg * HP);
-    x.hq0 = h * a.group + hg * HP;
-    const uint32_t units = units_of(lens[x.b]);
-    x.first = prefix[x.b] + x.hh * units;
-    x.c0 = owner(x.first);
-    x.c1 = owner(x.first + units - 1);
-    return x;
-  };
-  // where a CTA's share of a pass is in the workspace
-  auto slot_of = [](const Pass& x, uint32_t cta) -> int64_t { return static_cast<int64_t>(cta) * 2 + (cta == x.c0 ? 1 : 0); };
   const uint32_t mine = lane < 2 * W ? pass_of[lane] : kAtNone;
-  uint32_t used = __ballot_sync(0xffffffffu, mine != kAtNone);
+  const uint32_t used = __ballot_sync(0xffffffffu, mine != kAtNone);
+  if (used == 0) return;
   const uint32_t below = used & ((1u << lane) - 1u);
   const uint32_t previous = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
   const bool leads = mine != kAtNone && (!below || previous != mine);
   const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+  // the shares of share e's pass
+  auto shares_with = [&](uint32_t e) {
+    const uint32_t lead = 31 - __clz(leaders & ((2u << e) - 1u));
+    const uint32_t later = leaders & ~((2u << e) - 1u);
+    return used & ~((1u << lead) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
+  };
   if (warp == 0 && leads) leader_of[__popc(leaders & ((1u << lane) - 1u))] = lane;
+  if (warp == W - 1 && lane < 2) {
+    const uint32_t e = lane == 0 ? __ffs(used) - 1 : 31 - __clz(used);
+    const Share x = share_of[e];
+    Cross k{kAtNone, 0, 0, 0};
+    if ((x.first < t0 || x.first + x.units > t1) && !(lane == 1 && (leaders & (leaders - 1)) == 0))
+      k = Cross{pass_of[e], owner(x.first), owner(x.first + x.units - 1), 0};
+    cross[lane] = k;
+  }
+  // the factors of the shares, and their passes' {l, m, R}
+  for (uint32_t i = threadIdx.x; i < 2 * W * HP; i += THREADS) {
+    const uint32_t e = i / HP, head = i % HP;
+    if (!((used >> e) & 1u) || static_cast<int>(head) >= share_of[e].heads) continue;
+    const uint32_t own = shares_with(e);
+    auto row_at = [&](uint32_t q) { return parts + ((__ffs(q) - 1) * HP + head) * ROW + D; };
+    float mt = -INFINITY, Rt = -INFINITY;
+    for (uint32_t q = own; q; q &= q - 1) mt = fmaxf(mt, row_at(q)[1]);
+    for (uint32_t q = own; q; q &= q - 1) Rt = fmaxf(Rt, ref_at(row_at(q), mt));
+    float* row = parts + (e * HP + head) * ROW + D;
+    row[3] = sum_scale(row, mt, Rt);
+    if ((leaders >> e) & 1u) {
+      float lt = 0.0f;
+      for (uint32_t q = own; q; q &= q - 1) lt += row_at(q)[0] * l_scale(row_at(q), mt);
+      group_stats[e][head] = make_float4(lt, mt, Rt, 0.0f);
+    }
+  }
   __syncthreads();
   constexpr int kItems = HP * (D / 4);
   for (int i = threadIdx.x; i < __popc(leaders) * kItems; i += THREADS) {
     const uint32_t e0 = leader_of[i / kItems];
     const int head = i % kItems / (D / 4), d = i % (D / 4) * 4;
-    const Pass x = pass_at(pass_of[e0]);
+    const Share x = share_of[e0];
     if (head >= x.heads) continue;
-    uint32_t own = used & ~((1u << e0) - 1u);  // its shares: from e0 up to the next leader
-    const uint32_t later = leaders & ~((2u << e0) - 1u);
-    if (later) own &= (later & (0u - later)) - 1u;
-    float mt = -INFINITY, Rt = -INFINITY, lt = 0.0f;
-    for (uint32_t q = own; q; q &= q - 1) mt = fmaxf(mt, parts[((__ffs(q) - 1) * HP + head) * ROW + D + 1]);
-    for (uint32_t q = own; q; q &= q - 1) Rt = fmaxf(Rt, ref_at(parts + ((__ffs(q) - 1) * HP + head) * ROW + D, mt));
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (uint32_t q = own; q; q &= q - 1) {
+#pragma unroll 4
+    for (uint32_t q = shares_with(e0); q; q &= q - 1) {
       const float* row = parts + ((__ffs(q) - 1) * HP + head) * ROW;
       const float4 y = *reinterpret_cast<const float4*>(row + d);
-      const float f = sum_scale(row + D, mt, Rt);
+      const float f = row[D + 3];
       acc.x += y.x * f;
       acc.y += y.y * f;
       acc.z += y.z * f;
       acc.w += y.w * f;
-      lt += row[D] * l_scale(row + D, mt);
     }
-    if (x.c0 == x.c1) {
-      put4(x.b, x.hq0 + head, d, acc, lt, Rt);
+    const float4 g = group_stats[e0][head];
+    if (x.first >= t0 && x.first + x.units <= t1) {
+      put4(x.b, x.hq0 + head, d, acc, g.x, g.z);
     } else {
-      float* row = a.part + (slot_of(x, blockIdx.x) * HP + head) * ROW;
+      // (the pass's first CTA leaves its share in its second place: the first
+      // place may be that of a pass that ends in it)
+      float* row = a.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (x.first >= t0 ? 1 : 0)) * HP + head) * ROW;
       *reinterpret_cast<float4*>(row + d) = acc;
-      if (d == 0) *reinterpret_cast<float4*>(row + D) = make_float4(lt, mt, Rt, 0.0f);
+      if (d == 0) *reinterpret_cast<float4*>(row + D) = g;
     }
   }
+  if (cross[0].pass == kAtNone && cross[1].pass == kAtNone) return;
 
-  // ---- the CTAs' shares, of the first and the last pass of this run
-  uint32_t done = kAtNone;
+  // ---- the CTAs' shares, in two steps where there are many: kAtJoin
+  // neighbours by the last of them to arrive, then those by the last of all
+  __syncthreads();
+  int32_t* const part_counters = a.counters + static_cast<int64_t>(a.batch) * per_seq;
+  if (threadIdx.x < 2) {
+    Cross& k = cross[threadIdx.x];
+    if (k.pass != kAtNone) {
+      const uint32_t n = k.c1 - k.c0 + 1, lo = (blockIdx.x - k.c0) / kAtJoin * kAtJoin;
+      k.last = arrive_last(n <= kAtJoin ? a.counters + k.pass : part_counters + (k.c0 + lo) * 2 + (lo == 0 ? 1 : 0),
+                           min(kAtJoin, n - lo));
+    }
+  }
+  __syncthreads();
 #pragma unroll 1
-  for (int k = 0; k < 2 && used; ++k) {
-    const uint32_t e = k == 0 ? __ffs(used) - 1 : 31 - __clz(used);
-    const uint32_t p = pass_of[e];
-    const Pass x = pass_at(p);
-    if (p == done || x.c0 == x.c1) continue;
-    done = p;
-    // in two steps where there are many parts: kAtJoin neighbours by the last
-    // of them to arrive, then those by the last of all
-    const uint32_t n = x.c1 - x.c0 + 1, lo = (blockIdx.x - x.c0) / kAtJoin * kAtJoin, group = min(kAtJoin, n - lo);
+  for (int i = 0; i < 2; ++i) {
+    const Cross k = cross[i];
+    if (!k.last) continue;
+    const Share x = share_of[i == 0 ? __ffs(used) - 1 : 31 - __clz(used)];
+    const uint32_t n = k.c1 - k.c0 + 1, lo = (blockIdx.x - k.c0) / kAtJoin * kAtJoin;
     const bool all = n <= kAtJoin;
-    int32_t* pass_counter = a.counters + p;
-    int32_t* group_counter = a.counters + static_cast<int64_t>(a.batch) * per_seq + slot_of(x, x.c0 + lo);
-    if (!arrive_last(all ? pass_counter : group_counter, group, &flag)) continue;
-    join_parts<D, HP, THREADS>(a.part, smem_u, group, [&](uint32_t i) { return slot_of(x, x.c0 + lo + i); }, x.heads,
-                               [&](int head, int d, float4 acc, float lt, float mt, float Rt) {
-                                 if (all) {
-                                   put4(x.b, x.hq0 + head, d, acc, lt, Rt);
-                                 } else {
-                                   float* row = a.part + (slot_of(x, x.c0 + lo) * HP + head) * ROW;
-                                   *reinterpret_cast<float4*>(row + d) = acc;
-                                   if (d == 0) *reinterpret_cast<float4*>(row + D) = make_float4(lt, mt, Rt, 0.0f);
-                                 }
-                               });
+    auto slot_of = [&](uint32_t p) { return static_cast<int64_t>(k.c0 + p) * 2 + (p == 0 ? 1 : 0); };
+    auto put = [&](int head, int d, float4 acc, float lt, float mt, float Rt) { put4(x.b, x.hq0 + head, d, acc, lt, Rt); };
+    join_parts<D, THREADS>(a.part, HP, parts, min(kAtJoin, n - lo), [&](uint32_t p) { return slot_of(lo + p); }, x.heads,
+                           [&](int head, int d, float4 acc, float lt, float mt, float Rt) {
+                             if (all) {
+                               put(head, d, acc, lt, mt, Rt);
+                             } else {
+                               float* row = a.part + (slot_of(lo) * HP + head) * ROW;
+                               *reinterpret_cast<float4*>(row + d) = acc;
+                               if (d == 0) *reinterpret_cast<float4*>(row + D) = make_float4(lt, mt, Rt, 0.0f);
+                             }
+                           });
     if (all) continue;
     const uint32_t groups = (n + kAtJoin - 1) / kAtJoin;
-    if (!arrive_last(pass_counter, groups, &flag)) continue;
-    join_parts<D, HP, THREADS>(a.part, smem_u, groups, [&](uint32_t i) { return slot_of(x, x.c0 + i * kAtJoin); }, x.heads,
-                               [&](int head, int d, float4 acc, float lt, float mt, float Rt) {
-                                 put4(x.b, x.hq0 + head, d, acc, lt, Rt);
-                               });
+    if (threadIdx.x == 0) cross[i].last = arrive_last(a.counters + k.pass, groups);
+    __syncthreads();
+    if (cross[i].last)
+      join_parts<D, THREADS>(a.part, HP, parts, groups, [&](uint32_t p) { return slot_of(p * kAtJoin); }, x.heads, put);
   }
 }
 
