@@ -107,14 +107,25 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-// Joining partial results {l, m, R}: R against the common m, and the factors
-// of l and of the sum.  A part that saw no keys (m never set) counts nothing.
-__device__ __forceinline__ float ref_at(const float* s, float m) {
-  return s[1] == -INFINITY ? -INFINITY : s[1] - m + s[2];
-}
-__device__ __forceinline__ float l_scale(const float* s, float m) { return s[1] == -INFINITY ? 0.0f : ex2f(s[1] - m); }
-__device__ __forceinline__ float sum_scale(const float* s, float m, float R) {
-  return s[1] == -INFINITY ? 0.0f : ex2f(s[1] - m + s[2] - R);
+// Joining results {l, m, R}, one a lane, over the lanes [first, end] that this
+// lane is of: the joint {l, m, R}, and the factor of this lane's sum.  One that
+// saw no keys (m never set) counts nothing.
+__device__ __forceinline__ float4 join_lanes(float l, float m, float R, int first, int end) {
+  const int lane = threadIdx.x & 31;
+  auto over = [&](float v, auto op) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_down_sync(0xffffffffu, v, o);
+      if (lane + o <= end) v = op(v, y);
+    }
+    return __shfl_sync(0xffffffffu, v, first);
+  };
+  auto most = [](float x, float y) { return fmaxf(x, y); };
+  const bool none = m == -INFINITY;
+  const float mt = over(m, most);
+  const float Rt = over(none ? -INFINITY : m - mt + R, most);
+  const float lt = over(l * (none ? 0.0f : ex2f(m - mt)), [](float x, float y) { return x + y; });
+  return make_float4(lt, mt, Rt, none ? 0.0f : ex2f(m - mt + R - Rt));
 }
 
 // Count this CTA in at `counter`, whose `n`-th arrival sets it back to 0; true
@@ -129,45 +140,49 @@ __device__ __forceinline__ bool arrive_last(int32_t* counter, uint32_t n) {
   return true;
 }
 
-// Join n <= kAtJoin parts (rows of `heads` heads at their slots) by the whole
-// CTA: each thread four values of d of every SEGS-th part, all on their way at
-// once, with the parts' {l, m, R} through shared memory meanwhile.
+// Join n <= 32 parts (rows of `heads` heads at their slots) by the whole CTA:
+// each thread four values of d of every segs-th part, eight on their way at
+// once, while the parts' {l, m, R} are joined, a part a lane.
 template <int D, int THREADS, typename SlotOf, typename Put>
 __device__ __forceinline__ void join_parts(const float* part, int hp, float* smem, uint32_t n, SlotOf slot_of, int heads,
                                            Put put) {
   constexpr int ROW = D + 4, MOST = 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int items = heads * (D / 4);
   const int segs = max(THREADS / items, 1);
-  float4* stats = reinterpret_cast<float4*>(smem);  // [part][heads]
-  float4* sums = stats + n * heads;                 // [seg][items]
-  for (uint32_t i = threadIdx.x; i < n * heads; i += THREADS)
-    stats[i] = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(i / heads) * hp + i % heads) * ROW + D));
+  float* factor = smem;                                            // [head][32]
+  float4* stats = reinterpret_cast<float4*>(smem + heads * 32);    // [head]
+  float4* sums = stats + heads;                                    // [seg][items]
+#pragma unroll 1
   for (int i0 = 0; i0 < items * segs; i0 += THREADS) {  // (once, but for 16 heads of 128 by 256 threads)
     const int i = i0 + static_cast<int>(threadIdx.x), seg = i / items, it = i - seg * items;
     const int head = it / (D / 4), d = it % (D / 4) * 4;
     const bool mine = seg < segs;
-    float mt = -INFINITY, Rt = -INFINITY, lt = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (uint32_t p0 = seg; p0 < n || p0 == static_cast<uint32_t>(seg); p0 += MOST * segs) {
+#pragma unroll 1
+    for (uint32_t p0 = 0; p0 < n; p0 += MOST * segs) {
       float4 x[MOST];
 #pragma unroll
       for (int e = 0; e < MOST; ++e) {
         x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (const uint32_t p = p0 + e * segs; mine && p < n)
+        if (const uint32_t p = p0 + e * segs + seg; mine && p < n)
           x[e] = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p) * hp + head) * ROW + d));
       }
-      if (p0 == static_cast<uint32_t>(seg)) {
-        if (i0 == 0) __syncthreads();  // the {l, m, R}
-        if (mine) {
-          for (uint32_t p = 0; p < n; ++p) mt = fmaxf(mt, stats[p * heads + head].y);
-          for (uint32_t p = 0; p < n; ++p) Rt = fmaxf(Rt, ref_at(&stats[p * heads + head].x, mt));
-          for (uint32_t p = 0; p < n; ++p) lt += stats[p * heads + head].x * l_scale(&stats[p * heads + head].x, mt);
+      if (i0 == 0 && p0 == 0) {
+        for (int hd = warp; hd < heads; hd += THREADS / 32) {
+          float4 st = make_float4(0.0f, -INFINITY, -INFINITY, 0.0f);
+          if (lane < static_cast<int>(n))
+            st = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(lane) * hp + hd) * ROW + D));
+          st = join_lanes(st.x, st.y, st.z, 0, 31);
+          factor[hd * 32 + lane] = st.w;
+          if (lane == 0) stats[hd] = st;
         }
+        __syncthreads();
       }
 #pragma unroll
       for (int e = 0; e < MOST; ++e)
-        if (const uint32_t p = p0 + e * segs; mine && p < n) {
-          const float f = sum_scale(&stats[p * heads + head].x, mt, Rt);
+        if (const uint32_t p = p0 + e * segs + seg; mine && p < n) {
+          const float f = factor[head * 32 + p];
           acc.x += x[e].x * f;
           acc.y += x[e].y * f;
           acc.z += x[e].z * f;
@@ -186,7 +201,7 @@ __device__ __forceinline__ void join_parts(const float* part, int hp, float* sme
           acc.w += y.w;
         }
     }
-    if (seg == 0) put(head, d, acc, lt, mt, Rt);
+    if (seg == 0) put(head, d, acc, stats[head]);
   }
   __syncthreads();  // the shared memory is used again
 }
@@ -568,11 +583,11 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
   const uint32_t previous = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
   const bool leads = mine != kAtNone && (!below || previous != mine);
   const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
-  // the shares of share e's pass
-  auto shares_with = [&](uint32_t e) {
-    const uint32_t lead = 31 - __clz(leaders & ((2u << e) - 1u));
+  // the places of the shares of place e's pass
+  auto first_of = [&](uint32_t e) { return 31 - __clz((leaders | 1u) & ((2u << e) - 1u)); };
+  auto end_of = [&](uint32_t e) {
     const uint32_t later = leaders & ~((2u << e) - 1u);
-    return used & ~((1u << lead) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
+    return later ? __ffs(later) - 2 : 31;
   };
   if (warp == 0 && leads) leader_of[__popc(leaders & ((1u << lane) - 1u))] = lane;
   if (warp == W - 1 && lane < 2) {
@@ -583,22 +598,16 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
       k = Cross{pass_of[e], owner(x.first), owner(x.first + x.units - 1), 0};
     cross[lane] = k;
   }
-  // the factors of the shares, and their passes' {l, m, R}
-  for (uint32_t i = threadIdx.x; i < 2 * W * HP; i += THREADS) {
-    const uint32_t e = i / HP, head = i % HP;
-    if (!((used >> e) & 1u) || static_cast<int>(head) >= share_of[e].heads) continue;
-    const uint32_t own = shares_with(e);
-    auto row_at = [&](uint32_t q) { return parts + ((__ffs(q) - 1) * HP + head) * ROW + D; };
-    float mt = -INFINITY, Rt = -INFINITY;
-    for (uint32_t q = own; q; q &= q - 1) mt = fmaxf(mt, row_at(q)[1]);
-    for (uint32_t q = own; q; q &= q - 1) Rt = fmaxf(Rt, ref_at(row_at(q), mt));
-    float* row = parts + (e * HP + head) * ROW + D;
-    row[3] = sum_scale(row, mt, Rt);
-    if ((leaders >> e) & 1u) {
-      float lt = 0.0f;
-      for (uint32_t q = own; q; q &= q - 1) lt += row_at(q)[0] * l_scale(row_at(q), mt);
-      group_stats[e][head] = make_float4(lt, mt, Rt, 0.0f);
-    }
+  // the factors of the shares and their passes' {l, m, R}: a head a warp, a
+  // share a lane
+  for (int head = warp; head < HP; head += W) {
+    float4 st = make_float4(0.0f, -INFINITY, -INFINITY, 0.0f);
+    float* row = parts + (lane * HP + head) * ROW + D;
+    const bool has = mine != kAtNone && head < share_of[lane].heads;
+    if (has) st = *reinterpret_cast<const float4*>(row);
+    st = join_lanes(st.x, st.y, st.z, first_of(lane), end_of(lane));
+    if (has) row[3] = st.w;
+    if (leads) group_stats[lane][head] = st;
   }
   __syncthreads();
   constexpr int kItems = HP * (D / 4);
@@ -608,9 +617,11 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
     const Share x = share_of[e0];
     if (head >= x.heads) continue;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const uint32_t end = end_of(e0);
 #pragma unroll 4
-    for (uint32_t q = shares_with(e0); q; q &= q - 1) {
-      const float* row = parts + ((__ffs(q) - 1) * HP + head) * ROW;
+    for (uint32_t e = e0; e <= end; ++e) {
+      if (!((used >> e) & 1u)) continue;
+      const float* row = parts + (e * HP + head) * ROW;
       const float4 y = *reinterpret_cast<const float4*>(row + d);
       const float f = row[D + 3];
       acc.x += y.x * f;
@@ -652,15 +663,15 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
     const uint32_t n = k.c1 - k.c0 + 1, lo = (blockIdx.x - k.c0) / kAtJoin * kAtJoin;
     const bool all = n <= kAtJoin;
     auto slot_of = [&](uint32_t p) { return static_cast<int64_t>(k.c0 + p) * 2 + (p == 0 ? 1 : 0); };
-    auto put = [&](int head, int d, float4 acc, float lt, float mt, float Rt) { put4(x.b, x.hq0 + head, d, acc, lt, Rt); };
+    auto put = [&](int head, int d, float4 acc, float4 g) { put4(x.b, x.hq0 + head, d, acc, g.x, g.z); };
     join_parts<D, THREADS>(a.part, HP, parts, min(kAtJoin, n - lo), [&](uint32_t p) { return slot_of(lo + p); }, x.heads,
-                           [&](int head, int d, float4 acc, float lt, float mt, float Rt) {
+                           [&](int head, int d, float4 acc, float4 g) {
                              if (all) {
-                               put(head, d, acc, lt, mt, Rt);
+                               put(head, d, acc, g);
                              } else {
                                float* row = a.part + (slot_of(lo) * HP + head) * ROW;
                                *reinterpret_cast<float4*>(row + d) = acc;
-                               if (d == 0) *reinterpret_cast<float4*>(row + D) = make_float4(lt, mt, Rt, 0.0f);
+                               if (d == 0) *reinterpret_cast<float4*>(row + D) = g;
                              }
                            });
     if (all) continue;
