@@ -6,9 +6,9 @@
 // instructions on registers carry it and nothing goes through shared memory
 // on the way.
 //
-// Work.  A pass is one sequence, key head and group of up to 8 (16) query
-// heads; its units are its blocks of 16 keys and one more for what a pass
-// costs whatever its length.  The units of the whole batch, pass after pass,
+// Work.  A pass is one sequence, key head and group of up to 8 query heads; its
+// units are its blocks of 16 keys and two more for what a pass costs whatever
+// its length (64 ragged sequences: 44 us with one, 39.4 with two to four).  The units of the whole batch, pass after pass,
 // are cut into as many equal runs as there are CTAs, and a CTA's run into one
 // for each warp, so a long sequence among short ones spreads over the GPU and
 // every warp reads about the same number of bytes, without meeting another
@@ -19,8 +19,11 @@
 // CTA that arrives last on the pass's counter joins those.  All are joined in
 // the order of the keys.
 //
-// A warp takes 16 keys at a time (always inside one page).  With G <= 8 query
-// heads to a key head (NT = 1; 16 with NT = 2):
+// A warp takes blocks of 16 keys (always inside one page), one at a time at
+// head_dim 128 and two at 64, which is 4 KiB on its way either way, and up to
+// eight query heads of a key head; more heads are further passes over the
+// keys, which find them in L2 (16 heads in one pass need twice the registers,
+// so half the warps: 33 us against 26.5 at 4 x 16384 tokens, 48 / 3 heads).
 //   S^T = K Q^T    m16n8k16, 16 keys x 8 heads; the contraction over d may
 //                  take d in any order common to both, so a lane's fragments
 //                  are four consecutive codes of a 16-byte load.
@@ -47,7 +50,11 @@
 namespace lgt {
 namespace {
 
+constexpr int kAtWarps = 16;        // of 128 registers: they fill an SM
+constexpr int kAtThreads = kAtWarps * 32;
+constexpr int kAtHeads = 8;         // query heads of a pass
 constexpr int kAtKeys = 16;         // a unit
+constexpr int kAtPassUnits = 2;     // of a pass besides its keys
 constexpr int kAtMaxBatch = 8192;   // lengths and prefix sums in shared memory
 constexpr uint32_t kAtJoin = 32;    // CTAs' parts joined in one step; their number is at most its square
 constexpr uint32_t kAtNone = 0xffffffffu;
@@ -62,7 +69,7 @@ struct AttendArgs {
   int32_t* counters;  // one per pass, then one per part
   int64_t qs, os, table_stride;
   uint32_t pages;
-  int32_t max_pages, batch, hk, group, hgroups;  // hgroups: groups of 8 * NT query heads of a key head
+  int32_t max_pages, batch, hk, group, hgroups;  // hgroups: groups of 8 query heads of a key head
   int32_t max_len;
   MagicDiv div_page;
   float cs;  // scale * log2(e)
@@ -143,81 +150,69 @@ __device__ __forceinline__ bool arrive_last(int32_t* counter, uint32_t n) {
 // Join n <= 32 parts (rows of `heads` heads at their slots) by the whole CTA:
 // each thread four values of d of every segs-th part, eight on their way at
 // once, while the parts' {l, m, R} are joined, a part a lane.
-template <int D, int THREADS, typename SlotOf, typename Put>
-__device__ __forceinline__ void join_parts(const float* part, int hp, float* smem, uint32_t n, SlotOf slot_of, int heads,
-                                           Put put) {
-  constexpr int ROW = D + 4, MOST = 8;
+template <int D, typename SlotOf, typename Put>
+__device__ __forceinline__ void join_parts(const float* part, float* smem, uint32_t n, SlotOf slot_of, int heads, Put put) {
+  constexpr int ROW = D + 4, HP = kAtHeads, MOST = 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int items = heads * (D / 4);
-  const int segs = max(THREADS / items, 1);
+  const int items = heads * (D / 4);  // at most half of the threads
+  const int segs = kAtThreads / items;
   float* factor = smem;                                            // [head][32]
   float4* stats = reinterpret_cast<float4*>(smem + heads * 32);    // [head]
   float4* sums = stats + heads;                                    // [seg][items]
+  const int seg = static_cast<int>(threadIdx.x) / items, it = static_cast<int>(threadIdx.x) - seg * items;
+  const int head = it / (D / 4), d = it % (D / 4) * 4;
+  const bool mine = seg < segs;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-  for (int i0 = 0; i0 < items * segs; i0 += THREADS) {  // (once, but for 16 heads of 128 by 256 threads)
-    const int i = i0 + static_cast<int>(threadIdx.x), seg = i / items, it = i - seg * items;
-    const int head = it / (D / 4), d = it % (D / 4) * 4;
-    const bool mine = seg < segs;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-    for (uint32_t p0 = 0; p0 < n; p0 += MOST * segs) {
-      float4 x[MOST];
+  for (uint32_t p0 = 0; p0 < n; p0 += MOST * segs) {
+    float4 x[MOST];
 #pragma unroll
-      for (int e = 0; e < MOST; ++e) {
-        x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (const uint32_t p = p0 + e * segs + seg; mine && p < n)
-          x[e] = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p) * hp + head) * ROW + d));
-      }
-      if (i0 == 0 && p0 == 0) {
-        for (int hd = warp; hd < heads; hd += THREADS / 32) {
-          float4 st = make_float4(0.0f, -INFINITY, -INFINITY, 0.0f);
-          if (lane < static_cast<int>(n))
-            st = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(lane) * hp + hd) * ROW + D));
-          st = join_lanes(st.x, st.y, st.z, 0, 31);
-          factor[hd * 32 + lane] = st.w;
-          if (lane == 0) stats[hd] = st;
-        }
-        __syncthreads();
-      }
-#pragma unroll
-      for (int e = 0; e < MOST; ++e)
-        if (const uint32_t p = p0 + e * segs + seg; mine && p < n) {
-          const float f = factor[head * 32 + p];
-          acc.x += x[e].x * f;
-          acc.y += x[e].y * f;
-          acc.z += x[e].z * f;
-          acc.w += x[e].w * f;
-        }
+    for (int e = 0; e < MOST; ++e) {
+      x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (const uint32_t p = p0 + e * segs + seg; mine && p < n)
+        x[e] = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(p) * HP + head) * ROW + d));
     }
-    if (segs > 1) {
-      if (mine) sums[i] = acc;
+    if (p0 == 0) {
+      if (warp < heads) {
+        float4 st = make_float4(0.0f, -INFINITY, -INFINITY, 0.0f);
+        if (lane < static_cast<int>(n))
+          st = __ldcg(reinterpret_cast<const float4*>(part + (slot_of(lane) * HP + warp) * ROW + D));
+        st = join_lanes(st.x, st.y, st.z, 0, 31);
+        factor[warp * 32 + lane] = st.w;
+        if (lane == 0) stats[warp] = st;
+      }
       __syncthreads();
-      if (seg == 0)
-        for (int q = 1; q < segs; ++q) {
-          const float4 y = sums[q * items + it];
-          acc.x += y.x;
-          acc.y += y.y;
-          acc.z += y.z;
-          acc.w += y.w;
-        }
     }
-    if (seg == 0) put(head, d, acc, stats[head]);
+#pragma unroll
+    for (int e = 0; e < MOST; ++e)
+      if (const uint32_t p = p0 + e * segs + seg; mine && p < n) {
+        const float f = factor[head * 32 + p];
+        acc.x += x[e].x * f;
+        acc.y += x[e].y * f;
+        acc.z += x[e].z * f;
+        acc.w += x[e].w * f;
+      }
+  }
+  if (mine) sums[threadIdx.x] = acc;
+  __syncthreads();
+  if (seg == 0) {
+    for (int q = 1; q < segs; ++q) {
+      const float4 y = sums[q * items + it];
+      acc.x += y.x;
+      acc.y += y.y;
+      acc.z += y.z;
+      acc.w += y.w;
+    }
+    put(head, d, acc, stats[head]);
   }
   __syncthreads();  // the shared memory is used again
 }
 
-template <int NT>
-struct AttendCfg {
-  // registers: 16 warps of 128 (NT = 1) or 8 of 255 fill an SM
-  static constexpr int W = NT == 1 ? 16 : 8;
-  static constexpr int THREADS = W * 32;
-  static constexpr int HP = 8 * NT;  // query heads of a pass
-};
-
-template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int W = AttendCfg<NT>::W, THREADS = AttendCfg<NT>::THREADS, HP = AttendCfg<NT>::HP;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kAtThreads, 1) cache_attend_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int W = kAtWarps, THREADS = kAtThreads, HP = kAtHeads;
   constexpr int ROW = D + 4;       // floats of a part's row
+  constexpr int U = 128 / D;       // blocks of keys a step
   constexpr int KP = D / 64;       // 16-byte pieces of a key a lane loads
   constexpr int VW = D / 32;       // words of a value row a lane loads (D / 8 bytes)
   constexpr int MT = D / 16;       // m-tiles of O^T
@@ -247,7 +242,7 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
 
   // ---- lengths and prefix sums of the sequences' units
   const uint32_t per_seq = static_cast<uint32_t>(a.hk * a.hgroups);
-  auto units_of = [](int len) { return static_cast<uint32_t>((len + kAtKeys - 1) / kAtKeys + 1); };
+  auto units_of = [](int len) { return static_cast<uint32_t>((len + kAtKeys - 1) / kAtKeys + kAtPassUnits); };
   {
     uint32_t carry = 0;
     for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
@@ -321,9 +316,9 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
     int key = static_cast<int>(in) * kAtKeys;
 
     // ---- the first keys on their way
-    uint4 kw[2][KP];
-    uint32_t vw[4][VW];
-    int kx[2], vx[2];
+    uint4 kw[U][2][KP];
+    uint32_t vw[U][4][VW];
+    int kx[U][2], vx[U][2];
     auto page_of = [&](int at) -> uint32_t {
       if (at >= key1) return kAtNone;
       return static_cast<uint32_t>(
@@ -333,17 +328,17 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
       const int off = at - static_cast<int>(magic_div(static_cast<uint32_t>(at), a.div_page)) * a.page;
       return (static_cast<int64_t>(page) * a.hk + h) * a.page + off;
     };
-    auto load_k = [&](int at, uint32_t page) {
+    auto load_k = [&](int u, int at, uint32_t page) {
       if (page >= a.pages) return;
       const int64_t row = row_of(at, page);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int p = 0; p < KP; ++p) kw[i][p] = ld_stream_v4(a.k + (row + r + 8 * i) * D + p * 64 + c * 16);
-        kx[i] = a.ke[row + r + 8 * i];
+        for (int p = 0; p < KP; ++p) kw[u][i][p] = ld_stream_v4(a.k + (row + r + 8 * i) * D + p * 64 + c * 16);
+        kx[u][i] = a.ke[row + r + 8 * i];
       }
     };
-    auto load_v = [&](int at, uint32_t page) {
+    auto load_v = [&](int u, int at, uint32_t page) {
       if (page >= a.pages) return;
       const int64_t row = row_of(at, page);
 #pragma unroll
@@ -351,39 +346,41 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
         const uint8_t* p = a.v + (row + 2 * c + (i & 1) + 8 * (i >> 1)) * D + r * (D / 8);
         if constexpr (D == 128) {
           const uint4 x = ld_stream_v4(p);
-          vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
+          vw[u][i][0] = x.x; vw[u][i][1] = x.y; vw[u][i][2] = x.z; vw[u][i][3] = x.w;
         } else {
           const uint2 x = ld_stream_v2(p);
-          vw[i][0] = x.x; vw[i][1] = x.y;
+          vw[u][i][0] = x.x; vw[u][i][1] = x.y;
         }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) vx[i] = a.ve[row + r + 8 * i];
+      for (int i = 0; i < 2; ++i) vx[u][i] = a.ve[row + r + 8 * i];
     };
-    uint32_t page = page_of(key), next_page = page_of(key + kAtKeys);
-    load_k(key, page);
-    load_v(key, page);
+    uint32_t page[U], next_page[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      page[u] = page_of(key + u * kAtKeys);
+      next_page[u] = page_of(key + (U + u) * kAtKeys);
+      load_k(u, key + u * kAtKeys, page[u]);
+      load_v(u, key + u * kAtKeys, page[u]);
+    }
 
     // ---- the queries as B fragments: lane (r, c) has head r's values
     // p*64 + c*16 + 4j + {0, 1 | 2, 3} for step (p, j), in fp16 (bf16 ones
     // times a power of two that brings the head's largest to [1, 2))
-    uint32_t qf[NT][KP * 4][2];
-    float qscale[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int head = n * 8 + r;
+    uint32_t qf[KP * 4][2];
+    float qscale[2];
+    {
       uint4 w[KP][2];
 #pragma unroll
       for (int p = 0; p < KP; ++p)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           w[p][e] = make_uint4(0u, 0u, 0u, 0u);
-          if (head < heads)
+          if (r < heads)
             w[p][e] = *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(b) * a.qs +
-                                                      static_cast<int64_t>(hq0 + head) * D + p * 64 + c * 16 + e * 8);
+                                                      static_cast<int64_t>(hq0 + r) * D + p * 64 + c * 16 + e * 8);
         }
-      float mine = a.cs;
-      float inv = 1.0f;
+      float mine = a.cs, inv = 1.0f;
       if constexpr (BF16) {
         uint32_t top = 0;  // the largest exponent field of a finite value
 #pragma unroll
@@ -411,136 +408,121 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
           const uint32_t w0 = (j & 1) ? src.z : src.x, w1 = (j & 1) ? src.w : src.y;
           if constexpr (BF16) {
             const float2 x0 = unpack_pair16<true>(w0), x1 = unpack_pair16<true>(w1);
-            qf[n][p * 4 + j][0] = pack_pair16<false>(x0.x * inv, x0.y * inv);
-            qf[n][p * 4 + j][1] = pack_pair16<false>(x1.x * inv, x1.y * inv);
+            qf[p * 4 + j][0] = pack_pair16<false>(x0.x * inv, x0.y * inv);
+            qf[p * 4 + j][1] = pack_pair16<false>(x1.x * inv, x1.y * inv);
           } else {
-            qf[n][p * 4 + j][0] = w0;
-            qf[n][p * 4 + j][1] = w1;
+            qf[p * 4 + j][0] = w0;
+            qf[p * 4 + j][1] = w1;
           }
         }
       // this lane's columns of S are heads 2c and 2c + 1
-      qscale[n][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
-      qscale[n][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+      qscale[0] = __shfl_sync(0xffffffffu, mine, 8 * c);
+      qscale[1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
     }
 
-    float o[MT][NT][4];
-    float l[NT][2], m[NT][2], R[NT][2];
+    float o[MT][4];
+    float l[2] = {0.0f, 0.0f}, m[2] = {-INFINITY, -INFINITY}, R[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      l[n][0] = l[n][1] = 0.0f;
-      m[n][0] = m[n][1] = R[n][0] = R[n][1] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
-    }
+    for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-    // ---- the keys, 16 at a time
-    for (; key < key1; key += kAtKeys) {
-      const int next = key + kAtKeys;
-      const uint32_t page2 = page_of(next + kAtKeys);
-      const int valid = page < a.pages ? min(16, key1 - key) : 0;  // a page that is none holds no keys
-      if (valid > 0) {
-        float s[NT][4];
+    // ---- the keys
+    for (; key < key1; key += U * kAtKeys) {
+      const int next = key + U * kAtKeys;
+      uint32_t page2[U];
+      int valid[U];  // keys of the block (a page that is none holds none)
+      float s[U][4], ve[U][2];
+      bool over = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      for (int u = 0; u < U; ++u) {
+        page2[u] = page_of(next + (U + u) * kAtKeys);
+        valid[u] = page[u] < a.pages ? min(16, max(key1 - key - u * kAtKeys, 0)) : 0;
+        s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.0f;
 #pragma unroll
         for (int p = 0; p < KP; ++p) {
-          const uint32_t x0[4] = {kw[0][p].x, kw[0][p].y, kw[0][p].z, kw[0][p].w};
-          const uint32_t x1[4] = {kw[1][p].x, kw[1][p].y, kw[1][p].z, kw[1][p].w};
+          const uint32_t x0[4] = {kw[u][0][p].x, kw[u][0][p].y, kw[u][0][p].z, kw[u][0][p].w};
+          const uint32_t x1[4] = {kw[u][1][p].x, kw[u][1][p].y, kw[u][1][p].z, kw[u][1][p].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = widen_lo(x0[j]), a1 = widen_lo(x1[j]), a2 = widen_hi(x0[j]), a3 = widen_hi(x1[j]);
+          for (int j = 0; j < 4; ++j)
+            mma_16816(s[u], widen_lo(x0[j]), widen_lo(x1[j]), widen_hi(x0[j]), widen_hi(x1[j]), qf[p * 4 + j][0],
+                      qf[p * 4 + j][1]);
+        }
+        const float f0 = pow2i(kx[u][0] - 127), f1 = pow2i(kx[u][1] - 127);
+        ve[u][0] = static_cast<float>(vx[u][0] - 127);
+        ve[u][1] = static_cast<float>(vx[u][1] - 127);
+        load_k(u, next + u * kAtKeys, next_page[u]);
+        s[u][0] = r < valid[u] ? s[u][0] * f0 * qscale[0] : -INFINITY;
+        s[u][1] = r < valid[u] ? s[u][1] * f0 * qscale[1] : -INFINITY;
+        s[u][2] = r + 8 < valid[u] ? s[u][2] * f1 * qscale[0] : -INFINITY;
+        s[u][3] = r + 8 < valid[u] ? s[u][3] * f1 * qscale[1] : -INFINITY;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816(s[n], a0, a1, a2, a3, qf[n][p * 4 + j][0], qf[n][p * 4 + j][1]);
+        for (int e = 0; e < 2; ++e) {
+          const float ref = m[e] == -INFINITY ? 0.0f : m[e];
+          const float d0 = s[u][e] - ref, d1 = s[u][2 + e] - ref, top = R[e] + kAtLazy;
+          over |= d0 > kAtLazy || d1 > kAtLazy || d0 + ve[u][0] > top || d1 + ve[u][1] > top;
+        }
+      }
+      if (__any_sync(0xffffffffu, over)) {
+        // move the references to these keys' maxima, where they are larger
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(s[u][e], s[u][2 + e]));
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
+          const float mn = fmaxf(m[e], x), ref = mn == -INFINITY ? 0.0f : mn;
+#pragma unroll
+          for (int u = 0; u < U; ++u) y = fmaxf(y, fmaxf(s[u][e] - ref + ve[u][0], s[u][2 + e] - ref + ve[u][1]));
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, sh));
+          const float moved = m[e] == -INFINITY ? -INFINITY : m[e] - ref;  // <= 0
+          const float old = m[e] == -INFINITY ? -INFINITY : R[e] + moved;  // R against the new m
+          const float Rn = fmaxf(rintf(old), ceilf(y));
+          const float fl = ex2f(moved), fo = m[e] == -INFINITY ? 0.0f : ex2f(old - Rn);
+          l[e] *= fl;
+          m[e] = mn;
+          R[e] = Rn;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[i][e] *= fo;
+            o[i][2 + e] *= fo;
           }
         }
-        const int k0e = kx[0], k1e = kx[1];
-        const float v0e = static_cast<float>(vx[0] - 127), v1e = static_cast<float>(vx[1] - 127);
-        load_k(next, next_page);
-        const float f0 = pow2i(k0e - 127), f1 = pow2i(k1e - 127);
-        bool over = false;
+      }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          s[n][0] = r < valid ? s[n][0] * f0 * qscale[n][0] : -INFINITY;
-          s[n][1] = r < valid ? s[n][1] * f0 * qscale[n][1] : -INFINITY;
-          s[n][2] = r + 8 < valid ? s[n][2] * f1 * qscale[n][0] : -INFINITY;
-          s[n][3] = r + 8 < valid ? s[n][3] * f1 * qscale[n][1] : -INFINITY;
+      for (int u = 0; u < U; ++u) {
+        float w[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float ref = m[n][e] == -INFINITY ? 0.0f : m[n][e];
-            const float d0 = s[n][e] - ref, d1 = s[n][2 + e] - ref, top = R[n][e] + kAtLazy;
-            over |= d0 > kAtLazy || d1 > kAtLazy || d0 + v0e > top || d1 + v1e > top;
-          }
+        for (int e = 0; e < 2; ++e) {
+          const float ref = m[e] == -INFINITY ? 0.0f : m[e];
+          const float p0 = ex2f(s[u][e] - ref), p1 = ex2f(s[u][2 + e] - ref);
+          l[e] += p0 + p1;
+          // (R never set: every p is 0 or not a number)
+          const float down = m[e] == -INFINITY ? 0.0f : R[e];
+          w[e] = p0 * pow2i(static_cast<int>(ve[u][0] - down));
+          w[2 + e] = p1 * pow2i(static_cast<int>(ve[u][1] - down));
         }
-        if (__any_sync(0xffffffffu, over)) {
-          // move the references to these keys' maxima, where they are larger
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(s[n][e], s[n][2 + e]);
-#pragma unroll
-              for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
-              const float mn = fmaxf(m[n][e], x), ref = mn == -INFINITY ? 0.0f : mn;
-              float y = fmaxf(s[n][e] - ref + v0e, s[n][2 + e] - ref + v1e);
-#pragma unroll
-              for (int sh = 4; sh < 32; sh <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, sh));
-              const float moved = m[n][e] == -INFINITY ? -INFINITY : m[n][e] - ref;  // <= 0
-              const float old = m[n][e] == -INFINITY ? -INFINITY : R[n][e] + moved;  // R against the new m
-              const float Rn = fmaxf(rintf(old), ceilf(y));
-              const float fl = ex2f(moved), fo = m[n][e] == -INFINITY ? 0.0f : ex2f(old - Rn);
-              l[n][e] *= fl;
-              m[n][e] = mn;
-              R[n][e] = Rn;
-#pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                o[i][n][e] *= fo;
-                o[i][n][2 + e] *= fo;
-              }
-            }
-        }
-        uint32_t pf[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float ref = m[n][e] == -INFINITY ? 0.0f : m[n][e];
-            const float p0 = ex2f(s[n][e] - ref), p1 = ex2f(s[n][2 + e] - ref);
-            l[n][e] += p0 + p1;
-            // (R never set: every p is 0 or not a number)
-            const float down = m[n][e] == -INFINITY ? 0.0f : R[n][e];
-            w[e] = p0 * pow2i(static_cast<int>(v0e - down));
-            w[2 + e] = p1 * pow2i(static_cast<int>(v1e - down));
-          }
-          pf[n][0] = transpose_8x8(pack_pair16<false>(w[0], w[1]));
-          pf[n][1] = transpose_8x8(pack_pair16<false>(w[2], w[3]));
-        }
-        if (valid < 16) {  // what lies past the end may be anything, a NaN too
+        const uint32_t b0 = transpose_8x8(pack_pair16<false>(w[0], w[1]));
+        const uint32_t b1 = transpose_8x8(pack_pair16<false>(w[2], w[3]));
+        if (valid[u] < 16) {  // what lies past the end may be anything, a NaN too
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (2 * c + (i & 1) + 8 * (i >> 1) >= valid) {
+            if (2 * c + (i & 1) + 8 * (i >> 1) >= valid[u]) {
 #pragma unroll
-              for (int j = 0; j < VW; ++j) vw[i][j] = 0u;
+              for (int j = 0; j < VW; ++j) vw[u][i][j] = 0u;
             }
         }
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
-          const uint32_t lo0 = prmt(vw[0][j], vw[1][j], 0x5140u), lo1 = prmt(vw[0][j], vw[1][j], 0x7362u);
-          const uint32_t hi0 = prmt(vw[2][j], vw[3][j], 0x5140u), hi1 = prmt(vw[2][j], vw[3][j], 0x7362u);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t x = e ? lo1 : lo0, y = e ? hi1 : hi0;
-            const uint32_t a0 = widen_lo(x), a1 = widen_hi(x), a2 = widen_lo(y), a3 = widen_hi(y);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816(o[2 * j + e][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
-          }
+          const uint32_t lo0 = prmt(vw[u][0][j], vw[u][1][j], 0x5140u), lo1 = prmt(vw[u][0][j], vw[u][1][j], 0x7362u);
+          const uint32_t hi0 = prmt(vw[u][2][j], vw[u][3][j], 0x5140u), hi1 = prmt(vw[u][2][j], vw[u][3][j], 0x7362u);
+          mma_16816(o[2 * j], widen_lo(lo0), widen_hi(lo0), widen_lo(hi0), widen_hi(hi0), b0, b1);
+          mma_16816(o[2 * j + 1], widen_lo(lo1), widen_hi(lo1), widen_lo(hi1), widen_hi(hi1), b0, b1);
         }
-      } else {
-        load_k(next, next_page);
+        load_v(u, next + u * kAtKeys, next_page[u]);
+        page[u] = next_page[u];
+        next_page[u] = page2[u];
       }
-      load_v(next, next_page);
-      page = next_page;
-      next_page = page2;
     }
 
     // ---- a whole pass to the output, a share to shared memory
@@ -551,32 +533,30 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
       share_of[part] = Share{b, hq0, heads, prefix[b] + hh * units, units};
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int sh = 4; sh < 32; sh <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], sh);
+      const int head = 2 * c + e;
+      if (head < heads) {
+        float* row = parts + (part * HP + head) * ROW;
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], sh);
-        const int head = n * 8 + 2 * c + e;
-        if (head < heads) {
-          float* row = parts + (part * HP + head) * ROW;
-#pragma unroll
-          for (int i = 0; i < MT; i += 2) {
-            const float4 x = make_float4(o[i][n][e], o[i][n][2 + e], o[i + 1][n][e], o[i + 1][n][2 + e]);
-            const int d = r * (D / 8) + 2 * i;
-            if (whole)
-              put4(b, hq0 + head, d, x, l[n][e], R[n][e]);
-            else
-              *reinterpret_cast<float4*>(row + d) = x;
-          }
-          if (!whole && r == 0) *reinterpret_cast<float4*>(row + D) = make_float4(l[n][e], m[n][e], R[n][e], 0.0f);
+        for (int i = 0; i < MT; i += 2) {
+          const float4 x = make_float4(o[i][e], o[i][2 + e], o[i + 1][e], o[i + 1][2 + e]);
+          const int d = r * (D / 8) + 2 * i;
+          if (whole)
+            put4(b, hq0 + head, d, x, l[e], R[e]);
+          else
+            *reinterpret_cast<float4*>(row + d) = x;
         }
+        if (!whole && r == 0) *reinterpret_cast<float4*>(row + D) = make_float4(l[e], m[e], R[e], 0.0f);
       }
+    }
     t += stop - in;
   }
   __syncthreads();
 
   // ---- the warps' shares together: neighbouring ones of the same pass
-  const uint32_t mine = lane < 2 * W ? pass_of[lane] : kAtNone;
+  const uint32_t mine = pass_of[lane];
   const uint32_t used = __ballot_sync(0xffffffffu, mine != kAtNone);
   if (used == 0) return;
   const uint32_t below = used & ((1u << lane) - 1u);
@@ -600,7 +580,7 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
   }
   // the factors of the shares and their passes' {l, m, R}: a head a warp, a
   // share a lane
-  for (int head = warp; head < HP; head += W) {
+  if (const int head = warp; head < HP) {
     float4 st = make_float4(0.0f, -INFINITY, -INFINITY, 0.0f);
     float* row = parts + (lane * HP + head) * ROW + D;
     const bool has = mine != kAtNone && head < share_of[lane].heads;
@@ -664,7 +644,7 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
     const bool all = n <= kAtJoin;
     auto slot_of = [&](uint32_t p) { return static_cast<int64_t>(k.c0 + p) * 2 + (p == 0 ? 1 : 0); };
     auto put = [&](int head, int d, float4 acc, float4 g) { put4(x.b, x.hq0 + head, d, acc, g.x, g.z); };
-    join_parts<D, THREADS>(a.part, HP, parts, min(kAtJoin, n - lo), [&](uint32_t p) { return slot_of(lo + p); }, x.heads,
+    join_parts<D>(a.part, parts, min(kAtJoin, n - lo), [&](uint32_t p) { return slot_of(lo + p); }, x.heads,
                            [&](int head, int d, float4 acc, float4 g) {
                              if (all) {
                                put(head, d, acc, g);
@@ -679,12 +659,12 @@ __global__ void __launch_bounds__(AttendCfg<NT>::THREADS, 1) cache_attend_kernel
     if (threadIdx.x == 0) cross[i].last = arrive_last(a.counters + k.pass, groups);
     __syncthreads();
     if (cross[i].last)
-      join_parts<D, THREADS>(a.part, HP, parts, groups, [&](uint32_t p) { return slot_of(p * kAtJoin); }, x.heads, put);
+      join_parts<D>(a.part, parts, groups, [&](uint32_t p) { return slot_of(p * kAtJoin); }, x.heads, put);
   }
 }
 
 struct AttendPlan {
-  int nt, hgroups, ctas;
+  int hgroups, ctas;
   size_t part_bytes, bytes;
 };
 
@@ -695,24 +675,21 @@ bool plan_attend(int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t bat
     cudaGetLastError();
     return false;
   }
-  const int group = q_heads / k_heads;
-  p->nt = group <= 8 ? 1 : 2;
-  p->hgroups = (group + 8 * p->nt - 1) / (8 * p->nt);
+  p->hgroups = (q_heads / k_heads + kAtHeads - 1) / kAtHeads;
   p->ctas = sms;
-  p->part_bytes = static_cast<size_t>(p->ctas) * 2 * 8 * p->nt * (head_dim + 4) * sizeof(float);
+  p->part_bytes = static_cast<size_t>(p->ctas) * 2 * kAtHeads * (head_dim + 4) * sizeof(float);
   p->bytes = p->part_bytes + (static_cast<size_t>(batch) * k_heads * p->hgroups + 2 * p->ctas) * sizeof(int32_t);
   return true;
 }
 
-template <int D, int NT, bool BF16>
+template <int D, bool BF16>
 cudaError_t launch_attend(const AttendArgs& a, int ctas, cudaStream_t stream) {
-  using C = AttendCfg<NT>;
-  constexpr size_t parts = sizeof(float) * C::W * 2 * C::HP * (D + 4);
+  constexpr size_t parts = sizeof(float) * kAtWarps * 2 * kAtHeads * (D + 4);
   constexpr size_t most = parts + sizeof(uint32_t) * (2 * kAtMaxBatch + 1);
-  static_assert(most <= 227 * 1024 - 1024, "shared memory");
-  const cudaError_t e = set_smem_once<cache_attend_kernel<D, NT, BF16>>(static_cast<int>(most));
+  static_assert(most <= 227 * 1024 - 6 * 1024, "shared memory, with the 5 KiB that are not dynamic");
+  const cudaError_t e = set_smem_once<cache_attend_kernel<D, BF16>>(static_cast<int>(most));
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attend_kernel<D, NT, BF16>, dim3(static_cast<unsigned>(ctas)), dim3(C::THREADS),
+  return launch_pdl(cache_attend_kernel<D, BF16>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads),
                     parts + sizeof(uint32_t) * (2 * static_cast<size_t>(a.batch) + 1), stream, a);
 }
 
@@ -759,7 +736,7 @@ extern "C" gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void
   if (batch > lgt::kAtMaxBatch || max_len > (int64_t{1} << 30)) return GEMM_ERR_UNSUPPORTED;
   lgt::AttendPlan p;
   if (!lgt::plan_attend(q_heads, c.k_heads, c.head_dim, batch, &p)) return GEMM_ERR_CUDA;
-  if ((max_len / lgt::kAtKeys + 2) * batch * c.k_heads * p.hgroups >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
+  if ((max_len / lgt::kAtKeys + lgt::kAtPassUnits + 1) * batch * c.k_heads * p.hgroups >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
     return GEMM_ERR_WORKSPACE;
   lgt::AttendArgs a;
@@ -790,11 +767,9 @@ extern "C" gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void
   const bool bf16 = dtype == GEMM_BF16;
   cudaError_t e;
   if (c.head_dim == 128)
-    e = p.nt == 1 ? (bf16 ? lgt::launch_attend<128, 1, true>(a, p.ctas, s) : lgt::launch_attend<128, 1, false>(a, p.ctas, s))
-                  : (bf16 ? lgt::launch_attend<128, 2, true>(a, p.ctas, s) : lgt::launch_attend<128, 2, false>(a, p.ctas, s));
+    e = bf16 ? lgt::launch_attend<128, true>(a, p.ctas, s) : lgt::launch_attend<128, false>(a, p.ctas, s);
   else
-    e = p.nt == 1 ? (bf16 ? lgt::launch_attend<64, 1, true>(a, p.ctas, s) : lgt::launch_attend<64, 1, false>(a, p.ctas, s))
-                  : (bf16 ? lgt::launch_attend<64, 2, true>(a, p.ctas, s) : lgt::launch_attend<64, 2, false>(a, p.ctas, s));
+    e = bf16 ? lgt::launch_attend<64, true>(a, p.ctas, s) : lgt::launch_attend<64, false>(a, p.ctas, s);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
