@@ -453,32 +453,27 @@ def _torch_dtype(dtype):
     return torch.bfloat16 if dtype == GEMM_BF16 else torch.float16
 
 
-def _rows(what, name, t, heads, head_dim, dtype, rows=None):
-    """Check a [rows][heads][head_dim] device tensor of 16-bit values (dtype:
-    torch's) whose heads are contiguous; returns its row stride in elements."""
-    if not getattr(t, "is_cuda", False):
+def _rows(what, name, t, shape, dtype):
+    """Check a device tensor of `shape` [rows][heads][head_dim] and torch type
+    `dtype` whose heads are contiguous; returns its row stride in elements."""
+    if t.is_cuda and t.dtype is dtype and t.shape == shape:
+        row = shape[1] * shape[2]
+        if t.is_contiguous():
+            return row
+        stride = t.stride()
+        if stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1) and stride[0] >= row:
+            return stride[0]
+        raise ValueError(f"{what}: the heads of {name} must be contiguous and its rows must not overlap")
+    if not t.is_cuda:
         raise ValueError(f"{what}: {name} must be a CUDA tensor")
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or \
-            (rows is not None and shape[0] != rows):
-        raise ValueError(f"{what}: {name} must be [{'rows' if rows is None else rows}][{heads}][{head_dim}] of {dtype}, "
-                         f"got {tuple(shape)} of {t.dtype}")
-    if shape[0] == 0:
-        return heads * head_dim
-    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
-        raise ValueError(f"{what}: the heads of {name} must be contiguous")
-    if shape[0] == 1:
-        return heads * head_dim
-    if stride[0] < heads * head_dim:  # (0 would ask the library for its default)
-        raise ValueError(f"{what}: the rows of {name} overlap")
-    return stride[0]
+    raise ValueError(f"{what}: {name} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
 
 
 def _int32s(what, name, t, count):
-    """Check a contiguous device vector of `count` int32."""
-    if not getattr(t, "is_cuda", False) or t.dtype is not (_torch or _with_torch()).int32 or t.shape != (count,) or \
-            not t.is_contiguous():
-        raise ValueError(f"{what}: {name} must be a contiguous CUDA vector of {count} int32")
+    """Check a contiguous device vector of `count` int32; returns its address."""
+    if t.is_cuda and t.dtype is (_torch or _with_torch()).int32 and t.shape == (count,) and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what}: {name} must be a contiguous CUDA vector of {count} int32")
 
 
 def _stream(stream, t):
@@ -524,30 +519,27 @@ class QKNormRope:
         _check(st, "attn_rope_create")
         self.plan = h
         self.dtype = _torch_dtype(dtype)
+        self.q_shape, self.k_shape, self.w_shape = (q_heads, head_dim), (k_heads, head_dim), (head_dim,)
 
     def run(self, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, stream=None):
         """q_out, k_out: may be q and k themselves.  positions: int32."""
-        d, what = self.desc, "QKNormRope.run"
-        dim, dtype, hq, hk, n = d.head_dim, self.dtype, d.q_heads, d.k_heads, q.shape[0]
-        qs = _rows(what, "q", q, hq, dim, dtype)
-        ks = _rows(what, "k", k, hk, dim, dtype, n)
-        qos = qs if q_out is q else _rows(what, "q_out", q_out, hq, dim, dtype, n)
-        kos = ks if k_out is k else _rows(what, "k_out", k_out, hk, dim, dtype, n)
-        _int32s(what, "positions", positions, n)
-        wq = wk = None
-        if q_weight is not None:
-            wq = self._weight("q_weight", q_weight)
-        if k_weight is not None:
-            wk = self._weight("k_weight", k_weight)
-        st = _lib.attn_rope_run(self.plan, q.data_ptr(), qs, k.data_ptr(), ks, wq, wk, positions.data_ptr(), n,
-                                q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream(stream, q))
+        what, dtype, n = "QKNormRope.run", self.dtype, q.shape[0]
+        q_shape, k_shape = (n, *self.q_shape), (n, *self.k_shape)
+        qs, ks = _rows(what, "q", q, q_shape, dtype), _rows(what, "k", k, k_shape, dtype)
+        qos = qs if q_out is q else _rows(what, "q_out", q_out, q_shape, dtype)
+        kos = ks if k_out is k else _rows(what, "k_out", k_out, k_shape, dtype)
+        st = _lib.attn_rope_run(self.plan, q.data_ptr(), qs, k.data_ptr(), ks,
+                                None if q_weight is None else self._weight("q_weight", q_weight),
+                                None if k_weight is None else self._weight("k_weight", k_weight),
+                                _int32s(what, "positions", positions, n), n, q_out.data_ptr(), qos, k_out.data_ptr(), kos,
+                                _stream(stream, q))
         if st:
             _check(st, "attn_rope_run")
 
     def _weight(self, name, w):
-        if not w.is_cuda or w.dtype is not self.dtype or w.shape != (self.desc.head_dim,) or not w.is_contiguous():
-            raise ValueError(f"QKNormRope.run: {name} must be a contiguous CUDA vector of {self.desc.head_dim} {self.dtype}")
-        return w.data_ptr()
+        if w.is_cuda and w.dtype is self.dtype and w.shape == self.w_shape and w.is_contiguous():
+            return w.data_ptr()
+        raise ValueError(f"QKNormRope.run: {name} must be a contiguous CUDA vector of {self.w_shape[0]} {self.dtype}")
 
     def close(self):
         if self.plan:
@@ -579,21 +571,19 @@ class PromptAttention:
         _check(st, "attn_prompt_create")
         self.plan = h
         self.dtype = _torch_dtype(dtype)
+        self.q_shape, self.k_shape = (q_heads, head_dim), (k_heads, head_dim)
 
     def run(self, q, k, v, cu_q, cu_k, out, stream=None):
-        d, what = self.desc, "PromptAttention.run"
-        dim, dtype, hq, hk = d.head_dim, self.dtype, d.q_heads, d.k_heads
+        what, dtype = "PromptAttention.run", self.dtype
         nq, nk, cus = q.shape[0], k.shape[0], cu_q.shape[0]
-        sq = _rows(what, "q", q, hq, dim, dtype)
-        so = _rows(what, "out", out, hq, dim, dtype, nq)
-        sk = _rows(what, "k", k, hk, dim, dtype)
-        sv = _rows(what, "v", v, hk, dim, dtype, nk)
-        _int32s(what, "cu_q", cu_q, cus)
-        _int32s(what, "cu_k", cu_k, cus)
         if cus < 1:
             raise ValueError(f"{what}: cu_q and cu_k hold batch + 1 values")
-        st = _lib.attn_prompt_run(self.plan, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, cu_q.data_ptr(),
-                                  cu_k.data_ptr(), cus - 1, nq, nk, out.data_ptr(), so, _stream(stream, q))
+        q_shape, k_shape = (nq, *self.q_shape), (nk, *self.k_shape)
+        st = _lib.attn_prompt_run(self.plan, q.data_ptr(), _rows(what, "q", q, q_shape, dtype),
+                                  k.data_ptr(), _rows(what, "k", k, k_shape, dtype),
+                                  v.data_ptr(), _rows(what, "v", v, k_shape, dtype), _int32s(what, "cu_q", cu_q, cus),
+                                  _int32s(what, "cu_k", cu_k, cus), cus - 1, nq, nk,
+                                  out.data_ptr(), _rows(what, "out", out, q_shape, dtype), _stream(stream, q))
         if st:
             _check(st, "attn_prompt_run")
 
@@ -627,6 +617,7 @@ class KVCache:
             raise ValueError("KVCache: codes are [pages][k_heads][page_size][head_dim], exponents one dimension less")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.pages, self.k_heads, self.page_size, self.head_dim = k.shape
+        self.row_shape, self.page_shape = (self.k_heads, self.head_dim), tuple(k.shape[1:])
         self.c = attn_cache_t(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), self.pages,
                               self.page_size, self.k_heads, self.head_dim)
         self._ref = ctypes.byref(self.c)
@@ -639,28 +630,27 @@ class KVCache:
         return cls(*made)
 
     def _rows(self, what, k, v, slots):
-        """Check keys, values and slots; returns their count, row strides and type."""
+        """Check keys, values and slots; returns their count, row strides, the slots' address and the type."""
         torch = _torch or _with_torch()
         dtype, n = k.dtype, k.shape[0]
         if dtype is not torch.bfloat16 and dtype is not torch.float16:
             raise ValueError(f"{what}: k and v must be float16 or bfloat16, got {dtype}")
-        sk = _rows(what, "k", k, self.k_heads, self.head_dim, dtype)
-        sv = _rows(what, "v", v, self.k_heads, self.head_dim, dtype, n)
-        _int32s(what, "slots", slots, n)
-        return n, sk, sv, GEMM_BF16 if dtype is torch.bfloat16 else GEMM_F16
+        shape = (n, *self.row_shape)
+        return (n, _rows(what, "k", k, shape, dtype), _rows(what, "v", v, shape, dtype),
+                _int32s(what, "slots", slots, n), GEMM_BF16 if dtype is torch.bfloat16 else GEMM_F16)
 
     def write(self, k, v, slots, stream=None):
         """Quantise [token][k_heads][head_dim] keys and values into their slots (int32; negative: left out)."""
-        n, sk, sv, dtype = self._rows("KVCache.write", k, v, slots)
-        st = _lib.attn_cache_write(self._ref, k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(), n, dtype,
+        n, sk, sv, at, dtype = self._rows("KVCache.write", k, v, slots)
+        st = _lib.attn_cache_write(self._ref, k.data_ptr(), sk, v.data_ptr(), sv, at, n, dtype,
                                    _stream(stream, k))
         if st:
             _check(st, "attn_cache_write")
 
     def read(self, slots, k, v, stream=None):
         """The values of the slots into [token][k_heads][head_dim] tensors (zeros for a negative slot)."""
-        n, sk, sv, dtype = self._rows("KVCache.read", k, v, slots)
-        st = _lib.attn_cache_read(self._ref, slots.data_ptr(), n, k.data_ptr(), sk, v.data_ptr(), sv, dtype,
+        n, sk, sv, at, dtype = self._rows("KVCache.read", k, v, slots)
+        st = _lib.attn_cache_read(self._ref, at, n, k.data_ptr(), sk, v.data_ptr(), sv, dtype,
                                   _stream(stream, k))
         if st:
             _check(st, "attn_cache_read")
@@ -674,7 +664,7 @@ class CacheAttention:
     def __init__(self, q_heads, k_heads, head_dim, page_size, dtype=GEMM_BF16, scale=0.0, batch=64):
         self.q_heads, self.k_heads, self.head_dim, self.page_size = q_heads, k_heads, head_dim, page_size
         self.dtype, self.scale, self.code = _torch_dtype(dtype), scale, dtype
-        self.shape = (k_heads, page_size, head_dim)
+        self.q_shape, self.page_shape = (q_heads, head_dim), (k_heads, page_size, head_dim)
         self.workspace, self.ws_bytes, self.batch = None, 0, 0
         self._grow(batch)
 
@@ -691,12 +681,12 @@ class CacheAttention:
 
     def run(self, q, cache, page_table, lengths, out, stream=None):
         """q, out: [batch][q_heads][head_dim]; page_table: [batch][pages a sequence] int32; lengths: batch int32."""
-        what, n, dim, hq = "CacheAttention.run", q.shape[0], self.head_dim, self.q_heads
-        if cache.k.shape[1:] != self.shape:
+        what, n = "CacheAttention.run", q.shape[0]
+        if cache.page_shape != self.page_shape:
             raise ValueError(f"{what}: the cache has another shape than this was made for")
-        sq = _rows(what, "q", q, hq, dim, self.dtype)
-        so = _rows(what, "out", out, hq, dim, self.dtype, n)
-        _int32s(what, "lengths", lengths, n)
+        q_shape = (n, *self.q_shape)
+        sq, so = _rows(what, "q", q, q_shape, self.dtype), _rows(what, "out", out, q_shape, self.dtype)
+        lens = _int32s(what, "lengths", lengths, n)
         shape, pitch = page_table.shape, page_table.stride()
         if not page_table.is_cuda or page_table.dtype is not _torch.int32 or len(shape) != 2 or shape[0] != n or \
                 (shape[1] > 1 and pitch[1] != 1):
@@ -707,8 +697,8 @@ class CacheAttention:
         pitch = pitch[0] if n > 1 else most
         if pitch < most:
             raise ValueError(f"{what}: the rows of page_table overlap")
-        st = _lib.attn_cache_attend(cache._ref, q.data_ptr(), sq, hq, page_table.data_ptr(), pitch, most,
-                                    lengths.data_ptr(), n, self.scale, self.code, out.data_ptr(), so,
+        st = _lib.attn_cache_attend(cache._ref, q.data_ptr(), sq, self.q_heads, page_table.data_ptr(), pitch, most,
+                                    lens, n, self.scale, self.code, out.data_ptr(), so,
                                     self.workspace.data_ptr(), self.ws_bytes, _stream(stream, q))
         if st:
             _check(st, "attn_cache_attend")

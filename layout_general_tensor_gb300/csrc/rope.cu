@@ -32,9 +32,10 @@
 namespace lgt {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxPairs = 128;  // head_dim 256
-constexpr uint32_t kRopeBlocks = 8;  // blocks an SM the chunks are cut for
+constexpr uint32_t kRopeBlocks = 6;  // blocks an SM the chunks are cut for: what its registers hold (R = 8)
+constexpr int kRopeDepth = 2;        // heads of a group on their way
 
 struct RopeArgs {
   const uint16_t *q, *k, *wq, *wk;
@@ -103,66 +104,56 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const bool turned = 2 * R * u < a.rot;
   const bool norms = a.wq != nullptr || a.wk != nullptr;
   const int o0 = HALF && turned ? R * u : 2 * R * u, o1 = HALF && turned ? a.rot / 2 + R * u : 2 * R * u + R;
-  uint32_t turns_lo[R], turns_hi[R];
-#pragma unroll
-  for (int e = 0; e < R; ++e) {
-    const uint64_t f = turned ? a.turns[R * u + e] : 0u;
-    turns_lo[e] = static_cast<uint32_t>(f);
-    turns_hi[e] = static_cast<uint32_t>(f >> 32);
-  }
   uint32_t t, h;  // of the head that is loaded next
   magic_divmod(min(first, a.items - 1u), a.div_heads, t, h);
   auto is_query = [&](uint32_t hh) { return hh < static_cast<uint32_t>(a.hq); };
   pdl_wait();
 
-  Run<R> x0[2], x1[2];
-  uint32_t lt[2], lh[2];
-  auto load = [&](uint32_t item) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      lt[j] = t;
-      lh[j] = h;
-#pragma unroll
-      for (int i = 0; i < R / 2; ++i) x0[j].w[i] = x1[j].w[i] = 0u;
-      if (item + j < end) {
-        if (mine) {
-          const uint16_t* src = is_query(h) ? a.q + static_cast<int64_t>(t) * a.qs + h * a.d
-                                            : a.k + static_cast<int64_t>(t) * a.ks + (h - a.hq) * a.d;
-          x0[j] = load_run<R>(src + o0);
-          x1[j] = load_run<R>(src + o1);
-        }
-        if (++h == static_cast<uint32_t>(a.heads)) {
-          h = 0;
-          ++t;
-        }
+  // two heads on their way; the place of one is loaded again as soon as it is taken
+  Run<R> x0[kRopeDepth], x1[kRopeDepth];
+  uint32_t lt[kRopeDepth], lh[kRopeDepth];
+  auto load = [&](int j, uint32_t item) {
+    lt[j] = t;
+    lh[j] = h;
+    if (item < end) {
+      if (mine) {
+        const uint16_t* src = is_query(h) ? a.q + static_cast<int64_t>(t) * a.qs + h * a.d
+                                          : a.k + static_cast<int64_t>(t) * a.ks + (h - a.hq) * a.d;
+        x0[j] = load_run<R>(src + o0);
+        x1[j] = load_run<R>(src + o1);
+      }
+      if (++h == static_cast<uint32_t>(a.heads)) {
+        h = 0;
+        ++t;
       }
     }
   };
-  load(first);
+#pragma unroll
+  for (int j = 0; j < kRopeDepth; ++j) {
+#pragma unroll
+    for (int i = 0; i < R / 2; ++i) x0[j].w[i] = x1[j].w[i] = 0u;
+    load(j, first + j);
+  }
 
-  float cs[R], sn[R], w[2 * R];
+  float cs[R], sn[R];
+  Run<R> w0, w1;
   uint32_t have_t = 0xffffffffu;
   int have_w = -1;
   // (every lane of a warp goes round as often: the butterflies are of all)
-  for (uint32_t step = 0; step < a.chunk; step += 2) {
-    float y[2][2 * R];
-    uint32_t ct[2], ch[2];
+  for (uint32_t step = 0; step < a.chunk; step += kRopeDepth) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      ct[j] = lt[j];
-      ch[j] = lh[j];
-      widen_run<R, BF16>(x0[j], y[j]);
-      widen_run<R, BF16>(x1[j], y[j] + R);
-    }
-    const uint32_t item = first + step;
-    load(item + 2);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const bool is_q = is_query(ch[j]);
+    for (int j = 0; j < kRopeDepth; ++j) {
+      const uint32_t item = first + step + j;
+      const uint32_t ct = lt[j], ch = lh[j];
+      const bool is_q = is_query(ch);
+      float y[2 * R];
+      widen_run<R, BF16>(x0[j], y);
+      widen_run<R, BF16>(x1[j], y + R);
+      load(j, item + kRopeDepth);
       if (norms) {
         float ss[2] = {};
 #pragma unroll
-        for (int e = 0; e < 2 * R; ++e) ss[e & 1] = fmaf(y[j][e], y[j][e], ss[e & 1]);
+        for (int e = 0; e < 2 * R; ++e) ss[e & 1] = fmaf(y[e], y[e], ss[e & 1]);
         ss[0] += ss[1];
 #pragma unroll
         for (int o = LG / 2; o > 0; o >>= 1) ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], o);
@@ -172,26 +163,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           if (have_w != static_cast<int>(is_q)) {
             have_w = is_q;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              Run<R> v;
-#pragma unroll
-              for (int i = 0; i < R / 2; ++i) v.w[i] = __ldg(reinterpret_cast<const uint32_t*>(wt + (e ? o1 : o0)) + i);
-              widen_run<R, BF16>(v, w + e * R);
+            for (int i = 0; i < R / 2; ++i) {
+              w0.w[i] = __ldg(reinterpret_cast<const uint32_t*>(wt + o0) + i);
+              w1.w[i] = __ldg(reinterpret_cast<const uint32_t*>(wt + o1) + i);
             }
           }
+          float w[2 * R];
+          widen_run<R, BF16>(w0, w);
+          widen_run<R, BF16>(w1, w + R);
 #pragma unroll
-          for (int e = 0; e < 2 * R; ++e) y[j][e] = y[j][e] * r * w[e];
+          for (int e = 0; e < 2 * R; ++e) y[e] = y[e] * r * w[e];
         }
       }
       if (turned) {
-        if (ct[j] != have_t && item + j < end) {
-          have_t = ct[j];
-          const int32_t p = __ldg(a.pos + ct[j]);
+        if (ct != have_t && item < end) {
+          have_t = ct;
+          const int32_t p = __ldg(a.pos + ct);
 #pragma unroll
           for (int e = 0; e < R; ++e) {
             // bits 32 .. 63 of position * turns
-            const uint32_t phase = __umulhi(static_cast<uint32_t>(p), turns_lo[e]) + static_cast<uint32_t>(p) * turns_hi[e] -
-                                   (p < 0 ? turns_lo[e] : 0u);
+            const uint64_t f = a.turns[R * u + e];
+            const uint32_t lo = static_cast<uint32_t>(f), hi = static_cast<uint32_t>(f >> 32);
+            const uint32_t phase = __umulhi(static_cast<uint32_t>(p), lo) + static_cast<uint32_t>(p) * hi - (p < 0 ? lo : 0u);
             const float ang = static_cast<float>(static_cast<int32_t>(phase)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
             sn[e] = __sinf(ang) * a.magnitude;
             cs[e] = __cosf(ang) * a.magnitude;
@@ -199,18 +192,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
 #pragma unroll
         for (int e = 0; e < R; ++e) {
-          float& lo = HALF ? y[j][e] : y[j][2 * e];
-          float& hi = HALF ? y[j][R + e] : y[j][2 * e + 1];
+          float& lo = HALF ? y[e] : y[2 * e];
+          float& hi = HALF ? y[R + e] : y[2 * e + 1];
           const float c = lo * cs[e] - hi * sn[e], s = hi * cs[e] + lo * sn[e];
           lo = c;
           hi = s;
         }
       }
-      if (item + j < end && mine) {
-        uint16_t* dst = is_q ? a.qo + static_cast<int64_t>(ct[j]) * a.qos + ch[j] * a.d
-                             : a.ko + static_cast<int64_t>(ct[j]) * a.kos + (ch[j] - a.hq) * a.d;
-        store_run<R>(dst + o0, narrow_run<R, BF16>(y[j]));
-        store_run<R>(dst + o1, narrow_run<R, BF16>(y[j] + R));
+      if (item < end && mine) {
+        uint16_t* dst = is_q ? a.qo + static_cast<int64_t>(ct) * a.qos + ch * a.d
+                             : a.ko + static_cast<int64_t>(ct) * a.kos + (ch - a.hq) * a.d;
+        store_run<R>(dst + o0, narrow_run<R, BF16>(y));
+        store_run<R>(dst + o1, narrow_run<R, BF16>(y + R));
       }
     }
   }
@@ -222,7 +215,7 @@ cudaError_t launch_rope(RopeArgs& a, int sms, cudaStream_t stream) {
   // Chunks that give every SM kRopeBlocks blocks, whole pairs of heads; one
   // head a group where there are fewer than that.
   const uint32_t most = static_cast<uint32_t>(sms) * kRopeBlocks * groups;
-  a.chunk = a.items <= most ? 1u : ((a.items + most - 1u) / most + 1u) & ~1u;
+  a.chunk = (a.items + most - 1u) / most;
   const uint32_t per_block = groups * a.chunk, blocks = a.items / per_block + (a.items % per_block ? 1u : 0u);
   return launch_pdl(rope_kernel<R, LG, BF16, HALF>, dim3(blocks), dim3(kRopeThreads), 0, stream, a);
 }
