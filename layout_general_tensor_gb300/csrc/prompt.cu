@@ -286,10 +286,11 @@ __device__ __forceinline__ PromptSeq seq_at(const PromptArgs& a, int b) {
 // 32 / 8 heads of 128: one prompt of 512 tokens 10.7 us so cut, 12.0 not; one
 // of 64 after 8192 keys 35 and 58; four of 256, which it leaves alone, 13.0
 // and 9.8.)  The whole warp returns the same.
-__device__ __forceinline__ int narrow_above(const PromptArgs& a) {
+// (mine: this lane's of the first 32 sequences, here and below.)
+__device__ __forceinline__ int narrow_above(const PromptArgs& a, const PromptSeq& mine) {
   float sum = 0.0f;
   for (int b = threadIdx.x & 31; b < a.batch; b += 32) {
-    const PromptSeq s = seq_at(a, b);
+    const PromptSeq s = b < 32 ? mine : seq_at(a, b);
     const float walk = static_cast<float>(s.nk) - (a.causal ? 0.5f * static_cast<float>(s.nq) : 0.0f);
     sum += static_cast<float>(magic_div(static_cast<uint32_t>(s.nq + 2 * a.tok) - 1u, a.div_pair)) *
            (fmaxf(walk, 0.0f) * (1.0f / kPrKeys) + 0.5f);
@@ -301,12 +302,12 @@ __device__ __forceinline__ int narrow_above(const PromptArgs& a) {
 
 // Unit `u` of the list (sequences in order, each one's last tokens -- the
 // most keys -- first); every lane of the warp returns the same.
-__device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u, int narrow) {
+__device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u, int narrow, const PromptSeq& mine) {
   const int lane = threadIdx.x & 31;
   PromptUnit r{};
   uint32_t before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const PromptSeq q = seq_at(a, b0 + lane);
+    const PromptSeq q = b0 == 0 ? mine : seq_at(a, b0 + lane);
     const bool cut = (q.nk + kPrKeys - 1) / kPrKeys > narrow;
     const int my_span = cut ? a.tok : 2 * a.tok;
     const uint32_t n = magic_div(static_cast<uint32_t>(q.nq + my_span) - 1u, cut ? a.div_tok : a.div_pair);
@@ -721,40 +722,46 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     // -------------------------------------------------------------- units
     int64_t block = blockIdx.x;
     int turn = 0;  // of the next unit's first block at the ring's places
-    const int narrow = FEW ? narrow_above(a) : 0x7fffffff;
+    const PromptSeq mine = seq_at(a, lane);
+    const int narrow = FEW ? narrow_above(a, mine) : 0x7fffffff;
     bool ok = true;
-    for (int it = 0; ok; ++it) {
-      if (it >= 2 && !(ok = warp_wait(unit_empty(it & 1), ((it >> 1) - 1) & 1, limit, abort_flag))) break;
-      PromptUnit w{};
-      w.tokens = -1;
-      // (blocks past the last unit hold nothing)
-      while (block >= 0) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(taken, 16);
-          take_block(base + C::TAKEN_OFF, taken);
-        }
-        __syncwarp();
-        uint32_t unit, h;
-        magic_divmod(static_cast<uint32_t>(block), a.div_hk, unit, h);
-        w = find_unit(a, unit, narrow);
-        w.h = static_cast<int>(h);
-        shape_unit<FEW>(a, w, turn);
-        ++asked;
-        if (!(ok = warp_wait(taken, (asked - 1) & 1, limit, abort_flag))) break;
-        block = taken_block(base + C::TAKEN_OFF);
-        fence_proxy_async_smem();  // (read before the next answer is written)
-        __syncwarp();
-        if (w.tokens > 0) break;
-        w.tokens = -1;
-      }
-      if (!ok) break;
-      if (w.tokens > 0) turn ^= w.nb & 1;
+    int it = 0;
+    auto publish = [&](const PromptUnit& w) {
+      if (it >= 2 && !(ok = warp_wait(unit_empty(it & 1), ((it >> 1) - 1) & 1, limit, abort_flag))) return;
       if (lane == 0) {
         units[it & 1] = w;
         mbar_arrive(unit_full(it & 1));
       }
       __syncwarp();
-      if (w.tokens < 0) break;
+      ++it;
+    };
+    while (ok && block >= 0) {
+      uint32_t unit, h;
+      magic_divmod(static_cast<uint32_t>(block), a.div_hk, unit, h);
+      PromptUnit w = find_unit(a, unit, narrow, mine);
+      if (w.tokens > 0) {  // (blocks past the last unit hold nothing)
+        w.h = static_cast<int>(h);
+        shape_unit<FEW>(a, w, turn);
+        turn ^= w.nb & 1;
+        publish(w);
+        if (!ok) break;
+      }
+      // the next one (a CTA is at most one ahead of itself: the second of two
+      // places is free when the unit before the last is done)
+      if (lane == 0) {
+        mbar_arrive_expect_tx(taken, 16);
+        take_block(base + C::TAKEN_OFF, taken);
+      }
+      ++asked;
+      if (!(ok = warp_wait(taken, (asked - 1) & 1, limit, abort_flag))) break;
+      block = taken_block(base + C::TAKEN_OFF);
+      fence_proxy_async_smem();  // (read before the next answer is written)
+      __syncwarp();
+    }
+    if (ok) {
+      PromptUnit w{};
+      w.tokens = -1;
+      publish(w);
     }
     if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 4);
   } else {
@@ -783,15 +790,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       for (int j = 0; j < my_blocks; ++j, ++s_uses) {
         if (!(ok = warp_wait(s_full(t), s_uses & 1, limit, abort_flag))) break;
         tc_fence_after();
-        // The first half of P against the reference as it stands, while the
-        // block's maximum is found; in the rare block that exceeds the
-        // reference by 2^kPrLazy in some row (and the first), the reference
-        // moves and the half is made again.
+        // The first half of P against the reference as it stands (the first
+        // block's maximum), while the block's maximum is found; in the rare
+        // block that exceeds the reference by 2^kPrLazy in some row, the
+        // reference moves and the half is made again.
         const int valid = vis - key0 - j * key_step;
         const bool masked = __any_sync(0xffffffffu, valid < kPrKeys);
         const float2 cs2 = make_float2(a.cs, a.cs);
         float2 sum[4];
         uint32_t sv[128], pk[32];
+        bool known = j > 0;  // whether there is a reference to go by
         while (true) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -801,6 +809,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if (i >= valid) sv[i] = __float_as_uint(-INFINITY);
+          }
+          if (!known) {
+            known = true;
+            float mp[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mp[u] = __uint_as_float(sv[u]);
+#pragma unroll
+            for (int i = 4; i < 128; i += 4)
+              mp[(i >> 2) & 3] = max3(mp[(i >> 2) & 3], fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])),
+                                      fmaxf(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])));
+            m = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * a.cs;
+            if (!(m > -INFINITY)) m = -INFINITY;  // (nothing but NaN)
           }
           // (a row that has seen no key keeps weights of 2^-inf = 0)
           const float ref = m == -INFINITY ? 0.0f : m;
