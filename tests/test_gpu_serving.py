@@ -504,3 +504,69 @@ def test_one_layer_prompt_then_tokens(m):
     # both take the cache's values: they differ by the weights' and the results' rounding
     diff = (whole[n].float() - token[0].float()).abs()
     assert float(diff.max()) <= 4 * 2.0 ** -8 * float(cv.float().abs().max())
+
+
+def test_cache_offsets_past_32_bits(m):
+    """Pages whose codes lie past 2^32 bytes: written, read back and attended to there."""
+    hq, hk, d, page, n = 8, 8, 128, 64, 200
+    pages = (1 << 32) // (hk * page * d) + 8
+    cache = m.KVCache.empty(pages, page, hk, d)
+    table = torch.tensor([[pages - 1, 3, pages - 7, pages - 2]], dtype=torch.int32, device="cuda")
+    at = torch.arange(n, device="cuda")
+    slots = table[0, at // page] * page + (at % page).int()
+    k, v = _rand(100, n, hk, d, dtype=F16).cuda(), _rand(101, n, hk, d, dtype=F16).cuda()
+    cache.write(k, v, slots)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    cache.read(slots, ko, vo)
+    for x, got in ((k, ko), (v, vo)):
+        assert np.array_equal(_val(got), oracle.cache_decode(*oracle.cache_encode(_val(x))))
+    q, out = _rand(102, 1, hq, d, dtype=F16).cuda(), torch.empty(1, hq, d, dtype=torch.float16, device="cuda")
+    m.CacheAttention(hq, hk, d, page, dtype=m.GEMM_F16).run(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), out)
+    want, mag = oracle.prompt_attention(_val(q), _val(ko), _val(vo), [0, 1], [0, n], False)
+    tol = _attention_tol(F16, 2.0 ** -11, want, mag, (d + 5) * 2.0 ** -24 * 60, n, 8.0)
+    assert np.all(np.abs(_val(out) - want) <= tol)
+
+
+def test_rope_offsets_past_32_bits(m):
+    """Rows 2^25 values apart: the last ones start past 2^31 values."""
+    t, d, stride = 66, 64, 1 << 25
+    big = torch.empty((t - 1) * stride + 2 * d, dtype=torch.float16, device="cuda")
+    x = big.as_strided((t, 2, d), (stride, d, 1))
+    q = _rand(103, t, 2, d, dtype=F16)
+    x.copy_(q)
+    k = torch.zeros(t, 1, d, dtype=torch.float16, device="cuda")
+    pos = torch.arange(t, dtype=torch.int32) * 1000
+    m.QKNormRope(2, 1, d, dtype=m.GEMM_F16).run(x, k, pos.cuda(), x, k)
+    _check_rope(x, q, pos.numpy(), oracle.rope_frequencies(d, 10000.0), True, None, 0.0, 1.0, F16, "far rows")
+
+
+def test_example_layer_serves_what_a_longer_prompt_gives(m):
+    """The example's tokens over the cache against the same tokens as the last of longer prompts (whose keys and
+    values are not rounded to 8 bits).  The outputs have rms of about 1 / sqrt(visible keys); e4m3 holds a value to
+    2^-4, so an output to about a tenth of its rms, a quarter with room for the logits' share."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serving_layer.py")
+    spec = importlib.util.spec_from_file_location("serving_layer", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    prompts, hidden = (40, 3, 130), 256
+    outs = ex.serve(prompts, new_tokens=1, hidden=hidden, q_heads=4, k_heads=2, head_dim=64, page_size=16)
+    assert [tuple(o.shape) for o in outs] == [(173, hidden), (3, hidden)] and all(torch.isfinite(o).all() for o in outs)
+    # the same layer and inputs, the new token appended to each prompt
+    layer = ex.AttentionLayer(hidden, 4, 2, 64, 64, 16, 3)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    torch.randperm(3 * 9, generator=g, device="cuda")
+    x = torch.randn(sum(prompts), hidden, generator=g, device="cuda").bfloat16()
+    new = torch.randn(3, hidden, generator=g, device="cuda").bfloat16()
+    cu = np.cumsum([0, *prompts])
+    longer = torch.cat([torch.cat([x[a:b], new[i:i + 1]]) for i, (a, b) in enumerate(zip(cu[:-1], cu[1:]))])
+    position = torch.cat([torch.arange(p + 1) for p in prompts]).int().cuda()
+    cu1 = torch.from_numpy((cu + np.arange(4)).astype(np.int32)).cuda()
+    whole = layer.prompt(longer, position, torch.arange(176, dtype=torch.int32, device="cuda"), cu1)
+    last = whole[(cu1[1:] - 1).long()].float()
+    token = outs[1].float()
+    assert float((token - last).norm() / last.norm()) < 0.25
+    # and the prompts' own outputs do not depend on what follows them
+    keep = torch.cat([torch.arange(p + 1) < p for p in prompts]).cuda()
+    assert float((whole[keep].float() - outs[0].float()).norm() / outs[0].float().norm()) < 2.0 ** -7
