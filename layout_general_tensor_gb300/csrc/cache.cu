@@ -3,9 +3,9 @@
 //
 // One group of head_dim / 8 lanes per token and key head, eight values of K
 // and eight of V a lane (16 bytes each of the 16-bit tensors, 8 of the
-// codes).  The row's largest finite magnitude goes around the group as a bit
-// pattern (for magnitudes the order of the bits is the order of the values),
-// and the power of two comes out of its exponent and significand without a
+// codes).  The rows' largest finite magnitudes go around the group as bit
+// patterns, K's and V's in one word (for magnitudes the order of the bits is
+// the order of the values), and the power of two comes out of its exponent and significand without a
 // logarithm: with amax = m * 2^e, 1 <= m < 2, and 448 = 1.75 * 2^8,
 // ceil(log2(amax / 448)) is e - 8, and one more when m > 1.75.
 //
@@ -44,36 +44,49 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   }
 }
 
-// The bits of the largest finite magnitude.
-__device__ __forceinline__ uint32_t amax_bits(const float (&x)[8]) {
-  uint32_t m = 0;
+// The largest finite magnitude of eight 16-bit values, as the bits of its type:
+// two at a time as integers, and one by one only where that finds one that is
+// not finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t amax16(const uint4& w) {
+  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+  const uint32_t r[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
+  const uint32_t m = __vmaxu2(__vmaxu2(r[0], r[1]), __vmaxu2(r[2], r[3]));
+  uint32_t most = max(m & 0xffffu, m >> 16);
+  if (most >= kInf) {
+    most = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
-    m = max(m, b < 0x7f800000u ? b : 0u);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = r[i] & 0xffffu, hi = r[i] >> 16;
+      most = max(most, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
+    }
   }
-  return m;
+  return most;
 }
 
 // power + 127 of a row with this largest magnitude.  (A bf16 subnormal's
 // exponent field is 0, and so is the clamp's outcome for it.)
-__device__ __forceinline__ int row_exponent(uint32_t amax) {
+template <bool BF16>
+__device__ __forceinline__ int row_exponent(uint32_t amax16) {
+  const uint32_t amax = BF16 ? amax16 << 16 : __float_as_uint(unpack_pair16<false>(amax16).x);
   if (amax == 0) return 127;
   const int e = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
   return max(e, 1);
 }
 
-// Eight values times 2^(127 - exponent) as e4m3 codes.  The factor is applied
-// as two powers of two, since one alone could leave fp32's range.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], int exponent) {
-  const int p = 127 - exponent, p0 = p / 2, p1 = p - p0;
-  const float f0 = __uint_as_float(static_cast<uint32_t>(127 + p0) << 23);
-  const float f1 = __uint_as_float(static_cast<uint32_t>(127 + p1) << 23);
+// Eight values times 2^(127 - exponent) as e4m3 codes.  (The power is in
+// [-120, 126], and what the product loses below fp32's range is far below half
+// of the least code.)
+template <bool BF16>
+__device__ __forceinline__ uint2 encode8(const uint4& w, int exponent) {
+  const float f = __uint_as_float(static_cast<uint32_t>(254 - exponent) << 23);
+  float x[8];
+  unpack8<BF16>(w, x);
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x[2 * i + 1] * f0 * f1), "f"(x[2 * i] * f0 * f1));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x[2 * i + 1] * f), "f"(x[2 * i] * f));
     r[i] = c;
   }
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
@@ -118,19 +131,16 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
     vw = ld_stream_v4(a.vx + static_cast<int64_t>(t) * a.vs + h * D + u * 8);
     slot = a.slots[t];
   }
-  float k[8], v[8];
-  unpack8<BF16>(kw, k);
-  unpack8<BF16>(vw, v);
-  uint32_t km = amax_bits(k), vm = amax_bits(v);
+  uint32_t both = amax16<BF16>(kw) | (amax16<BF16>(vw) << 16);
 #pragma unroll
   for (int o = LG / 2; o > 0; o >>= 1) {
-    km = max(km, __shfl_xor_sync(0xffffffffu, km, o));
-    vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+    both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
   }
+  const uint32_t km = both & 0xffffu, vm = both >> 16;
   if (slot < 0 || slot >= a.num_slots) return;
   const int64_t row = cache_row(a, slot, h);
-  const int ke = row_exponent(km), ve = row_exponent(vm);
-  const uint2 kc = encode8(k, ke), vc = encode8(v, ve);
+  const int ke = row_exponent<BF16>(km), ve = row_exponent<BF16>(vm);
+  const uint2 kc = encode8<BF16>(kw, ke), vc = encode8<BF16>(vw, ve);
   st_global_v2(a.k + row * D + u * 8, kc.x, kc.y);
   st_global_v2(a.v + row * D + u * 8, vc.x, vc.y);
   if (u == 0) {
