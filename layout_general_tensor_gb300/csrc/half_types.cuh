@@ -1,5 +1,5 @@
-// 16-bit element helpers shared by the attention-layer kernels: pairs of
-// fp16 / bf16 values in one 32-bit word, to and from fp32.
+// Helpers shared by the attention-layer kernels: pairs of fp16 / bf16 values in
+// one 32-bit word, to and from fp32; packed fp32 arithmetic; streaming loads.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -44,6 +44,26 @@ __device__ __forceinline__ uint32_t pack_pair16_sat(float lo, float hi) {
   return w;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t x, y, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
 // Streaming loads: every byte is read once, so nothing is kept in L1.
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
   uint4 v;
