@@ -15,6 +15,7 @@ import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libgemm.so")
+_BINDING_PATH = os.path.join(_HERE, "_lib", "_binding.so")
 
 GEMM_OK = 0
 GEMM_ERR_INVALID_ARG = 1
@@ -432,19 +433,29 @@ class Attention:
 
 
 _torch = None
-_raw_stream = None
+_binding = None
 
 
 def _with_torch():
-    """The torch module and its function for a device's current stream
-    (imported at the first use: the rest of the binding does without)."""
-    global _torch, _raw_stream
+    """torch and the binding's part in C (csrc/binding.c), which goes by
+    torch's types; both at the first use, the rest does without."""
+    global _torch, _binding
+    import importlib.machinery
+    import importlib.util
+
     import torch
-    # (the plain way to the current stream costs 3.5 us a call on the host, a
-    # third of a small operator's whole call)
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    if not os.path.exists(_BINDING_PATH):
+        raise ImportError(f"{_BINDING_PATH} is missing: build it with `python layout_general_tensor_gb300/build.py`")
+    loader = importlib.machinery.ExtensionFileLoader("_binding", _BINDING_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+    loader.exec_module(module)
+    # (the plain way to the current stream costs 3.5 us a call on the host)
+    raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
-    _torch = torch
+    module.setup(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
+                   ("attn_rope_run", "attn_prompt_run", "attn_cache_write", "attn_cache_read", "attn_cache_attend")),
+                 raw_stream, torch.int32, torch.float16, torch.bfloat16)
+    _torch, _binding = torch, module
     return torch
 
 
@@ -453,36 +464,20 @@ def _torch_dtype(dtype):
     return torch.bfloat16 if dtype == GEMM_BF16 else torch.float16
 
 
-def _rows(what, name, t, shape, dtype):
-    """Check a device tensor of `shape` [rows][heads][head_dim] and torch type
-    `dtype` whose heads are contiguous; returns its row stride in elements."""
-    if t.is_cuda and t.dtype is dtype and t.shape == shape:
-        row = shape[1] * shape[2]
-        if t.is_contiguous():
-            return row
-        stride = t.stride()
-        if stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1) and stride[0] >= row:
-            return stride[0]
-        raise ValueError(f"{what}: the heads of {name} must be contiguous and its rows must not overlap")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: {name} must be a CUDA tensor")
-    raise ValueError(f"{what}: {name} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
-
-
-def _int32s(what, name, t, count):
-    """Check a contiguous device vector of `count` int32; returns its address."""
-    if t.is_cuda and t.dtype is (_torch or _with_torch()).int32 and t.shape == (count,) and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{what}: {name} must be a contiguous CUDA vector of {count} int32")
-
-
-def _stream(stream, t):
-    """`stream`, or the current one of the device of tensor `t`."""
-    if stream is not None:
-        return stream
-    if _raw_stream is None:
-        _with_torch()
-    return _raw_stream(t.get_device())
+def _refuse(what, status, *checks):
+    """Raise for a call's status; at -1 the binding refused a tensor: find it
+    among checks of (name, tensor, shape, torch type, whether its rows may be
+    strided)."""
+    if status != -1:
+        _check(status, what)
+    for name, t, shape, dtype, rows in checks:
+        if not getattr(t, "is_cuda", False):
+            raise ValueError(f"{what}: {name} must be a CUDA tensor")
+        if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: {name} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
+        if not rows and not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+    raise ValueError(f"{what}: within a row the values of a tensor must be contiguous, and rows must not overlap")
 
 
 def attn_rope_frequencies(desc: attn_rope_desc_t):
@@ -519,32 +514,23 @@ class QKNormRope:
         _check(st, "attn_rope_create")
         self.plan = h
         self.dtype = _torch_dtype(dtype)
-        self.q_shape, self.k_shape, self.w_shape = (q_heads, head_dim), (k_heads, head_dim), (head_dim,)
+        self.handle = (h, self.dtype, q_heads, k_heads, head_dim)
 
     def run(self, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, stream=None):
         """q_out, k_out: may be q and k themselves.  positions: int32."""
-        what, dtype, n = "QKNormRope.run", self.dtype, q.shape[0]
-        q_shape, k_shape = (n, *self.q_shape), (n, *self.k_shape)
-        qs, ks = _rows(what, "q", q, q_shape, dtype), _rows(what, "k", k, k_shape, dtype)
-        qos = qs if q_out is q else _rows(what, "q_out", q_out, q_shape, dtype)
-        kos = ks if k_out is k else _rows(what, "k_out", k_out, k_shape, dtype)
-        st = _lib.attn_rope_run(self.plan, q.data_ptr(), qs, k.data_ptr(), ks,
-                                None if q_weight is None else self._weight("q_weight", q_weight),
-                                None if k_weight is None else self._weight("k_weight", k_weight),
-                                _int32s(what, "positions", positions, n), n, q_out.data_ptr(), qos, k_out.data_ptr(), kos,
-                                _stream(stream, q))
+        st = _binding.rope(self.handle, q, k, positions, q_out, k_out, q_weight, k_weight, stream)
         if st:
-            _check(st, "attn_rope_run")
-
-    def _weight(self, name, w):
-        if w.is_cuda and w.dtype is self.dtype and w.shape == self.w_shape and w.is_contiguous():
-            return w.data_ptr()
-        raise ValueError(f"QKNormRope.run: {name} must be a contiguous CUDA vector of {self.w_shape[0]} {self.dtype}")
+            d, dt, n = self.desc, self.dtype, len(q)
+            qs, ks, ws = (n, d.q_heads, d.head_dim), (n, d.k_heads, d.head_dim), (d.head_dim,)
+            _refuse("attn_rope_run", st, ("q", q, qs, dt, True), ("k", k, ks, dt, True),
+                    ("positions", positions, (n,), _torch.int32, False), ("q_out", q_out, qs, dt, True),
+                    ("k_out", k_out, ks, dt, True),
+                    *((name, w, ws, dt, False) for name, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None))
 
     def close(self):
         if self.plan:
             _lib.attn_rope_destroy(self.plan)
-            self.plan = None
+            self.plan, self.handle = None, (0, *self.handle[1:])
 
     def __del__(self):
         try:
@@ -571,21 +557,18 @@ class PromptAttention:
         _check(st, "attn_prompt_create")
         self.plan = h
         self.dtype = _torch_dtype(dtype)
-        self.q_shape, self.k_shape = (q_heads, head_dim), (k_heads, head_dim)
+        self.handle = (h, self.dtype, q_heads, k_heads, head_dim)
 
     def run(self, q, k, v, cu_q, cu_k, out, stream=None):
-        what, dtype = "PromptAttention.run", self.dtype
-        nq, nk, cus = q.shape[0], k.shape[0], cu_q.shape[0]
-        if cus < 1:
-            raise ValueError(f"{what}: cu_q and cu_k hold batch + 1 values")
-        q_shape, k_shape = (nq, *self.q_shape), (nk, *self.k_shape)
-        st = _lib.attn_prompt_run(self.plan, q.data_ptr(), _rows(what, "q", q, q_shape, dtype),
-                                  k.data_ptr(), _rows(what, "k", k, k_shape, dtype),
-                                  v.data_ptr(), _rows(what, "v", v, k_shape, dtype), _int32s(what, "cu_q", cu_q, cus),
-                                  _int32s(what, "cu_k", cu_k, cus), cus - 1, nq, nk,
-                                  out.data_ptr(), _rows(what, "out", out, q_shape, dtype), _stream(stream, q))
+        st = _binding.prompt(self.handle, q, k, v, cu_q, cu_k, out, stream)
         if st:
-            _check(st, "attn_prompt_run")
+            d, dt, n, nk, cus = self.desc, self.dtype, len(q), len(k), len(cu_q)
+            qs, ks = (n, d.q_heads, d.head_dim), (nk, d.k_heads, d.head_dim)
+            if st == -1 and cus < 1:
+                raise ValueError("attn_prompt_run: cu_q and cu_k hold batch + 1 values")
+            _refuse("attn_prompt_run", st, ("q", q, qs, dt, True), ("k", k, ks, dt, True), ("v", v, ks, dt, True),
+                    ("cu_q", cu_q, (cus,), _torch.int32, False), ("cu_k", cu_k, (cus,), _torch.int32, False),
+                    ("out", out, qs, dt, True))
 
     def sync_status(self, stream=None) -> int:
         torch = _torch or _with_torch()
@@ -594,7 +577,7 @@ class PromptAttention:
     def close(self):
         if self.plan:
             _lib.attn_prompt_destroy(self.plan)
-            self.plan = None
+            self.plan, self.handle = None, (0, *self.handle[1:])
 
     def __del__(self):
         try:
@@ -609,7 +592,7 @@ class KVCache:
     exponents [pages][k_heads][page_size]."""
 
     def __init__(self, k, v, k_exp, v_exp):
-        import torch
+        torch = _torch or _with_torch()
         for name, t in (("k", k), ("v", v), ("k_exp", k_exp), ("v_exp", v_exp)):
             if not getattr(t, "is_cuda", False) or t.dtype != torch.uint8 or not t.is_contiguous():
                 raise ValueError(f"KVCache: {name} must be a contiguous CUDA tensor of uint8")
@@ -617,10 +600,10 @@ class KVCache:
             raise ValueError("KVCache: codes are [pages][k_heads][page_size][head_dim], exponents one dimension less")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.pages, self.k_heads, self.page_size, self.head_dim = k.shape
-        self.row_shape, self.page_shape = (self.k_heads, self.head_dim), tuple(k.shape[1:])
         self.c = attn_cache_t(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), self.pages,
                               self.page_size, self.k_heads, self.head_dim)
-        self._ref = ctypes.byref(self.c)
+        self._ref, self.address = ctypes.byref(self.c), ctypes.addressof(self.c)
+        self.handle = (self.address, self.k_heads, self.head_dim)
 
     @classmethod
     def empty(cls, pages, page_size, k_heads, head_dim, device="cuda"):
@@ -629,31 +612,25 @@ class KVCache:
         made += [torch.zeros(pages, k_heads, page_size, dtype=torch.uint8, device=device) for _ in range(2)]
         return cls(*made)
 
-    def _rows(self, what, k, v, slots):
-        """Check keys, values and slots; returns their count, row strides, the slots' address and the type."""
-        torch = _torch or _with_torch()
-        dtype, n = k.dtype, k.shape[0]
-        if dtype is not torch.bfloat16 and dtype is not torch.float16:
-            raise ValueError(f"{what}: k and v must be float16 or bfloat16, got {dtype}")
-        shape = (n, *self.row_shape)
-        return (n, _rows(what, "k", k, shape, dtype), _rows(what, "v", v, shape, dtype),
-                _int32s(what, "slots", slots, n), GEMM_BF16 if dtype is torch.bfloat16 else GEMM_F16)
-
     def write(self, k, v, slots, stream=None):
         """Quantise [token][k_heads][head_dim] keys and values into their slots (int32; negative: left out)."""
-        n, sk, sv, at, dtype = self._rows("KVCache.write", k, v, slots)
-        st = _lib.attn_cache_write(self._ref, k.data_ptr(), sk, v.data_ptr(), sv, at, n, dtype,
-                                   _stream(stream, k))
+        st = _binding.cache_write(self.handle, k, v, slots, stream)
         if st:
-            _check(st, "attn_cache_write")
+            self._refuse("attn_cache_write", st, k, v, slots)
 
     def read(self, slots, k, v, stream=None):
         """The values of the slots into [token][k_heads][head_dim] tensors (zeros for a negative slot)."""
-        n, sk, sv, at, dtype = self._rows("KVCache.read", k, v, slots)
-        st = _lib.attn_cache_read(self._ref, at, n, k.data_ptr(), sk, v.data_ptr(), sv, dtype,
-                                  _stream(stream, k))
+        st = _binding.cache_read(self.handle, k, v, slots, stream)
         if st:
-            _check(st, "attn_cache_read")
+            self._refuse("attn_cache_read", st, k, v, slots)
+
+    def _refuse(self, what, st, k, v, slots):
+        if st == -1 and k.dtype not in (_torch.float16, _torch.bfloat16):
+            raise ValueError(f"{what}: k and v must be float16 or bfloat16, got {k.dtype}")
+        n = len(k)
+        shape = (n, self.k_heads, self.head_dim)
+        _refuse(what, st, ("k", k, shape, k.dtype, True), ("v", v, shape, k.dtype, True),
+                ("slots", slots, (n,), _torch.int32, False))
 
 
 class CacheAttention:
@@ -664,7 +641,6 @@ class CacheAttention:
     def __init__(self, q_heads, k_heads, head_dim, page_size, dtype=GEMM_BF16, scale=0.0, batch=64):
         self.q_heads, self.k_heads, self.head_dim, self.page_size = q_heads, k_heads, head_dim, page_size
         self.dtype, self.scale, self.code = _torch_dtype(dtype), scale, dtype
-        self.q_shape, self.page_shape = (q_heads, head_dim), (k_heads, page_size, head_dim)
         self.workspace, self.ws_bytes, self.batch = None, 0, 0
         self._grow(batch)
 
@@ -678,27 +654,19 @@ class CacheAttention:
         self.workspace = torch.zeros(n.value, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
         self.ws_bytes, self.batch = n.value, batch
+        self.handle = (self.dtype, self.q_heads, self.k_heads, self.head_dim, self.page_size, self.code, float(self.scale),
+                       self.workspace.data_ptr(), self.ws_bytes, batch)
 
     def run(self, q, cache, page_table, lengths, out, stream=None):
         """q, out: [batch][q_heads][head_dim]; page_table: [batch][pages a sequence] int32; lengths: batch int32."""
-        what, n = "CacheAttention.run", q.shape[0]
-        if cache.page_shape != self.page_shape:
-            raise ValueError(f"{what}: the cache has another shape than this was made for")
-        q_shape = (n, *self.q_shape)
-        sq, so = _rows(what, "q", q, q_shape, self.dtype), _rows(what, "out", out, q_shape, self.dtype)
-        lens = _int32s(what, "lengths", lengths, n)
-        shape, pitch = page_table.shape, page_table.stride()
-        if not page_table.is_cuda or page_table.dtype is not _torch.int32 or len(shape) != 2 or shape[0] != n or \
-                (shape[1] > 1 and pitch[1] != 1):
-            raise ValueError(f"{what}: page_table must be a CUDA tensor [{n}][pages] of int32 with contiguous rows")
-        if n > self.batch:
-            self._grow(n)
-        most = shape[1]
-        pitch = pitch[0] if n > 1 else most
-        if pitch < most:
-            raise ValueError(f"{what}: the rows of page_table overlap")
-        st = _lib.attn_cache_attend(cache._ref, q.data_ptr(), sq, self.q_heads, page_table.data_ptr(), pitch, most,
-                                    lens, n, self.scale, self.code, out.data_ptr(), so,
-                                    self.workspace.data_ptr(), self.ws_bytes, _stream(stream, q))
+        st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)
+        if st == -1 and len(q) > self.batch:
+            self._grow(len(q))
+            st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)
         if st:
-            _check(st, "attn_cache_attend")
+            what, n, dt = "attn_cache_attend", len(q), self.dtype
+            if st == -1 and (cache.k_heads, cache.head_dim, cache.page_size) != (self.k_heads, self.head_dim, self.page_size):
+                raise ValueError(f"{what}: the cache has another shape than this was made for")
+            shape = (n, self.q_heads, self.head_dim)
+            _refuse(what, st, ("q", q, shape, dt, True), ("page_table", page_table, (n, page_table.shape[-1]), _torch.int32, True),
+                    ("lengths", lengths, (n,), _torch.int32, False), ("out", out, shape, dt, True))

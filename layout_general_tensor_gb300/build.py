@@ -1,7 +1,8 @@
 """Build the C-ABI library ``_lib/libgemm.so`` with nvcc for sm_103a.
 
 Each translation unit compiles in parallel; the shared library links against
-the CUDA runtime only (driver entry points are resolved at run time).  Run as
+the CUDA runtime only (driver entry points are resolved at run time).  Beside
+it, ``_lib/_binding.so``: the part of the Python binding that is in C.  Run as
 ``python layout_general_tensor_gb300/build.py`` or call :func:`build` (the
 package itself loads the built library on import, so this file is loaded by
 path).
@@ -13,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libgemm.so")
+BINDING = os.path.join(OUT_DIR, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "api_int4.cu", "gemm_tc.cu", "gemm_tc_pair.cu", "gemm_int4.cu", "gemm_int4_f8.cu",
@@ -42,9 +45,9 @@ def _deps():
 
 
 def _up_to_date():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -70,13 +73,24 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        include = [os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"), sysconfig.get_paths()["include"], INCLUDE]
+        cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-fPIC", "-shared", *(f"-I{d}" for d in include),
+               os.path.join(CSRC, "binding.c"), "-o", BINDING + ".tmp"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"binding.c does not compile:\n{r.stdout}\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
     os.replace(tmp, LIB)
     return LIB
 
