@@ -10,6 +10,9 @@
 // ceil(log2(amax / 448)) is e - 8, and one more when m > 1.75.
 //
 // Bound: memory; every value is read once and every code written once.
+// Measured (16384 tokens, 8 heads of 128, bf16): write and read back 30.7 us,
+// 6.6 TB/s, 97 % of a copy's rate; with the maxima found in fp32 and the power
+// applied as two factors the write was bound by arithmetic (35 us).
 #include <cstdint>
 
 #include "cache.h"

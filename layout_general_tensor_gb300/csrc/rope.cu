@@ -18,8 +18,11 @@
 // within 2^-20.9 absolute, a thousandth of an fp16 rounding.
 //
 // Bound: memory, each value read and written once.  A group takes a chunk of
-// neighbouring heads, two at a time with the next two on their way, and
-// computes the sines again only where the token changes.
+// neighbouring heads with two on their way, and computes the sines again only
+// where the token changes; the blocks are one wave of what the registers hold.
+// Measured (16384 tokens, 32 + 8 heads of 128, bf16): 58.7 us, 5.72 TB/s, 84 %
+// of a copy's rate; runs of four values 84.5, chunks for eight blocks an SM 65,
+// one head on its way 84, a ring in shared memory 63.  64 tokens: 2.9 us.
 #include <cmath>
 #include <cstdint>
 #include <new>
