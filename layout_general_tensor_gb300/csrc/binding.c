@@ -80,7 +80,7 @@ static int look_vector(PyObject* t, PyObject* dtype, int64_t count, view* x) {
   return look(t, dtype, 1, x) && x->contiguous && (count < 0 || x->dim[0] == count);
 }
 
-/* The stream given, or the current one of t's device. */
+/* The stream given, or the current one of t's device; 0 with an exception set where it is neither. */
 static int look_stream(PyObject* stream, PyObject* t, void** to) {
   PyObject *device, *s;
   if (stream != Py_None) {
@@ -123,8 +123,9 @@ static PyObject* py_rope(PyObject* self, PyObject* const* args, Py_ssize_t nargs
   if (!look_rows(args[1], dtype, -1, hq, d, &q) || !look_rows(args[2], dtype, q.dim[0], hk, d, &k) ||
       !look_vector(args[3], t_int32, q.dim[0], &pos) || !look_rows(args[4], dtype, q.dim[0], hq, d, &qo) ||
       !look_rows(args[5], dtype, q.dim[0], hk, d, &ko) || (args[6] != Py_None && !look_vector(args[6], dtype, d, &wq)) ||
-      (args[7] != Py_None && !look_vector(args[7], dtype, d, &wk)) || !look_stream(args[8], args[1], &stream))
+      (args[7] != Py_None && !look_vector(args[7], dtype, d, &wk)))
     return refused();
+  if (!look_stream(args[8], args[1], &stream)) return NULL;
   return status(rope_run(address(h, 0), q.ptr, q.stride[0], k.ptr, k.stride[0], wq.ptr, wk.ptr, pos.ptr, q.dim[0], qo.ptr,
                          qo.stride[0], ko.ptr, ko.stride[0], stream));
 }
@@ -139,8 +140,9 @@ static PyObject* py_prompt(PyObject* self, PyObject* const* args, Py_ssize_t nar
   if (!look_rows(args[1], dtype, -1, hq, d, &q) || !look_rows(args[2], dtype, -1, hk, d, &k) ||
       !look_rows(args[3], dtype, k.dim[0], hk, d, &v) || !look_vector(args[4], t_int32, -1, &cq) || cq.dim[0] < 1 ||
       cq.dim[0] > INT32_MAX || !look_vector(args[5], t_int32, cq.dim[0], &ck) ||
-      !look_rows(args[6], dtype, q.dim[0], hq, d, &out) || !look_stream(args[7], args[1], &stream))
+      !look_rows(args[6], dtype, q.dim[0], hq, d, &out))
     return refused();
+  if (!look_stream(args[7], args[1], &stream)) return NULL;
   return status(prompt_run(address(h, 0), q.ptr, q.stride[0], k.ptr, k.stride[0], v.ptr, v.stride[0], cq.ptr, ck.ptr,
                            (int32_t)(cq.dim[0] - 1), q.dim[0], k.dim[0], out.ptr, out.stride[0], stream));
 }
@@ -154,11 +156,11 @@ static PyObject* cache_call(PyObject* const* args, Py_ssize_t nargs, int write) 
   PyObject* dtype = PyObject_GetAttr(args[1], n_dtype);
   const int64_t hk = whole(h, 1), d = whole(h, 2);
   const int ok = (dtype == t_float16 || dtype == t_bfloat16) && look_rows(args[1], dtype, -1, hk, d, &k) &&
-                 look_rows(args[2], dtype, k.dim[0], hk, d, &v) && look_vector(args[3], t_int32, k.dim[0], &slots) &&
-                 look_stream(args[4], args[1], &stream);
+                 look_rows(args[2], dtype, k.dim[0], hk, d, &v) && look_vector(args[3], t_int32, k.dim[0], &slots);
   const int32_t code = dtype == t_bfloat16 ? GEMM_BF16 : GEMM_F16;
   Py_XDECREF(dtype);
   if (!ok) return refused();
+  if (!look_stream(args[4], args[1], &stream)) return NULL;
   if (write)
     return status(cache_write(address(h, 0), k.ptr, k.stride[0], v.ptr, v.stride[0], slots.ptr, k.dim[0], code, stream));
   return status(cache_read(address(h, 0), slots.ptr, k.dim[0], k.ptr, k.stride[0], v.ptr, v.stride[0], code, stream));
@@ -178,8 +180,9 @@ static PyObject* py_attend(PyObject* self, PyObject* const* args, Py_ssize_t nar
   if (!cache || cache->k_heads != whole(h, 2) || cache->head_dim != d || cache->page_size != whole(h, 4) ||
       !look_rows(args[2], dtype, -1, hq, d, &q) || !look(args[3], t_int32, 2, &table) || table.dim[0] != q.dim[0] ||
       table.dim[1] > INT32_MAX || !look_vector(args[4], t_int32, q.dim[0], &lengths) ||
-      !look_rows(args[5], dtype, q.dim[0], hq, d, &out) || q.dim[0] > whole(h, 9) || !look_stream(args[6], args[2], &stream))
+      !look_rows(args[5], dtype, q.dim[0], hq, d, &out) || q.dim[0] > whole(h, 9))
     return refused();
+  if (!look_stream(args[6], args[2], &stream)) return NULL;
   if (table.contiguous) {
     table.stride[0] = table.dim[1];
   } else if ((table.dim[1] > 1 && table.stride[1] != 1) || table.stride[0] < table.dim[1]) {

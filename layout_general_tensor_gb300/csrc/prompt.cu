@@ -1037,6 +1037,7 @@ uint64_t prompt_wait_limit() {
 
 struct attn_prompt_plan {
   attn_prompt_desc_t d;
+  int device = -1;
   lgt::DeviceStatus* d_status = nullptr;
   uint64_t wait_limit_ns = 0;
 };
@@ -1060,6 +1061,7 @@ gemm_status_t attn_prompt_create(const attn_prompt_desc_t* desc, attn_prompt_pla
   attn_prompt_plan* p = new (std::nothrow) attn_prompt_plan();
   if (!p) return GEMM_ERR_CUDA;
   p->d = d;
+  p->device = dev;
   p->wait_limit_ns = lgt::prompt_wait_limit();
   if (cudaMalloc(&p->d_status, 16) != cudaSuccess || cudaMemset(p->d_status, 0, 16) != cudaSuccess) {
     cudaGetLastError();
@@ -1098,6 +1100,7 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
+  if (dev != plan->device) return GEMM_ERR_INVALID_ARG;  // (the status word is there)
   const int64_t wide = (total_q / (2 * tok) + batch) * d.k_heads;
   const bool few = wide < static_cast<int64_t>(lgt::kPrFill) * sms;
   const int64_t units = few ? (total_q / tok + batch) * d.k_heads : wide;

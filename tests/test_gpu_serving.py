@@ -270,6 +270,8 @@ def test_prompt_refusals(m):
                 dict(cu_k=cu[:1]), dict(k=k.transpose(0, 1).contiguous().transpose(0, 1)), dict(cu_q=cu[:0], cu_k=cu[:0])):
         with pytest.raises(ValueError):
             op.run(**{**dict(q=q, k=k, v=k, cu_q=cu, cu_k=cu, out=torch.empty_like(q)), **bad})
+    with pytest.raises(TypeError):
+        op.run(q, k, k, cu, cu, torch.empty_like(q), stream=torch.cuda.Stream())
     run, p = m._lib.attn_prompt_run, lambda t: t.data_ptr()
     ok = [op.plan, p(q), 0, p(k), 0, p(k), 0, p(cu), p(cu), 1, 5, 6, p(q), 0, None]
     for i, bad, st in ((0, None, 1), (1, None, 1), (3, None, 1), (5, None, 1), (7, None, 1), (8, None, 1), (12, None, 1), (9, -1, 1), (10, -1, 1),
