@@ -35,13 +35,15 @@
 // control), so that it loads the next unit's tiles and issues their first
 // products while the softmax warps still write the last unit's result.
 //
-// Warps (384 threads): 0-3 softmax of tile 0, 4-7 of tile 1, 8 loads Q and K,
-// 9 issues the products, 11 finds the units, 10 loads V and looks over the
-// rows of it that some query of the CTA must not see, since a weight of 0 does
-// not cancel an infinity or a NaN: rows that no query sees (later ones, or the
-// next sequence's) are cleared; in the others (2T at most) values that are not
-// finite are, and are added to the results of the queries that do see them at
-// the end, where a sum with a positive weight would have left the same.
+// Warps (384 threads): 0-3 softmax of tile 0, 4-7 of tile 1, 8 loads K,
+// 9 issues the products, 11 finds the units and loads Q, 10 loads V (three
+// warps load because issuing a copy holds its thread for 250 cycles or more)
+// and looks over the rows of it that some query of the CTA must not see, since
+// a weight of 0 does not cancel an infinity or a NaN: rows that no query sees
+// (later ones, or the next sequence's) are cleared; in the others (2T at most)
+// values that are not finite are, and are added to the results of the queries
+// that do see them at the end, where a sum with a positive weight would have
+// left the same.
 // Tensor memory: S of the tiles at columns 0 and 128, O at 256 and
 // 256 + head_dim; P lies over its own S (head_dim 128: the columns are all
 // taken; the products that read P and write the next S are of one shape and
@@ -51,8 +53,8 @@
 //
 // Bound: the tensor core, whose S reads all of the shared memory's rate (8 KiB
 // in 64 cycles), and in long runs the power limit.  Measured (bf16, head_dim
-// 128, causal, visible products only): 4 prompts of 4096, 32 / 8 heads, 345 us,
-// 1595 TFLOP/s, 83 % of cuBLAS's burst rate (380 us in long runs); 1 of 16384,
+// 128, causal, visible products only): 4 prompts of 4096, 32 / 8 heads, 340 us,
+// 1615 TFLOP/s, 84 % of cuBLAS's burst rate (375 us in long runs); 1 of 16384,
 // 16 / 2 heads, 620 us, 1773 TFLOP/s, 92 % (tensor pipe 83 % of cycles).  Steps
 // of the latter: products issued by a whole warp, maximum before weights 718;
 // maximum beside weights, halves handed over 680; one issuing thread, waits
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   const uint64_t limit = a.wait_limit_ns;
   auto unit_ready = [&](int it) { return warp_wait(unit_full(it & 1), (it >> 1) & 1, limit, abort_flag); };
   int issued = 0;                 // loads of K (warp 8), of V (warp 10)
-  int q_uses[2] = {0, 0};         // loads of Q (warp 8)
+  int q_uses[2] = {0, 0};         // loads of Q (warp 11)
   int asked = 0;                  // blocks asked for (warp 11)
 
   // Load block j of K (which = 0) or V (1) of unit w into its next place.
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   };
 
   if (warp == 8) {
-    // --------------------------------------------------- loads of Q and K
+    // -------------------------------------------------------- loads of K
     const bool leader = elect_one();
     bool ok = true;
     for (int it = 0; ok; ++it) {
@@ -476,22 +478,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       if (w.tokens < 0) break;
       for (int j = 0; ok && j < w.nb; ++j) {
         if (!(ok = load(0, j, w, &a.tm_k, leader))) break;
-        if (j > 0) continue;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || (w.split ? t != 0 : w.blocks[t] == 0)) continue;
-          // (the last products that read this tile of Q are done)
-          if (q_uses[t] > 0 && !(ok = warp_wait(q_empty(t), (q_uses[t] - 1) & 1, limit, abort_flag))) continue;
-          if (leader) {
-            mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tok * a.group) * 128u * (D / 64));
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(base + C::Q_OFF + t * C::TILE + c * C::CHUNK, &a.tm_q, q_full(t), c * 64, w.h * a.group,
-                          w.row0 + t * a.tok);
-          }
-          __syncwarp();
-          ++q_uses[t];
-        }
       }
       if (lane == 0) mbar_arrive(unit_empty(it & 1));
     }
@@ -711,7 +697,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     }
     if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 3);
   } else if (warp == 11) {
-    // -------------------------------------------------------------- units
+    // ------------------------------------------------- units, loads of Q
     int64_t block = blockIdx.x;
     int turn = 0;  // of the next unit's first block at the ring's places
     const PromptSeq mine = seq_at(a, lane);
@@ -736,6 +722,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         shape_unit<FEW>(a, w, turn);
         turn ^= w.nb & 1;
         publish(w);
+        if (!ok) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || w.nb == 0 || (w.split ? t != 0 : w.blocks[t] == 0)) continue;
+          // (the last products that read this tile of Q are done)
+          if (q_uses[t] > 0 && !(ok = warp_wait(q_empty(t), (q_uses[t] - 1) & 1, limit, abort_flag))) continue;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tok * a.group) * 128u * (D / 64));
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(base + C::Q_OFF + t * C::TILE + c * C::CHUNK, &a.tm_q, q_full(t), c * 64, w.h * a.group,
+                          w.row0 + t * a.tok);
+          }
+          __syncwarp();
+          ++q_uses[t];
+        }
         if (!ok) break;
       }
       // the next one (a CTA is at most one ahead of itself: the second of two
@@ -975,14 +977,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   if ((warp == 8 || warp == 10) && *abort_flag) {
     // let the loads still in flight land before the CTA exits
     volatile int no_abort = 0;
-    for (int t = 0; t < 2; ++t)
-      if (q_uses[t] > 0) mbar_wait_bounded(q_full(t), (q_uses[t] - 1) & 1, limit, &no_abort);
     for (int n = issued > 2 ? issued - 2 : 0; n < issued; ++n)
       mbar_wait_bounded(full(2 * (n & 1) + (warp == 10)), (n >> 1) & 1, limit, &no_abort);
   }
-  if (warp == 11 && *abort_flag && asked > 0) {
+  if (warp == 11 && *abort_flag) {
     volatile int no_abort = 0;
-    mbar_wait_bounded(taken, (asked - 1) & 1, limit, &no_abort);
+    for (int t = 0; t < 2; ++t)
+      if (q_uses[t] > 0) mbar_wait_bounded(q_full(t), (q_uses[t] - 1) & 1, limit, &no_abort);
+    if (asked > 0) mbar_wait_bounded(taken, (asked - 1) & 1, limit, &no_abort);
   }
   if (warp == 9) {
     volatile int no_abort = 0;
