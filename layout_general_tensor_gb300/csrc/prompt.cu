@@ -26,8 +26,11 @@
 // the walk over the keys, which is what such a unit takes, is half as long.
 // Where there are few units, a sequence whose walk over its keys is longer than
 // twice what each SM would have to do is cut into units of T tokens, so that
-// all of them are of this kind.  (A kernel of its own, FEW: in the other the
-// code that no unit uses costs 2 %.)
+// all of them are of this kind.  (A kernel of its own, kPrFew: in the other the
+// code that no unit uses costs 2 %.)  Where there are so few that most SMs would
+// have none, the keys of a unit are cut over a cluster of two to eight CTAs
+// (kPrCut); each leaves its sums in its shared memory, and the cluster joins
+// them, a share of the columns a CTA, in the order of the keys.
 //
 // Work.  A unit is 2T tokens (or T) of a sequence and a key head.  The grid has a
 // block for every unit, the ones with the most keys of a sequence first; a
@@ -54,7 +57,7 @@
 // Bound: the tensor core, whose S reads all of the shared memory's rate (8 KiB
 // in 64 cycles), and in long runs the power limit.  Measured (bf16, head_dim
 // 128, causal, visible products only): 4 prompts of 4096, 32 / 8 heads, 340 us,
-// 1615 TFLOP/s, 84 % of cuBLAS's burst rate (375 us in long runs); 1 of 16384,
+// 1615 TFLOP/s, 84 % of cuBLAS's burst rate (372 us in long runs); 1 of 16384,
 // 16 / 2 heads, 620 us, 1773 TFLOP/s, 92 % (tensor pipe 83 % of cycles).  Steps
 // of the latter: products issued by a whole warp, maximum before weights 718;
 // maximum beside weights, halves handed over 680; one issuing thread, waits
@@ -64,7 +67,9 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstdlib>
 #include <new>
@@ -85,6 +90,18 @@ constexpr int kPrKeys = 128;   // keys of a block
 constexpr int kPrTimeout = GEMM_ERR_TIMEOUT;
 constexpr float kPrLazy = 8.0f;
 constexpr int kPrFill = 2;     // units an SM below which the kernel for few is taken
+constexpr int kPrParts = 8;    // CTAs of a cluster that may share a unit
+// Blocks of keys, in the mean, that sharing takes from a CTA's walk at least:
+// the cluster's start and join cost 1.5 us with a row, 2.5 with all, what two
+// pairs of blocks do.  (us, shared and not: 1 token after about 4096 keys, 32 /
+// 8 heads of 128, 8.7 and 18.4, after 32768 23.6 and 120; 64 after 8192 17.2 and
+// 33.7; 512 after about 400, 8 / 2 heads, 11.0 and 11.1; 1000 after none, 8 / 8
+// heads, where sharing spares 4, 14.3 and 12.8.)
+constexpr int kPrSpare = 5;
+
+// The kernels: for many units, for few (of one tile where walks are long),
+// and for so few that the keys of each are cut over a cluster.
+enum PromptKind { kPrMany, kPrFew, kPrCut };
 
 struct PromptArgs {
   CUtensorMap tm_q;        // {head_dim, q_heads, rows}, box {64, group, T}
@@ -99,6 +116,7 @@ struct PromptArgs {
   int32_t hk, group, tok;  // tok: T
   int32_t sms;
   int32_t causal;
+  int32_t lg_parts;  // log2 of the CTAs that share a unit
   MagicDiv div_hk, div_group, div_tok, div_pair;  // by T, by 2T
   float cs;  // scale * log2(e)
   uint32_t idesc_s, idesc_pv;
@@ -120,11 +138,12 @@ struct PromptUnit {
   // (three at most: they span 2T keys) hold some that not all see
   int all_see, any_sees, mixed;
   int odd;                 // V held values that are not finite
-  int pad[15];
+  int from, keys;          // first key of the part that this CTA has (key_row, nk and shift are the part's), and all keys
+  int pad[13];
 };
 static_assert(sizeof(PromptUnit) == 128, "two of them in shared memory");
 
-template <bool FEW>
+template <PromptKind KIND>
 __device__ __forceinline__ void shape_unit(const PromptArgs& a, PromptUnit& x, int turn) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -134,7 +153,7 @@ __device__ __forceinline__ void shape_unit(const PromptArgs& a, PromptUnit& x, i
     x.blocks[t] = (vis + kPrKeys - 1) / kPrKeys;
   }
   x.nb = max(x.blocks[0], x.blocks[1]);
-  x.split = FEW && x.tokens <= a.tok;
+  x.split = KIND != kPrMany && x.tokens <= a.tok;
   x.start = turn;
   if (x.split) {
     x.toks[1] = x.toks[0];
@@ -144,6 +163,18 @@ __device__ __forceinline__ void shape_unit(const PromptArgs& a, PromptUnit& x, i
   x.all_see = a.causal ? min(max(x.shift + 1, 0), x.nk) : x.nk;
   x.any_sees = a.causal ? min(max(x.tokens + x.shift, 0), x.nk) : x.nk;
   x.mixed = x.all_see / kPrKeys;
+}
+
+// Part `rank` of the unit's blocks of keys, as a unit of its own.
+__device__ __forceinline__ void cut_unit(const PromptArgs& a, PromptUnit& x, int rank) {
+  const int sees = a.causal ? min(max(x.tokens + x.shift, 0), x.nk) : x.nk;
+  const int nb = (sees + kPrKeys - 1) / kPrKeys;
+  const int b0 = (nb * rank) >> a.lg_parts, b1 = (nb * (rank + 1)) >> a.lg_parts;
+  x.keys = x.nk;
+  x.from = b0 * kPrKeys;
+  x.nk = min(x.nk, b1 * kPrKeys) - min(x.nk, x.from);
+  x.key_row += x.from;
+  x.shift -= x.from;
 }
 
 template <int D>
@@ -162,6 +193,11 @@ struct PromptCfg {
   static constexpr uint32_t XCH_OFF = UNIT_OFF + 2 * sizeof(PromptUnit);     // {m, l} of both tiles' rows
   static constexpr uint32_t MISC_OFF = XCH_OFF + 2 * kPrRows * 8;
   static constexpr uint32_t SMEM = MISC_OFF + 16 + 1024;  // slack for the 1024-byte alignment
+  // A part's sums, where the ring was: four columns of all rows, the next four
+  // (apart by a place more than the rows, for the banks), ..., {m, l} of the rows.
+  static constexpr uint32_t PART_OFF = RING_OFF, PART_STEP = (kPrRows + 1) * 16u;
+  static constexpr uint32_t PART_ML_OFF = PART_OFF + (D / 4) * PART_STEP;
+  static_assert(PART_ML_OFF + kPrRows * 8 <= RING_OFF + NS * TILE, "a part's sums");
   static constexpr uint32_t S_COL = 128;                  // between the tiles' S
   static constexpr uint32_t O_COL = 256;
   static constexpr uint32_t P_COL = D == 128 ? 0 : 384;
@@ -341,18 +377,24 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
 // All bits of the halves whose sign bits are set.
 __device__ __forceinline__ uint32_t spread_halves(uint32_t signs) { return (signs >> 15) * 0xffffu; }
 
-// Add the values of 32 columns of V (at `p`) that are not finite to a row's
-// sums.  (They stay what they are, or become NaN, in the division by the
-// row's sum of weights.)
+// Add the values of V that are not finite to a row's sums: two columns', 32
+// columns' (at `p`).  (They stay what they are, or become NaN, in the division
+// by the row's sum of weights.)
+template <bool BF16>
+__device__ __forceinline__ void add_odd_pair(uint32_t x, float& s0, float& s1) {
+  const uint32_t bad = odd_halves<BF16>(x);
+  const float2 y = unpack_pair16<BF16>(x);
+  if (bad & 0x8000u) s0 += y.x;
+  if (bad & 0x80000000u) s1 += y.y;
+}
 template <bool BF16>
 __device__ __forceinline__ void add_odd(const uint16_t* p, uint32_t (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint32_t x = reinterpret_cast<const uint32_t*>(p)[i];
-    const uint32_t bad = odd_halves<BF16>(x);
-    const float2 y = unpack_pair16<BF16>(x);
-    if (bad & 0x8000u) v[2 * i] = __float_as_uint(__uint_as_float(v[2 * i]) + y.x);
-    if (bad & 0x80000000u) v[2 * i + 1] = __float_as_uint(__uint_as_float(v[2 * i + 1]) + y.y);
+    float s0 = __uint_as_float(v[2 * i]), s1 = __uint_as_float(v[2 * i + 1]);
+    add_odd_pair<BF16>(reinterpret_cast<const uint32_t*>(p)[i], s0, s1);
+    v[2 * i] = __float_as_uint(s0);
+    v[2 * i + 1] = __float_as_uint(s1);
   }
 }
 
@@ -374,7 +416,89 @@ __device__ __forceinline__ void exchange4(uint32_t (&y)[16], int lane) {
     }
 }
 
-template <int D, bool BF16, bool FEW>
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_v2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Join the 2^LG parts of a unit: this CTA, `rank` of the cluster, has its share
+// of the columns.  A thread takes four columns of kU rows at a time, so that
+// kPrParts loads are on their way whatever the parts are, and adds the parts in
+// the order of the keys.
+template <int D, bool BF16, int LG>
+__device__ __forceinline__ void join_parts(const PromptArgs& a, const PromptUnit& w, uint32_t base, uint32_t rank) {
+  using C = PromptCfg<D>;
+  constexpr int P = 1 << LG, kU = kPrParts / P, kShare = D / 4 / P;
+  const int items = w.toks[0] * a.group * kShare;
+  uint32_t odd = 0;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    odd |= ld_cluster_u32(mapa_shared(base + C::UNIT_OFF + static_cast<uint32_t>(offsetof(PromptUnit, odd)), p));
+  for (int i0 = threadIdx.x; i0 < items; i0 += kPrThreads * kU) {
+    float2 ml[kU][P];
+    float4 x[kU][P];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int i = min(i0 + u * kPrThreads, items - 1), row = i / kShare, c4 = static_cast<int>(rank) * kShare + i % kShare;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        ml[u][p] = ld_cluster_v2(mapa_shared(base + C::PART_ML_OFF + row * 8, p));
+        x[u][p] = ld_cluster_v4(mapa_shared(base + C::PART_OFF + c4 * C::PART_STEP + row * 16, p));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int i = i0 + u * kPrThreads, row = i / kShare, c4 = static_cast<int>(rank) * kShare + i % kShare;
+      if (i >= items) break;
+      float top = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) top = fmaxf(top, ml[u][p].x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float f = ex2(ml[u][p].x - ref);
+        l = fmaf(ml[u][p].y, f, l);
+        sum = make_float4(fmaf(x[u][p].x, f, sum.x), fmaf(x[u][p].y, f, sum.y), fmaf(x[u][p].z, f, sum.z),
+                          fmaf(x[u][p].w, f, sum.w));
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      sum = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+      uint32_t tok, g;
+      magic_divmod(static_cast<uint32_t>(row), a.div_group, tok, g);
+      if (odd) {
+        const int shift = w.shift + w.from;
+        const int vis = a.causal ? min(static_cast<int>(tok) + shift + 1, w.keys) : w.keys;
+        for (int k = a.causal ? min(max(shift + 1, 0), w.keys) : w.keys; k < vis; ++k) {
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v + static_cast<int64_t>(w.key_row - w.from + k) * a.vs +
+                                                                w.h * D + c4 * 4);
+          add_odd_pair<BF16>(v[0], sum.x, sum.y);
+          add_odd_pair<BF16>(v[1], sum.z, sum.w);
+        }
+      }
+      const uint2 y = l == 0.0f ? make_uint2(0u, 0u)
+                                : make_uint2(pack_pair16<BF16>(sum.x, sum.y), pack_pair16<BF16>(sum.z, sum.w));
+      *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(w.row0 + static_cast<int>(tok)) * a.os +
+                                static_cast<int64_t>(w.h * a.group + static_cast<int>(g)) * D + c4 * 4) = y;
+    }
+  }
+}
+
+template <int D, bool BF16, PromptKind KIND>
 __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_constant__ PromptArgs a) {
   using C = PromptCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -615,7 +739,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         blocks[0] = units[it & 1].blocks[0];
         blocks[1] = units[it & 1].blocks[1];
         if (units[it & 1].tokens < 0) break;
-        if (FEW && units[it & 1].split) {
+        if (KIND != kPrMany && units[it & 1].split) {
           if (nb > 0 && wait(q_full(0), q_parity[0])) {
             q_parity[0] ^= 1u;
             for (int j = 0; ok && j < min(nb, 2); ++j) {
@@ -698,10 +822,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 3);
   } else if (warp == 11) {
     // ------------------------------------------------- units, loads of Q
-    int64_t block = blockIdx.x;
+    int64_t block = KIND == kPrCut ? blockIdx.x >> a.lg_parts : blockIdx.x;
     int turn = 0;  // of the next unit's first block at the ring's places
     const PromptSeq mine = seq_at(a, lane);
-    const int narrow = FEW ? narrow_above(a, mine) : 0x7fffffff;
+    const int narrow = KIND == kPrFew ? narrow_above(a, mine) : KIND == kPrCut ? -1 : 0x7fffffff;
     bool ok = true;
     int it = 0;
     auto publish = [&](const PromptUnit& w) {
@@ -719,7 +843,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       PromptUnit w = find_unit(a, unit, narrow, mine);
       if (w.tokens > 0) {  // (blocks past the last unit hold nothing)
         w.h = static_cast<int>(h);
-        shape_unit<FEW>(a, w, turn);
+        if (KIND == kPrCut) cut_unit(a, w, static_cast<int>(cluster_ctarank()));
+        shape_unit<KIND>(a, w, turn);
         turn ^= w.nb & 1;
         publish(w);
         if (!ok) break;
@@ -740,6 +865,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         }
         if (!ok) break;
       }
+      if (KIND == kPrCut) break;  // (a cluster has one unit)
       // the next one (a CTA is at most one ahead of itself: the second of two
       // places is free when the unit before the last is done)
       if (lane == 0) {
@@ -774,7 +900,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       if (!(ok = unit_ready(it))) break;
       const PromptUnit* w = &units[it & 1];
       if (w->tokens < 0) break;
-      const int my_blocks = w->blocks[t], split = FEW ? w->split : 0;
+      const int my_blocks = w->blocks[t], split = KIND != kPrMany ? w->split : 0;
       const bool live = static_cast<int>(tok) < w->toks[t];
       const int my_tok = static_cast<int>(tok) + (split ? 0 : t * a.tok);
       const int vis = a.causal ? min(my_tok + w->shift + 1, w->nk) : w->nk;
@@ -883,7 +1009,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       }
       // f0, f1: what the tiles' sums are multiplied by (f1 only where two are
       // joined), 0 for one that has none
-      float f0 = l == 0.0f ? 0.0f : 1.0f / l, f1 = 0.0f;
+      float f0 = l == 0.0f ? 0.0f : 1.0f / l, f1 = 0.0f, top = m;
       bool use0 = my_blocks > 0, use1 = false;
       uint32_t o0 = o_addr, o1 = o_addr;
       int c0 = 0, c1 = D;
@@ -902,10 +1028,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         }
         if (ok) {
           const float om = ld_shared_f32(xch + (t ^ 1) * kPrRows * 8), ol = ld_shared_f32(xch + (t ^ 1) * kPrRows * 8 + 4);
-          const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.0f : top;
+          top = fmaxf(m, om);
+          const float ref = top == -INFINITY ? 0.0f : top;
           const float g0 = ex2(m - ref), g1 = ex2(om - ref);
           l = l * g0 + ol * g1;
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const float inv = KIND == kPrCut ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
           f0 = g0 * inv;
           f1 = g1 * inv;
           use1 = w->blocks[t ^ 1] > 0;
@@ -916,6 +1043,37 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       }
       if (!ok) break;
       tc_fence_after();
+      if constexpr (KIND == kPrCut) {
+        // The part's sums go where the ring was (nothing reads it any more:
+        // both tiles' last products are done).
+        if (t == 0) {
+          st_shared_f32(base + C::PART_ML_OFF + row * 8, top);
+          st_shared_f32(base + C::PART_ML_OFF + row * 8 + 4, l);
+        }
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          uint32_t v[32], u[32];
+          if (use0) {
+            tc_ld_32x32b_x32(o0 + c, v);
+            tc_wait_ld_regs(v);
+          }
+          if (use1) {
+            tc_ld_32x32b_x32(o1 + c, u);
+            tc_wait_ld_regs(u);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float x = use0 ? __uint_as_float(v[i]) * f0 : 0.0f;
+            v[i] = __float_as_uint(use1 ? fmaf(__uint_as_float(u[i]), f1, x) : x);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            st_shared_v4(base + C::PART_OFF + (c / 4 + i) * C::PART_STEP + row * 16, v[4 * i], v[4 * i + 1], v[4 * i + 2],
+                         v[4 * i + 3]);
+        }
+        tc_fence_before();
+        break;
+      }
       const bool odd = *const_cast<volatile int*>(&w->odd) != 0;  // (set before the last product was let go)
       // Four lanes exchange 16-byte pieces of their rows, so that a store
       // writes 64 bytes of each of eight rows (a row a lane, 16 bytes of 32
@@ -990,23 +1148,65 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     volatile int no_abort = 0;
     mbar_wait_bounded(teardown, 0, limit, &no_abort);
   }
+  if constexpr (KIND == kPrCut) {
+    // (every thread of the cluster comes here, whether its waits ran out or
+    // not; a unit's geometry is written without a wait)
+    __syncwarp();
+    cluster_sync_all();
+    if (units[0].tokens > 0) {
+      const uint32_t rank = cluster_ctarank();
+      static_assert(kPrParts == 8, "2, 4 or 8 parts");
+      if (a.lg_parts == 1)
+        join_parts<D, BF16, 1>(a, units[0], base, rank);
+      else if (a.lg_parts == 2)
+        join_parts<D, BF16, 2>(a, units[0], base, rank);
+      else
+        join_parts<D, BF16, 3>(a, units[0], base, rank);
+    }
+    __syncwarp();
+    cluster_sync_all();  // the parts have been read
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool BF16, bool FEW>
+template <int D, bool BF16, PromptKind KIND>
 cudaError_t launch_prompt_as(const PromptArgs& a, unsigned grid, cudaStream_t stream) {
   using C = PromptCfg<D>;
-  const cudaError_t e = set_smem_once<prompt_kernel<D, BF16, FEW>>(static_cast<int>(C::SMEM));
+  const cudaError_t e = set_smem_once<prompt_kernel<D, BF16, KIND>>(static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
-  return launch_pdl(prompt_kernel<D, BF16, FEW>, dim3(grid), dim3(kPrThreads), C::SMEM, stream, a);
+  if (KIND == kPrCut)
+    return launch_pdl_cluster(prompt_kernel<D, BF16, KIND>, dim3(grid), dim3(kPrThreads), C::SMEM, stream, 1u << a.lg_parts, a);
+  return launch_pdl(prompt_kernel<D, BF16, KIND>, dim3(grid), dim3(kPrThreads), C::SMEM, stream, a);
 }
 
 template <int D, bool BF16>
-cudaError_t launch_prompt(const PromptArgs& a, bool few, unsigned grid, cudaStream_t stream) {
-  return few ? launch_prompt_as<D, BF16, true>(a, grid, stream) : launch_prompt_as<D, BF16, false>(a, grid, stream);
+cudaError_t launch_prompt(const PromptArgs& a, PromptKind kind, unsigned grid, cudaStream_t stream) {
+  return kind == kPrCut   ? launch_prompt_as<D, BF16, kPrCut>(a, grid, stream)
+         : kind == kPrFew ? launch_prompt_as<D, BF16, kPrFew>(a, grid, stream)
+                          : launch_prompt_as<D, BF16, kPrMany>(a, grid, stream);
+}
+
+// CTAs that run at once in clusters of `parts` CTAs (of a whole number of
+// which a group of SMs has room); < 0: an error.
+template <int D, bool BF16>
+int resident_ctas(unsigned parts) {
+  using C = PromptCfg<D>;
+  if (set_smem_once<prompt_kernel<D, BF16, kPrCut>>(static_cast<int>(C::SMEM)) != cudaSuccess) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(parts);
+  cfg.blockDim = dim3(kPrThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {parts, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, prompt_kernel<D, BF16, kPrCut>, &cfg) != cudaSuccess) return -1;
+  return n * static_cast<int>(parts);
 }
 
 // Rows of `heads` heads, pitch `stride` elements: boxes of 64 values, `box_heads` heads, `box_rows` rows.
@@ -1040,6 +1240,7 @@ uint64_t prompt_wait_limit() {
 struct attn_prompt_plan {
   attn_prompt_desc_t d;
   int device = -1;
+  int resident[3] = {0, 0, 0};  // CTAs that run at once in clusters of 2, 4, 8
   lgt::DeviceStatus* d_status = nullptr;
   uint64_t wait_limit_ns = 0;
 };
@@ -1071,6 +1272,17 @@ gemm_status_t attn_prompt_create(const attn_prompt_desc_t* desc, attn_prompt_pla
     delete p;
     return GEMM_ERR_CUDA;
   }
+  for (int i = 0; i < 3; ++i) {
+    const bool bf16 = d.dtype == GEMM_BF16;
+    p->resident[i] = d.head_dim == 128 ? (bf16 ? lgt::resident_ctas<128, true>(2u << i) : lgt::resident_ctas<128, false>(2u << i))
+                                       : (bf16 ? lgt::resident_ctas<64, true>(2u << i) : lgt::resident_ctas<64, false>(2u << i));
+    if (p->resident[i] < 0) {
+      cudaGetLastError();
+      cudaFree(p->d_status);
+      delete p;
+      return GEMM_ERR_CUDA;
+    }
+  }
   *plan = p;
   return GEMM_OK;
 }
@@ -1094,8 +1306,6 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return GEMM_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) % 4 != 0) return GEMM_ERR_ALIGNMENT;
   const int group = d.q_heads / d.k_heads, tok = lgt::kPrRows / group;
-  // A sequence of n tokens has at most n / 2T + 1 units of 2T, n / T + 1 of T.
-  // (At most: what is past the last unit is found out by the CTAs.)
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -1103,9 +1313,17 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
     return GEMM_ERR_CUDA;
   }
   if (dev != plan->device) return GEMM_ERR_INVALID_ARG;  // (the status word is there)
-  const int64_t wide = (total_q / (2 * tok) + batch) * d.k_heads;
-  const bool few = wide < static_cast<int64_t>(lgt::kPrFill) * sms;
-  const int64_t units = few ? (total_q / tok + batch) * d.k_heads : wide;
+  // Units of `span` tokens, at most: what is past the last one is found out by the CTAs.
+  const int64_t seqs = std::min<int64_t>(batch, total_q);
+  auto units_of = [&](int64_t span) { return (total_q + seqs * (span - 1)) / span * d.k_heads; };
+  const int64_t narrow = units_of(tok), blocks = total_k / lgt::kPrKeys / seqs;
+  int lg = 0;
+  for (int i = 1; i <= 3; ++i)
+    if (narrow << i <= plan->resident[i - 1] && blocks - (blocks >> i) >= lgt::kPrSpare) lg = i;
+  const lgt::PromptKind kind = lg > 0                                                         ? lgt::kPrCut
+                               : units_of(2 * tok) < static_cast<int64_t>(lgt::kPrFill) * sms ? lgt::kPrFew
+                                                                                              : lgt::kPrMany;
+  const int64_t units = kind == lgt::kPrMany ? units_of(2 * tok) : narrow << lg;
   if (total_q > (int64_t{1} << 30) || total_k > (int64_t{1} << 30) || units >= (int64_t{1} << 31))
     return GEMM_ERR_UNSUPPORTED;
   lgt::PromptArgs a;
@@ -1131,6 +1349,7 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
   a.group = group;
   a.tok = tok;
   a.causal = d.causal;
+  a.lg_parts = lg;
   a.div_hk = lgt::magic_encode(static_cast<uint32_t>(d.k_heads));
   a.div_group = lgt::magic_encode(static_cast<uint32_t>(group));
   a.sms = sms;
@@ -1143,8 +1362,8 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(units);
   const cudaError_t e = d.head_dim == 128
-                            ? (bf16 ? lgt::launch_prompt<128, true>(a, few, grid, s) : lgt::launch_prompt<128, false>(a, few, grid, s))
-                            : (bf16 ? lgt::launch_prompt<64, true>(a, few, grid, s) : lgt::launch_prompt<64, false>(a, few, grid, s));
+                            ? (bf16 ? lgt::launch_prompt<128, true>(a, kind, grid, s) : lgt::launch_prompt<128, false>(a, kind, grid, s))
+                            : (bf16 ? lgt::launch_prompt<64, true>(a, kind, grid, s) : lgt::launch_prompt<64, false>(a, kind, grid, s));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;

@@ -247,6 +247,50 @@ def test_prompt_peaked_logits_move_the_reference(m):
     _check_prompt(_run_prompt(m, q, k, v, cu, cu, F16, scale=0.5), q, k, v, cu, cu, F16, True, 0.5)
 
 
+# Few queries before long keys: each unit's keys are cut over a cluster of 2, 4 or 8 CTAs.
+CUT = [([1], [2000], 8, 1, 128, BF16, True), ([1], [4100], 8, 2, 64, F16, True), ([3, 0, 1], [1500, 700, 2600], 12, 4, 64, BF16, True),
+       ([40, 1], [5000, 3], 6, 2, 128, F16, True), ([130], [4200], 1, 1, 128, BF16, False), ([64], [1100], 128, 1, 64, F16, True),
+       ([600, 2], [40, 9000], 2, 2, 64, BF16, True), ([1, 1, 1], [0, 8000, 129], 32, 8, 128, BF16, True), ([33], [1500], 7, 1, 128, F16, False)]
+
+
+@pytest.mark.parametrize("nq,nk,hq,hk,d,dtype,causal", CUT)
+def test_prompt_few_queries_before_long_keys(m, nq, nk, hq, hk, d, dtype, causal):
+    cu_q, cu_k = _cu(nq), _cu(nk)
+    q, k, v = _rand(55, sum(nq), hq, d, dtype=dtype), _rand(56, sum(nk), hk, d, dtype=dtype), _rand(57, sum(nk), hk, d, dtype=dtype)
+    got = _run_prompt(m, q, k, v, cu_q, cu_k, dtype, causal=causal, pad=8)
+    _check_prompt(got, q, k, v, cu_q, cu_k, dtype, causal, None, str((nq, nk)))
+    assert torch.equal(got, _run_prompt(m, q, k, v, cu_q, cu_k, dtype, causal=causal))
+
+
+def test_prompt_cut_keys_hold_what_nobody_else_sees(m):
+    """As for long prompts: infinities and NaN of V reach the queries that see them, across the cuts (each block of
+    the first sequence's 300 keys is another CTA's), those of another sequence nobody."""
+    cu_q, cu_k = _cu([200, 64, 3]), _cu([300, 9000, 2000])
+    q, k, v = _rand(65, 267, 2, 128, dtype=BF16), _rand(66, 11300, 2, 128, dtype=BF16), _rand(67, 11300, 2, 128, dtype=BF16)
+    clean = _run_prompt(m, q, k, v, cu_q, cu_k, BF16).cpu()
+    v[210, 0, 5], v[280, 1, 100], v[290, 1, 100], v[220, 1, 7], v[127, 0, 9], v[128, 0, 10] = (
+        float(x) for x in ("inf", "inf", "-inf", "nan", "-inf", "inf"))
+    v[400, 0, 1] = float("inf")
+    q[264:], k[9300:], v[9300:] = float("nan"), float("inf"), float("nan")
+    got = _run_prompt(m, q, k, v, cu_q, cu_k, BF16).cpu()
+    want = clean.clone()
+    inf, nan = float("inf"), float("nan")
+    want[110:200, 0, 5], want[180:200, 1, 100], want[190:200, 1, 100], want[120:200, 1, 7] = inf, inf, nan, nan
+    want[27:200, 0, 9], want[28:200, 0, 10], want[200:264, 0, 1], want[264:] = -inf, inf, inf, nan
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got[~want.isnan()], want[~want.isnan()])
+
+
+def test_prompt_cut_keys_with_peaked_logits(m):
+    """The parts' references lie far apart, the largest logits in any of them."""
+    size = torch.linspace(0.05, 2.0, 4000)[:, None, None].half()
+    for sizes in (size, size.flip(0)):
+        cu_q, cu_k = _cu([20]), _cu([4000])
+        q, k, v = _rand(58, 20, 4, 64, dtype=F16, scale=2.5), _rand(59, 4000, 1, 64, dtype=F16, scale=2.5), _rand(60, 4000, 1, 64, dtype=F16)
+        k *= sizes
+        _check_prompt(_run_prompt(m, q, k, v, cu_q, cu_k, F16, scale=0.5), q, k, v, cu_q, cu_k, F16, True, 0.5)
+
+
 def test_prompt_repeats_bitwise_on_another_stream(m):
     lens = [300, 17, 555]
     cu, n = torch.from_numpy(_cu(lens)).cuda(), sum(lens)
