@@ -74,8 +74,9 @@ gemm_status_t attn_cache_attend_workspace_size(int32_t q_heads, int32_t k_heads,
  *      is not one of the cache's counts as no keys.
  *   scale > 0; 0 = 1 / sqrt(head_dim).
  * Logits, softmax and sums are fp32; the products take the codes' values as
- * they are and the queries and weights in fp16 (the queries times a power of
- * two), which loses nothing of a bf16 query and holds a weight to 2^-11.
+ * they are and the queries and weights in fp16 (a query's head times a power
+ * of two), which loses of a bf16 query only what is below 2^-25 of its largest
+ * value and holds a weight to 2^-11.
  * The result does not depend on the other sequences of the batch except in
  * the order of fp32 sums. */
 gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void* Q, int64_t q_stride, int32_t q_heads,

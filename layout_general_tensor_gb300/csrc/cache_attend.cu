@@ -11,9 +11,10 @@
 //
 // Work.  A pass is one sequence, key head and group of up to 8 query heads; its
 // units are its blocks of 16 keys and two more for what a pass costs whatever
-// its length (64 ragged sequences: 44 us with one, 39.4 with two to four).  The units of the whole batch, pass after pass,
-// are cut into as many equal runs as there are CTAs, and a CTA's run into one
-// for each warp, so a long sequence among short ones spreads over the GPU and
+// its length (64 ragged sequences: 44 us with one, 39.4 with two to four).  The
+// units of the whole batch, pass after pass, are cut into as many equal runs as
+// there are CTAs, and a CTA's run into one for each warp, so a long sequence
+// among short ones spreads over the GPU and
 // every warp reads about the same number of bytes, without meeting another
 // before the end of its run.  A pass that lies in one warp's run goes straight
 // to the output.  Of the others each warp leaves its unnormalised share (at

@@ -573,6 +573,26 @@ def test_cache_offsets_past_32_bits(m):
     assert np.all(np.abs(_val(out) - want) <= tol)
 
 
+@pytest.mark.parametrize("hk", [1, 16, 80])
+def test_prompt_offsets_past_32_bits(m, hk):
+    """Rows 2^23 values apart, the last ones past 2^32: the result of the same rows side by side, for the units' keys
+    cut over clusters, few units and many.  (An infinity among the last values is fetched by itself.)"""
+    n, d, stride = 1000, 64, 1 << 23
+    big = torch.empty((n - 1) * stride + 4 * hk * d, dtype=torch.float16, device="cuda")
+    far = [big[i * hk * d:].as_strided((n, hk, d), (stride, d, 1)) for i in range(4)]
+    near = [_rand(110 + i, n, hk, d, dtype=F16).cuda() for i in range(3)]
+    near[2][n - 5, hk - 1, 3] = float("inf")
+    near.append(torch.empty_like(near[0]))
+    for x, y in zip(far[:3], near):
+        x.copy_(y)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    op = m.PromptAttention(hk, hk, d, dtype=m.GEMM_F16)
+    op.run(*near[:3], cu, cu, near[3])
+    op.run(*far[:3], cu, cu, far[3])
+    assert op.sync_status() == m.GEMM_OK
+    assert torch.equal(near[3], far[3]) and near[3][n - 5:, hk - 1, 3].isposinf().all()
+
+
 def test_rope_offsets_past_32_bits(m):
     """Rows 2^25 values apart: the last ones start past 2^31 values."""
     t, d, stride = 66, 64, 1 << 25
