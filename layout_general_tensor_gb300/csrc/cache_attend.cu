@@ -4,9 +4,9 @@
 // Bound: memory, the codes of every key and value read once; the arithmetic
 // per byte is small (2 * group multiply-adds), so warp-level matrix
 // instructions on registers carry it and nothing goes through shared memory
-// on the way.  Measured (32 / 8 heads of 128): 1 sequence of 65536 tokens 31.0
-// us, of which the stream takes 20 at 6.7 TB/s, 64 of 1 to 8192 38.9 us (25 at
-// a copy's rate), 64 of 2048 55 us (72 %); 5 of 1 to 200 (12 / 2 heads of 64)
+// on the way.  Measured (32 / 8 heads of 128): 1 sequence of 65536 tokens 30.7
+// us, of which the stream takes 20 at 6.7 TB/s, 64 of 1 to 8192 38.5 us (25 at
+// a copy's rate), 64 of 2048 54.5 us (74 %); 5 of 1 to 200 (12 / 2 heads of 64)
 // 6.1 us, five dependent trips to memory.
 //
 // Work.  A pass is one sequence, key head and group of up to 8 query heads; its
@@ -43,6 +43,7 @@
 // spans fp16 whatever the rows' magnitudes are, and the largest contribution
 // to the result is the one that is held most exactly.  The result is the
 // product's sum times 2^R / l.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -59,7 +60,7 @@ constexpr int kAtThreads = kAtWarps * 32;
 constexpr int kAtHeads = 8;         // query heads of a pass
 constexpr int kAtKeys = 16;         // a unit
 constexpr int kAtPassUnits = 2;     // of a pass besides its keys
-constexpr uint32_t kAtWhole = 4;    // units a warp up to which a pass is not cut among CTAs
+constexpr uint32_t kAtWhole = 4;    // units a warp above an even share up to which passes are not cut among CTAs
 constexpr int kAtMaxBatch = 8192;   // lengths and prefix sums in shared memory
 constexpr uint32_t kAtJoin = 32;    // CTAs' parts joined in one step; their number is at most its square
 constexpr uint32_t kAtNone = 0xffffffffu;
@@ -76,7 +77,8 @@ struct AttendArgs {
   uint32_t pages;
   int32_t max_pages, batch, hk, group, hgroups;  // hgroups: groups of 8 query heads of a key head
   int32_t max_len;
-  MagicDiv div_page;
+  MagicDiv div_page, div_seq;  // by the passes of a sequence
+  uint32_t each, extra;        // passes of a CTA, and how many have one more, where they are not cut
   float cs;  // scale * log2(e)
   int32_t page;
 };
@@ -294,13 +296,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) cache_attend_kernel(const __gri
   };
   uint32_t t0, t1;
   const uint32_t passes = static_cast<uint32_t>(a.batch) * per_seq;
-  if (passes <= gridDim.x && most <= kAtWhole * W) {
-    // few passes, all of them short: each to a CTA of its own, so that no join
-    // goes past a CTA (5 sequences of up to 200 tokens: 8.6 us cut, 6.5 whole)
-    if (blockIdx.x >= passes) return;
-    const uint32_t seq = blockIdx.x / per_seq;
-    t0 = prefix[seq] + (blockIdx.x - seq * per_seq) * units_of(lens[seq]);
-    t1 = t0 + units_of(lens[seq]);
+  const int64_t spare = static_cast<int64_t>(a.each + (a.extra > 0 ? 1u : 0u)) * most - kAtWhole * W;
+  if (spare * gridDim.x <= total) {
+    // Passes that are few and short, or of about the same length: as many whole
+    // ones to a CTA, so that no join goes past it, which takes 4 us.  (Cut and
+    // whole: 5 sequences of up to 200 tokens 8.6 us and 6.5; 32 / 8 heads of 128:
+    // 64 of 100 tokens 13.4 and 9.4, 24 of 200 12.4 and 8.3, 256 of 512 57 and
+    // 53, 38 of 500, 8 / 4 heads, 10.2 both; where a CTA's whole passes are 6
+    // units a warp above an even share, 64 of 2048, 54.5 and 56.1.)
+    if (blockIdx.x >= min(passes, gridDim.x)) return;
+    auto pass_start = [&](uint32_t cta) {
+      const uint32_t pass = cta * a.each + min(cta, a.extra), seq = magic_div(pass, a.div_seq);
+      return pass == passes ? total : prefix[seq] + (pass - seq * per_seq) * units_of(lens[seq]);
+    };
+    t0 = pass_start(blockIdx.x);
+    t1 = pass_start(blockIdx.x + 1);
   } else {
     if (blockIdx.x >= ctas) return;
     t0 = run_start(blockIdx.x);
@@ -759,7 +769,8 @@ extern "C" gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void
   if (batch > lgt::kAtMaxBatch || max_len > (int64_t{1} << 30)) return GEMM_ERR_UNSUPPORTED;
   lgt::AttendPlan p;
   if (!lgt::plan_attend(q_heads, c.k_heads, c.head_dim, batch, &p)) return GEMM_ERR_CUDA;
-  if ((max_len / lgt::kAtKeys + lgt::kAtPassUnits + 1) * batch * c.k_heads * p.hgroups >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t passes = static_cast<int64_t>(batch) * c.k_heads * p.hgroups;
+  if ((max_len / lgt::kAtKeys + lgt::kAtPassUnits + 1) * passes >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
     return GEMM_ERR_WORKSPACE;
   lgt::AttendArgs a;
@@ -784,6 +795,9 @@ extern "C" gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void
   a.hgroups = p.hgroups;
   a.max_len = static_cast<int32_t>(max_len);
   a.div_page = lgt::magic_encode(static_cast<uint32_t>(c.page_size));
+  a.div_seq = lgt::magic_encode(static_cast<uint32_t>(a.hk * a.hgroups));
+  a.each = static_cast<uint32_t>(std::max<int64_t>(passes / p.ctas, 1));
+  a.extra = passes > p.ctas ? static_cast<uint32_t>(passes % p.ctas) : 0u;
   a.cs = (scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(c.head_dim))) * 1.4426950408889634f;
   a.page = c.page_size;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

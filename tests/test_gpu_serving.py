@@ -490,6 +490,17 @@ def test_decode_bad_pages_count_as_no_keys(m):
     assert torch.equal(out[0], want[0]) and not out[1].any()
 
 
+@pytest.mark.parametrize("lens,hq,hk,d,page,dtype", [
+    ([169] * 20 + [0], 16, 8, 128, 48, BF16), ([50] * 100, 4, 4, 64, 16, F16), ([(7 * i) % 60 for i in range(90)], 12, 4, 128, 16, F16),
+    ([257] * 31, 45, 5, 64, 64, BF16)])
+def test_decode_more_short_passes_than_ctas(m, lens, hq, hk, d, page, dtype):
+    """Whole ones to a CTA, one or several."""
+    op, cache, table, q, n, out = _check_decode(m, lens, hq, hk, d, page, dtype)
+    again = torch.empty_like(out)
+    op.run(q, cache, torch.from_numpy(table).cuda(), n, again)
+    assert torch.equal(out, again)
+
+
 def test_decode_repeats_bitwise_and_grows(m):
     op, cache, table, q, n, out = _check_decode(m, [9000, 30, 4000], 8, 2, 128, 64, BF16)
     first, t = out.clone(), torch.from_numpy(table).cuda()
