@@ -17,12 +17,17 @@
 // taken of an angle in [-pi, pi], where the hardware's approximations are
 // within 2^-20.9 absolute, a thousandth of an fp16 rounding.
 //
-// Bound: memory, each value read and written once.  A group takes a chunk of
-// neighbouring heads with two on their way, and computes the sines again only
-// where the token changes; the blocks are one wave of what the registers hold.
-// Measured (16384 tokens, 32 + 8 heads of 128, bf16): 58.7 us, 5.72 TB/s, 84 %
-// of a copy's rate; runs of four values 84.5, chunks for eight blocks an SM 65,
-// one head on its way 84, a ring in shared memory 63.  64 tokens: 2.9 us.
+// Bound: memory, each value read and written once.  A warp takes a chunk of
+// neighbouring heads, its groups every G-th of them (or a run each, where a
+// token has so few heads that the sines would be taken every few steps), two on
+// their way a group; the sines are computed again only where the token changes;
+// the blocks are one wave of what the registers hold.
+// Measured (16384 tokens, 32 + 8 heads of 128, bf16): 55.3 us, 6.07 TB/s, 89 %
+// of a copy's rate (without any arithmetic it takes as long).  A run a group
+// 57.4, with loads that are not kept in L1 and plain stores 58.7; every
+// sixteenth of a block's heads 62; three heads on their way with five blocks 55,
+// but 1000 tokens 7.6 against 6.9; runs of four values 84, one head on its way
+// 84, a ring in shared memory 63.  64 tokens: 2.9 us.
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -37,7 +42,8 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxPairs = 128;  // head_dim 256
-constexpr uint32_t kRopeBlocks = 6;  // blocks an SM the chunks are cut for: what its registers hold (R = 8)
+constexpr uint32_t kRopeBlocks = 6;   // blocks an SM the chunks are cut for: what its registers hold (R = 8)
+constexpr uint32_t kRopeBlocks4 = 9;  // the same for R = 4 (4000 tokens, 40 heads of 96, 40 turned: 18.5 us, with six 24.6)
 constexpr int kRopeDepth = 2;        // heads of a group on their way
 
 struct RopeArgs {
@@ -47,6 +53,7 @@ struct RopeArgs {
   int64_t qs, ks, qos, kos;
   uint32_t items;  // tokens * heads
   uint32_t chunk;  // of a group
+  uint32_t stride;  // between the heads of a group
   MagicDiv div_heads;
   int32_t hq, heads, d, rot;
   float eps, inv_d, magnitude;
@@ -74,9 +81,9 @@ __device__ __forceinline__ Run<R> load_run(const uint16_t* p) {
 template <int R>
 __device__ __forceinline__ void store_run(uint16_t* p, const Run<R>& r) {
   if constexpr (R == 8)
-    st_global_v4(p, r.w[0], r.w[1], r.w[2], r.w[3]);
+    st_stream_v4(p, r.w[0], r.w[1], r.w[2], r.w[3]);
   else
-    st_global_v2(p, r.w[0], r.w[1]);
+    st_stream_v2(p, r.w[0], r.w[1]);
 }
 
 template <int R, bool BF16>
@@ -101,14 +108,15 @@ template <int R, int LG, bool BF16, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   pdl_launch_dependents();
   const int u = threadIdx.x % LG;
-  const uint32_t group = blockIdx.x * (kRopeThreads / LG) + threadIdx.x / LG;
-  const uint32_t first = min(group * a.chunk, a.items), end = min(first + a.chunk, a.items);
+  constexpr uint32_t G = 32 / LG;  // groups of a warp
+  const uint32_t warp = blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32, in_warp = threadIdx.x % 32 / LG;
+  const uint32_t begin = min(warp * G * a.chunk, a.items), stop = min(begin + G * a.chunk, a.items);
+  const uint32_t first = a.stride == 1 ? min(begin + in_warp * a.chunk, stop) : begin + in_warp;
+  const uint32_t end = a.stride == 1 ? min(first + a.chunk, stop) : stop;
   const bool mine = 2 * R * u < a.d;
   const bool turned = 2 * R * u < a.rot;
   const bool norms = a.wq != nullptr || a.wk != nullptr;
   const int o0 = HALF && turned ? R * u : 2 * R * u, o1 = HALF && turned ? a.rot / 2 + R * u : 2 * R * u + R;
-  uint32_t t, h;  // of the head that is loaded next
-  magic_divmod(min(first, a.items - 1u), a.div_heads, t, h);
   auto is_query = [&](uint32_t hh) { return hh < static_cast<uint32_t>(a.hq); };
   pdl_wait();
 
@@ -116,18 +124,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   Run<R> x0[kRopeDepth], x1[kRopeDepth];
   uint32_t lt[kRopeDepth], lh[kRopeDepth];
   auto load = [&](int j, uint32_t item) {
-    lt[j] = t;
-    lh[j] = h;
     if (item < end) {
+      magic_divmod(item, a.div_heads, lt[j], lh[j]);
+      const uint32_t t = lt[j], h = lh[j];
       if (mine) {
         const uint16_t* src = is_query(h) ? a.q + static_cast<int64_t>(t) * a.qs + h * a.d
                                           : a.k + static_cast<int64_t>(t) * a.ks + (h - a.hq) * a.d;
         x0[j] = load_run<R>(src + o0);
         x1[j] = load_run<R>(src + o1);
-      }
-      if (++h == static_cast<uint32_t>(a.heads)) {
-        h = 0;
-        ++t;
       }
     }
   };
@@ -135,7 +139,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (int j = 0; j < kRopeDepth; ++j) {
 #pragma unroll
     for (int i = 0; i < R / 2; ++i) x0[j].w[i] = x1[j].w[i] = 0u;
-    load(j, first + j);
+    lt[j] = lh[j] = 0u;
+    load(j, first + j * a.stride);
   }
 
   float cs[R], sn[R];
@@ -146,13 +151,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (uint32_t step = 0; step < a.chunk; step += kRopeDepth) {
 #pragma unroll
     for (int j = 0; j < kRopeDepth; ++j) {
-      const uint32_t item = first + step + j;
+      const uint32_t item = first + (step + j) * a.stride;
       const uint32_t ct = lt[j], ch = lh[j];
       const bool is_q = is_query(ch);
       float y[2 * R];
       widen_run<R, BF16>(x0[j], y);
       widen_run<R, BF16>(x1[j], y + R);
-      load(j, item + kRopeDepth);
+      load(j, item + kRopeDepth * a.stride);
       if (norms) {
         float ss[2] = {};
 #pragma unroll
@@ -217,8 +222,11 @@ cudaError_t launch_rope(RopeArgs& a, int sms, cudaStream_t stream) {
   constexpr uint32_t groups = kRopeThreads / LG;
   // Chunks that give every SM kRopeBlocks blocks, whole pairs of heads; one
   // head a group where there are fewer than that.
-  const uint32_t most = static_cast<uint32_t>(sms) * kRopeBlocks * groups;
+  const uint32_t most = static_cast<uint32_t>(sms) * (R == 8 ? kRopeBlocks : kRopeBlocks4) * groups;
   a.chunk = (a.items + most - 1u) / most;
+  // (16384 tokens, 8 + 1 heads, 64 of 128 turned: 17.4 us a run a group, 18.8
+  // interleaved; 32 + 8 heads 57.4 and 55.3, 16 + 4 heads of 256 27.8 and 24.4)
+  a.stride = a.heads < 16 ? 1u : 32 / LG;
   const uint32_t per_block = groups * a.chunk, blocks = a.items / per_block + (a.items % per_block ? 1u : 0u);
   return launch_pdl(rope_kernel<R, LG, BF16, HALF>, dim3(blocks), dim3(kRopeThreads), 0, stream, a);
 }
