@@ -35,8 +35,9 @@
 // Work.  A unit is 2T tokens (or T) of a sequence and a key head.  The grid has a
 // block for every unit, the ones with the most keys of a sequence first; a
 // running CTA takes over blocks that have not started (cluster launch
-// control), so that it loads the next unit's tiles and issues their first
-// products while the softmax warps still write the last unit's result.
+// control) shortly before it is done with its own, so that it loads the next
+// unit's tiles and issues their first products while the softmax warps still
+// write the last unit's result.
 //
 // Warps (384 threads): 0-3 softmax of tile 0, 4-7 of tile 1, 8 loads K,
 // 9 issues the products, 11 finds the units and loads Q, 10 loads V (three
@@ -56,8 +57,8 @@
 //
 // Bound: the tensor core, whose S reads all of the shared memory's rate (8 KiB
 // in 64 cycles), and in long runs the power limit.  Measured (bf16, head_dim
-// 128, causal, visible products only): 4 prompts of 4096, 32 / 8 heads, 340 us,
-// 1615 TFLOP/s, 84 % of cuBLAS's burst rate (372 us in long runs); 1 of 16384,
+// 128, causal, visible products only): 4 prompts of 4096, 32 / 8 heads, 334 us,
+// 1646 TFLOP/s, 86 % of cuBLAS's burst rate (372 us in long runs); 1 of 16384,
 // 16 / 2 heads, 620 us, 1773 TFLOP/s, 92 % (tensor pipe 83 % of cycles).  Steps
 // of the latter: products issued by a whole warp, maximum before weights 718;
 // maximum beside weights, halves handed over 680; one issuing thread, waits
@@ -89,6 +90,12 @@ constexpr int kPrRows = 128;   // rows of a tile
 constexpr int kPrKeys = 128;   // keys of a block
 constexpr int kPrTimeout = GEMM_ERR_TIMEOUT;
 constexpr float kPrLazy = 8.0f;
+// Blocks of keys before a unit's end at which the next one is taken: soon
+// enough that its tiles are there when the tensor core is free, and not while
+// another CTA would come to it earlier.  (us, taken at once and so: one prompt of
+// 2048 tokens, 32 / 8 heads of 128, 39.1 and 31.4; 13 ragged ones, 12 / 4 of 64,
+// 23.1 and 20.2; 4 of 4096 338 and 334.  One to six blocks are within 2 %.)
+constexpr int kPrClaim = 4;
 constexpr int kPrFill = 2;     // units an SM below which the kernel for few is taken
 constexpr int kPrParts = 8;    // CTAs of a cluster that may share a unit
 // Blocks of keys, in the mean, that sharing takes from a CTA's walk at least:
@@ -186,8 +193,8 @@ struct PromptCfg {
   static constexpr uint32_t RING_OFF = 2 * TILE;
   static constexpr uint32_t BAR_OFF = RING_OFF + NS * TILE;
   // full[NS], empty[NS], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], v_clean[2][3],
-  // unit_full[2], unit_empty[2], taken, teardown, join_ready[2][4], join_done[2][4]
-  static constexpr int NBARS = 2 * NS + 40;
+  // unit_full[2], unit_empty[2], taken, teardown, join_ready[2][4], join_done[2][4], near_end
+  static constexpr int NBARS = 2 * NS + 41;
   static constexpr uint32_t TAKEN_OFF = BAR_OFF + ((NBARS * 8 + 15) & ~15);  // 16 bytes: a block taken over
   static constexpr uint32_t UNIT_OFF = TAKEN_OFF + 16;                       // two PromptUnit
   static constexpr uint32_t XCH_OFF = UNIT_OFF + 2 * sizeof(PromptUnit);     // {m, l} of both tiles' rows
@@ -525,6 +532,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   const uint32_t teardown = bar0 + 8u * (kB + 23);
   auto join_ready = [&](int t, int q) { return bar0 + 8u * (kB + 24 + t * 4 + q); };
   auto join_done = [&](int t, int q) { return bar0 + 8u * (kB + 32 + t * 4 + q); };
+  const uint32_t near_end = bar0 + 8u * (kB + 40);
   PromptUnit* units = reinterpret_cast<PromptUnit*>(smem + C::UNIT_OFF);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
@@ -551,6 +559,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       mbar_init(join_done(i >> 2, i & 3), 1);
     }
     mbar_init(taken, 1);
+    mbar_init(near_end, 1);
     mbar_init(teardown, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -602,7 +611,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       if (w.tokens < 0) break;
       for (int j = 0; ok && j < w.nb; ++j) {
         if (!(ok = load(0, j, w, &a.tm_k, leader))) break;
+        if (j == max(w.nb - kPrClaim, 0) && lane == 0) mbar_arrive(near_end);
       }
+      if (w.nb == 0 && lane == 0) mbar_arrive(near_end);
       if (lane == 0) mbar_arrive(unit_empty(it & 1));
     }
     if (!ok && lane == 0 && !*abort_flag) prompt_timeout(a, abort_flag, 0);
@@ -864,8 +875,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           ++q_uses[t];
         }
         if (!ok) break;
+        if (KIND == kPrCut) break;  // (a cluster has one unit)
+        if (!(ok = warp_wait(near_end, (it - 1) & 1, limit, abort_flag))) break;
       }
-      if (KIND == kPrCut) break;  // (a cluster has one unit)
+      if (KIND == kPrCut) break;
       // the next one (a CTA is at most one ahead of itself: the second of two
       // places is free when the unit before the last is done)
       if (lane == 0) {
