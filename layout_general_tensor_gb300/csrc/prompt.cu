@@ -63,7 +63,8 @@
 // of the latter: products issued by a whole warp, maximum before weights 718;
 // maximum beside weights, halves handed over 680; one issuing thread, waits
 // ahead 646; constant ring places 619.  Short ones are bound by the walk of a
-// CTA over its keys: 1.35 us a block of 128 for both tiles, 6 us at the ends.
+// CTA over its keys: 1.25 us a block of 128 for both tiles (1 at head_dim 64),
+// 6 us at the ends.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -184,11 +185,19 @@ __device__ __forceinline__ void cut_unit(const PromptArgs& a, PromptUnit& x, int
   x.shift -= x.from;
 }
 
-template <int D>
+template <int D, PromptKind KIND>
 struct PromptCfg {
   static constexpr uint32_t CHUNK = 128u * 128u;      // 64 values of 128 rows
   static constexpr uint32_t TILE = (D / 64) * CHUNK;  // a tile of Q, K or V
-  static constexpr int NS = 4;                        // places: K, V, K, V, two blocks of each
+  // Blocks of K and of V in the ring.  Where a unit's two tiles take every other
+  // block, a place is free for the time of one product only: four of each and
+  // a small loop that issues the products (its instructions are fetched again
+  // each time round) against two and one stretch of code a place, head_dim 64:
+  // 13 ragged prompts 15.4 us and 16.8, single queries 16.5 and 18.0.  The
+  // kernel for many units: 153 us so and 97.7 (8 x 512 tokens after 3000).
+  static constexpr uint32_t TURNS = D == 64 && KIND != kPrMany ? 4 : 2;
+  static constexpr bool UNROLL = TURNS == 2;
+  static constexpr int NS = 2 * static_cast<int>(TURNS);                // its places: K, V, K, V, ...
   static constexpr uint32_t Q_OFF = 0;                // two tiles
   static constexpr uint32_t RING_OFF = 2 * TILE;
   static constexpr uint32_t BAR_OFF = RING_OFF + NS * TILE;
@@ -448,7 +457,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // the order of the keys.
 template <int D, bool BF16, int LG>
 __device__ __forceinline__ void join_parts(const PromptArgs& a, const PromptUnit& w, uint32_t base, uint32_t rank) {
-  using C = PromptCfg<D>;
+  using C = PromptCfg<D, kPrCut>;
   constexpr int P = 1 << LG, kU = kPrParts / P, kShare = D / 4 / P;
   const int items = w.toks[0] * a.group * kShare;
   uint32_t odd = 0;
@@ -507,7 +516,7 @@ __device__ __forceinline__ void join_parts(const PromptArgs& a, const PromptUnit
 
 template <int D, bool BF16, PromptKind KIND>
 __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_constant__ PromptArgs a) {
-  using C = PromptCfg<D>;
+  using C = PromptCfg<D, KIND>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -578,18 +587,23 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
+  // Where P does not lie over S, a tile's next S is issued as soon as the first
+  // half of P says that S has been read, and o_full is of every block.  (8 x 512
+  // tokens after 3000, 32 / 8 heads of 64: 97.7 us, after the product 102.8.)
+  constexpr bool kApart = C::P_COL != 0;
+
   // Every role walks the same list of units; it and every ring and barrier go
   // on from one unit to the next, so each role counts its own uses of them.
   const uint64_t limit = a.wait_limit_ns;
   auto unit_ready = [&](int it) { return warp_wait(unit_full(it & 1), (it >> 1) & 1, limit, abort_flag); };
-  int issued = 0;                 // loads of K (warp 8), of V (warp 10)
+  uint32_t issued = 0;                 // loads of K (warp 8), of V (warp 10)
   int q_uses[2] = {0, 0};         // loads of Q (warp 11)
   int asked = 0;                  // blocks asked for (warp 11)
 
   // Load block j of K (which = 0) or V (1) of unit w into its next place.
   auto load = [&](int which, int j, const PromptUnit& w, const CUtensorMap* map, bool leader) {
-    const int s = 2 * (issued & 1) + which;
-    if (issued >= 2 && !warp_wait(empty(s), ((issued >> 1) - 1) & 1, limit, abort_flag)) return false;
+    const uint32_t s = 2 * (issued % C::TURNS) + which;
+    if (issued >= C::TURNS && !warp_wait(empty(s), (issued / C::TURNS - 1) & 1, limit, abort_flag)) return false;
     if (leader) {
       mbar_arrive_expect_tx(full(s), C::TILE);
 #pragma unroll
@@ -630,9 +644,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         return ok;
       };
       // (this thread is the pace of the CTA: blocks are taken by turns with the
-      // ring's two places for K and for V, so that every address is a constant
-      // in the code of its turn)
-      auto wait_full = [&](int slot, uint32_t block) { return wait(full(slot), (block >> 1) & 1u); };
+      // ring's places for K and for V, and where there are two of each, every
+      // address is a constant in the code of its turn)
+      auto wait_full = [&](int slot, uint32_t block) { return wait(full(slot), block / C::TURNS & 1u); };
       // 16 values of d are 32 bytes further in a 64-value chunk
       const uint64_t q_desc = sw128_desc(base + C::Q_OFF, 16u, 1024u), k_desc = sw128_desc(base + C::RING_OFF, 16u, 1024u);
       const uint64_t v_desc = sw128_desc(base + C::RING_OFF, C::CHUNK, 1024u);
@@ -657,17 +671,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           mma_ts(dst, pa + k * 8, vd + static_cast<uint64_t>(k * 2048u >> 4), idesc_pv, (first && i == 0) ? 0u : 1u);
         }
       };
-      uint32_t p_parity[2] = {0, 0}, q_parity[2] = {0, 0};
+      uint32_t p_parity = 0, q_parity = 0;  // a bit a tile
       uint32_t v_parity = 0;      // of the uses of v_clean
       uint32_t block = 0;         // of the CTA's, counted through
       int nb = 0, mixed = 0, blocks[2] = {0, 0}, it = 0;
       auto first_s = [&](auto turn) {
-        constexpr int ks = 2 * decltype(turn)::value;
+        const int ks = 2 * turn;
         if (!wait_full(ks, block)) return;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (blocks[t] > 0 && wait(q_full(t), q_parity[t])) {
-            q_parity[t] ^= 1u;
+          if (blocks[t] > 0 && wait(q_full(t), q_parity >> t & 1u)) {
+            q_parity ^= 1u << t;
             tc_fence_after();
             issue_s(t, t, ks);
             if (blocks[t] == 1) tc_commit(q_empty(t));
@@ -676,7 +690,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         wait_full(ks + 1, block);
       };
       auto step = [&](auto turn, int j) {
-        constexpr int vs = 2 * decltype(turn)::value + 1, ks = 2 * (1 - decltype(turn)::value);
+        const int vs = 2 * turn + 1, ks = 2 * ((turn + 1) % static_cast<int>(C::TURNS));
         const bool more = j + 1 < nb;
         if (j >= mixed) {
           const int i = (it & 1) * 3 + j - mixed;
@@ -685,32 +699,35 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
+          auto next_s = [&] {
+            if (j + 1 >= blocks[t]) return;
+            issue_s(t, t, ks);
+            if (j + 2 == blocks[t]) tc_commit(q_empty(t));
+          };
           if (j < blocks[t]) {
-            if (!wait(p_full(t, 0), p_parity[t])) return;
+            if (!wait(p_full(t, 0), p_parity >> t & 1u)) return;
             tc_fence_after();
             issue_pv(t, vs, 0, j == 0);
             if (t == 0 && more && !wait_full(ks, block + 1)) return;
-            if (!wait(p_full(t, 1), p_parity[t])) return;
+            if (kApart) next_s();
+            if (!wait(p_full(t, 1), p_parity >> t & 1u)) return;
             tc_fence_after();
             issue_pv(t, vs, 1, false);
-            p_parity[t] ^= 1u;
-            if (j + 1 == blocks[t]) tc_commit(o_full(t));
+            p_parity ^= 1u << t;
+            if (kApart || j + 1 == blocks[t]) tc_commit(o_full(t));
           } else if (t == 0 && more && !wait_full(ks, block + 1)) {
             return;
           }
           if (t == 1) tc_commit(empty(vs));
           if (t == 1 && more && !wait_full(ks + 1, block + 1)) return;
-          if (j + 1 < blocks[t]) {
-            issue_s(t, t, ks);
-            if (j + 2 == blocks[t]) tc_commit(q_empty(t));
-          }
+          if (!kApart) next_s();
         }
         if (more) tc_commit(empty(ks));
       };
       // The same for units whose tiles share their rows: blocks go to the tile
       // of their place in the ring, so the tile is the turn.
       auto first_s_split = [&](auto turn, int j) {
-        constexpr int t = decltype(turn)::value, ks = 2 * t;
+        const int t = turn % 2, ks = 2 * turn;
         if (!wait_full(ks, block + j)) return;
         tc_fence_after();
         issue_s(t, 0, ks);
@@ -718,31 +735,37 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         if (j + 1 == nb) tc_commit(q_empty(0));
       };
       auto step_split = [&](auto turn, int j) {
-        constexpr int t = decltype(turn)::value, ks = 2 * t, vs = ks + 1;
+        const int t = turn % 2, vs = 2 * turn + 1, ks = 2 * ((turn + 2) % static_cast<int>(C::TURNS));
         if (!wait_full(vs, block)) return;
         if (j >= mixed) {
           const int i = (it & 1) * 3 + j - mixed;
           if (!wait(v_clean(i), (v_parity >> i) & 1u)) return;
           v_parity ^= 1u << i;
         }
-        if (!wait(p_full(t, 0), p_parity[t])) return;
+        if (!wait(p_full(t, 0), p_parity >> t & 1u)) return;
         tc_fence_after();
         issue_pv(t, vs, 0, j < 2);
         if (j + 2 < nb && !wait_full(ks, block + 2)) return;
-        if (!wait(p_full(t, 1), p_parity[t])) return;
-        tc_fence_after();
-        issue_pv(t, vs, 1, false);
-        p_parity[t] ^= 1u;
-        if (j + 2 >= nb) tc_commit(o_full(t));
-        tc_commit(empty(vs));
-        if (j + 2 < nb) {
+        auto next_s = [&] {
+          if (j + 2 >= nb) return;
           issue_s(t, 0, ks);
           tc_commit(empty(ks));
           if (j + 3 == nb) tc_commit(q_empty(0));
-        }
+        };
+        if (kApart) next_s();
+        if (!wait(p_full(t, 1), p_parity >> t & 1u)) return;
+        tc_fence_after();
+        issue_pv(t, vs, 1, false);
+        p_parity ^= 1u << t;
+        if (kApart || j + 2 >= nb) tc_commit(o_full(t));
+        tc_commit(empty(vs));
+        if (!kApart) next_s();
       };
+      // (written out: one more lambda around them costs the kernel for many 5 %
+      // at head_dim 64)
       constexpr std::integral_constant<int, 0> even{};
       constexpr std::integral_constant<int, 1> odd{};
+      auto turn_of = [](uint32_t n) { return static_cast<int>(n % C::TURNS); };
       for (; ok; ++it) {
         if (!wait(unit_full(it & 1), (it >> 1) & 1)) break;
         nb = units[it & 1].nb;
@@ -751,30 +774,38 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         blocks[1] = units[it & 1].blocks[1];
         if (units[it & 1].tokens < 0) break;
         if (KIND != kPrMany && units[it & 1].split) {
-          if (nb > 0 && wait(q_full(0), q_parity[0])) {
-            q_parity[0] ^= 1u;
+          if (nb > 0 && wait(q_full(0), q_parity & 1u)) {
+            q_parity ^= 1u;
             for (int j = 0; ok && j < min(nb, 2); ++j) {
-              if ((block + j) & 1u)
+              if constexpr (!C::UNROLL)
+                first_s_split(turn_of(block + j), j);
+              else if ((block + j) & 1u)
                 first_s_split(odd, j);
               else
                 first_s_split(even, j);
             }
           }
           for (int j = 0; ok && j < nb; ++j, ++block) {
-            if (block & 1u)
+            if constexpr (!C::UNROLL)
+              step_split(turn_of(block), j);
+            else if (block & 1u)
               step_split(odd, j);
             else
               step_split(even, j);
           }
         } else {
           if (nb > 0) {
-            if (block & 1u)
+            if constexpr (!C::UNROLL)
+              first_s(turn_of(block));
+            else if (block & 1u)
               first_s(odd);
             else
               first_s(even);
           }
           for (int j = 0; ok && j < nb; ++j, ++block) {
-            if (block & 1u)
+            if constexpr (!C::UNROLL)
+              step(turn_of(block), j);
+            else if (block & 1u)
               step(odd, j);
             else
               step(even, j);
@@ -800,8 +831,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         if (j < w.nb && !(ok = load(1, j, w, &a.tm_v, leader))) break;
         const int jj = j - 1;
         if (jj < w.mixed || jj < 0) continue;
-        const int n = issued - (j < w.nb ? 2 : 1), s = 2 * (n & 1) + 1;
-        if (!(ok = warp_wait(full(s), (n >> 1) & 1, limit, abort_flag))) break;
+        const uint32_t n = issued - (j < w.nb ? 2u : 1u), s = 2 * (n % C::TURNS) + 1;
+        if (!(ok = warp_wait(full(s), n / C::TURNS & 1, limit, abort_flag))) break;
         const uint32_t vb = base + C::RING_OFF + s * C::TILE;
         const int look = max(w.all_see - jj * kPrKeys, 0), clear = min(w.any_sees - jj * kPrKeys, kPrKeys);
         uint32_t odd = 0;
@@ -933,6 +964,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         float2 sum[4];
         uint32_t sv[128], pk[32];
         bool known = j > 0;  // whether there is a reference to go by
+        // (the block before has been added to O, and the second half of its P
+        // read; with P over S that is so once S is there)
+        bool added = !kApart || j == 0;
+        auto wait_added = [&] {
+          if (!added && ok) {
+            ok = warp_wait(o_full(t), (o_uses + j - 1) & 1, limit, abort_flag);
+            tc_fence_after();
+          }
+          added = true;
+          return ok;
+        };
         while (true) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -980,8 +1022,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           if (over) m = mx;
           l *= alpha;
           if (j > 0) {
-            // the product before has completed: this S was issued after it by
-            // the same thread, and its barrier covers all that was issued before
+            // (P over S: the product before has completed, since this S was
+            // issued after it by the same thread, and its barrier covers all
+            // that was issued before)
+            if (!wait_added()) break;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t v[32];
@@ -994,6 +1038,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
             st_tmem_wait();
           }
         }
+        if (!ok) break;
         st_tmem_x32(p_addr, pk);
         st_tmem_wait();
         tc_fence_before();
@@ -1008,6 +1053,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           sum[i & 3] = add2(sum[i & 3], e);
           pk[i] = pack_pair16<BF16>(e.x, e.y);
         }
+        if (!wait_added()) break;
         st_tmem_x32(p_addr + 32u, pk);
         st_tmem_wait();
         tc_fence_before();
@@ -1017,6 +1063,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         l += s4.x + s4.y;
       }
       if (ok && my_blocks > 0) {
+        if (kApart) o_uses += my_blocks - 1;
         ok = warp_wait(o_full(t), o_uses & 1, limit, abort_flag);
         ++o_uses;
       }
@@ -1148,8 +1195,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   if ((warp == 8 || warp == 10) && *abort_flag) {
     // let the loads still in flight land before the CTA exits
     volatile int no_abort = 0;
-    for (int n = issued > 2 ? issued - 2 : 0; n < issued; ++n)
-      mbar_wait_bounded(full(2 * (n & 1) + (warp == 10)), (n >> 1) & 1, limit, &no_abort);
+    for (uint32_t n = issued > C::TURNS ? issued - C::TURNS : 0u; n < issued; ++n)
+      mbar_wait_bounded(full(2 * (n % C::TURNS) + (warp == 10)), n / C::TURNS & 1, limit, &no_abort);
   }
   if (warp == 11 && *abort_flag) {
     volatile int no_abort = 0;
@@ -1187,7 +1234,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
 template <int D, bool BF16, PromptKind KIND>
 cudaError_t launch_prompt_as(const PromptArgs& a, unsigned grid, cudaStream_t stream) {
-  using C = PromptCfg<D>;
+  using C = PromptCfg<D, KIND>;
   const cudaError_t e = set_smem_once<prompt_kernel<D, BF16, KIND>>(static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   if (KIND == kPrCut)
@@ -1206,7 +1253,7 @@ cudaError_t launch_prompt(const PromptArgs& a, PromptKind kind, unsigned grid, c
 // which a group of SMs has room); < 0: an error.
 template <int D, bool BF16>
 int resident_ctas(unsigned parts) {
-  using C = PromptCfg<D>;
+  using C = PromptCfg<D, kPrCut>;
   if (set_smem_once<prompt_kernel<D, BF16, kPrCut>>(static_cast<int>(C::SMEM)) != cudaSuccess) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(parts);

@@ -291,6 +291,42 @@ def test_prompt_cut_keys_with_peaked_logits(m):
         _check_prompt(_run_prompt(m, q, k, v, cu_q, cu_k, F16, scale=0.5), q, k, v, cu_q, cu_k, F16, True, 0.5)
 
 
+# Enough units for two and more on every SM.
+@pytest.mark.parametrize("nq,nk,hq,hk,d,dtype,causal", [
+    ([130, 257, 1, 400], [130, 257, 1, 400], 48, 48, 64, F16, True), ([130, 257, 1, 400], [130, 300, 513, 400], 48, 48, 128, BF16, True),
+    ([300, 700, 33], [300, 1000, 20], 63, 21, 64, BF16, True), ([500, 520, 9], [500, 520, 700], 128, 32, 128, F16, True),
+    ([200, 300], [70, 513], 80, 80, 64, F16, False)])
+def test_prompt_many_units(m, nq, nk, hq, hk, d, dtype, causal):
+    cu_q, cu_k = _cu(nq), _cu(nk)
+    q, k, v = _rand(120, sum(nq), hq, d, dtype=dtype), _rand(121, sum(nk), hk, d, dtype=dtype), _rand(122, sum(nk), hk, d, dtype=dtype)
+    got = _run_prompt(m, q, k, v, cu_q, cu_k, dtype, causal=causal, pad=8)
+    _check_prompt(got, q, k, v, cu_q, cu_k, dtype, causal, None, str((nq, nk)))
+    assert torch.equal(got, _run_prompt(m, q, k, v, cu_q, cu_k, dtype, causal=causal))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_many_units_values_that_are_not_finite(m, d):
+    cu, h = _cu([300]), 160
+    q, k, v = (_rand(125 + i, 300, h, d, dtype=BF16) for i in range(3))
+    clean = _run_prompt(m, q, k, v, cu, cu, BF16).cpu()
+    inf, nan = float("inf"), float("nan")
+    v[210, 0, 5], v[280, 1, 60], v[290, 1, 60], v[220, 159, 7] = inf, inf, -inf, nan
+    got = _run_prompt(m, q, k, v, cu, cu, BF16).cpu()
+    want = clean.clone()
+    want[210:, 0, 5], want[280:, 1, 60], want[290:, 1, 60], want[220:, 159, 7] = inf, inf, nan, nan
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got[~want.isnan()], want[~want.isnan()])
+
+
+@pytest.mark.parametrize("h,d", [(2, 64), (104, 64), (104, 128)])
+def test_prompt_peaked_logits_in_each_kernel(m, h, d):
+    """The reference moves in many blocks: sums that are being added to are multiplied."""
+    cu = _cu([700])
+    q, k, v = _rand(130, 700, h, d, dtype=F16, scale=2.5), _rand(131, 700, h, d, dtype=F16, scale=2.5), _rand(132, 700, h, d, dtype=F16)
+    k *= torch.linspace(0.2, 2.0, 700)[:, None, None].half()
+    _check_prompt(_run_prompt(m, q, k, v, cu, cu, F16, scale=0.5), q, k, v, cu, cu, F16, True, 0.5)
+
+
 def test_prompt_repeats_bitwise_on_another_stream(m):
     lens = [300, 17, 555]
     cu, n = torch.from_numpy(_cu(lens)).cuda(), sum(lens)
