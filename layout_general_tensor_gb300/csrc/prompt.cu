@@ -907,7 +907,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         }
         if (!ok) break;
         if (KIND == kPrCut) break;  // (a cluster has one unit)
-        if (!(ok = warp_wait(near_end, (it - 1) & 1, limit, abort_flag))) break;
+        // (as long as the unit is: 10 us a block of keys besides the limit)
+        if (!(ok = warp_wait(near_end, (it - 1) & 1, limit + static_cast<uint64_t>(w.nb) * 10000u, abort_flag))) break;
       }
       if (KIND == kPrCut) break;
       // the next one (a CTA is at most one ahead of itself: the second of two

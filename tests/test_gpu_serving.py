@@ -327,6 +327,20 @@ def test_prompt_peaked_logits_in_each_kernel(m, h, d):
     _check_prompt(_run_prompt(m, q, k, v, cu, cu, F16, scale=0.5), q, k, v, cu, cu, F16, True, 0.5)
 
 
+@pytest.mark.parametrize("nq,h", [(3, 1), (300, 40)])
+def test_prompt_very_long_keys(m, nq, h):
+    """Logits of size 8 over long keys: the largest weights, wherever they lie, make the result."""
+    n, d = 150000 if h == 1 else 20000, 64
+    cu_q, cu_k = _cu([nq]), _cu([n])
+    q, k, v = _rand(140, nq, h, d, dtype=BF16), _rand(141, n, h, d, dtype=BF16), _rand(142, n, h, d, dtype=BF16)
+    got = _run_prompt(m, q, k, v, cu_q, cu_k, BF16, scale=1.0)
+    pick = [0, 1, nq - 1]  # (rows by themselves: a query sees the keys up to its own place)
+    for i in pick:
+        seen = n - nq + i + 1
+        one, to = np.array([0, 1], dtype=np.int32), np.array([0, seen], dtype=np.int32)
+        _check_prompt(got[i:i + 1], q[i:i + 1], k[:seen], v[:seen], one, to, BF16, True, 1.0, f"row {i}")
+
+
 def test_prompt_repeats_bitwise_on_another_stream(m):
     lens = [300, 17, 555]
     cu, n = torch.from_numpy(_cu(lens)).cuda(), sum(lens)
