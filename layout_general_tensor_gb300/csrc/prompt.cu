@@ -87,17 +87,22 @@ namespace lgt {
 namespace {
 
 constexpr int kPrThreads = 384;  // 168 registers each
-constexpr int kPrRows = 128;   // rows of a tile
-constexpr int kPrKeys = 128;   // keys of a block
+constexpr int kPrRows = 128;     // rows of a tile
+constexpr int kPrKeys = 128;     // keys of a block
 constexpr int kPrTimeout = GEMM_ERR_TIMEOUT;
 constexpr float kPrLazy = 8.0f;
 // Blocks of keys before a unit's end at which the next one is taken: soon
 // enough that its tiles are there when the tensor core is free, and not while
 // another CTA would come to it earlier.  (us, taken at once and so: one prompt of
 // 2048 tokens, 32 / 8 heads of 128, 39.1 and 31.4; 13 ragged ones, 12 / 4 of 64,
-// 23.1 and 20.2; 4 of 4096 338 and 334.  One to six blocks are within 2 %.)
+// 23.1 and 20.2; 4 of 4096 338 and 334.  Between one and six blocks it is the
+// same but for the ragged ones: 20.8 to 19.6.)
 constexpr int kPrClaim = 4;
-constexpr int kPrFill = 2;     // units an SM below which the kernel for few is taken
+// Units an SM below which the kernel for few is taken.  (us with one, two and
+// four: 13 ragged prompts 24.0, 16.7, 16.7; 13 of up to 766 after about 1400, 28 /
+// 4 heads of 64, 50.3, 50.3, 46.7; one of 3431, 32 / 4, 58.5, 58.5, 61.7; one of
+// 4096, 32 / 8 heads of 128, 53.9, 53.9, 56.4.)
+constexpr int kPrFill = 2;
 constexpr int kPrParts = 8;    // CTAs of a cluster that may share a unit
 // Blocks of keys, in the mean, that sharing takes from a CTA's walk at least:
 // the cluster's start and join cost 1.5 us with a row, 2.5 with all, what two
@@ -1088,11 +1093,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           ok = warp_wait(join_ready(t ^ 1, q), joins & 1, limit, abort_flag);
         }
         if (ok) {
+          // (products and sums rounded each by itself, so that it is the same
+          // whichever tile is which: that depends on what the CTA had before)
           const float om = ld_shared_f32(xch + (t ^ 1) * kPrRows * 8), ol = ld_shared_f32(xch + (t ^ 1) * kPrRows * 8 + 4);
           top = fmaxf(m, om);
           const float ref = top == -INFINITY ? 0.0f : top;
           const float g0 = ex2(m - ref), g1 = ex2(om - ref);
-          l = l * g0 + ol * g1;
+          l = __fadd_rn(__fmul_rn(l, g0), __fmul_rn(ol, g1));
           const float inv = KIND == kPrCut ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
           f0 = g0 * inv;
           f1 = g1 * inv;
@@ -1124,8 +1131,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float x = use0 ? __uint_as_float(v[i]) * f0 : 0.0f;
-            v[i] = __float_as_uint(use1 ? fmaf(__uint_as_float(u[i]), f1, x) : x);
+            const float x = use0 ? __fmul_rn(__uint_as_float(v[i]), f0) : 0.0f;
+            v[i] = __float_as_uint(use1 ? __fadd_rn(__fmul_rn(__uint_as_float(u[i]), f1), x) : x);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -1154,14 +1161,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           tc_ld_32x32b_x32(o0 + c, v);
           tc_wait_ld_regs(v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f0);
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), f0));
         }
         if (use1) {
           uint32_t u[32];
           tc_ld_32x32b_x32(o1 + c, u);
           tc_wait_ld_regs(u);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), f1, __uint_as_float(v[i])));
+          for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(u[i]), f1), __uint_as_float(v[i])));
         }
         if (odd && live) {
 #pragma unroll 1

@@ -356,6 +356,20 @@ def test_prompt_repeats_bitwise_on_another_stream(m):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_prompt_repeats_bitwise_whatever_a_cta_had_before(m, d, dtype):
+    """Which units a CTA takes, and so which tile has a unit's first block, differs from run to run."""
+    cu_q, cu_k = torch.from_numpy(_cu([1500, 1500, 995])).cuda(), torch.from_numpy(_cu([1503, 1501, 1000])).cuda()
+    q, k, v = (_rand(150 + i, 3995 if i == 0 else 4004, 8 if i == 0 else 2, d, dtype=dtype).cuda() for i in range(3))
+    op = m.PromptAttention(8, 2, d, dtype=m.GEMM_BF16 if dtype == BF16 else m.GEMM_F16)
+    outs = [torch.empty_like(q) for _ in range(30)]
+    for out in outs:
+        op.run(q, k, v, cu_q, cu_k, out)
+        torch.cuda.synchronize()
+    assert op.sync_status() == m.GEMM_OK
+    assert all(torch.equal(outs[0], out) for out in outs)
+
+
 def test_prompt_refusals(m):
     op = m.PromptAttention(4, 2, 64, dtype=m.GEMM_F16)
     q, k = torch.zeros(5, 4, 64, dtype=torch.float16, device="cuda"), torch.zeros(6, 2, 64, dtype=torch.float16, device="cuda")
