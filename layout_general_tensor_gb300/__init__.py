@@ -635,13 +635,17 @@ class KVCache:
 
 class CacheAttention:
     """Attention of one query a sequence over a KVCache (include/attn_cache.h),
-    with its (zero-filled) device workspace for `batch` sequences; a larger batch
-    waits for the device and makes a larger one.  Runs that may be under way at the same time need objects of their own."""
+    with its (zero-filled) device workspace for `batch` sequences.  A larger batch
+    waits for the device and makes a larger one; the one before is kept as long as
+    the object is, since a captured graph goes on using it.  While a graph is being
+    captured there is no waiting, so a larger batch is refused: make the object for
+    the largest one.  Runs that may be under way at the same time need objects of
+    their own, and a graph needs the object that it was captured from."""
 
     def __init__(self, q_heads, k_heads, head_dim, page_size, dtype=GEMM_BF16, scale=0.0, batch=64):
         self.q_heads, self.k_heads, self.head_dim, self.page_size = q_heads, k_heads, head_dim, page_size
         self.dtype, self.scale, self.code = _torch_dtype(dtype), scale, dtype
-        self.workspace, self.ws_bytes, self.batch = None, 0, 0
+        self.workspace, self.ws_bytes, self.batch, self._earlier = None, 0, 0, []
         self._grow(batch)
 
     def _grow(self, batch):
@@ -649,8 +653,13 @@ class CacheAttention:
         n = ctypes.c_size_t()
         _check(_lib.attn_cache_attend_workspace_size(self.q_heads, self.k_heads, self.head_dim, batch,
                                                      ctypes.byref(n)), "attn_cache_attend_workspace_size")
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError(f"CacheAttention: the workspace is for {self.batch} sequences and cannot be made larger while a "
+                               f"graph is being captured: make the object with batch={batch} before")
         # (the old one may be in use and the new one is used on any stream)
         torch.cuda.synchronize()
+        if self.workspace is not None:
+            self._earlier.append(self.workspace)
         self.workspace = torch.zeros(n.value, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
         self.ws_bytes, self.batch = n.value, batch
@@ -661,7 +670,8 @@ class CacheAttention:
         """q, out: [batch][q_heads][head_dim]; page_table: [batch][pages a sequence] int32; lengths: batch int32."""
         st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)
         if st == -1 and len(q) > self.batch:
-            self._grow(len(q))
+            # (twice as many at least, up to the library's most: what is kept stays a few times the last)
+            self._grow(max(len(q), min(2 * self.batch, 8192)))
             st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)
         if st:
             what, n, dt = "attn_cache_attend", len(q), self.dtype

@@ -1,0 +1,134 @@
+"""How the serving operators are called on the GPU: captured in a graph, with
+workspaces that are shared or grow, by sequences alone and among others, with
+magnitudes at the types' ends, and with lengths that every key's count shows.
+
+The tolerances of results are those of test_gpu_serving.py; where another is
+used, its derivation stands at the test."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from helpers import lib
+
+pytestmark = pytest.mark.gpu
+
+TD = {oracle.F16: torch.float16, oracle.BF16: torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def m():
+    return lib()
+
+
+def _randn(seed, *shape, dtype=torch.float16, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def _filled(m, lens, hk, d, page, seed=0, k=None, v=None, dtype=torch.float16):
+    """A cache of sequences of these lengths in shuffled pages, with its table and lengths."""
+    need = [-(-n // page) for n in lens]
+    order = torch.randperm(sum(need) + 1, generator=torch.Generator().manual_seed(seed)).int().cuda()
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device="cuda")
+    cache, used = m.KVCache.empty(sum(need) + 1, page, hk, d), 0
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = order[used:used + need[b]]
+        used += need[b]
+        at = torch.arange(n, device="cuda")
+        cache.write(k[b] if k else _randn(seed + 2 * b + 1, n, hk, d, dtype=dtype), v[b] if v else _randn(seed + 2 * b + 2, n, hk, d, dtype=dtype),
+                    table[b, at // page] * page + (at % page).int())
+    return cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def _captured(f):
+    """f once outside, then in a graph."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        f()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        f()
+    return g
+
+
+# ------------------------------------------------------------ graphs
+
+def test_graph_of_the_four_operators_replays(m):
+    """All four in one graph, replayed on other inputs in the same buffers: bitwise what the calls give."""
+    t, hq, hk, d, page = 70, 8, 2, 128, 16
+    rope, prompt, decode = m.QKNormRope(hq, hk, d), m.PromptAttention(hq, hk, d), m.CacheAttention(hq, hk, d, page)
+    qkv = torch.empty(t, (hq + 2 * hk) * d, dtype=torch.bfloat16, device="cuda")
+    q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hk * d, hk * d], 1))
+    qr, kr = torch.empty(t, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(t, hk, d, dtype=torch.bfloat16, device="cuda")
+    out, token = torch.empty_like(qr), torch.empty(1, hq, d, dtype=torch.bfloat16, device="cuda")
+    cache, table = m.KVCache.empty(6, page, hk, d), torch.tensor([[4, 1, 5, 0, 2]], dtype=torch.int32, device="cuda")
+    at = torch.arange(t, device="cuda")
+    slots, cu = table[0, at // page] * page + (at % page).int(), torch.tensor([0, t], dtype=torch.int32, device="cuda")
+    n, positions = torch.tensor([t], dtype=torch.int32, device="cuda"), at.int()
+
+    def layer():
+        rope.run(q, k, positions, qr, kr)
+        cache.write(kr, v, slots)
+        prompt.run(qr, kr, v, cu, cu, out)
+        decode.run(qr[t - 1:], cache, table, n, token)
+    qkv.copy_(_randn(1, t, qkv.shape[1]))
+    graph = _captured(layer)
+    for seed in (2, 3):
+        qkv.copy_(_randn(seed, t, qkv.shape[1]))
+        layer()
+        want = out.clone(), token.clone()
+        out.zero_(), token.zero_(), cache.k.zero_(), cache.v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(token, want[1])
+    assert prompt.sync_status() == m.GEMM_OK
+
+
+def test_graph_keeps_its_workspace_when_the_object_grows(m):
+    """The graph's passes cross CTAs, so it goes by the counters in its workspace: what is
+    allocated after the growth must not lie there."""
+    hq, hk, d, page = 8, 2, 128, 64
+    cache, table, n = _filled(m, [20000], hk, d, page)
+    op = m.CacheAttention(hq, hk, d, page, dtype=m.GEMM_F16, batch=1)
+    q, out = _randn(5, 1, hq, d), torch.empty(1, hq, d, dtype=torch.float16, device="cuda")
+    graph = _captured(lambda: op.run(q, cache, table, n, out))
+    want, place, size = out.clone(), op.workspace.data_ptr(), op.ws_bytes
+    few = torch.tensor([100] * 40, dtype=torch.int32, device="cuda")
+    many = torch.empty(40, hq, d, dtype=torch.float16, device="cuda")
+    op.run(q.expand(40, hq, d).contiguous(), cache, table.expand(40, -1).contiguous(), few, many)
+    assert op.batch >= 40 and op.workspace.data_ptr() != place
+    others = [torch.full((size,), 77, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert all(x.data_ptr() >= place + size or x.data_ptr() + size <= place for x in others)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert all((x == 77).all() for x in others)
+
+
+def test_growth_is_refused_while_a_graph_is_captured(m):
+    hq, hk, d, page = 4, 2, 64, 16
+    cache, table, n = _filled(m, [40, 50, 60], hk, d, page)
+    op = m.CacheAttention(hq, hk, d, page, dtype=m.GEMM_F16, batch=1)
+    q, out = _randn(6, 3, hq, d), torch.empty(3, hq, d, dtype=torch.float16, device="cuda")
+    one = torch.empty(1, hq, d, dtype=torch.float16, device="cuda")
+    op.run(q[:1], cache, table[:1], n[:1], one)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    again = torch.empty_like(one)
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="batch=3"):
+            op.run(q, cache, table, n, out)
+        op.run(q[:1], cache, table[:1], n[:1], again)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, one) and op.batch == 1
+    op.run(q, cache, table, n, out)
+    assert op.batch == 3 and torch.equal(out[:1], one)
