@@ -669,7 +669,7 @@ class CacheAttention:
     def run(self, q, cache, page_table, lengths, out, stream=None):
         """q, out: [batch][q_heads][head_dim]; page_table: [batch][pages a sequence] int32; lengths: batch int32."""
         st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)
-        if st == -1 and len(q) > self.batch:
+        if st == -2:
             # (twice as many at least, up to the library's most: what is kept stays a few times the last)
             self._grow(max(len(q), min(2 * self.batch, 8192)))
             st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)

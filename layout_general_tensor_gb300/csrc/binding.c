@@ -7,6 +7,7 @@
  *
  * Each function returns the library's status, or -1 where a tensor is not what
  * the operator takes; the caller, in Python, then says what is wrong with it.
+ * (attend: -2 where everything is, but the workspace is for fewer sequences.)
  * The library's functions come as addresses (setup), so nothing is linked.
  */
 #define PY_SSIZE_T_CLEAN
@@ -180,14 +181,15 @@ static PyObject* py_attend(PyObject* self, PyObject* const* args, Py_ssize_t nar
   if (!cache || cache->k_heads != whole(h, 2) || cache->head_dim != d || cache->page_size != whole(h, 4) ||
       !look_rows(args[2], dtype, -1, hq, d, &q) || !look(args[3], t_int32, 2, &table) || table.dim[0] != q.dim[0] ||
       table.dim[1] > INT32_MAX || !look_vector(args[4], t_int32, q.dim[0], &lengths) ||
-      !look_rows(args[5], dtype, q.dim[0], hq, d, &out) || q.dim[0] > whole(h, 9))
+      !look_rows(args[5], dtype, q.dim[0], hq, d, &out))
     return refused();
-  if (!look_stream(args[6], args[2], &stream)) return NULL;
   if (table.contiguous) {
     table.stride[0] = table.dim[1];
   } else if ((table.dim[1] > 1 && table.stride[1] != 1) || table.stride[0] < table.dim[1]) {
     return refused();
   }
+  if (q.dim[0] > whole(h, 9)) return status(-2);
+  if (!look_stream(args[6], args[2], &stream)) return NULL;
   return status(cache_attend(cache, q.ptr, q.stride[0], (int32_t)hq, table.ptr, table.stride[0], (int32_t)table.dim[1],
                              lengths.ptr, (int32_t)q.dim[0], (float)PyFloat_AsDouble(PyTuple_GET_ITEM(h, 6)),
                              (int32_t)whole(h, 5), out.ptr, out.stride[0], address(h, 7), (size_t)whole(h, 8), stream));

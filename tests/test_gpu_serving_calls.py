@@ -132,3 +132,23 @@ def test_growth_is_refused_while_a_graph_is_captured(m):
     assert torch.equal(again, one) and op.batch == 1
     op.run(q, cache, table, n, out)
     assert op.batch == 3 and torch.equal(out[:1], one)
+
+
+def test_refused_calls_leave_the_workspace(m):
+    hq, hk, d, page, n = 4, 2, 64, 16, 90
+    cache, table, _ = _filled(m, [40], hk, d, page)
+    op = m.CacheAttention(hq, hk, d, page, dtype=m.GEMM_F16, batch=2)
+    place = op.workspace.data_ptr()
+    ok = dict(q=_randn(7, n, hq, d), cache=cache, page_table=table.expand(n, -1).contiguous(), lengths=torch.full((n,), 40, dtype=torch.int32, device="cuda"),
+              out=torch.empty(n, hq, d, dtype=torch.float16, device="cuda"))
+    for bad in (dict(q=ok["q"].bfloat16()), dict(q=ok["q"].cpu()), dict(out=ok["out"][:5]), dict(lengths=ok["lengths"].long()),
+                dict(page_table=ok["page_table"].t().contiguous().t()), dict(cache=m.KVCache.empty(4, 32, hk, d))):
+        with pytest.raises(ValueError):
+            op.run(**{**ok, **bad})
+        assert op.batch == 2 and op.workspace.data_ptr() == place
+    op.run(**ok)
+    assert op.batch == n
+    with pytest.raises(m.GemmError):  # more than the library takes
+        op.run(*(x.expand(8193, *x.shape[1:]).contiguous() if x is not cache else x
+                 for x in (ok["q"][:1], cache, table, ok["lengths"][:1], ok["out"][:1])))
+    assert op.batch == n
