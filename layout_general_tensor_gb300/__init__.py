@@ -454,7 +454,8 @@ def _with_torch():
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
     module.setup(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
                    ("attn_rope_run", "attn_prompt_run", "attn_cache_write", "attn_cache_read", "attn_cache_attend")),
-                 raw_stream, torch.int32, torch.float16, torch.bfloat16)
+                 getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device, raw_stream, torch.int32,
+                 torch.float16, torch.bfloat16)
     _torch, _binding = torch, module
     return torch
 
@@ -464,19 +465,23 @@ def _torch_dtype(dtype):
     return torch.bfloat16 if dtype == GEMM_BF16 else torch.float16
 
 
-def _refuse(what, status, *checks):
+def _refuse(what, status, *checks, kept=()):
     """Raise for a call's status; at -1 the binding refused a tensor: find it
     among checks of (name, tensor, shape, torch type, whether its rows may be
-    strided)."""
+    strided), or in `kept`, pairs of (name, device) of what the object holds."""
     if status != -1:
         _check(status, what)
     for name, t, shape, dtype, rows in checks:
         if not getattr(t, "is_cuda", False):
             raise ValueError(f"{what}: {name} must be a CUDA tensor")
+        kept = (*kept, (name, t.get_device()))
         if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
             raise ValueError(f"{what}: {name} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
         if not rows and not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be contiguous")
+    for name, device in kept:
+        if device != _torch.cuda.current_device():
+            raise ValueError(f"{what}: {name} is on cuda:{device}, the current device is cuda:{_torch.cuda.current_device()}")
     raise ValueError(f"{what}: within a row the values of a tensor must be contiguous, and rows must not overlap")
 
 
@@ -499,7 +504,8 @@ class QKNormRope:
     in one pass over [token][head][head_dim] tensors, which may be slices of
     one projection's output (include/attn_rope.h).  Without weights there is
     no norm.  `frequencies` (rot_dim / 2 radians a position) takes the place
-    of base, factor, context, low_turns and high_turns."""
+    of base, factor, context, low_turns and high_turns.  The tensors of a call
+    are on the current device."""
 
     def __init__(self, q_heads, k_heads, head_dim, rot_dim=None, layout=ATTN_ROPE_HALF, dtype=GEMM_BF16, eps=1e-6,
                  base=10000.0, factor=1.0, context=0.0, low_turns=0.0, high_turns=0.0, magnitude=1.0,
@@ -548,7 +554,8 @@ def attn_prompt_create_status(desc: attn_prompt_desc_t):
 class PromptAttention:
     """Attention over packed sequences of different lengths, causal or not,
     with grouped heads (include/attn_prompt.h), on [row][head][head_dim]
-    tensors and cumulative lengths (batch + 1 int32 on the device)."""
+    tensors and cumulative lengths (batch + 1 int32 on the device).  The tensors
+    of a call are on the current device, the one the object was made on."""
 
     def __init__(self, q_heads, k_heads, head_dim, dtype=GEMM_BF16, causal=True, scale=0.0):
         self.plan = None
@@ -589,13 +596,16 @@ class PromptAttention:
 class KVCache:
     """A paged cache of keys and values in 8 bits (include/attn_cache.h), on
     four uint8 tensors: codes [pages][k_heads][page_size][head_dim] and
-    exponents [pages][k_heads][page_size]."""
+    exponents [pages][k_heads][page_size].  They and the tensors of a call are
+    on the current device."""
 
     def __init__(self, k, v, k_exp, v_exp):
         torch = _torch or _with_torch()
         for name, t in (("k", k), ("v", v), ("k_exp", k_exp), ("v_exp", v_exp)):
             if not getattr(t, "is_cuda", False) or t.dtype != torch.uint8 or not t.is_contiguous():
                 raise ValueError(f"KVCache: {name} must be a contiguous CUDA tensor of uint8")
+            if t.get_device() != k.get_device():
+                raise ValueError(f"KVCache: {name} is on another device than k")
         if k.dim() != 4 or v.shape != k.shape or k_exp.shape != k.shape[:3] or v_exp.shape != k.shape[:3]:
             raise ValueError("KVCache: codes are [pages][k_heads][page_size][head_dim], exponents one dimension less")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
@@ -603,7 +613,7 @@ class KVCache:
         self.c = attn_cache_t(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), self.pages,
                               self.page_size, self.k_heads, self.head_dim)
         self._ref, self.address = ctypes.byref(self.c), ctypes.addressof(self.c)
-        self.handle = (self.address, self.k_heads, self.head_dim)
+        self.handle = (self.address, self.k_heads, self.head_dim, k.get_device())
 
     @classmethod
     def empty(cls, pages, page_size, k_heads, head_dim, device="cuda"):
@@ -630,7 +640,7 @@ class KVCache:
         n = len(k)
         shape = (n, self.k_heads, self.head_dim)
         _refuse(what, st, ("k", k, shape, k.dtype, True), ("v", v, shape, k.dtype, True),
-                ("slots", slots, (n,), _torch.int32, False))
+                ("slots", slots, (n,), _torch.int32, False), kept=(("the cache", self.handle[3]),))
 
 
 class CacheAttention:
@@ -640,7 +650,9 @@ class CacheAttention:
     the object is, since a captured graph goes on using it.  While a graph is being
     captured there is no waiting, so a larger batch is refused: make the object for
     the largest one.  Runs that may be under way at the same time need objects of
-    their own, and a graph needs the object that it was captured from."""
+    their own, and a graph needs the object that it was captured from.  The tensors
+    of a call and the cache are on the current device, the one the object was made
+    on."""
 
     def __init__(self, q_heads, k_heads, head_dim, page_size, dtype=GEMM_BF16, scale=0.0, batch=64):
         self.q_heads, self.k_heads, self.head_dim, self.page_size = q_heads, k_heads, head_dim, page_size
@@ -664,19 +676,20 @@ class CacheAttention:
         torch.cuda.synchronize()
         self.ws_bytes, self.batch = n.value, batch
         self.handle = (self.dtype, self.q_heads, self.k_heads, self.head_dim, self.page_size, self.code, float(self.scale),
-                       self.workspace.data_ptr(), self.ws_bytes, batch)
+                       self.workspace.data_ptr(), self.ws_bytes, batch, self.workspace.get_device())
 
     def run(self, q, cache, page_table, lengths, out, stream=None):
         """q, out: [batch][q_heads][head_dim]; page_table: [batch][pages a sequence] int32; lengths: batch int32."""
-        st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)
+        st = _binding.attend(self.handle, cache.handle, q, page_table, lengths, out, stream)
         if st == -2:
             # (twice as many at least, up to the library's most: what is kept stays a few times the last)
             self._grow(max(len(q), min(2 * self.batch, 8192)))
-            st = _binding.attend(self.handle, cache.address, q, page_table, lengths, out, stream)
+            st = _binding.attend(self.handle, cache.handle, q, page_table, lengths, out, stream)
         if st:
             what, n, dt = "attn_cache_attend", len(q), self.dtype
             if st == -1 and (cache.k_heads, cache.head_dim, cache.page_size) != (self.k_heads, self.head_dim, self.page_size):
                 raise ValueError(f"{what}: the cache has another shape than this was made for")
             shape = (n, self.q_heads, self.head_dim)
             _refuse(what, st, ("q", q, shape, dt, True), ("page_table", page_table, (n, page_table.shape[-1]), _torch.int32, True),
-                    ("lengths", lengths, (n,), _torch.int32, False), ("out", out, shape, dt, True))
+                    ("lengths", lengths, (n,), _torch.int32, False), ("out", out, shape, dt, True),
+                    kept=(("the workspace", self.handle[10]), ("the cache", cache.handle[3])))
