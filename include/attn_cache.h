@@ -44,7 +44,10 @@ typedef struct attn_cache {
  * GEMM_BF16; head h of token t at [t * stride + h * head_dim], strides in
  * elements, 0 = k_heads * head_dim, a multiple of 8) into their slots (int32,
  * device memory).  A token whose slot is negative or past the last page is
- * left out; two tokens of one call with the same slot leave either's rows. */
+ * left out, which is the way to pad a call.  The other slots of a call are
+ * distinct: where two tokens have the same one, what is left in it is
+ * unspecified (codes of one with the exponent of the other, even), and no
+ * other slot is touched. */
 gemm_status_t attn_cache_write(const attn_cache_t* cache, const void* K, int64_t k_stride, const void* V,
                                int64_t v_stride, const int32_t* slots, int64_t tokens, int32_t dtype, void* stream);
 

@@ -623,7 +623,8 @@ class KVCache:
         return cls(*made)
 
     def write(self, k, v, slots, stream=None):
-        """Quantise [token][k_heads][head_dim] keys and values into their slots (int32; negative: left out)."""
+        """Quantise [token][k_heads][head_dim] keys and values into their slots (int32, distinct within a call;
+        negative: left out, which is the way to pad)."""
         st = _binding.cache_write(self.handle, k, v, slots, stream)
         if st:
             self._refuse("attn_cache_write", st, k, v, slots)

@@ -152,3 +152,30 @@ def test_refused_calls_leave_the_workspace(m):
         op.run(*(x.expand(8193, *x.shape[1:]).contiguous() if x is not cache else x
                  for x in (ok["q"][:1], cache, table, ok["lengths"][:1], ok["out"][:1])))
     assert op.batch == n
+
+
+# ------------------------------------------------------------ the cache
+
+def test_cache_pads_with_negative_slots_and_a_doubled_slot_stays_in_its_row(m):
+    """A call padded with negative slots writes what the call without them does; what two tokens with one slot
+    leave there is unspecified, but every other row of the cache is as if they were not there."""
+    hk, d, page, t = 3, 128, 16, 40
+    k, v = _randn(10, t, hk, d), _randn(11, t, hk, d, scale=2.0 ** 6)
+    k[20:] *= 2.0 ** -7  # (rows of other exponents)
+    slots = torch.randperm(4 * page, generator=torch.Generator().manual_seed(0))[:t].int().cuda()
+    plain, padded, doubled = (m.KVCache.empty(4, page, hk, d) for _ in range(3))
+    for c in (plain, padded, doubled):
+        for x in (c.k, c.v, c.k_exp, c.v_exp):
+            x.fill_(9)
+    plain.write(k[: t - 8], v[: t - 8], slots[: t - 8])
+    pad = slots.clone()
+    pad[t - 8:] = -1
+    padded.write(k, v, pad)
+    twice = slots.clone()
+    twice[t - 8:] = slots[3]
+    doubled.write(k, v, twice)
+    for name in ("k", "v", "k_exp", "v_exp"):
+        a, b, c = (getattr(x, name).transpose(1, 2).flatten(0, 1) for x in (plain, padded, doubled))  # [slot][head]...
+        assert torch.equal(a, b)
+        keep = torch.arange(4 * page, device="cuda") != slots[3]
+        assert torch.equal(a[keep], c[keep])
