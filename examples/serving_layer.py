@@ -3,8 +3,10 @@
     x --Gemm--> q, k, v --norm and rotation (in place)--> q, k --+--> 8-bit paged cache
                                                                  +--> attention --Gemm--> out
 
-`prompt` takes the packed tokens of several sequences (their whole prompts, or
-a later piece of them), `token` one new token of each sequence over the cache.
+`prompt` takes the packed whole prompts of several sequences, `token` one new
+token of each sequence over the cache.  (A later piece of a prompt needs the keys
+and values of the tokens before it, at 16 bits and in front of its own, with
+cumulative lengths of the keys of its own; this layer keeps them in the cache alone.)
 Weights and inputs are random.
 
     python examples/serving_layer.py
@@ -57,7 +59,7 @@ class AttentionLayer:
         return q, k, v
 
     def prompt(self, x, positions, slots, cu):
-        """x [tokens][hidden] of packed whole prompts whose cumulative lengths are cu."""
+        """x [tokens][hidden] of packed whole prompts, each from its first token on, whose cumulative lengths are cu."""
         q, k, v = self._heads(x, positions, slots)
         out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
         self.attend.run(q, k, v, cu, cu, out)
