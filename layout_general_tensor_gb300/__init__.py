@@ -445,7 +445,8 @@ def _with_torch():
 
     import torch
     if not os.path.exists(_BINDING_PATH):
-        raise ImportError(f"{_BINDING_PATH} is missing: build it with `python layout_general_tensor_gb300/build.py`")
+        raise ImportError(f"{_BINDING_PATH} is missing: build it with `python layout_general_tensor_gb300/build.py`, "
+                          "with a C compiler and Python's headers (there is no other way to the serving operators)")
     loader = importlib.machinery.ExtensionFileLoader("_binding", _BINDING_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
     loader.exec_module(module)

@@ -2,7 +2,9 @@
 
 Each translation unit compiles in parallel; the shared library links against
 the CUDA runtime only (driver entry points are resolved at run time).  Beside
-it, ``_lib/_binding.so``: the part of the Python binding that is in C.  Run as
+it, ``_lib/_binding.so``: the part of the Python binding that is in C, which
+the serving operators' calls go through and nothing else does.  Where it cannot
+be built (no headers of Python's), the library is built all the same.  Run as
 ``python layout_general_tensor_gb300/build.py`` or call :func:`build` (the
 package itself loads the built library on import, so this file is loaded by
 path).
@@ -37,23 +39,49 @@ def nvcc_path():
     raise RuntimeError("nvcc not found")
 
 
+def _binding_deps():
+    files = [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
+    return [*files, os.path.join(CSRC, "binding.c"), os.path.abspath(__file__)]
+
+
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "binding.c"]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 
 
-def _up_to_date():
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _up_to_date(target, deps):
+    if not os.path.exists(target):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in deps)
+
+
+def _build_binding(nvcc):
+    """The binding's part in C; one that cannot be built is said on stderr and none is left."""
+    include = [os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"), sysconfig.get_paths()["include"], INCLUDE]
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-fPIC", "-shared", *(f"-I{d}" for d in include),
+           os.path.join(CSRC, "binding.c"), "-o", BINDING + ".tmp"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = f"{r.stdout}\n{r.stderr}" if r.returncode != 0 else None
+    except OSError as e:
+        failed = str(e)
+    if failed is None:
+        os.replace(BINDING + ".tmp", BINDING)
+        return
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
+    print(f"binding.c does not compile, so the serving operators have no Python calls:\n{failed}", file=sys.stderr)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if anything changed) and return the library path."""
-    if not force and _up_to_date():
+    binding = force or not _up_to_date(BINDING, _binding_deps())
+    if not force and _up_to_date(LIB, _deps()):
+        if binding:
+            _build_binding(nvcc_path())
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = nvcc_path()
@@ -73,25 +101,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(r.stderr, file=sys.stderr)
         return obj
 
-    def compile_binding():
-        include = [os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"), sysconfig.get_paths()["include"], INCLUDE]
-        cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-fPIC", "-shared", *(f"-I{d}" for d in include),
-               os.path.join(CSRC, "binding.c"), "-o", BINDING + ".tmp"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"binding.c does not compile:\n{r.stdout}\n{r.stderr}")
-
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(compile_binding)
+        bound = ex.submit(_build_binding, nvcc) if binding else None
         objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(BINDING + ".tmp", BINDING)
     os.replace(tmp, LIB)
+    if bound:
+        bound.result()
     return LIB
 
 

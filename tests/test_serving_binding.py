@@ -2,6 +2,7 @@
 import ctypes
 import importlib.machinery
 import importlib.util
+import os
 import shutil
 
 import pytest
@@ -183,3 +184,43 @@ def test_a_cache_is_on_one_device(lib):
         with pytest.raises(ValueError, match="another device"):
             lib.KVCache(k, v, ke, ve)
         x.device = 0
+
+
+@pytest.fixture
+def builder(lib, tmp_path, monkeypatch):
+    """build.py over an output folder of its own and one small source."""
+    path = os.path.join(os.path.dirname(lib.__file__), "build.py")
+    spec = importlib.util.spec_from_file_location("build_under_test", path)
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    monkeypatch.setattr(b, "OUT_DIR", str(tmp_path))
+    for name in ("LIB", "BINDING"):
+        monkeypatch.setattr(b, name, str(tmp_path / os.path.basename(getattr(b, name))))
+    monkeypatch.setattr(b, "SOURCES", ["noalloc.cu"])
+    return b
+
+
+@pytest.mark.parametrize("missing", ["headers", "compiler"])
+def test_the_library_builds_where_the_binding_cannot(builder, monkeypatch, capfd, missing):
+    """Products, the reduction and the dense attention go by ctypes and need neither."""
+    with monkeypatch.context() as without:
+        if missing == "headers":
+            without.setattr(builder.sysconfig, "get_paths", lambda: {"include": "/nowhere"})
+        else:
+            which = shutil.which
+            without.setattr(builder.shutil, "which", lambda x: "/nowhere/gcc" if x == "gcc" else which(x))
+        open(builder.BINDING, "w").close()  # (one from before, of other sources)
+        assert builder.build(force=True) == builder.LIB
+        assert os.path.exists(builder.LIB) and not os.path.exists(builder.BINDING)
+        assert "binding.c does not compile" in capfd.readouterr().err
+    # where it can be built it is, by itself
+    built = os.path.getmtime(builder.LIB)
+    builder.build()
+    assert os.path.exists(builder.BINDING) and os.path.getmtime(builder.LIB) == built
+    assert capfd.readouterr().err == ""
+
+
+def test_a_missing_binding_is_said(lib, monkeypatch):
+    monkeypatch.setattr(lib, "_BINDING_PATH", "/nowhere/_binding.so")
+    with pytest.raises(ImportError, match="headers"):
+        lib._with_torch()
