@@ -11,11 +11,13 @@ built -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libgemm.so")
-_BINDING_PATH = os.path.join(_HERE, "_lib", "_binding.so")
+# (of this interpreter: the part in C goes by the layouts of one)
+_BINDING_PATH = os.path.join(_HERE, "_lib", "_binding" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 GEMM_OK = 0
 GEMM_ERR_INVALID_ARG = 1
@@ -440,7 +442,6 @@ def _with_torch():
     """torch and the binding's part in C (csrc/binding.c), which goes by
     torch's types; both at the first use, the rest does without."""
     global _torch, _binding
-    import importlib.machinery
     import importlib.util
 
     import torch

@@ -2,7 +2,7 @@
 
 Each translation unit compiles in parallel; the shared library links against
 the CUDA runtime only (driver entry points are resolved at run time).  Beside
-it, ``_lib/_binding.so``: the part of the Python binding that is in C, which
+it, ``_lib/_binding.*.so``: the part of the Python binding that is in C, which
 the serving operators' calls go through and nothing else does.  Where it cannot
 be built (no headers of Python's), the library is built all the same.  Run as
 ``python layout_general_tensor_gb300/build.py`` or call :func:`build` (the
@@ -12,6 +12,7 @@ path).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -22,7 +23,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libgemm.so")
-BINDING = os.path.join(OUT_DIR, "_binding.so")
+# (named for the interpreter that it is built for; another one does not find it)
+BINDING = os.path.join(OUT_DIR, "_binding" + importlib.machinery.EXTENSION_SUFFIXES[0])
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "api_int4.cu", "gemm_tc.cu", "gemm_tc_pair.cu", "gemm_int4.cu", "gemm_int4_f8.cu",

@@ -224,3 +224,23 @@ def test_a_missing_binding_is_said(lib, monkeypatch):
     monkeypatch.setattr(lib, "_BINDING_PATH", "/nowhere/_binding.so")
     with pytest.raises(ImportError, match="headers"):
         lib._with_torch()
+
+
+def test_the_binding_is_of_one_interpreter(lib, monkeypatch):
+    """Built and looked for under this interpreter's suffix, so that another one's is missing, not loaded."""
+    import sysconfig
+    here = sysconfig.get_config_var("EXT_SUFFIX")
+    assert sysconfig.get_config_var("SOABI") in here
+    folder = os.path.dirname(lib.__file__)
+
+    def paths():
+        found = []
+        for name, attribute in (("build", "BINDING"), ("__init__", "_BINDING_PATH")):
+            spec = importlib.util.spec_from_file_location(f"read_{name}", os.path.join(folder, f"{name}.py"))
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            found.append(getattr(module, attribute))
+        return found
+    assert paths() == [os.path.join(folder, "_lib", "_binding" + here)] * 2 and os.path.exists(paths()[0])
+    monkeypatch.setattr(importlib.machinery, "EXTENSION_SUFFIXES", [".cpython-399-other.so"])
+    assert paths() == [os.path.join(folder, "_lib", "_binding.cpython-399-other.so")] * 2
