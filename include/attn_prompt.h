@@ -68,6 +68,13 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
  * GEMM_ERR_TIMEOUT. */
 gemm_status_t attn_prompt_sync_status(attn_prompt_plan_t* plan, void* stream);
 
+/* Test aid for failure detection, without a fault: the plan's next run leaves
+ * out the first load of keys of one CTA, so the CTA's waits run out after the
+ * plan's limit (LGT_GEMM_WAIT_LIMIT_MS at attn_prompt_create, 2 s by default).
+ * It winds down -- the copies that it did make land first -- and the run's
+ * status is GEMM_ERR_TIMEOUT; runs after it are normal. */
+gemm_status_t attn_prompt_withhold_load(attn_prompt_plan_t* plan);
+
 gemm_status_t attn_prompt_destroy(attn_prompt_plan_t* plan);
 
 #ifdef __cplusplus

@@ -51,7 +51,8 @@ EXPORTS = (
     "reduce_rows_workspace_size", "reduce_rows_f32",
     "attn_create", "attn_run", "attn_sync_status", "attn_destroy",
     "attn_rope_frequencies", "attn_rope_create", "attn_rope_run", "attn_rope_destroy",
-    "attn_prompt_create", "attn_prompt_run", "attn_prompt_sync_status", "attn_prompt_destroy",
+    "attn_prompt_create", "attn_prompt_run", "attn_prompt_sync_status",
+    "attn_prompt_withhold_load", "attn_prompt_destroy",
     "attn_cache_write", "attn_cache_read", "attn_cache_attend_workspace_size", "attn_cache_attend",
 )
 
@@ -151,6 +152,7 @@ def _load():
         "attn_prompt_create": (ctypes.c_int, [ctypes.POINTER(attn_prompt_desc_t), ctypes.POINTER(P)]),
         "attn_prompt_run": (ctypes.c_int, [P, P, I64, P, I64, P, I64, P, P, I32, I64, I64, P, I64, P]),
         "attn_prompt_sync_status": (ctypes.c_int, [P, P]),
+        "attn_prompt_withhold_load": (ctypes.c_int, [P]),
         "attn_prompt_destroy": (ctypes.c_int, [P]),
         "attn_cache_write": (ctypes.c_int, [ctypes.POINTER(attn_cache_t), P, I64, P, I64, P, I64, I32, P]),
         "attn_cache_read": (ctypes.c_int, [ctypes.POINTER(attn_cache_t), P, I64, P, I64, P, I64, I32, P]),

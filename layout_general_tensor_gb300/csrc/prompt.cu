@@ -90,6 +90,10 @@ constexpr int kPrThreads = 384;  // 168 registers each
 constexpr int kPrRows = 128;     // rows of a tile
 constexpr int kPrKeys = 128;     // keys of a block
 constexpr int kPrTimeout = GEMM_ERR_TIMEOUT;
+// The least time that a CTA which winds down gives its own copies and products
+// in flight, whatever the limit of its waits: what lands after the CTA has left
+// lands in another's shared memory.
+constexpr uint64_t kPrDrainNs = 2000ull * 1000ull * 1000ull;
 constexpr float kPrLazy = 8.0f;
 // Blocks of keys before a unit's end at which the next one is taken: soon
 // enough that its tiles are there when the tensor core is free, and not while
@@ -130,6 +134,7 @@ struct PromptArgs {
   int32_t sms;
   int32_t causal;
   int32_t lg_parts;  // log2 of the CTAs that share a unit
+  int32_t withhold;  // test aid: CTA 0 never makes its first load of K
   MagicDiv div_hk, div_group, div_tok, div_pair;  // by T, by 2T
   float cs;  // scale * log2(e)
   uint32_t idesc_s, idesc_pv;
@@ -605,11 +610,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   int q_uses[2] = {0, 0};         // loads of Q (warp 11)
   int asked = 0;                  // blocks asked for (warp 11)
 
+  auto withheld = [&](int which, uint32_t n) { return a.withhold && blockIdx.x == 0 && which == 0 && n == 0; };
   // Load block j of K (which = 0) or V (1) of unit w into its next place.
   auto load = [&](int which, int j, const PromptUnit& w, const CUtensorMap* map, bool leader) {
     const uint32_t s = 2 * (issued % C::TURNS) + which;
     if (issued >= C::TURNS && !warp_wait(empty(s), (issued / C::TURNS - 1) & 1, limit, abort_flag)) return false;
-    if (leader) {
+    if (leader && !withheld(which, issued)) {
       mbar_arrive_expect_tx(full(s), C::TILE);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
@@ -1201,21 +1207,23 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   // ------------------------------------------------------------ teardown
   __syncthreads();
+  const uint64_t drain = max(limit, kPrDrainNs);
   if ((warp == 8 || warp == 10) && *abort_flag) {
     // let the loads still in flight land before the CTA exits
     volatile int no_abort = 0;
+    const int which = warp == 10;
     for (uint32_t n = issued > C::TURNS ? issued - C::TURNS : 0u; n < issued; ++n)
-      mbar_wait_bounded(full(2 * (n % C::TURNS) + (warp == 10)), n / C::TURNS & 1, limit, &no_abort);
+      if (!withheld(which, n)) mbar_wait_bounded(full(2 * (n % C::TURNS) + which), n / C::TURNS & 1, drain, &no_abort);
   }
   if (warp == 11 && *abort_flag) {
     volatile int no_abort = 0;
     for (int t = 0; t < 2; ++t)
-      if (q_uses[t] > 0) mbar_wait_bounded(q_full(t), (q_uses[t] - 1) & 1, limit, &no_abort);
-    if (asked > 0) mbar_wait_bounded(taken, (asked - 1) & 1, limit, &no_abort);
+      if (q_uses[t] > 0) mbar_wait_bounded(q_full(t), (q_uses[t] - 1) & 1, drain, &no_abort);
+    if (asked > 0) mbar_wait_bounded(taken, (asked - 1) & 1, drain, &no_abort);
   }
   if (warp == 9) {
     volatile int no_abort = 0;
-    mbar_wait_bounded(teardown, 0, limit, &no_abort);
+    mbar_wait_bounded(teardown, 0, drain, &no_abort);
   }
   if constexpr (KIND == kPrCut) {
     // (every thread of the cluster comes here, whether its waits ran out or
@@ -1312,6 +1320,7 @@ struct attn_prompt_plan {
   int resident[3] = {0, 0, 0};  // CTAs that run at once in clusters of 2, 4, 8
   lgt::DeviceStatus* d_status = nullptr;
   uint64_t wait_limit_ns = 0;
+  int withhold_armed = 0;  // attn_prompt_withhold_load: the next run withholds a load (one shot)
 };
 
 extern "C" {
@@ -1419,6 +1428,7 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
   a.tok = tok;
   a.causal = d.causal;
   a.lg_parts = lg;
+  a.withhold = plan->withhold_armed ? __atomic_exchange_n(&plan->withhold_armed, 0, __ATOMIC_ACQ_REL) : 0;
   a.div_hk = lgt::magic_encode(static_cast<uint32_t>(d.k_heads));
   a.div_group = lgt::magic_encode(static_cast<uint32_t>(group));
   a.sms = sms;
@@ -1449,6 +1459,12 @@ gemm_status_t attn_prompt_sync_status(attn_prompt_plan_t* plan, void* stream) {
     if (cudaMemset(plan->d_status, 0, sizeof(st)) != cudaSuccess) return GEMM_ERR_CUDA;
     return static_cast<gemm_status_t>(st.code);
   }
+  return GEMM_OK;
+}
+
+gemm_status_t attn_prompt_withhold_load(attn_prompt_plan_t* plan) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  __atomic_store_n(&plan->withhold_armed, 1, __ATOMIC_RELEASE);
   return GEMM_OK;
 }
 

@@ -179,3 +179,33 @@ def test_cache_pads_with_negative_slots_and_a_doubled_slot_stays_in_its_row(m):
         assert torch.equal(a, b)
         keep = torch.arange(4 * page, device="cuda") != slots[3]
         assert torch.equal(a[keep], c[keep])
+
+
+# ------------------------------------------------------------ a wait that runs out
+
+def _prompt_case(nq, nk, hq, hk, d, dtype):
+    cu_q, cu_k = (torch.tensor([0, *np.cumsum(x)], dtype=torch.int32, device="cuda") for x in (nq, nk))
+    return [_randn(20 + i, n, h, d, dtype=TD[dtype]) for i, (n, h) in enumerate(((sum(nq), hq), (sum(nk), hk), (sum(nk), hk)))] + [cu_q, cu_k]
+
+
+# (the kernels for many units, for few, and for keys cut over clusters of 8 and of 2)
+@pytest.mark.parametrize("nq,nk,hq,hk,d,dtype", [
+    ([200, 300], [700, 513], 110, 110, 64, oracle.F16), ([500, 520, 9], [500, 520, 700], 128, 32, 128, oracle.BF16),
+    ([129, 1, 127, 300], [1290, 1, 700, 300], 2, 2, 128, oracle.F16), ([33, 77], [330, 900], 12, 4, 64, oracle.BF16),
+    ([1], [4100], 8, 2, 64, oracle.F16), ([130], [4200], 1, 1, 128, oracle.BF16), ([130], [4200], 30, 30, 64, oracle.BF16)])
+def test_prompt_withheld_load_times_out_and_the_next_run_is_right(m, monkeypatch, nq, nk, hq, hk, d, dtype):
+    """The waits run out after 20 ms; the status says so once, and the same plan and buffers go on as if nothing had been."""
+    args = _prompt_case(nq, nk, hq, hk, d, dtype)
+    code = m.GEMM_BF16 if dtype == oracle.BF16 else m.GEMM_F16
+    want, out = torch.empty_like(args[0]), torch.empty_like(args[0])
+    m.PromptAttention(hq, hk, d, dtype=code).run(*args, want)
+    monkeypatch.setenv("LGT_GEMM_WAIT_LIMIT_MS", "20")
+    op = m.PromptAttention(hq, hk, d, dtype=code)
+    monkeypatch.delenv("LGT_GEMM_WAIT_LIMIT_MS")
+    for _ in range(2):
+        assert m._lib.attn_prompt_withhold_load(op.plan) == m.GEMM_OK
+        op.run(*args, out)
+        assert op.sync_status() == m.GEMM_ERR_TIMEOUT and op.sync_status() == m.GEMM_OK
+        out.fill_(float("nan"))
+        op.run(*args, out)
+        assert op.sync_status() == m.GEMM_OK and torch.equal(out, want)

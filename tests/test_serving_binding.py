@@ -220,6 +220,13 @@ def test_the_library_builds_where_the_binding_cannot(builder, monkeypatch, capfd
     assert capfd.readouterr().err == ""
 
 
+def test_prompt_calls_without_a_plan(lib):
+    for name in ("attn_prompt_withhold_load", "attn_prompt_sync_status"):
+        args = [None] * len(getattr(lib._lib, name).argtypes)
+        assert getattr(lib._lib, name)(*args) == lib.GEMM_ERR_INVALID_ARG
+    assert lib._lib.attn_prompt_destroy(None) == lib.GEMM_OK
+
+
 def test_a_missing_binding_is_said(lib, monkeypatch):
     monkeypatch.setattr(lib, "_BINDING_PATH", "/nowhere/_binding.so")
     with pytest.raises(ImportError, match="headers"):
