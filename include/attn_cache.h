@@ -60,7 +60,8 @@ gemm_status_t attn_cache_read(const attn_cache_t* cache, const int32_t* slots, i
 /* Bytes of device workspace attn_cache_attend needs on the current device for
  * `batch` sequences of q_heads query heads (at most 8192 sequences).  It must
  * be zero-filled before its first use and every run leaves it usable by the
- * next; concurrent runs need distinct workspaces. */
+ * next, of whatever heads, head_dim, type and batch it is large enough for;
+ * concurrent runs need distinct workspaces. */
 gemm_status_t attn_cache_attend_workspace_size(int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t batch,
                                                size_t* bytes);
 

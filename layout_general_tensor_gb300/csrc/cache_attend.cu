@@ -59,6 +59,7 @@ constexpr int kAtWarps = 16;        // of 128 registers: they fill an SM
 constexpr int kAtThreads = kAtWarps * 32;
 constexpr int kAtHeads = 8;         // query heads of a pass
 constexpr int kAtKeys = 16;         // a unit
+constexpr int kAtMaxDim = 128;
 constexpr int kAtPassUnits = 2;     // of a pass besides its keys
 constexpr uint32_t kAtWhole = 4;    // units a warp above an even share up to which passes are not cut among CTAs
 constexpr int kAtMaxBatch = 8192;   // lengths and prefix sums in shared memory
@@ -701,7 +702,7 @@ struct AttendPlan {
   size_t part_bytes, bytes;
 };
 
-bool plan_attend(int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t batch, AttendPlan* p) {
+bool plan_attend(int32_t q_heads, int32_t k_heads, int32_t batch, AttendPlan* p) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -710,7 +711,9 @@ bool plan_attend(int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t bat
   }
   p->hgroups = (q_heads / k_heads + kAtHeads - 1) / kAtHeads;
   p->ctas = sms;
-  p->part_bytes = static_cast<size_t>(p->ctas) * 2 * kAtHeads * (head_dim + 4) * sizeof(float);
+  // (room for the parts of any head_dim, so that the counters, which every run
+  // leaves zero, are at the same place whatever else a workspace is used for)
+  p->part_bytes = static_cast<size_t>(p->ctas) * 2 * kAtHeads * (kAtMaxDim + 4) * sizeof(float);
   p->bytes = p->part_bytes + (static_cast<size_t>(batch) * k_heads * p->hgroups + 2 * p->ctas) * sizeof(int32_t);
   return true;
 }
@@ -739,7 +742,7 @@ extern "C" gemm_status_t attn_cache_attend_workspace_size(int32_t q_heads, int32
   *bytes = 0;
   if (batch > lgt::kAtMaxBatch) return GEMM_ERR_UNSUPPORTED;
   lgt::AttendPlan p;
-  if (!lgt::plan_attend(q_heads, k_heads, head_dim, batch, &p)) return GEMM_ERR_CUDA;
+  if (!lgt::plan_attend(q_heads, k_heads, batch, &p)) return GEMM_ERR_CUDA;
   *bytes = p.bytes;
   return GEMM_OK;
 }
@@ -768,7 +771,7 @@ extern "C" gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void
   const int64_t max_len = static_cast<int64_t>(max_pages) * c.page_size;
   if (batch > lgt::kAtMaxBatch || max_len > (int64_t{1} << 30)) return GEMM_ERR_UNSUPPORTED;
   lgt::AttendPlan p;
-  if (!lgt::plan_attend(q_heads, c.k_heads, c.head_dim, batch, &p)) return GEMM_ERR_CUDA;
+  if (!lgt::plan_attend(q_heads, c.k_heads, batch, &p)) return GEMM_ERR_CUDA;
   const int64_t passes = static_cast<int64_t>(batch) * c.k_heads * p.hgroups;
   if ((max_len / lgt::kAtKeys + lgt::kAtPassUnits + 1) * passes >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)

@@ -209,3 +209,31 @@ def test_prompt_withheld_load_times_out_and_the_next_run_is_right(m, monkeypatch
         out.fill_(float("nan"))
         op.run(*args, out)
         assert op.sync_status() == m.GEMM_OK and torch.equal(out, want)
+
+
+# ------------------------------------------------------------ attention over the cache
+
+def test_one_workspace_serves_any_shape_in_turn(m):
+    """Shapes whose parts lie over one another's, each with passes that cross CTAs, so that each goes by the counters."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    runs = []
+    for i, (lens, hq, hk, d, dtype) in enumerate([([40000], 8, 2, 64, torch.float16), ([30000, 9000], 8, 1, 128, torch.bfloat16), ([41000], 16, 1, 64, torch.bfloat16),
+                                                  ([20000] * 5, 4, 4, 128, torch.float16), ([900] * 70, 24, 8, 64, torch.float16)]):
+        cache, table, n = _filled(m, lens, hk, d, 64, seed=100 * i)
+        size = ctypes.c_size_t()
+        assert m._lib.attn_cache_attend_workspace_size(hq, hk, d, len(lens), ctypes.byref(size)) == m.GEMM_OK
+        assert sum(-(-x // 16) for x in lens) * hk > 16 * sms  # more than a block of keys for every warp
+        runs.append((cache, table, n, _randn(200 + i, len(lens), hq, d, dtype=dtype), hq, m.GEMM_BF16 if dtype is torch.bfloat16 else m.GEMM_F16, size.value))
+    shared = torch.zeros(max(r[-1] for r in runs), dtype=torch.uint8, device="cuda")
+
+    def run(r, workspace):
+        cache, table, n, q, hq, code, size = r
+        out = torch.full_like(q, float("nan"))
+        st = m._lib.attn_cache_attend(cache._ref, q.data_ptr(), 0, hq, table.data_ptr(), 0, table.shape[1], n.data_ptr(), len(q), 0.0, code, out.data_ptr(), 0,
+                                      workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream().cuda_stream)
+        assert st == m.GEMM_OK
+        return out
+    want = [run(r, torch.zeros(r[-1], dtype=torch.uint8, device="cuda")) for r in runs]
+    assert all(torch.isfinite(x).all() for x in want)
+    for i in [0, 1, 0, 2, 1, 3, 0, 4, 2, 4, 3, 1, 0, 0]:
+        assert torch.equal(run(runs[i], shared), want[i]), i
