@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) cache_attend_kernel(const __gri
 
     // ---- the queries as B fragments: lane (r, c) has head r's values
     // p*64 + c*16 + 4j + {0, 1 | 2, 3} for step (p, j), in fp16 (bf16 ones
-    // times a power of two that brings the head's largest to [1, 2))
+    // times a power of two that brings the head's largest to [1, 4))
     uint32_t qf[KP * 4][2];
     float qscale[2];
     {
@@ -430,8 +430,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) cache_attend_kernel(const __gri
           }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max(static_cast<int>(top), 1) - 127;
-        inv = pow2i(-max(e, -126));
+        // (at most 126: 2^-127 is none of pow2i's)
+        const int e = min(max(static_cast<int>(top), 1) - 127, 126);
+        inv = pow2i(-e);
         mine = a.cs * pow2i(e);
       }
 #pragma unroll

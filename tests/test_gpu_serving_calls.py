@@ -237,3 +237,27 @@ def test_one_workspace_serves_any_shape_in_turn(m):
     assert all(torch.isfinite(x).all() for x in want)
     for i in [0, 1, 0, 2, 1, 3, 0, 4, 2, 4, 3, 1, 0, 0]:
         assert torch.equal(run(runs[i], shared), want[i]), i
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [-126, -20, 120, 126, 127])
+def test_decode_queries_of_any_size(m, d, power):
+    """bf16 queries up to the type's largest and down to its subnormals, over keys and with a scale that bring the
+    logits back to where they were.  Queries are multiples of 2^-6 below 2, so every form of them is exact and
+    all else differs by powers of two: the results are bitwise those of the queries as they were."""
+    hq, hk, n, page = 4, 2, 300, 16
+    q = _randn(30, 1, hq, d, dtype=torch.float64)
+    q = ((q * (127 / q.abs().amax(-1, keepdim=True))).round() / 64).bfloat16()  # the largest of a head in [1, 2)
+    near = m.KVCache.empty(20, page, hk, d)
+    slots, table = torch.arange(n, dtype=torch.int32, device="cuda"), torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    lengths, scale = torch.tensor([n], dtype=torch.int32, device="cuda"), float(np.float32(1 / np.sqrt(d)))
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    near.write(_randn(31, n, hk, d, dtype=torch.bfloat16, scale=2.0), _randn(32, n, hk, d, dtype=torch.bfloat16), slots)
+    m.CacheAttention(hq, hk, d, page, scale=scale).run(q, near, table, lengths, want)
+    # queries times 2^power, keys over 2^shift, the rest in the scale
+    shift = max(min(power, 100), -100)
+    far = m.KVCache(near.k, near.v, (near.k_exp.int() - shift).to(torch.uint8), near.v_exp)
+    big = (q.double() * 2.0 ** power).bfloat16()
+    assert torch.equal(big.double() * 2.0 ** -power, q.double())
+    m.CacheAttention(hq, hk, d, page, scale=scale * 2.0 ** (shift - power)).run(big, far, table, lengths, got)
+    assert torch.equal(got, want) and want.abs().max() > 0.1
