@@ -261,3 +261,30 @@ def test_decode_queries_of_any_size(m, d, power):
     assert torch.equal(big.double() * 2.0 ** -power, q.double())
     m.CacheAttention(hq, hk, d, page, scale=scale * 2.0 ** (shift - power)).run(big, far, table, lengths, got)
     assert torch.equal(got, want) and want.abs().max() > 0.1
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_very_large_keys_under_very_small_queries(m, d):
+    """Logits of size 10 from keys near the type's largest and queries near its smallest, as above bitwise those of
+    keys and queries near 1; and logits of 0 from keys and queries that are both very large."""
+    hq, hk, n, page = 4, 2, 300, 16
+    q = _randn(33, 1, hq, d, dtype=torch.float64)
+    q = ((q * (127 / q.abs().amax(-1, keepdim=True))).round() / 64).bfloat16()
+    near = m.KVCache.empty(20, page, hk, d)
+    slots, table = torch.arange(n, dtype=torch.int32, device="cuda"), torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    lengths, want, got = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.empty_like(q), torch.empty_like(q)
+    near.write(_randn(34, n, hk, d, dtype=torch.bfloat16, scale=0.5), _randn(35, n, hk, d, dtype=torch.bfloat16), slots)
+    op = m.CacheAttention(hq, hk, d, page, scale=1.0)
+    op.run(q, near, table, lengths, want)
+    op.run((q.double() * 2.0 ** -126).bfloat16(), m.KVCache(near.k, near.v, (near.k_exp.int() + 126).to(torch.uint8), near.v_exp), table, lengths, got)
+    assert torch.isfinite(want).all() and torch.equal(got, want)
+    k = torch.zeros(n, hk, d, dtype=torch.bfloat16, device="cuda")
+    k[:, :, 1::2] = 2.0 ** 120
+    q = torch.zeros_like(q)
+    q[:, :, ::2] = 2.0 ** 100
+    v = torch.ones_like(k)
+    v[:, :, 0] = torch.arange(n, device="cuda")[:, None] % 2
+    near.write(k, v, slots)
+    op.run(q, near, table, lengths, got)
+    # (half the keys have the value 1: weights and sums are exact, the one rounding is that of 1 over the sum)
+    assert torch.all(got[:, :, 1:] == 1) and torch.all(got[:, :, 0] == 0.5)
