@@ -56,7 +56,7 @@ gemm_status_t attn_prompt_create(const attn_prompt_desc_t* desc, attn_prompt_pla
  *      that belong to no sequence are left as they are.
  * batch = 0 or total_q = 0 does nothing.  The plan's device must be current.
  * GEMM_ERR_INVALID_ARG, GEMM_ERR_ALIGNMENT, GEMM_ERR_UNSUPPORTED (more than
- * 2^30 rows, or 2^31 or more work units), GEMM_ERR_CUDA (launch failure).  A kernel whose bounded wait ran out
+ * 2^30 rows or 2^20 sequences, or 2^31 or more work units), GEMM_ERR_CUDA (launch failure).  A kernel whose bounded wait ran out
  * records GEMM_ERR_TIMEOUT in the plan's status word
  * (attn_prompt_sync_status); out is then invalid. */
 gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q_stride, const void* K,

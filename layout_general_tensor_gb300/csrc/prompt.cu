@@ -140,6 +140,10 @@ struct PromptArgs {
   uint32_t idesc_s, idesc_pv;
 };
 
+// Sequences of a call: a CTA's way through the cumulative lengths, 0.7 us for 32
+// of them, is far within the limit of its waits.
+constexpr int kPrMaxBatch = 1 << 20;
+
 // What a CTA works on, 2T tokens of one sequence and key head, and what
 // follows from that for its tiles and blocks of keys.
 struct PromptUnit {
@@ -356,14 +360,28 @@ __device__ __forceinline__ int narrow_above(const PromptArgs& a, const PromptSeq
   return static_cast<int>(fminf(2.0f * sum * static_cast<float>(a.hk) / static_cast<float>(a.sms), 1e9f));
 }
 
+// Where in the list of units a warp is: 32 sequences from b0 on, this lane's of
+// them, and the units before them.  Blocks are taken over in their order, so the
+// search for the next unit goes on from here, and a CTA goes through the batch
+// once.  (From the first sequence on for each unit it is the batch squared:
+// 4096 sequences of one token, 4 / 1 heads of 64, 421 us and 97, 16384 5700 and 357.)
+struct PromptPlace {
+  int b0;
+  uint32_t before;
+  PromptSeq seq;
+};
+
 // Unit `u` of the list (sequences in order, each one's last tokens -- the
 // most keys -- first); every lane of the warp returns the same.
-__device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u, int narrow, const PromptSeq& mine) {
+__device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u, int narrow, PromptPlace& at) {
   const int lane = threadIdx.x & 31;
   PromptUnit r{};
-  uint32_t before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const PromptSeq q = b0 == 0 ? mine : seq_at(a, b0 + lane);
+  bool moved = u < at.before;  // (no order of the takeovers is promised)
+  if (moved) at.b0 = 0, at.before = 0u;
+  for (; at.b0 < a.batch; at.b0 += 32) {
+    if (moved) at.seq = seq_at(a, at.b0 + lane);
+    moved = true;
+    const PromptSeq& q = at.seq;
     const bool cut = (q.nk + kPrKeys - 1) / kPrKeys > narrow;
     const int my_span = cut ? a.tok : 2 * a.tok;
     const uint32_t n = magic_div(static_cast<uint32_t>(q.nq + my_span) - 1u, cut ? a.div_tok : a.div_pair);
@@ -374,8 +392,8 @@ __device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u,
       if (lane >= o) x += y;
     }
     const uint32_t all = __shfl_sync(0xffffffffu, x, 31);
-    if (u - before < all) {  // (u >= before)
-      const uint32_t in = u - before;
+    if (u - at.before < all) {  // (u >= before)
+      const uint32_t in = u - at.before;
       const unsigned hit = __ballot_sync(0xffffffffu, x > in);
       const int src = __ffs(hit) - 1;
       auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
@@ -389,7 +407,7 @@ __device__ __forceinline__ PromptUnit find_unit(const PromptArgs& a, uint32_t u,
       r.shift = i0 + r.nk - nq;
       return r;
     }
-    before += all;
+    at.before += all;
   }
   return r;
 }
@@ -877,8 +895,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     // ------------------------------------------------- units, loads of Q
     int64_t block = KIND == kPrCut ? blockIdx.x >> a.lg_parts : blockIdx.x;
     int turn = 0;  // of the next unit's first block at the ring's places
-    const PromptSeq mine = seq_at(a, lane);
-    const int narrow = KIND == kPrFew ? narrow_above(a, mine) : KIND == kPrCut ? -1 : 0x7fffffff;
+    PromptPlace place{0, 0u, seq_at(a, lane)};
+    const int narrow = KIND == kPrFew ? narrow_above(a, place.seq) : KIND == kPrCut ? -1 : 0x7fffffff;
     bool ok = true;
     int it = 0;
     auto publish = [&](const PromptUnit& w) {
@@ -893,7 +911,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     while (ok && block >= 0) {
       uint32_t unit, h;
       magic_divmod(static_cast<uint32_t>(block), a.div_hk, unit, h);
-      PromptUnit w = find_unit(a, unit, narrow, mine);
+      PromptUnit w = find_unit(a, unit, narrow, place);
       if (w.tokens > 0) {  // (blocks past the last unit hold nothing)
         w.h = static_cast<int>(h);
         if (KIND == kPrCut) cut_unit(a, w, static_cast<int>(cluster_ctarank()));
@@ -1402,7 +1420,7 @@ gemm_status_t attn_prompt_run(attn_prompt_plan_t* plan, const void* Q, int64_t q
                                : units_of(2 * tok) < static_cast<int64_t>(lgt::kPrFill) * sms ? lgt::kPrFew
                                                                                               : lgt::kPrMany;
   const int64_t units = kind == lgt::kPrMany ? units_of(2 * tok) : narrow << lg;
-  if (total_q > (int64_t{1} << 30) || total_k > (int64_t{1} << 30) || units >= (int64_t{1} << 31))
+  if (total_q > (int64_t{1} << 30) || total_k > (int64_t{1} << 30) || units >= (int64_t{1} << 31) || batch > lgt::kPrMaxBatch)
     return GEMM_ERR_UNSUPPORTED;
   lgt::PromptArgs a;
   // (no keys: nothing is loaded, any valid address will do)

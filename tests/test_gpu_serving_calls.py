@@ -12,6 +12,7 @@ import torch
 
 import oracle
 from helpers import lib
+from test_gpu_serving import _check_prompt, _run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -308,3 +309,42 @@ def test_decode_sequences_alone_and_among_others(m, hq, hk, d):
         tol = 2.0 ** -10 * out[b].float().abs() + (2.0 ** -11 + lens[b] * 2.0 ** -24) * most
         assert torch.all((alone[b].float() - out[b].float()).abs() <= tol), lens[b]
     assert float((alone != out).float().mean()) <= 0.03
+
+
+# ------------------------------------------------------------ packed attention: many sequences
+
+def _spread(batch, tokens, seed):
+    """`tokens` tokens in runs of 1 to 3 over `batch` sequences, most of which may be empty; the last has some."""
+    rng = np.random.default_rng(seed)
+    n = np.zeros(batch, dtype=np.int64)
+    for b in [batch - 1, *rng.permutation(batch - 1)]:
+        n[b] = min(int(rng.integers(1, 4)), tokens - n.sum())
+    return n
+
+
+# (the kernels for many units, for few, and for keys cut over clusters)
+@pytest.mark.parametrize("batch,tokens,keys,hq,hk,d,dtype", [(3000, 5000, 1, 4, 2, 64, oracle.F16), (700, 1200, 9, 6, 3, 128, oracle.BF16),
+                                                             (3000, 40, 30, 4, 2, 128, oracle.F16), (2000, 2, 4500, 4, 1, 64, oracle.BF16)])
+def test_prompt_many_sequences(m, batch, tokens, keys, hq, hk, d, dtype):
+    """Far more sequences than a warp looks at a time, runs of empty ones among them."""
+    nq = _spread(batch, tokens, batch)
+    nk = nq * keys
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (nq, nk))
+    q, k, v = (_randn(70 + i, int(n), h, d, dtype=TD[dtype]).cpu() for i, (n, h) in enumerate(((nq.sum(), hq), (nk.sum(), hk), (nk.sum(), hk))))
+    got = _run_prompt(m, q, k, v, cu_q, cu_k, dtype)
+    _check_prompt(got, q, k, v, cu_q, cu_k, dtype, what=str((batch, tokens)))
+    assert torch.equal(got, _run_prompt(m, q, k, v, cu_q, cu_k, dtype))
+
+
+def test_prompt_sequences_are_limited(m):
+    x, cu = _randn(75, 8, 2, 64), torch.zeros((1 << 20) + 2, dtype=torch.int32, device="cuda")
+    out = torch.full_like(x, 3.0)
+    op = m.PromptAttention(2, 2, 64, dtype=m.GEMM_F16)
+    with pytest.raises(m.GemmError):
+        op.run(x, x, x, cu, cu, out)
+    cu[-2:] = 8
+    op.run(x, x, x, cu[:-1], cu[:-1], out)  # 2^20: all tokens are the last sequence's
+    want = torch.empty_like(x)
+    few = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    op.run(x, x, x, few, few, want)
+    assert op.sync_status() == m.GEMM_OK and torch.equal(out, want)
