@@ -348,3 +348,105 @@ def test_prompt_sequences_are_limited(m):
     few = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
     op.run(x, x, x, few, few, want)
     assert op.sync_status() == m.GEMM_OK and torch.equal(out, want)
+
+
+# ------------------------------------------------------------ every key counts once
+
+def _marked_values(n, hk, d, dtype):
+    """Values [n][hk][d] that are 1 in one column, another for each run of n / d keys, and 0 elsewhere; and the keys of
+    a run.  Under queries of 0 every visible key has the same weight, exactly, so a result's column is the number of
+    visible keys of its run over that of all: a key left out, or taken twice, of a run of 512 changes it by 2^-9."""
+    run = -(-n // d)
+    v = torch.zeros(n, hk, d, dtype=dtype, device="cuda")
+    at = torch.arange(n, device="cuda")
+    v[at, :, at // run] = 1.0
+    return v, run
+
+
+def _shares(seen, run, d):
+    """What the columns are for rows that see this many keys."""
+    seen = seen.double()[:, None]
+    return (seen - run * torch.arange(d, device="cuda")).clamp(0, run) / seen
+
+
+@pytest.mark.parametrize("lens,hq,hk,d", [
+    ([65536], 16, 1, 128), ([65536], 1, 1, 128), ([60000], 8, 1, 64), ([30000, 7, 20000], 8, 4, 128), ([1000] * 40, 12, 2, 64),
+    ([17 * i + 1 for i in range(200)], 4, 2, 128), ([100] * 300, 2, 1, 64)])
+def test_decode_counts_every_key_once(m, lens, hq, hk, d):
+    """Passes over 1 to 152 CTAs, joined in groups of 32.  Weights and sums are exact, so a result is off by its one
+    rounding and that of the quotient in fp32."""
+    page = 16
+    marked = [_marked_values(n, hk, d, torch.float16) for n in lens]
+    cache, table, n = _filled(m, lens, hk, d, page, v=[x for x, _ in marked])
+    q = torch.zeros(len(lens), hq, d, dtype=torch.float16, device="cuda")
+    out = torch.empty_like(q)
+    m.CacheAttention(hq, hk, d, page, dtype=m.GEMM_F16).run(q, cache, table, n, out)
+    for b, length in enumerate(lens):
+        want = _shares(n[b:b + 1], marked[b][1], d)
+        assert torch.all((out[b].double() - want).abs() <= (2.0 ** -11 + 2.0 ** -20) * want + 2.0 ** -25), (b, length)
+
+
+# (keys cut over clusters of 8, 8, 4 and 2; the kernel for few units, and for many)
+@pytest.mark.parametrize("nq,nk,hq,hk,d,dtype", [
+    ([3], [150000], 1, 1, 64, oracle.BF16), ([1, 20], [32768, 9000], 8, 2, 128, oracle.F16), ([64], [20000], 24, 6, 128, oracle.F16),
+    ([130], [6000], 30, 30, 64, oracle.F16), ([300, 40], [20000, 700], 40, 40, 64, oracle.F16), ([300, 500], [5000, 300], 110, 110, 64, oracle.F16),
+    ([700, 1, 90], [3000, 4000, 90], 128, 32, 128, oracle.F16)])
+def test_prompt_counts_every_key_once(m, nq, nk, hq, hk, d, dtype):
+    """As for the cache: weights of 1 and sums below 2^24 are exact in either type."""
+    op = m.PromptAttention(hq, hk, d, dtype=m.GEMM_BF16 if dtype == oracle.BF16 else m.GEMM_F16)
+    marked = [_marked_values(n, hk, d, TD[dtype]) for n in nk]
+    v = torch.cat([x for x, _ in marked])
+    k, q = _randn(80, *v.shape, dtype=TD[dtype]), torch.zeros(sum(nq), hq, d, dtype=TD[dtype], device="cuda")
+    cu_q, cu_k = (torch.tensor([0, *np.cumsum(x)], dtype=torch.int32, device="cuda") for x in (nq, nk))
+    out = torch.empty_like(q)
+    op.run(q, k, v, cu_q, cu_k, out)
+    assert op.sync_status() == m.GEMM_OK
+    u = 2.0 ** (-8 if dtype == oracle.BF16 else -11)
+    for b, (a, n) in enumerate(zip(nq, nk)):
+        seen = (torch.arange(a, device="cuda") + n - a + 1).clamp(0, n)
+        rows = out[int(cu_q[b]):int(cu_q[b + 1])].double()
+        want = torch.where(seen[:, None] > 0, _shares(seen.clamp(min=1), marked[b][1], d), 0.0)[:, None]
+        assert torch.all((rows - want).abs() <= (u + 2.0 ** -20) * want + 2.0 ** -25), b
+
+
+# ------------------------------------------------------------ the size of errors over long keys
+
+def _rms_of_rounded_weights(weights, v, out, u_w, u):
+    """The rms error of sums of rounded weights times values [n][d], themselves rounded: a rounding is off by u / sqrt 3
+    of its value in the mean square, and roundings are independent.  (At most u, so where one weight is all of a
+    result, sqrt 3 of it.)"""
+    return float(((u_w ** 2 * (weights ** 2 @ v ** 2) + u ** 2 * out ** 2) / 3).mean().sqrt())
+
+
+@pytest.mark.parametrize("scale", [0.125, 1.0])
+def test_prompt_error_over_long_keys_is_that_of_rounded_weights(m, scale):
+    """bf16 weights have fp32's range, so nothing is lost however many keys there are: rms within twice the roundings'."""
+    nq, n, d = 3, 150000, 64
+    q, k, v = (_randn(90 + i, x, 1, d, dtype=torch.bfloat16) for i, x in enumerate((nq, n, n)))
+    cu_q, cu_k, out = torch.tensor([0, nq], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    m.PromptAttention(1, 1, d, scale=scale).run(q, k, v, cu_q, cu_k, out)
+    logits = q[:, 0].double() @ k[:, 0].double().T * scale
+    logits.masked_fill_(torch.triu(torch.ones(nq, n, dtype=torch.bool, device="cuda"), n - nq + 1), -float("inf"))
+    weights = torch.softmax(logits, -1)
+    want = weights @ v[:, 0].double()
+    rms = float((out[:, 0].double() - want).square().mean().sqrt())
+    assert rms <= 2 * _rms_of_rounded_weights(weights, v[:, 0].double(), want, 2.0 ** -8, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("n,hq,hk,d,dtype", [(20000, 8, 8, 64, oracle.F16), (60000, 8, 1, 128, oracle.F16), (60000, 2, 1, 128, oracle.BF16)])
+def test_decode_error_over_long_keys_is_that_of_rounded_weights(m, n, hq, hk, d, dtype):
+    """fp16 weights, the largest contribution's in its middle: those of logits of size 1 all lie above 2^-14 of it."""
+    page = 64
+    cache, table, lengths = _filled(m, [n], hk, d, page, seed=7, dtype=TD[dtype])
+    q, out = _randn(95, 1, hq, d, dtype=TD[dtype]), torch.empty(1, hq, d, dtype=TD[dtype], device="cuda")
+    m.CacheAttention(hq, hk, d, page, dtype=m.GEMM_BF16 if dtype == oracle.BF16 else m.GEMM_F16).run(q, cache, table, lengths, out)
+    at = torch.arange(n, device="cuda")
+    slots = table[0, at // page] * page + (at % page).int()
+    k, v = (torch.empty(n, hk, d, dtype=TD[dtype], device="cuda") for _ in range(2))
+    cache.read(slots, k, v)  # (exact: the codes' values of rows of this size are values of either type)
+    for h in range(hq):
+        kv = h // (hq // hk)
+        weights = torch.softmax(q[:, h].double() @ k[:, kv].double().T / d ** 0.5, -1)
+        want = weights @ v[:, kv].double()
+        rms = float((out[:, h].double() - want).square().mean().sqrt())
+        assert rms <= 2 * _rms_of_rounded_weights(weights, v[:, kv].double(), want, 2.0 ** -11, 2.0 ** (-8 if dtype == oracle.BF16 else -11)), h
