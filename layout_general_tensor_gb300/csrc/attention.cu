@@ -448,15 +448,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
   if (*abort_flag && warp == 0 && lane == 0) {
     // let the loads still in flight land before the CTA exits
     volatile int no_abort = 0;
-    if (q_issued) mbar_wait_bounded(q_full, 0, a.wait_limit_ns, &no_abort);
+    if (q_issued) mbar_wait_bounded(q_full, 0, drain_ns(a.wait_limit_ns), &no_abort);
     for (int j = k_issued > C::NSK ? k_issued - C::NSK : 0; j < k_issued; ++j)
-      mbar_wait_bounded(k_full(j % C::NSK), (j / C::NSK) & 1, a.wait_limit_ns, &no_abort);
+      mbar_wait_bounded(k_full(j % C::NSK), (j / C::NSK) & 1, drain_ns(a.wait_limit_ns), &no_abort);
     for (int j = v_issued > C::NSV ? v_issued - C::NSV : 0; j < v_issued; ++j)
-      mbar_wait_bounded(v_full(j % C::NSV), (j / C::NSV) & 1, a.wait_limit_ns, &no_abort);
+      mbar_wait_bounded(v_full(j % C::NSV), (j / C::NSV) & 1, drain_ns(a.wait_limit_ns), &no_abort);
   }
   if (warp == 1 && lane == 0) {
     volatile int no_abort = 0;
-    mbar_wait_bounded(teardown, 0, a.wait_limit_ns, &no_abort);
+    mbar_wait_bounded(teardown, 0, drain_ns(a.wait_limit_ns), &no_abort);
   }
   tc_fence_before();
   __syncthreads();

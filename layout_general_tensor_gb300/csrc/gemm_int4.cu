@@ -667,15 +667,15 @@ __global__ void __launch_bounds__(kThreads4, 1) int4_gemm_kernel(const __grid_co
     // freeing it), so only each ring's last round of uses can be pending.
     volatile int no_abort = 0;
     for (int c = w_issued > C::WST ? w_issued - C::WST : 0; c < w_issued; ++c)
-      mbar_wait_bounded(full_w(c % C::WST), (c / C::WST) & 1, a.wait_limit_ns, &no_abort);
+      mbar_wait_bounded(full_w(c % C::WST), (c / C::WST) & 1, drain_ns(a.wait_limit_ns), &no_abort);
     for (int c = x_issued > C::XST ? x_issued - C::XST : 0; c < x_issued; ++c)
-      mbar_wait_bounded(full_x(c % C::XST), (c / C::XST) & 1, a.wait_limit_ns, &no_abort);
+      mbar_wait_bounded(full_x(c % C::XST), (c / C::XST) & 1, drain_ns(a.wait_limit_ns), &no_abort);
   }
   // every issuer's MMAs completed before the TMEM is released
   if (warp >= kIssWarp0 && warp < kIssWarp0 + NI && lane == 0) tc_commit(teardown_bar);
   if (warp == kIssWarp0 && lane == 0) {
     volatile int no_abort = 0;
-    mbar_wait_bounded(teardown_bar, 0, a.wait_limit_ns, &no_abort);
+    mbar_wait_bounded(teardown_bar, 0, drain_ns(a.wait_limit_ns), &no_abort);
   }
   tc_fence_before();
   __syncthreads();

@@ -671,17 +671,17 @@ __global__ void __launch_bounds__(kF8Threads, 1) int4f8_gemm_kernel(const __grid
     volatile int no_abort = 0;
     if (warp == 0) {
       for (int c = w_issued > kF8WST ? w_issued - kF8WST : 0; c < w_issued; ++c)
-        mbar_wait_bounded(full_w(c % kF8WST), (c / kF8WST) & 1, a.wait_limit_ns, &no_abort);
+        mbar_wait_bounded(full_w(c % kF8WST), (c / kF8WST) & 1, drain_ns(a.wait_limit_ns), &no_abort);
     } else {
       for (int c = x_issued > kF8XST ? x_issued - kF8XST : 0; c < x_issued; ++c)
-        mbar_wait_bounded(full_x(c % kF8XST), (c / kF8XST) & 1, a.wait_limit_ns, &no_abort);
+        mbar_wait_bounded(full_x(c % kF8XST), (c / kF8XST) & 1, drain_ns(a.wait_limit_ns), &no_abort);
     }
   }
   // every issuer's MMAs completed before the TMEM is released
   if (warp >= kF8IssWarp0 && warp < kF8IssWarp0 + kF8Issuers && lane == 0) tc_commit(teardown_bar);
   if (warp == kF8IssWarp0 && lane == 0) {
     volatile int no_abort = 0;
-    mbar_wait_bounded(teardown_bar, 0, a.wait_limit_ns, &no_abort);
+    mbar_wait_bounded(teardown_bar, 0, drain_ns(a.wait_limit_ns), &no_abort);
   }
   tc_fence_before();
   __syncthreads();

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
         // copies still in flight land before the CTA exits
         volatile int no_abort = 0;
         for (int it = stg_done; it < stg_issued; ++it)
-          mbar_wait_bounded(stg_full(it % rl_nstg), (it / rl_nstg) & 1, a.wait_limit_ns, &no_abort);
+          mbar_wait_bounded(stg_full(it % rl_nstg), (it / rl_nstg) & 1, drain_ns(a.wait_limit_ns), &no_abort);
       }
     } else if (a.tail_tiles) {
       // ---------------------------------------------------------- stream-K fixup
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
       const int consumed = *consumed_slot;
       for (int it = consumed; it < issued; ++it) {
         if (a.withhold && blockIdx.x == 0 && it == 0) continue;  // the withheld stage has no copy in flight
-        mbar_wait_bounded(full_bar(it % nst), (it / nst) & 1, a.wait_limit_ns, &no_abort);
+        mbar_wait_bounded(full_bar(it % nst), (it / nst) & 1, drain_ns(a.wait_limit_ns), &no_abort);
       }
 
     }
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
     // Wait until every MMA this CTA issued has completed.
     volatile int no_abort = 0;
     tc_commit(teardown_bar);
-    mbar_wait_bounded(teardown_bar, 0, a.wait_limit_ns, &no_abort);
+    mbar_wait_bounded(teardown_bar, 0, drain_ns(a.wait_limit_ns), &no_abort);
   }
   tc_fence_before();
   __syncthreads();

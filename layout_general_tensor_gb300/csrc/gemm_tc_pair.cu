@@ -317,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // copies still in flight land before the CTA exits
         volatile int no_abort = 0;
         for (int it = stg_done; it < stg_issued; ++it)
-          mbar_wait_bounded(stg_full(it % rl_nstg), (it / rl_nstg) & 1, a.wait_limit_ns, &no_abort);
+          mbar_wait_bounded(stg_full(it % rl_nstg), (it / rl_nstg) & 1, drain_ns(a.wait_limit_ns), &no_abort);
       }
     } else if (a.tail_tiles) {
       // ---------------------------------------------------------- stream-K fixup
@@ -353,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Wait until every MMA of the pair has completed.
     volatile int no_abort = 0;
     tc_commit_pair_mc(teardown_bar, 0x1);
-    mbar_wait_bounded(teardown_bar, 0, a.wait_limit_ns, &no_abort);
+    mbar_wait_bounded(teardown_bar, 0, drain_ns(a.wait_limit_ns), &no_abort);
   }
   tc_fence_before();
   __syncthreads();

@@ -90,10 +90,6 @@ constexpr int kPrThreads = 384;  // 168 registers each
 constexpr int kPrRows = 128;     // rows of a tile
 constexpr int kPrKeys = 128;     // keys of a block
 constexpr int kPrTimeout = GEMM_ERR_TIMEOUT;
-// The least time that a CTA which winds down gives its own copies and products
-// in flight, whatever the limit of its waits: what lands after the CTA has left
-// lands in another's shared memory.
-constexpr uint64_t kPrDrainNs = 2000ull * 1000ull * 1000ull;
 constexpr float kPrLazy = 8.0f;
 // Blocks of keys before a unit's end at which the next one is taken: soon
 // enough that its tiles are there when the tensor core is free, and not while
@@ -1225,7 +1221,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   // ------------------------------------------------------------ teardown
   __syncthreads();
-  const uint64_t drain = max(limit, kPrDrainNs);
+  const uint64_t drain = drain_ns(limit);
   if ((warp == 8 || warp == 10) && *abort_flag) {
     // let the loads still in flight land before the CTA exits
     volatile int no_abort = 0;

@@ -164,6 +164,14 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The limit of the waits of a CTA that winds down, on its own copies and
+// products in flight: two seconds at least, whatever the limit of its other
+// waits.  What lands after the CTA has left lands in another's memory.
+__device__ __forceinline__ uint64_t drain_ns(uint64_t limit_ns) {
+  constexpr uint64_t kLeast = 2000ull * 1000ull * 1000ull;
+  return limit_ns > kLeast ? limit_ns : kLeast;
+}
+
 // ---------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0,
