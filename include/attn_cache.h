@@ -81,11 +81,8 @@ gemm_status_t attn_cache_attend_workspace_size(int32_t q_heads, int32_t k_heads,
  * they are and the queries and weights in fp16 (a query's head times a power
  * of two), which loses of a bf16 query only what is below 2^-25 of its largest
  * value and holds a weight to 2^-11.
- * A result depends on the other sequences of the batch in the order of its
- * fp32 sums, in the last fp16 bit of the rare weight that this brings across a
- * rounding boundary, and in weights below 2^-14 of the largest contribution,
- * which are held to 2^-24 of it.  So it is not bitwise the same in another
- * batch; in the same one it is. */
+ * The result does not depend on the other sequences of the batch except in
+ * the order of fp32 sums. */
 gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void* Q, int64_t q_stride, int32_t q_heads,
                                 const int32_t* page_table, int64_t table_stride, int32_t max_pages,
                                 const int32_t* lengths, int32_t batch, float scale, int32_t dtype, void* out,

@@ -38,14 +38,11 @@
 // e4m3 codes widen to fp16 exactly.  The keys' powers of two multiply the
 // logits; the values' multiply the weights: with t the logit in log2 units
 // and e the value's power, the sum l takes p = 2^(t - m) and the product
-// w = 2^(t - m + e - R), an R of its own; m and R are whole numbers, and are
-// moved only when something exceeds them by 2^8.  So w spans fp16 whatever the
-// rows' magnitudes are, and the largest contribution to the result is the one
-// that is held most exactly.  The result is the product's sum times 2^R / l.
-// Where a pass is cut, and so what m and R a weight goes by, depends on the
-// rest of the batch; as whole numbers they change a weight by a power of two,
-// so it rounds to the same significand in fp16 (of a sequence's values 0 to 0.3 %
-// come out other alone than in a batch; with m a logit itself up to a third).
+// w = 2^(t - m + e - R), an integer R of its own so that w is p times a power
+// of two; m and R are moved only when something exceeds them by 2^8.  So w
+// spans fp16 whatever the rows' magnitudes are, and the largest contribution
+// to the result is the one that is held most exactly.  The result is the
+// product's sum times 2^R / l.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -524,14 +521,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) cache_attend_kernel(const __gri
           for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(s[u][e], s[u][2 + e]));
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
-          const float mn = fmaxf(m[e], ceilf(x)), ref = mn == -INFINITY ? 0.0f : mn;
+          const float mn = fmaxf(m[e], x), ref = mn == -INFINITY ? 0.0f : mn;
 #pragma unroll
           for (int u = 0; u < U; ++u) y = fmaxf(y, fmaxf(s[u][e] - ref + ve[u][0], s[u][2 + e] - ref + ve[u][1]));
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, sh));
           const float moved = m[e] == -INFINITY ? -INFINITY : m[e] - ref;  // <= 0
           const float old = m[e] == -INFINITY ? -INFINITY : R[e] + moved;  // R against the new m
-          const float Rn = fmaxf(old, ceilf(y));
+          const float Rn = fmaxf(rintf(old), ceilf(y));
           const float fl = ex2f(moved), fo = m[e] == -INFINITY ? 0.0f : ex2f(old - Rn);
           l[e] *= fl;
           m[e] = mn;
