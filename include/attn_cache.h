@@ -81,8 +81,12 @@ gemm_status_t attn_cache_attend_workspace_size(int32_t q_heads, int32_t k_heads,
  * they are and the queries and weights in fp16 (a query's head times a power
  * of two), which loses of a bf16 query only what is below 2^-25 of its largest
  * value and holds a weight to 2^-11.
- * The result does not depend on the other sequences of the batch except in
- * the order of fp32 sums. */
+ * The other sequences of the batch decide where a sequence's keys are cut into
+ * shares, and a share's weights are rounded against a reference of its own.  So
+ * the same sequence in another batch gives other bits: its fp32 sums have
+ * another order, and every weight is rounded anew, each time to within 2^-11 of
+ * it (below 2^-14 of the largest contribution, to within 2^-24 of that).  In the
+ * same batch it gives the same bits. */
 gemm_status_t attn_cache_attend(const attn_cache_t* cache, const void* Q, int64_t q_stride, int32_t q_heads,
                                 const int32_t* page_table, int64_t table_stride, int32_t max_pages,
                                 const int32_t* lengths, int32_t batch, float scale, int32_t dtype, void* out,

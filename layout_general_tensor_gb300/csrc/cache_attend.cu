@@ -43,6 +43,10 @@
 // spans fp16 whatever the rows' magnitudes are, and the largest contribution
 // to the result is the one that is held most exactly.  The result is the
 // product's sum times 2^R / l.
+// m is a logit, not rounded to a whole number: so the largest weight of a short
+// or peaked row is 1 exactly.  (Rounded up, a sequence alone and in a batch
+// differed in 0.3 % of its values instead of up to a third, but the error of a
+// sequence of 9 keys beside one of 8962 was 1.9e-4 instead of 4e-6.)
 #include <algorithm>
 #include <cfloat>
 #include <cmath>

@@ -291,6 +291,27 @@ def test_decode_very_large_keys_under_very_small_queries(m, d):
     assert torch.all(got[:, :, 1:] == 1) and torch.all(got[:, :, 0] == 0.5)
 
 
+@pytest.mark.parametrize("hq,hk,d", [(8, 1, 128), (6, 2, 64)])
+def test_decode_sequences_alone_and_among_others(m, hq, hk, d):
+    """The rest of the batch decides where a sequence's keys are cut, and each cut rounds the weights anew: 2^-11 S
+    either side, with S <= max |v|, the results' own roundings 2^-11 |r| either side, n 2^-24 max |v| of fp32 and
+    subnormal weights.  A sequence of one block of keys is not cut, and in the same batch nothing changes."""
+    lens, page = [2000, 1, 900, 3500, 16, 5000, 311, 1800], 16
+    k, v = ([_randn(40 + 2 * b + i, n, hk, d) for b, n in enumerate(lens)] for i in range(2))
+    cache, table, n = _filled(m, lens, hk, d, page, k=k, v=v)
+    q = _randn(60, len(lens), hq, d, scale=3.0)
+    op, out, again, alone = m.CacheAttention(hq, hk, d, page, dtype=m.GEMM_F16), torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    op.run(q, cache, table, n, out)
+    op.run(q, cache, table, n, again)
+    assert torch.equal(out, again)
+    for b in range(len(lens)):
+        op.run(q[b:b + 1], cache, table[b:b + 1], n[b:b + 1], alone[b:b + 1])
+        most = float(v[b].abs().max()) * 1.0625  # (as e4m3 holds it)
+        tol = 2.0 ** -10 * out[b].float().abs() + (2.0 ** -10 + lens[b] * 2.0 ** -24) * most
+        assert torch.all((alone[b].float() - out[b].float()).abs() <= tol), lens[b]
+        assert lens[b] > page or torch.equal(alone[b], out[b])
+
+
 # ------------------------------------------------------------ packed attention: many sequences
 
 def _spread(batch, tokens, seed):
