@@ -13,7 +13,8 @@
  * another sequence's rows reaches a result.
  *
  * Logits, softmax and sums in fp32; the weights are rounded to the input type
- * for the second product; one rounding of the result.
+ * for the second product (an fp16 one below 2^-14 of the row's largest so far
+ * to 2^-25 of that); one rounding of the result.
  *
  * Errors are status codes (gemm_status_t); nothing aborts or prints.
  */

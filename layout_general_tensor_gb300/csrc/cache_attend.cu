@@ -4,10 +4,10 @@
 // Bound: memory, the codes of every key and value read once; the arithmetic
 // per byte is small (2 * group multiply-adds), so warp-level matrix
 // instructions on registers carry it and nothing goes through shared memory
-// on the way.  Measured (32 / 8 heads of 128): 1 sequence of 65536 tokens 30.7
-// us, of which the stream takes 20 at 6.7 TB/s, 64 of 1 to 8192 38.5 us (25 at
-// a copy's rate), 64 of 2048 54.5 us (74 %); 5 of 1 to 200 (12 / 2 heads of 64)
-// 6.1 us, five dependent trips to memory.
+// on the way.  Measured (32 / 8 heads of 128): 1 sequence of 65536 tokens 30.4
+// us, of which the stream takes 20 at 6.7 TB/s, 64 of 1 to 8192 38.1 us (25 at
+// a copy's rate), 64 of 2048 53.6 us (74 %); 5 of 1 to 200 (12 / 2 heads of 64)
+// 5.9 us, five dependent trips to memory.
 //
 // Work.  A pass is one sequence, key head and group of up to 8 query heads; its
 // units are its blocks of 16 keys and two more for what a pass costs whatever

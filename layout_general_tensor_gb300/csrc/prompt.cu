@@ -204,7 +204,7 @@ struct PromptCfg {
   // a small loop that issues the products (its instructions are fetched again
   // each time round) against two and one stretch of code a place, head_dim 64:
   // 13 ragged prompts 15.4 us and 16.8, single queries 16.5 and 18.0.  The
-  // kernel for many units: 153 us so and 97.7 (8 x 512 tokens after 3000).
+  // kernel for many units: 153 us so and 97.7 (8 x 512 tokens after 1500 to 3000).
   static constexpr uint32_t TURNS = D == 64 && KIND != kPrMany ? 4 : 2;
   static constexpr bool UNROLL = TURNS == 2;
   static constexpr int NS = 2 * static_cast<int>(TURNS);                // its places: K, V, K, V, ...
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   // Where P does not lie over S, a tile's next S is issued as soon as the first
   // half of P says that S has been read, and o_full is of every block.  (8 x 512
-  // tokens after 3000, 32 / 8 heads of 64: 97.7 us, after the product 102.8.)
+  // tokens after 1500 to 3000, 32 / 8 heads of 64: 97.7 us, after the product 102.8.)
   constexpr bool kApart = C::P_COL != 0;
 
   // Every role walks the same list of units; it and every ring and barrier go

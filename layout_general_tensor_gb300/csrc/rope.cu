@@ -27,7 +27,8 @@
 // 57.4, with loads that are not kept in L1 and plain stores 58.7; every
 // sixteenth of a block's heads 62; three heads on their way with five blocks 55,
 // but 1000 tokens 7.6 against 6.9; runs of four values 84, one head on its way
-// 84, a ring in shared memory 63.  64 tokens: 2.9 us.
+// 84, a ring in shared memory 63.  64 tokens: 3.8 us in a graph over three sets of
+// inputs.
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -224,8 +225,9 @@ cudaError_t launch_rope(RopeArgs& a, int sms, cudaStream_t stream) {
   // head a group where there are fewer than that.
   const uint32_t most = static_cast<uint32_t>(sms) * (R == 8 ? kRopeBlocks : kRopeBlocks4) * groups;
   a.chunk = (a.items + most - 1u) / most;
-  // (16384 tokens, 8 + 1 heads, 64 of 128 turned: 17.4 us a run a group, 18.8
-  // interleaved; 32 + 8 heads 57.4 and 55.3, 16 + 4 heads of 256 27.8 and 24.4)
+  // (16384 tokens, us a run a group and interleaved: 8 + 1 heads of 128, 64
+  // turned, 17.6 and 19.1; 8 + 8 of 128 25.7 and 24.6; 32 + 8 of 128 58.3 and
+  // 57.1; 16 + 4 of 256 60.3 and 58.0; 12 + 4 of 64 16.1 and 15.2)
   a.stride = a.heads < 16 ? 1u : 32 / LG;
   const uint32_t per_block = groups * a.chunk, blocks = a.items / per_block + (a.items % per_block ? 1u : 0u);
   return launch_pdl(rope_kernel<R, LG, BF16, HALF>, dim3(blocks), dim3(kRopeThreads), 0, stream, a);
