@@ -559,7 +559,8 @@ class PromptAttention:
     """Attention over packed sequences of different lengths, causal or not,
     with grouped heads (include/attn_prompt.h), on [row][head][head_dim]
     tensors and cumulative lengths (batch + 1 int32 on the device).  The tensors
-    of a call are on the current device, the one the object was made on."""
+    of a call are on the current device, the one the object was made on.  A graph
+    needs the object that it was captured from (its status word)."""
 
     def __init__(self, q_heads, k_heads, head_dim, dtype=GEMM_BF16, causal=True, scale=0.0):
         self.plan = None
