@@ -1,7 +1,9 @@
 """Python binding of the any-layout GEMM C ABI (``include/gemm.h``), the fp32
 row reduction (``include/reduce.h``), the fused attention
-(``include/attention.h``) and the operators of a serving attention layer
-(``include/attn_rope.h``, ``include/attn_prompt.h``, ``include/attn_cache.h``).
+(``include/attention.h``), the operators of a serving attention layer
+(``include/attn_rope.h``, ``include/attn_prompt.h``, ``include/attn_cache.h``)
+and the products over groups of rows (``include/row_groups.h``,
+``include/gemm_grouped.h``).
 
 Argument marshalling only: every function forwards to the entry point of the
 same name in ``_lib/libgemm.so``; all arithmetic runs in the library's CUDA
@@ -39,6 +41,9 @@ GEMM_BF16 = 1
 GEMM_INT4 = 2
 GEMM_F32 = 3
 
+GEMM_GROUPED_M = 0
+GEMM_GROUPED_K = 1
+
 ATTN_ROPE_HALF = 0
 ATTN_ROPE_INTERLEAVED = 1
 
@@ -54,6 +59,9 @@ EXPORTS = (
     "attn_prompt_create", "attn_prompt_run", "attn_prompt_sync_status",
     "attn_prompt_withhold_load", "attn_prompt_destroy",
     "attn_cache_write", "attn_cache_read", "attn_cache_attend_workspace_size", "attn_cache_attend",
+    "gemm_row_groups",
+    "gemm_grouped_create", "gemm_grouped_run", "gemm_grouped_sync_status", "gemm_grouped_withhold_load",
+    "gemm_grouped_destroy",
 )
 
 
@@ -97,6 +105,14 @@ class attn_cache_t(ctypes.Structure):
         ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
         ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("k_heads", ctypes.c_int32),
         ("head_dim", ctypes.c_int32),
+    ]
+
+
+class gemm_grouped_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int32), ("form", ctypes.c_int32),
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("b_layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
     ]
 
 
@@ -159,6 +175,12 @@ def _load():
         "attn_cache_attend_workspace_size": (ctypes.c_int, [I32, I32, I32, I32, ctypes.POINTER(ctypes.c_size_t)]),
         "attn_cache_attend": (ctypes.c_int, [ctypes.POINTER(attn_cache_t), P, I64, I32, P, I64, I32, P, I32,
                                              ctypes.c_float, I32, P, I64, P, ctypes.c_size_t, P]),
+        "gemm_row_groups": (ctypes.c_int, [P, I64, I32, P, P, P, P]),
+        "gemm_grouped_create": (ctypes.c_int, [ctypes.POINTER(gemm_grouped_desc_t), ctypes.POINTER(P)]),
+        "gemm_grouped_run": (ctypes.c_int, [P, P, I64, P, I64, I64, P, I64, P, I64, I64, P]),
+        "gemm_grouped_sync_status": (ctypes.c_int, [P, P]),
+        "gemm_grouped_withhold_load": (ctypes.c_int, [P]),
+        "gemm_grouped_destroy": (ctypes.c_int, [P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -460,6 +482,8 @@ def _with_torch():
                    ("attn_rope_run", "attn_prompt_run", "attn_cache_write", "attn_cache_read", "attn_cache_attend")),
                  getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device, raw_stream, torch.int32,
                  torch.float16, torch.bfloat16)
+    module.setup_groups(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
+                          ("gemm_row_groups", "gemm_grouped_run")))
     _torch, _binding = torch, module
     return torch
 
@@ -699,3 +723,90 @@ class CacheAttention:
             _refuse(what, st, ("q", q, shape, dt, True), ("page_table", page_table, (n, page_table.shape[-1]), _torch.int32, True),
                     ("lengths", lengths, (n,), _torch.int32, False), ("out", out, shape, dt, True),
                     kept=(("the workspace", self.handle[10]), ("the cache", cache.handle[3])))
+
+
+def row_groups(ids, offsets, order, places=None, stream=None):
+    """Put rows in order by the group that each belongs to (include/row_groups.h): from `ids`, the rows' group
+    numbers, `offsets` (groups + 1 values: the rows of group g are order[offsets[g]:offsets[g + 1]]), `order` (the
+    rows of each group, ascending, then those of no group) and its reverse, `places`.  All int32, on the current
+    device; the number of groups, at most 1024, is that of `offsets` less one."""
+    if _binding is None:
+        _with_torch()
+    st = _binding.row_groups(ids, offsets, order, places, stream)
+    if st:
+        n, int32 = len(ids), _torch.int32
+        if st == -1 and len(offsets) < 2:
+            raise ValueError("gemm_row_groups: offsets holds groups + 1 values")
+        _refuse("gemm_row_groups", st, ("ids", ids, (n,), int32, False), ("offsets", offsets, (len(offsets),), int32, False),
+                ("order", order, (n,), int32, False), *((("places", places, (n,), int32, False),) if places is not None else ()))
+
+
+def gemm_grouped_create_status(desc: gemm_grouped_desc_t):
+    """gemm_grouped_create returning (status, handle or None) without raising."""
+    h = ctypes.c_void_p()
+    return _lib.gemm_grouped_create(ctypes.byref(desc), ctypes.byref(h)), h.value
+
+
+class _Grouped:
+    """What the two forms of products over groups of rows share."""
+
+    def __init__(self, groups, form, M, N, K, b_layout, dtype):
+        self.plan = None
+        self.desc = gemm_grouped_desc_t(groups, form, M, N, K, b_layout, dtype)
+        st, h = gemm_grouped_create_status(self.desc)
+        _check(st, "gemm_grouped_create")
+        self.plan = h
+        self.dtype = _torch_dtype(dtype)
+        self.handle = (h, self.dtype, groups, M, N, K, int(b_layout == GEMM_K_CONTIG))
+
+    def run(self, A, B, offsets, C, stream=None):
+        st = _binding.grouped(self.handle, A, B, offsets, C, stream)
+        if st:
+            rows, groups = len(A), self.desc.groups
+            a, b, c = self._shapes(rows)
+            _refuse("gemm_grouped_run", st, ("A", A, a, self.dtype, True), ("B", B, b, self.dtype, True),
+                    ("offsets", offsets, (groups + 1,), _torch.int32, False), ("C", C, c, self.dtype, True))
+
+    def sync_status(self, stream=None) -> int:
+        torch = _torch or _with_torch()
+        return _lib.gemm_grouped_sync_status(self.plan, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+
+    def close(self):
+        if self.plan:
+            _lib.gemm_grouped_destroy(self.plan)
+            self.plan, self.handle = None, (0, *self.handle[1:])
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class GroupedGemm(_Grouped):
+    """C[r] = A[r] B[g] for the rows r of every group g (include/gemm_grouped.h), as the experts of a layer need:
+    A [rows][K], B [groups][N][K] (GEMM_K_CONTIG) or [groups][K][N] (GEMM_MN_CONTIG), C [rows][N], and `offsets`,
+    groups + 1 int32 on the device (row_groups makes them): group g has the rows offsets[g] to offsets[g + 1] - 1.
+    Rows of no group are left as they are.  The gradient to A is the same product with the other layout, that to B
+    is GroupedGemmK.  Rows may be strided; the tensors of a call are on the current device, the one the object was
+    made on.  A graph needs the object that it was captured from (its status word)."""
+
+    def __init__(self, groups, N, K, b_layout=GEMM_K_CONTIG, dtype=GEMM_BF16):
+        super().__init__(groups, GEMM_GROUPED_M, 0, N, K, b_layout, dtype)
+
+    def _shapes(self, rows):
+        d = self.desc
+        return (rows, d.K), (d.groups, *((d.N, d.K) if d.b_layout == GEMM_K_CONTIG else (d.K, d.N))), (rows, d.N)
+
+
+class GroupedGemmK(_Grouped):
+    """C[g] = A_g^T B_g over the rows of every group (include/gemm_grouped.h), the gradient to GroupedGemm's
+    matrices: A [rows][M], B [rows][N], C [groups][M][N]; zeros for a group without rows.  For B [groups][N][K]
+    that is run(dC, A, offsets, dB), for [groups][K][N] run(A, dC, offsets, dB).  Otherwise as GroupedGemm."""
+
+    def __init__(self, groups, M, N, dtype=GEMM_BF16):
+        super().__init__(groups, GEMM_GROUPED_K, M, N, 0, GEMM_MN_CONTIG, dtype)
+
+    def _shapes(self, rows):
+        d = self.desc
+        return (rows, d.M), (rows, d.N), (d.groups, d.M, d.N)

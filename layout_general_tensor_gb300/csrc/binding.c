@@ -1,6 +1,7 @@
 /*
- * The serving operators' calls from Python (the functions of attn_rope.h,
- * attn_prompt.h and attn_cache.h on torch tensors): the tensors' checks and
+ * The calls from Python of the serving operators (the functions of attn_rope.h,
+ * attn_prompt.h and attn_cache.h on torch tensors) and of those over groups of
+ * rows (row_groups.h, gemm_grouped.h): the tensors' checks and
  * the marshalling, in C, because a call for one token lasts a few
  * microseconds and most of it is the host's (norm and rotation of 64 tokens:
  * 7.4 us a call with the checks in Python, of which the launch is 2.4).
@@ -17,6 +18,8 @@
 #include "attn_cache.h"
 #include "attn_prompt.h"
 #include "attn_rope.h"
+#include "gemm_grouped.h"
+#include "row_groups.h"
 
 static PyObject *n_dtype, *n_shape, *n_stride, *n_data_ptr, *n_is_contiguous, *n_get_device;
 static PyObject *current_device, *raw_stream, *t_int32, *t_float16, *t_bfloat16;
@@ -25,6 +28,8 @@ static __typeof__(&attn_prompt_run) prompt_run;
 static __typeof__(&attn_cache_write) cache_write;
 static __typeof__(&attn_cache_read) cache_read;
 static __typeof__(&attn_cache_attend) cache_attend;
+static __typeof__(&gemm_row_groups) group_rows;
+static __typeof__(&gemm_grouped_run) grouped_run;
 
 typedef struct {
   void* ptr;
@@ -85,6 +90,38 @@ static int look_rows(PyObject* t, PyObject* dtype, int64_t rows, int64_t heads, 
 /* A contiguous vector of `count` values (any number where count < 0). */
 static int look_vector(PyObject* t, PyObject* dtype, int64_t count, view* x, int64_t* device) {
   return look(t, dtype, 1, x, device) && x->contiguous && (count < 0 || x->dim[0] == count);
+}
+
+/* [rows][cols] (rows < 0: any number of them); its pitch in stride[0], 0 where
+ * it is the dense one or there is but one row. */
+static int look_matrix(PyObject* t, PyObject* dtype, int64_t rows, int64_t cols, view* x, int64_t* device) {
+  if (!look(t, dtype, 2, x, device) || x->dim[1] != cols || (rows >= 0 && x->dim[0] != rows)) return 0;
+  if (x->contiguous || x->dim[0] <= 1) {
+    if (!x->contiguous && x->stride[1] != 1) return 0;
+    x->stride[0] = 0;
+    return 1;
+  }
+  return x->stride[1] == 1 && x->stride[0] >= cols;
+}
+
+/* [count][rows][cols]: its matrices' distance in stride[0], their pitch in
+ * stride[1], 0 as above. */
+static int look_matrices(PyObject* t, PyObject* dtype, int64_t count, int64_t rows, int64_t cols, view* x, int64_t* device) {
+  if (!look(t, dtype, 3, x, device) || x->dim[0] != count || x->dim[1] != rows || x->dim[2] != cols) return 0;
+  if (x->contiguous) {
+    x->stride[0] = x->stride[1] = 0;
+    return 1;
+  }
+  if (x->stride[2] != 1 && cols > 1) return 0;
+  if (rows == 1)
+    x->stride[1] = 0;
+  else if (x->stride[1] < cols)
+    return 0;
+  if (count == 1)
+    x->stride[0] = 0;
+  else if (x->stride[0] < (rows - 1) * x->stride[1] + cols)
+    return 0;
+  return 1;
 }
 
 /* The stream given, or the current one of the tensors' device, which has to be
@@ -230,6 +267,56 @@ static PyObject* py_attend(PyObject* self, PyObject* const* args, Py_ssize_t nar
                              (int32_t)whole(h, 5), out.ptr, out.stride[0], address(h, 7), (size_t)whole(h, 8), stream));
 }
 
+/* ids, offsets, order, places (or None), stream */
+static PyObject* py_row_groups(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  view ids, offsets, order, places = {0};
+  void* stream;
+  int64_t device = -1;
+  if (nargs != 5) {
+    PyErr_SetString(PyExc_TypeError, "wrong arguments");
+    return NULL;
+  }
+  if (!look_vector(args[0], t_int32, -1, &ids, &device) || !look_vector(args[1], t_int32, -1, &offsets, &device) ||
+      offsets.dim[0] < 2 || offsets.dim[0] > INT32_MAX || !look_vector(args[2], t_int32, ids.dim[0], &order, &device) ||
+      (args[3] != Py_None && !look_vector(args[3], t_int32, ids.dim[0], &places, &device)))
+    return refused();
+  STREAM(args[4]);
+  return status(group_rows(ids.ptr, ids.dim[0], (int32_t)(offsets.dim[0] - 1), offsets.ptr, order.ptr, places.ptr, stream));
+}
+
+/* (plan, dtype, groups, M, N, K, whether B's K is contiguous), A, B, offsets, C, stream; M > 0: groups along K */
+static PyObject* py_grouped(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  view A, B, offsets, C;
+  void* stream;
+  int64_t device = -1;
+  TAKES(6);
+  PyObject *h = args[0], *dtype = PyTuple_GET_ITEM(h, 1);
+  const int64_t groups = whole(h, 2), m = whole(h, 3), n = whole(h, 4), k = whole(h, 5), k_contig = whole(h, 6);
+  int ok;
+  if (m > 0)
+    ok = look_matrix(args[1], dtype, -1, m, &A, &device) && look_matrix(args[2], dtype, A.dim[0], n, &B, &device) &&
+         look_matrices(args[4], dtype, groups, m, n, &C, &device);
+  else
+    ok = look_matrix(args[1], dtype, -1, k, &A, &device) &&
+         look_matrices(args[2], dtype, groups, k_contig ? n : k, k_contig ? k : n, &B, &device) &&
+         look_matrix(args[4], dtype, A.dim[0], n, &C, &device);
+  if (!ok || !look_vector(args[3], t_int32, groups + 1, &offsets, &device)) return refused();
+  STREAM(args[5]);
+  const int64_t ldb = m > 0 ? B.stride[0] : B.stride[1], ldc = m > 0 ? C.stride[1] : C.stride[0];
+  return status(grouped_run(address(h, 0), A.ptr, A.stride[0], B.ptr, ldb, m > 0 ? 0 : B.stride[0], offsets.ptr, A.dim[0],
+                            C.ptr, ldc, m > 0 ? C.stride[0] : 0, stream));
+}
+
+/* the addresses of the functions over groups of rows */
+static PyObject* py_setup_groups(PyObject* self, PyObject* args) {
+  PyObject *order, *grouped;
+  if (!PyArg_ParseTuple(args, "OO", &order, &grouped)) return NULL;
+  group_rows = (__typeof__(group_rows))PyLong_AsVoidPtr(order);
+  grouped_run = (__typeof__(grouped_run))PyLong_AsVoidPtr(grouped);
+  if (PyErr_Occurred()) return NULL;
+  Py_RETURN_NONE;
+}
+
 /* the addresses of the five functions, the current device, the current stream of a device, torch's int32, float16
  * and bfloat16 */
 static PyObject* py_setup(PyObject* self, PyObject* args) {
@@ -258,6 +345,9 @@ static PyMethodDef methods[] = {
     {"cache_write", (PyCFunction)(void (*)(void))py_cache_write, METH_FASTCALL, NULL},
     {"cache_read", (PyCFunction)(void (*)(void))py_cache_read, METH_FASTCALL, NULL},
     {"attend", (PyCFunction)(void (*)(void))py_attend, METH_FASTCALL, NULL},
+    {"setup_groups", py_setup_groups, METH_VARARGS, NULL},
+    {"row_groups", (PyCFunction)(void (*)(void))py_row_groups, METH_FASTCALL, NULL},
+    {"grouped", (PyCFunction)(void (*)(void))py_grouped, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

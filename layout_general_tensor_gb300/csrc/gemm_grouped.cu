@@ -1,0 +1,706 @@
+// Products over groups of rows (include/gemm_grouped.h) on tcgen05.
+//
+// Both forms are one kernel.  The matrix instruction's M side (128 rows of
+// tensor-memory lanes a CTA, 256 a pair) takes C's contiguous index n, its N
+// side C's row index, so a tile's accumulator is C transposed:
+//   groups along M: M side = B of the group (n), N side = rows of A,  K = k
+//   groups along K: M side = B's columns (n),    N side = A's columns, K = rows
+// The rows of a group are thus on the side that the instruction takes in steps
+// of 16 (32 a pair): a group of any size costs its own rows, rounded up, and not
+// a tile's 128 (4 rows of 1536 x 2048: one eighth).  A group's rows are spread
+// evenly over as few tiles as hold them.  Columns of the accumulator that stand
+// for rows of another group are computed and not stored; they touch no other.
+//
+// Work.  The sizes are on the device, so every CTA sums them up itself (a scan
+// over the group's tiles in shared memory) and takes every G-th tile, G the
+// CTAs or pairs: no launch depends on a size.  Within a group the tiles of one
+// stretch of n follow each other, so that they read its weights together.
+//
+// Groups along K end inside a block of 64 rows.  What the block holds beyond is
+// the next group's, and a zero on one side would not cancel an infinity on the
+// other, so those rows of both operands are cleared in shared memory between
+// the copy and the product, by a warp of each CTA that has nothing else to do:
+// at most 15 of them, since the product's steps are 16 deep and whole steps are
+// left out.
+//
+// Roles (256 threads; pairs: in both CTAs):
+//   warp 0      copies of the M side        warp 6  copies of the N side
+//   warp 1      tensor memory; issues the products (the even CTA of a pair)
+//   warps 2..5  results      warp 7  clears the last block's rows (along K)
+#include <algorithm>
+#include <cstdint>
+#include <cstdlib>
+#include <new>
+
+#include "gemm_grouped.h"
+#include "half_types.cuh"
+#include "kernels.h"
+#include "plan.h"
+#include "ptx.cuh"
+
+namespace lgt {
+namespace {
+
+constexpr int kGgThreads = 256;
+constexpr int kGgEpiWarp0 = 2;
+constexpr int kGgMaxGroups = 1024;
+constexpr uint32_t kGgRows = 128;                       // M-side rows a CTA
+constexpr uint32_t kGgPBytes = kGgRows * TILE_K * 2;    // 16 KiB of them a stage
+constexpr uint32_t kGgChunk = 64 * TILE_K * 2;          // a box of 64 x 64 values along n or m
+constexpr uint32_t kGgMost = 256;                       // N-side columns of a tile
+constexpr uint32_t kGgMaxStages = 12;
+constexpr uint32_t kGgEpiBytes = 4 * 2048;              // a warp's 32 rows of C, 32 values each
+constexpr uint32_t kGgBars = 4 * kGgMaxStages + 5;      // full, empty, tail, fixed; accumulators full, empty; end
+constexpr uint32_t kGgSmem = 227 * 1024;
+constexpr uint64_t kGgSettleNs = 200ull * 1000ull * 1000ull;
+
+struct GroupedArgs {
+  CUtensorMap tm_p, tm_q;
+  uint16_t* c;
+  const int32_t* offsets;
+  DeviceStatus* status;
+  uint64_t wait_limit_ns;
+  int64_t ldc, c_stride;
+  int32_t groups, rows;
+  int32_t along_k;
+  int32_t n, m;           // extent of the M side; of the N side (along K)
+  int32_t kb_total;       // blocks of K (along M)
+  uint32_t p_tiles, q_most;
+  uint32_t q_tiles, q_width;  // along K
+  uint32_t q_box;             // along M: rows of an N-side copy, of each CTA
+  uint32_t q_chunks;          // along K: copies of 64 columns, of each CTA
+  uint32_t stages, stage_bytes;
+  int32_t p_mn;
+  uint32_t idesc;  // without N
+  int32_t withhold;
+};
+
+// One tile.
+struct GroupedTile {
+  int32_t group;
+  int32_t p0, q0;     // its first n; its first column of the N side (along M: a row of A)
+  uint32_t count;     // columns to store
+  uint32_t cols;      // of the product
+  int32_t row0, len;  // along K: the group's rows
+  int32_t nkb;
+};
+
+template <bool PAIR>
+struct GroupedCfg {
+  static constexpr uint32_t CTAS = PAIR ? 2 : 1;
+  static constexpr uint32_t STEP = PAIR ? 32 : 16;  // of the product's N
+};
+
+__device__ __forceinline__ uint32_t scan_max(uint32_t v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v = max(v, y);
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t scan_add(uint32_t v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += y;
+  }
+  return v;
+}
+
+// The groups' first rows (never decreasing, never past the last row) and, along
+// M, their first tiles, by the whole CTA.
+__device__ __forceinline__ void grouped_tables(const GroupedArgs& a, uint32_t* off, uint32_t* first, uint32_t* scratch) {
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t n = static_cast<uint32_t>(a.groups) + 1;
+  const uint32_t per = (n + kGgThreads - 1) / kGgThreads;
+  const uint32_t lo = min(tid * per, n), hi = min(lo + per, n);
+  uint32_t most = 0;
+  for (uint32_t i = lo; i < hi; ++i) {
+    most = max(most, static_cast<uint32_t>(min(max(a.offsets[i], 0), a.rows)));
+    off[i] = most;
+  }
+  uint32_t upto = scan_max(most);
+  if (lane == 31) scratch[warp] = upto;
+  __syncthreads();
+  uint32_t before = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (lane == 0) before = 0;
+  for (uint32_t w = 0; w < warp; ++w) before = max(before, scratch[w]);
+  for (uint32_t i = lo; i < hi; ++i) off[i] = max(off[i], before);
+  if (a.along_k) return;  // (the caller's barrier follows)
+  __syncthreads();
+  uint32_t sum = 0;
+  for (uint32_t i = lo; i < hi; ++i) {
+    first[i] = sum;
+    if (i + 1 < n) sum += (off[i + 1] - off[i] + a.q_most - 1) / a.q_most * a.p_tiles;
+  }
+  upto = scan_add(sum);
+  if (lane == 31) scratch[8 + warp] = upto;
+  __syncthreads();
+  before = upto - sum;
+  for (uint32_t w = 0; w < warp; ++w) before += scratch[8 + w];
+  for (uint32_t i = lo; i < hi; ++i) first[i] += before;
+}
+
+template <bool PAIR>
+struct GroupedWork {
+  const uint32_t *off, *first;
+  uint32_t tile, step, end;
+  __device__ GroupedWork(const GroupedArgs& a, const uint32_t* off_, const uint32_t* first_) : off(off_), first(first_) {
+    tile = blockIdx.x / GroupedCfg<PAIR>::CTAS;
+    step = gridDim.x / GroupedCfg<PAIR>::CTAS;
+    end = a.along_k ? static_cast<uint32_t>(a.groups) * a.p_tiles * a.q_tiles : first[a.groups];
+  }
+  __device__ bool next(const GroupedArgs& a, GroupedTile& t) {
+    if (tile >= end) return false;
+    constexpr uint32_t STEP = GroupedCfg<PAIR>::STEP;
+    const uint32_t u = tile;
+    tile += step;
+    if (a.along_k) {
+      const uint32_t g = u / (a.p_tiles * a.q_tiles), r = u - g * (a.p_tiles * a.q_tiles), p = r / a.q_tiles;
+      t.group = static_cast<int32_t>(g);
+      t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
+      const uint32_t q0 = (r - p * a.q_tiles) * a.q_width;
+      t.q0 = static_cast<int32_t>(q0);
+      t.count = min(a.q_width, static_cast<uint32_t>(a.m) - q0);
+      t.row0 = static_cast<int32_t>(off[g]);
+      t.len = static_cast<int32_t>(off[g + 1] - off[g]);
+      t.nkb = (t.len + TILE_K - 1) / TILE_K;
+    } else {
+      // the last group whose first tile is not past this one (one without tiles has its successor's)
+      uint32_t g = 0, n = static_cast<uint32_t>(a.groups);
+      while (n > 1) {
+        const uint32_t half = n >> 1;
+        if (first[g + half] <= u) g += half;
+        n -= half;
+      }
+      const uint32_t r = u - first[g], len = off[g + 1] - off[g];
+      const uint32_t qt = (len + a.q_most - 1) / a.q_most;
+      const uint32_t width = ((len + qt - 1) / qt + STEP - 1) / STEP * STEP;
+      const uint32_t p = r / qt, q = (r - p * qt) * width;
+      t.group = static_cast<int32_t>(g);
+      t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
+      t.q0 = static_cast<int32_t>(off[g] + q);
+      t.count = min(width, len - q);
+      t.nkb = a.kb_total;
+    }
+    t.cols = (t.count + STEP - 1) / STEP * STEP;
+    return true;
+  }
+};
+
+// Rows of the last block that the product takes and that are another group's: [from, to).
+__device__ __forceinline__ bool tail_rows(const GroupedArgs& a, const GroupedTile& t, int kb, uint32_t& from, uint32_t& to) {
+  to = TILE_K;
+  if (!a.along_k || kb + 1 < t.nkb) return false;
+  from = static_cast<uint32_t>(t.len - kb * TILE_K);
+  to = (from + 15) & ~15u;
+  return from < to;
+}
+
+template <bool PAIR, bool BF16>
+__global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
+  pdl_launch_dependents();
+  constexpr uint32_t CTAS = GroupedCfg<PAIR>::CTAS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw_base);
+  const uint32_t epi_off = a.stages * a.stage_bytes;
+  const uint32_t bar0 = base + epi_off + kGgEpiBytes;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + epi_off + kGgEpiBytes + kGgBars * 8);
+  volatile uint32_t* tmem_slot = misc;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  uint32_t* off = misc + 20;  // (16 words of the scan's lie between)
+  uint32_t* first = off + a.groups + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  auto full = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty = [&](uint32_t s) { return bar0 + 8u * (kGgMaxStages + s); };
+  auto tail = [&](uint32_t s) { return bar0 + 8u * (2 * kGgMaxStages + s); };
+  auto fixed = [&](uint32_t s) { return bar0 + 8u * (3 * kGgMaxStages + s); };
+  auto accf = [&](int b) { return bar0 + 8u * (4 * kGgMaxStages + b); };
+  auto acce = [&](int b) { return bar0 + 8u * (4 * kGgMaxStages + 2 + b); };
+  const uint32_t end_bar = bar0 + 8u * (4 * kGgMaxStages + 4);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    const bool got = PAIR ? mbar_wait_bounded_cluster(bar, parity, a.wait_limit_ns, abort_flag)
+                          : mbar_wait_bounded(bar, parity, a.wait_limit_ns, abort_flag);
+    if (!got) {
+      *abort_flag = 1;
+      a.status->where = warp;
+      a.status->code = GEMM_ERR_TIMEOUT;
+    }
+    return got;
+  };
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < a.stages; ++s) {
+      mbar_init(full(s), 2);      // the two copying warps (of the even CTA), and the bytes
+      mbar_init(empty(s), 1);     // the products' commit, to both CTAs
+      mbar_init(tail(s), 2);      // the two copying warps of this CTA, and its bytes
+      mbar_init(fixed(s), CTAS);  // the clearing warps
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf(b), 1);
+      mbar_init(acce(b), 4 * CTAS);
+    }
+    mbar_init(end_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&a.tm_p);
+    tma_prefetch_desc(&a.tm_q);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+      tmem_relinquish();
+    }
+  }
+  pdl_wait();  // (the operands, the offsets and C may be the previous kernel's)
+  grouped_tables(a, off, first, misc + 4);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // the even CTA's barriers
+  const uint32_t full_lead = PAIR ? mapa_shared(full(0), 0) : full(0);
+  const uint32_t fixed_lead = PAIR ? mapa_shared(fixed(0), 0) : fixed(0);
+  const uint32_t acce_lead = PAIR ? mapa_shared(acce(0), 0) : acce(0);
+
+  GroupedWork<PAIR> work(a, off, first);
+  GroupedTile t;
+  if (warp == 0 || warp == 6) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      const bool is_p = warp == 0;
+      const CUtensorMap* tm = is_p ? &a.tm_p : &a.tm_q;
+      const uint32_t at = is_p ? 0u : kGgPBytes;
+      const uint32_t bytes = is_p ? kGgPBytes : a.along_k ? a.q_chunks * kGgChunk : a.q_box * TILE_K * 2;
+      const uint32_t boxes = is_p ? (a.p_mn ? 2u : 1u) : a.along_k ? a.q_chunks : 1u;
+      // coordinates: whether the box runs along K first
+      const bool k_first = is_p ? !a.p_mn : !a.along_k;
+      uint32_t s = 0, phase = 0, issued = 0;
+      bool ok = true;
+      while (ok && work.next(a, t)) {
+        const int32_t x0 = is_p ? t.p0 + static_cast<int32_t>(rank * kGgRows)
+                                : t.q0 + static_cast<int32_t>(rank * (t.cols / CTAS));
+        const int32_t z = is_p && !a.along_k ? t.group : 0;
+        const int32_t k0 = a.along_k ? t.row0 : 0;
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          if (!(ok = wait(empty(s), phase ^ 1u))) break;
+          uint32_t from, to;
+          const bool clear = tail_rows(a, t, kb, from, to);
+          // A block with rows to clear lands on this CTA's own barrier.
+          uint32_t bar = full_lead + 8u * s;
+          if (clear) {
+            bar = PAIR ? mapa_shared(tail(s), rank) : tail(s);
+            mbar_arrive_expect_tx(tail(s), bytes);
+            if (leader) mbar_arrive(full(s));
+          } else if (leader) {
+            mbar_arrive_expect_tx(full(s), bytes * CTAS);
+          }
+          const uint32_t dst = base + s * a.stage_bytes + at;
+          const int32_t k = k0 + kb * TILE_K;
+          for (uint32_t j = 0; j < boxes; ++j) {
+            const int32_t x = x0 + static_cast<int32_t>(64 * j);
+            if (a.withhold && !is_p && blockIdx.x == 0 && issued == 0) continue;
+            if constexpr (PAIR)
+              tma_load_3d_pair(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, z);
+            else
+              tma_load_3d(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, z);
+          }
+          ++issued;
+          if (++s == a.stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every commit to this CTA's barriers has arrived before it leaves.
+      const uint32_t from = issued > a.stages ? issued - a.stages : 0u;
+      for (uint32_t i = from; ok && i < issued; ++i) ok = wait(empty(i % a.stages), i / a.stages & 1u);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (leader && lane == 0) {
+      const uint32_t p_step = a.p_mn ? 2048u : 32u, q_step = a.along_k ? 2048u : 32u;
+      const uint32_t p_lbo = a.p_mn ? kGgChunk : 16u, q_lbo = a.along_k ? kGgChunk : 16u;
+      uint32_t s = 0, phase = 0, uses = 0, fixes = 0;
+      bool ok = true;
+      while (ok && work.next(a, t)) {
+        if (t.nkb == 0) continue;
+        const int buf = static_cast<int>(uses & 1u);
+        if (!(ok = wait(acce(buf), (uses >> 1 & 1u) ^ 1u))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(buf) * kGgMost;
+        const uint32_t idesc = a.idesc | (t.cols >> 3) << 17;
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          if (!(ok = wait(full(s), phase))) break;
+          uint32_t from, to;
+          if (tail_rows(a, t, kb, from, to)) {
+            if (!(ok = wait(fixed(s), fixes >> s & 1u))) break;
+            fixes ^= 1u << s;
+          }
+          tc_fence_after();
+          const uint32_t sp = base + s * a.stage_bytes, sq = sp + kGgPBytes;
+#pragma unroll
+          for (uint32_t k = 0; k < TILE_K / 16; ++k) {
+            if (k * 16 >= to) break;
+            const uint64_t pd = sw128_desc(sp + k * p_step, p_lbo, 1024u);
+            const uint64_t qd = sw128_desc(sq + k * q_step, q_lbo, 1024u);
+            if constexpr (PAIR)
+              tc_mma_f16_ss_pair(d, pd, qd, idesc, (kb | k) != 0 ? 1u : 0u);
+            else
+              tc_mma_f16_ss(d, pd, qd, idesc, (kb | k) != 0 ? 1u : 0u);
+          }
+          if constexpr (PAIR)
+            tc_commit_pair_mc(empty(s), 0x3);
+          else
+            tc_commit(empty(s));
+          if (++s == a.stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if constexpr (PAIR)
+          tc_commit_pair_mc(accf(buf), 0x3);
+        else
+          tc_commit(accf(buf));
+        ++uses;
+      }
+    }
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ rows of the next group
+    if (a.along_k) {
+      uint32_t s = 0, done = 0;
+      bool ok = true;
+      while (ok && work.next(a, t)) {
+        if (t.nkb == 0) continue;
+        s = (s + static_cast<uint32_t>(t.nkb) - 1) % a.stages;  // (the last block's)
+        uint32_t from, to;
+        if (tail_rows(a, t, t.nkb - 1, from, to)) {
+          if (!(ok = __all_sync(0xffffffffu, wait(tail(s), done >> s & 1u)))) break;
+          done ^= 1u << s;
+          const uint32_t at = base + s * a.stage_bytes + from * 128u + lane * 16u;
+          const uint32_t bytes = (to - from) * 128u;
+          for (uint32_t c = 0; c < 2 + a.q_chunks; ++c)
+            for (uint32_t i = lane * 16u; i < bytes; i += 512u) st_shared_v4(at + c * kGgChunk + i - lane * 16u, 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR)
+              mbar_arrive_cluster(fixed_lead + 8u * s);
+            else
+              mbar_arrive(fixed(s));
+          }
+        }
+        if (++s == a.stages) s = 0;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ results
+    const uint32_t quad = static_cast<uint32_t>(warp & 3);
+    const uint32_t stage = base + epi_off + static_cast<uint32_t>(warp - kGgEpiWarp0) * 2048u;
+    // Places in the warp's 32 x 64 bytes: row r at 64 r, its 16-byte pieces
+    // exchanged so that eight rows' pieces are in eight different bank groups.
+    const uint32_t put = stage + (lane & 7u) * 64u + ((static_cast<uint32_t>(lane >> 3) ^ (lane >> 1 & 3u)) << 4);
+    const uint32_t row = static_cast<uint32_t>(lane >> 2), piece = static_cast<uint32_t>(lane & 3);
+    const uint32_t get = stage + row * 64u + ((piece ^ (row >> 1 & 3u)) << 4);
+    uint32_t uses = 0;
+    bool ok = true;
+    while (ok && work.next(a, t)) {
+      const int buf = static_cast<int>(uses & 1u);
+      if (t.nkb > 0) {
+        if (!(ok = __all_sync(0xffffffffu, wait(accf(buf), uses >> 1 & 1u)))) break;
+        tc_fence_after();
+      }
+      const uint32_t d = tmem + static_cast<uint32_t>(buf) * kGgMost + (quad * 32u << 16);
+      const int32_t n = t.p0 + static_cast<int32_t>(rank * kGgRows + quad * 32u + piece * 8u);
+      const bool inside = n < a.n;
+      uint16_t* out = a.c + (a.along_k ? t.group * a.c_stride : 0) + static_cast<int64_t>(t.q0) * a.ldc + n;
+      for (uint32_t c = 0; c < t.count; c += 32) {
+        uint32_t x[16], y[16];
+        if (t.nkb > 0) {
+          tc_ld_16x256b_x4(d + c, x);
+          tc_ld_16x256b_x4(d + c + (16u << 16), y);
+          tc_wait_ld_regs(x);
+          tc_regs_after_wait(y);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = y[i] = 0u;
+        }
+        auto pair = [](uint32_t lo, uint32_t hi) { return pack_pair16<BF16>(__uint_as_float(lo), __uint_as_float(hi)); };
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+          stmatrix_x4_trans(put + i * 512u, pair(x[4 * i], x[4 * i + 1]), pair(x[4 * i + 2], x[4 * i + 3]),
+                            pair(y[4 * i], y[4 * i + 1]), pair(y[4 * i + 2], y[4 * i + 3]));
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t r = c + i * 8u + row;
+          const uint4 v = ld_shared_v4(get + i * 512u);
+          if (r < t.count && inside) st_global_v4(out + static_cast<int64_t>(r) * a.ldc, v.x, v.y, v.z, v.w);
+        }
+        __syncwarp();
+      }
+      if (t.nkb > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_cluster(acce_lead + 8u * buf);
+          else
+            mbar_arrive(acce(buf));
+        }
+        ++uses;
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ end
+  __syncthreads();
+  if (*abort_flag) {
+    // Copies that were made may still be landing, on a barrier that will not
+    // complete: they take microseconds, and are given far more.
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kGgSettleNs) {
+    }
+  }
+  if (leader && warp == 1 && lane == 0) {
+    volatile int no_abort = 0;
+    if constexpr (PAIR)
+      tc_commit_pair_mc(end_bar, 0x1);
+    else
+      tc_commit(end_bar);
+    mbar_wait_bounded(end_bar, 0, drain_ns(a.wait_limit_ns), &no_abort);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool PAIR, bool BF16>
+cudaError_t launch_grouped_as(const GroupedArgs& a, unsigned workers, cudaStream_t stream) {
+  const cudaError_t e = set_smem_once<grouped_kernel<PAIR, BF16>>(static_cast<int>(kGgSmem));
+  if (e != cudaSuccess) return e;
+  if (PAIR)
+    return launch_pdl_cluster(grouped_kernel<PAIR, BF16>, dim3(2 * workers), dim3(kGgThreads), kGgSmem, stream, 2u, a);
+  return launch_pdl(grouped_kernel<PAIR, BF16>, dim3(workers), dim3(kGgThreads), kGgSmem, stream, a);
+}
+
+cudaError_t launch_grouped(const GroupedArgs& a, bool pair, bool bf16, unsigned workers, cudaStream_t stream) {
+  if (pair) return bf16 ? launch_grouped_as<true, true>(a, workers, stream) : launch_grouped_as<true, false>(a, workers, stream);
+  return bf16 ? launch_grouped_as<false, true>(a, workers, stream) : launch_grouped_as<false, false>(a, workers, stream);
+}
+
+// [d2][d1][d0] with pitches s1 and s2 in elements, boxes of 64 x box1.
+bool encode_3d(CUtensorMap* map, const void* ptr, bool bf16, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2,
+               uint32_t box1) {
+  auto enc = get_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
+  cuuint32_t box[3] = {64, box1, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint64_t grouped_wait_limit() {
+  const char* s = std::getenv("LGT_GEMM_WAIT_LIMIT_MS");
+  if (s && *s) {
+    const double ms = std::atof(s);
+    if (ms > 0) return static_cast<uint64_t>(ms * 1e6);
+  }
+  return 2000ull * 1000ull * 1000ull;  // 2 s
+}
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+}  // namespace
+}  // namespace lgt
+
+struct gemm_grouped_plan {
+  gemm_grouped_desc_t d;
+  int device = -1;
+  int sms = 0;
+  lgt::DeviceStatus* d_status = nullptr;
+  uint64_t wait_limit_ns = 0;
+  int withhold_armed = 0;  // gemm_grouped_withhold_load: the next run withholds a load (one shot)
+};
+
+extern "C" {
+
+gemm_status_t gemm_grouped_create(const gemm_grouped_desc_t* desc, gemm_grouped_plan_t** plan) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  *plan = nullptr;
+  if (!desc) return GEMM_ERR_INVALID_ARG;
+  const gemm_grouped_desc_t& d = *desc;
+  auto size = [](int64_t v) { return v >= 8 && v % 8 == 0 && v < (int64_t{1} << 30); };
+  const bool along_k = d.form == GEMM_GROUPED_K;
+  if (d.groups < 1 || d.groups > lgt::kGgMaxGroups || (d.form != GEMM_GROUPED_M && !along_k) || !size(d.N) ||
+      (d.dtype != GEMM_F16 && d.dtype != GEMM_BF16) ||
+      (along_k ? !size(d.M) || d.K != 0 || d.b_layout != GEMM_MN_CONTIG
+               : !size(d.K) || d.M != 0 || (d.b_layout != GEMM_K_CONTIG && d.b_layout != GEMM_MN_CONTIG)))
+    return GEMM_ERR_INVALID_ARG;
+  gemm_grouped_plan* p = new (std::nothrow) gemm_grouped_plan();
+  if (!p) return GEMM_ERR_CUDA;
+  p->d = d;
+  p->wait_limit_ns = lgt::grouped_wait_limit();
+  if (cudaGetDevice(&p->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
+    cudaGetLastError();
+    p->device = -1;
+  } else if (cudaMalloc(&p->d_status, 16) != cudaSuccess || cudaMemset(p->d_status, 0, 16) != cudaSuccess) {
+    cudaGetLastError();
+    if (p->d_status) cudaFree(p->d_status);
+    delete p;
+    return GEMM_ERR_CUDA;
+  }
+  *plan = p;
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t lda, const void* B, int64_t ldb,
+                               int64_t b_stride, const int32_t* offsets, int64_t rows, void* C, int64_t ldc,
+                               int64_t c_stride, void* stream) {
+  using namespace lgt;
+  if (!plan || rows < 0) return GEMM_ERR_INVALID_ARG;
+  const gemm_grouped_desc_t& d = plan->d;
+  const bool along_k = d.form == GEMM_GROUPED_K, b_mn = d.b_layout == GEMM_MN_CONTIG, bf16 = d.dtype == GEMM_BF16;
+  const int64_t a_row = along_k ? d.M : d.K, b_row = b_mn ? d.N : d.K;
+  if (lda == 0) lda = a_row;
+  if (ldb == 0) ldb = b_row;
+  if (ldc == 0) ldc = d.N;
+  const int64_t b_rows = b_mn ? d.K : d.N;
+  // (a copy's pitches are below 2^40 bytes, and no product of a pitch and a size passes 64 bits)
+  constexpr int64_t kPitch = int64_t{1} << 32, kStride = int64_t{1} << 38;
+  for (int64_t v : {lda, ldb, ldc})
+    if (v < 0 || v % 8 != 0 || v > kPitch) return GEMM_ERR_INVALID_ARG;
+  if (along_k)
+    b_stride = 8;
+  else
+    c_stride = 0;
+  if (!along_k && b_stride == 0) b_stride = b_rows * ldb;
+  if (along_k && c_stride == 0) c_stride = d.M * ldc;
+  for (int64_t v : {b_stride, c_stride})
+    if (v < 0 || v % 8 != 0 || v > kStride) return GEMM_ERR_INVALID_ARG;
+  if (lda < a_row || ldb < b_row || ldc < d.N || (!along_k && b_stride < (b_rows - 1) * ldb + b_row) ||
+      (along_k && c_stride < (d.M - 1) * ldc + d.N))
+    return GEMM_ERR_INVALID_ARG;
+  if (rows == 0 && !along_k) return GEMM_OK;
+  if (!offsets || !C || (rows > 0 && (!A || !B))) return GEMM_ERR_INVALID_ARG;
+  for (const void* p : {A, B, static_cast<const void*>(C)})
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return GEMM_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(offsets) % 4 != 0) return GEMM_ERR_ALIGNMENT;
+  if (rows > (int64_t{1} << 30)) return GEMM_ERR_UNSUPPORTED;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  if (dev != plan->device) return GEMM_ERR_INVALID_ARG;  // (the status word is there)
+
+  GroupedArgs a = {};
+  const int64_t busy = std::min<int64_t>(d.groups, std::max<int64_t>(rows, 1));
+  const int64_t mean = (rows + busy - 1) / busy;
+  const bool pair = d.N > kGgRows && (along_k ? d.M > 64 : mean > 96);
+  const uint32_t ctas = pair ? 2 : 1, step = pair ? 32 : 16;
+  a.p_tiles = static_cast<uint32_t>((d.N + kGgRows * ctas - 1) / (kGgRows * ctas));
+  int64_t tiles;
+  if (along_k) {
+    a.q_tiles = static_cast<uint32_t>((d.M + kGgMost - 1) / kGgMost);
+    a.q_width = static_cast<uint32_t>(up((d.M + a.q_tiles - 1) / a.q_tiles, step));
+    a.q_most = a.q_width;
+    a.q_chunks = (a.q_width / ctas + 63) / 64;
+    a.stage_bytes = kGgPBytes + a.q_chunks * kGgChunk;
+    tiles = static_cast<int64_t>(d.groups) * a.p_tiles * a.q_tiles;
+  } else {
+    a.q_most = kGgMost;
+    if (!pair)
+      for (uint32_t w : {128u, 64u, 32u, 16u})
+        if (2 * mean <= static_cast<int64_t>(w)) a.q_most = w;
+    a.q_box = a.q_most / ctas;
+    a.stage_bytes = kGgPBytes + a.q_box * TILE_K * 2;
+    tiles = (rows / a.q_most + busy) * a.p_tiles;
+  }
+  if (tiles >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
+  const uint32_t tables = 96 + 2 * static_cast<uint32_t>(d.groups + 1) * 4;
+  a.stages = std::min<uint32_t>(kGgMaxStages, (kGgSmem - 1024 - kGgEpiBytes - kGgBars * 8 - tables) / a.stage_bytes);
+
+  // (no rows: nothing is copied, any valid address will do)
+  const void* ap = rows > 0 ? A : C;
+  const void* bp = rows > 0 ? B : C;
+  const int64_t some = std::max<int64_t>(rows, 1);
+  const bool encoded =
+      along_k ? encode_3d(&a.tm_p, bp, bf16, d.N, some, 1, ldb, ldb, 64) &&
+                    encode_3d(&a.tm_q, ap, bf16, d.M, some, 1, lda, lda, 64)
+              : encode_3d(&a.tm_p, bp, bf16, b_row, b_rows, d.groups, ldb, b_stride, b_mn ? 64 : kGgRows) &&
+                    encode_3d(&a.tm_q, ap, bf16, d.K, some, 1, lda, lda, a.q_box);
+  if (!encoded) return GEMM_ERR_CUDA;
+  a.c = static_cast<uint16_t*>(C);
+  a.offsets = offsets;
+  a.status = plan->d_status;
+  a.wait_limit_ns = plan->wait_limit_ns;
+  a.ldc = ldc;
+  a.c_stride = c_stride;
+  a.groups = d.groups;
+  a.rows = static_cast<int32_t>(rows);
+  a.along_k = along_k;
+  a.n = static_cast<int32_t>(d.N);
+  a.m = static_cast<int32_t>(d.M);
+  a.kb_total = static_cast<int32_t>((d.K + TILE_K - 1) / TILE_K);
+  a.p_mn = b_mn;
+  a.idesc = idesc_f16(bf16, b_mn, along_k, kGgRows * ctas, 0);
+  a.withhold = plan->withhold_armed ? __atomic_exchange_n(&plan->withhold_armed, 0, __ATOMIC_ACQ_REL) : 0;
+  const unsigned workers = static_cast<unsigned>(std::min<int64_t>(tiles, plan->sms / ctas));
+  if (launch_grouped(a, pair, bf16, workers, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_grouped_sync_status(gemm_grouped_plan_t* plan, void* stream) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  if (!plan->d_status) return GEMM_ERR_CUDA;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
+  lgt::DeviceStatus st;
+  if (cudaMemcpy(&st, plan->d_status, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (st.code != 0) {
+    if (cudaMemset(plan->d_status, 0, sizeof(st)) != cudaSuccess) return GEMM_ERR_CUDA;
+    return static_cast<gemm_status_t>(st.code);
+  }
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_grouped_withhold_load(gemm_grouped_plan_t* plan) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  __atomic_store_n(&plan->withhold_armed, 1, __ATOMIC_RELEASE);
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_grouped_destroy(gemm_grouped_plan_t* plan) {
+  if (!plan) return GEMM_OK;
+  if (plan->d_status) cudaFree(plan->d_status);
+  delete plan;
+  return GEMM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,185 @@
+"""Rows in groups on the GPU: row_groups, GroupedGemm and GroupedGemmK against
+their definitions in 64 bits.
+
+Most inputs are small whole numbers, so every sum is below 2^24 and exact in
+fp32: the result is then the exact sum rounded once to the output type, and has
+to be equal to it, bit by bit.  For normal inputs the tolerance is half a step of
+the output type (torch.finfo(t).eps / 2 of the value) and, for the sums, two
+roundings of 2^-24 at a magnitude of at most sum |a b| / sqrt(K) * 8 for each of
+the K terms, in the mean of K signs: sqrt(K) * 2 * 2^-24 * 8 / sqrt(K) * sum |a b|
+= 2^-20 sum |a b|."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from helpers import lib
+
+pytestmark = pytest.mark.gpu
+
+TD = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def m():
+    return lib()
+
+
+def _code(m, t):
+    return m.GEMM_BF16 if t == "bf16" else m.GEMM_F16
+
+
+def _ints(seed, *shape, dtype, most=3):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda").to(dtype)
+
+
+def _pitched(t, extra):
+    """t with rows `extra` values longer, which hold NaN."""
+    if not extra:
+        return t
+    wide = torch.full((*t.shape[:-1], t.shape[-1] + extra), float("nan"), dtype=t.dtype, device="cuda")
+    wide[..., :t.shape[-1]] = t
+    return wide[..., :t.shape[-1]]
+
+
+def _offsets(sizes, start=0):
+    return torch.tensor(np.concatenate([[0], np.cumsum(sizes)]) + start, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ row_groups
+
+def _check_groups(m, ids, groups, places=True):
+    n = len(ids)
+    offsets = torch.full((groups + 1,), -7, dtype=torch.int32, device="cuda")
+    order = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    back = torch.full((n,), -7, dtype=torch.int32, device="cuda") if places else None
+    m.row_groups(ids, offsets, order, back)
+    host = ids.cpu().numpy().astype(np.int64)
+    key = np.where((host < 0) | (host >= groups), groups, host)
+    want = np.argsort(key, kind="stable")
+    assert np.array_equal(offsets.cpu().numpy(), np.concatenate([[0], np.cumsum(np.bincount(key, minlength=groups + 1)[:groups])]))
+    assert np.array_equal(order.cpu().numpy(), want)
+    if places:
+        assert np.array_equal(back.cpu().numpy(), np.argsort(want, kind="stable"))
+
+
+@pytest.mark.parametrize("rows", [0, 1, 31, 32, 33, 1000, 1024, 4096, 4097, 8191, 40000, 131072, 300001])
+@pytest.mark.parametrize("groups", [1, 5, 128, 1024])
+def test_row_groups(m, rows, groups):
+    g = torch.Generator(device="cuda").manual_seed(rows * 7 + groups)
+    ids = torch.randint(-2, groups + 2, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    _check_groups(m, ids, groups, places=rows % 2 == 1)
+
+
+@pytest.mark.parametrize("kind", ["one", "none", "last", "steps", "far"])
+def test_row_groups_lopsided(m, kind):
+    n, groups = 20011, 77
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    if kind == "none":
+        ids -= 1
+    elif kind == "last":
+        ids += groups - 1
+    elif kind == "steps":
+        ids = (torch.arange(n, device="cuda") // 300).int()
+    elif kind == "far":
+        ids = torch.tensor([-2**31, 2**31 - 1, groups, -1, 0] * (n // 5), dtype=torch.int32, device="cuda")
+    _check_groups(m, ids, groups)
+
+
+# ------------------------------------------------------------------ groups along M
+
+def _rows_reference(a, b, at, k_contig):
+    out = {}
+    for g in range(len(at) - 1):
+        lo, hi = at[g], at[g + 1]
+        if hi > lo:
+            w = b[g].double()
+            out[(lo, hi)] = a[lo:hi].double() @ (w.T if k_contig else w)
+    return out
+
+
+def _check_rows(m, sizes, n, k, k_contig, dtype, pad=0, start=0, extra=(0, 0, 0), seed=0):
+    t, rows = TD[dtype], sum(sizes) + pad + start
+    a = _pitched(_ints(seed, rows, k, dtype=t), extra[0])
+    b = _pitched(_ints(seed + 1, len(sizes), *((n, k) if k_contig else (k, n)), dtype=t), extra[1])
+    c = _pitched(torch.full((rows, n), -77.0, dtype=t, device="cuda"), extra[2])
+    offsets = _offsets(sizes, start)
+    if start:
+        a[:start] = float("nan")
+    if pad:
+        a[rows - pad:] = float("inf")
+    op = m.GroupedGemm(len(sizes), n, k, b_layout=m.GEMM_K_CONTIG if k_contig else m.GEMM_MN_CONTIG, dtype=_code(m, dtype))
+    op.run(a, b, offsets, c)
+    assert op.sync_status() == m.GEMM_OK
+    want = torch.full((rows, n), -77.0, dtype=t, device="cuda")
+    for (lo, hi), v in _rows_reference(a, b, offsets.tolist(), k_contig).items():
+        want[lo:hi] = v.to(t)
+    assert torch.equal(c, want), (c != want).nonzero()[:5]
+    op.close()
+
+
+SIZES = [[1], [0, 1, 0], [16], [17, 0, 3], [5] * 40, [0] * 9 + [31], [33, 1, 128, 64], [130, 250, 1, 0, 257, 90], [600, 513],
+         [97] * 7, [1000, 0, 0, 3, 24], [256, 512, 255], [1] * 200]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{max(s)}_{sum(s)}")
+@pytest.mark.parametrize("k_contig", [True, False])
+@pytest.mark.parametrize("n,k", [(8, 8), (136, 72), (264, 200), (512, 1000)])
+def test_rows(m, sizes, k_contig, n, k):
+    _check_rows(m, sizes, n, k, k_contig, "bf16" if (n + len(sizes)) % 16 else "f16", seed=len(sizes))
+
+
+@pytest.mark.parametrize("k_contig", [True, False])
+@pytest.mark.parametrize("sizes", [[3, 0, 20], [200, 111, 300]], ids=["few", "many"])
+def test_rows_strided_padded(m, sizes, k_contig):
+    _check_rows(m, sizes, 264, 136, k_contig, "f16", pad=19, start=5, extra=(8, 16, 24), seed=3)
+    _check_rows(m, sizes, 264, 136, k_contig, "bf16", pad=300, start=130, extra=(0, 8, 0), seed=4)
+
+
+@pytest.mark.parametrize("groups", [255, 256, 257, 1024])
+def test_rows_many_groups(m, groups):
+    r = random.Random(groups)
+    _check_rows(m, [r.choice((0, 0, 1, 2, 40)) for _ in range(groups)], 72, 64, groups % 2 == 0, "bf16", seed=groups)
+    _check_rows(m, [r.choice((0, 100, 300)) for _ in range(groups)], 136, 64, groups % 2 == 0, "f16", seed=groups)
+
+
+# ------------------------------------------------------------------ groups along K
+
+def _check_sums(m, sizes, mm, n, dtype, pad=0, start=0, extra=(0, 0, 0), seed=0):
+    t, rows = TD[dtype], sum(sizes) + pad + start
+    a, b = _pitched(_ints(seed, rows, mm, dtype=t), extra[0]), _pitched(_ints(seed + 1, rows, n, dtype=t), extra[1])
+    c = _pitched(torch.full((len(sizes), mm, n), -77.0, dtype=t, device="cuda"), extra[2])
+    offsets = _offsets(sizes, start)
+    for x in (a, b):
+        x[:start] = float("nan")
+        x[rows - pad:] = float("inf")
+    op = m.GroupedGemmK(len(sizes), mm, n, dtype=_code(m, dtype))
+    op.run(a, b, offsets, c)
+    assert op.sync_status() == m.GEMM_OK
+    at = offsets.tolist()
+    for g in range(len(sizes)):
+        want = (a[at[g]:at[g + 1]].double().T @ b[at[g]:at[g + 1]].double()).to(t)
+        assert torch.equal(c[g], want), (g, (c[g] != want).nonzero()[:5])
+    op.close()
+
+
+SUM_SIZES = [[0], [1], [0, 0, 7, 0], [64], [65, 63], [128, 1, 0, 15, 16, 17], [5] * 40, [31, 33, 47, 48, 49, 63, 64, 65, 80], [1000, 24], [700, 0, 901]]
+
+
+@pytest.mark.parametrize("sizes", SUM_SIZES, ids=lambda s: f"{len(s)}x{max(s)}_{sum(s)}")
+@pytest.mark.parametrize("mm,n", [(8, 8), (64, 520), (72, 136), (264, 200), (1000, 512), (520, 120)])
+def test_sums(m, sizes, mm, n):
+    _check_sums(m, sizes, mm, n, "bf16" if (mm + len(sizes)) % 16 else "f16", seed=len(sizes))
+
+
+def test_sums_strided_padded(m):
+    _check_sums(m, [33, 0, 20], 136, 264, "f16", pad=19, start=5, extra=(8, 16, 24), seed=3)
+    _check_sums(m, [233, 0, 120, 1], 264, 72, "bf16", pad=70, start=65, extra=(0, 8, 16), seed=4)
+
+
+@pytest.mark.parametrize("groups", [256, 1024])
+def test_sums_many_groups(m, groups):
+    r = random.Random(groups)
+    _check_sums(m, [r.choice((0, 1, 2, 40, 100)) for _ in range(groups)], 72, 136, "bf16", seed=groups)
