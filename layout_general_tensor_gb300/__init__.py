@@ -2,8 +2,8 @@
 row reduction (``include/reduce.h``), the fused attention
 (``include/attention.h``), the operators of a serving attention layer
 (``include/attn_rope.h``, ``include/attn_prompt.h``, ``include/attn_cache.h``)
-and the products over groups of rows (``include/row_groups.h``,
-``include/gemm_grouped.h``).
+and what works on rows in groups (``include/row_groups.h``,
+``include/gemm_grouped.h``, ``include/adapters.h``).
 
 Argument marshalling only: every function forwards to the entry point of the
 same name in ``_lib/libgemm.so``; all arithmetic runs in the library's CUDA
@@ -62,6 +62,7 @@ EXPORTS = (
     "gemm_row_groups",
     "gemm_grouped_create", "gemm_grouped_run", "gemm_grouped_sync_status", "gemm_grouped_withhold_load",
     "gemm_grouped_destroy",
+    "gemm_adapters_run",
 )
 
 
@@ -113,6 +114,13 @@ class gemm_grouped_desc_t(ctypes.Structure):
         ("groups", ctypes.c_int32), ("form", ctypes.c_int32),
         ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
         ("b_layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
+    ]
+
+
+class gemm_adapters_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int32), ("rank", ctypes.c_int32), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
     ]
 
 
@@ -181,6 +189,8 @@ def _load():
         "gemm_grouped_sync_status": (ctypes.c_int, [P, P]),
         "gemm_grouped_withhold_load": (ctypes.c_int, [P]),
         "gemm_grouped_destroy": (ctypes.c_int, [P]),
+        "gemm_adapters_run": (ctypes.c_int, [ctypes.POINTER(gemm_adapters_desc_t), P, I64, P, P, P, P, P, I64, P, I64,
+                                             P, I64, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -483,7 +493,7 @@ def _with_torch():
                  getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device, raw_stream, torch.int32,
                  torch.float16, torch.bfloat16)
     module.setup_groups(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
-                          ("gemm_row_groups", "gemm_grouped_run")))
+                          ("gemm_row_groups", "gemm_grouped_run", "gemm_adapters_run")), torch.float32)
     _torch, _binding = torch, module
     return torch
 
@@ -810,3 +820,28 @@ class GroupedGemmK(_Grouped):
     def _shapes(self, rows):
         d = self.desc
         return (rows, d.M), (rows, d.N), (d.groups, d.M, d.N)
+
+
+class Adapters:
+    """Low-rank adapters of many requests at once beside a shared projection (include/adapters.h):
+    out[r] = base[r] + scales[g] (x[r] A[g]^T) B[g]^T for the rows r of every group g, base[r] for a row of none.
+    x [rows][K], A [groups][rank][K], B [groups][N][rank], base and out [rows][N] (out may be base), offsets and
+    order from row_groups over the rows' adapter numbers; without order (None) the rows of a group follow each
+    other.  Rows of x, base and out may be strided; the tensors of a call are on the current device."""
+
+    def __init__(self, groups, N, K, rank, dtype=GEMM_BF16):
+        self.desc = gemm_adapters_desc_t(groups, rank, N, K, dtype)
+        if not (1 <= groups <= 1024 and 8 <= rank <= 128 and rank % 8 == 0 and N >= 8 and N % 8 == 0 and K >= 8 and K % 8 == 0):
+            raise GemmError(GEMM_ERR_INVALID_ARG, "Adapters")
+        self.dtype = _torch_dtype(dtype)
+        self.handle = (ctypes.addressof(self.desc), self.dtype, groups, N, K, rank)
+
+    def run(self, x, A, B, offsets, order, base, out, scales=None, stream=None):
+        st = _binding.adapters(self.handle, x, A, B, offsets, order, base, out, scales, stream)
+        if st:
+            d, dt, n = self.desc, self.dtype, len(x)
+            _refuse("gemm_adapters_run", st, ("x", x, (n, d.K), dt, True), ("A", A, (d.groups, d.rank, d.K), dt, False),
+                    ("B", B, (d.groups, d.N, d.rank), dt, False), ("offsets", offsets, (d.groups + 1,), _torch.int32, False),
+                    *((("order", order, (n,), _torch.int32, False),) if order is not None else ()),
+                    ("base", base, (n, d.N), dt, True), ("out", out, (n, d.N), dt, True),
+                    *((("scales", scales, (d.groups,), _torch.float32, False),) if scales is not None else ()))

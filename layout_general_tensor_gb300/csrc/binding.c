@@ -1,7 +1,7 @@
 /*
  * The calls from Python of the serving operators (the functions of attn_rope.h,
  * attn_prompt.h and attn_cache.h on torch tensors) and of those over groups of
- * rows (row_groups.h, gemm_grouped.h): the tensors' checks and
+ * rows (row_groups.h, gemm_grouped.h, adapters.h): the tensors' checks and
  * the marshalling, in C, because a call for one token lasts a few
  * microseconds and most of it is the host's (norm and rotation of 64 tokens:
  * 7.4 us a call with the checks in Python, of which the launch is 2.4).
@@ -15,6 +15,7 @@
 #include <Python.h>
 #include <stdint.h>
 
+#include "adapters.h"
 #include "attn_cache.h"
 #include "attn_prompt.h"
 #include "attn_rope.h"
@@ -22,7 +23,7 @@
 #include "row_groups.h"
 
 static PyObject *n_dtype, *n_shape, *n_stride, *n_data_ptr, *n_is_contiguous, *n_get_device;
-static PyObject *current_device, *raw_stream, *t_int32, *t_float16, *t_bfloat16;
+static PyObject *current_device, *raw_stream, *t_int32, *t_float16, *t_bfloat16, *t_float32;
 static __typeof__(&attn_rope_run) rope_run;
 static __typeof__(&attn_prompt_run) prompt_run;
 static __typeof__(&attn_cache_write) cache_write;
@@ -30,6 +31,7 @@ static __typeof__(&attn_cache_read) cache_read;
 static __typeof__(&attn_cache_attend) cache_attend;
 static __typeof__(&gemm_row_groups) group_rows;
 static __typeof__(&gemm_grouped_run) grouped_run;
+static __typeof__(&gemm_adapters_run) adapters_run;
 
 typedef struct {
   void* ptr;
@@ -307,10 +309,33 @@ static PyObject* py_grouped(PyObject* self, PyObject* const* args, Py_ssize_t na
                             C.ptr, ldc, m > 0 ? C.stride[0] : 0, stream));
 }
 
-/* the addresses of the functions over groups of rows */
+/* (the description's address, dtype, groups, N, K, rank), x, A, B, offsets, order (or None), base, out, scales (or None),
+ * stream */
+static PyObject* py_adapters(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  view x, A, B, offsets, order = {0}, base, out, scales = {0};
+  void* stream;
+  int64_t device = -1;
+  TAKES(10);
+  PyObject *h = args[0], *dtype = PyTuple_GET_ITEM(h, 1);
+  const int64_t groups = whole(h, 2), n = whole(h, 3), k = whole(h, 4), rank = whole(h, 5);
+  if (!look_matrix(args[1], dtype, -1, k, &x, &device) || !look_matrices(args[2], dtype, groups, rank, k, &A, &device) ||
+      !A.contiguous || !look_matrices(args[3], dtype, groups, n, rank, &B, &device) || !B.contiguous ||
+      !look_vector(args[4], t_int32, groups + 1, &offsets, &device) ||
+      (args[5] != Py_None && !look_vector(args[5], t_int32, x.dim[0], &order, &device)) ||
+      !look_matrix(args[6], dtype, x.dim[0], n, &base, &device) || !look_matrix(args[7], dtype, x.dim[0], n, &out, &device) ||
+      (args[8] != Py_None && !look_vector(args[8], t_float32, groups, &scales, &device)))
+    return refused();
+  STREAM(args[9]);
+  return status(adapters_run(address(h, 0), x.ptr, x.stride[0], A.ptr, B.ptr, scales.ptr, offsets.ptr, order.ptr, x.dim[0],
+                             base.ptr, base.stride[0], out.ptr, out.stride[0], stream));
+}
+
+/* the addresses of the functions over groups of rows, and torch's float32 */
 static PyObject* py_setup_groups(PyObject* self, PyObject* args) {
-  PyObject *order, *grouped;
-  if (!PyArg_ParseTuple(args, "OO", &order, &grouped)) return NULL;
+  PyObject *order, *grouped, *adapters;
+  if (!PyArg_ParseTuple(args, "OOOO", &order, &grouped, &adapters, &t_float32)) return NULL;
+  Py_INCREF(t_float32);
+  adapters_run = (__typeof__(adapters_run))PyLong_AsVoidPtr(adapters);
   group_rows = (__typeof__(group_rows))PyLong_AsVoidPtr(order);
   grouped_run = (__typeof__(grouped_run))PyLong_AsVoidPtr(grouped);
   if (PyErr_Occurred()) return NULL;
@@ -348,6 +373,7 @@ static PyMethodDef methods[] = {
     {"setup_groups", py_setup_groups, METH_VARARGS, NULL},
     {"row_groups", (PyCFunction)(void (*)(void))py_row_groups, METH_FASTCALL, NULL},
     {"grouped", (PyCFunction)(void (*)(void))py_grouped, METH_FASTCALL, NULL},
+    {"adapters", (PyCFunction)(void (*)(void))py_adapters, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -33,6 +33,7 @@
 #include <new>
 
 #include "gemm_grouped.h"
+#include "groups.cuh"
 #include "half_types.cuh"
 #include "kernels.h"
 #include "plan.h"
@@ -91,57 +92,6 @@ struct GroupedCfg {
   static constexpr uint32_t STEP = PAIR ? 32 : 16;  // of the product's N
 };
 
-__device__ __forceinline__ uint32_t scan_max(uint32_t v) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) >= o) v = max(v, y);
-  }
-  return v;
-}
-__device__ __forceinline__ uint32_t scan_add(uint32_t v) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) >= o) v += y;
-  }
-  return v;
-}
-
-// The groups' first rows (never decreasing, never past the last row) and, along
-// M, their first tiles, by the whole CTA.
-__device__ __forceinline__ void grouped_tables(const GroupedArgs& a, uint32_t* off, uint32_t* first, uint32_t* scratch) {
-  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t n = static_cast<uint32_t>(a.groups) + 1;
-  const uint32_t per = (n + kGgThreads - 1) / kGgThreads;
-  const uint32_t lo = min(tid * per, n), hi = min(lo + per, n);
-  uint32_t most = 0;
-  for (uint32_t i = lo; i < hi; ++i) {
-    most = max(most, static_cast<uint32_t>(min(max(a.offsets[i], 0), a.rows)));
-    off[i] = most;
-  }
-  uint32_t upto = scan_max(most);
-  if (lane == 31) scratch[warp] = upto;
-  __syncthreads();
-  uint32_t before = __shfl_up_sync(0xffffffffu, upto, 1);
-  if (lane == 0) before = 0;
-  for (uint32_t w = 0; w < warp; ++w) before = max(before, scratch[w]);
-  for (uint32_t i = lo; i < hi; ++i) off[i] = max(off[i], before);
-  if (a.along_k) return;  // (the caller's barrier follows)
-  __syncthreads();
-  uint32_t sum = 0;
-  for (uint32_t i = lo; i < hi; ++i) {
-    first[i] = sum;
-    if (i + 1 < n) sum += (off[i + 1] - off[i] + a.q_most - 1) / a.q_most * a.p_tiles;
-  }
-  upto = scan_add(sum);
-  if (lane == 31) scratch[8 + warp] = upto;
-  __syncthreads();
-  before = upto - sum;
-  for (uint32_t w = 0; w < warp; ++w) before += scratch[8 + w];
-  for (uint32_t i = lo; i < hi; ++i) first[i] += before;
-}
-
 template <bool PAIR>
 struct GroupedWork {
   const uint32_t *off, *first;
@@ -167,13 +117,7 @@ struct GroupedWork {
       t.len = static_cast<int32_t>(off[g + 1] - off[g]);
       t.nkb = (t.len + TILE_K - 1) / TILE_K;
     } else {
-      // the last group whose first tile is not past this one (one without tiles has its successor's)
-      uint32_t g = 0, n = static_cast<uint32_t>(a.groups);
-      while (n > 1) {
-        const uint32_t half = n >> 1;
-        if (first[g + half] <= u) g += half;
-        n -= half;
-      }
+      const uint32_t g = group_of(first, a.groups, u);
       const uint32_t r = u - first[g], len = off[g + 1] - off[g];
       const uint32_t qt = (len + a.q_most - 1) / a.q_most;
       const uint32_t width = ((len + qt - 1) / qt + STEP - 1) / STEP * STEP;
@@ -211,7 +155,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + epi_off + kGgEpiBytes + kGgBars * 8);
   volatile uint32_t* tmem_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  uint32_t* off = misc + 20;  // (16 words of the scan's lie between)
+  uint32_t* off = misc + 36;  // (32 words of the scan's lie between)
   uint32_t* first = off + a.groups + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -263,7 +207,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     }
   }
   pdl_wait();  // (the operands, the offsets and C may be the previous kernel's)
-  grouped_tables(a, off, first, misc + 4);
+  group_tables<kGgThreads>(a.offsets, a.groups, a.rows, a.along_k ? 0u : a.q_most, a.p_tiles, off, first, misc + 4);
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();
@@ -641,7 +585,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     tiles = (rows / a.q_most + busy) * a.p_tiles;
   }
   if (tiles >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
-  const uint32_t tables = 96 + 2 * static_cast<uint32_t>(d.groups + 1) * 4;
+  const uint32_t tables = 144 + 2 * static_cast<uint32_t>(d.groups + 1) * 4;
   a.stages = std::min<uint32_t>(kGgMaxStages, (kGgSmem - 1024 - kGgEpiBytes - kGgBars * 8 - tables) / a.stage_bytes);
 
   // (no rows: nothing is copied, any valid address will do)

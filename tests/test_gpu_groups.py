@@ -183,3 +183,59 @@ def test_sums_strided_padded(m):
 def test_sums_many_groups(m, groups):
     r = random.Random(groups)
     _check_sums(m, [r.choice((0, 1, 2, 40, 100)) for _ in range(groups)], 72, 136, "bf16", seed=groups)
+
+
+# ------------------------------------------------------------------ adapters
+
+def _check_adapters(m, sizes, none, n, k, rank, dtype, order=True, scaled=True, in_place=False, extra=(0, 0, 0), ints=True, start=0, seed=0):
+    t, rows, groups = TD[dtype], sum(sizes) + none + start, len(sizes)
+    g = torch.Generator(device="cuda").manual_seed(seed + 9)
+    if ints:
+        x, base = _ints(seed, rows, k, dtype=t), _ints(seed + 1, rows, n, dtype=t, most=9)
+        a, b = _ints(seed + 2, groups, rank, k, dtype=t, most=1), _ints(seed + 3, groups, n, rank, dtype=t, most=1)
+        scales = (torch.randint(1, 5, (groups,), generator=g, device="cuda") / 2).float() if scaled else None
+    else:
+        def normal(*shape, scale=1.0):
+            return (torch.randn(shape, generator=g, device="cuda") * scale).to(t)
+        x, base, a, b = normal(rows, k), normal(rows, n), normal(groups, rank, k, scale=k**-0.5), normal(groups, n, rank, scale=0.3)
+        scales = torch.rand(groups, generator=g, device="cuda") if scaled else None
+    x, base = _pitched(x, extra[0]), _pitched(base, extra[1])
+    out = base if in_place else _pitched(torch.full((rows, n), -77.0, dtype=t, device="cuda"), extra[2])
+    offsets, at = _offsets(sizes, start), np.concatenate([[0], np.cumsum(sizes)]) + start
+    perm = torch.randperm(rows, generator=g, device="cuda") if order else torch.arange(rows, device="cuda")
+    want, size = base.double(), base.double().abs()
+    for e in range(groups):
+        r = perm[at[e]:at[e + 1]]
+        s = scales[e].double() if scaled else 1.0
+        u = x[r].double() @ a[e].double().T
+        want[r] += s * (u @ b[e].double().T)
+        size[r] += s * ((x[r].double().abs() @ a[e].double().abs().T) * 2.0**-20 + u.abs().amax(-1, keepdim=True) * 2.0**-16) @ b[e].double().abs().T
+    m.Adapters(groups, n, k, rank, dtype=_code(m, dtype)).run(x, a, b, offsets, perm.int() if order else None, base, out, scales=scales)
+    if ints:
+        # u below 2^15 in magnitude is held exactly by the pair: 8 + 8 bits (bf16) or 11 + 11 of the row's largest
+        assert torch.equal(out, want.to(t)), (out != want.to(t)).nonzero()[:5]
+    else:
+        # u's own rounding and its pair's (2^-16 of the row's largest), then the result's
+        tolerance = want.abs() * torch.finfo(t).eps / 2 + (size - want.abs()).clamp(min=0) + base.double().abs() * 2.0**-20
+        assert ((out.double() - want).abs() <= tolerance).all(), ((out.double() - want).abs() - tolerance).max()
+
+
+@pytest.mark.parametrize("sizes,none", [([1], 0), ([0, 1, 0, 0], 0), ([1, 2, 1, 0, 1], 3), ([8, 9, 7], 1), ([1] * 60, 4), ([0, 0], 5),
+                                        ([33, 0, 64, 200], 7), ([700, 300], 0), ([5] * 150, 50), ([3000], 0), ([1] * 400, 1)])
+@pytest.mark.parametrize("n,k,rank", [(8, 8, 8), (136, 72, 16), (1000, 2056, 24), (4096, 512, 64), (264, 1024, 128)])
+def test_adapters(m, sizes, none, n, k, rank):
+    i = len(sizes) + rank
+    _check_adapters(m, sizes, none, n, k, rank, "bf16" if i % 2 else "f16", order=i % 3 > 0, scaled=i % 5 > 0, in_place=i % 4 == 0, seed=i)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rank", [8, 40, 64, 88])
+def test_adapters_normal(m, dtype, rank):
+    _check_adapters(m, [1, 0, 30, 2], 3, 520, 1032, rank, dtype, ints=False, seed=rank)
+    _check_adapters(m, [100, 60, 0], 9, 520, 1032, rank, dtype, ints=False, order=False, seed=rank + 1)
+
+
+def test_adapters_strided(m):
+    _check_adapters(m, [3, 0, 20], 2, 264, 136, 16, "f16", extra=(8, 16, 24), start=4, seed=1)
+    _check_adapters(m, [200, 111, 300], 50, 264, 136, 32, "bf16", extra=(0, 8, 16), order=False, start=7, seed=2)
+    _check_adapters(m, [40, 1], 50, 264, 136, 32, "bf16", extra=(8, 8, 8), in_place=True, seed=2)
