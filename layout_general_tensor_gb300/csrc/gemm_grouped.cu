@@ -273,9 +273,13 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (leader && lane == 0) {
-      const uint32_t p_step = a.p_mn ? 2048u : 32u, q_step = a.along_k ? 2048u : 32u;
-      const uint32_t p_lbo = a.p_mn ? kGgChunk : 16u, q_lbo = a.along_k ? kGgChunk : 16u;
+    // (the elected thread's operands go through uniform registers; descriptors are
+    // one sum each, since this thread's own instructions are the pace)
+    if (leader && elect_one()) {
+      const uint32_t p_step = (a.p_mn ? 2048u : 32u) >> 4, q_step = (a.along_k ? 2048u : 32u) >> 4;
+      const uint64_t p_desc = sw128_desc(base, a.p_mn ? kGgChunk : 16u, 1024u);
+      const uint64_t q_desc = sw128_desc(base + kGgPBytes, a.along_k ? kGgChunk : 16u, 1024u);
+      const uint32_t stage_step = a.stage_bytes >> 4;
       uint32_t s = 0, phase = 0, uses = 0, fixes = 0;
       bool ok = true;
       while (ok && work.next(a, t)) {
@@ -287,22 +291,20 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         const uint32_t idesc = a.idesc | (t.cols >> 3) << 17;
         for (int kb = 0; kb < t.nkb; ++kb) {
           if (!(ok = wait(full(s), phase))) break;
-          uint32_t from, to;
-          if (tail_rows(a, t, kb, from, to)) {
+          uint32_t from, to = TILE_K;
+          if (a.along_k && tail_rows(a, t, kb, from, to)) {
             if (!(ok = wait(fixed(s), fixes >> s & 1u))) break;
             fixes ^= 1u << s;
           }
           tc_fence_after();
-          const uint32_t sp = base + s * a.stage_bytes, sq = sp + kGgPBytes;
+          const uint64_t pd = p_desc + s * stage_step, qd = q_desc + s * stage_step;
 #pragma unroll
           for (uint32_t k = 0; k < TILE_K / 16; ++k) {
             if (k * 16 >= to) break;
-            const uint64_t pd = sw128_desc(sp + k * p_step, p_lbo, 1024u);
-            const uint64_t qd = sw128_desc(sq + k * q_step, q_lbo, 1024u);
             if constexpr (PAIR)
-              tc_mma_f16_ss_pair(d, pd, qd, idesc, (kb | k) != 0 ? 1u : 0u);
+              tc_mma_f16_ss_pair(d, pd + k * p_step, qd + k * q_step, idesc, (kb | k) != 0 ? 1u : 0u);
             else
-              tc_mma_f16_ss(d, pd, qd, idesc, (kb | k) != 0 ? 1u : 0u);
+              tc_mma_f16_ss(d, pd + k * p_step, qd + k * q_step, idesc, (kb | k) != 0 ? 1u : 0u);
           }
           if constexpr (PAIR)
             tc_commit_pair_mc(empty(s), 0x3);

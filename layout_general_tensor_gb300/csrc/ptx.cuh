@@ -21,6 +21,13 @@ __device__ __forceinline__ uint32_t elect_lane0() {
   return (threadIdx.x & 31u) == 0u;
 }
 
+// Whether this lane is the one that issues for its (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------ programmatic dependent launch
 // A kernel launched with programmatic stream serialization may start while
 // the previous kernel in its stream is still running.  `pdl_launch_dependents`
