@@ -69,7 +69,10 @@ struct GroupedArgs {
   uint32_t p_tiles, q_most;
   uint32_t q_tiles, q_width;  // along K
   uint32_t q_box;             // along M: rows of an N-side copy, of each CTA
-  uint32_t q_chunks;          // along K: copies of 64 columns, of each CTA
+  uint32_t q_chunks;          // along K: stretches of 64 columns, of each CTA
+  uint32_t p_boxes, q_boxes;  // copies of a stage's operand
+  int32_t p_whole, q_whole;   // the one copy is of several stretches
+  uint32_t q_step;            // along K: what a tile's columns are a multiple of
   uint32_t stages, stage_bytes;
   int32_t p_mn;
   uint32_t idesc;  // without N
@@ -128,7 +131,8 @@ struct GroupedWork {
       t.count = min(width, len - q);
       t.nkb = a.kb_total;
     }
-    t.cols = (t.count + STEP - 1) / STEP * STEP;
+    const uint32_t multiple = a.along_k ? a.q_step : STEP;
+    t.cols = (t.count + multiple - 1) / multiple * multiple;
     return true;
   }
 };
@@ -222,14 +226,14 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   GroupedTile t;
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ copies
-    if (lane == 0) {
+    if (elect_one()) {
       const bool is_p = warp == 0;
       const CUtensorMap* tm = is_p ? &a.tm_p : &a.tm_q;
       const uint32_t at = is_p ? 0u : kGgPBytes;
       const uint32_t bytes = is_p ? kGgPBytes : a.along_k ? a.q_chunks * kGgChunk : a.q_box * TILE_K * 2;
-      const uint32_t boxes = is_p ? (a.p_mn ? 2u : 1u) : a.along_k ? a.q_chunks : 1u;
-      // coordinates: whether the box runs along K first
-      const bool k_first = is_p ? !a.p_mn : !a.along_k;
+      const uint32_t boxes = is_p ? a.p_boxes : a.q_boxes;
+      // coordinates: whether the box runs along K first; whether it is all of the stage's stretches
+      const bool k_first = is_p ? !a.p_mn : !a.along_k, whole = is_p ? a.p_whole : a.q_whole;
       uint32_t s = 0, phase = 0, issued = 0;
       bool ok = true;
       while (ok && work.next(a, t)) {
@@ -252,14 +256,15 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
           }
           const uint32_t dst = base + s * a.stage_bytes + at;
           const int32_t k = k0 + kb * TILE_K;
-          for (uint32_t j = 0; j < boxes; ++j) {
-            const int32_t x = x0 + static_cast<int32_t>(64 * j);
-            if (a.withhold && !is_p && blockIdx.x == 0 && issued == 0) continue;
-            if constexpr (PAIR)
-              tma_load_3d_pair(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, z);
-            else
-              tma_load_3d(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, z);
-          }
+          const int32_t stretch = whole ? x0 >> 6 : 0;
+          if (!(a.withhold && !is_p && blockIdx.x == 0 && issued == 0))
+            for (uint32_t j = 0; j < boxes; ++j) {
+              const int32_t x = whole ? 0 : x0 + static_cast<int32_t>(64 * j);
+              if constexpr (PAIR)
+                tma_load_4d_pair(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, stretch, z);
+              else
+                tma_load_4d(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, stretch, z);
+            }
           ++issued;
           if (++s == a.stages) {
             s = 0;
@@ -454,16 +459,22 @@ cudaError_t launch_grouped(const GroupedArgs& a, bool pair, bool bf16, unsigned 
   return bf16 ? launch_grouped_as<false, true>(a, workers, stream) : launch_grouped_as<false, false>(a, workers, stream);
 }
 
-// [d2][d1][d0] with pitches s1 and s2 in elements, boxes of 64 x box1.
-bool encode_3d(CUtensorMap* map, const void* ptr, bool bf16, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2,
-               uint32_t box1) {
+// A matrix [d2][d1][d0] with pitches s1 and s2 in elements, by boxes of 64 of d0
+// times box1 of d1.  `stretches` > 1 of them, next to each other along d0, are one
+// box, one after the other in shared memory: d0 in pieces of 64 is a dimension of
+// its own then (d0 has to be a multiple of 64, or the last piece of the last row
+// would reach past the matrix).
+bool encode_matrices(CUtensorMap* map, const void* ptr, bool bf16, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2,
+                     uint32_t box1, uint32_t stretches) {
   auto enc = get_encoder();
   if (!enc) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
-  cuuint32_t box[3] = {64, box1, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims,
+  const bool cut = stretches > 1;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(cut ? 64 : d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(cut ? d0 / 64 : 1),
+                        static_cast<cuuint64_t>(d2)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(s1) * 2, 128, static_cast<cuuint64_t>(s2) * 2};
+  cuuint32_t box[4] = {64, box1, stretches, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims,
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -570,11 +581,19 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   const uint32_t ctas = pair ? 2 : 1, step = pair ? 32 : 16;
   a.p_tiles = static_cast<uint32_t>((d.N + kGgRows * ctas - 1) / (kGgRows * ctas));
   int64_t tiles;
+  // Operands that run along n or m: one copy a stage where the matrix is whole
+  // stretches of 64 (the copying thread is held for each: 4096 x 4096 of
+  // [k][n], 16 groups of 1024 rows, P_ONE us against P_TWO), else one a stretch.
+  const bool p_whole = b_mn && d.N % 64 == 0, q_whole = along_k && d.M % 64 == 0;
+  a.p_boxes = b_mn && !p_whole ? 2 : 1;
+  a.q_boxes = 1;
+  a.q_step = q_whole ? 64 * ctas : step;
   if (along_k) {
     a.q_tiles = static_cast<uint32_t>((d.M + kGgMost - 1) / kGgMost);
-    a.q_width = static_cast<uint32_t>(up((d.M + a.q_tiles - 1) / a.q_tiles, step));
+    a.q_width = static_cast<uint32_t>(up((d.M + a.q_tiles - 1) / a.q_tiles, a.q_step));
     a.q_most = a.q_width;
     a.q_chunks = (a.q_width / ctas + 63) / 64;
+    if (!q_whole) a.q_boxes = a.q_chunks;
     a.stage_bytes = kGgPBytes + a.q_chunks * kGgChunk;
     tiles = static_cast<int64_t>(d.groups) * a.p_tiles * a.q_tiles;
   } else {
@@ -594,11 +613,14 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   const void* ap = rows > 0 ? A : C;
   const void* bp = rows > 0 ? B : C;
   const int64_t some = std::max<int64_t>(rows, 1);
+  const uint32_t p_stretches = p_whole ? 2 : 1, q_stretches = q_whole ? a.q_chunks : 1;
+  a.p_whole = p_stretches > 1;
+  a.q_whole = q_stretches > 1;
   const bool encoded =
-      along_k ? encode_3d(&a.tm_p, bp, bf16, d.N, some, 1, ldb, ldb, 64) &&
-                    encode_3d(&a.tm_q, ap, bf16, d.M, some, 1, lda, lda, 64)
-              : encode_3d(&a.tm_p, bp, bf16, b_row, b_rows, d.groups, ldb, b_stride, b_mn ? 64 : kGgRows) &&
-                    encode_3d(&a.tm_q, ap, bf16, d.K, some, 1, lda, lda, a.q_box);
+      along_k ? encode_matrices(&a.tm_p, bp, bf16, d.N, some, 1, ldb, ldb, 64, p_stretches) &&
+                    encode_matrices(&a.tm_q, ap, bf16, d.M, some, 1, lda, lda, 64, q_stretches)
+              : encode_matrices(&a.tm_p, bp, bf16, b_row, b_rows, d.groups, ldb, b_stride, b_mn ? 64 : kGgRows, p_stretches) &&
+                    encode_matrices(&a.tm_q, ap, bf16, d.K, some, 1, lda, lda, a.q_box, 1);
   if (!encoded) return GEMM_ERR_CUDA;
   a.c = static_cast<uint16_t*>(C);
   a.offsets = offsets;
