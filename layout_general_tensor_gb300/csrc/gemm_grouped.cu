@@ -23,10 +23,10 @@
 // at most 15 of them, since the product's steps are 16 deep and whole steps are
 // left out.
 //
-// Roles (256 threads; pairs: in both CTAs):
-//   warp 0      copies of the M side        warp 6  copies of the N side
+// Roles (384 threads; pairs: in both CTAs):
+//   warp 0      copies of the M side        warp 10  copies of the N side
 //   warp 1      tensor memory; issues the products (the even CTA of a pair)
-//   warps 2..5  results      warp 7  clears the last block's rows (along K)
+//   warps 2..9  results      warp 11  clears the last block's rows (along K)
 #include <algorithm>
 #include <cstdint>
 #include <cstdlib>
@@ -42,15 +42,18 @@
 namespace lgt {
 namespace {
 
-constexpr int kGgThreads = 256;
+constexpr int kGgThreads = 384;
 constexpr int kGgEpiWarp0 = 2;
+constexpr int kGgEpiWarps = 8;
+constexpr int kGgQWarp = kGgEpiWarp0 + kGgEpiWarps;
+constexpr int kGgClearWarp = kGgQWarp + 1;
 constexpr int kGgMaxGroups = 1024;
 constexpr uint32_t kGgRows = 128;                       // M-side rows a CTA
 constexpr uint32_t kGgPBytes = kGgRows * TILE_K * 2;    // 16 KiB of them a stage
 constexpr uint32_t kGgChunk = 64 * TILE_K * 2;          // a box of 64 x 64 values along n or m
 constexpr uint32_t kGgMost = 256;                       // N-side columns of a tile
 constexpr uint32_t kGgMaxStages = 12;
-constexpr uint32_t kGgEpiBytes = 4 * 2048;              // a warp's 32 rows of C, 32 values each
+constexpr uint32_t kGgEpiBytes = kGgEpiWarps * 2048;              // a warp's 32 rows of C, 32 values each
 constexpr uint32_t kGgBars = 4 * kGgMaxStages + 5;      // full, empty, tail, fixed; accumulators full, empty; end
 constexpr uint32_t kGgSmem = 227 * 1024;
 constexpr uint64_t kGgSettleNs = 200ull * 1000ull * 1000ull;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf(b), 1);
-      mbar_init(acce(b), 4 * CTAS);
+      mbar_init(acce(b), kGgEpiWarps * CTAS);
     }
     mbar_init(end_bar, 1);
     *abort_flag = 0;
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
 
   GroupedWork<PAIR> work(a, off, first);
   GroupedTile t;
-  if (warp == 0 || warp == 6) {
+  if (warp == 0 || warp == kGgQWarp) {
     // ------------------------------------------------------------ copies
     if (elect_one()) {
       const bool is_p = warp == 0;
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         ++uses;
       }
     }
-  } else if (warp == 7) {
+  } else if (warp == kGgClearWarp) {
     // ------------------------------------------------------------ rows of the next group
     if (a.along_k) {
       uint32_t s = 0, done = 0;
@@ -377,7 +380,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       const int32_t n = t.p0 + static_cast<int32_t>(rank * kGgRows + quad * 32u + piece * 8u);
       const bool inside = n < a.n;
       uint16_t* out = a.c + (a.along_k ? t.group * a.c_stride : 0) + static_cast<int64_t>(t.q0) * a.ldc + n;
-      for (uint32_t c = 0; c < t.count; c += 32) {
+      // (two warps have the same lanes; each takes every other 32 columns)
+      for (uint32_t c = static_cast<uint32_t>(warp - kGgEpiWarp0) / 4 * 32; c < t.count; c += 64) {
         uint32_t x[16], y[16];
         if (t.nkb > 0) {
           tc_ld_16x256b_x4(d + c, x);
