@@ -79,7 +79,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
 gemm_status_t gemm_grouped_sync_status(gemm_grouped_plan_t* plan, void* stream);
 
 /* Test aid for failure detection, without a fault: the plan's next run leaves
- * out one CTA's first load of B, so waits run out after the plan's limit
+ * out one CTA's first load of A's rows, so waits run out after the plan's limit
  * (LGT_GEMM_WAIT_LIMIT_MS at gemm_grouped_create, 2 s by default), the kernel
  * winds down and the run's status is GEMM_ERR_TIMEOUT; runs after it are
  * normal. */

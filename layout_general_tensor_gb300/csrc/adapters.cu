@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
   const uint32_t rank = a.ctas > 1 ? cluster_ctarank() : 0u;
 
   pdl_wait();
-  group_tables<kAdThreads>(a.offsets, a.groups, a.rows, C::TOK, 1u, off, first, scratch);
+  group_rows<kAdThreads>(a.offsets, a.groups, a.rows, off, scratch);
+  __syncthreads();
+  group_tiles<kAdThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + C::TOK - 1) / C::TOK; }, first, scratch + 16);
   __syncthreads();
   const uint32_t tiles = first[a.groups], clusters = gridDim.x / a.ctas;
   const int steps = (a.k + 31) / 32, blocks = (a.n + 31) / 32;

@@ -12,16 +12,21 @@
 // for rows of another group are computed and not stored; they touch no other.
 //
 // Work.  The sizes are on the device, so every CTA sums them up itself (a scan
-// over the group's tiles in shared memory) and takes every G-th tile, G the
+// over the groups' tiles in shared memory) and takes every G-th tile, G the
 // CTAs or pairs: no launch depends on a size.  Within a group the tiles of one
-// stretch of n follow each other, so that they read its weights together.
+// stretch of n follow each other, so that they read its weights together.  (Groups
+// with the largest tiles first would leave small ones for the last round, but
+// few rows and many weights then meet at the end: 4000 rows of 24 groups, 3000 x
+// 2880, 85 to 88 us, and 16384 rows of 16 groups no better.)
 //
-// Groups along K end inside a block of 64 rows.  What the block holds beyond is
-// the next group's, and a zero on one side would not cancel an infinity on the
-// other, so those rows of both operands are cleared in shared memory between
-// the copy and the product, by a warp of each CTA that has nothing else to do:
-// at most 15 of them, since the product's steps are 16 deep and whole steps are
-// left out.
+// Groups along K.  The product's steps are 16 rows deep; what is left of a group
+// behind its last whole step shares a step with the next group's rows, and a zero
+// on one side would not cancel an infinity on the other.  So those rows have a
+// small buffer of their own (16 rows of both operands, two of them), loaded as the
+// tile begins, in which a warp of each CTA that has nothing else to do clears the
+// rows beyond, and the product takes that step last.  (Cleared in the last block
+// of 64 on its way through the ring, each tile waited for it: 16 groups of 1000
+// rows, 2048 x 4096, 207 us against 157 for groups of 1024.)
 //
 // Roles (384 threads; pairs: in both CTAs):
 //   warp 0      copies of the M side        warp 10  copies of the N side
@@ -54,12 +59,14 @@ constexpr uint32_t kGgChunk = 64 * TILE_K * 2;          // a box of 64 x 64 valu
 constexpr uint32_t kGgMost = 256;                       // N-side columns of a tile
 constexpr uint32_t kGgMaxStages = 12;
 constexpr uint32_t kGgEpiBytes = kGgEpiWarps * 2048;              // a warp's 32 rows of C, 32 values each
-constexpr uint32_t kGgBars = 4 * kGgMaxStages + 5;      // full, empty, tail, fixed; accumulators full, empty; end
+constexpr uint32_t kGgStep = 16 * 128;                  // a step's 16 rows of 64 values along n or m
+constexpr uint32_t kGgBars = 2 * kGgMaxStages + 11;     // full, empty; rest landed, cleared, empty; accumulators full, empty; end
 constexpr uint32_t kGgSmem = 227 * 1024;
 constexpr uint64_t kGgSettleNs = 200ull * 1000ull * 1000ull;
 
 struct GroupedArgs {
   CUtensorMap tm_p, tm_q;
+  CUtensorMap tm_pr, tm_qr;  // along K: boxes of one step
   uint16_t* c;
   const int32_t* offsets;
   DeviceStatus* status;
@@ -88,8 +95,10 @@ struct GroupedTile {
   int32_t p0, q0;     // its first n; its first column of the N side (along M: a row of A)
   uint32_t count;     // columns to store
   uint32_t cols;      // of the product
-  int32_t row0, len;  // along K: the group's rows
-  int32_t nkb;
+  int32_t row0;       // along K: the group's first row
+  int32_t steps;      // of the product, of 16
+  int32_t nkb;        // blocks of 64 that hold them
+  int32_t rest;       // along K: rows behind them
 };
 
 template <bool PAIR>
@@ -116,38 +125,31 @@ struct GroupedWork {
       const uint32_t g = u / (a.p_tiles * a.q_tiles), r = u - g * (a.p_tiles * a.q_tiles), p = r / a.q_tiles;
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
-      const uint32_t q0 = (r - p * a.q_tiles) * a.q_width;
+      const uint32_t q0 = (r - p * a.q_tiles) * a.q_width, len = off[g + 1] - off[g];
       t.q0 = static_cast<int32_t>(q0);
       t.count = min(a.q_width, static_cast<uint32_t>(a.m) - q0);
+      t.cols = (t.count + a.q_step - 1) / a.q_step * a.q_step;
       t.row0 = static_cast<int32_t>(off[g]);
-      t.len = static_cast<int32_t>(off[g + 1] - off[g]);
-      t.nkb = (t.len + TILE_K - 1) / TILE_K;
+      t.steps = static_cast<int32_t>(len >> 4);
+      t.rest = static_cast<int32_t>(len & 15u);
     } else {
       const uint32_t g = group_of(first, a.groups, u);
       const uint32_t r = u - first[g], len = off[g + 1] - off[g];
-      const uint32_t qt = (len + a.q_most - 1) / a.q_most;
-      const uint32_t width = ((len + qt - 1) / qt + STEP - 1) / STEP * STEP;
-      const uint32_t p = r / qt, q = (r - p * qt) * width;
+      const uint32_t tiles = (len + a.q_most - 1) / a.q_most;
+      const uint32_t width = ((len + tiles - 1) / tiles + STEP - 1) / STEP * STEP;
+      const uint32_t p = r / tiles, q = (r - p * tiles) * width;
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
       t.q0 = static_cast<int32_t>(off[g] + q);
       t.count = min(width, len - q);
-      t.nkb = a.kb_total;
+      t.cols = (t.count + STEP - 1) / STEP * STEP;
+      t.steps = a.kb_total * (TILE_K / 16);  // (the last block's end is zeros)
+      t.rest = 0;
     }
-    const uint32_t multiple = a.along_k ? a.q_step : STEP;
-    t.cols = (t.count + multiple - 1) / multiple * multiple;
+    t.nkb = (t.steps + TILE_K / 16 - 1) / (TILE_K / 16);
     return true;
   }
 };
-
-// Rows of the last block that the product takes and that are another group's: [from, to).
-__device__ __forceinline__ bool tail_rows(const GroupedArgs& a, const GroupedTile& t, int kb, uint32_t& from, uint32_t& to) {
-  to = TILE_K;
-  if (!a.along_k || kb + 1 < t.nkb) return false;
-  from = static_cast<uint32_t>(t.len - kb * TILE_K);
-  to = (from + 15) & ~15u;
-  return from < to;
-}
 
 template <bool PAIR, bool BF16>
 __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
@@ -157,7 +159,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw_base);
-  const uint32_t epi_off = a.stages * a.stage_bytes;
+  const uint32_t rest_off = a.stages * a.stage_bytes;
+  const uint32_t rest_bytes = a.along_k ? (2 + a.q_chunks) * kGgStep : 0u;  // each of two
+  const uint32_t epi_off = rest_off + 2 * rest_bytes;
   const uint32_t bar0 = base + epi_off + kGgEpiBytes;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + epi_off + kGgEpiBytes + kGgBars * 8);
   volatile uint32_t* tmem_slot = misc;
@@ -170,11 +174,12 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   const bool leader = rank == 0;
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty = [&](uint32_t s) { return bar0 + 8u * (kGgMaxStages + s); };
-  auto tail = [&](uint32_t s) { return bar0 + 8u * (2 * kGgMaxStages + s); };
-  auto fixed = [&](uint32_t s) { return bar0 + 8u * (3 * kGgMaxStages + s); };
-  auto accf = [&](int b) { return bar0 + 8u * (4 * kGgMaxStages + b); };
-  auto acce = [&](int b) { return bar0 + 8u * (4 * kGgMaxStages + 2 + b); };
-  const uint32_t end_bar = bar0 + 8u * (4 * kGgMaxStages + 4);
+  auto landed = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + b); };
+  auto cleared = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + 2 + b); };
+  auto rest_empty = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + 4 + b); };
+  auto accf = [&](int b) { return bar0 + 8u * (2 * kGgMaxStages + 6 + b); };
+  auto acce = [&](int b) { return bar0 + 8u * (2 * kGgMaxStages + 8 + b); };
+  const uint32_t end_bar = bar0 + 8u * (2 * kGgMaxStages + 10);
   auto wait = [&](uint32_t bar, uint32_t parity) {
     const bool got = PAIR ? mbar_wait_bounded_cluster(bar, parity, a.wait_limit_ns, abort_flag)
                           : mbar_wait_bounded(bar, parity, a.wait_limit_ns, abort_flag);
@@ -190,10 +195,11 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     for (uint32_t s = 0; s < a.stages; ++s) {
       mbar_init(full(s), 2);      // the two copying warps (of the even CTA), and the bytes
       mbar_init(empty(s), 1);     // the products' commit, to both CTAs
-      mbar_init(tail(s), 2);      // the two copying warps of this CTA, and its bytes
-      mbar_init(fixed(s), CTAS);  // the clearing warps
     }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(landed(b), 2);      // the two copying warps of this CTA, and its bytes
+      mbar_init(cleared(b), CTAS);  // the clearing warps
+      mbar_init(rest_empty(b), 1);
       mbar_init(accf(b), 1);
       mbar_init(acce(b), kGgEpiWarps * CTAS);
     }
@@ -203,6 +209,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     fence_proxy_async_smem();
     tma_prefetch_desc(&a.tm_p);
     tma_prefetch_desc(&a.tm_q);
+    if (a.along_k) {
+      tma_prefetch_desc(&a.tm_pr);
+      tma_prefetch_desc(&a.tm_qr);
+    }
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -214,7 +224,11 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     }
   }
   pdl_wait();  // (the operands, the offsets and C may be the previous kernel's)
-  group_tables<kGgThreads>(a.offsets, a.groups, a.rows, a.along_k ? 0u : a.q_most, a.p_tiles, off, first, misc + 4);
+  group_rows<kGgThreads>(a.offsets, a.groups, a.rows, off, misc + 4);
+  __syncthreads();
+  if (!a.along_k)
+    group_tiles<kGgThreads>(
+        a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + a.q_most - 1) / a.q_most * a.p_tiles; }, first, misc + 20);
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();
@@ -222,7 +236,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   // the even CTA's barriers
   const uint32_t full_lead = PAIR ? mapa_shared(full(0), 0) : full(0);
-  const uint32_t fixed_lead = PAIR ? mapa_shared(fixed(0), 0) : fixed(0);
+  const uint32_t cleared_lead = PAIR ? mapa_shared(cleared(0), 0) : cleared(0);
   const uint32_t acce_lead = PAIR ? mapa_shared(acce(0), 0) : acce(0);
 
   GroupedWork<PAIR> work(a, off, first);
@@ -232,42 +246,43 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     if (elect_one()) {
       const bool is_p = warp == 0;
       const CUtensorMap* tm = is_p ? &a.tm_p : &a.tm_q;
+      const CUtensorMap* tm_rest = is_p ? &a.tm_pr : &a.tm_qr;
       const uint32_t at = is_p ? 0u : kGgPBytes;
+      const uint32_t chunks = is_p ? 2u : a.q_chunks;
       const uint32_t bytes = is_p ? kGgPBytes : a.along_k ? a.q_chunks * kGgChunk : a.q_box * TILE_K * 2;
       const uint32_t boxes = is_p ? a.p_boxes : a.q_boxes;
       // coordinates: whether the box runs along K first; whether it is all of the stage's stretches
       const bool k_first = is_p ? !a.p_mn : !a.along_k, whole = is_p ? a.p_whole : a.q_whole;
-      uint32_t s = 0, phase = 0, issued = 0;
+      auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t apart, uint32_t bar, int32_t x0, int32_t k, int32_t z) {
+        const int32_t stretch = whole ? x0 >> 6 : 0;
+        for (uint32_t j = 0; j < boxes; ++j) {
+          const int32_t x = whole ? 0 : x0 + static_cast<int32_t>(64 * j);
+          if constexpr (PAIR)
+            tma_load_4d_pair(dst + j * apart, map, bar, k_first ? k : x, k_first ? x : k, stretch, z);
+          else
+            tma_load_4d(dst + j * apart, map, bar, k_first ? k : x, k_first ? x : k, stretch, z);
+        }
+      };
+      uint32_t s = 0, phase = 0, issued = 0, rests = 0;
       bool ok = true;
       while (ok && work.next(a, t)) {
         const int32_t x0 = is_p ? t.p0 + static_cast<int32_t>(rank * kGgRows)
                                 : t.q0 + static_cast<int32_t>(rank * (t.cols / CTAS));
         const int32_t z = is_p && !a.along_k ? t.group : 0;
         const int32_t k0 = a.along_k ? t.row0 : 0;
+        if (t.rest > 0) {
+          const uint32_t b = rests & 1u;
+          if (!(ok = wait(rest_empty(b), (rests >> 1 & 1u) ^ 1u))) break;
+          mbar_arrive_expect_tx(landed(b), chunks * kGgStep);
+          copy(tm_rest, base + rest_off + b * rest_bytes + (is_p ? 0u : 2 * kGgStep), kGgStep,
+               PAIR ? mapa_shared(landed(b), rank) : landed(b), x0, k0 + t.steps * 16, z);
+          ++rests;
+        }
         for (int kb = 0; kb < t.nkb; ++kb) {
           if (!(ok = wait(empty(s), phase ^ 1u))) break;
-          uint32_t from, to;
-          const bool clear = tail_rows(a, t, kb, from, to);
-          // A block with rows to clear lands on this CTA's own barrier.
-          uint32_t bar = full_lead + 8u * s;
-          if (clear) {
-            bar = PAIR ? mapa_shared(tail(s), rank) : tail(s);
-            mbar_arrive_expect_tx(tail(s), bytes);
-            if (leader) mbar_arrive(full(s));
-          } else if (leader) {
-            mbar_arrive_expect_tx(full(s), bytes * CTAS);
-          }
-          const uint32_t dst = base + s * a.stage_bytes + at;
-          const int32_t k = k0 + kb * TILE_K;
-          const int32_t stretch = whole ? x0 >> 6 : 0;
+          if (leader) mbar_arrive_expect_tx(full(s), bytes * CTAS);
           if (!(a.withhold && !is_p && blockIdx.x == 0 && issued == 0))
-            for (uint32_t j = 0; j < boxes; ++j) {
-              const int32_t x = whole ? 0 : x0 + static_cast<int32_t>(64 * j);
-              if constexpr (PAIR)
-                tma_load_4d_pair(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, stretch, z);
-              else
-                tma_load_4d(dst + j * kGgChunk, tm, bar, k_first ? k : x, k_first ? x : k, stretch, z);
-            }
+            copy(tm, base + s * a.stage_bytes + at, kGgChunk, full_lead + 8u * s, x0, k0 + kb * TILE_K, z);
           ++issued;
           if (++s == a.stages) {
             s = 0;
@@ -276,8 +291,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         }
       }
       // Every commit to this CTA's barriers has arrived before it leaves.
-      const uint32_t from = issued > a.stages ? issued - a.stages : 0u;
-      for (uint32_t i = from; ok && i < issued; ++i) ok = wait(empty(i % a.stages), i / a.stages & 1u);
+      for (uint32_t i = issued > a.stages ? issued - a.stages : 0u; ok && i < issued; ++i)
+        ok = wait(empty(i % a.stages), i / a.stages & 1u);
+      for (uint32_t i = rests > 2 ? rests - 2 : 0u; ok && i < rests; ++i) ok = wait(rest_empty(i & 1u), i >> 1 & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
@@ -288,10 +304,16 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       const uint64_t p_desc = sw128_desc(base, a.p_mn ? kGgChunk : 16u, 1024u);
       const uint64_t q_desc = sw128_desc(base + kGgPBytes, a.along_k ? kGgChunk : 16u, 1024u);
       const uint32_t stage_step = a.stage_bytes >> 4;
-      uint32_t s = 0, phase = 0, uses = 0, fixes = 0;
+      auto product = [](uint32_t d, uint64_t p, uint64_t q, uint32_t idesc, uint32_t accumulate) {
+        if constexpr (PAIR)
+          tc_mma_f16_ss_pair(d, p, q, idesc, accumulate);
+        else
+          tc_mma_f16_ss(d, p, q, idesc, accumulate);
+      };
+      uint32_t s = 0, phase = 0, uses = 0, rests = 0;
       bool ok = true;
       while (ok && work.next(a, t)) {
-        if (t.nkb == 0) continue;
+        if (t.nkb == 0 && t.rest == 0) continue;
         const int buf = static_cast<int>(uses & 1u);
         if (!(ok = wait(acce(buf), (uses >> 1 & 1u) ^ 1u))) break;
         tc_fence_after();
@@ -299,20 +321,13 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         const uint32_t idesc = a.idesc | (t.cols >> 3) << 17;
         for (int kb = 0; kb < t.nkb; ++kb) {
           if (!(ok = wait(full(s), phase))) break;
-          uint32_t from, to = TILE_K;
-          if (a.along_k && tail_rows(a, t, kb, from, to)) {
-            if (!(ok = wait(fixed(s), fixes >> s & 1u))) break;
-            fixes ^= 1u << s;
-          }
           tc_fence_after();
           const uint64_t pd = p_desc + s * stage_step, qd = q_desc + s * stage_step;
+          const int here = t.steps - kb * (TILE_K / 16);
 #pragma unroll
-          for (uint32_t k = 0; k < TILE_K / 16; ++k) {
-            if (k * 16 >= to) break;
-            if constexpr (PAIR)
-              tc_mma_f16_ss_pair(d, pd + k * p_step, qd + k * q_step, idesc, (kb | k) != 0 ? 1u : 0u);
-            else
-              tc_mma_f16_ss(d, pd + k * p_step, qd + k * q_step, idesc, (kb | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < TILE_K / 16; ++k) {
+            if (k >= here) break;
+            product(d, pd + k * p_step, qd + k * q_step, idesc, (kb | k) != 0 ? 1u : 0u);
           }
           if constexpr (PAIR)
             tc_commit_pair_mc(empty(s), 0x3);
@@ -324,6 +339,18 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
           }
         }
         if (!ok) break;
+        if (t.rest > 0) {
+          const uint32_t b = rests & 1u;
+          if (!(ok = wait(cleared(b), rests >> 1 & 1u))) break;
+          tc_fence_after();
+          const uint32_t at = base + rest_off + b * rest_bytes;
+          product(d, sw128_desc(at, kGgStep, 1024u), sw128_desc(at + 2 * kGgStep, kGgStep, 1024u), idesc, t.nkb > 0 ? 1u : 0u);
+          if constexpr (PAIR)
+            tc_commit_pair_mc(rest_empty(b), 0x3);
+          else
+            tc_commit(rest_empty(b));
+          ++rests;
+        }
         if constexpr (PAIR)
           tc_commit_pair_mc(accf(buf), 0x3);
         else
@@ -334,29 +361,25 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   } else if (warp == kGgClearWarp) {
     // ------------------------------------------------------------ rows of the next group
     if (a.along_k) {
-      uint32_t s = 0, done = 0;
+      uint32_t rests = 0;
       bool ok = true;
       while (ok && work.next(a, t)) {
-        if (t.nkb == 0) continue;
-        s = (s + static_cast<uint32_t>(t.nkb) - 1) % a.stages;  // (the last block's)
-        uint32_t from, to;
-        if (tail_rows(a, t, t.nkb - 1, from, to)) {
-          if (!(ok = __all_sync(0xffffffffu, wait(tail(s), done >> s & 1u)))) break;
-          done ^= 1u << s;
-          const uint32_t at = base + s * a.stage_bytes + from * 128u + lane * 16u;
-          const uint32_t bytes = (to - from) * 128u;
-          for (uint32_t c = 0; c < 2 + a.q_chunks; ++c)
-            for (uint32_t i = lane * 16u; i < bytes; i += 512u) st_shared_v4(at + c * kGgChunk + i - lane * 16u, 0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR)
-              mbar_arrive_cluster(fixed_lead + 8u * s);
-            else
-              mbar_arrive(fixed(s));
-          }
+        if (t.rest == 0) continue;
+        const uint32_t b = rests & 1u;
+        if (!(ok = __all_sync(0xffffffffu, wait(landed(b), rests >> 1 & 1u)))) break;
+        ++rests;
+        const uint32_t at = base + rest_off + b * rest_bytes;
+        for (uint32_t c = 0; c < 2 + a.q_chunks; ++c)
+          for (uint32_t i = static_cast<uint32_t>(t.rest) * 128u + lane * 16u; i < kGgStep; i += 512u)
+            st_shared_v4(at + c * kGgStep + i, 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_cluster(cleared_lead + 8u * b);
+          else
+            mbar_arrive(cleared(b));
         }
-        if (++s == a.stages) s = 0;
       }
     }
   } else {
@@ -371,8 +394,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     uint32_t uses = 0;
     bool ok = true;
     while (ok && work.next(a, t)) {
+      const bool some = t.nkb > 0 || t.rest > 0;
       const int buf = static_cast<int>(uses & 1u);
-      if (t.nkb > 0) {
+      if (some) {
         if (!(ok = __all_sync(0xffffffffu, wait(accf(buf), uses >> 1 & 1u)))) break;
         tc_fence_after();
       }
@@ -383,7 +407,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       // (two warps have the same lanes; each takes every other 32 columns)
       for (uint32_t c = static_cast<uint32_t>(warp - kGgEpiWarp0) / 4 * 32; c < t.count; c += 64) {
         uint32_t x[16], y[16];
-        if (t.nkb > 0) {
+        if (some) {
           tc_ld_16x256b_x4(d + c, x);
           tc_ld_16x256b_x4(d + c + (16u << 16), y);
           tc_wait_ld_regs(x);
@@ -406,7 +430,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         }
         __syncwarp();
       }
-      if (t.nkb > 0) {
+      if (some) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -610,8 +634,9 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     tiles = (rows / a.q_most + busy) * a.p_tiles;
   }
   if (tiles >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
-  const uint32_t tables = 144 + 2 * static_cast<uint32_t>(d.groups + 1) * 4;
-  a.stages = std::min<uint32_t>(kGgMaxStages, (kGgSmem - 1024 - kGgEpiBytes - kGgBars * 8 - tables) / a.stage_bytes);
+  const uint32_t tables = 144 + static_cast<uint32_t>(d.groups + 1) * 8;
+  const uint32_t rest = along_k ? 2 * (2 + a.q_chunks) * kGgStep : 0;
+  a.stages = std::min<uint32_t>(kGgMaxStages, (kGgSmem - 1024 - kGgEpiBytes - kGgBars * 8 - tables - rest) / a.stage_bytes);
 
   // (no rows: nothing is copied, any valid address will do)
   const void* ap = rows > 0 ? A : C;
@@ -622,7 +647,9 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   a.q_whole = q_stretches > 1;
   const bool encoded =
       along_k ? encode_matrices(&a.tm_p, bp, bf16, d.N, some, 1, ldb, ldb, 64, p_stretches) &&
-                    encode_matrices(&a.tm_q, ap, bf16, d.M, some, 1, lda, lda, 64, q_stretches)
+                    encode_matrices(&a.tm_q, ap, bf16, d.M, some, 1, lda, lda, 64, q_stretches) &&
+                    encode_matrices(&a.tm_pr, bp, bf16, d.N, some, 1, ldb, ldb, 16, p_stretches) &&
+                    encode_matrices(&a.tm_qr, ap, bf16, d.M, some, 1, lda, lda, 16, q_stretches)
               : encode_matrices(&a.tm_p, bp, bf16, b_row, b_rows, d.groups, ldb, b_stride, b_mn ? 64 : kGgRows, p_stretches) &&
                     encode_matrices(&a.tm_q, ap, bf16, d.K, some, 1, lda, lda, a.q_box, 1);
   if (!encoded) return GEMM_ERR_CUDA;
