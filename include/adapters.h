@@ -38,6 +38,13 @@ typedef struct gemm_adapters_desc {
   int32_t dtype;   /* GEMM_F16 or GEMM_BF16 */
 } gemm_adapters_desc_t;
 
+typedef struct gemm_adapters_plan gemm_adapters_plan_t;
+
+/* Validate `desc` and make a plan (host state and a 16-byte device status word
+ * on the current device; without a device the plan's runs are refused).
+ * GEMM_ERR_INVALID_ARG, GEMM_ERR_CUDA. */
+gemm_status_t gemm_adapters_create(const gemm_adapters_desc_t* desc, gemm_adapters_plan_t** plan);
+
 /* Enqueue the pass on `stream` (a cudaStream_t; NULL = legacy default stream).
  *   x, base, out: `rows` rows of pitch x_stride, base_stride, out_stride, in
  *      elements (0 = dense; multiples of 8).  out may be base itself, with its
@@ -49,13 +56,28 @@ typedef struct gemm_adapters_desc {
  *      (as in gemm_grouped.h).  order: `rows` int32, all different; one that is no
  *      row's number is left out.  Both in device memory.
  * Device pointers, 16-byte aligned (scales, offsets and order: 4).
- * rows = 0 does nothing.
+ * rows = 0 does nothing.  The plan's device must be current.  A plan holds no
+ * workspace: runs of it may be under way at the same time.
  * GEMM_ERR_INVALID_ARG, GEMM_ERR_ALIGNMENT, GEMM_ERR_UNSUPPORTED (more than 2^30
- * rows), GEMM_ERR_CUDA (launch failure). */
-gemm_status_t gemm_adapters_run(const gemm_adapters_desc_t* desc, const void* x, int64_t x_stride, const void* A,
-                                const void* B, const float* scales, const int32_t* offsets, const int32_t* order,
-                                int64_t rows, const void* base, int64_t base_stride, void* out, int64_t out_stride,
-                                void* stream);
+ * rows), GEMM_ERR_CUDA (launch failure).  A kernel whose bounded wait ran out
+ * records GEMM_ERR_TIMEOUT in the plan's status word
+ * (gemm_adapters_sync_status); out is then invalid. */
+gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64_t x_stride, const void* A, const void* B,
+                                const float* scales, const int32_t* offsets, const int32_t* order, int64_t rows,
+                                const void* base, int64_t base_stride, void* out, int64_t out_stride, void* stream);
+
+/* Synchronise `stream`, read and clear the plan's status word: GEMM_OK or
+ * GEMM_ERR_TIMEOUT. */
+gemm_status_t gemm_adapters_sync_status(gemm_adapters_plan_t* plan, void* stream);
+
+/* Test aid for failure detection, without a fault: the plan's next run on the
+ * tensor cores' large form (many rows) leaves out one CTA's first load of A, so
+ * waits run out after the plan's limit (LGT_GEMM_WAIT_LIMIT_MS at
+ * gemm_adapters_create, 2 s by default), the kernel winds down and the run's
+ * status is GEMM_ERR_TIMEOUT; runs after it are normal. */
+gemm_status_t gemm_adapters_withhold_load(gemm_adapters_plan_t* plan);
+
+gemm_status_t gemm_adapters_destroy(gemm_adapters_plan_t* plan);
 
 #ifdef __cplusplus
 }

@@ -62,7 +62,8 @@ EXPORTS = (
     "gemm_row_groups",
     "gemm_grouped_create", "gemm_grouped_run", "gemm_grouped_sync_status", "gemm_grouped_withhold_load",
     "gemm_grouped_destroy",
-    "gemm_adapters_run",
+    "gemm_adapters_create", "gemm_adapters_run", "gemm_adapters_sync_status", "gemm_adapters_withhold_load",
+    "gemm_adapters_destroy",
 )
 
 
@@ -189,8 +190,11 @@ def _load():
         "gemm_grouped_sync_status": (ctypes.c_int, [P, P]),
         "gemm_grouped_withhold_load": (ctypes.c_int, [P]),
         "gemm_grouped_destroy": (ctypes.c_int, [P]),
-        "gemm_adapters_run": (ctypes.c_int, [ctypes.POINTER(gemm_adapters_desc_t), P, I64, P, P, P, P, P, I64, P, I64,
-                                             P, I64, P]),
+        "gemm_adapters_create": (ctypes.c_int, [ctypes.POINTER(gemm_adapters_desc_t), ctypes.POINTER(P)]),
+        "gemm_adapters_run": (ctypes.c_int, [P, P, I64, P, P, P, P, P, I64, P, I64, P, I64, P]),
+        "gemm_adapters_sync_status": (ctypes.c_int, [P, P]),
+        "gemm_adapters_withhold_load": (ctypes.c_int, [P]),
+        "gemm_adapters_destroy": (ctypes.c_int, [P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -822,19 +826,28 @@ class GroupedGemmK(_Grouped):
         return (rows, d.M), (rows, d.N), (d.groups, d.M, d.N)
 
 
+def gemm_adapters_create_status(desc: gemm_adapters_desc_t):
+    """gemm_adapters_create returning (status, handle or None) without raising."""
+    h = ctypes.c_void_p()
+    return _lib.gemm_adapters_create(ctypes.byref(desc), ctypes.byref(h)), h.value
+
+
 class Adapters:
     """Low-rank adapters of many requests at once beside a shared projection (include/adapters.h):
     out[r] = base[r] + scales[g] (x[r] A[g]^T) B[g]^T for the rows r of every group g, base[r] for a row of none.
     x [rows][K], A [groups][rank][K], B [groups][N][rank], base and out [rows][N] (out may be base), offsets and
     order from row_groups over the rows' adapter numbers; without order (None) the rows of a group follow each
-    other.  Rows of x, base and out may be strided; the tensors of a call are on the current device."""
+    other.  Rows of x, base and out may be strided; the tensors of a call are on the current device, the one the
+    object was made on.  A graph needs the object that it was captured from (its status word)."""
 
     def __init__(self, groups, N, K, rank, dtype=GEMM_BF16):
+        self.plan = None
         self.desc = gemm_adapters_desc_t(groups, rank, N, K, dtype)
-        if not (1 <= groups <= 1024 and 8 <= rank <= 128 and rank % 8 == 0 and N >= 8 and N % 8 == 0 and K >= 8 and K % 8 == 0):
-            raise GemmError(GEMM_ERR_INVALID_ARG, "Adapters")
+        st, h = gemm_adapters_create_status(self.desc)
+        _check(st, "gemm_adapters_create")
+        self.plan = h
         self.dtype = _torch_dtype(dtype)
-        self.handle = (ctypes.addressof(self.desc), self.dtype, groups, N, K, rank)
+        self.handle = (h, self.dtype, groups, N, K, rank)
 
     def run(self, x, A, B, offsets, order, base, out, scales=None, stream=None):
         st = _binding.adapters(self.handle, x, A, B, offsets, order, base, out, scales, stream)
@@ -845,3 +858,18 @@ class Adapters:
                     *((("order", order, (n,), _torch.int32, False),) if order is not None else ()),
                     ("base", base, (n, d.N), dt, True), ("out", out, (n, d.N), dt, True),
                     *((("scales", scales, (d.groups,), _torch.float32, False),) if scales is not None else ()))
+
+    def sync_status(self, stream=None) -> int:
+        torch = _torch or _with_torch()
+        return _lib.gemm_adapters_sync_status(self.plan, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+
+    def close(self):
+        if self.plan:
+            _lib.gemm_adapters_destroy(self.plan)
+            self.plan, self.handle = None, (0, *self.handle[1:])
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -20,11 +20,14 @@
 // neighbours of a row: base and out move in 16-byte pieces.
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
+#include <new>
 
 #include "adapters.h"
 #include "groups.cuh"
 #include "half_types.cuh"
 #include "kernels.h"
+#include "plan.h"
 #include "ptx.cuh"
 
 namespace lgt {
@@ -33,6 +36,7 @@ namespace {
 constexpr int kAdWarps = 8;
 constexpr int kAdThreads = kAdWarps * 32;
 constexpr int kAdMaxGroups = 1024;
+constexpr int64_t kAdManyRows = 32;  // rows a group and an SM from which the large form is taken
 
 struct AdapterArgs {
   const uint16_t *x, *a, *b, *base;
@@ -85,6 +89,20 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   const float2 h = unpack_pair16<BF16>(hi);
   // (what is no number or infinite has nothing left over)
   lo = pack_pair16<BF16>(isfinite(h.x) ? x - h.x : 0.0f, isfinite(h.y) ? y - h.y : 0.0f);
+}
+
+// Rows of no group, at the places before the first group and behind the last:
+// base to out, by all CTAs.
+__device__ __forceinline__ void copy_others(const AdapterArgs& a, const uint32_t* off, uint32_t threads) {
+  const uint32_t head = off[0], none = head + static_cast<uint32_t>(a.rows) - off[a.groups];
+  const uint32_t pieces = static_cast<uint32_t>(a.n) / 8;
+  for (uint32_t i = blockIdx.x; i < none; i += gridDim.x) {
+    int32_t r = static_cast<int32_t>(i < head ? i : off[a.groups] + (i - head));
+    if (a.order) r = a.order[r];
+    if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) continue;
+    for (uint32_t c = threadIdx.x; c < pieces; c += threads)
+      *reinterpret_cast<uint4*>(a.out + r * a.os + c * 8) = *reinterpret_cast<const uint4*>(a.base + r * a.bs + c * 8);
+  }
 }
 
 template <int MT, int NT>
@@ -318,19 +336,391 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
       __syncthreads();
   }
 
-  if (a.copy) {
-    // Rows of no group: the places before the first group and behind the last.
-    const uint32_t head = off[0], none = head + static_cast<uint32_t>(a.rows) - off[a.groups];
-    const uint32_t pieces = static_cast<uint32_t>(a.n) / 8;
-    for (uint32_t i = blockIdx.x; i < none; i += gridDim.x) {
-      int32_t r = static_cast<int32_t>(i < head ? i : off[a.groups] + (i - head));
-      if (a.order) r = a.order[r];
-      if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) continue;
-      for (uint32_t c = threadIdx.x; c < pieces; c += kAdThreads)
-        *reinterpret_cast<uint4*>(a.out + r * a.os + c * 8) = *reinterpret_cast<const uint4*>(a.base + r * a.bs + c * 8);
+  if (a.copy) copy_others(a, off, kAdThreads);
+  if (a.ctas > 1) cluster_sync_all();
+}
+
+// ------------------------------------------------------------ many rows
+//
+// The same pass on tcgen05: a tile is up to 128 rows of one group and a CTA does
+// it by itself, first
+//   u = x A^T:    rows on the instruction's M side (lanes of tensor memory), rank
+//                 on its N side; x and A come by a ring of copies, x's rows by
+//                 their numbers, four a copy, where there is an order;
+// then four warps take u from tensor memory, a row a lane, to its two parts of
+// 16 bits in shared memory, and
+//   out^T = B u^T: columns of out on the M side, 128 at a time, rows on the N
+//                 side in steps of 16; eight warps add base, whose pieces are on
+//                 their way four deep, through shared memory, where a transposing
+//                 load and store of 8 x 8 pieces turn them to the accumulator's
+//                 order and back.
+//
+// Roles (416 threads): warps 0..3 copies of x (0: of A too, 1: of B), warp 4
+// tensor memory and products, warps 5..12 results.
+constexpr int kAtcThreads = 416;
+constexpr int kAtcMmaWarp = 4, kAtcEpiWarp0 = 5, kAtcEpiWarps = 8;
+constexpr uint32_t kAtcRows = 128;
+constexpr uint32_t kAtcTile = 128 * 128;               // 128 rows of 64 values
+constexpr uint32_t kAtcMaxStages = 8;
+constexpr uint32_t kAtcPieces = 4;                     // of base, a warp
+constexpr uint32_t kAtcStaging = kAtcEpiWarps * kAtcPieces * 2048;
+constexpr uint32_t kAtcBars = 2 * kAtcMaxStages + 14;  // (13, and what follows is loaded 16 bytes at a time)
+static_assert(kAtcBars * 8 % 16 == 0);
+constexpr uint32_t kAtcSmem = 227 * 1024;
+constexpr uint64_t kAtcSettleNs = 200ull * 1000ull * 1000ull;
+
+struct AdapterTcArgs {
+  CUtensorMap tm_x, tm_a, tm_b;
+  AdapterArgs p;
+  DeviceStatus* status;
+  uint64_t wait_limit_ns;
+  uint32_t rank16, chunks;  // the rank in steps of 16; in stretches of 64
+  uint32_t stages, stage_bytes, region;  // region: of the ring, then of u and B
+  uint32_t idesc_u, idesc_out;  // the second without N
+  int32_t withhold;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __grid_constant__ AdapterTcArgs t) {
+  pdl_launch_dependents();
+  const AdapterArgs& a = t.p;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw_base);
+  const uint32_t u_hi = base, u_lo = base + t.chunks * kAtcTile, b_ring = base + 2 * t.chunks * kAtcTile;
+  const uint32_t staging = base + t.region;
+  const uint32_t bar0 = staging + kAtcStaging;
+  uint8_t* rest = smem + t.region + kAtcStaging + kAtcBars * 8;
+  int32_t* row_of = reinterpret_cast<int32_t*>(rest);                 // [2][128], of this tile and the next
+  float* factor = reinterpret_cast<float*>(rest + 1024);              // [128]
+  volatile uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 1536);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(rest + 1540);
+  uint32_t* scratch = reinterpret_cast<uint32_t*>(rest + 1544);       // [32]
+  uint32_t* off = scratch + 32;
+  uint32_t* first = off + a.groups + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto full = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty = [&](uint32_t s) { return bar0 + 8u * (kAtcMaxStages + s); };
+  auto rows_full = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + b); };
+  const uint32_t u_done = bar0 + 8u * (2 * kAtcMaxStages + 2), u_full = u_done + 8, tile_done = u_done + 16, end_bar = u_done + 24;
+  auto b_full = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + 6 + b); };
+  auto out_full = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + 8 + b); };
+  auto out_empty = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + 10 + b); };
+  const uint32_t results_done = bar0 + 8u * (2 * kAtcMaxStages + 12);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    const bool got = mbar_wait_bounded(bar, parity, t.wait_limit_ns, abort_flag);
+    if (!got) {
+      *abort_flag = 1;
+      t.status->where = warp;
+      t.status->code = GEMM_ERR_TIMEOUT;
+    }
+    return got;
+  };
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < t.stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(u_done, 1);     // the first product is
+    mbar_init(u_full, 4);     // its parts are in shared memory
+    mbar_init(tile_done, 1);  // u and B have been read
+    mbar_init(results_done, kAtcEpiWarps);
+    mbar_init(end_bar, 1);
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(rows_full(b), 4);
+      mbar_init(b_full(b), 1);
+      mbar_init(out_full(b), 1);
+      mbar_init(out_empty(b), kAtcEpiWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&t.tm_x);
+    tma_prefetch_desc(&t.tm_a);
+    tma_prefetch_desc(&t.tm_b);
+  }
+  if (warp == kAtcMmaWarp) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  group_rows<kAtcThreads>(a.offsets, a.groups, a.rows, off, scratch);
+  __syncthreads();
+  group_tiles<kAtcThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + kAtcRows - 1) / kAtcRows; }, first, scratch + 16);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tiles = first[a.groups];
+  const int nkb = (a.k + TILE_K - 1) / TILE_K;
+  const int nnb = (a.n + 127) / 128;
+  // A tile: its group, first place and rows.
+  struct Tile {
+    uint32_t g, at, count;
+  };
+  auto tile_at = [&](uint32_t i) {
+    Tile w;
+    w.g = group_of(first, a.groups, i);
+    const uint32_t len = off[w.g + 1] - off[w.g], n = (len + kAtcRows - 1) / kAtcRows;
+    const uint32_t width = ((len + n - 1) / n + 15) & ~15u;
+    w.at = off[w.g] + (i - first[w.g]) * width;
+    w.count = min(width, off[w.g + 1] - w.at);
+    return w;
+  };
+  const uint32_t u_tmem = tmem, out_tmem = tmem + 128;
+
+  if (warp < kAtcMmaWarp) {
+    // ------------------------------------------------------------ copies
+    uint32_t s = 0, phase = 0, it = 0, issued = 0, b_uses = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++it) {
+      const Tile w = tile_at(i);
+      int32_t* rows = row_of + (it & 1) * kAtcRows;
+      // u and B of the tile before lie where the ring is.  (And the results of the
+      // one before that, whose rows stood here, were done before its u was made.)
+      if (it > 0 && !(ok = warp_wait(tile_done, (it - 1) & 1u))) break;
+      int32_t r = -1;
+      const uint32_t place = warp * 32 + lane;
+      if (place < w.count) {
+        r = static_cast<int32_t>(w.at + place);
+        if (a.order) r = a.order[r];
+        if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) r = -1;
+      }
+      rows[place] = r;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_full(it & 1));
+      if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
+      if (elect_one()) {
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!(ok = wait(empty(s), phase ^ 1u))) break;
+          const uint32_t dst = base + s * t.stage_bytes;
+          if (warp == 0) {
+            mbar_arrive_expect_tx(full(s), t.stage_bytes);
+            if (!(t.withhold && blockIdx.x == 0 && issued == 0))
+              tma_load_3d(dst + kAtcTile, &t.tm_a, full(s), kb * TILE_K, 0, static_cast<int32_t>(w.g));
+          }
+          if (a.order) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              int4 r = *reinterpret_cast<const int4*>(rows + warp * 32 + 4 * j);
+              // (a row past the last gives zeros)
+              r.x = r.x < 0 ? a.rows : r.x;
+              r.y = r.y < 0 ? a.rows : r.y;
+              r.z = r.z < 0 ? a.rows : r.z;
+              r.w = r.w < 0 ? a.rows : r.w;
+              tma_gather4(dst + (warp * 32 + 4 * j) * 128, &t.tm_x, full(s), kb * TILE_K, r);
+            }
+          } else if (warp == 0) {
+            tma_load_2d(dst, &t.tm_x, full(s), kb * TILE_K, static_cast<int32_t>(w.at));
+          }
+          ++issued;
+          if (++s == t.stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (warp == 1 && ok && (ok = wait(u_done, it & 1u))) {
+          for (int b = 0; b < nnb; ++b, ++b_uses) {
+            // (what the products of the block before the last have read is free once they are done)
+            if (b_uses >= 2 && !(ok = wait(out_full(b_uses & 1u), (b_uses >> 1 & 1u) ^ 1u))) break;
+            mbar_arrive_expect_tx(b_full(b_uses & 1u), t.chunks * kAtcTile);
+            for (uint32_t c = 0; c < t.chunks; ++c)
+              tma_load_3d(b_ring + ((b_uses & 1u) * t.chunks + c) * kAtcTile, &t.tm_b, b_full(b_uses & 1u),
+                          static_cast<int32_t>(64 * c), b * 128, static_cast<int32_t>(w.g));
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+  } else if (warp == kAtcMmaWarp) {
+    // ------------------------------------------------------------ products
+    if (elect_one()) {
+      const uint64_t x_desc = sw128_desc(base, 16u, 1024u), a_desc = sw128_desc(base + kAtcTile, 16u, 1024u);
+      const uint64_t hi_desc = sw128_desc(u_hi, 16u, 1024u), lo_desc = sw128_desc(u_lo, 16u, 1024u);
+      const uint64_t b_desc = sw128_desc(b_ring, 16u, 1024u);
+      uint32_t s = 0, phase = 0, it = 0, uses = 0;
+      bool ok = true;
+      for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++it) {
+        const Tile w = tile_at(i);
+        // (the results' warps have read the u of the tile before: its parts were full)
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!(ok = wait(full(s), phase))) break;
+          tc_fence_after();
+          const uint64_t xd = x_desc + s * (t.stage_bytes >> 4), ad = a_desc + s * (t.stage_bytes >> 4);
+#pragma unroll
+          for (int k = 0; k < TILE_K / 16; ++k) tc_mma_f16_ss(u_tmem, xd + 2 * k, ad + 2 * k, t.idesc_u, (kb | k) != 0 ? 1u : 0u);
+          tc_commit(empty(s));
+          if (++s == t.stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit(u_done);
+        if (!(ok = wait(u_full, it & 1u))) break;
+        const uint32_t idesc = t.idesc_out | ((w.count + 15) & ~15u) >> 3 << 17;
+        for (int b = 0; b < nnb; ++b, ++uses) {
+          const uint32_t buf = uses & 1u;
+          if (!(ok = wait(b_full(buf), uses >> 1 & 1u) && wait(out_empty(buf), (uses >> 1 & 1u) ^ 1u))) break;
+          tc_fence_after();
+          const uint32_t d = out_tmem + buf * 128;
+          for (uint32_t k = 0; k < t.rank16; ++k) {
+            const uint32_t at = (k >> 2) * (kAtcTile >> 4) + (k & 3) * 2;
+            const uint64_t bd = b_desc + buf * t.chunks * (kAtcTile >> 4) + at;
+            tc_mma_f16_ss(d, bd, hi_desc + at, idesc, k > 0 ? 1u : 0u);
+            tc_mma_f16_ss(d, bd, lo_desc + at, idesc, 1u);
+          }
+          tc_commit(out_full(buf));
+        }
+        if (!ok) break;
+        tc_commit(tile_done);
+      }
+      tc_commit(end_bar);
+    }
+  } else {
+    // ------------------------------------------------------------ results
+    const uint32_t quad = static_cast<uint32_t>(warp & 3), half = static_cast<uint32_t>(warp - kAtcEpiWarp0) / 4;
+    const uint32_t mine = staging + static_cast<uint32_t>(warp - kAtcEpiWarp0) * kAtcPieces * 2048u;
+    const uint32_t row8 = static_cast<uint32_t>(lane >> 2), piece = static_cast<uint32_t>(lane & 3);
+    // places in a piece of 32 rows of 64 bytes, as in the grouped products' results
+    const uint32_t put = (lane & 7u) * 64u + ((static_cast<uint32_t>(lane >> 3) ^ (lane >> 1 & 3u)) << 4);
+    const uint32_t get = row8 * 64u + ((piece ^ (row8 >> 1 & 3u)) << 4);
+    uint32_t it = 0, uses = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++it) {
+      const Tile w = tile_at(i);
+      if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
+      const int32_t* rows = row_of + (it & 1) * kAtcRows;
+      // Pieces of base: 2 a block of 128 columns, rows 32 half and 64 beyond.
+      const int n0 = static_cast<int>(quad * 32 + piece * 8);
+      auto fetch = [&](int q) {
+        const int n = (q >> 1) * 128 + n0;
+        const uint32_t tok0 = half * 32 + (q & 1) * 64;
+        if (q < 2 * nnb && n < a.n) {
+          const uint32_t dst = mine + (q % kAtcPieces) * 2048u + get;
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            const int32_t r = rows[tok0 + 8 * j + row8];
+            if (r >= 0) cp_async_16(dst + j * 512u, a.base + r * a.bs + n);
+          }
+        }
+        cp_async_commit();
+      };
+      for (int q = 0; q < static_cast<int>(kAtcPieces) - 1; ++q) fetch(q);
+      if (half == 0) {
+        // u, a row a lane: the power of two that takes its largest value to [0.5, 1), then its parts.
+        // (The rows' factors of the tile before are in use until its results are done.)
+        if (!(ok = warp_wait(u_done, it & 1u) && (it == 0 || warp_wait(results_done, (it - 1) & 1u)))) break;
+        tc_fence_after();
+        const uint32_t row = quad * 32 + lane, from = u_tmem + (quad * 32u << 16);
+        float most = 0.0f;
+        for (uint32_t c = 0; c < t.rank16 * 16; c += 16) {
+          uint32_t v[16];
+          tc_ld_32x32b_x16(from + c, v);
+          tc_wait_ld_regs(v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (static_cast<int>(c) + e < a.rank) most = fmaxf(most, fabsf(__uint_as_float(v[e])));
+        }
+        const int e = static_cast<int>(__float_as_uint(most) >> 23);
+        const int p = e == 0 || e == 255 ? 0 : min(e - 126, 126);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - p) << 23);
+        for (uint32_t c = 0; c < t.rank16 * 16; c += 16) {
+          uint32_t v[16];
+          tc_ld_32x32b_x16(from + c, v);
+          tc_wait_ld_regs(v);
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            // (past the rank are sums of what x holds times 0, which is not 0 for an infinity)
+            const bool in = static_cast<int>(c) + 2 * j < a.rank;
+            split_pair<BF16>(in ? __uint_as_float(v[2 * j]) * down : 0.0f, in ? __uint_as_float(v[2 * j + 1]) * down : 0.0f, hi[j], lo[j]);
+          }
+          const uint32_t at = (c >> 6) * kAtcTile + row * 128;
+#pragma unroll
+          for (uint32_t j = 0; j < 2; ++j) {
+            const uint32_t to = at + ((((c & 63u) >> 3) + j) ^ (row & 7u)) * 16;
+            st_shared_v4(u_hi + to, hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+            st_shared_v4(u_lo + to, lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+          }
+        }
+        factor[row] = __uint_as_float(static_cast<uint32_t>(127 + p) << 23) * (a.scales ? a.scales[w.g] : 1.0f);
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_full);
+      }
+      if (!(ok = warp_wait(u_full, it & 1u))) break;
+      for (int b = 0; ok && b < nnb; ++b, ++uses) {
+        const uint32_t buf = uses & 1u;
+        if (!(ok = warp_wait(out_full(buf), uses >> 1 & 1u))) break;
+        tc_fence_after();
+        const int n = b * 128 + n0;
+#pragma unroll 1
+        for (uint32_t j = 0; j < 2; ++j) {
+          const int q = 2 * b + static_cast<int>(j);
+          const uint32_t tok0 = half * 32 + j * 64;
+          fetch(q + kAtcPieces - 1);
+          cp_async_wait<kAtcPieces - 1>();
+          __syncwarp();
+          if (tok0 >= w.count) continue;
+          const uint32_t here = mine + (q % kAtcPieces) * 2048u;
+          uint32_t x[16], y[16];
+          tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + (quad * 32u << 16), x);
+          tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + ((quad * 32u + 16u) << 16), y);
+          tc_wait_ld_regs(x);
+          tc_regs_after_wait(y);
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const uint4 old = ldmatrix_x4_trans(here + put + e * 512u);
+            const float2 f = *reinterpret_cast<const float2*>(factor + tok0 + 8 * e + 2 * piece);
+            auto sum = [&](uint32_t lo, uint32_t hi, uint32_t o) {
+              const float2 was = unpack_pair16<BF16>(o);
+              return pack_pair16<BF16>(fmaf(__uint_as_float(lo), f.x, was.x), fmaf(__uint_as_float(hi), f.y, was.y));
+            };
+            stmatrix_x4_trans(here + put + e * 512u, sum(x[4 * e], x[4 * e + 1], old.x), sum(x[4 * e + 2], x[4 * e + 3], old.y),
+                              sum(y[4 * e], y[4 * e + 1], old.z), sum(y[4 * e + 2], y[4 * e + 3], old.w));
+          }
+          __syncwarp();
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const uint4 v = ld_shared_v4(here + get + e * 512u);
+            const int32_t r = rows[tok0 + 8 * e + row8];
+            if (r >= 0 && n < a.n) st_global_v4(a.out + r * a.os + n, v.x, v.y, v.z, v.w);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(out_empty(buf));
+      }
+      if (lane == 0) mbar_arrive(results_done);
+    }
+    cp_async_wait<0>();
+  }
+
+  // ------------------------------------------------------------ end
+  if (a.copy && !*abort_flag) copy_others(a, off, kAtcThreads);
+  __syncthreads();
+  if (*abort_flag) {
+    // Copies that were made may still be landing, on a barrier that will not
+    // complete: they take microseconds, and are given far more.
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kAtcSettleNs) {
     }
   }
-  if (a.ctas > 1) cluster_sync_all();
+  if (warp == kAtcMmaWarp) {
+    volatile int no_abort = 0;
+    mbar_wait_bounded(end_bar, 0, drain_ns(t.wait_limit_ns), &no_abort);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kAtcMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <int MT, int NT, bool BF16>
@@ -355,20 +745,95 @@ cudaError_t launch_adapters(const AdapterArgs& a, int nt, unsigned clusters, cud
                         : launch_adapters_mt<8, BF16>(a, nt, clusters, stream);
 }
 
+// [d2][d1][d0], dense, by boxes of 64 x box1.
+bool encode_dense(CUtensorMap* map, const void* ptr, bool bf16, int64_t d0, int64_t d1, int64_t d2, uint32_t box1) {
+  auto enc = get_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d0) * 2, static_cast<cuuint64_t>(d0 * d1) * 2};
+  cuuint32_t box[3] = {64, box1, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// x's rows, boxes of 64 values of box1 rows.
+bool encode_x(CUtensorMap* map, const void* ptr, bool bf16, int64_t k, int64_t rows, int64_t stride, uint32_t box1) {
+  auto enc = get_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[2] = {64, box1};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(ptr), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16>
+cudaError_t launch_adapters_tc(const AdapterTcArgs& t, unsigned ctas, cudaStream_t stream) {
+  const cudaError_t e = set_smem_once<adapters_tc_kernel<BF16>>(static_cast<int>(kAtcSmem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(adapters_tc_kernel<BF16>, dim3(ctas), dim3(kAtcThreads), kAtcSmem, stream, t);
+}
+
+uint64_t adapters_wait_limit() {
+  const char* s = std::getenv("LGT_GEMM_WAIT_LIMIT_MS");
+  if (s && *s) {
+    const double ms = std::atof(s);
+    if (ms > 0) return static_cast<uint64_t>(ms * 1e6);
+  }
+  return 2000ull * 1000ull * 1000ull;  // 2 s
+}
+
 }  // namespace
 }  // namespace lgt
 
-extern "C" gemm_status_t gemm_adapters_run(const gemm_adapters_desc_t* desc, const void* x, int64_t x_stride, const void* A,
-                                           const void* B, const float* scales, const int32_t* offsets, const int32_t* order,
-                                           int64_t rows, const void* base, int64_t base_stride, void* out,
-                                           int64_t out_stride, void* stream) {
-  using namespace lgt;
-  if (!desc || rows < 0) return GEMM_ERR_INVALID_ARG;
+struct gemm_adapters_plan {
+  gemm_adapters_desc_t d;
+  int device = -1;
+  int sms = 0;
+  lgt::DeviceStatus* d_status = nullptr;
+  uint64_t wait_limit_ns = 0;
+  int withhold_armed = 0;  // gemm_adapters_withhold_load: the next run of the large form withholds a load (one shot)
+};
+
+extern "C" {
+
+gemm_status_t gemm_adapters_create(const gemm_adapters_desc_t* desc, gemm_adapters_plan_t** plan) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  *plan = nullptr;
+  if (!desc) return GEMM_ERR_INVALID_ARG;
   const gemm_adapters_desc_t& d = *desc;
   auto size = [](int64_t v) { return v >= 8 && v % 8 == 0 && v < (int64_t{1} << 30); };
-  if (d.groups < 1 || d.groups > kAdMaxGroups || d.rank < 8 || d.rank > 128 || d.rank % 8 != 0 || !size(d.N) || !size(d.K) ||
-      (d.dtype != GEMM_F16 && d.dtype != GEMM_BF16))
+  if (d.groups < 1 || d.groups > lgt::kAdMaxGroups || d.rank < 8 || d.rank > 128 || d.rank % 8 != 0 || !size(d.N) ||
+      !size(d.K) || (d.dtype != GEMM_F16 && d.dtype != GEMM_BF16))
     return GEMM_ERR_INVALID_ARG;
+  gemm_adapters_plan* p = new (std::nothrow) gemm_adapters_plan();
+  if (!p) return GEMM_ERR_CUDA;
+  p->d = d;
+  p->wait_limit_ns = lgt::adapters_wait_limit();
+  if (cudaGetDevice(&p->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
+    cudaGetLastError();
+    p->device = -1;
+  } else if (cudaMalloc(&p->d_status, 16) != cudaSuccess || cudaMemset(p->d_status, 0, 16) != cudaSuccess) {
+    cudaGetLastError();
+    if (p->d_status) cudaFree(p->d_status);
+    delete p;
+    return GEMM_ERR_CUDA;
+  }
+  *plan = p;
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64_t x_stride, const void* A, const void* B,
+                                const float* scales, const int32_t* offsets, const int32_t* order, int64_t rows,
+                                const void* base, int64_t base_stride, void* out, int64_t out_stride, void* stream) {
+  using namespace lgt;
+  if (!plan || rows < 0) return GEMM_ERR_INVALID_ARG;
+  const gemm_adapters_desc_t& d = plan->d;
   if (x_stride == 0) x_stride = d.K;
   if (base_stride == 0) base_stride = d.N;
   if (out_stride == 0) out_stride = d.N;
@@ -383,12 +848,13 @@ extern "C" gemm_status_t gemm_adapters_run(const gemm_adapters_desc_t* desc, con
   for (const void* p : {static_cast<const void*>(scales), static_cast<const void*>(offsets), static_cast<const void*>(order)})
     if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return GEMM_ERR_ALIGNMENT;
   if (rows > (int64_t{1} << 30)) return GEMM_ERR_UNSUPPORTED;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
+  if (dev != plan->device) return GEMM_ERR_INVALID_ARG;  // (the status word is there)
+  const int sms = plan->sms;
   AdapterArgs a;
   a.x = static_cast<const uint16_t*>(x);
   a.a = static_cast<const uint16_t*>(A);
@@ -407,18 +873,71 @@ extern "C" gemm_status_t gemm_adapters_run(const gemm_adapters_desc_t* desc, con
   a.n = static_cast<int32_t>(d.N);
   a.k = static_cast<int32_t>(d.K);
   a.copy = out != base;
-  const int64_t busy = std::min<int64_t>(d.groups, rows);
-  const int nt = rows > 8 * busy ? 4 : 1;
-  const int64_t tiles = rows / (8 * nt) + busy;
-  // A cluster as large as leaves a CTA for every SM, or what there is to share.
   a.ctas = 1;
-  while (a.ctas < 8 && tiles * a.ctas * 2 <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
-  const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * sms / a.ctas));
+  const int64_t busy = std::min<int64_t>(d.groups, rows);
+  const bool bf16 = d.dtype == GEMM_BF16;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = d.dtype == GEMM_BF16 ? launch_adapters<true>(a, nt, clusters, s) : launch_adapters<false>(a, nt, clusters, s);
+  cudaError_t e;
+  if (rows >= busy * kAdManyRows && rows >= static_cast<int64_t>(sms) * kAdManyRows) {
+    AdapterTcArgs t;
+    t.p = a;
+    t.status = plan->d_status;
+    // (a wait may be for all of a tile's blocks)
+    t.wait_limit_ns = plan->wait_limit_ns + static_cast<uint64_t>(d.K / TILE_K + d.N / 128) * 4000;
+    t.rank16 = static_cast<uint32_t>(d.rank + 15) / 16;
+    t.chunks = (t.rank16 + 3) / 4;
+    t.stage_bytes = kAtcTile + t.rank16 * 16 * 128;
+    const uint32_t tables = kAtcBars * 8 + 1544 + 128 + 8 * static_cast<uint32_t>(d.groups + 1);
+    t.stages = std::min<uint32_t>(kAtcMaxStages, (kAtcSmem - 1024 - kAtcStaging - tables) / t.stage_bytes);
+    t.region = std::max(t.stages * t.stage_bytes, 4 * t.chunks * kAtcTile);
+    t.idesc_u = idesc_f16(bf16, 0u, 0u, kAtcRows, t.rank16 * 16);
+    t.idesc_out = idesc_f16(bf16, 0u, 0u, kAtcRows, 0u);
+    t.withhold = plan->withhold_armed ? __atomic_exchange_n(&plan->withhold_armed, 0, __ATOMIC_ACQ_REL) : 0;
+    if (!encode_x(&t.tm_x, x, bf16, d.K, rows, x_stride, order ? 1 : kAtcRows) ||
+        !encode_dense(&t.tm_a, A, bf16, d.K, d.rank, d.groups, t.rank16 * 16) ||
+        !encode_dense(&t.tm_b, B, bf16, d.rank, d.N, d.groups, 128))
+      return GEMM_ERR_CUDA;
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(rows / kAtcRows + busy, sms));
+    e = bf16 ? launch_adapters_tc<true>(t, ctas, s) : launch_adapters_tc<false>(t, ctas, s);
+  } else {
+    const int nt = rows > 8 * busy ? 4 : 1;
+    const int64_t tiles = rows / (8 * nt) + busy;
+    // A cluster as large as leaves a CTA for every SM, or what there is to share.
+    while (a.ctas < 8 && tiles * a.ctas * 2 <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
+    const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * sms / a.ctas));
+    e = bf16 ? launch_adapters<true>(a, nt, clusters, s) : launch_adapters<false>(a, nt, clusters, s);
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
   return GEMM_OK;
 }
+
+gemm_status_t gemm_adapters_sync_status(gemm_adapters_plan_t* plan, void* stream) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  if (!plan->d_status) return GEMM_ERR_CUDA;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
+  lgt::DeviceStatus st;
+  if (cudaMemcpy(&st, plan->d_status, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (st.code != 0) {
+    if (cudaMemset(plan->d_status, 0, sizeof(st)) != cudaSuccess) return GEMM_ERR_CUDA;
+    return static_cast<gemm_status_t>(st.code);
+  }
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_adapters_withhold_load(gemm_adapters_plan_t* plan) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  __atomic_store_n(&plan->withhold_armed, 1, __ATOMIC_RELEASE);
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_adapters_destroy(gemm_adapters_plan_t* plan) {
+  if (!plan) return GEMM_OK;
+  if (plan->d_status) cudaFree(plan->d_status);
+  delete plan;
+  return GEMM_OK;
+}
+
+}  // extern "C"

@@ -309,7 +309,7 @@ static PyObject* py_grouped(PyObject* self, PyObject* const* args, Py_ssize_t na
                             C.ptr, ldc, m > 0 ? C.stride[0] : 0, stream));
 }
 
-/* (the description's address, dtype, groups, N, K, rank), x, A, B, offsets, order (or None), base, out, scales (or None),
+/* (plan, dtype, groups, N, K, rank), x, A, B, offsets, order (or None), base, out, scales (or None),
  * stream */
 static PyObject* py_adapters(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
   view x, A, B, offsets, order = {0}, base, out, scales = {0};

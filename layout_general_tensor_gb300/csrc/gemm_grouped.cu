@@ -357,6 +357,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
           tc_commit(accf(buf));
         ++uses;
       }
+      if constexpr (PAIR)
+        tc_commit_pair_mc(end_bar, 0x1);
+      else
+        tc_commit(end_bar);
     }
   } else if (warp == kGgClearWarp) {
     // ------------------------------------------------------------ rows of the next group
@@ -453,12 +457,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     while (global_timer_ns() - t0 < kGgSettleNs) {
     }
   }
-  if (leader && warp == 1 && lane == 0) {
+  if (leader && warp == 1) {
     volatile int no_abort = 0;
-    if constexpr (PAIR)
-      tc_commit_pair_mc(end_bar, 0x1);
-    else
-      tc_commit(end_bar);
     mbar_wait_bounded(end_bar, 0, drain_ns(a.wait_limit_ns), &no_abort);
   }
   tc_fence_before();
@@ -656,7 +656,8 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   a.c = static_cast<uint16_t*>(C);
   a.offsets = offsets;
   a.status = plan->d_status;
-  a.wait_limit_ns = plan->wait_limit_ns;
+  // (a wait may be for all of a tile's blocks)
+  a.wait_limit_ns = plan->wait_limit_ns + static_cast<uint64_t>((along_k ? rows : d.K) / TILE_K) * 2000;
   a.ldc = ldc;
   a.c_stride = c_stride;
   a.groups = d.groups;

@@ -203,20 +203,26 @@ def _check_adapters(m, sizes, none, n, k, rank, dtype, order=True, scaled=True, 
     out = base if in_place else _pitched(torch.full((rows, n), -77.0, dtype=t, device="cuda"), extra[2])
     offsets, at = _offsets(sizes, start), np.concatenate([[0], np.cumsum(sizes)]) + start
     perm = torch.randperm(rows, generator=g, device="cuda") if order else torch.arange(rows, device="cuda")
-    want, size = base.double(), base.double().abs()
+    want, error = base.double(), torch.zeros(rows, n, dtype=torch.float64, device="cuda")
     for e in range(groups):
         r = perm[at[e]:at[e + 1]]
         s = scales[e].double() if scaled else 1.0
-        u = x[r].double() @ a[e].double().T
-        want[r] += s * (u @ b[e].double().T)
-        size[r] += s * ((x[r].double().abs() @ a[e].double().abs().T) * 2.0**-20 + u.abs().amax(-1, keepdim=True) * 2.0**-16) @ b[e].double().abs().T
-    m.Adapters(groups, n, k, rank, dtype=_code(m, dtype)).run(x, a, b, offsets, perm.int() if order else None, base, out, scales=scales)
+        u, up = x[r].double() @ a[e].double().T, b[e].double().T
+        want[r] += s * (u @ up)
+        # u is off by its sum's 2^-20 sum |x a| (above) and by its pair's 2^-16 of the row's largest, and the
+        # second sum by 2^-20 sum |u b|
+        off = 2.0**-20 * (x[r].double().abs() @ a[e].double().abs().T) + 2.0**-16 * u.abs().amax(-1, keepdim=True)
+        error[r] = s * ((off + 2.0**-20 * u.abs()) @ up.abs())
+    op = m.Adapters(groups, n, k, rank, dtype=_code(m, dtype))
+    op.run(x, a, b, offsets, perm.int() if order else None, base, out, scales=scales)
+    assert op.sync_status() == m.GEMM_OK
     if ints:
         # u below 2^15 in magnitude is held exactly by the pair: 8 + 8 bits (bf16) or 11 + 11 of the row's largest
         assert torch.equal(out, want.to(t)), (out != want.to(t)).nonzero()[:5]
     else:
-        # u's own rounding and its pair's (2^-16 of the row's largest), then the result's
-        tolerance = want.abs() * torch.finfo(t).eps / 2 + (size - want.abs()).clamp(min=0) + base.double().abs() * 2.0**-20
+        # one addition in fp32 (2^-24 of the sum) and the result's half step, of a value that is off already
+        half = torch.finfo(t).eps / 2
+        tolerance = error + (want.abs() + error) * (half + 2.0**-23)
         assert ((out.double() - want).abs() <= tolerance).all(), ((out.double() - want).abs() - tolerance).max()
 
 
@@ -233,6 +239,20 @@ def test_adapters(m, sizes, none, n, k, rank):
 def test_adapters_normal(m, dtype, rank):
     _check_adapters(m, [1, 0, 30, 2], 3, 520, 1032, rank, dtype, ints=False, seed=rank)
     _check_adapters(m, [100, 60, 0], 9, 520, 1032, rank, dtype, ints=False, order=False, seed=rank + 1)
+
+
+@pytest.mark.parametrize("sizes,none", [([5000], 0), ([2600, 0, 2500], 60), ([200] * 40, 0), ([1, 6000, 17, 129, 128], 1)])
+@pytest.mark.parametrize("n,k,rank", [(8, 8, 8), (136, 72, 16), (1000, 328, 24), (520, 512, 64), (264, 200, 72), (392, 1024, 128)])
+def test_adapters_many_rows(m, sizes, none, n, k, rank):
+    i = len(sizes) + rank // 8
+    _check_adapters(m, sizes, none, n, k, rank, "bf16" if i % 2 else "f16", order=i % 3 > 0, scaled=i % 5 > 0, in_place=i % 4 == 0, seed=i)
+    _check_adapters(m, sizes, none, n, k, rank, "f16" if i % 2 else "bf16", order=i % 3 == 0, in_place=i % 4 == 1, extra=(8, 16, 16 if i % 4 == 1 else 24), start=11, seed=i + 1)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rank", [8, 64, 88])
+def test_adapters_many_rows_normal(m, dtype, rank):
+    _check_adapters(m, [4000, 1500], 9, 520, 1032, rank, dtype, ints=False, order=rank == 64, seed=rank)
 
 
 def test_adapters_strided(m):
