@@ -350,19 +350,19 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
 // then four warps take u from tensor memory, a row a lane, to its two parts of
 // 16 bits in shared memory, and
 //   out^T = B u^T: columns of out on the M side, 128 at a time, rows on the N
-//                 side in steps of 16; eight warps add base, whose pieces are on
-//                 their way four deep, through shared memory, where a transposing
+//                 side in steps of 16; sixteen warps add base, whose pieces are on
+//                 their way a block ahead, through shared memory, where a transposing
 //                 load and store of 8 x 8 pieces turn them to the accumulator's
 //                 order and back.
 //
-// Roles (416 threads): warps 0..3 copies of x (0: of A too, 1: of B), warp 4
-// tensor memory and products, warps 5..12 results.
-constexpr int kAtcThreads = 416;
-constexpr int kAtcMmaWarp = 4, kAtcEpiWarp0 = 5, kAtcEpiWarps = 8;
+// Roles (608 threads): warps 0 and 1 copies of x (0: of A too, 1: of B), warp 2
+// tensor memory and products, warps 3..18 results.
+constexpr int kAtcThreads = 608;
+constexpr int kAtcMmaWarp = 2, kAtcEpiWarp0 = 3, kAtcEpiWarps = 16;
 constexpr uint32_t kAtcRows = 128;
 constexpr uint32_t kAtcTile = 128 * 128;               // 128 rows of 64 values
 constexpr uint32_t kAtcMaxStages = 8;
-constexpr uint32_t kAtcPieces = 4;                     // of base, a warp
+constexpr uint32_t kAtcPieces = 2;                     // of base, a warp
 constexpr uint32_t kAtcStaging = kAtcEpiWarps * kAtcPieces * 2048;
 constexpr uint32_t kAtcBars = 2 * kAtcMaxStages + 14;  // (13, and what follows is loaded 16 bytes at a time)
 static_assert(kAtcBars * 8 % 16 == 0);
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   float* factor = reinterpret_cast<float*>(rest + 1024);              // [128]
   volatile uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 1536);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(rest + 1540);
-  uint32_t* scratch = reinterpret_cast<uint32_t*>(rest + 1544);       // [32]
-  uint32_t* off = scratch + 32;
+  uint32_t* scratch = reinterpret_cast<uint32_t*>(rest + 1544);       // [2][32]
+  uint32_t* off = scratch + 64;
   uint32_t* first = off + a.groups + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
     mbar_init(results_done, kAtcEpiWarps);
     mbar_init(end_bar, 1);
     for (uint32_t b = 0; b < 2; ++b) {
-      mbar_init(rows_full(b), 4);
+      mbar_init(rows_full(b), kAtcMmaWarp);
       mbar_init(b_full(b), 1);
       mbar_init(out_full(b), 1);
       mbar_init(out_empty(b), kAtcEpiWarps);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   pdl_wait();
   group_rows<kAtcThreads>(a.offsets, a.groups, a.rows, off, scratch);
   __syncthreads();
-  group_tiles<kAtcThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + kAtcRows - 1) / kAtcRows; }, first, scratch + 16);
+  group_tiles<kAtcThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + kAtcRows - 1) / kAtcRows; }, first, scratch + 32);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -483,14 +483,17 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       // u and B of the tile before lie where the ring is.  (And the results of the
       // one before that, whose rows stood here, were done before its u was made.)
       if (it > 0 && !(ok = warp_wait(tile_done, (it - 1) & 1u))) break;
-      int32_t r = -1;
-      const uint32_t place = warp * 32 + lane;
-      if (place < w.count) {
-        r = static_cast<int32_t>(w.at + place);
-        if (a.order) r = a.order[r];
-        if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) r = -1;
+#pragma unroll
+      for (uint32_t h = 0; h < 64; h += 32) {
+        int32_t r = -1;
+        const uint32_t place = warp * 64 + h + lane;
+        if (place < w.count) {
+          r = static_cast<int32_t>(w.at + place);
+          if (a.order) r = a.order[r];
+          if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) r = -1;
+        }
+        rows[place] = r;
       }
-      rows[place] = r;
       __syncwarp();
       if (lane == 0) mbar_arrive(rows_full(it & 1));
       if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
@@ -504,15 +507,15 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
               tma_load_3d(dst + kAtcTile, &t.tm_a, full(s), kb * TILE_K, 0, static_cast<int32_t>(w.g));
           }
           if (a.order) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              int4 r = *reinterpret_cast<const int4*>(rows + warp * 32 + 4 * j);
+#pragma unroll 4
+            for (int j = 0; j < 16; ++j) {
+              int4 r = *reinterpret_cast<const int4*>(rows + warp * 64 + 4 * j);
               // (a row past the last gives zeros)
               r.x = r.x < 0 ? a.rows : r.x;
               r.y = r.y < 0 ? a.rows : r.y;
               r.z = r.z < 0 ? a.rows : r.z;
               r.w = r.w < 0 ? a.rows : r.w;
-              tma_gather4(dst + (warp * 32 + 4 * j) * 128, &t.tm_x, full(s), kb * TILE_K, r);
+              tma_gather4(dst + (warp * 64 + 4 * j) * 128, &t.tm_x, full(s), kb * TILE_K, r);
             }
           } else if (warp == 0) {
             tma_load_2d(dst, &t.tm_x, full(s), kb * TILE_K, static_cast<int32_t>(w.at));
@@ -583,7 +586,8 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
     }
   } else {
     // ------------------------------------------------------------ results
-    const uint32_t quad = static_cast<uint32_t>(warp & 3), half = static_cast<uint32_t>(warp - kAtcEpiWarp0) / 4;
+    const uint32_t quad = static_cast<uint32_t>(warp & 3), share = static_cast<uint32_t>(warp - kAtcEpiWarp0) / 4;
+    const uint32_t tok0 = share * 32;  // this warp's rows of the tile: 32
     const uint32_t mine = staging + static_cast<uint32_t>(warp - kAtcEpiWarp0) * kAtcPieces * 2048u;
     const uint32_t row8 = static_cast<uint32_t>(lane >> 2), piece = static_cast<uint32_t>(lane & 3);
     // places in a piece of 32 rows of 64 bytes, as in the grouped products' results
@@ -595,23 +599,23 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       const Tile w = tile_at(i);
       if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
       const int32_t* rows = row_of + (it & 1) * kAtcRows;
-      // Pieces of base: 2 a block of 128 columns, rows 32 half and 64 beyond.
+      // Pieces of base: 32 rows of 32 columns, of each block of 128.
       const int n0 = static_cast<int>(quad * 32 + piece * 8);
-      auto fetch = [&](int q) {
-        const int n = (q >> 1) * 128 + n0;
-        const uint32_t tok0 = half * 32 + (q & 1) * 64;
-        if (q < 2 * nnb && n < a.n) {
-          const uint32_t dst = mine + (q % kAtcPieces) * 2048u + get;
+      int32_t r[4];
 #pragma unroll
-          for (uint32_t j = 0; j < 4; ++j) {
-            const int32_t r = rows[tok0 + 8 * j + row8];
-            if (r >= 0) cp_async_16(dst + j * 512u, a.base + r * a.bs + n);
-          }
+      for (uint32_t j = 0; j < 4; ++j) r[j] = rows[tok0 + 8 * j + row8];
+      auto fetch = [&](int b) {
+        const int n = b * 128 + n0;
+        if (b < nnb && n < a.n) {
+          const uint32_t dst = mine + (b % kAtcPieces) * 2048u + get;
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j)
+            if (r[j] >= 0) cp_async_16(dst + j * 512u, a.base + r[j] * a.bs + n);
         }
         cp_async_commit();
       };
-      for (int q = 0; q < static_cast<int>(kAtcPieces) - 1; ++q) fetch(q);
-      if (half == 0) {
+      for (int b = 0; b < static_cast<int>(kAtcPieces) - 1; ++b) fetch(b);
+      if (share == 0) {
         // u, a row a lane: the power of two that takes its largest value to [0.5, 1), then its parts.
         // (The rows' factors of the tile before are in use until its results are done.)
         if (!(ok = warp_wait(u_done, it & 1u) && (it == 0 || warp_wait(results_done, (it - 1) & 1u)))) break;
@@ -655,32 +659,30 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
         if (lane == 0) mbar_arrive(u_full);
       }
       if (!(ok = warp_wait(u_full, it & 1u))) break;
+      float2 f[4];  // of rows 8 e + 2 piece and the next
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float2*>(factor + tok0 + 8 * e + 2 * piece);
       for (int b = 0; ok && b < nnb; ++b, ++uses) {
         const uint32_t buf = uses & 1u;
+        fetch(b + kAtcPieces - 1);
         if (!(ok = warp_wait(out_full(buf), uses >> 1 & 1u))) break;
         tc_fence_after();
-        const int n = b * 128 + n0;
-#pragma unroll 1
-        for (uint32_t j = 0; j < 2; ++j) {
-          const int q = 2 * b + static_cast<int>(j);
-          const uint32_t tok0 = half * 32 + j * 64;
-          fetch(q + kAtcPieces - 1);
-          cp_async_wait<kAtcPieces - 1>();
-          __syncwarp();
-          if (tok0 >= w.count) continue;
-          const uint32_t here = mine + (q % kAtcPieces) * 2048u;
+        if (tok0 < w.count) {
+          const uint32_t here = mine + (b % kAtcPieces) * 2048u;
+          const int n = b * 128 + n0;
           uint32_t x[16], y[16];
           tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + (quad * 32u << 16), x);
           tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + ((quad * 32u + 16u) << 16), y);
+          cp_async_wait<kAtcPieces - 1>();
+          __syncwarp();
           tc_wait_ld_regs(x);
           tc_regs_after_wait(y);
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
             const uint4 old = ldmatrix_x4_trans(here + put + e * 512u);
-            const float2 f = *reinterpret_cast<const float2*>(factor + tok0 + 8 * e + 2 * piece);
             auto sum = [&](uint32_t lo, uint32_t hi, uint32_t o) {
               const float2 was = unpack_pair16<BF16>(o);
-              return pack_pair16<BF16>(fmaf(__uint_as_float(lo), f.x, was.x), fmaf(__uint_as_float(hi), f.y, was.y));
+              return pack_pair16<BF16>(fmaf(__uint_as_float(lo), f[e].x, was.x), fmaf(__uint_as_float(hi), f[e].y, was.y));
             };
             stmatrix_x4_trans(here + put + e * 512u, sum(x[4 * e], x[4 * e + 1], old.x), sum(x[4 * e + 2], x[4 * e + 3], old.y),
                               sum(y[4 * e], y[4 * e + 1], old.z), sum(y[4 * e + 2], y[4 * e + 3], old.w));
@@ -689,10 +691,8 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
             const uint4 v = ld_shared_v4(here + get + e * 512u);
-            const int32_t r = rows[tok0 + 8 * e + row8];
-            if (r >= 0 && n < a.n) st_global_v4(a.out + r * a.os + n, v.x, v.y, v.z, v.w);
+            if (r[e] >= 0 && n < a.n) st_global_v4(a.out + r[e] * a.os + n, v.x, v.y, v.z, v.w);
           }
-          __syncwarp();
         }
         tc_fence_before();
         __syncwarp();
@@ -887,7 +887,7 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
     t.rank16 = static_cast<uint32_t>(d.rank + 15) / 16;
     t.chunks = (t.rank16 + 3) / 4;
     t.stage_bytes = kAtcTile + t.rank16 * 16 * 128;
-    const uint32_t tables = kAtcBars * 8 + 1544 + 128 + 8 * static_cast<uint32_t>(d.groups + 1);
+    const uint32_t tables = kAtcBars * 8 + 1544 + 256 + 8 * static_cast<uint32_t>(d.groups + 1);
     t.stages = std::min<uint32_t>(kAtcMaxStages, (kAtcSmem - 1024 - kAtcStaging - tables) / t.stage_bytes);
     t.region = std::max(t.stages * t.stage_bytes, 4 * t.chunks * kAtcTile);
     t.idesc_u = idesc_f16(bf16, 0u, 0u, kAtcRows, t.rank16 * 16);

@@ -22,13 +22,12 @@ __device__ __forceinline__ uint32_t scan_add(uint32_t v) {
   return v;
 }
 
-// By a whole CTA of THREADS threads (at most 512): off[g], the groups' first
-// rows, never decreasing and never past `rows`.  off holds groups + 1 values,
-// scratch 16.  A barrier of the CTA has to follow.
+// By a whole CTA of THREADS threads: off[g], the groups' first rows, never
+// decreasing and never past `rows`.  off holds groups + 1 values, scratch one for
+// each warp.  A barrier of the CTA has to follow.
 template <int THREADS>
 __device__ __forceinline__ void group_rows(const int32_t* offsets, int32_t groups, int32_t rows, uint32_t* off,
                                            uint32_t* scratch) {
-  static_assert(THREADS <= 512, "scratch: a value of each warp");
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t n = static_cast<uint32_t>(groups) + 1;
   const uint32_t per = (n + THREADS - 1) / THREADS;
@@ -51,7 +50,6 @@ __device__ __forceinline__ void group_rows(const int32_t* offsets, int32_t group
 // them; first[entries] is their number.
 template <int THREADS, typename TilesOf>
 __device__ __forceinline__ void group_tiles(int32_t entries, TilesOf tiles_of, uint32_t* first, uint32_t* scratch) {
-  static_assert(THREADS <= 512, "scratch: a value of each warp");
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t n = static_cast<uint32_t>(entries) + 1;
   const uint32_t per = (n + THREADS - 1) / THREADS;
