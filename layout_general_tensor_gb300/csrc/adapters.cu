@@ -92,11 +92,13 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
 }
 
 // Rows of no group, at the places before the first group and behind the last:
-// base to out, by all CTAs.
-__device__ __forceinline__ void copy_others(const AdapterArgs& a, const uint32_t* off, uint32_t threads) {
+// base to out, by the CTAs that have no tile where there are some, else by all.
+__device__ __forceinline__ void copy_others(const AdapterArgs& a, const uint32_t* off, uint32_t busy_ctas, uint32_t threads) {
+  const uint32_t from = busy_ctas < gridDim.x ? busy_ctas : 0u;
+  if (blockIdx.x < from) return;
   const uint32_t head = off[0], none = head + static_cast<uint32_t>(a.rows) - off[a.groups];
   const uint32_t pieces = static_cast<uint32_t>(a.n) / 8;
-  for (uint32_t i = blockIdx.x; i < none; i += gridDim.x) {
+  for (uint32_t i = blockIdx.x - from; i < none; i += gridDim.x - from) {
     int32_t r = static_cast<int32_t>(i < head ? i : off[a.groups] + (i - head));
     if (a.order) r = a.order[r];
     if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) continue;
@@ -112,6 +114,7 @@ struct AdapterCfg {
   static constexpr int TOK16 = (TOK + 15) / 16 * 16;
   static constexpr int M2 = TOK16 / 16 == 1 || MT == 8 ? 1 : 2;  // 16-row groups of a warp in the second product
   static constexpr int SHARES = TOK16 / (16 * M2);         // warps that share a block of columns
+  static constexpr int BATCH = MT * M2 == 1 ? 4 : MT * M2 <= 4 ? 2 : 1;  // blocks of columns on their way, as registers allow
   static constexpr int PITCH = RANK + 4;                   // fp32: 8 lanes' columns and 4 lanes' rows in 32 banks
   static constexpr int UPITCH = RANK + 8;                  // 16-bit
   static constexpr size_t PART = sizeof(float) * kAdWarps * TOK * PITCH;
@@ -206,6 +209,42 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
           for (int e = 0; e < 4; ++e)
             p[(8 * j + 2 * q + (e & 1)) * C::PITCH + 16 * i + l4 + 8 * (e >> 1)] = acc[i][j][e];
     }
+    // What the second product reads, a batch of blocks of 32 columns at a time; the
+    // first batch is on its way while the sums are joined.
+    const int share = warp % C::SHARES, apart = kAdWarps / C::SHARES;
+    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / a.ctas) + warp / C::SHARES;
+    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / a.ctas);
+    const uint16_t* br = a.b + static_cast<int64_t>(g) * a.n * a.rank + 4 * q;
+    uint2 bv[C::BATCH][4][MT];
+    uint4 old[C::BATCH][C::M2][2];
+    int32_t row[C::M2][2];
+#pragma unroll
+    for (int m = 0; m < C::M2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = (share * C::M2 + m) * 16 + 8 * h + l4;
+        row[m][h] = t < C::TOK ? row_of[t] : -1;
+      }
+    auto load_blocks = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < C::BATCH; ++i) {
+        const bool in = b + i * apart < b1;
+        const int n = (b + i * apart) * 32;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = n + 8 * (l4 >> 1) + 2 * j + (l4 & 1);
+#pragma unroll
+          for (int s = 0; s < MT; ++s)
+            bv[i][j][s] = load8(br + static_cast<int64_t>(c) * a.rank + 16 * s, in && c < a.n && 16 * s + 4 * q < a.rank);
+        }
+#pragma unroll
+        for (int m = 0; m < C::M2; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            old[i][m][h] = load16(a.base + row[m][h] * a.bs + n + 8 * q, in && n + 8 * q < a.n && row[m][h] >= 0);
+      }
+    };
+    load_blocks(b0);
     __syncthreads();
     constexpr int PER = C::RANK / 4;  // lanes of a row, a power of two
     float4 mine4[(C::TOK * PER + kAdThreads - 1) / kAdThreads];
@@ -264,9 +303,7 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
     // ------------------------------------------------------------ out = base + u B^T
     {
       constexpr int M2 = C::M2;
-      const int share = warp % C::SHARES;
       uint2 hi[M2][MT][2], lo[M2][MT][2];
-      int32_t row[M2][2];
       float f[M2][2];
 #pragma unroll
       for (int m = 0; m < M2; ++m)
@@ -274,7 +311,6 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
         for (int h = 0; h < 2; ++h) {
           const int t = (share * M2 + m) * 16 + 8 * h + l4;
           const bool live = t < C::TOK;
-          row[m][h] = live ? row_of[t] : -1;
           f[m][h] = live ? factor[t] : 0.0f;
 #pragma unroll
           for (int s = 0; s < MT; ++s) {
@@ -282,48 +318,36 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
             lo[m][s][h] = live ? *reinterpret_cast<const uint2*>(ul + t * C::UPITCH + 16 * s + 4 * q) : make_uint2(0u, 0u);
           }
         }
-      const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / a.ctas);
-      const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / a.ctas);
-      const uint16_t* br = a.b + static_cast<int64_t>(g) * a.n * a.rank + 4 * q;
-      for (int b = b0 + warp / C::SHARES; b < b1; b += kAdWarps / C::SHARES) {
-        uint2 bv[4][MT];
-        uint4 old[M2][2];
-        const int n = b * 32;
+      for (int b = b0; b < b1; b += C::BATCH * apart) {
+        if (b > b0) load_blocks(b);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = n + 8 * (l4 >> 1) + 2 * j + (l4 & 1);
+        for (int i = 0; i < C::BATCH; ++i) {
+          const int n = (b + i * apart) * 32 + 8 * q;
+          const bool in = b + i * apart < b1 && n < a.n;
 #pragma unroll
-          for (int s = 0; s < MT; ++s)
-            bv[j][s] = load8(br + static_cast<int64_t>(c) * a.rank + 16 * s, c < a.n && 16 * s + 4 * q < a.rank);
-        }
-        const bool in = n + 8 * q < a.n;
-#pragma unroll
-        for (int m = 0; m < M2; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) old[m][h] = load16(a.base + row[m][h] * a.bs + n + 8 * q, in && row[m][h] >= 0);
-#pragma unroll
-        for (int m = 0; m < M2; ++m) {
-          float acc[4][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-#pragma unroll
-            for (int s = 0; s < MT; ++s) {
-              mma16816<BF16>(acc[j], hi[m][s][0].x, hi[m][s][1].x, hi[m][s][0].y, hi[m][s][1].y, bv[j][s].x, bv[j][s].y);
-              mma16816<BF16>(acc[j], lo[m][s][0].x, lo[m][s][1].x, lo[m][s][0].y, lo[m][s][1].y, bv[j][s].x, bv[j][s].y);
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w[4] = {old[m][h].x, old[m][h].y, old[m][h].z, old[m][h].w};
-            uint32_t y[4];
+          for (int m = 0; m < M2; ++m) {
+            float acc[4][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 o = unpack_pair16<BF16>(w[j]);
-              y[j] = pack_pair16<BF16>(fmaf(acc[j][2 * h], f[m][h], o.x), fmaf(acc[j][2 * h + 1], f[m][h], o.y));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+#pragma unroll
+              for (int s = 0; s < MT; ++s) {
+                mma16816<BF16>(acc[j], hi[m][s][0].x, hi[m][s][1].x, hi[m][s][0].y, hi[m][s][1].y, bv[i][j][s].x, bv[i][j][s].y);
+                mma16816<BF16>(acc[j], lo[m][s][0].x, lo[m][s][1].x, lo[m][s][0].y, lo[m][s][1].y, bv[i][j][s].x, bv[i][j][s].y);
+              }
             }
-            if (in && row[m][h] >= 0) st_global_v4(a.out + row[m][h] * a.os + n + 8 * q, y[0], y[1], y[2], y[3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w[4] = {old[i][m][h].x, old[i][m][h].y, old[i][m][h].z, old[i][m][h].w};
+              uint32_t y[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 o = unpack_pair16<BF16>(w[j]);
+                y[j] = pack_pair16<BF16>(fmaf(acc[j][2 * h], f[m][h], o.x), fmaf(acc[j][2 * h + 1], f[m][h], o.y));
+              }
+              if (in && row[m][h] >= 0) st_global_v4(a.out + row[m][h] * a.os + n, y[0], y[1], y[2], y[3]);
+            }
           }
         }
       }
@@ -336,7 +360,7 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
       __syncthreads();
   }
 
-  if (a.copy) copy_others(a, off, kAdThreads);
+  if (a.copy) copy_others(a, off, tiles * a.ctas, kAdThreads);
   if (a.ctas > 1) cluster_sync_all();
 }
 
@@ -703,7 +727,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   }
 
   // ------------------------------------------------------------ end
-  if (a.copy && !*abort_flag) copy_others(a, off, kAtcThreads);
+  if (a.copy && !*abort_flag) copy_others(a, off, tiles, kAtcThreads);
   __syncthreads();
   if (*abort_flag) {
     // Copies that were made may still be landing, on a barrier that will not
@@ -901,8 +925,8 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
   } else {
     const int nt = rows > 8 * busy ? 4 : 1;
     const int64_t tiles = rows / (8 * nt) + busy;
-    // A cluster as large as leaves a CTA for every SM, or what there is to share.
-    while (a.ctas < 8 && tiles * a.ctas * 2 <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
+    // A cluster as large as leaves every SM two CTAs, or what there is to share.
+    while (a.ctas < 8 && tiles * a.ctas <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
     const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * sms / a.ctas));
     e = bf16 ? launch_adapters<true>(a, nt, clusters, s) : launch_adapters<false>(a, nt, clusters, s);
   }
