@@ -26,6 +26,20 @@ cudaError_t set_smem_once(int bytes) {
   return e;
 }
 
+// Likewise clusters of more than 8 CTAs.
+template <auto Kernel>
+cudaError_t allow_large_clusters_once() {
+  static unsigned long long done = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (bit && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && bit) __atomic_fetch_or(&done, bit, __ATOMIC_RELEASE);
+  return e;
+}
+
 // Launch with programmatic stream serialization: the kernel's prologue
 // (barrier set-up, TMEM allocation, descriptor prefetch) overlaps the end of
 // the previous kernel in the stream; every kernel here calls pdl_wait()

@@ -180,7 +180,7 @@ extern "C" gemm_status_t gemm_row_groups(const int32_t* ids, int64_t rows, int32
   a.run = static_cast<uint32_t>((rows + warps * 32 - 1) / (warps * 32) * 32);
   const int smem = kRgWarps * (groups + 1) * static_cast<int>(sizeof(Bin));
   cudaError_t e = set_smem_once<row_groups_kernel>(kRgWarps * (kRgMaxGroups + 1) * static_cast<int>(sizeof(Bin)));
-  if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(row_groups_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && ctas > 8) e = allow_large_clusters_once<row_groups_kernel>();
   if (e == cudaSuccess)
     e = launch_pdl_cluster(row_groups_kernel, dim3(ctas), dim3(kRgThreads), static_cast<size_t>(smem),
                            static_cast<cudaStream_t>(stream), ctas, a);

@@ -1,0 +1,458 @@
+"""How the operators over groups of rows are called on the GPU: together, as an
+expert layer and as adapters on a projection; their gradients; in captured graphs
+and on other streams, two at once; with offsets and orders that are not what they
+should be; with infinities and NaN in rows of other groups, magnitudes at the
+types' ends and addresses past 2^31 values; and waits that run out.
+
+Where results are compared for equality, inputs are small whole numbers, so that
+every sum is exact in fp32 (test_gpu_groups.py)."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import lib
+from test_gpu_groups import TD, _code, _ints, _offsets
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    return lib()
+
+
+def _order(m, ids, groups):
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device="cuda")
+    order, places = torch.empty_like(ids), torch.empty_like(ids)
+    m.row_groups(ids, offsets, order, places)
+    return offsets, order, places
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("tokens,dtype", [(1, "bf16"), (37, "f16"), (700, "bf16")])
+def test_expert_layer(m, tokens, dtype):
+    """Two of 12 experts for each token: order, products up and down, and back to the tokens with weights."""
+    t, experts, top, hidden, inner = TD[dtype], 12, 2, 192, 320
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    x = (torch.randn(tokens, hidden, generator=g, device="cuda")).to(t)
+    up, down = ((torch.randn(experts, *s, generator=g, device="cuda") * s[1] ** -0.5).to(t) for s in ((inner, hidden), (hidden, inner)))
+    weights, ids = torch.softmax(torch.randn(tokens, experts, generator=g, device="cuda"), -1).topk(top)
+    offsets, order, places = _order(m, ids.int().flatten(), experts)
+    rows = x[order // top]
+    h, y = torch.empty(tokens * top, inner, dtype=t, device="cuda"), torch.empty(tokens * top, hidden, dtype=t, device="cuda")
+    m.GroupedGemm(experts, inner, hidden, dtype=_code(m, dtype)).run(rows, up, offsets, h)
+    a = torch.nn.functional.silu(h.float()).to(t)
+    m.GroupedGemm(experts, hidden, inner, dtype=_code(m, dtype)).run(a, down, offsets, y)
+    out = (y[places.long()].view(tokens, top, hidden).double() * weights[..., None].double()).sum(1)
+    want = torch.zeros(tokens, hidden, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for i in range(tokens):
+        for j in range(top):
+            e = ids[i, j]
+            hh = torch.nn.functional.silu(up[e].double() @ x[i].double())
+            want[i] += weights[i, j].double() * (down[e].double() @ hh)
+            size[i] += weights[i, j].double() * (down[e].double().abs() @ hh.abs())
+    # h, a and y are rounded: at most half a step each of the products' magnitudes, and silu's slope is below 1.1
+    # (h's own rounding is of its value: |h| and not |silu h|, which for negative h is up to |h| / |silu h| more,
+    # but no more than 0.28 / 0.28 where the product counts; 4 half steps of sum |down| max(|a|, half |h|) hold it)
+    big = torch.zeros_like(want)
+    for i in range(tokens):
+        for j in range(top):
+            e = ids[i, j]
+            big[i] += weights[i, j].double() * (down[e].double().abs() @ (up[e].double() @ x[i].double()).abs())
+    assert ((out - want).abs() <= torch.finfo(t).eps / 2 * (1.2 * big + size + want.abs()) + 2.0**-18 * (size + big)).all()
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_adapters_on_a_projection(m, int4):
+    """The shared projection, dense or of int4 weights, and the adapters' change added in place."""
+    rows, n, k, rank, groups = 24, 256, 512, 16, 6
+    t = torch.float16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, k, generator=g, device="cuda").to(t)
+    y = torch.empty(rows, n, dtype=t, device="cuda")
+    if int4:
+        w = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+        scales, zeros = torch.full((n, k // 128), 0.01, dtype=t, device="cuda"), torch.full((n, k // 128), 8.0, dtype=t, device="cuda")
+        op = m.Gemm(m.make_desc(rows, n, k, a_dtype=m.GEMM_F16, b_dtype=m.GEMM_INT4, split_k=0, group_size=128))
+        op.run(x, w, y, scales=scales, zeros=zeros)
+    else:
+        op = m.Gemm(m.make_desc(rows, n, k, a_dtype=m.GEMM_F16, split_k=0))
+        op.run(x, (torch.randn(n, k, generator=g, device="cuda") * k**-0.5).to(t), y)
+    shared = y.clone()
+    a, b = (torch.randn(groups, rank, k, generator=g, device="cuda") * k**-0.5).to(t), (torch.randn(groups, n, rank, generator=g, device="cuda") * 0.3).to(t)
+    ids = torch.randint(-1, groups, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    offsets, order, _ = _order(m, ids, groups)
+    m.Adapters(groups, n, k, rank, dtype=m.GEMM_F16).run(x, a, b, offsets, order, y, y)
+    for r, e in enumerate(ids.tolist()):
+        if e < 0:
+            assert torch.equal(y[r], shared[r])
+            continue
+        u = a[e].double() @ x[r].double()
+        want = shared[r].double() + b[e].double() @ u
+        off = 2.0**-20 * (a[e].double().abs() @ x[r].double().abs()) + 2.0**-16 * u.abs().max() + 2.0**-20 * u.abs()
+        error = b[e].double().abs() @ off
+        assert ((y[r].double() - want).abs() <= error + (want.abs() + error) * (2.0**-11 + 2.0**-23)).all()
+
+
+# ------------------------------------------------------------------ gradients
+
+@pytest.mark.parametrize("k_contig", [True, False])
+@pytest.mark.parametrize("sizes", [[5, 0, 40, 1], [130, 300, 0, 77]], ids=["few", "many"])
+def test_gradients(m, k_contig, sizes):
+    """f = sum(C * dC): its gradients to A and B by the products, against the formula and against differences
+    (f is linear in each, and whole numbers make both exact)."""
+    t, n, k, groups, rows = torch.float16, 72, 136, len(sizes), sum(sizes)
+    a, dc = _ints(1, rows, k, dtype=t), _ints(2, rows, n, dtype=t)
+    b = _ints(3, groups, *((n, k) if k_contig else (k, n)), dtype=t)
+    offsets, at = _offsets(sizes), np.concatenate([[0], np.cumsum(sizes)])
+    layout, other = (m.GEMM_K_CONTIG, m.GEMM_MN_CONTIG) if k_contig else (m.GEMM_MN_CONTIG, m.GEMM_K_CONTIG)
+    da, db = torch.empty_like(a), torch.empty_like(b)
+    m.GroupedGemm(groups, k, n, b_layout=other, dtype=m.GEMM_F16).run(dc, b, offsets, da)
+    op = m.GroupedGemmK(groups, *((n, k) if k_contig else (k, n)), dtype=m.GEMM_F16)
+    op.run(*((dc, a) if k_contig else (a, dc)), offsets, db)
+    for g in range(groups):
+        lo, hi = at[g], at[g + 1]
+        w = b[g].double() if k_contig else b[g].double().T
+        assert torch.equal(da[lo:hi], (dc[lo:hi].double() @ w).to(t))
+        want = dc[lo:hi].double().T @ a[lo:hi].double()
+        assert torch.equal(db[g], (want if k_contig else want.T).to(t))
+
+    forward = m.GroupedGemm(groups, n, k, b_layout=layout, dtype=m.GEMM_F16)
+
+    def f(a, b):
+        c = torch.zeros(rows, n, dtype=t, device="cuda")
+        forward.run(a, b, offsets, c)
+        return (c.double() * dc.double()).sum()
+    for r, i in ((0, 0), (rows - 1, k - 1), (rows // 2, 77)):
+        moved = a.clone()
+        moved[r, i] += 1
+        assert f(moved, b) - f(a, b) == da[r, i].double()
+    for g in range(groups):
+        for i, j in ((0, 0), (b.shape[1] - 1, b.shape[2] - 1)):
+            moved = b.clone()
+            moved[g, i, j] += 1
+            assert f(a, moved) - f(a, b) == db[g, i, j].double()
+
+
+# ------------------------------------------------------------------ graphs, streams, repeats
+
+def _operators(m, big):
+    """Each operator on whole numbers: (its call, its output, what the output has to be for the present ids)."""
+    t, groups, n, k, rank = torch.float16, 6, 136, 200, 16
+    rows = 6000 if big else 50
+    ids = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    offsets, order, places = torch.zeros(groups + 1, dtype=torch.int32, device="cuda"), torch.zeros_like(ids), torch.zeros_like(ids)
+    a, b = _ints(1, rows, k, dtype=t), _ints(2, groups, n, k, dtype=t)
+    c, d = torch.zeros(rows, n, dtype=t, device="cuda"), torch.zeros(groups, k, n, dtype=t, device="cuda")
+    e = _ints(3, rows, n, dtype=t, most=1)
+    down, up = _ints(4, groups, rank, k, dtype=t, most=1), _ints(5, groups, n, rank, dtype=t, most=1)
+    out = torch.zeros_like(c)
+    objects = m.GroupedGemm(groups, n, k, dtype=m.GEMM_F16), m.GroupedGemmK(groups, k, n, dtype=m.GEMM_F16), m.Adapters(groups, n, k, rank, dtype=m.GEMM_F16)
+
+    def run(stream=None):
+        m.row_groups(ids, offsets, order, places, stream=stream)
+        objects[0].run(a, b, offsets, c, stream=stream)
+        objects[1].run(a, e, offsets, d, stream=stream)
+        objects[2].run(a, down, up, offsets, order, e, out, stream=stream)
+
+    def check():
+        assert all(o.sync_status() == m.GEMM_OK for o in objects)
+        key = torch.where((ids < 0) | (ids >= groups), groups, ids).long()
+        want = torch.sort(key, stable=True).indices
+        assert torch.equal(order.long(), want)
+        at = [int((key < g).sum()) for g in range(groups + 1)]
+        assert offsets.tolist() == at
+        wo = e.double()
+        for g in range(groups):
+            lo, hi = at[g], at[g + 1]
+            assert torch.equal(c[lo:hi], (a[lo:hi].double() @ b[g].double().T).to(t))
+            assert torch.equal(d[g], (a[lo:hi].double().T @ e[lo:hi].double()).to(t))
+            r = want[lo:hi]
+            wo[r] += (a[r].double() @ down[g].double().T) @ up[g].double().T
+        assert torch.equal(out, wo.to(t))
+
+    def draw(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ids.copy_(torch.randint(-1, groups, (rows,), generator=g, device="cuda"))
+        if seed % 2:
+            ids[ids == 2] = 3
+    return run, check, draw, (c, d, out, order)
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_graph_replays_take_the_sizes_of_the_time(m, big):
+    run, check, draw, _ = _operators(m, big)
+    draw(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in range(1, 5):
+        draw(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        check()
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_streams(m, big):
+    """On a stream of the call's own, and two sets of operators at once on two streams."""
+    first, second = _operators(m, big), _operators(m, big)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for seed in range(3):
+        first[2](seed)
+        second[2](seed + 7)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            first[0](s1.cuda_stream)
+            second[0](s2.cuda_stream)
+        torch.cuda.synchronize()
+        first[1]()
+        second[1]()
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_one_object_on_two_streams(m, big):
+    """Objects hold no workspace: runs of one may be under way at the same time."""
+    t, n, k, sizes = torch.float16, 520, 264, [700, 0, 900, 41] if big else [3, 0, 9, 1]
+    offsets = _offsets(sizes)
+    op, opk = m.GroupedGemm(4, n, k, dtype=m.GEMM_F16), m.GroupedGemmK(4, k, n, dtype=m.GEMM_F16)
+    sets = []
+    for i in range(2):
+        a, b, e = _ints(i, sum(sizes), k, dtype=t), _ints(i + 5, 4, n, k, dtype=t), _ints(i + 9, sum(sizes), n, dtype=t)
+        sets.append((torch.cuda.Stream(), a, b, e, torch.empty(sum(sizes), n, dtype=t, device="cuda"), torch.empty(4, k, n, dtype=t, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, a, b, e, c, d in sets:
+            op.run(a, b, offsets, c, stream=s.cuda_stream)
+            opk.run(a, e, offsets, d, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    at = offsets.tolist()
+    for _, a, b, e, c, d in sets:
+        for g in range(4):
+            lo, hi = at[g], at[g + 1]
+            assert torch.equal(c[lo:hi], (a[lo:hi].double() @ b[g].double().T).to(t))
+            assert torch.equal(d[g], (a[lo:hi].double().T @ e[lo:hi].double()).to(t))
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_repeated_calls_give_the_same_bits(m, big):
+    sizes = [2100, 0, 3111, 17] if big else [4, 0, 31, 1]
+    rows, n, k, rank = sum(sizes), 264, 1000, 24
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def normal(*s):
+        return torch.randn(s, generator=g, device="cuda").bfloat16()
+    offsets, a, b, e, down, up = _offsets(sizes), normal(rows, k), normal(4, n, k), normal(rows, n), normal(4, rank, k), normal(4, n, rank)
+    ops = m.GroupedGemm(4, n, k), m.GroupedGemmK(4, k, n), m.Adapters(4, n, k, rank)
+    seen = []
+    for _ in range(4):
+        c, d, out = torch.empty(rows, n, dtype=a.dtype, device="cuda"), torch.empty(4, k, n, dtype=a.dtype, device="cuda"), torch.empty_like(e)
+        ops[0].run(a, b, offsets, c)
+        ops[1].run(a, e, offsets, d)
+        ops[2].run(a, down, up, offsets, None, e, out)
+        seen.append((c, d, out))
+    for other in seen[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(seen[0], other))
+
+
+# ------------------------------------------------------------------ offsets and orders
+
+@pytest.mark.parametrize("offsets,means", [([0, 5, 3, 9], [0, 5, 5, 9]), ([-4, -1, 6, 60], [0, 0, 6, 20]), ([30, 40, 50, 60], [20, 20, 20, 20]),
+                                           ([4, 4, 4, 4], [4, 4, 4, 4]), ([0, 2**31 - 1, -2**31, 7], [0, 20, 20, 20])])
+def test_offsets_that_are_not_what_they_should_be(m, offsets, means):
+    t, n, k, rank, rows = torch.float16, 72, 72, 8, 20
+    at = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    a, b, e = _ints(1, rows, k, dtype=t), _ints(2, 3, n, k, dtype=t), _ints(3, rows, n, dtype=t)
+    down, up = _ints(4, 3, rank, k, dtype=t, most=1), _ints(5, 3, n, rank, dtype=t, most=1)
+    c, d, out = torch.full((rows, n), -7.0, dtype=t, device="cuda"), torch.empty(3, k, n, dtype=t, device="cuda"), torch.empty_like(e)
+    m.GroupedGemm(3, n, k, dtype=m.GEMM_F16).run(a, b, at, c)
+    m.GroupedGemmK(3, k, n, dtype=m.GEMM_F16).run(a, e, at, d)
+    m.Adapters(3, n, k, rank, dtype=m.GEMM_F16).run(a, down, up, at, None, e, out)
+    wc, wo = torch.full((rows, n), -7.0, dtype=torch.float64, device="cuda"), e.double()
+    for g in range(3):
+        lo, hi = means[g], means[g + 1]
+        wc[lo:hi] = a[lo:hi].double() @ b[g].double().T
+        assert torch.equal(d[g], (a[lo:hi].double().T @ e[lo:hi].double()).to(t))
+        wo[lo:hi] += (a[lo:hi].double() @ down[g].double().T) @ up[g].double().T
+    assert torch.equal(c, wc.to(t)) and torch.equal(out, wo.to(t))
+
+
+@pytest.mark.parametrize("rows", [40, 6000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_order_with_numbers_of_no_row(m, rows, in_place):
+    """They are left out: their places' rows stay as they were."""
+    t, n, k, rank = torch.float16, 136, 72, 8
+    order = torch.randperm(rows, device="cuda").int()
+    gone = order[::7].clone()
+    order[::7] = torch.tensor([-1, rows, 2**31 - 1, -2**31], dtype=torch.int32, device="cuda").repeat(rows)[:len(gone)]
+    x, e = _ints(1, rows, k, dtype=t), _ints(2, rows, n, dtype=t)
+    down, up = _ints(4, 2, rank, k, dtype=t, most=1), _ints(5, 2, n, rank, dtype=t, most=1)
+    before = e.clone()
+    out = e if in_place else torch.full_like(e, -9.0)
+    sizes = [rows // 2, rows // 3]
+    m.Adapters(2, n, k, rank, dtype=m.GEMM_F16).run(x, down, up, _offsets(sizes), order, e, out)
+    want, at = before.double(), 0
+    for g, size in enumerate(sizes):
+        r = order[at:at + size].long()
+        r = r[(r >= 0) & (r < rows)]
+        want[r] += (x[r].double() @ down[g].double().T) @ up[g].double().T
+        at += size
+    if not in_place:
+        want[gone.long()] = -9.0
+    assert torch.equal(out, want.to(t))
+
+
+# ------------------------------------------------------------------ infinities, NaN, magnitudes
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("sizes", [[7, 3, 9, 0, 20], [200, 33, 150, 0, 300], [2000, 1100, 2500, 0, 600]], ids=["few", "some", "many"])
+def test_a_group_reaches_no_other(m, value, sizes):
+    """Group 1's rows, weights and adapter hold what is not finite; every other result is exact."""
+    t, n, k, rank, rows, groups = torch.float16, 136, 200, 24, sum(sizes), len(sizes)
+    offsets, at = _offsets(sizes), np.concatenate([[0], np.cumsum(sizes)])
+    lo1, hi1 = at[1], at[2]
+    a, b, e = _ints(1, rows, k, dtype=t), _ints(2, groups, n, k, dtype=t), _ints(3, rows, n, dtype=t, most=1)
+    down, up = _ints(4, groups, rank, k, dtype=t, most=1), _ints(5, groups, n, rank, dtype=t, most=1)
+    for x in (a[lo1:hi1], e[lo1:hi1], b[1], down[1], up[1]):
+        x.fill_(value)
+    a[0, 3] = value  # and one row of group 0
+    c, d, out = torch.zeros(rows, n, dtype=t, device="cuda"), torch.empty(groups, k, n, dtype=t, device="cuda"), torch.zeros(rows, n, dtype=t, device="cuda")
+    m.GroupedGemm(groups, n, k, dtype=m.GEMM_F16).run(a, b, offsets, c)
+    m.GroupedGemmK(groups, k, n, dtype=m.GEMM_F16).run(a, e, offsets, d)
+    m.Adapters(groups, n, k, rank, dtype=m.GEMM_F16).run(a, down, up, offsets, None, e, out)
+    for g in (0, 2, 3, 4):
+        lo, hi = at[g] + (g == 0), at[g + 1]
+        assert torch.equal(c[lo:hi], (a[lo:hi].double() @ b[g].double().T).to(t))
+        assert torch.equal(out[lo:hi], (e[lo:hi].double() + (a[lo:hi].double() @ down[g].double().T) @ up[g].double().T).to(t))
+        if g:
+            assert torch.equal(d[g], (a[lo:hi].double().T @ e[lo:hi].double()).to(t))
+    assert not c[lo1:hi1].isfinite().any() and not out[lo1:hi1].isfinite().any() and not d[1].isfinite().any() and not c[0].isfinite().all()
+    col = torch.ones(k, dtype=torch.bool, device="cuda")
+    col[3] = False
+    assert torch.equal(d[0][col], (a[:lo1].double().T @ e[:lo1].double()).to(t)[col])
+
+
+@pytest.mark.parametrize("rows", [5, 6000])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", ["large", "small"])
+def test_adapters_between_magnitudes(m, rows, dtype, scale):
+    """A first product past the type's range, or below its least value, of a result that is neither."""
+    t, n, k, rank = TD[dtype], 72, 256, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    top = {"f16": {"large": (2.0**9, 2.0**9, 2.0**-14), "small": (2.0**-11, 2.0**-11, 2.0**12)},
+           "bf16": {"large": (2.0**60, 2.0**60, 2.0**-120), "small": (2.0**-60, 2.0**-60, 2.0**118)}}[dtype][scale]
+    x, a, b = ((torch.randn(s, generator=g, device="cuda") * v).to(t) for s, v in (((rows, k), top[0]), ((1, rank, k), top[1]), ((1, n, rank), top[2])))
+    base, out = torch.zeros(rows, n, dtype=t, device="cuda"), torch.empty(rows, n, dtype=t, device="cuda")
+    m.Adapters(1, n, k, rank, dtype=_code(m, dtype)).run(x, a, b, _offsets([rows]), None, base, out)
+    u = x.double() @ a[0].double().T
+    assert (u.abs().max() > 65504) if scale == "large" else (u.abs().max() < 2.0**-15)
+    want = u @ b[0].double().T
+    off = 2.0**-20 * (x.double().abs() @ a[0].double().abs().T) + 2.0**-16 * u.abs().amax(-1, keepdim=True) + 2.0**-20 * u.abs()
+    error = off @ b[0].double().abs().T
+    assert ((out.double() - want).abs() <= error + (want.abs() + error) * (torch.finfo(t).eps / 2 + 2.0**-23) + torch.finfo(t).smallest_normal * torch.finfo(t).eps).all()
+
+
+# ------------------------------------------------------------------ far addresses
+
+def test_rows_past_31_bits(m):
+    """More than 2^31 values in A and C, and in B."""
+    t, rows, n, k = torch.bfloat16, 150000, 16384, 64
+    a, b = torch.zeros(rows, k, dtype=t, device="cuda"), _ints(2, 3, n, k, dtype=t)
+    c = torch.zeros(rows, n, dtype=t, device="cuda")
+    sizes = [140000, 3, 9000]
+    marked = [0, 131071, 131072, 139999, 140001, 149002]
+    for r in marked:
+        a[r] = _ints(r, k, dtype=t)
+    m.GroupedGemm(3, n, k).run(a, b, _offsets(sizes), c)
+    for r in marked:
+        g = 0 if r < 140000 else 1 if r < 140003 else 2
+        assert torch.equal(c[r], (b[g].double() @ a[r].double()).to(t))
+        a[r], c[r] = 0, 0
+    assert not c.any()
+    del a, b, c
+    groups, n, k = 40, 8192, 8192
+    a, b, c = _ints(1, 20, k, dtype=t), torch.zeros(groups, n, k, dtype=t, device="cuda"), torch.zeros(20, n, dtype=t, device="cuda")
+    b[33, ::3], b[39, 1::2] = 1, 1
+    sizes = [0] * groups
+    sizes[33], sizes[39] = 12, 8
+    m.GroupedGemm(groups, n, k).run(a, b, _offsets(sizes), c)
+    want = torch.cat([a[:12].double() @ b[33].double().T, a[12:].double() @ b[39].double().T])
+    assert torch.equal(c, want.to(t))
+
+
+def test_sums_past_31_bits(m):
+    t, groups, mm, n = torch.bfloat16, 40, 8192, 8192
+    sizes = [0] * groups
+    sizes[0], sizes[38], sizes[39] = 3, 20, 1
+    a, b = _ints(1, 24, mm, dtype=t), _ints(2, 24, n, dtype=t)
+    c = torch.ones(groups, mm, n, dtype=t, device="cuda")
+    m.GroupedGemmK(groups, mm, n).run(a, b, _offsets(sizes), c)
+    for g, lo, hi in ((0, 0, 3), (38, 3, 23), (39, 23, 24)):
+        assert torch.equal(c[g], (a[lo:hi].float().T @ b[lo:hi].float()).to(t))
+    assert not c[1:38].any()
+
+
+@pytest.mark.parametrize("spread", [False, True])
+def test_adapters_past_31_bits(m, spread):
+    """More than 2^31 values in x and out, for few groups of many rows and for many of one row."""
+    t, rows, n, k, rank = torch.bfloat16, 36000, 65536, 65536, 8
+    x, base = torch.zeros(rows, k, dtype=t, device="cuda"), torch.zeros(rows, n, dtype=t, device="cuda")
+    groups = 2 if not spread else 5
+    down, up = torch.zeros(groups, rank, k, dtype=t, device="cuda"), _ints(2, groups, n, rank, dtype=t)
+    down[:, :, ::4096] = 1
+    marked = [0, 32767, 32768, 35999]
+    for r in marked:
+        x[r, ::4096] = r % 5 + 1
+    if spread:  # the marked rows alone, each with an adapter
+        order = torch.tensor(marked, dtype=torch.int32, device="cuda")
+        order = torch.cat([order, torch.tensor([r for r in range(rows) if r not in marked], dtype=torch.int32, device="cuda")])
+        offsets = torch.tensor([0, 1, 2, 3, 4, 4], dtype=torch.int32, device="cuda")
+    else:
+        order, offsets = None, _offsets([34000, 2000])
+    m.Adapters(groups, n, k, rank).run(x, down, up, offsets, order, base, base)
+    for i, r in enumerate(marked):
+        g = i if spread else int(r >= 34000)
+        assert torch.equal(base[r], (up[g].double().sum(-1) * 16 * (r % 5 + 1)).to(t)), r
+        base[r] = 0
+    assert not base.any()
+
+
+# ------------------------------------------------------------------ waits that run out
+
+@pytest.mark.parametrize("kind", ["few rows", "many rows", "along K", "along K, narrow", "adapters"])
+def test_waits_run_out(m, kind, monkeypatch):
+    """A load that is withheld: the run's status says so, and the next run is right."""
+    monkeypatch.setenv("LGT_GEMM_WAIT_LIMIT_MS", "20")
+    t = torch.float16
+    if kind in ("few rows", "many rows"):
+        sizes, n, k = ([3, 9], 264, 200) if kind == "few rows" else ([700, 400], 264, 200)
+        a, b, c = _ints(1, sum(sizes), k, dtype=t), _ints(2, 2, n, k, dtype=t), torch.zeros(sum(sizes), n, dtype=t, device="cuda")
+        op, args = m.GroupedGemm(2, n, k, dtype=m.GEMM_F16), (a, b, _offsets(sizes), c)
+        want = torch.cat([a[:sizes[0]].double() @ b[0].double().T, a[sizes[0]:].double() @ b[1].double().T]).to(t)
+        got, withhold = c, m._lib.gemm_grouped_withhold_load
+    elif kind.startswith("along K"):
+        n = 264 if kind == "along K" else 72
+        a, b, c = _ints(1, 300, 200, dtype=t), _ints(2, 300, n, dtype=t), torch.zeros(2, 200, n, dtype=t, device="cuda")
+        op, args = m.GroupedGemmK(2, 200, n, dtype=m.GEMM_F16), (a, b, _offsets([133, 167]), c)
+        want = torch.stack([a[:133].double().T @ b[:133].double(), a[133:].double().T @ b[133:].double()]).to(t)
+        got, withhold = c, m._lib.gemm_grouped_withhold_load
+    else:
+        x, down, up, base = _ints(1, 6000, 200, dtype=t), _ints(2, 1, 8, 200, dtype=t, most=1), _ints(3, 1, 72, 8, dtype=t, most=1), _ints(4, 6000, 72, dtype=t)
+        got = torch.zeros_like(base)
+        op, args = m.Adapters(1, 72, 200, 8, dtype=m.GEMM_F16), (x, down, up, _offsets([6000]), None, base, got)
+        want, withhold = (base.double() + (x.double() @ down[0].double().T) @ up[0].double().T).to(t), m._lib.gemm_adapters_withhold_load
+    assert withhold(op.plan) == m.GEMM_OK
+    op.run(*args)
+    assert op.sync_status() == m.GEMM_ERR_TIMEOUT
+    assert op.sync_status() == m.GEMM_OK
+    op.run(*args)
+    assert op.sync_status() == m.GEMM_OK and torch.equal(got, want)
