@@ -96,6 +96,37 @@ def test_adapters_on_a_projection(m, int4):
         assert ((y[r].double() - want).abs() <= error + (want.abs() + error) * (2.0**-11 + 2.0**-23)).all()
 
 
+def test_the_layer_example_runs():
+    """It runs, and its gradients are those of the same layer in 64 bits (of its own choices of experts), but for the
+    roundings of what lies between: half a step at each of six places of values that are sums of as many random signs,
+    so 6 * 2^-8 of a gradient's norm is far beyond them and far below a wrong product's."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    layer = ex.ExpertLayer(128, 192, 8, 2, adapters=3, rank=8)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, d_out = (torch.randn(150, 128, generator=g, device="cuda").bfloat16() for _ in range(2))
+    adapter = torch.randint(-1, 3, (150,), generator=g, device="cuda", dtype=torch.int32)
+    out, kept = layer.forward(x, adapter)
+    grads = layer.backward(kept, d_out)
+    weights, ids = torch.softmax(x.float() @ layer.w_router.float().T, -1).topk(2)
+    xd, up, down = (t.double().requires_grad_() for t in (x, layer.w_up, layer.w_down))
+    mixed = torch.zeros(150, 128, dtype=torch.float64, device="cuda")
+    for j in range(2):
+        h = torch.einsum("th,tih->ti", xd, up[ids[:, j]])
+        mixed = mixed + weights[:, j, None].double() * torch.einsum("ti,thi->th", torch.nn.functional.silu(h), down[ids[:, j]])
+    want = torch.autograd.grad((mixed * d_out.double()).sum(), (xd, up, down))
+    shared = x.double() @ layer.w_shared.double().T
+    for r, e in enumerate(adapter.tolist()):
+        if e >= 0:
+            shared[r] += 2.0 * (layer.b[e].double() @ (layer.a[e].double() @ x[r].double()))
+    for got, right in ((out, mixed.detach() + shared), *zip(grads, want)):
+        assert float((got.double() - right).norm() / right.norm()) < 6 * 2.0**-8
+
+
 # ------------------------------------------------------------------ gradients
 
 @pytest.mark.parametrize("k_contig", [True, False])
