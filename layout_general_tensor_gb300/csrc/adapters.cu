@@ -91,19 +91,36 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   lo = pack_pair16<BF16>(isfinite(h.x) ? x - h.x : 0.0f, isfinite(h.y) ? y - h.y : 0.0f);
 }
 
-// Rows of no group, at the places before the first group and behind the last:
-// base to out, by the CTAs that have no tile where there are some, else by all.
-__device__ __forceinline__ void copy_others(const AdapterArgs& a, const uint32_t* off, uint32_t busy_ctas, uint32_t threads) {
-  const uint32_t from = busy_ctas < gridDim.x ? busy_ctas : 0u;
-  if (blockIdx.x < from) return;
-  const uint32_t head = off[0], none = head + static_cast<uint32_t>(a.rows) - off[a.groups];
-  const uint32_t pieces = static_cast<uint32_t>(a.n) / 8;
-  for (uint32_t i = blockIdx.x - from; i < none; i += gridDim.x - from) {
-    int32_t r = static_cast<int32_t>(i < head ? i : off[a.groups] + (i - head));
+// Rows of no group, at the places before the first group and behind the last, go
+// from base to out, as tiles of their own behind the groups': `tile` of `per` rows,
+// by `threads` of each CTA of a cluster, whose CTAs (`share` of `shares`) take
+// pieces in turn.
+__device__ __forceinline__ uint32_t other_rows(const AdapterArgs& a, const uint32_t* off) {
+  return a.copy ? off[0] + static_cast<uint32_t>(a.rows) - off[a.groups] : 0u;
+}
+__device__ __forceinline__ void copy_others(const AdapterArgs& a, const uint32_t* off, uint32_t tile, uint32_t per, uint32_t share,
+                                            uint32_t shares, uint32_t thread, uint32_t threads) {
+  const uint32_t from = tile * per, rows = min(per, other_rows(a, off) - from), pieces = static_cast<uint32_t>(a.n) / 8;
+  // (lanes take neighbouring pieces of a row; four are on their way at once)
+  const uint32_t across = min(threads, (pieces + 31) / 32 * 32), high = threads / across;
+  const uint32_t c0 = thread % across, r0 = thread / across;
+  if (r0 >= high) return;
+  for (uint32_t i = r0; i < rows; i += high) {
+    const uint32_t place = from + i;
+    int32_t r = static_cast<int32_t>(place < off[0] ? place : off[a.groups] + (place - off[0]));
     if (a.order) r = a.order[r];
     if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) continue;
-    for (uint32_t c = threadIdx.x; c < pieces; c += threads)
-      *reinterpret_cast<uint4*>(a.out + r * a.os + c * 8) = *reinterpret_cast<const uint4*>(a.base + r * a.bs + c * 8);
+    const uint16_t* src = a.base + r * a.bs;
+    uint16_t* dst = a.out + r * a.os;
+    const uint32_t step = across * shares;
+    for (uint32_t c = c0 + share * across; c < pieces; c += 4 * step) {
+      uint4 v[4];
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) v[j] = load16(src + static_cast<int64_t>(c + j * step) * 8, c + j * step < pieces);
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j)
+        if (c + j * step < pieces) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(c + j * step) * 8) = v[j];
+    }
   }
 }
 
@@ -144,9 +161,14 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
   group_tiles<kAdThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + C::TOK - 1) / C::TOK; }, first, scratch + 16);
   __syncthreads();
   const uint32_t tiles = first[a.groups], clusters = gridDim.x / a.ctas;
+  const uint32_t all_tiles = tiles + (other_rows(a, off) + C::TOK - 1) / C::TOK;
   const int steps = (a.k + 31) / 32, blocks = (a.n + 31) / 32;
 
-  for (uint32_t tile = blockIdx.x / a.ctas; tile < tiles; tile += clusters) {
+  for (uint32_t tile = blockIdx.x / a.ctas; tile < all_tiles; tile += clusters) {
+    if (tile >= tiles) {
+      copy_others(a, off, tile - tiles, C::TOK, rank, a.ctas, threadIdx.x, kAdThreads);
+      continue;
+    }
     const uint32_t g = group_of(first, a.groups, tile);
     const uint32_t at = off[g] + (tile - first[g]) * C::TOK;
     const uint32_t count = min(static_cast<uint32_t>(C::TOK), off[g + 1] - at);
@@ -360,7 +382,6 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
       __syncthreads();
   }
 
-  if (a.copy) copy_others(a, off, tiles * a.ctas, kAdThreads);
   if (a.ctas > 1) cluster_sync_all();
 }
 
@@ -724,10 +745,13 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       if (lane == 0) mbar_arrive(results_done);
     }
     cp_async_wait<0>();
+    // (the tiles of rows of no group go on where this CTA's turns leave off)
+    const uint32_t all_tiles = tiles + (other_rows(a, off) + kAtcRows - 1) / kAtcRows;
+    for (uint32_t i = blockIdx.x + it * gridDim.x; ok && i < all_tiles; i += gridDim.x)
+      copy_others(a, off, i - tiles, kAtcRows, 0, 1, threadIdx.x - kAtcEpiWarp0 * 32, kAtcEpiWarps * 32);
   }
 
   // ------------------------------------------------------------ end
-  if (a.copy && !*abort_flag) copy_others(a, off, tiles, kAtcThreads);
   __syncthreads();
   if (*abort_flag) {
     // Copies that were made may still be landing, on a barrier that will not
@@ -920,11 +944,11 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
         !encode_dense(&t.tm_a, A, bf16, d.K, d.rank, d.groups, t.rank16 * 16) ||
         !encode_dense(&t.tm_b, B, bf16, d.rank, d.N, d.groups, 128))
       return GEMM_ERR_CUDA;
-    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(rows / kAtcRows + busy, sms));
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(rows / kAtcRows + busy + 1, sms));
     e = bf16 ? launch_adapters_tc<true>(t, ctas, s) : launch_adapters_tc<false>(t, ctas, s);
   } else {
     const int nt = rows > 8 * busy ? 4 : 1;
-    const int64_t tiles = rows / (8 * nt) + busy;
+    const int64_t tiles = rows / (8 * nt) + busy + 1;  // (at most, those of rows of no group among them)
     // A cluster as large as leaves every SM two CTAs, or what there is to share.
     while (a.ctas < 8 && tiles * a.ctas <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
     const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * sms / a.ctas));

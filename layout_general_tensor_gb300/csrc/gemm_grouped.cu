@@ -28,10 +28,13 @@
 // of 64 on its way through the ring, each tile waited for it: 16 groups of 1000
 // rows, 2048 x 4096, 207 us against 157 for groups of 1024.)
 //
-// Roles (384 threads; pairs: in both CTAs):
-//   warp 0      copies of the M side        warp 10  copies of the N side
+// Roles (448 threads; pairs: in both CTAs):
+//   warp 0, 12  copies of the M side (a stage's first, third, ... and the others,
+//               where it takes several: a thread is held for each, and with one
+//               warp a side that was the pace of a block)
+//   warp 10, 13 the same of the N side
 //   warp 1      tensor memory; issues the products (the even CTA of a pair)
-//   warps 2..9  results      warp 11  clears the last block's rows (along K)
+//   warps 2..9  results      warp 11  clears the last step's rows (along K)
 #include <algorithm>
 #include <cstdint>
 #include <cstdlib>
@@ -47,11 +50,12 @@
 namespace lgt {
 namespace {
 
-constexpr int kGgThreads = 384;
+constexpr int kGgThreads = 448;
 constexpr int kGgEpiWarp0 = 2;
 constexpr int kGgEpiWarps = 8;
 constexpr int kGgQWarp = kGgEpiWarp0 + kGgEpiWarps;
 constexpr int kGgClearWarp = kGgQWarp + 1;
+constexpr int kGgOddP = kGgClearWarp + 1, kGgOddQ = kGgOddP + 1;
 constexpr int kGgMaxGroups = 1024;
 constexpr uint32_t kGgRows = 128;                       // M-side rows a CTA
 constexpr uint32_t kGgPBytes = kGgRows * TILE_K * 2;    // 16 KiB of them a stage
@@ -241,10 +245,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
 
   GroupedWork<PAIR> work(a, off, first);
   GroupedTile t;
-  if (warp == 0 || warp == kGgQWarp) {
+  if (warp == 0 || warp == kGgQWarp || warp >= kGgOddP) {
     // ------------------------------------------------------------ copies
-    if (elect_one()) {
-      const bool is_p = warp == 0;
+    const bool is_p = warp == 0 || warp == kGgOddP, odd = warp >= kGgOddP;
+    if ((!odd || (is_p ? a.p_boxes : a.q_boxes) > 1) && elect_one()) {
       const CUtensorMap* tm = is_p ? &a.tm_p : &a.tm_q;
       const CUtensorMap* tm_rest = is_p ? &a.tm_pr : &a.tm_qr;
       const uint32_t at = is_p ? 0u : kGgPBytes;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       const bool k_first = is_p ? !a.p_mn : !a.along_k, whole = is_p ? a.p_whole : a.q_whole;
       auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t apart, uint32_t bar, int32_t x0, int32_t k, int32_t z) {
         const int32_t stretch = whole ? x0 >> 6 : 0;
-        for (uint32_t j = 0; j < boxes; ++j) {
+        for (uint32_t j = odd; j < boxes; j += 2) {
           const int32_t x = whole ? 0 : x0 + static_cast<int32_t>(64 * j);
           if constexpr (PAIR)
             tma_load_4d_pair(dst + j * apart, map, bar, k_first ? k : x, k_first ? x : k, stretch, z);
@@ -273,14 +277,14 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         if (t.rest > 0) {
           const uint32_t b = rests & 1u;
           if (!(ok = wait(rest_empty(b), (rests >> 1 & 1u) ^ 1u))) break;
-          mbar_arrive_expect_tx(landed(b), chunks * kGgStep);
+          if (!odd) mbar_arrive_expect_tx(landed(b), chunks * kGgStep);
           copy(tm_rest, base + rest_off + b * rest_bytes + (is_p ? 0u : 2 * kGgStep), kGgStep,
                PAIR ? mapa_shared(landed(b), rank) : landed(b), x0, k0 + t.steps * 16, z);
           ++rests;
         }
         for (int kb = 0; kb < t.nkb; ++kb) {
           if (!(ok = wait(empty(s), phase ^ 1u))) break;
-          if (leader) mbar_arrive_expect_tx(full(s), bytes * CTAS);
+          if (leader && !odd) mbar_arrive_expect_tx(full(s), bytes * CTAS);
           if (!(a.withhold && !is_p && blockIdx.x == 0 && issued == 0))
             copy(tm, base + s * a.stage_bytes + at, kGgChunk, full_lead + 8u * s, x0, k0 + kb * TILE_K, z);
           ++issued;
