@@ -42,6 +42,9 @@ typedef struct gemm_adapters_plan gemm_adapters_plan_t;
 
 /* Validate `desc` and make a plan (host state and a 16-byte device status word
  * on the current device; without a device the plan's runs are refused).
+ * LGT_GEMM_ADAPTERS_FORM in the environment, for tests and measurements: the form
+ * that the plan's runs take where the sizes allow it, 0 the one for few rows, 1, 2,
+ * 4, 8 the one for many rows with so many CTAs a tile.
  * GEMM_ERR_INVALID_ARG, GEMM_ERR_CUDA. */
 gemm_status_t gemm_adapters_create(const gemm_adapters_desc_t* desc, gemm_adapters_plan_t** plan);
 
@@ -71,7 +74,7 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
 gemm_status_t gemm_adapters_sync_status(gemm_adapters_plan_t* plan, void* stream);
 
 /* Test aid for failure detection, without a fault: the plan's next run on the
- * tensor cores' large form (many rows) leaves out one CTA's first load of A, so
+ * form for many rows leaves out one CTA's first load of A, so
  * waits run out after the plan's limit (LGT_GEMM_WAIT_LIMIT_MS at
  * gemm_adapters_create, 2 s by default), the kernel winds down and the run's
  * status is GEMM_ERR_TIMEOUT; runs after it are normal. */

@@ -36,7 +36,7 @@ namespace {
 constexpr int kAdWarps = 8;
 constexpr int kAdThreads = kAdWarps * 32;
 constexpr int kAdMaxGroups = 1024;
-constexpr int64_t kAdManyRows = 32;  // rows a group and an SM from which the large form is taken
+constexpr uint32_t kAdMaxCluster = 8;
 
 struct AdapterArgs {
   const uint16_t *x, *a, *b, *base;
@@ -80,6 +80,13 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+// The power of two that takes a row's largest value to [0.5, 1), and its reverse.
+__device__ __forceinline__ float2 row_power(float most) {
+  const int e = static_cast<int>(__float_as_uint(most) >> 23);  // (biased; no sign)
+  const int p = e == 0 || e == 255 ? 0 : min(e - 126, 126);
+  return make_float2(__uint_as_float(static_cast<uint32_t>(127 - p) << 23), __uint_as_float(static_cast<uint32_t>(127 + p) << 23));
 }
 
 // Two values as the sum of two pairs of the type.
@@ -307,17 +314,14 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
       float most = fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w)));
 #pragma unroll
       for (int o = 1; o < PER; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      const int e = static_cast<int>(__float_as_uint(most) >> 23);  // (biased; no sign)
-      const int p = e == 0 || e == 255 ? 0 : min(e - 126, 126);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - p) << 23);
+      const float2 power = row_power(most);
       if (live) {
         uint32_t h0, h1, g0, g1;
-        split_pair<BF16>(s.x * down, s.y * down, h0, g0);
-        split_pair<BF16>(s.z * down, s.w * down, h1, g1);
+        split_pair<BF16>(s.x * power.x, s.y * power.x, h0, g0);
+        split_pair<BF16>(s.z * power.x, s.w * power.x, h1, g1);
         *reinterpret_cast<uint2*>(uh + t * C::UPITCH + c) = make_uint2(h0, h1);
         *reinterpret_cast<uint2*>(ul + t * C::UPITCH + c) = make_uint2(g0, g1);
-        if (c == 0)
-          factor[t] = __uint_as_float(static_cast<uint32_t>(127 + p) << 23) * (a.scales ? a.scales[g] : 1.0f);
+        if (c == 0) factor[t] = power.y * (a.scales ? a.scales[g] : 1.0f);
       }
     }
     __syncthreads();
@@ -387,13 +391,14 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
 
 // ------------------------------------------------------------ many rows
 //
-// The same pass on tcgen05: a tile is up to 128 rows of one group and a CTA does
-// it by itself, first
+// The same pass on tcgen05: a tile is up to 128 rows of one group, done by a
+// cluster of 1 to 8 CTAs (an SM moves some 60 bytes a ns, and where there are
+// fewer tiles than SMs that is the limit), each with a stretch of K, then one of N:
 //   u = x A^T:    rows on the instruction's M side (lanes of tensor memory), rank
 //                 on its N side; x and A come by a ring of copies, x's rows by
-//                 their numbers, four a copy, where there is an order;
-// then four warps take u from tensor memory, a row a lane, to its two parts of
-// 16 bits in shared memory, and
+//                 their numbers, four a copy, where there is an order.
+// The CTAs leave their parts of u in shared memory, and each adds all of them, in
+// order, and keeps the sum's two parts of 16 bits.  Then
 //   out^T = B u^T: columns of out on the M side, 128 at a time, rows on the N
 //                 side in steps of 16; sixteen warps add base, whose pieces are on
 //                 their way a block ahead, through shared memory, where a transposing
@@ -411,7 +416,7 @@ constexpr uint32_t kAtcTile = 128 * 128;               // 128 rows of 64 values
 constexpr uint32_t kAtcMaxStages = 8;
 constexpr uint32_t kAtcPieces = 2;                     // of base, a warp
 constexpr uint32_t kAtcStaging = kAtcEpiWarps * kAtcPieces * 2048;
-constexpr uint32_t kAtcBars = 2 * kAtcMaxStages + 14;  // (13, and what follows is loaded 16 bytes at a time)
+constexpr uint32_t kAtcBars = 2 * kAtcMaxStages + 16;  // (15, and what follows is loaded 16 bytes at a time)
 static_assert(kAtcBars * 8 % 16 == 0);
 constexpr uint32_t kAtcSmem = 227 * 1024;
 constexpr uint64_t kAtcSettleNs = 200ull * 1000ull * 1000ull;
@@ -422,12 +427,14 @@ struct AdapterTcArgs {
   DeviceStatus* status;
   uint64_t wait_limit_ns;
   uint32_t rank16, chunks;  // the rank in steps of 16; in stretches of 64
-  uint32_t stages, stage_bytes, region;  // region: of the ring, then of u and B
+  uint32_t stages, stage_bytes;
+  uint32_t region, parts;  // bytes of the ring, and then of u, B and this CTA's part of u, which begins at `parts`
   uint32_t idesc_u, idesc_out;  // the second without N
   int32_t withhold;
 };
 
-template <bool BF16>
+// SHARED: clusters of several CTAs.
+template <bool BF16, bool SHARED>
 __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __grid_constant__ AdapterTcArgs t) {
   pdl_launch_dependents();
   const AdapterArgs& a = t.p;
@@ -436,6 +443,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw_base);
   const uint32_t u_hi = base, u_lo = base + t.chunks * kAtcTile, b_ring = base + 2 * t.chunks * kAtcTile;
+  const uint32_t parts = base + t.parts;
   const uint32_t staging = base + t.region;
   const uint32_t bar0 = staging + kAtcStaging;
   uint8_t* rest = smem + t.region + kAtcStaging + kAtcBars * 8;
@@ -448,6 +456,8 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   uint32_t* first = off + a.groups + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = SHARED ? cluster_ctarank() : 0u;
+  const uint32_t ctas = SHARED ? a.ctas : 1u;
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty = [&](uint32_t s) { return bar0 + 8u * (kAtcMaxStages + s); };
   auto rows_full = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + b); };
@@ -455,9 +465,8 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   auto b_full = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + 6 + b); };
   auto out_full = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + 8 + b); };
   auto out_empty = [&](uint32_t b) { return bar0 + 8u * (2 * kAtcMaxStages + 10 + b); };
-  const uint32_t results_done = bar0 + 8u * (2 * kAtcMaxStages + 12);
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    const bool got = mbar_wait_bounded(bar, parity, t.wait_limit_ns, abort_flag);
+  const uint32_t results_done = bar0 + 8u * (2 * kAtcMaxStages + 12), parts_full = results_done + 8, parts_read = results_done + 16;
+  auto given_up = [&](bool got) {
     if (!got) {
       *abort_flag = 1;
       t.status->where = warp;
@@ -465,17 +474,28 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
     }
     return got;
   };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return given_up(mbar_wait_bounded(bar, parity, t.wait_limit_ns, abort_flag)); };
   auto warp_wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+  // (what the cluster's other CTAs complete)
+  auto wait_cluster = [&](uint32_t bar, uint32_t parity) {
+    return given_up(mbar_wait_bounded_cluster(bar, parity, t.wait_limit_ns, abort_flag));
+  };
+  auto arrive_all = [&](uint32_t bar) {  // in every CTA, once a warp
+    __syncwarp();
+    if (lane < static_cast<int>(ctas)) mbar_arrive_cluster(mapa_shared(bar, static_cast<uint32_t>(lane)));
+  };
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < t.stages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    mbar_init(u_done, 1);     // the first product is
-    mbar_init(u_full, 4);     // its parts are in shared memory
+    mbar_init(u_done, 1);     // this CTA's part of the first product is
+    mbar_init(u_full, SHARED ? kAtcEpiWarps : 4);  // u's 16-bit parts are in shared memory
     mbar_init(tile_done, 1);  // u and B have been read
     mbar_init(results_done, kAtcEpiWarps);
+    mbar_init(parts_full, kAtcEpiWarps * ctas);  // every CTA's part is in its shared memory
+    mbar_init(parts_read, kAtcEpiWarps * ctas);  // this CTA's part has been read
     mbar_init(end_bar, 1);
     for (uint32_t b = 0; b < 2; ++b) {
       mbar_init(rows_full(b), kAtcMmaWarp);
@@ -500,11 +520,14 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   group_tiles<kAtcThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + kAtcRows - 1) / kAtcRows; }, first, scratch + 32);
   tc_fence_before();
   __syncthreads();
+  if constexpr (SHARED) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tiles = first[a.groups];
-  const int nkb = (a.k + TILE_K - 1) / TILE_K;
-  const int nnb = (a.n + 127) / 128;
+  const uint32_t tiles = first[a.groups], turn0 = blockIdx.x / ctas, turns = gridDim.x / ctas;
+  // This CTA's blocks of K and of N.
+  const int nkb = (a.k + TILE_K - 1) / TILE_K, nnb = (a.n + 127) / 128;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / ctas), kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / ctas);
+  const int nb0 = static_cast<int>(static_cast<int64_t>(nnb) * rank / ctas), nb1 = static_cast<int>(static_cast<int64_t>(nnb) * (rank + 1) / ctas);
   // A tile: its group, first place and rows.
   struct Tile {
     uint32_t g, at, count;
@@ -524,12 +547,14 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
     // ------------------------------------------------------------ copies
     uint32_t s = 0, phase = 0, it = 0, issued = 0, b_uses = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++it) {
+    for (uint32_t i = turn0; ok && i < tiles; i += turns, ++it) {
       const Tile w = tile_at(i);
       int32_t* rows = row_of + (it & 1) * kAtcRows;
-      // u and B of the tile before lie where the ring is.  (And the results of the
-      // one before that, whose rows stood here, were done before its u was made.)
-      if (it > 0 && !(ok = warp_wait(tile_done, (it - 1) & 1u))) break;
+      // u, B and the parts of the tile before lie where the ring is.  (And the
+      // results of the one before that, whose rows stood here, were done before its
+      // u was made.)
+      if (it > 0 && !(ok = warp_wait(tile_done, (it - 1) & 1u) && (!SHARED || __all_sync(0xffffffffu, wait_cluster(parts_read, (it - 1) & 1u))))) break;
+      fence_proxy_async_smem();
       int32_t r = -1;
       const uint32_t place = warp * 32 + lane;
       if (place < w.count) {
@@ -542,7 +567,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       if (lane == 0) mbar_arrive(rows_full(it & 1));
       if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
       if (elect_one()) {
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait(empty(s), phase ^ 1u))) break;
           const uint32_t dst = base + s * t.stage_bytes;
           if (warp == 0) {
@@ -570,8 +595,11 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
             phase ^= 1u;
           }
         }
-        if (warp == 1 && ok && (ok = wait(u_done, it & 1u))) {
-          for (int b = 0; b < nnb; ++b, ++b_uses) {
+        // B's blocks, from when the ring is done with and, where the parts lie in
+        // their place, those have been read
+        if (warp == 1 && ok && (ok = wait(u_done, it & 1u) && (!SHARED || t.parts > 2 * t.chunks * kAtcTile || wait_cluster(parts_read, it & 1u)))) {
+          fence_proxy_async_smem();
+          for (int b = nb0; b < nb1; ++b, ++b_uses) {
             // (what the products of the block before the last have read is free once they are done)
             if (b_uses >= 2 && !(ok = wait(out_full(b_uses & 1u), (b_uses >> 1 & 1u) ^ 1u))) break;
             mbar_arrive_expect_tx(b_full(b_uses & 1u), t.chunks * kAtcTile);
@@ -591,15 +619,16 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       const uint64_t b_desc = sw128_desc(b_ring, 16u, 1024u);
       uint32_t s = 0, phase = 0, it = 0, uses = 0;
       bool ok = true;
-      for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++it) {
+      for (uint32_t i = turn0; ok && i < tiles; i += turns, ++it) {
         const Tile w = tile_at(i);
-        // (the results' warps have read the u of the tile before: its parts were full)
-        for (int kb = 0; kb < nkb; ++kb) {
+        // (u of the tile before has been read: its parts were full)
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait(full(s), phase))) break;
           tc_fence_after();
           const uint64_t xd = x_desc + s * (t.stage_bytes >> 4), ad = a_desc + s * (t.stage_bytes >> 4);
 #pragma unroll
-          for (int k = 0; k < TILE_K / 16; ++k) tc_mma_f16_ss(u_tmem, xd + 2 * k, ad + 2 * k, t.idesc_u, (kb | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < TILE_K / 16; ++k)
+            tc_mma_f16_ss(u_tmem, xd + 2 * k, ad + 2 * k, t.idesc_u, kb > kb0 || k > 0 ? 1u : 0u);
           tc_commit(empty(s));
           if (++s == t.stages) {
             s = 0;
@@ -610,7 +639,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
         tc_commit(u_done);
         if (!(ok = wait(u_full, it & 1u))) break;
         const uint32_t idesc = t.idesc_out | ((w.count + 15) & ~15u) >> 3 << 17;
-        for (int b = 0; b < nnb; ++b, ++uses) {
+        for (int b = nb0; b < nb1; ++b, ++uses) {
           const uint32_t buf = uses & 1u;
           if (!(ok = wait(b_full(buf), uses >> 1 & 1u) && wait(out_empty(buf), (uses >> 1 & 1u) ^ 1u))) break;
           tc_fence_after();
@@ -631,38 +660,117 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   } else {
     // ------------------------------------------------------------ results
     const uint32_t quad = static_cast<uint32_t>(warp & 3), share = static_cast<uint32_t>(warp - kAtcEpiWarp0) / 4;
-    const uint32_t tok0 = share * 32;  // this warp's rows of the tile: 32
     const uint32_t mine = staging + static_cast<uint32_t>(warp - kAtcEpiWarp0) * kAtcPieces * 2048u;
     const uint32_t row8 = static_cast<uint32_t>(lane >> 2), piece = static_cast<uint32_t>(lane & 3);
     // places in a piece of 32 rows of 64 bytes, as in the grouped products' results
     const uint32_t put = (lane & 7u) * 64u + ((static_cast<uint32_t>(lane >> 3) ^ (lane >> 1 & 3u)) << 4);
     const uint32_t get = row8 * 64u + ((piece ^ (row8 >> 1 & 3u)) << 4);
+    // A part of u: rows of 16 rank16 values, whose 16-byte pieces are exchanged by
+    // the row's number within eight, or four where they are no multiple of eight.  A
+    // warp writes a quarter of its 32 rows, a thread adds one
+    // of a row.
+    const uint32_t turn = t.rank16 % 2 == 0 ? 7u : 3u, pitch = t.rank16 * 64u;
+    const uint32_t put_row = quad * 32u + lane, add_row = static_cast<uint32_t>(threadIdx.x - kAtcEpiWarp0 * 32) >> 2;
     uint32_t it = 0, uses = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++it) {
+    for (uint32_t i = turn0; ok && i < tiles; i += turns, ++it) {
       const Tile w = tile_at(i);
       if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
       const int32_t* rows = row_of + (it & 1) * kAtcRows;
+      // The four warps of a quarter of the lanes share the rows, 32 each, or, where
+      // there are fewer, the blocks of columns.
+      const uint32_t by_rows = w.count > 64 ? 4u : w.count > 32 ? 2u : 1u, every = 4u / by_rows;
+      const uint32_t tok0 = share % by_rows * 32u;
+      const int skip = static_cast<int>(share / by_rows);
       // Pieces of base: 32 rows of 32 columns, of each block of 128.
       const int n0 = static_cast<int>(quad * 32 + piece * 8);
       int32_t r[4];
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) r[j] = rows[tok0 + 8 * j + row8];
-      auto fetch = [&](int b) {
-        const int n = b * 128 + n0;
-        if (b < nnb && n < a.n) {
-          const uint32_t dst = mine + (b % kAtcPieces) * 2048u + get;
+      uint32_t fetched = 0, used = 0;
+      int ahead = nb0 + skip;
+      auto fetch = [&]() {
+        const int n = ahead * 128 + n0;
+        if (ahead < nb1 && n < a.n) {
+          const uint32_t dst = mine + (fetched % kAtcPieces) * 2048u + get;
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
             if (r[j] >= 0) cp_async_16(dst + j * 512u, a.base + r[j] * a.bs + n);
         }
         cp_async_commit();
+        ++fetched;
+        ahead += static_cast<int>(every);
       };
-      for (int b = 0; b < static_cast<int>(kAtcPieces) - 1; ++b) fetch(b);
-      if (share == 0) {
-        // u, a row a lane: the power of two that takes its largest value to [0.5, 1), then its parts.
-        // (The rows' factors of the tile before are in use until its results are done.)
+      for (uint32_t b = 0; b + 1 < kAtcPieces; ++b) fetch();
+      // (The rows' factors of the tile before are in use until its results are done.)
+      if (SHARED || share == 0)
         if (!(ok = warp_wait(u_done, it & 1u) && (it == 0 || warp_wait(results_done, (it - 1) & 1u)))) break;
+      if constexpr (SHARED) {
+        // This CTA's part.
+        tc_fence_after();
+        {
+          uint32_t v[32];
+          const uint32_t c0 = share * t.rank16;  // in pieces of 4
+  #pragma unroll
+          for (uint32_t k = 0; k < 8; ++k)
+            if (k < t.rank16) tc_ld_32x32b_x4(u_tmem + (quad * 32u << 16) + 4 * (c0 + k), v + 4 * k);
+          tc_wait_ld_regs(v);
+  #pragma unroll
+          for (uint32_t k = 0; k < 8; ++k)
+            if (k < t.rank16)
+              st_shared_v4(parts + put_row * pitch + (((c0 + k) ^ (put_row & turn)) << 4), v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+        tc_fence_before();
+        arrive_all(parts_full);
+        if (!(ok = __all_sync(0xffffffffu, wait_cluster(parts_full, it & 1u)))) break;
+        // The sum of all parts; its row's power of two, which takes the largest value to [0.5, 1); its two parts of 16 bits.
+        {
+          float4 v[8];
+  #pragma unroll
+          for (uint32_t k = 0; k < 8; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          // (every fourth piece of a row, so that four lanes read 64 bytes together)
+          for (uint32_t from = 0; from < ctas; ++from) {
+            const uint32_t local = parts + add_row * pitch, at = mapa_shared(local, from);
+  #pragma unroll
+            for (uint32_t k = 0; k < 8; ++k)
+              if (k < t.rank16) {
+                const uint32_t o = ((piece + 4 * k) ^ (add_row & turn)) << 4;
+                const float4 x = from == rank ? ld_shared_f32x4(local + o) : ld_cluster_f32x4(at + o);
+                v[k].x += x.x, v[k].y += x.y, v[k].z += x.z, v[k].w += x.w;
+              }
+          }
+          float most = 0.0f;
+  #pragma unroll
+          for (uint32_t k = 0; k < 8; ++k) {
+            // (past the rank are sums of what x holds times 0, which is not 0 for an infinity)
+            if (k >= t.rank16 || static_cast<int>(4 * (piece + 4 * k)) >= a.rank) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            most = fmaxf(most, fmaxf(fmaxf(fabsf(v[k].x), fabsf(v[k].y)), fmaxf(fabsf(v[k].z), fabsf(v[k].w))));
+          }
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          const float2 power = row_power(most);
+  #pragma unroll
+          for (uint32_t k = 0; k < 8; ++k)
+            if (k < t.rank16) {
+              uint32_t h0, h1, l0, l1;
+              split_pair<BF16>(v[k].x * power.x, v[k].y * power.x, h0, l0);
+              split_pair<BF16>(v[k].z * power.x, v[k].w * power.x, h1, l1);
+              const uint32_t c = 4 * (piece + 4 * k);
+              const uint32_t to = (c >> 6) * kAtcTile + add_row * 128 + (((c & 63u) >> 3) ^ (add_row & 7u)) * 16 + (c & 4u) * 2;
+              st_shared_v2(u_hi + to, h0, h1);
+              st_shared_v2(u_lo + to, l0, l1);
+            }
+          if (piece == 0)
+            factor[add_row] = power.y * (a.scales ? a.scales[w.g] : 1.0f);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_full);
+        // (behind the stores, which have taken what was read: an arrival alone does not
+        // wait for loads)
+        arrive_all(parts_read);
+      } else if (share == 0) {
+        // u, a row a lane: the power of two that takes its largest value to [0.5, 1), then its two parts of 16 bits.
         tc_fence_after();
         const uint32_t row = quad * 32 + lane, from = u_tmem + (quad * 32u << 16);
         float most = 0.0f;
@@ -674,9 +782,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
           for (int e = 0; e < 16; ++e)
             if (static_cast<int>(c) + e < a.rank) most = fmaxf(most, fabsf(__uint_as_float(v[e])));
         }
-        const int e = static_cast<int>(__float_as_uint(most) >> 23);
-        const int p = e == 0 || e == 255 ? 0 : min(e - 126, 126);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - p) << 23);
+        const float2 power = row_power(most);
         for (uint32_t c = 0; c < t.rank16 * 16; c += 16) {
           uint32_t v[16];
           tc_ld_32x32b_x16(from + c, v);
@@ -686,7 +792,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
           for (int j = 0; j < 8; ++j) {
             // (past the rank are sums of what x holds times 0, which is not 0 for an infinity)
             const bool in = static_cast<int>(c) + 2 * j < a.rank;
-            split_pair<BF16>(in ? __uint_as_float(v[2 * j]) * down : 0.0f, in ? __uint_as_float(v[2 * j + 1]) * down : 0.0f, hi[j], lo[j]);
+            split_pair<BF16>(in ? __uint_as_float(v[2 * j]) * power.x : 0.0f, in ? __uint_as_float(v[2 * j + 1]) * power.x : 0.0f, hi[j], lo[j]);
           }
           const uint32_t at = (c >> 6) * kAtcTile + row * 128;
 #pragma unroll
@@ -696,7 +802,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
             st_shared_v4(u_lo + to, lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
           }
         }
-        factor[row] = __uint_as_float(static_cast<uint32_t>(127 + p) << 23) * (a.scales ? a.scales[w.g] : 1.0f);
+        factor[row] = power.y * (a.scales ? a.scales[w.g] : 1.0f);
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
@@ -706,36 +812,39 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       float2 f[4];  // of rows 8 e + 2 piece and the next
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float2*>(factor + tok0 + 8 * e + 2 * piece);
-      for (int b = 0; ok && b < nnb; ++b, ++uses) {
+      for (int b = nb0; ok && b < nb1; ++b, ++uses) {
         const uint32_t buf = uses & 1u;
-        fetch(b + kAtcPieces - 1);
+        const bool turn_here = static_cast<uint32_t>(b - nb0) % every == static_cast<uint32_t>(skip);
+        if (turn_here) fetch();
         if (!(ok = warp_wait(out_full(buf), uses >> 1 & 1u))) break;
         tc_fence_after();
-        if (tok0 < w.count) {
-          const uint32_t here = mine + (b % kAtcPieces) * 2048u;
+        if (turn_here) {
+          const uint32_t here = mine + (used++ % kAtcPieces) * 2048u;
           const int n = b * 128 + n0;
-          uint32_t x[16], y[16];
-          tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + (quad * 32u << 16), x);
-          tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + ((quad * 32u + 16u) << 16), y);
-          cp_async_wait<kAtcPieces - 1>();
-          __syncwarp();
-          tc_wait_ld_regs(x);
-          tc_regs_after_wait(y);
+          if (tok0 < w.count) {
+            uint32_t x[16], y[16];
+            tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + (quad * 32u << 16), x);
+            tc_ld_16x256b_x4(out_tmem + buf * 128 + tok0 + ((quad * 32u + 16u) << 16), y);
+            cp_async_wait<kAtcPieces - 1>();
+            __syncwarp();
+            tc_wait_ld_regs(x);
+            tc_regs_after_wait(y);
 #pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            const uint4 old = ldmatrix_x4_trans(here + put + e * 512u);
-            auto sum = [&](uint32_t lo, uint32_t hi, uint32_t o) {
-              const float2 was = unpack_pair16<BF16>(o);
-              return pack_pair16<BF16>(fmaf(__uint_as_float(lo), f[e].x, was.x), fmaf(__uint_as_float(hi), f[e].y, was.y));
-            };
-            stmatrix_x4_trans(here + put + e * 512u, sum(x[4 * e], x[4 * e + 1], old.x), sum(x[4 * e + 2], x[4 * e + 3], old.y),
-                              sum(y[4 * e], y[4 * e + 1], old.z), sum(y[4 * e + 2], y[4 * e + 3], old.w));
-          }
-          __syncwarp();
+            for (uint32_t e = 0; e < 4; ++e) {
+              const uint4 old = ldmatrix_x4_trans(here + put + e * 512u);
+              auto sum = [&](uint32_t lo, uint32_t hi, uint32_t o) {
+                const float2 was = unpack_pair16<BF16>(o);
+                return pack_pair16<BF16>(fmaf(__uint_as_float(lo), f[e].x, was.x), fmaf(__uint_as_float(hi), f[e].y, was.y));
+              };
+              stmatrix_x4_trans(here + put + e * 512u, sum(x[4 * e], x[4 * e + 1], old.x), sum(x[4 * e + 2], x[4 * e + 3], old.y),
+                                sum(y[4 * e], y[4 * e + 1], old.z), sum(y[4 * e + 2], y[4 * e + 3], old.w));
+            }
+            __syncwarp();
 #pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            const uint4 v = ld_shared_v4(here + get + e * 512u);
-            if (r[e] >= 0 && n < a.n) st_global_v4(a.out + r[e] * a.os + n, v.x, v.y, v.z, v.w);
+            for (uint32_t e = 0; e < 4; ++e) {
+              const uint4 v = ld_shared_v4(here + get + e * 512u);
+              if (r[e] >= 0 && n < a.n) st_global_v4(a.out + r[e] * a.os + n, v.x, v.y, v.z, v.w);
+            }
           }
         }
         tc_fence_before();
@@ -745,10 +854,10 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       if (lane == 0) mbar_arrive(results_done);
     }
     cp_async_wait<0>();
-    // (the tiles of rows of no group go on where this CTA's turns leave off)
+    // (the tiles of rows of no group go on where this cluster's turns leave off)
     const uint32_t all_tiles = tiles + (other_rows(a, off) + kAtcRows - 1) / kAtcRows;
-    for (uint32_t i = blockIdx.x + it * gridDim.x; ok && i < all_tiles; i += gridDim.x)
-      copy_others(a, off, i - tiles, kAtcRows, 0, 1, threadIdx.x - kAtcEpiWarp0 * 32, kAtcEpiWarps * 32);
+    for (uint32_t i = turn0 + it * turns; ok && i < all_tiles; i += turns)
+      copy_others(a, off, i - tiles, kAtcRows, rank, ctas, threadIdx.x - kAtcEpiWarp0 * 32, kAtcEpiWarps * 32);
   }
 
   // ------------------------------------------------------------ end
@@ -766,6 +875,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (SHARED) cluster_sync_all();  // (nobody's parts or barriers are in use any more)
   tc_fence_after();
   if (warp == kAtcMmaWarp) tmem_dealloc(tmem, 512);
 }
@@ -819,10 +929,32 @@ bool encode_x(CUtensorMap* map, const void* ptr, bool bf16, int64_t k, int64_t r
 }
 
 template <bool BF16>
-cudaError_t launch_adapters_tc(const AdapterTcArgs& t, unsigned ctas, cudaStream_t stream) {
-  const cudaError_t e = set_smem_once<adapters_tc_kernel<BF16>>(static_cast<int>(kAtcSmem));
+cudaError_t launch_adapters_tc(const AdapterTcArgs& t, unsigned clusters, cudaStream_t stream) {
+  if (t.p.ctas == 1) {
+    const cudaError_t e = set_smem_once<adapters_tc_kernel<BF16, false>>(static_cast<int>(kAtcSmem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(adapters_tc_kernel<BF16, false>, dim3(clusters), dim3(kAtcThreads), kAtcSmem, stream, t);
+  }
+  const cudaError_t e = set_smem_once<adapters_tc_kernel<BF16, true>>(static_cast<int>(kAtcSmem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(adapters_tc_kernel<BF16>, dim3(ctas), dim3(kAtcThreads), kAtcSmem, stream, t);
+  return launch_pdl_cluster(adapters_tc_kernel<BF16, true>, dim3(clusters * t.p.ctas), dim3(kAtcThreads), kAtcSmem, stream, t.p.ctas, t);
+}
+
+// Clusters of `ctas` that run at once; < 0: an error.
+template <bool BF16>
+int resident_adapter_clusters(unsigned ctas) {
+  if (set_smem_once<adapters_tc_kernel<BF16, true>>(static_cast<int>(kAtcSmem)) != cudaSuccess) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kAtcThreads);
+  cfg.dynamicSmemBytes = kAtcSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {ctas, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, adapters_tc_kernel<BF16, true>, &cfg) == cudaSuccess ? n : -1;
 }
 
 uint64_t adapters_wait_limit() {
@@ -841,6 +973,8 @@ struct gemm_adapters_plan {
   gemm_adapters_desc_t d;
   int device = -1;
   int sms = 0;
+  int resident[4] = {0, 0, 0, 0};  // clusters of 1, 2, 4, 8 CTAs of the form for many rows that run at once
+  int form = -1;  // LGT_GEMM_ADAPTERS_FORM: 0 the first form, 1, 2, 4, 8 the one for many rows with that many CTAs a tile
   lgt::DeviceStatus* d_status = nullptr;
   uint64_t wait_limit_ns = 0;
   int withhold_armed = 0;  // gemm_adapters_withhold_load: the next run of the large form withholds a load (one shot)
@@ -861,6 +995,7 @@ gemm_status_t gemm_adapters_create(const gemm_adapters_desc_t* desc, gemm_adapte
   if (!p) return GEMM_ERR_CUDA;
   p->d = d;
   p->wait_limit_ns = lgt::adapters_wait_limit();
+  if (const char* form = std::getenv("LGT_GEMM_ADAPTERS_FORM"); form && *form) p->form = std::atoi(form);
   if (cudaGetDevice(&p->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
     cudaGetLastError();
@@ -870,6 +1005,16 @@ gemm_status_t gemm_adapters_create(const gemm_adapters_desc_t* desc, gemm_adapte
     if (p->d_status) cudaFree(p->d_status);
     delete p;
     return GEMM_ERR_CUDA;
+  }
+  p->resident[0] = p->sms;
+  for (unsigned i = 1; p->device >= 0 && i < 4; ++i) {
+    p->resident[i] = d.dtype == GEMM_BF16 ? lgt::resident_adapter_clusters<true>(1u << i) : lgt::resident_adapter_clusters<false>(1u << i);
+    if (p->resident[i] < 0) {
+      cudaGetLastError();
+      cudaFree(p->d_status);
+      delete p;
+      return GEMM_ERR_CUDA;
+    }
   }
   *plan = p;
   return GEMM_OK;
@@ -924,19 +1069,51 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
   const int64_t busy = std::min<int64_t>(d.groups, rows);
   const bool bf16 = d.dtype == GEMM_BF16;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // The two forms' times, in us, from their rounds of tiles (measured at K = N =
+  // 4096; the sizes of the groups are not known here, and half a tile of each is
+  // counted as empty).
+  // The first: a CTA's share of a tile of 32 rows takes 34 us at two CTAs an SM and
+  // ranks up to 16, 1.2, 2.4 and 4.3 times that up to 32, 64, 128.
+  const int nt = rows > 8 * busy ? 4 : 1;
+  const int64_t tiles = rows / (8 * nt) + busy + 1;  // (at most, those of rows of no group among them)
+  // A cluster as large as leaves every SM two CTAs, or what there is to share.
+  while (a.ctas < kAdMaxCluster && tiles * a.ctas <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
+  const double row_bytes = 2.0 * static_cast<double>(d.K + 2 * d.N), scale = row_bytes / (2.0 * 3 * 4096);
+  const double by_rank = d.rank <= 16 ? 1.0 : d.rank <= 32 ? 1.2 : d.rank <= 64 ? 2.4 : 4.3;
+  const double small_us = 8.0 + static_cast<double>((tiles * a.ctas + 2 * sms - 1) / (2 * sms)) * 34.0 * scale * by_rank / a.ctas;
+  // The form for many rows: an SM moves 60 bytes a ns (45 where it gathers), all of
+  // them together 6.1 TB/s, and the exchange of parts takes 3 us and 0.1 us x CTAs^2
+  // for every 16 of the rank.
+  const int64_t rank16 = (d.rank + 15) / 16, large_tiles = (2 * rows / kAtcRows + busy + 1) / 2 + 1;
+  const double all_us = static_cast<double>(rows) * row_bytes / 6.1e6;
+  int lg = -1;
+  double best_us = small_us;
+  for (int i = 0; i < 4 && (nt > 1 || plan->form > 0); ++i) {
+    const int64_t at_once = plan->resident[i];
+    if (at_once < 1 || d.K < static_cast<int64_t>(TILE_K) << i || d.N < int64_t{128} << i) break;
+    const double tile_us = kAtcRows * row_bytes / (order ? 45e3 : 60e3) / (1 << i) + (i > 0 ? 0.1 * static_cast<double>(rank16 << (2 * i)) : 0.0);
+    const double us = (i > 0 ? 12.0 : 9.0) + std::max(all_us, static_cast<double>((large_tiles + at_once - 1) / at_once) * tile_us);
+    if (plan->form < 0 ? us < best_us : plan->form == 1 << i) {
+      best_us = us;
+      lg = i;
+    }
+  }
+  if (lg >= 0) a.ctas = 1;
   cudaError_t e;
-  if (rows >= busy * kAdManyRows && rows >= static_cast<int64_t>(sms) * kAdManyRows) {
+  if (lg >= 0) {
     AdapterTcArgs t;
     t.p = a;
     t.status = plan->d_status;
     // (a wait may be for all of a tile's blocks)
     t.wait_limit_ns = plan->wait_limit_ns + static_cast<uint64_t>(d.K / TILE_K + d.N / 128) * 4000;
-    t.rank16 = static_cast<uint32_t>(d.rank + 15) / 16;
+    t.rank16 = static_cast<uint32_t>(rank16);
     t.chunks = (t.rank16 + 3) / 4;
     t.stage_bytes = kAtcTile + t.rank16 * 16 * 128;
     const uint32_t tables = kAtcBars * 8 + 1544 + 256 + 8 * static_cast<uint32_t>(d.groups + 1);
     t.stages = std::min<uint32_t>(kAtcMaxStages, (kAtcSmem - 1024 - kAtcStaging - tables) / t.stage_bytes);
-    t.region = std::max(t.stages * t.stage_bytes, 4 * t.chunks * kAtcTile);
+    // (a rank of one stretch leaves room for the parts behind u and B, one of two has them in B's place)
+    t.parts = t.chunks == 1 ? 4 * kAtcTile : 2 * t.chunks * kAtcTile;
+    t.region = std::max(t.stages * t.stage_bytes, t.chunks == 1 ? t.parts + kAtcRows * t.rank16 * 64 : 4 * t.chunks * kAtcTile);
     t.idesc_u = idesc_f16(bf16, 0u, 0u, kAtcRows, t.rank16 * 16);
     t.idesc_out = idesc_f16(bf16, 0u, 0u, kAtcRows, 0u);
     t.withhold = plan->withhold_armed ? __atomic_exchange_n(&plan->withhold_armed, 0, __ATOMIC_ACQ_REL) : 0;
@@ -944,13 +1121,10 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
         !encode_dense(&t.tm_a, A, bf16, d.K, d.rank, d.groups, t.rank16 * 16) ||
         !encode_dense(&t.tm_b, B, bf16, d.rank, d.N, d.groups, 128))
       return GEMM_ERR_CUDA;
-    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(rows / kAtcRows + busy + 1, sms));
-    e = bf16 ? launch_adapters_tc<true>(t, ctas, s) : launch_adapters_tc<false>(t, ctas, s);
+    t.p.ctas = 1u << lg;
+    const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(rows / kAtcRows + busy + 1, plan->resident[lg]));
+    e = bf16 ? launch_adapters_tc<true>(t, clusters, s) : launch_adapters_tc<false>(t, clusters, s);
   } else {
-    const int nt = rows > 8 * busy ? 4 : 1;
-    const int64_t tiles = rows / (8 * nt) + busy + 1;  // (at most, those of rows of no group among them)
-    // A cluster as large as leaves every SM two CTAs, or what there is to share.
-    while (a.ctas < 8 && tiles * a.ctas <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
     const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * sms / a.ctas));
     e = bf16 ? launch_adapters<true>(a, nt, clusters, s) : launch_adapters<false>(a, nt, clusters, s);
   }

@@ -241,17 +241,33 @@ def test_adapters_normal(m, dtype, rank):
     _check_adapters(m, [100, 60, 0], 9, 520, 1032, rank, dtype, ints=False, order=False, seed=rank + 1)
 
 
-@pytest.mark.parametrize("sizes,none", [([5000], 0), ([2600, 0, 2500], 60), ([200] * 40, 0), ([1, 6000, 17, 129, 128], 1)])
-@pytest.mark.parametrize("n,k,rank", [(8, 8, 8), (136, 72, 16), (1000, 328, 24), (520, 512, 64), (264, 200, 72), (392, 1024, 128)])
-def test_adapters_many_rows(m, sizes, none, n, k, rank):
+# (every form of the operator, whatever the sizes would choose)
+@pytest.mark.parametrize("form", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("sizes,none", [([5000], 0), ([2600, 0, 2500], 60), ([200] * 40, 0), ([1, 6000, 17, 129, 128], 1), ([300, 33], 0),
+                                        ([1000, 1, 700, 64], 500), ([0, 3], 2)], ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("n,k,rank", [(8, 8, 8), (136, 72, 16), (1000, 328, 24), (520, 512, 64), (264, 200, 72), (392, 1024, 128), (1096, 1032, 48)])
+def test_adapters_forms(m, form, sizes, none, n, k, rank, monkeypatch):
+    if form and (k < 64 * form or n < 128 * form):
+        pytest.skip("fewer blocks than CTAs: another form is taken")
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
     i = len(sizes) + rank // 8
     _check_adapters(m, sizes, none, n, k, rank, "bf16" if i % 2 else "f16", order=i % 3 > 0, scaled=i % 5 > 0, in_place=i % 4 == 0, seed=i)
     _check_adapters(m, sizes, none, n, k, rank, "f16" if i % 2 else "bf16", order=i % 3 == 0, in_place=i % 4 == 1, extra=(8, 16, 16 if i % 4 == 1 else 24), start=11, seed=i + 1)
 
 
+@pytest.mark.parametrize("sizes,none", [([5000], 0), ([200] * 40, 0), ([1, 16000, 17, 129, 128], 1), ([1000, 1, 700, 64], 500)],
+                         ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("n,k,rank", [(4104, 2056, 64), (2048, 4096, 48), (3000, 2880, 128)])
+def test_adapters_many_rows(m, sizes, none, n, k, rank):
+    i = len(sizes) + rank // 8
+    _check_adapters(m, sizes, none, n, k, rank, "bf16" if i % 2 else "f16", order=i % 3 > 0, seed=i)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("rank", [8, 64, 88])
-def test_adapters_many_rows_normal(m, dtype, rank):
+@pytest.mark.parametrize("form", [0, 1, 4])
+def test_adapters_forms_normal(m, dtype, rank, form, monkeypatch):
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
     _check_adapters(m, [4000, 1500], 9, 520, 1032, rank, dtype, ints=False, order=rank == 64, seed=rank)
 
 

@@ -171,7 +171,7 @@ def test_gradients(m, k_contig, sizes):
 
 def _operators(m, big):
     """Each operator on whole numbers: (its call, its output, what the output has to be for the present ids)."""
-    t, groups, n, k, rank = torch.float16, 6, 136, 200, 16
+    t, groups, n, k, rank = torch.float16, 6, 264, 200, 16
     rows = 6000 if big else 50
     ids = torch.zeros(rows, dtype=torch.int32, device="cuda")
     offsets, order, places = torch.zeros(groups + 1, dtype=torch.int32, device="cuda"), torch.zeros_like(ids), torch.zeros_like(ids)
@@ -212,8 +212,9 @@ def _operators(m, big):
     return run, check, draw, (c, d, out, order)
 
 
-@pytest.mark.parametrize("big", [False, True])
-def test_graph_replays_take_the_sizes_of_the_time(m, big):
+@pytest.mark.parametrize("big,form", [(False, ""), (True, ""), (True, "1"), (True, "2")])
+def test_graph_replays_take_the_sizes_of_the_time(m, big, form, monkeypatch):
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", form)
     run, check, draw, _ = _operators(m, big)
     draw(0)
     side = torch.cuda.Stream()
@@ -233,9 +234,10 @@ def test_graph_replays_take_the_sizes_of_the_time(m, big):
         check()
 
 
-@pytest.mark.parametrize("big", [False, True])
-def test_streams(m, big):
+@pytest.mark.parametrize("big,form", [(False, ""), (True, ""), (True, "1"), (True, "2")])
+def test_streams(m, big, form, monkeypatch):
     """On a stream of the call's own, and two sets of operators at once on two streams."""
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", form)
     first, second = _operators(m, big), _operators(m, big)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     for seed in range(3):
@@ -274,10 +276,11 @@ def test_one_object_on_two_streams(m, big):
             assert torch.equal(d[g], (a[lo:hi].double().T @ e[lo:hi].double()).to(t))
 
 
-@pytest.mark.parametrize("big", [False, True])
-def test_repeated_calls_give_the_same_bits(m, big):
+@pytest.mark.parametrize("big,form", [(False, 0), (True, 0), (True, 1), (True, 2), (True, 4)])
+def test_repeated_calls_give_the_same_bits(m, big, form, monkeypatch):
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
     sizes = [2100, 0, 3111, 17] if big else [4, 0, 31, 1]
-    rows, n, k, rank = sum(sizes), 264, 1000, 24
+    rows, n, k, rank = sum(sizes), 520, 1000, 24
     g = torch.Generator(device="cuda").manual_seed(0)
 
     def normal(*s):
@@ -319,9 +322,11 @@ def test_offsets_that_are_not_what_they_should_be(m, offsets, means):
 
 @pytest.mark.parametrize("rows", [40, 6000])
 @pytest.mark.parametrize("in_place", [False, True])
-def test_order_with_numbers_of_no_row(m, rows, in_place):
+@pytest.mark.parametrize("form", [0, 1, 2])
+def test_order_with_numbers_of_no_row(m, rows, in_place, form, monkeypatch):
     """They are left out: their places' rows stay as they were."""
-    t, n, k, rank = torch.float16, 136, 72, 8
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
+    t, n, k, rank = torch.float16, 264, 136, 8
     order = torch.randperm(rows, device="cuda").int()
     gone = order[::7].clone()
     order[::7] = torch.tensor([-1, rows, 2**31 - 1, -2**31], dtype=torch.int32, device="cuda").repeat(rows)[:len(gone)]
@@ -346,9 +351,11 @@ def test_order_with_numbers_of_no_row(m, rows, in_place):
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("sizes", [[7, 3, 9, 0, 20], [200, 33, 150, 0, 300], [2000, 1100, 2500, 0, 600]], ids=["few", "some", "many"])
-def test_a_group_reaches_no_other(m, value, sizes):
+@pytest.mark.parametrize("form", [0, 1, 2])
+def test_a_group_reaches_no_other(m, value, sizes, form, monkeypatch):
     """Group 1's rows, weights and adapter hold what is not finite; every other result is exact."""
-    t, n, k, rank, rows, groups = torch.float16, 136, 200, 24, sum(sizes), len(sizes)
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
+    t, n, k, rank, rows, groups = torch.float16, 264, 200, 24, sum(sizes), len(sizes)
     offsets, at = _offsets(sizes), np.concatenate([[0], np.cumsum(sizes)])
     lo1, hi1 = at[1], at[2]
     a, b, e = _ints(1, rows, k, dtype=t), _ints(2, groups, n, k, dtype=t), _ints(3, rows, n, dtype=t, most=1)
@@ -372,12 +379,13 @@ def test_a_group_reaches_no_other(m, value, sizes):
     assert torch.equal(d[0][col], (a[:lo1].double().T @ e[:lo1].double()).to(t)[col])
 
 
-@pytest.mark.parametrize("rows", [5, 6000])
+@pytest.mark.parametrize("rows,form", [(5, 0), (600, 0), (600, 1), (600, 2)])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("scale", ["large", "small"])
-def test_adapters_between_magnitudes(m, rows, dtype, scale):
+def test_adapters_between_magnitudes(m, rows, form, dtype, scale, monkeypatch):
     """A first product past the type's range, or below its least value, of a result that is neither."""
-    t, n, k, rank = TD[dtype], 72, 256, 16
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
+    t, n, k, rank = TD[dtype], 264, 256, 16
     g = torch.Generator(device="cuda").manual_seed(3)
     top = {"f16": {"large": (2.0**9, 2.0**9, 2.0**-14), "small": (2.0**-11, 2.0**-11, 2.0**12)},
            "bf16": {"large": (2.0**60, 2.0**60, 2.0**-120), "small": (2.0**-60, 2.0**-60, 2.0**118)}}[dtype][scale]
@@ -432,9 +440,10 @@ def test_sums_past_31_bits(m):
     assert not c[1:38].any()
 
 
-@pytest.mark.parametrize("spread", [False, True])
-def test_adapters_past_31_bits(m, spread):
+@pytest.mark.parametrize("spread,form", [(False, 1), (False, 0), (False, 2), (True, 0)])
+def test_adapters_past_31_bits(m, spread, form, monkeypatch):
     """More than 2^31 values in x and out, for few groups of many rows and for many of one row."""
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
     t, rows, n, k, rank = torch.bfloat16, 36000, 65536, 65536, 8
     x, base = torch.zeros(rows, k, dtype=t, device="cuda"), torch.zeros(rows, n, dtype=t, device="cuda")
     groups = 2 if not spread else 5
@@ -459,7 +468,7 @@ def test_adapters_past_31_bits(m, spread):
 
 # ------------------------------------------------------------------ waits that run out
 
-@pytest.mark.parametrize("kind", ["few rows", "many rows", "along K", "along K, narrow", "adapters"])
+@pytest.mark.parametrize("kind", ["few rows", "many rows", "along K", "along K, narrow", "adapters 1", "adapters 2", "adapters 8"])
 def test_waits_run_out(m, kind, monkeypatch):
     """A load that is withheld: the run's status says so, and the next run is right."""
     monkeypatch.setenv("LGT_GEMM_WAIT_LIMIT_MS", "20")
@@ -477,9 +486,10 @@ def test_waits_run_out(m, kind, monkeypatch):
         want = torch.stack([a[:133].double().T @ b[:133].double(), a[133:].double().T @ b[133:].double()]).to(t)
         got, withhold = c, m._lib.gemm_grouped_withhold_load
     else:
-        x, down, up, base = _ints(1, 6000, 200, dtype=t), _ints(2, 1, 8, 200, dtype=t, most=1), _ints(3, 1, 72, 8, dtype=t, most=1), _ints(4, 6000, 72, dtype=t)
+        monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", kind.split()[1])
+        x, down, up, base = _ints(1, 900, 520, dtype=t), _ints(2, 1, 8, 520, dtype=t, most=1), _ints(3, 1, 1032, 8, dtype=t, most=1), _ints(4, 900, 1032, dtype=t)
         got = torch.zeros_like(base)
-        op, args = m.Adapters(1, 72, 200, 8, dtype=m.GEMM_F16), (x, down, up, _offsets([6000]), None, base, got)
+        op, args = m.Adapters(1, 1032, 520, 8, dtype=m.GEMM_F16), (x, down, up, _offsets([900]), None, base, got)
         want, withhold = (base.double() + (x.double() @ down[0].double().T) @ up[0].double().T).to(t), m._lib.gemm_adapters_withhold_load
     assert withhold(op.plan) == m.GEMM_OK
     op.run(*args)
