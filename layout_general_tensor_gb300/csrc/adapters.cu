@@ -818,6 +818,12 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
         if (turn_here) fetch();
         if (!(ok = warp_wait(out_full(buf), uses >> 1 & 1u))) break;
         tc_fence_after();
+        // (the sums are free as soon as they have been read, before the results are stored)
+        auto done = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(out_empty(buf));
+        };
         if (turn_here) {
           const uint32_t here = mine + (used++ % kAtcPieces) * 2048u;
           const int n = b * 128 + n0;
@@ -829,6 +835,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
             __syncwarp();
             tc_wait_ld_regs(x);
             tc_regs_after_wait(y);
+            done();
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e) {
               const uint4 old = ldmatrix_x4_trans(here + put + e * 512u);
@@ -845,11 +852,12 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
               const uint4 v = ld_shared_v4(here + get + e * 512u);
               if (r[e] >= 0 && n < a.n) st_global_v4(a.out + r[e] * a.os + n, v.x, v.y, v.z, v.w);
             }
+          } else {
+            done();
           }
+        } else {
+          done();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(out_empty(buf));
       }
       if (lane == 0) mbar_arrive(results_done);
     }
