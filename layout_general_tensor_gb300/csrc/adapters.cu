@@ -73,15 +73,6 @@ __device__ __forceinline__ uint2 load8(const uint16_t* p, bool there) {
   return there ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
 }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 // The power of two that takes a row's largest value to [0.5, 1), and its reverse.
 __device__ __forceinline__ float2 row_power(float most) {
   const int e = static_cast<int>(__float_as_uint(most) >> 23);  // (biased; no sign)

@@ -19,6 +19,11 @@
 // few rows and many weights then meet at the end: 4000 rows of 24 groups, 3000 x
 // 2880, 85 to 88 us, and 16384 rows of 16 groups no better.)
 //
+// Where the tiles are too few for the SMs, the CTAs of a cluster take a stretch of
+// K each (SPLIT): each leaves its fp32 sums in its shared memory, and each adds and
+// stores a share of the columns, in the CTAs' order (6 rows of one group, 632 x
+// 2048: 12.2 to 7.2 us; 3302 rows along K, 192 x 168: 19.6 to 10.9).
+//
 // Groups along K.  The product's steps are 16 rows deep; what is left of a group
 // behind its last whole step shares a step with the next group's rows, and a zero
 // on one side would not cancel an infinity on the other.  So those rows have a
@@ -55,7 +60,7 @@ constexpr int kGgEpiWarp0 = 2;
 constexpr int kGgEpiWarps = 8;
 constexpr int kGgQWarp = kGgEpiWarp0 + kGgEpiWarps;
 constexpr int kGgClearWarp = kGgQWarp + 1;
-constexpr int kGgOddP = kGgClearWarp + 1, kGgOddQ = kGgOddP + 1;
+constexpr int kGgOddP = kGgClearWarp + 1;  // (the N side's: the one behind it)
 constexpr int kGgMaxGroups = 1024;
 constexpr uint32_t kGgRows = 128;                       // M-side rows a CTA
 constexpr uint32_t kGgPBytes = kGgRows * TILE_K * 2;    // 16 KiB of them a stage
@@ -89,6 +94,7 @@ struct GroupedArgs {
   int32_t p_whole, q_whole;   // the one copy is of several stretches
   uint32_t q_step;            // along K: what a tile's columns are a multiple of
   uint32_t stages, stage_bytes;
+  uint32_t split;  // CTAs that share a tile's K (SPLIT)
   uint32_t rests;  // along K: buffers for what is left behind a group's last whole step, a power of two
   int32_t p_mn;
   uint32_t idesc;  // without N
@@ -104,6 +110,7 @@ struct GroupedTile {
   int32_t row0;       // along K: the group's first row
   int32_t steps;      // of the product, of 16
   int32_t nkb;        // blocks of 64 that hold them
+  int32_t kb0;        // the first of them
   int32_t rest;       // along K: rows behind them
 };
 
@@ -113,13 +120,14 @@ struct GroupedCfg {
   static constexpr uint32_t STEP = PAIR ? 32 : 16;  // of the product's N
 };
 
-template <bool PAIR>
+template <bool PAIR, bool SPLIT>
 struct GroupedWork {
   const uint32_t *off, *first;
   uint32_t tile, step, end;
   __device__ GroupedWork(const GroupedArgs& a, const uint32_t* off_, const uint32_t* first_) : off(off_), first(first_) {
-    tile = blockIdx.x / GroupedCfg<PAIR>::CTAS;
-    step = gridDim.x / GroupedCfg<PAIR>::CTAS;
+    const uint32_t ctas = SPLIT ? a.split : GroupedCfg<PAIR>::CTAS;
+    tile = blockIdx.x / ctas;
+    step = gridDim.x / ctas;
     end = a.along_k ? static_cast<uint32_t>(a.groups) * a.p_tiles * a.q_tiles : first[a.groups];
   }
   __device__ bool next(const GroupedArgs& a, GroupedTile& t) {
@@ -153,11 +161,20 @@ struct GroupedWork {
       t.rest = 0;
     }
     t.nkb = (t.steps + TILE_K / 16 - 1) / (TILE_K / 16);
+    t.kb0 = 0;
+    if constexpr (SPLIT) {
+      // this CTA's stretch; the last one has the rest, too
+      const uint32_t r = cluster_ctarank();
+      t.kb0 = static_cast<int32_t>(static_cast<int64_t>(t.nkb) * r / a.split);
+      t.nkb = static_cast<int32_t>(static_cast<int64_t>(t.nkb) * (r + 1) / a.split) - t.kb0;
+      t.steps = min(t.steps - t.kb0 * (TILE_K / 16), t.nkb * (TILE_K / 16));
+      if (r + 1 < a.split) t.rest = 0;
+    }
     return true;
   }
 };
 
-template <bool PAIR, bool BF16>
+template <bool PAIR, bool SPLIT, bool BF16>
 __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
   pdl_launch_dependents();
   constexpr uint32_t CTAS = GroupedCfg<PAIR>::CTAS;
@@ -255,7 +272,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   const uint32_t cleared_lead = PAIR ? mapa_shared(cleared(0), 0) : cleared(0);
   const uint32_t acce_lead = PAIR ? mapa_shared(acce(0), 0) : acce(0);
 
-  GroupedWork<PAIR> work(a, off, first);
+  GroupedWork<PAIR, SPLIT> work(a, off, first);
   GroupedTile t;
   if (warp == 0 || warp == kGgQWarp || warp >= kGgOddP) {
     // ------------------------------------------------------------ copies
@@ -285,7 +302,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         const int32_t x0 = is_p ? t.p0 + static_cast<int32_t>(rank * kGgRows)
                                 : t.q0 + static_cast<int32_t>(rank * (t.cols / CTAS));
         const int32_t z = is_p && !a.along_k ? t.group : 0;
-        const int32_t k0 = a.along_k ? t.row0 : 0;
+        const int32_t k0 = (a.along_k ? t.row0 : 0) + t.kb0 * TILE_K;
         if (t.rest > 0) {
           const uint32_t b = rests & rest_mask;
           if (!(ok = wait(rest_empty(b), (rests >> rest_shift & 1u) ^ 1u))) break;
@@ -427,6 +444,23 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         tc_fence_after();
       }
       const uint32_t d = tmem + static_cast<uint32_t>(buf) * kGgMost + (quad * 32u << 16);
+      if constexpr (SPLIT) {
+        // this CTA's sums, column by column, where the ring was (it has but this tile)
+        for (uint32_t c = set * 32; c < t.count; c += 64) {
+          uint32_t v[32];
+          if (some) {
+            tc_ld_32x32b_x32(d + c, v);
+            tc_wait_ld_regs(v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+#pragma unroll
+          for (uint32_t i = 0; i < 32; ++i)
+            st_shared_f32(base + (c + i) * (kGgRows * 4) + (quad * 32u + lane) * 4u, __uint_as_float(v[i]));
+        }
+        break;
+      }
       const int32_t n = t.p0 + static_cast<int32_t>(rank * kGgRows + piece * 8u);
       const bool inside = n < a.n;
       uint16_t* out = a.c + (a.along_k ? t.group * a.c_stride : 0) + static_cast<int64_t>(t.q0) * a.ldc + n;
@@ -506,8 +540,27 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync_all();
+  if constexpr (PAIR || SPLIT) cluster_sync_all();
   tc_fence_after();
+  if constexpr (SPLIT) {
+    // A share of the columns, the CTAs' sums in order: a column a warp, four values a lane.
+    GroupedWork<PAIR, SPLIT> again(a, off, first);
+    if (again.next(a, t)) {
+      const uint32_t r = cluster_ctarank(), c1 = t.count * (r + 1) / a.split;
+      const int32_t n = t.p0 + 4 * lane;
+      for (uint32_t c = t.count * r / a.split + warp; c < c1; c += kGgThreads / 32) {
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (uint32_t i = 0; i < a.split; ++i) {
+          const float4 v = ld_cluster_f32x4(mapa_shared(base + c * (kGgRows * 4) + lane * 16u, i));
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        if (n < a.n)
+          st_global_v2(a.c + (a.along_k ? t.group * a.c_stride : 0) + (t.q0 + static_cast<int64_t>(c)) * a.ldc + n,
+                       pack_pair16<BF16>(sum.x, sum.y), pack_pair16<BF16>(sum.z, sum.w));
+      }
+    }
+    cluster_sync_all();  // (the others have read this CTA's)
+  }
   if (warp == 1) {
     if constexpr (PAIR)
       tmem_dealloc_pair(tmem, 512);
@@ -516,18 +569,21 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   }
 }
 
-template <bool PAIR, bool BF16>
+template <bool PAIR, bool SPLIT, bool BF16>
 cudaError_t launch_grouped_as(const GroupedArgs& a, unsigned workers, cudaStream_t stream) {
-  const cudaError_t e = set_smem_once<grouped_kernel<PAIR, BF16>>(static_cast<int>(kGgSmem));
+  const cudaError_t e = set_smem_once<grouped_kernel<PAIR, SPLIT, BF16>>(static_cast<int>(kGgSmem));
   if (e != cudaSuccess) return e;
-  if (PAIR)
-    return launch_pdl_cluster(grouped_kernel<PAIR, BF16>, dim3(2 * workers), dim3(kGgThreads), kGgSmem, stream, 2u, a);
-  return launch_pdl(grouped_kernel<PAIR, BF16>, dim3(workers), dim3(kGgThreads), kGgSmem, stream, a);
+  const unsigned ctas = PAIR ? 2 : SPLIT ? a.split : 1;
+  if (ctas > 1)
+    return launch_pdl_cluster(grouped_kernel<PAIR, SPLIT, BF16>, dim3(ctas * workers), dim3(kGgThreads), kGgSmem, stream, ctas, a);
+  return launch_pdl(grouped_kernel<PAIR, SPLIT, BF16>, dim3(workers), dim3(kGgThreads), kGgSmem, stream, a);
 }
 
-cudaError_t launch_grouped(const GroupedArgs& a, bool pair, bool bf16, unsigned workers, cudaStream_t stream) {
-  if (pair) return bf16 ? launch_grouped_as<true, true>(a, workers, stream) : launch_grouped_as<true, false>(a, workers, stream);
-  return bf16 ? launch_grouped_as<false, true>(a, workers, stream) : launch_grouped_as<false, false>(a, workers, stream);
+template <bool BF16>
+cudaError_t launch_grouped(const GroupedArgs& a, bool pair, unsigned workers, cudaStream_t stream) {
+  return pair          ? launch_grouped_as<true, false, BF16>(a, workers, stream)
+         : a.split > 1 ? launch_grouped_as<false, true, BF16>(a, workers, stream)
+                       : launch_grouped_as<false, false, BF16>(a, workers, stream);
 }
 
 // A matrix [d2][d1][d0] with pitches s1 and s2 in elements, by boxes of 64 of d0
@@ -648,13 +704,26 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   GroupedArgs a = {};
   const int64_t busy = std::min<int64_t>(d.groups, std::max<int64_t>(rows, 1));
   const int64_t mean = (rows + busy - 1) / busy;
-  const bool pair = d.N > kGgRows && (along_k ? d.M > 64 : mean > 96);
+  // Few rows a group: tiles as wide as twice the mean, so that most groups have one.
+  uint32_t narrow = kGgMost;
+  for (uint32_t w : {128u, 64u, 32u, 16u})
+    if (2 * mean <= static_cast<int64_t>(w)) narrow = w;
+  // Tiles of single CTAs, and blocks of K of each: where a cluster for each tile
+  // leaves no SM twice the work, and the blocks that a CTA then does not do are worth
+  // the exchange (a block 0.25 us, the exchange 2.5), K is split.
+  const int64_t single = (along_k ? static_cast<int64_t>(d.groups) * ((d.M + kGgMost - 1) / kGgMost) : rows / narrow + busy) *
+                         ((d.N + kGgRows - 1) / kGgRows);
+  const int64_t deep = (along_k ? mean : d.K) / TILE_K;
+  a.split = 1;
+  for (uint32_t c : {2u, 4u, 8u})  // (an SM group holds whole clusters of 8 only)
+    if (single * c * 16 <= plan->sms * (c == 8 ? 12 : 15) && deep * (c - 1) >= 10 * c) a.split = c;
+  const bool pair = a.split == 1 && d.N > kGgRows && (along_k ? d.M > 64 : mean > 96);
   const uint32_t ctas = pair ? 2 : 1, step = pair ? 32 : 16;
   a.p_tiles = static_cast<uint32_t>((d.N + kGgRows * ctas - 1) / (kGgRows * ctas));
   int64_t tiles;
   // Operands that run along n or m: one copy a stage where the matrix is whole
-  // stretches of 64 (the copying thread is held for each: 4096 x 4096 of
-  // [k][n], 16 groups of 1024 rows, P_ONE us against P_TWO), else one a stretch.
+  // stretches of 64 (the copying thread is held for each: 4096 x 4096 of [k][n], 16
+  // groups of 1024 rows, 293 us against 356 with one warp a side), else one a stretch.
   const bool p_whole = b_mn && d.N % 64 == 0, q_whole = along_k && d.M % 64 == 0;
   a.p_boxes = b_mn && !p_whole ? 2 : 1;
   a.q_boxes = 1;
@@ -668,10 +737,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     a.stage_bytes = kGgPBytes + a.q_chunks * kGgChunk;
     tiles = static_cast<int64_t>(d.groups) * a.p_tiles * a.q_tiles;
   } else {
-    a.q_most = kGgMost;
-    if (!pair)
-      for (uint32_t w : {128u, 64u, 32u, 16u})
-        if (2 * mean <= static_cast<int64_t>(w)) a.q_most = w;
+    a.q_most = pair ? kGgMost : narrow;
     a.q_box = a.q_most / ctas;
     a.stage_bytes = kGgPBytes + a.q_box * TILE_K * 2;
     tiles = (rows / a.q_most + busy) * a.p_tiles;
@@ -713,8 +779,10 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   a.p_mn = b_mn;
   a.idesc = idesc_f16(bf16, b_mn, along_k, kGgRows * ctas, 0);
   a.withhold = plan->withhold_armed ? __atomic_exchange_n(&plan->withhold_armed, 0, __ATOMIC_ACQ_REL) : 0;
-  const unsigned workers = static_cast<unsigned>(std::min<int64_t>(tiles, plan->sms / ctas));
-  if (launch_grouped(a, pair, bf16, workers, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+  // (split, every tile has a cluster of its own)
+  const unsigned workers = static_cast<unsigned>(a.split > 1 ? tiles : std::min<int64_t>(tiles, plan->sms / ctas));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((bf16 ? launch_grouped<true>(a, pair, workers, s) : launch_grouped<false>(a, pair, workers, s)) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }

@@ -145,6 +145,14 @@ def test_rows_many_groups(m, groups):
     _check_rows(m, [r.choice((0, 100, 300)) for _ in range(groups)], 136, 64, groups % 2 == 0, "f16", seed=groups)
 
 
+@pytest.mark.parametrize("sizes", [[1], [0, 5, 0, 16], [40], [200], [3, 60, 1, 17, 130, 9], [0, 0]], ids=lambda s: f"{len(s)}x{max(s)}_{sum(s)}")
+@pytest.mark.parametrize("k_contig", [True, False])
+@pytest.mark.parametrize("n,k", [(8, 1304), (136, 712), (200, 4096), (1024, 2000)])
+def test_rows_few_tiles(m, sizes, k_contig, n, k):
+    """Tiles too few for the SMs: K is split over clusters of two to eight CTAs."""
+    _check_rows(m, sizes, n, k, k_contig, "bf16" if (n + len(sizes)) % 16 else "f16", pad=3, start=2, extra=(8, 0, 8), seed=len(sizes))
+
+
 # ------------------------------------------------------------------ groups along K
 
 def _check_sums(m, sizes, mm, n, dtype, pad=0, start=0, extra=(0, 0, 0), seed=0):
@@ -172,6 +180,12 @@ SUM_SIZES = [[0], [1], [0, 0, 7, 0], [64], [65, 63], [128, 1, 0, 15, 16, 17], [5
 @pytest.mark.parametrize("mm,n", [(8, 8), (64, 520), (72, 136), (264, 200), (1000, 512), (520, 120)])
 def test_sums(m, sizes, mm, n):
     _check_sums(m, sizes, mm, n, "bf16" if (mm + len(sizes)) % 16 else "f16", seed=len(sizes))
+
+
+@pytest.mark.parametrize("sizes", [[900], [1313], [5000, 3], [0, 2000, 17, 1500], [1300, 1301]], ids=lambda s: f"{len(s)}x{max(s)}_{sum(s)}")
+@pytest.mark.parametrize("mm,n", [(8, 8), (264, 136), (64, 520), (200, 200), (512, 256)])
+def test_sums_few_tiles(m, sizes, mm, n):
+    _check_sums(m, sizes, mm, n, "bf16" if (mm + len(sizes)) % 16 else "f16", pad=70, start=5, extra=(0, 8, 8), seed=len(sizes))
 
 
 def test_sums_strided_padded(m):

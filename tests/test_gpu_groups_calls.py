@@ -276,7 +276,7 @@ def test_one_object_on_two_streams(m, big):
             assert torch.equal(d[g], (a[lo:hi].double().T @ e[lo:hi].double()).to(t))
 
 
-@pytest.mark.parametrize("big,form", [(False, 0), (True, 0), (True, 1), (True, 2), (True, 4)])
+@pytest.mark.parametrize("big,form", [(False, 0), (False, 8), (True, 0), (True, 1), (True, 2), (True, 4)])
 def test_repeated_calls_give_the_same_bits(m, big, form, monkeypatch):
     monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
     sizes = [2100, 0, 3111, 17] if big else [4, 0, 31, 1]
@@ -468,13 +468,13 @@ def test_adapters_past_31_bits(m, spread, form, monkeypatch):
 
 # ------------------------------------------------------------------ waits that run out
 
-@pytest.mark.parametrize("kind", ["few rows", "many rows", "along K", "along K, narrow", "adapters 1", "adapters 2", "adapters 8"])
+@pytest.mark.parametrize("kind", ["few rows", "few tiles", "many rows", "along K", "along K, narrow", "adapters 1", "adapters 2", "adapters 8"])
 def test_waits_run_out(m, kind, monkeypatch):
     """A load that is withheld: the run's status says so, and the next run is right."""
     monkeypatch.setenv("LGT_GEMM_WAIT_LIMIT_MS", "20")
     t = torch.float16
-    if kind in ("few rows", "many rows"):
-        sizes, n, k = ([3, 9], 264, 200) if kind == "few rows" else ([700, 400], 264, 200)
+    if kind in ("few rows", "few tiles", "many rows"):
+        sizes, n, k = ([3, 9], 264, 200) if kind == "few rows" else ([3, 9], 264, 2000) if kind == "few tiles" else ([700, 400], 264, 200)
         a, b, c = _ints(1, sum(sizes), k, dtype=t), _ints(2, 2, n, k, dtype=t), torch.zeros(sum(sizes), n, dtype=t, device="cuda")
         op, args = m.GroupedGemm(2, n, k, dtype=m.GEMM_F16), (a, b, _offsets(sizes), c)
         want = torch.cat([a[:sizes[0]].double() @ b[0].double().T, a[sizes[0]:].double() @ b[1].double().T]).to(t)
