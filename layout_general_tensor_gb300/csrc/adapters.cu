@@ -69,9 +69,24 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint4 load16(const uint16_t* p, bool there) {
   return there ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
-__device__ __forceinline__ uint2 load8(const uint16_t* p, bool there) {
-  return there ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
-}
+// A lane's values of a row for the second product: eight of every 32, which are two
+// steps of it, or four of 16 where that is the rank.
+template <int MT>
+struct RankPiece {
+  static constexpr int COUNT = MT / 2, VALUES = 8, STEPS = 2;
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p, bool there) { v = load16(p, there); }
+  __device__ __forceinline__ uint2 step(int s) const { return s ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y); }
+};
+template <>
+struct RankPiece<1> {
+  static constexpr int COUNT = 1, VALUES = 4, STEPS = 1;
+  uint2 v;
+  __device__ __forceinline__ void load(const uint16_t* p, bool there) {
+    v = there ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+  }
+  __device__ __forceinline__ uint2 step(int) const { return v; }
+};
 
 // The power of two that takes a row's largest value to [0.5, 1), and its reverse.
 __device__ __forceinline__ float2 row_power(float most) {
@@ -91,33 +106,27 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
 
 // Rows of no group, at the places before the first group and behind the last, go
 // from base to out, as tiles of their own behind the groups': `tile` of `per` rows,
-// by `threads` of each CTA of a cluster, whose CTAs (`share` of `shares`) take
-// pieces in turn.
+// a row a warp, of which this is number `warp` of `warps` (of a cluster's).
 __device__ __forceinline__ uint32_t other_rows(const AdapterArgs& a, const uint32_t* off) {
   return a.copy ? off[0] + static_cast<uint32_t>(a.rows) - off[a.groups] : 0u;
 }
-__device__ __forceinline__ void copy_others(const AdapterArgs& a, const uint32_t* off, uint32_t tile, uint32_t per, uint32_t share,
-                                            uint32_t shares, uint32_t thread, uint32_t threads) {
+__device__ __forceinline__ void copy_others(const AdapterArgs& a, const uint32_t* off, uint32_t tile, uint32_t per, uint32_t warp,
+                                            uint32_t warps) {
   const uint32_t from = tile * per, rows = min(per, other_rows(a, off) - from), pieces = static_cast<uint32_t>(a.n) / 8;
-  // (lanes take neighbouring pieces of a row; four are on their way at once)
-  const uint32_t across = min(threads, (pieces + 31) / 32 * 32), high = threads / across;
-  const uint32_t c0 = thread % across, r0 = thread / across;
-  if (r0 >= high) return;
-  for (uint32_t i = r0; i < rows; i += high) {
+  for (uint32_t i = warp; i < rows; i += warps) {
     const uint32_t place = from + i;
     int32_t r = static_cast<int32_t>(place < off[0] ? place : off[a.groups] + (place - off[0]));
     if (a.order) r = a.order[r];
     if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.rows)) continue;
     const uint16_t* src = a.base + r * a.bs;
     uint16_t* dst = a.out + r * a.os;
-    const uint32_t step = across * shares;
-    for (uint32_t c = c0 + share * across; c < pieces; c += 4 * step) {
-      uint4 v[4];
+    for (uint32_t c = threadIdx.x & 31; c < pieces; c += 8 * 32) {  // (eight on their way at once)
+      uint4 v[8];
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) v[j] = load16(src + static_cast<int64_t>(c + j * step) * 8, c + j * step < pieces);
+      for (uint32_t j = 0; j < 8; ++j) v[j] = load16(src + static_cast<int64_t>(c + 32 * j) * 8, c + 32 * j < pieces);
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j)
-        if (c + j * step < pieces) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(c + j * step) * 8) = v[j];
+      for (uint32_t j = 0; j < 8; ++j)
+        if (c + 32 * j < pieces) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(c + 32 * j) * 8) = v[j];
     }
   }
 }
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
 
   for (uint32_t tile = blockIdx.x / a.ctas; tile < all_tiles; tile += clusters) {
     if (tile >= tiles) {
-      copy_others(a, off, tile - tiles, C::TOK, rank, a.ctas, threadIdx.x, kAdThreads);
+      copy_others(a, off, tile - tiles, C::TOK, rank * kAdWarps + warp, a.ctas * kAdWarps);
       continue;
     }
     const uint32_t g = group_of(first, a.groups, tile);
@@ -234,8 +243,9 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
     const int share = warp % C::SHARES, apart = kAdWarps / C::SHARES;
     const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / a.ctas) + warp / C::SHARES;
     const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / a.ctas);
-    const uint16_t* br = a.b + static_cast<int64_t>(g) * a.n * a.rank + 4 * q;
-    uint2 bv[C::BATCH][4][MT];
+    using Piece = RankPiece<MT>;
+    const uint16_t* br = a.b + static_cast<int64_t>(g) * a.n * a.rank + Piece::VALUES * q;
+    Piece bv[C::BATCH][4][Piece::COUNT];
     uint4 old[C::BATCH][C::M2][2];
     int32_t row[C::M2][2];
 #pragma unroll
@@ -254,8 +264,9 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
         for (int j = 0; j < 4; ++j) {
           const int c = n + 8 * (l4 >> 1) + 2 * j + (l4 & 1);
 #pragma unroll
-          for (int s = 0; s < MT; ++s)
-            bv[i][j][s] = load8(br + static_cast<int64_t>(c) * a.rank + 16 * s, in && c < a.n && 16 * s + 4 * q < a.rank);
+          for (int s = 0; s < Piece::COUNT; ++s)
+            bv[i][j][s].load(br + static_cast<int64_t>(c) * a.rank + 4 * Piece::VALUES * s,
+                             in && c < a.n && Piece::VALUES * (4 * s + q) < a.rank);
         }
 #pragma unroll
         for (int m = 0; m < C::M2; ++m)
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
     // ------------------------------------------------------------ out = base + u B^T
     {
       constexpr int M2 = C::M2;
-      uint2 hi[M2][MT][2], lo[M2][MT][2];
+      Piece hi[M2][Piece::COUNT][2], lo[M2][Piece::COUNT][2];
       float f[M2][2];
 #pragma unroll
       for (int m = 0; m < M2; ++m)
@@ -330,9 +341,9 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
           const bool live = t < C::TOK;
           f[m][h] = live ? factor[t] : 0.0f;
 #pragma unroll
-          for (int s = 0; s < MT; ++s) {
-            hi[m][s][h] = live ? *reinterpret_cast<const uint2*>(uh + t * C::UPITCH + 16 * s + 4 * q) : make_uint2(0u, 0u);
-            lo[m][s][h] = live ? *reinterpret_cast<const uint2*>(ul + t * C::UPITCH + 16 * s + 4 * q) : make_uint2(0u, 0u);
+          for (int s = 0; s < Piece::COUNT; ++s) {
+            hi[m][s][h].load(uh + t * C::UPITCH + Piece::VALUES * (4 * s + q), live);
+            lo[m][s][h].load(ul + t * C::UPITCH + Piece::VALUES * (4 * s + q), live);
           }
         }
       for (int b = b0; b < b1; b += C::BATCH * apart) {
@@ -349,10 +360,14 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
 #pragma unroll
-              for (int s = 0; s < MT; ++s) {
-                mma16816<BF16>(acc[j], hi[m][s][0].x, hi[m][s][1].x, hi[m][s][0].y, hi[m][s][1].y, bv[i][j][s].x, bv[i][j][s].y);
-                mma16816<BF16>(acc[j], lo[m][s][0].x, lo[m][s][1].x, lo[m][s][0].y, lo[m][s][1].y, bv[i][j][s].x, bv[i][j][s].y);
-              }
+              for (int s = 0; s < Piece::COUNT; ++s)
+#pragma unroll
+                for (int k = 0; k < Piece::STEPS; ++k) {
+                  const uint2 b2 = bv[i][j][s].step(k), h0 = hi[m][s][0].step(k), h1 = hi[m][s][1].step(k);
+                  const uint2 l0 = lo[m][s][0].step(k), l1 = lo[m][s][1].step(k);
+                  mma16816<BF16>(acc[j], h0.x, h1.x, h0.y, h1.y, b2.x, b2.y);
+                  mma16816<BF16>(acc[j], l0.x, l1.x, l0.y, l1.y, b2.x, b2.y);
+                }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -856,7 +871,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
     // (the tiles of rows of no group go on where this cluster's turns leave off)
     const uint32_t all_tiles = tiles + (other_rows(a, off) + kAtcRows - 1) / kAtcRows;
     for (uint32_t i = turn0 + it * turns; ok && i < all_tiles; i += turns)
-      copy_others(a, off, i - tiles, kAtcRows, rank, ctas, threadIdx.x - kAtcEpiWarp0 * 32, kAtcEpiWarps * 32);
+      copy_others(a, off, i - tiles, kAtcRows, rank * kAtcEpiWarps + (warp - kAtcEpiWarp0), ctas * kAtcEpiWarps);
   }
 
   // ------------------------------------------------------------ end
