@@ -255,14 +255,16 @@ def test_adapters_normal(m, dtype, rank):
     _check_adapters(m, [100, 60, 0], 9, 520, 1032, rank, dtype, ints=False, order=False, seed=rank + 1)
 
 
-# (every form of the operator, whatever the sizes would choose)
-@pytest.mark.parametrize("form", [0, 1, 2, 4, 8])
+# (every form of the operator, whatever the sizes would choose; with fewer blocks than CTAs another one would be taken)
+FORMS = [(form, n, k, rank) for form in (0, 1, 2, 4, 8)
+         for n, k, rank in ((8, 8, 8), (136, 72, 16), (1000, 328, 24), (520, 512, 64), (264, 200, 72), (392, 1024, 128), (1096, 1032, 48))
+         if k >= 64 * form and n >= 128 * form]
+
+
 @pytest.mark.parametrize("sizes,none", [([5000], 0), ([2600, 0, 2500], 60), ([200] * 40, 0), ([1, 6000, 17, 129, 128], 1), ([300, 33], 0),
                                         ([1000, 1, 700, 64], 500), ([0, 3], 2)], ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
-@pytest.mark.parametrize("n,k,rank", [(8, 8, 8), (136, 72, 16), (1000, 328, 24), (520, 512, 64), (264, 200, 72), (392, 1024, 128), (1096, 1032, 48)])
+@pytest.mark.parametrize("form,n,k,rank", FORMS)
 def test_adapters_forms(m, form, sizes, none, n, k, rank, monkeypatch):
-    if form and (k < 64 * form or n < 128 * form):
-        pytest.skip("fewer blocks than CTAs: another form is taken")
     monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
     i = len(sizes) + rank // 8
     _check_adapters(m, sizes, none, n, k, rank, "bf16" if i % 2 else "f16", order=i % 3 > 0, scaled=i % 5 > 0, in_place=i % 4 == 0, seed=i)
