@@ -31,7 +31,8 @@
 // tile begins, in which a warp of each CTA that has nothing else to do clears the
 // rows beyond, and the product takes that step last.  (Cleared in the last block
 // of 64 on its way through the ring, each tile waited for it: 16 groups of 1000
-// rows, 2048 x 4096, 207 us against 157 for groups of 1024.)
+// rows, 2048 x 4096, 207 us against 157 for groups of 1024.  More than two buffers
+// make no difference.)
 //
 // Roles (448 threads; pairs: in both CTAs):
 //   warp 0, 12  copies of the M side (a stage's first, third, ... and the others,
@@ -69,8 +70,8 @@ constexpr uint32_t kGgMost = 256;                       // N-side columns of a t
 constexpr uint32_t kGgMaxStages = 12;
 constexpr uint32_t kGgEpiBytes = 2 * 2 * 8192;          // 32 rows of C, 128 values each, of two sets of warps, twice
 constexpr uint32_t kGgStep = 16 * 128;                  // a step's 16 rows of 64 values along n or m
-constexpr uint32_t kGgMaxRests = 8;
-constexpr uint32_t kGgBars = 2 * kGgMaxStages + 3 * kGgMaxRests + 5;  // full, empty; rest landed, cleared, empty; accumulators full, empty; end
+constexpr uint32_t kGgRests = 2;                        // buffers for what is left behind a group's last whole step
+constexpr uint32_t kGgBars = 2 * kGgMaxStages + 3 * kGgRests + 5;  // full, empty; rest landed, cleared, empty; accumulators full, empty; end
 constexpr uint32_t kGgSmem = 227 * 1024;
 constexpr uint64_t kGgSettleNs = 200ull * 1000ull * 1000ull;
 
@@ -95,7 +96,6 @@ struct GroupedArgs {
   uint32_t q_step;            // along K: what a tile's columns are a multiple of
   uint32_t stages, stage_bytes;
   uint32_t split;  // CTAs that share a tile's K (SPLIT)
-  uint32_t rests;  // along K: buffers for what is left behind a group's last whole step, a power of two
   int32_t p_mn;
   uint32_t idesc;  // without N
   int32_t withhold;
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw_base);
   const uint32_t rest_off = a.stages * a.stage_bytes;
-  const uint32_t rest_bytes = (2 + a.q_chunks) * kGgStep;  // each
-  const uint32_t epi_off = rest_off + a.rests * rest_bytes;
+  const uint32_t rest_bytes = a.along_k ? (2 + a.q_chunks) * kGgStep : 0u;  // each
+  const uint32_t epi_off = rest_off + kGgRests * rest_bytes;
   const uint32_t bar0 = base + epi_off + kGgEpiBytes;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + epi_off + kGgEpiBytes + kGgBars * 8);
   volatile uint32_t* tmem_slot = misc;
@@ -198,13 +198,12 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty = [&](uint32_t s) { return bar0 + 8u * (kGgMaxStages + s); };
   auto landed = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + b); };
-  auto cleared = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + kGgMaxRests + b); };
-  auto rest_empty = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + 2 * kGgMaxRests + b); };
-  const uint32_t acc0 = bar0 + 8u * (2 * kGgMaxStages + 3 * kGgMaxRests);
+  auto cleared = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + kGgRests + b); };
+  auto rest_empty = [&](uint32_t b) { return bar0 + 8u * (2 * kGgMaxStages + 2 * kGgRests + b); };
+  const uint32_t acc0 = bar0 + 8u * (2 * kGgMaxStages + 3 * kGgRests);
   auto accf = [&](int b) { return acc0 + 8u * b; };
   auto acce = [&](int b) { return acc0 + 16u + 8u * b; };
   const uint32_t end_bar = acc0 + 32u;
-  const uint32_t rest_mask = a.rests - 1, rest_shift = 31 - __clz(max(a.rests, 1u));
   auto wait = [&](uint32_t bar, uint32_t parity) {
     const bool got = PAIR ? mbar_wait_bounded_cluster_sleep(bar, parity, a.wait_limit_ns, abort_flag)
                           : mbar_wait_bounded(bar, parity, a.wait_limit_ns, abort_flag);
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       mbar_init(full(s), 2);      // the two copying warps (of the even CTA), and the bytes
       mbar_init(empty(s), 1);     // the products' commit, to both CTAs
     }
-    for (uint32_t b = 0; b < a.rests; ++b) {
+    for (uint32_t b = 0; b < kGgRests; ++b) {
       mbar_init(landed(b), 2);      // the two copying warps of this CTA, and its bytes
       mbar_init(cleared(b), CTAS);  // the clearing warps
       mbar_init(rest_empty(b), 1);
@@ -304,8 +303,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         const int32_t z = is_p && !a.along_k ? t.group : 0;
         const int32_t k0 = (a.along_k ? t.row0 : 0) + t.kb0 * TILE_K;
         if (t.rest > 0) {
-          const uint32_t b = rests & rest_mask;
-          if (!(ok = wait(rest_empty(b), (rests >> rest_shift & 1u) ^ 1u))) break;
+          const uint32_t b = rests % kGgRests;
+          if (!(ok = wait(rest_empty(b), (rests / kGgRests & 1u) ^ 1u))) break;
           if (!odd) mbar_arrive_expect_tx(landed(b), chunks * kGgStep);
           copy(tm_rest, base + rest_off + b * rest_bytes + (is_p ? 0u : 2 * kGgStep), kGgStep,
                PAIR ? mapa_shared(landed(b), rank) : landed(b), x0, k0 + t.steps * 16, z);
@@ -326,8 +325,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       // Every commit to this CTA's barriers has arrived before it leaves.
       for (uint32_t i = issued > a.stages ? issued - a.stages : 0u; ok && i < issued; ++i)
         ok = wait(empty(i % a.stages), i / a.stages & 1u);
-      for (uint32_t i = rests > a.rests ? rests - a.rests : 0u; ok && i < rests; ++i)
-        ok = wait(rest_empty(i & rest_mask), i >> rest_shift & 1u);
+      for (uint32_t i = rests > kGgRests ? rests - kGgRests : 0u; ok && i < rests; ++i)
+        ok = wait(rest_empty(i % kGgRests), i / kGgRests & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
@@ -374,8 +373,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         }
         if (!ok) break;
         if (t.rest > 0) {
-          const uint32_t b = rests & rest_mask;
-          if (!(ok = wait(cleared(b), rests >> rest_shift & 1u))) break;
+          const uint32_t b = rests % kGgRests;
+          if (!(ok = wait(cleared(b), rests / kGgRests & 1u))) break;
           tc_fence_after();
           const uint32_t at = base + rest_off + b * rest_bytes;
           product(d, sw128_desc(at, kGgStep, 1024u), sw128_desc(at + 2 * kGgStep, kGgStep, 1024u), idesc, t.nkb > 0 ? 1u : 0u);
@@ -403,8 +402,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       bool ok = true;
       while (ok && work.next(a, t)) {
         if (t.rest == 0) continue;
-        const uint32_t b = rests & rest_mask;
-        if (!(ok = warp_wait(landed(b), rests >> rest_shift & 1u))) break;
+        const uint32_t b = rests % kGgRests;
+        if (!(ok = warp_wait(landed(b), rests / kGgRests & 1u))) break;
         ++rests;
         const uint32_t at = base + rest_off + b * rest_bytes;
         for (uint32_t c = 0; c < 2 + a.q_chunks; ++c)
@@ -744,8 +743,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   }
   if (tiles >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
   const uint32_t tables = 144 + static_cast<uint32_t>(d.groups + 1) * 8;
-  a.rests = along_k ? 2 : 0;
-  const uint32_t rest = a.rests * (2 + a.q_chunks) * kGgStep;
+  const uint32_t rest = along_k ? kGgRests * (2 + a.q_chunks) * kGgStep : 0;
   a.stages = std::min<uint32_t>(kGgMaxStages, (kGgSmem - 1024 - kGgEpiBytes - kGgBars * 8 - tables - rest) / a.stage_bytes);
 
   // (no rows: nothing is copied, any valid address will do)
