@@ -3,9 +3,14 @@
 //
 // Bound: memory.  A row costs K + 2 N values and 2 rank (K + N) multiply-adds, a
 // group its two matrices, so the whole adapter is one pass that keeps the first
-// product's result u on the chip: no workspace, one launch.
+// product's result u on the chip: no workspace, one launch.  Many rows come near
+// that (16384 rows, K = N = 4096, rank 64: 76 us, 79 % of a copy's rate).  Few are a
+// chain of trips to memory, one after the other: offsets, order, rows, the joins of
+// u, results (one row 5.8 us, 60 rows of 60 adapters 8.0, 801 rows of 13 and 198 of
+// none, 3000 x 2880, 14.1).
 //
-// A tile is up to 8 NT rows of one group, done by a cluster of 1 to 8 CTAs:
+// For few rows (for many: adapters_tc_kernel below) a tile is up to 8 NT rows of one
+// group, done by a cluster of 1 to 8 CTAs:
 //   u = x A^T:       every warp of the cluster takes a stretch of K for all of
 //                    the tile's rows and the whole rank, m16n8k16 with the rank
 //                    on the 16-side and rows on the 8-side (a single new token
@@ -420,7 +425,7 @@ constexpr int kAtcMmaWarp = 4, kAtcEpiWarp0 = 5, kAtcEpiWarps = 16;
 constexpr uint32_t kAtcRows = 128;
 constexpr uint32_t kAtcTile = 128 * 128;               // 128 rows of 64 values
 constexpr uint32_t kAtcMaxStages = 8;
-constexpr uint32_t kAtcPieces = 2;                     // of base, a warp
+constexpr uint32_t kAtcPieces = 2;                     // of base, a warp (three: 32768 rows 147 to 151 us, K = 64 51 to 49)
 constexpr uint32_t kAtcStaging = kAtcEpiWarps * kAtcPieces * 2048;
 constexpr uint32_t kAtcBars = 2 * kAtcMaxStages + 16;  // (15, and what follows is loaded 16 bytes at a time)
 static_assert(kAtcBars * 8 % 16 == 0);

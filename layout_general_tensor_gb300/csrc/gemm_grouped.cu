@@ -11,6 +11,16 @@
 // evenly over as few tiles as hold them.  Columns of the accumulator that stand
 // for rows of another group are computed and not stored; they touch no other.
 //
+// Bound, and measured on one GB300 (copies run at 6.79 TB/s, library products at
+// 1922 TFLOP/s, 1708 for long): with many rows a group the tensor pipe, and in runs
+// of many such products the power limit (16384 rows of 16 groups, 4096 x 4096:
+// 316 us alone, 1740 TFLOP/s, pipe busy for 90 % of the time; 360 one after the
+// other; along K, 2048 x 4096: 165 and 188); with few rows the weights' bytes (512
+// rows of 128 groups, 1536 x 2048: 114 us, 97 % of the copy's rate; 8 rows of 8
+// groups, 2048 x 4096: 20 us, of which 4 are its ends), along K those of C (1001
+// rows of 40 groups, 1000 x 2880: 61 us, a fill of C 60); between the two, rounds of
+// tiles (4000 rows of 24 groups, 3000 x 2880: 86 us, 68 by its bytes).
+//
 // Work.  The sizes are on the device, so every CTA sums them up itself (a scan
 // over the groups' tiles in shared memory) and takes every G-th tile, G the
 // CTAs or pairs: no launch depends on a size.  Within a group the tiles of one

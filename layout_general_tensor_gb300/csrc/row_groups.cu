@@ -2,7 +2,10 @@
 //
 // Bound: latency.  A row costs 12 bytes (131072 rows: 0.2 us of memory), so what
 // counts is the number of dependent steps: one launch, the CTAs of one cluster
-// with their counts in shared memory, no pass through global memory between.
+// with their counts in shared memory, no pass through global memory between (512
+// rows of 128 groups 3.4 us).  Many rows are bound by the shared-memory wavefronts
+// of the counters that a step's rows hit, some 40 a step of 32 rows (131072 rows
+// 9.9 us).
 //
 // The rows are cut into equal runs, in order, one a warp, with a counter of its
 // own for each group.  The first pass counts; then the counters become places (the
