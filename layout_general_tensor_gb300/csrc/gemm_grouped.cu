@@ -29,8 +29,8 @@
 // few rows and many weights then meet at the end: 4000 rows of 24 groups, 3000 x
 // 2880, 85 to 88 us, and 16384 rows of 16 groups no better.)
 //
-// Where the tiles are too few for the SMs, the CTAs of a cluster take a stretch of
-// K each (SPLIT): each leaves its fp32 sums in its shared memory, and each adds and
+// Where the tiles are too few for the SMs, the 2 to 8 CTAs of a cluster take a stretch
+// of K each (SPLIT): each leaves its fp32 sums in its shared memory, and each adds and
 // stores a share of the columns, in the CTAs' order (6 rows of one group, 632 x
 // 2048: 12.2 to 7.2 us; 3302 rows along K, 192 x 168: 19.6 to 10.9).
 //
@@ -77,9 +77,14 @@ constexpr uint32_t kGgRows = 128;                       // M-side rows a CTA
 constexpr uint32_t kGgPBytes = kGgRows * TILE_K * 2;    // 16 KiB of them a stage
 constexpr uint32_t kGgChunk = 64 * TILE_K * 2;          // a box of 64 x 64 values along n or m
 constexpr uint32_t kGgMost = 256;                       // N-side columns of a tile
+// Rows of A in a copy: a tile's are as many copies as it has rows for, since a tile
+// much narrower than the widest is the usual one (5266 rows of 69 groups, 3976 x
+// 1144: 128 us with copies of 64 rows, 123 of 32, against 186 with one for the widest).
+constexpr uint32_t kGgPiece = 32;
 constexpr uint32_t kGgMaxStages = 12;
 constexpr uint32_t kGgEpiBytes = 2 * 2 * 8192;          // 32 rows of C, 128 values each, of two sets of warps, twice
 constexpr uint32_t kGgStep = 16 * 128;                  // a step's 16 rows of 64 values along n or m
+constexpr uint32_t kGgMaxSplit = 8;                     // CTAs that share a tile's K
 constexpr uint32_t kGgRests = 2;                        // buffers for what is left behind a group's last whole step
 constexpr uint32_t kGgBars = 2 * kGgMaxStages + 3 * kGgRests + 5;  // full, empty; rest landed, cleared, empty; accumulators full, empty; end
 constexpr uint32_t kGgSmem = 227 * 1024;
@@ -99,7 +104,7 @@ struct GroupedArgs {
   int32_t kb_total;       // blocks of K (along M)
   uint32_t p_tiles, q_most;
   uint32_t q_tiles, q_width;  // along K
-  uint32_t q_box;             // along M: rows of an N-side copy, of each CTA
+  uint32_t q_box;             // columns of an N-side copy
   uint32_t q_chunks;          // along K: stretches of 64 columns, of each CTA
   uint32_t p_boxes, q_boxes;  // copies of a stage's operand
   int32_t p_whole, q_whole;   // the one copy is of several stretches
@@ -291,14 +296,14 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       const CUtensorMap* tm_rest = is_p ? &a.tm_pr : &a.tm_qr;
       const uint32_t at = is_p ? 0u : kGgPBytes;
       const uint32_t chunks = is_p ? 2u : a.q_chunks;
-      const uint32_t bytes = is_p ? kGgPBytes : a.along_k ? a.q_chunks * kGgChunk : a.q_box * TILE_K * 2;
-      const uint32_t boxes = is_p ? a.p_boxes : a.q_boxes;
+      const uint32_t box = is_p ? 64u : a.q_box;
+      uint32_t bytes = is_p ? kGgPBytes : a.q_chunks * kGgChunk, boxes = is_p ? a.p_boxes : a.q_boxes;
       // coordinates: whether the box runs along K first; whether it is all of the stage's stretches
       const bool k_first = is_p ? !a.p_mn : !a.along_k, whole = is_p ? a.p_whole : a.q_whole;
       auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t apart, uint32_t bar, int32_t x0, int32_t k, int32_t z) {
         const int32_t stretch = whole ? x0 >> 6 : 0;
         for (uint32_t j = odd; j < boxes; j += 2) {
-          const int32_t x = whole ? 0 : x0 + static_cast<int32_t>(64 * j);
+          const int32_t x = whole ? 0 : x0 + static_cast<int32_t>(box * j);
           if constexpr (PAIR)
             tma_load_4d_pair(dst + j * apart, map, bar, k_first ? k : x, k_first ? x : k, stretch, z);
           else
@@ -311,6 +316,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         const int32_t x0 = is_p ? t.p0 + static_cast<int32_t>(rank * kGgRows)
                                 : t.q0 + static_cast<int32_t>(rank * (t.cols / CTAS));
         const int32_t z = is_p && !a.along_k ? t.group : 0;
+        if (!is_p && !a.along_k) {  // (as many rows as the tile has)
+          boxes = (t.cols / CTAS + box - 1) / box;
+          bytes = boxes * box * (TILE_K * 2);
+        }
         const int32_t k0 = (a.along_k ? t.row0 : 0) + t.kb0 * TILE_K;
         if (t.rest > 0) {
           const uint32_t b = rests % kGgRests;
@@ -324,7 +333,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
           if (!(ok = wait(empty(s), phase ^ 1u))) break;
           if (leader && !odd) mbar_arrive_expect_tx(full(s), bytes * CTAS);
           if (!(a.withhold && !is_p && blockIdx.x == 0 && issued == 0))
-            copy(tm, base + s * a.stage_bytes + at, kGgChunk, full_lead + 8u * s, x0, k0 + kb * TILE_K, z);
+            copy(tm, base + s * a.stage_bytes + at, box * (TILE_K * 2), full_lead + 8u * s, x0, k0 + kb * TILE_K, z);
           ++issued;
           if (++s == a.stages) {
             s = 0;
@@ -595,6 +604,25 @@ cudaError_t launch_grouped(const GroupedArgs& a, bool pair, unsigned workers, cu
                        : launch_grouped_as<false, false, BF16>(a, workers, stream);
 }
 
+// Clusters of `ctas` CTAs of the split form that run at once on this device; below 0: an error.
+template <bool BF16>
+int resident_split_clusters(unsigned ctas) {
+  constexpr auto kernel = grouped_kernel<false, true, BF16>;
+  if (set_smem_once<kernel>(static_cast<int>(kGgSmem)) != cudaSuccess) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kGgThreads);
+  cfg.dynamicSmemBytes = kGgSmem;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  return cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess ? clusters : -1;
+}
+
 // A matrix [d2][d1][d0] with pitches s1 and s2 in elements, by boxes of 64 of d0
 // times box1 of d1.  `stretches` > 1 of them, next to each other along d0, are one
 // box, one after the other in shared memory: d0 in pieces of 64 is a dimension of
@@ -633,6 +661,7 @@ struct gemm_grouped_plan {
   gemm_grouped_desc_t d;
   int device = -1;
   int sms = 0;
+  int resident[lgt::kGgMaxSplit + 1] = {};  // clusters of so many CTAs (SPLIT) that run at once
   lgt::DeviceStatus* d_status = nullptr;
   uint64_t wait_limit_ns = 0;
   int withhold_armed = 0;  // gemm_grouped_withhold_load: the next run withholds a load (one shot)
@@ -665,6 +694,15 @@ gemm_status_t gemm_grouped_create(const gemm_grouped_desc_t* desc, gemm_grouped_
     if (p->d_status) cudaFree(p->d_status);
     delete p;
     return GEMM_ERR_CUDA;
+  }
+  for (unsigned c = 2; p->device >= 0 && c <= lgt::kGgMaxSplit; ++c) {
+    p->resident[c] = d.dtype == GEMM_BF16 ? lgt::resident_split_clusters<true>(c) : lgt::resident_split_clusters<false>(c);
+    if (p->resident[c] < 0) {
+      cudaGetLastError();
+      cudaFree(p->d_status);
+      delete p;
+      return GEMM_ERR_CUDA;
+    }
   }
   *plan = p;
   return GEMM_OK;
@@ -717,15 +755,19 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   uint32_t narrow = kGgMost;
   for (uint32_t w : {128u, 64u, 32u, 16u})
     if (2 * mean <= static_cast<int64_t>(w)) narrow = w;
-  // Tiles of single CTAs, and blocks of K of each: where a cluster for each tile
-  // leaves no SM twice the work, and the blocks that a CTA then does not do are worth
-  // the exchange (a block 0.25 us, the exchange 2.5), K is split.
-  const int64_t single = (along_k ? static_cast<int64_t>(d.groups) * ((d.M + kGgMost - 1) / kGgMost) : rows / narrow + busy) *
+  // Tiles of single CTAs (along M a guess between their least and greatest number,
+  // since the sizes are not known here), and blocks of K of each: where clusters for all of them
+  // run at once, and the blocks that a CTA then does not do are worth the exchange (a
+  // block 0.25 us, the exchange 2.5), K is split, over as many CTAs as that allows (428
+  // rows of 4 groups, 952 x 5672: four 19.5 us, two 28, none 33.7; 3881 of 10, 2176 x
+  // 920, 340 tiles: none 24.6, two 66).
+  const int64_t single = (along_k ? static_cast<int64_t>(d.groups) * ((d.M + kGgMost - 1) / kGgMost)
+                                  : std::min(rows / narrow + busy, std::max(busy + busy / 8, rows / narrow + (busy + 3) / 2))) *
                          ((d.N + kGgRows - 1) / kGgRows);
   const int64_t deep = (along_k ? mean : d.K) / TILE_K;
   a.split = 1;
-  for (uint32_t c : {2u, 4u, 8u})  // (an SM group holds whole clusters of 8 only)
-    if (single * c * 16 <= plan->sms * (c == 8 ? 12 : 15) && deep * (c - 1) >= 10 * c) a.split = c;
+  for (uint32_t c = 2; c <= kGgMaxSplit; ++c)
+    if (single <= plan->resident[c] && deep * (c - 1) >= 10 * c) a.split = c;
   const bool pair = a.split == 1 && d.N > kGgRows && (along_k ? d.M > 64 : mean > 96);
   const uint32_t ctas = pair ? 2 : 1, step = pair ? 32 : 16;
   a.p_tiles = static_cast<uint32_t>((d.N + kGgRows * ctas - 1) / (kGgRows * ctas));
@@ -743,12 +785,14 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     a.q_most = a.q_width;
     a.q_chunks = (a.q_width / ctas + 63) / 64;
     if (!q_whole) a.q_boxes = a.q_chunks;
+    a.q_box = 64;
     a.stage_bytes = kGgPBytes + a.q_chunks * kGgChunk;
     tiles = static_cast<int64_t>(d.groups) * a.p_tiles * a.q_tiles;
   } else {
     a.q_most = pair ? kGgMost : narrow;
-    a.q_box = a.q_most / ctas;
-    a.stage_bytes = kGgPBytes + a.q_box * TILE_K * 2;
+    a.q_box = std::min(a.q_most / ctas, kGgPiece);
+    a.q_boxes = a.q_most / ctas / a.q_box;
+    a.stage_bytes = kGgPBytes + a.q_most / ctas * TILE_K * 2;
     tiles = (rows / a.q_most + busy) * a.p_tiles;
   }
   if (tiles >= (int64_t{1} << 31)) return GEMM_ERR_UNSUPPORTED;
