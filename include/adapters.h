@@ -45,6 +45,8 @@ typedef struct gemm_adapters_plan gemm_adapters_plan_t;
  * LGT_GEMM_ADAPTERS_FORM in the environment, for tests and measurements: the form
  * that the plan's runs take where the sizes allow it, 0 the one for few rows, 1, 2,
  * 4, 8 the one for many rows with so many CTAs a tile.
+ * LGT_GEMM_ADAPTERS_ROWS, likewise: 8, 16 or 32 rows a tile of the form for few rows
+ * (16 for ranks up to 64, 32 up to 32 and from 72).
  * GEMM_ERR_INVALID_ARG, GEMM_ERR_CUDA. */
 gemm_status_t gemm_adapters_create(const gemm_adapters_desc_t* desc, gemm_adapters_plan_t** plan);
 

@@ -7,7 +7,7 @@
 // that (16384 rows, K = N = 4096, rank 64: 76 us, 79 % of a copy's rate).  Few are a
 // chain of trips to memory, one after the other: offsets, order, rows, the joins of
 // u, results (one row 5.8 us, 60 rows of 60 adapters 8.0, 801 rows of 13 and 198 of
-// none, 3000 x 2880, 14.1).
+// none, 3000 x 2880, 10.2).
 //
 // For few rows (for many: adapters_tc_kernel below) a tile is up to 8 NT rows of one
 // group, done by a cluster of 1 to 8 CTAs:
@@ -24,6 +24,7 @@
 // 32 are dealt to the instruction's 8-sides so that a lane ends up with eight
 // neighbours of a row: base and out move in 16-byte pieces.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <new>
@@ -908,9 +909,15 @@ cudaError_t launch_adapters_as(const AdapterArgs& a, unsigned clusters, cudaStre
                             a.ctas, a);
 }
 
+// (nt: as gemm_adapters_run chooses them)
 template <int MT, bool BF16>
 cudaError_t launch_adapters_mt(const AdapterArgs& a, int nt, unsigned clusters, cudaStream_t stream) {
-  return nt == 1 ? launch_adapters_as<MT, 1, BF16>(a, clusters, stream) : launch_adapters_as<MT, 4, BF16>(a, clusters, stream);
+  if (nt == 1) return launch_adapters_as<MT, 1, BF16>(a, clusters, stream);
+  if constexpr (MT <= 4)
+    if (nt == 2) return launch_adapters_as<MT, 2, BF16>(a, clusters, stream);
+  if constexpr (MT != 4)
+    if (nt == 4) return launch_adapters_as<MT, 4, BF16>(a, clusters, stream);
+  return cudaErrorInvalidValue;
 }
 
 template <bool BF16>
@@ -993,6 +1000,7 @@ struct gemm_adapters_plan {
   int device = -1;
   int sms = 0;
   int resident[4] = {0, 0, 0, 0};  // clusters of 1, 2, 4, 8 CTAs of the form for many rows that run at once
+  int tile_rows = 0;  // LGT_GEMM_ADAPTERS_ROWS: rows of a tile of the form for few rows
   int form = -1;  // LGT_GEMM_ADAPTERS_FORM: 0 the first form, 1, 2, 4, 8 the one for many rows with that many CTAs a tile
   lgt::DeviceStatus* d_status = nullptr;
   uint64_t wait_limit_ns = 0;
@@ -1014,6 +1022,12 @@ gemm_status_t gemm_adapters_create(const gemm_adapters_desc_t* desc, gemm_adapte
   if (!p) return GEMM_ERR_CUDA;
   p->d = d;
   p->wait_limit_ns = lgt::adapters_wait_limit();
+  if (const char* rows = std::getenv("LGT_GEMM_ADAPTERS_ROWS"); rows && *rows) {
+    p->tile_rows = std::atoi(rows);
+    if ((d.rank > 64 && p->tile_rows == 16) || (d.rank > 32 && d.rank <= 64 && p->tile_rows == 32) ||
+        (p->tile_rows != 8 && p->tile_rows != 16 && p->tile_rows != 32))
+      p->tile_rows = 0;
+  }
   if (const char* form = std::getenv("LGT_GEMM_ADAPTERS_FORM"); form && *form) p->form = std::atoi(form);
   if (cudaGetDevice(&p->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
@@ -1089,25 +1103,53 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
   const bool bf16 = d.dtype == GEMM_BF16;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // The two forms' times, in us, from their rounds of tiles (measured at K = N =
-  // 4096; the sizes of the groups are not known here, and half a tile of each is
-  // counted as empty).
-  // The first: a CTA's share of a tile of 32 rows takes 34 us at two CTAs an SM and
-  // ranks up to 16, 1.2, 2.4 and 4.3 times that up to 32, 64, 128.
-  const int nt = rows > 8 * busy ? 4 : 1;
-  const int64_t tiles = rows / (8 * nt) + busy + 1;  // (at most, those of rows of no group among them)
-  // A cluster as large as leaves every SM two CTAs, or what there is to share.
-  while (a.ctas < kAdMaxCluster && tiles * a.ctas <= sms && std::max(d.N, d.K) >= static_cast<int64_t>(a.ctas) * 512) a.ctas *= 2;
+  // 4096).  The sizes of the groups are not known here: as many of them have rows as
+  // if every row had chosen one by itself, and half a tile of each is counted as empty
+  // (834 rows of 54 groups, rank 88, 2536 x 1832, in the first form 24 us, with four
+  // CTAs a tile, which 35 tiles would allow, 50).
+  // The form for few rows: a CTA by itself takes so long for a tile with two on an SM
+  // (but 1 us), 3/4 of that with one; a cluster its share, and 0.3 us a CTA for the joins.  4 us (8
+  // above a rank of 64) come to it.  Small tiles read the group's matrices more often,
+  // from L2, but there are more of them (64 rows of 4 groups, rank 64: 8 rows a tile 8.9
+  // us, 16 10.7; 4096 rows of 100, rank 24: 47, 33, 32 rows a tile 51).  0: no such
+  // kernel, since it was nowhere the fastest.
+  static constexpr double kTileUs[4][3] = {{12.5, 21.0, 38.0}, {20.0, 27.0, 52.0}, {29.0, 50.0, 0.0}, {60.0, 0.0, 68.0}};
+  const int mt = d.rank <= 16 ? 0 : d.rank <= 32 ? 1 : d.rank <= 64 ? 2 : 3;
+  const double with_rows = d.groups * (1.0 - std::exp(-static_cast<double>(rows) / d.groups));
+  auto tiles_of = [&](int64_t height) {
+    return static_cast<int64_t>(std::max(with_rows, static_cast<double>(rows) / static_cast<double>(height) + with_rows / 2) + 0.5);
+  };
   const double row_bytes = 2.0 * static_cast<double>(d.K + 2 * d.N), scale = row_bytes / (2.0 * 3 * 4096);
-  const double by_rank = d.rank <= 16 ? 1.0 : d.rank <= 32 ? 1.2 : d.rank <= 64 ? 2.4 : 4.3;
-  const double small_us = 8.0 + static_cast<double>((tiles * a.ctas + 2 * sms - 1) / (2 * sms)) * 34.0 * scale * by_rank / a.ctas;
+  int nt = 1;
+  double best_us = 1e30;
+  for (int i = 2; i >= 0; --i) {
+    if (kTileUs[mt][i] == 0.0 || (plan->tile_rows > 0 && plan->tile_rows != 8 << i)) continue;
+    const int on_sm = i == 2 && mt == 3 ? 1 : 2;
+    for (int lg = 0; lg < 4 && (lg == 0 || std::max(d.N, d.K) >= int64_t{256} << lg); ++lg) {
+      // (as many clusters run at once as of the other form, on each CTA that an SM has room for)
+      const double clusters = static_cast<double>(tiles_of(8 << i)), rounds = clusters / (on_sm * plan->resident[lg]);
+      if (lg > 0 && rounds > 1.0) break;
+      double tile_us = std::max(1.0, kTileUs[mt][i] * scale / (1 << lg));
+      if (rounds > 1.0)
+        tile_us *= (std::ceil(rounds - 0.05) + 1.1 * rounds) / 2;
+      else if (on_sm == 2 && clusters * (1 << lg) <= sms)
+        tile_us *= 0.75;
+      const double us = (mt == 3 ? 8.0 : 4.0) + (lg > 0 ? 0.3 * (1 << lg) : 0.0) + tile_us;
+      if (us < best_us) {
+        best_us = us;
+        nt = 1 << i;
+        a.ctas = 1u << lg;
+      }
+    }
+  }
+  const int64_t tiles = rows / (8 * nt) + busy + 1;  // (at most, those of rows of no group among them)
   // The form for many rows: an SM moves 60 bytes a ns (45 where it gathers), all of
   // them together 6.1 TB/s, and the exchange of parts takes 3 us and 0.1 us x CTAs^2
   // for every 16 of the rank.
-  const int64_t rank16 = (d.rank + 15) / 16, large_tiles = (2 * rows / kAtcRows + busy + 1) / 2 + 1;
+  const int64_t rank16 = (d.rank + 15) / 16, large_tiles = tiles_of(kAtcRows);
   const double all_us = static_cast<double>(rows) * row_bytes / 6.1e6;
   int lg = -1;
-  double best_us = small_us;
-  for (int i = 0; i < 4 && (nt > 1 || plan->form > 0); ++i) {
+  for (int i = 0; i < 4 && (rows > 8 * busy || plan->form > 0); ++i) {
     const int64_t at_once = plan->resident[i];
     if (at_once < 1 || d.K < static_cast<int64_t>(TILE_K) << i || d.N < int64_t{128} << i) break;
     const double tile_us = kAtcRows * row_bytes / (order ? 45e3 : 60e3) / (1 << i) + (i > 0 ? 0.1 * static_cast<double>(rank16 << (2 * i)) : 0.0);

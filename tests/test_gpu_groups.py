@@ -279,6 +279,19 @@ def test_adapters_many_rows(m, sizes, none, n, k, rank):
     _check_adapters(m, sizes, none, n, k, rank, "bf16" if i % 2 else "f16", order=i % 3 > 0, seed=i)
 
 
+# (every height of a tile of the form for few rows that there is, alone and in clusters: those of few tiles)
+@pytest.mark.parametrize("sizes,none", [([1], 0), ([17, 0, 33, 8], 5), ([700, 300], 0), ([9] * 150, 50), ([5000, 1], 31)],
+                         ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("height,n,k,rank", [(h, n, k, rank) for n, k, rank in ((136, 72, 16), (1000, 2056, 24), (4096, 512, 64), (264, 1032, 128))
+                                             for h in (8, 16, 32) if (rank, h) not in ((64, 32), (128, 16))])
+def test_adapters_heights(m, height, sizes, none, n, k, rank, monkeypatch):
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", "0")
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_ROWS", str(height))
+    i = len(sizes) + height // 8 + rank // 8
+    _check_adapters(m, sizes, none, n, k, rank, "bf16" if i % 2 else "f16", order=i % 3 > 0, scaled=i % 5 > 0, in_place=i % 4 == 0, seed=i)
+    _check_adapters(m, sizes, none, n, k, rank, "f16" if i % 2 else "bf16", ints=False, order=i % 3 == 0, extra=(8, 16, 24), start=11, seed=i + 1)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("rank", [8, 64, 88])
 @pytest.mark.parametrize("form", [0, 1, 4])
