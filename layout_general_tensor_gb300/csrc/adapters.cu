@@ -4,7 +4,7 @@
 // Bound: memory.  A row costs K + 2 N values and 2 rank (K + N) multiply-adds, a
 // group its two matrices, so the whole adapter is one pass that keeps the first
 // product's result u on the chip: no workspace, one launch.  Many rows come near
-// that (16384 rows, K = N = 4096, rank 64: 76 us, 79 % of a copy's rate).  Few are a
+// that (16384 rows, K = N = 4096, rank 64: 76 us, 80 % of a copy's rate).  Few are a
 // chain of trips to memory, one after the other: offsets, order, rows, the joins of
 // u, results (one row 5.8 us, 60 rows of 60 adapters 8.0, 801 rows of 13 and 198 of
 // none, 3000 x 2880, 10.2).
@@ -439,6 +439,7 @@ struct AdapterTcArgs {
   DeviceStatus* status;
   uint64_t wait_limit_ns;
   uint32_t rank16, chunks;  // the rank in steps of 16; in stretches of 64
+  uint32_t height;  // a tile's rows at most, a multiple of 16
   uint32_t stages, stage_bytes;
   uint32_t region, parts;  // bytes of the ring, and then of u, B and this CTA's part of u, which begins at `parts`
   uint32_t idesc_u, idesc_out;  // the second without N
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   pdl_wait();
   group_rows<kAtcThreads>(a.offsets, a.groups, a.rows, off, scratch);
   __syncthreads();
-  group_tiles<kAtcThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + kAtcRows - 1) / kAtcRows; }, first, scratch + 32);
+  group_tiles<kAtcThreads>(a.groups, [&](uint32_t g) { return (off[g + 1] - off[g] + t.height - 1) / t.height; }, first, scratch + 32);
   tc_fence_before();
   __syncthreads();
   if constexpr (SHARED) cluster_sync_all();
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
   auto tile_at = [&](uint32_t i) {
     Tile w;
     w.g = group_of(first, a.groups, i);
-    const uint32_t len = off[w.g + 1] - off[w.g], n = (len + kAtcRows - 1) / kAtcRows;
+    const uint32_t len = off[w.g + 1] - off[w.g], n = (len + t.height - 1) / t.height;
     const uint32_t width = ((len + n - 1) / n + 15) & ~15u;
     w.at = off[w.g] + (i - first[w.g]) * width;
     w.count = min(width, off[w.g + 1] - w.at);
@@ -578,25 +579,27 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(rows_full(it & 1));
       if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
+      // (by fours as far as the tile has rows, or all of a box)
+      const uint32_t fours = (w.count + 3) / 4, load_bytes = (a.order ? fours * 512 : t.height * 128) + t.rank16 * 16 * 128;
       if (elect_one()) {
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait(empty(s), phase ^ 1u))) break;
           const uint32_t dst = base + s * t.stage_bytes;
           if (warp == 0) {
-            mbar_arrive_expect_tx(full(s), t.stage_bytes);
+            mbar_arrive_expect_tx(full(s), load_bytes);
             if (!(t.withhold && blockIdx.x == 0 && issued == 0))
               tma_load_3d(dst + kAtcTile, &t.tm_a, full(s), kb * TILE_K, 0, static_cast<int32_t>(w.g));
           }
           if (a.order) {
 #pragma unroll 4
-            for (int j = 0; j < 8; ++j) {
-              int4 r = *reinterpret_cast<const int4*>(rows + warp * 32 + 4 * j);
+            for (uint32_t j = warp; j < fours; j += kAtcMmaWarp) {
+              int4 r = *reinterpret_cast<const int4*>(rows + 4 * j);
               // (a row past the last gives zeros)
               r.x = r.x < 0 ? a.rows : r.x;
               r.y = r.y < 0 ? a.rows : r.y;
               r.z = r.z < 0 ? a.rows : r.z;
               r.w = r.w < 0 ? a.rows : r.w;
-              tma_gather4(dst + (warp * 32 + 4 * j) * 128, &t.tm_x, full(s), kb * TILE_K, r);
+              tma_gather4(dst + j * 512, &t.tm_x, full(s), kb * TILE_K, r);
             }
           } else if (warp == 0) {
             tma_load_2d(dst, &t.tm_x, full(s), kb * TILE_K, static_cast<int32_t>(w.at));
@@ -1143,20 +1146,35 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
     }
   }
   const int64_t tiles = rows / (8 * nt) + busy + 1;  // (at most, those of rows of no group among them)
-  // The form for many rows: an SM moves 60 bytes a ns (45 where it gathers), all of
-  // them together 6.1 TB/s, and the exchange of parts takes 3 us and 0.1 us x CTAs^2
-  // for every 16 of the rank.
-  const int64_t rank16 = (d.rank + 15) / 16, large_tiles = tiles_of(kAtcRows);
+  // The form for many rows: an SM moves 60 bytes a ns (45 where it gathers), a tile's
+  // ends are as long as 16 rows, all SMs together move 6.1 TB/s, and the exchange of
+  // parts takes 3 us and 0.1 us x CTAs^2 for every 16 of the rank.
+  const int64_t rank16 = (d.rank + 15) / 16;
   const double all_us = static_cast<double>(rows) * row_bytes / 6.1e6;
   int lg = -1;
+  uint32_t height = kAtcRows;
   for (int i = 0; i < 4 && (rows > 8 * busy || plan->form > 0); ++i) {
     const int64_t at_once = plan->resident[i];
     if (at_once < 1 || d.K < static_cast<int64_t>(TILE_K) << i || d.N < int64_t{128} << i) break;
-    const double tile_us = kAtcRows * row_bytes / (order ? 45e3 : 60e3) / (1 << i) + (i > 0 ? 0.1 * static_cast<double>(rank16 << (2 * i)) : 0.0);
-    const double us = (i > 0 ? 12.0 : 9.0) + std::max(all_us, static_cast<double>((large_tiles + at_once - 1) / at_once) * tile_us);
+    // Tiles as high as fill the last round best (a round is bound by what one SM moves:
+    // 16384 rows of 8 groups, rank 64, in 132 tiles of 128 rows 77 us, in 150 of 112 75.8;
+    // 12000 of 6 in 108 of 128 68.8, in 138 of 96 63.8).
+    uint32_t h = kAtcRows;
+    int64_t rounds = 0, least = 0;
+    for (uint32_t x = kAtcRows; x >= 64; x -= 16) {
+      const int64_t r = (tiles_of(x) + static_cast<int64_t>(std::sqrt(with_rows / 3)) + at_once - 1) / at_once, cost = r * (x + 16);
+      if (x == kAtcRows || cost < least) {
+        least = cost;
+        rounds = r;
+        h = x;
+      }
+    }
+    const double tile_us = (h + 16) * row_bytes / (order ? 45e3 : 60e3) / (1 << i) + (i > 0 ? 0.1 * static_cast<double>(rank16 << (2 * i)) : 0.0);
+    const double us = (i > 0 ? 12.0 : 9.0) + std::max(all_us, static_cast<double>(rounds) * tile_us);
     if (plan->form < 0 ? us < best_us : plan->form == 1 << i) {
       best_us = us;
       lg = i;
+      height = h;
     }
   }
   if (lg >= 0) a.ctas = 1;
@@ -1169,6 +1187,7 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
     t.wait_limit_ns = plan->wait_limit_ns + static_cast<uint64_t>(d.K / TILE_K + d.N / 128) * 4000;
     t.rank16 = static_cast<uint32_t>(rank16);
     t.chunks = (t.rank16 + 3) / 4;
+    t.height = height;
     t.stage_bytes = kAtcTile + t.rank16 * 16 * 128;
     const uint32_t tables = kAtcBars * 8 + 1544 + 256 + 8 * static_cast<uint32_t>(d.groups + 1);
     t.stages = std::min<uint32_t>(kAtcMaxStages, (kAtcSmem - 1024 - kAtcStaging - tables) / t.stage_bytes);
@@ -1178,12 +1197,12 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
     t.idesc_u = idesc_f16(bf16, 0u, 0u, kAtcRows, t.rank16 * 16);
     t.idesc_out = idesc_f16(bf16, 0u, 0u, kAtcRows, 0u);
     t.withhold = plan->withhold_armed ? __atomic_exchange_n(&plan->withhold_armed, 0, __ATOMIC_ACQ_REL) : 0;
-    if (!encode_x(&t.tm_x, x, bf16, d.K, rows, x_stride, order ? 1 : kAtcRows) ||
+    if (!encode_x(&t.tm_x, x, bf16, d.K, rows, x_stride, order ? 1 : height) ||
         !encode_dense(&t.tm_a, A, bf16, d.K, d.rank, d.groups, t.rank16 * 16) ||
         !encode_dense(&t.tm_b, B, bf16, d.rank, d.N, d.groups, 128))
       return GEMM_ERR_CUDA;
     t.p.ctas = 1u << lg;
-    const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(rows / kAtcRows + busy + 1, plan->resident[lg]));
+    const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(rows / height + busy + 1, plan->resident[lg]));
     e = bf16 ? launch_adapters_tc<true>(t, clusters, s) : launch_adapters_tc<false>(t, clusters, s);
   } else {
     const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * sms / a.ctas));
