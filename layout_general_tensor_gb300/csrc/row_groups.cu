@@ -3,9 +3,7 @@
 // Bound: latency.  A row costs 12 bytes (131072 rows: 0.2 us of memory), so what
 // counts is the number of dependent steps: one launch, the CTAs of one cluster
 // with their counts in shared memory, no pass through global memory between (512
-// rows of 128 groups 3.4 us).  Many rows are bound by the shared-memory wavefronts
-// of the counters that a step's rows hit, some 40 a step of 32 rows (131072 rows
-// 9.9 us).
+// rows of 128 groups 3.4 us).
 //
 // The rows are cut into equal runs, in order, one a warp, with a counter of its
 // own for each group.  The first pass counts; then the counters become places (the
@@ -15,6 +13,13 @@
 // below its own.  (Found by the match instruction instead, 131072 rows of 128
 // groups took 33 us on 8 CTAs; by a vote on each bit of the number, with twice the
 // warps, 9.8 us on 16 against 9.9, but 6.2 against 5.7 for 4096 rows.)
+//
+// A step of the second pass is some 40 wavefronts of shared memory, one of the first
+// a fifth of that.  So where a warp has several steps, up to eight clusters do the
+// whole first pass each, and each only its part of every run in the second: they need
+// nothing of one another (131072 rows of 128 groups, one cluster 10.1 us, two 7.7,
+// six 5.9; 4096 rows 6.0, eight 4.2).
+#include <algorithm>
 #include <cstdint>
 
 #include "groups.cuh"
@@ -35,6 +40,8 @@ struct RowGroupArgs {
   const int32_t* ids;
   int32_t *offsets, *order, *places;
   uint32_t rows, run;  // run: rows of a warp, a multiple of 32
+  uint32_t lg_ctas;  // of a cluster
+  uint32_t part;     // rows of a run that a cluster puts in place
   int32_t groups;
 };
 
@@ -62,6 +69,8 @@ __device__ __forceinline__ void load_batch(const RowGroupArgs& a, uint32_t first
   }
 }
 
+// PARTS: several clusters (one does not pay for them: 512 rows 3.1 us, 3.4).
+template <bool PARTS>
 __global__ void __launch_bounds__(kRgThreads, 1) row_groups_kernel(const RowGroupArgs a) {
   pdl_launch_dependents();
   extern __shared__ __align__(8) uint8_t rg_smem[];
@@ -70,7 +79,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) row_groups_kernel(const RowGrou
   __shared__ uint32_t scratch[16];
   const int bins = a.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
+  const uint32_t rank = cluster_ctarank(), ctas = 1u << a.lg_ctas;
   Bin* bin = reinterpret_cast<Bin*>(rg_smem);  // [warp][bins]
   Bin* mine = bin + warp * bins;
   for (int i = lane; i < bins; i += 32) mine[i] = Bin{0u, 0u};
@@ -78,18 +87,23 @@ __global__ void __launch_bounds__(kRgThreads, 1) row_groups_kernel(const RowGrou
   pdl_wait();
   const uint32_t first = (rank * kRgWarps + warp) * a.run;
   const uint32_t end = first < a.rows ? min(a.run, a.rows - first) : 0u;
+  // this cluster's part of the run
+  const uint32_t from = PARTS ? (blockIdx.x >> a.lg_ctas) * a.part : 0u, to = PARTS ? min(end, from + a.part) : end;
   int32_t id[kRgBatch];
   for (uint32_t i = 0; i < end; i += 32 * kRgBatch) {
     load_batch(a, first, i, end, id);
 #pragma unroll
     for (uint32_t j = 0; j < kRgBatch; ++j)
-      if (i + 32 * j + lane < end) atomicAdd(&mine[bin_of(a, id[j])].count, 1u);
+      if (i + 32 * j + lane < end) {
+        Bin* at = mine + bin_of(a, id[j]);
+        atomicAdd(PARTS && i + 32 * j < from ? &at->lanes : &at->count, 1u);
+      }
   }
   __syncthreads();
   for (int b = threadIdx.x; b < bins; b += kRgThreads) {
     uint32_t s = 0;
 #pragma unroll
-    for (int w = 0; w < kRgWarps; ++w) s += bin[w * bins + b].count;
+    for (int w = 0; w < kRgWarps; ++w) s += bin[w * bins + b].count + (PARTS ? bin[w * bins + b].lanes : 0u);
     total[b] = s;
   }
   cluster_sync_all();
@@ -111,25 +125,29 @@ __global__ void __launch_bounds__(kRgThreads, 1) row_groups_kernel(const RowGrou
   __syncthreads();
   // The warps' counters become the places of their first rows.
   for (int b = threadIdx.x; b < bins; b += kRgThreads) {
-    if (rank == 0) a.offsets[b] = static_cast<int32_t>(first_of[b]);
-    uint32_t at = first_of[b] + before[b], n[kRgWarps];
+    if (blockIdx.x == 0) a.offsets[b] = static_cast<int32_t>(first_of[b]);
+    uint32_t at = first_of[b] + before[b];
+    Bin n[kRgWarps];
 #pragma unroll
-    for (int w = 0; w < kRgWarps; ++w) n[w] = bin[w * bins + b].count;
+    for (int w = 0; w < kRgWarps; ++w) n[w] = Bin{PARTS ? bin[w * bins + b].lanes : 0u, bin[w * bins + b].count};
 #pragma unroll
     for (int w = 0; w < kRgWarps; ++w) {
-      bin[w * bins + b].count = at;
-      at += n[w];
+      bin[w * bins + b].count = at + n[w].lanes;
+      if (PARTS) bin[w * bins + b].lanes = 0u;
+      at += n[w].lanes + n[w].count;
     }
   }
   cluster_sync_all();  // (the totals have been read; a CTA leaves its shared memory to no one before)
   const uint32_t below = (1u << lane) - 1u;
-  for (uint32_t i = 0; i < end; i += 32 * kRgBatch) {
-    if (a.run > 32 * kRgBatch) load_batch(a, first, i, end, id);  // (else they are still here)
+  const bool again = a.run > 32 * kRgBatch;  // (else they are still here)
+  for (uint32_t i = again ? from : 0u; i < to; i += 32 * kRgBatch) {
+    if (again) load_batch(a, first, i, to, id);
 #pragma unroll
     for (uint32_t j = 0; j < kRgBatch; ++j) {
-      if (i + 32 * j >= end) break;
+      if (i + 32 * j < from) continue;
+      if (i + 32 * j >= to) break;
       const uint32_t r = i + 32 * j + lane;
-      const bool live = r < end;
+      const bool live = r < to;
       Bin* at = mine + bin_of(a, id[j]);
       if (live) atomicOr(&at->lanes, 1u << lane);
       __syncwarp();
@@ -145,6 +163,15 @@ __global__ void __launch_bounds__(kRgThreads, 1) row_groups_kernel(const RowGrou
       }
     }
   }
+}
+
+template <bool PARTS>
+cudaError_t launch_row_groups(const RowGroupArgs& a, unsigned ctas, unsigned clusters, size_t smem, cudaStream_t stream) {
+  constexpr auto kernel = row_groups_kernel<PARTS>;
+  cudaError_t e = set_smem_once<kernel>(kRgWarps * (kRgMaxGroups + 1) * static_cast<int>(sizeof(Bin)));
+  if (e == cudaSuccess && ctas > 8) e = allow_large_clusters_once<kernel>();
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(kernel, dim3(ctas * clusters), dim3(kRgThreads), smem, stream, ctas, a);
 }
 
 bool overlaps(const void* p, int64_t np, const void* q, int64_t nq) {
@@ -177,16 +204,20 @@ extern "C" gemm_status_t gemm_row_groups(const int32_t* ids, int64_t rows, int32
   a.rows = static_cast<uint32_t>(rows);
   a.groups = groups;
   // as many CTAs as keep every warp at eight steps or fewer, up to a cluster's most
-  unsigned ctas = 1;
-  while (ctas < kRgMaxCluster && rows > static_cast<int64_t>(ctas) * kRgThreads * 8) ctas *= 2;
+  a.lg_ctas = 0;
+  while (1u << a.lg_ctas < kRgMaxCluster && rows > (int64_t{kRgThreads} * 8 << a.lg_ctas)) ++a.lg_ctas;
+  const unsigned ctas = 1u << a.lg_ctas;
   const int64_t warps = static_cast<int64_t>(ctas) * kRgWarps;
   a.run = static_cast<uint32_t>((rows + warps * 32 - 1) / (warps * 32) * 32);
+  // (a GPU's SM groups hold six clusters of 16 at once with room to spare; one that has
+  // to wait for another takes as long again: eight 10.5 us for 131072 rows, six 5.9)
+  const uint32_t steps = a.run / 32, most = ctas > 8 ? 6 : 8, part = std::max(1u, (steps + most - 1) / most);
+  const unsigned clusters = std::max(1u, (steps + part - 1) / part);
+  a.part = part * 32;
   const int smem = kRgWarps * (groups + 1) * static_cast<int>(sizeof(Bin));
-  cudaError_t e = set_smem_once<row_groups_kernel>(kRgWarps * (kRgMaxGroups + 1) * static_cast<int>(sizeof(Bin)));
-  if (e == cudaSuccess && ctas > 8) e = allow_large_clusters_once<row_groups_kernel>();
-  if (e == cudaSuccess)
-    e = launch_pdl_cluster(row_groups_kernel, dim3(ctas), dim3(kRgThreads), static_cast<size_t>(smem),
-                           static_cast<cudaStream_t>(stream), ctas, a);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = clusters > 1 ? launch_row_groups<true>(a, ctas, clusters, static_cast<size_t>(smem), st)
+                                     : launch_row_groups<false>(a, ctas, clusters, static_cast<size_t>(smem), st);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
