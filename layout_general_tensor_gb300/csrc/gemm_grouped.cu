@@ -24,7 +24,9 @@
 // Work.  The sizes are on the device, so every CTA sums them up itself (a scan
 // over the groups' tiles in shared memory) and takes every G-th tile, G the
 // CTAs or pairs: no launch depends on a size.  Within a group the tiles of one
-// stretch of n follow each other, so that they read its weights together.  (Groups
+// stretch of n follow each other, so that they read its weights together, in bands of
+// eight of them, so that those that run at once have no more of the rows between them
+// than the L2 holds (16384 rows of one group, 4096 x 4096: 391 us without, 341).  (Groups
 // with the largest tiles first would leave small ones for the last round, but
 // few rows and many weights then meet at the end: 4000 rows of 24 groups, 3000 x
 // 2880, 85 to 88 us, and 16384 rows of 16 groups no better.)
@@ -80,7 +82,11 @@ constexpr uint32_t kGgMost = 256;                       // N-side columns of a t
 // Rows of A in a copy: a tile's are as many copies as it has rows for, since a tile
 // much narrower than the widest is the usual one (5266 rows of 69 groups, 3976 x
 // 1144: 128 us with copies of 64 rows, 123 of 32, against 186 with one for the widest).
+// From 2048 rows a group on most tiles are full (16384 rows of one group, 4096 x 4096,
+// one after the other: 341 us with copies of 32, 333 of 128).
 constexpr uint32_t kGgPiece = 32;
+constexpr int64_t kGgWideMean = 2048;
+constexpr uint32_t kGgBand = 8;                         // tiles of the N side
 constexpr uint32_t kGgMaxStages = 12;
 constexpr uint32_t kGgEpiBytes = 2 * 2 * 8192;          // 32 rows of C, 128 values each, of two sets of warps, twice
 constexpr uint32_t kGgStep = 16 * 128;                  // a step's 16 rows of 64 values along n or m
@@ -145,16 +151,30 @@ struct GroupedWork {
     step = gridDim.x / ctas;
     end = a.along_k ? static_cast<uint32_t>(a.groups) * a.p_tiles * a.q_tiles : first[a.groups];
   }
+  // Tile r of a group's p_tiles x q_tiles: in bands of the N side, so that those that
+  // run at once read no more of either operand than they have to.
+  __device__ void place(uint32_t r, uint32_t p_tiles, uint32_t q_tiles, uint32_t& p, uint32_t& q) {
+    uint32_t band = 0, high = q_tiles;
+    if (q_tiles > kGgBand) {
+      band = r / (p_tiles * kGgBand);
+      r -= band * (p_tiles * kGgBand);
+      high = min(kGgBand, q_tiles - band * kGgBand);
+    }
+    p = r / high;
+    q = band * kGgBand + r - p * high;
+  }
   __device__ bool next(const GroupedArgs& a, GroupedTile& t) {
     if (tile >= end) return false;
     constexpr uint32_t STEP = GroupedCfg<PAIR>::STEP;
     const uint32_t u = tile;
     tile += step;
     if (a.along_k) {
-      const uint32_t g = u / (a.p_tiles * a.q_tiles), r = u - g * (a.p_tiles * a.q_tiles), p = r / a.q_tiles;
+      const uint32_t g = u / (a.p_tiles * a.q_tiles), r = u - g * (a.p_tiles * a.q_tiles);
+      uint32_t p, q;
+      place(r, a.p_tiles, a.q_tiles, p, q);
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
-      const uint32_t q0 = (r - p * a.q_tiles) * a.q_width, len = off[g + 1] - off[g];
+      const uint32_t q0 = q * a.q_width, len = off[g + 1] - off[g];
       t.q0 = static_cast<int32_t>(q0);
       t.count = min(a.q_width, static_cast<uint32_t>(a.m) - q0);
       t.cols = (t.count + a.q_step - 1) / a.q_step * a.q_step;
@@ -166,11 +186,12 @@ struct GroupedWork {
       const uint32_t r = u - first[g], len = off[g + 1] - off[g];
       const uint32_t tiles = (len + a.q_most - 1) / a.q_most;
       const uint32_t width = ((len + tiles - 1) / tiles + STEP - 1) / STEP * STEP;
-      const uint32_t p = r / tiles, q = (r - p * tiles) * width;
+      uint32_t p, q;
+      place(r, a.p_tiles, tiles, p, q);
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
-      t.q0 = static_cast<int32_t>(off[g] + q);
-      t.count = min(width, len - q);
+      t.q0 = static_cast<int32_t>(off[g] + q * width);
+      t.count = min(width, len - q * width);
       t.cols = (t.count + STEP - 1) / STEP * STEP;
       t.steps = a.kb_total * (TILE_K / 16);  // (the last block's end is zeros)
       t.rest = 0;
@@ -793,7 +814,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     tiles = static_cast<int64_t>(d.groups) * a.p_tiles * a.q_tiles;
   } else {
     a.q_most = pair ? kGgMost : narrow;
-    a.q_box = std::min(a.q_most / ctas, kGgPiece);
+    a.q_box = mean >= kGgWideMean ? a.q_most / ctas : std::min(a.q_most / ctas, kGgPiece);
     a.q_boxes = a.q_most / ctas / a.q_box;
     a.stage_bytes = kGgPBytes + a.q_most / ctas * TILE_K * 2;
     tiles = (rows / a.q_most + busy) * a.p_tiles;
