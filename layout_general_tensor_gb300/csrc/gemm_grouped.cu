@@ -84,7 +84,10 @@ constexpr uint32_t kGgMost = 256;                       // N-side columns of a t
 // 1144: 128 us with copies of 64 rows, 123 of 32, against 186 with one for the widest).
 // From 2048 rows a group on most tiles are full (16384 rows of one group, 4096 x 4096,
 // one after the other: 341 us with copies of 32, 333 of 128).
+// Up to 4, one of half the size does for most (8 rows of 8 groups, 2048 x 4096, where
+// each SM's stream is the limit: 24.1 us, 21.0).
 constexpr uint32_t kGgPiece = 32;
+constexpr int64_t kGgNarrowMean = 4;
 constexpr int64_t kGgWideMean = 2048;
 constexpr uint32_t kGgBand = 8;                         // tiles of the N side
 constexpr uint32_t kGgMaxStages = 12;
@@ -772,10 +775,11 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   GroupedArgs a = {};
   const int64_t busy = std::min<int64_t>(d.groups, std::max<int64_t>(rows, 1));
   const int64_t mean = (rows + busy - 1) / busy;
-  // Few rows a group: tiles as wide as twice the mean, so that most groups have one.
-  uint32_t narrow = kGgMost;
-  for (uint32_t w : {128u, 64u, 32u, 16u})
-    if (2 * mean <= static_cast<int64_t>(w)) narrow = w;
+  // Few rows a group: tiles as wide as twice the mean, so that most groups have one, and
+  // the ring is deep (512 rows of 128 groups, 1536 x 2048: 124 us in tiles of 256), but
+  // no narrower than 64 for the groups that have many (8192 rows in 4 of 512 groups,
+  // 1024 x 2048: 104 us in tiles of 16 to 32, 58 of 64).
+  const uint32_t narrow = 2 * mean <= 64 ? 64 : 2 * mean <= 128 ? 128 : kGgMost;
   // Tiles of single CTAs (along M a guess between their least and greatest number,
   // since the sizes are not known here), and blocks of K of each: where clusters for all of them
   // run at once, and the blocks that a CTA then does not do are worth the exchange (a
@@ -814,7 +818,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     tiles = static_cast<int64_t>(d.groups) * a.p_tiles * a.q_tiles;
   } else {
     a.q_most = pair ? kGgMost : narrow;
-    a.q_box = mean >= kGgWideMean ? a.q_most / ctas : std::min(a.q_most / ctas, kGgPiece);
+    a.q_box = mean >= kGgWideMean ? a.q_most / ctas : mean <= kGgNarrowMean ? kGgPiece / 2 : kGgPiece;
     a.q_boxes = a.q_most / ctas / a.q_box;
     a.stage_bytes = kGgPBytes + a.q_most / ctas * TILE_K * 2;
     tiles = (rows / a.q_most + busy) * a.p_tiles;
