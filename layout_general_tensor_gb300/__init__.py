@@ -837,7 +837,9 @@ class Adapters:
     out[r] = base[r] + scales[g] (x[r] A[g]^T) B[g]^T for the rows r of every group g, base[r] for a row of none.
     x [rows][K], A [groups][rank][K], B [groups][N][rank], base and out [rows][N] (out may be base), offsets and
     order from row_groups over the rows' adapter numbers; without order (None) the rows of a group follow each
-    other.  Rows of x, base and out may be strided; the tensors of a call are on the current device, the one the
+    other.  The gradients are products over the same groups: with rows in order and dout scaled, du = GroupedGemm of
+    dout and B (GEMM_MN_CONTIG), dx of du and A (likewise), dA = GroupedGemmK of du and x, dB of dout and u, which is
+    GroupedGemm of x and A.  Rows of x, base and out may be strided; the tensors of a call are on the current device, the one the
     object was made on.  A graph needs the object that it was captured from (its status word)."""
 
     def __init__(self, groups, N, K, rank, dtype=GEMM_BF16):

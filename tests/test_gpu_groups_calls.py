@@ -167,6 +167,48 @@ def test_gradients(m, k_contig, sizes):
             assert f(a, moved) - f(a, b) == db[g, i, j].double()
 
 
+@pytest.mark.parametrize("sizes", [[5, 0, 40, 1], [130, 300, 0, 77]], ids=["few", "many"])
+@pytest.mark.parametrize("rank", [8, 48])
+def test_adapter_gradients(m, sizes, rank):
+    """The gradients through the adapters are products over groups: f = sum(out * dout), against the formula, and
+    against differences of the adapters' own results.  Sums of at most 136 products of -1, 0
+    and 1 are whole numbers that bf16 holds, those that may be larger are exact in fp32 and rounded once."""
+    t, n, k, groups, rows = torch.bfloat16, 72, 136, len(sizes), sum(sizes)
+    x, dout, base = (_ints(i, rows, c, dtype=t, most=1) for i, c in ((1, k), (2, n), (3, n)))
+    a, b = _ints(4, groups, rank, k, dtype=t, most=1), _ints(5, groups, n, rank, dtype=t, most=1)
+    offsets, at = _offsets(sizes), np.concatenate([[0], np.cumsum(sizes)])
+    u, du, dx = (torch.empty(rows, c, dtype=t, device="cuda") for c in (rank, rank, k))
+    da, db = torch.empty_like(a), torch.empty_like(b)
+    m.GroupedGemm(groups, rank, k).run(x, a, offsets, u)
+    m.GroupedGemm(groups, rank, n, b_layout=m.GEMM_MN_CONTIG).run(dout, b, offsets, du)
+    m.GroupedGemm(groups, k, rank, b_layout=m.GEMM_MN_CONTIG).run(du, a, offsets, dx)
+    m.GroupedGemmK(groups, rank, k).run(du, x, offsets, da)
+    m.GroupedGemmK(groups, n, rank).run(dout, u, offsets, db)
+    for g in range(groups):
+        r = slice(at[g], at[g + 1])
+        ud, dud = x[r].double() @ a[g].double().T, dout[r].double() @ b[g].double()
+        assert torch.equal(u[r], ud.to(t)) and torch.equal(du[r], dud.to(t))
+        assert torch.equal(dx[r], (dud @ a[g].double()).to(t))
+        assert torch.equal(da[g], (dud.T @ x[r].double()).to(t)) and torch.equal(db[g], (dout[r].double().T @ ud).to(t))
+
+    forward = m.Adapters(groups, n, k, rank)
+
+    def f(x, a, b):
+        out = torch.empty_like(base)
+        forward.run(x, a, b, offsets, None, base, out)
+        return out.double()
+    # a step of one value of x: what it changes in its row is exact where bf16 holds both results, below 2^8
+    for r, i in ((0, 0), (rows - 1, k - 1)):
+        moved = x.clone()
+        moved[r, i] += 1
+        lo, hi = f(x, a, b)[r], f(moved, a, b)[r]
+        exact = (lo.abs() < 256) & (hi.abs() < 256)
+        g = next(j for j in range(groups) if at[j] <= r < at[j + 1])
+        step = b[g].double() @ a[g, :, i].double()
+        assert exact.any() and torch.equal((hi - lo)[exact], step[exact])
+        assert dx[r, i] == (dout[r].double() @ step).to(t)
+
+
 # ------------------------------------------------------------------ graphs, streams, repeats
 
 def _operators(m, big):
