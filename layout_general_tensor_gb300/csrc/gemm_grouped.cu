@@ -102,6 +102,7 @@ constexpr uint64_t kGgSettleNs = 200ull * 1000ull * 1000ull;
 struct GroupedArgs {
   CUtensorMap tm_p, tm_q;
   CUtensorMap tm_pr, tm_qr;  // along K: boxes of one step
+  CUtensorMap tm_c;          // boxes of 32 rows of 64 values
   uint16_t* c;
   const int32_t* offsets;
   DeviceStatus* status;
@@ -117,7 +118,9 @@ struct GroupedArgs {
   uint32_t q_chunks;          // along K: stretches of 64 columns, of each CTA
   uint32_t p_boxes, q_boxes;  // copies of a stage's operand
   int32_t p_whole, q_whole;   // the one copy is of several stretches
-  uint32_t q_step;            // along K: what a tile's columns are a multiple of
+  uint32_t q_step;            // along K: what a tile's columns are a multiple of, a power of two
+  uint32_t lg_most;           // along M: of q_most
+  uint32_t recip[kGgBand + 1];  // 2^32 / d, rounded up
   uint32_t stages, stage_bytes;
   uint32_t split;  // CTAs that share a tile's K (SPLIT)
   int32_t p_mn;
@@ -148,49 +151,68 @@ template <bool PAIR, bool SPLIT>
 struct GroupedWork {
   const uint32_t *off, *first;
   uint32_t tile, step, end;
+  // along K: of the next tile, and of a step
+  uint32_t g, r, step_g, step_r;
   __device__ GroupedWork(const GroupedArgs& a, const uint32_t* off_, const uint32_t* first_) : off(off_), first(first_) {
     const uint32_t ctas = SPLIT ? a.split : GroupedCfg<PAIR>::CTAS;
     tile = blockIdx.x / ctas;
     step = gridDim.x / ctas;
     end = a.along_k ? static_cast<uint32_t>(a.groups) * a.p_tiles * a.q_tiles : first[a.groups];
+    if (a.along_k) {
+      const uint32_t all = a.p_tiles * a.q_tiles;
+      g = tile / all;
+      r = tile - g * all;
+      step_g = step / all;
+      step_r = step - step_g * all;
+    }
   }
+  // (n / d for d up to kGgBand and n below 2^29)
+  __device__ static uint32_t few(const GroupedArgs& a, uint32_t n, uint32_t d) { return d == 1 ? n : __umulhi(n, a.recip[d]); }
   // Tile r of a group's p_tiles x q_tiles: in bands of the N side, so that those that
   // run at once read no more of either operand than they have to.
-  __device__ void place(uint32_t r, uint32_t p_tiles, uint32_t q_tiles, uint32_t& p, uint32_t& q) {
+  __device__ static void place(const GroupedArgs& a, uint32_t r, uint32_t q_tiles, uint32_t& p, uint32_t& q) {
     uint32_t band = 0, high = q_tiles;
     if (q_tiles > kGgBand) {
-      band = r / (p_tiles * kGgBand);
-      r -= band * (p_tiles * kGgBand);
+      band = r / (a.p_tiles * kGgBand);
+      r -= band * (a.p_tiles * kGgBand);
       high = min(kGgBand, q_tiles - band * kGgBand);
     }
-    p = r / high;
+    p = few(a, r, high);
     q = band * kGgBand + r - p * high;
   }
+  // (Every role asks for every tile, and short tiles take little longer than this did
+  // with divisions: 1001 rows of 40 groups along K, 57.5 to 50.1 us.  There is one left
+  // where a group has more than a band.)
   __device__ bool next(const GroupedArgs& a, GroupedTile& t) {
     if (tile >= end) return false;
     constexpr uint32_t STEP = GroupedCfg<PAIR>::STEP;
     const uint32_t u = tile;
     tile += step;
     if (a.along_k) {
-      const uint32_t g = u / (a.p_tiles * a.q_tiles), r = u - g * (a.p_tiles * a.q_tiles);
       uint32_t p, q;
-      place(r, a.p_tiles, a.q_tiles, p, q);
+      place(a, r, a.q_tiles, p, q);
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
       const uint32_t q0 = q * a.q_width, len = off[g + 1] - off[g];
       t.q0 = static_cast<int32_t>(q0);
       t.count = min(a.q_width, static_cast<uint32_t>(a.m) - q0);
-      t.cols = (t.count + a.q_step - 1) / a.q_step * a.q_step;
+      t.cols = (t.count + a.q_step - 1) & ~(a.q_step - 1);
       t.row0 = static_cast<int32_t>(off[g]);
       t.steps = static_cast<int32_t>(len >> 4);
       t.rest = static_cast<int32_t>(len & 15u);
+      g += step_g;
+      r += step_r;
+      if (r >= a.p_tiles * a.q_tiles) {
+        r -= a.p_tiles * a.q_tiles;
+        ++g;
+      }
     } else {
       const uint32_t g = group_of(first, a.groups, u);
-      const uint32_t r = u - first[g], len = off[g + 1] - off[g];
-      const uint32_t tiles = (len + a.q_most - 1) / a.q_most;
-      const uint32_t width = ((len + tiles - 1) / tiles + STEP - 1) / STEP * STEP;
+      const uint32_t len = off[g + 1] - off[g], tiles = (len + a.q_most - 1) >> a.lg_most;
+      const uint32_t each = tiles <= kGgBand ? few(a, len + tiles - 1, tiles) : (len + tiles - 1) / tiles;
+      const uint32_t width = (each + STEP - 1) / STEP * STEP;
       uint32_t p, q;
-      place(r, a.p_tiles, tiles, p, q);
+      place(a, u - first[g], tiles, p, q);
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
       t.q0 = static_cast<int32_t>(off[g] + q * width);
@@ -280,6 +302,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     fence_proxy_async_smem();
     tma_prefetch_desc(&a.tm_p);
     tma_prefetch_desc(&a.tm_q);
+    tma_prefetch_desc(&a.tm_c);
     if (a.along_k) {
       tma_prefetch_desc(&a.tm_pr);
       tma_prefetch_desc(&a.tm_qr);
@@ -464,25 +487,28 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     }
   } else {
     // ------------------------------------------------------------ results
-    // The four warps of a set (one for each quarter of the lanes) put 32 columns
-    // together in shared memory and store 256 bytes of a row of C in a piece (pieces
-    // of 64 bytes, a warp's own: 217 us against 177 for 127 rows of 41 groups, 920 x
-    // 7928).  The arrivals here and at the cleared rows release at CTA scope: at the
-    // cluster's they wait for the stores, 2000 to 3500 cycles of a tile's 6500 (the
-    // same case 177 to 145 us, 17024 rows of 121 groups, 376 x 6584, 280 to 185).
+    // Two warps of a set (each has a quarter of the lanes) put 32 columns of 64 values
+    // together in shared memory, and a copy of the box takes them to C (by single stores
+    // of 256 bytes in a piece, four warps together, 1001 rows of 40 groups along K,
+    // 1000 x 2880, took 61.8 us, so 57.5; of 64 bytes, a warp's own, 127 rows of 41,
+    // 920 x 7928, 217 against 177).  The arrivals here and at the cleared rows release at
+    // CTA scope: at the cluster's they wait for the stores, 2000 to 3500 cycles of a
+    // tile's 6500 (the same case 177 to 145 us, 17024 rows of 121 groups, 376 x 6584,
+    // 280 to 185).
     const uint32_t quad = static_cast<uint32_t>(warp & 3), set = static_cast<uint32_t>(warp - kGgEpiWarp0) / 4;
-    const uint32_t stage = base + epi_off + set * 2 * 8192u;
-    // Places: row r at 256 r, its 16-byte pieces exchanged so that eight rows' pieces
-    // are in eight different bank groups.
-    const uint32_t put = stage + (lane & 7u) * 256u + ((quad * 4u + static_cast<uint32_t>(lane >> 3)) ^ (lane & 7u)) * 16u;
-    const uint32_t row = quad * 8u + static_cast<uint32_t>(lane >> 4), piece = static_cast<uint32_t>(lane & 15);
+    const uint32_t half = quad >> 1, stage = base + epi_off + set * 2 * 8192u + half * 4096u;
+    // Places as a copy of boxes takes them: row r at 128 r, its 16-byte pieces exchanged
+    // so that eight rows' pieces are in eight different bank groups.
+    const uint32_t put = stage + (lane & 7u) * 128u + (((quad & 1u) * 4u + static_cast<uint32_t>(lane >> 3)) ^ (lane & 7u)) * 16u;
+    const uint32_t row = (quad & 1u) * 16u + static_cast<uint32_t>(lane >> 3), piece = static_cast<uint32_t>(lane & 7);
+    const bool issues = (quad & 1u) == 0 && lane == 0;
     uint32_t uses = 0, pieces = 0;
     while (work.next(a, t)) {
       const int buf = static_cast<int>(uses & 1u);
       const bool some = t.nkb > 0 || t.rest > 0;
       if (some) {
         // (the warps meet below, so they give up together)
-        if (named_bar_or(1, kGgEpiWarps * 32, !warp_wait(accf(buf), uses >> 1 & 1u))) break;
+        if (named_bar_or(2 + set * 2 + half, 64, !warp_wait(accf(buf), uses >> 1 & 1u))) break;
         tc_fence_after();
       }
       const uint32_t d = tmem + static_cast<uint32_t>(buf) * kGgMost + (quad * 32u << 16);
@@ -503,9 +529,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         }
         break;
       }
-      const int32_t n = t.p0 + static_cast<int32_t>(rank * kGgRows + piece * 8u);
-      const bool inside = n < a.n;
+      const int32_t n0 = t.p0 + static_cast<int32_t>(rank * kGgRows + half * 64u), n = n0 + static_cast<int32_t>(piece * 8u);
       uint16_t* out = a.c + (a.along_k ? t.group * a.c_stride : 0) + static_cast<int64_t>(t.q0) * a.ldc + n;
+      const bool last = a.along_k && t.q0 + static_cast<int32_t>(t.count) == a.m;  // (rows behind the matrix are not stored)
       // (the sets take turns of 32 columns; the next ones are on their way while these are stored)
       uint32_t x[16], y[16];
       auto load = [&](uint32_t c) {
@@ -550,21 +576,32 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
           else
             done();
         }
-        // (of two places, the one that all four read before they last met)
+        // (of two places, the one that was read before the two warps last met)
         const uint32_t here = (pieces & 1u) * 8192u;
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i)
-          stmatrix_x4_trans(put + here + i * 2048u, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        named_bar_sync(2 + set, 128);
+          stmatrix_x4_trans(put + here + i * 1024u, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        fence_proxy_async_smem();
+        if (issues) bulk_wait_group_read<0>();  // (the other place)
+        named_bar_sync(2 + set * 2 + half, 64);
+        // A box that has rows of another tile goes by single stores.
+        if (c + 32 <= t.count || last) {
+          if (issues && n0 < a.n) {
+            tma_store_4d(&a.tm_c, stage + here, n0, t.q0 + static_cast<int32_t>(c), 0, a.along_k ? t.group : 0);
+            bulk_commit_group();
+          }
+        } else {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint32_t r = row + 2 * i;
-          const uint4 v = ld_shared_v4(stage + here + r * 256u + ((piece ^ (r & 7u)) << 4));
-          if (c + r < t.count && inside) st_global_v4(out + static_cast<int64_t>(c + r) * a.ldc, v.x, v.y, v.z, v.w);
+          for (uint32_t i = 0; i < 4; ++i) {
+            const uint32_t r = row + 4 * i;
+            const uint4 v = ld_shared_v4(stage + here + r * 128u + ((piece ^ (r & 7u)) << 4));
+            if (c + r < t.count && n < a.n) st_global_v4(out + static_cast<int64_t>(c + r) * a.ldc, v.x, v.y, v.z, v.w);
+          }
         }
       }
       uses += some;
     }
+    if (issues) bulk_wait_group<0>();
   }
 
   // ------------------------------------------------------------ end
@@ -773,6 +810,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   if (dev != plan->device) return GEMM_ERR_INVALID_ARG;  // (the status word is there)
 
   GroupedArgs a = {};
+  for (uint32_t i = 2; i <= kGgBand; ++i) a.recip[i] = static_cast<uint32_t>(((uint64_t{1} << 32) + i - 1) / i);
   const int64_t busy = std::min<int64_t>(d.groups, std::max<int64_t>(rows, 1));
   const int64_t mean = (rows + busy - 1) / busy;
   // Few rows a group: tiles as wide as twice the mean, so that most groups have one, and
@@ -818,6 +856,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     tiles = static_cast<int64_t>(d.groups) * a.p_tiles * a.q_tiles;
   } else {
     a.q_most = pair ? kGgMost : narrow;
+    while (1u << a.lg_most < a.q_most) ++a.lg_most;
     a.q_box = mean >= kGgWideMean ? a.q_most / ctas : mean <= kGgNarrowMean ? kGgPiece / 2 : kGgPiece;
     a.q_boxes = a.q_most / ctas / a.q_box;
     a.stage_bytes = kGgPBytes + a.q_most / ctas * TILE_K * 2;
@@ -843,6 +882,8 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
               : encode_matrices(&a.tm_p, bp, bf16, b_row, b_rows, d.groups, ldb, b_stride, b_mn ? 64 : kGgRows, p_stretches) &&
                     encode_matrices(&a.tm_q, ap, bf16, d.K, some, 1, lda, lda, a.q_box, 1);
   if (!encoded) return GEMM_ERR_CUDA;
+  if (!encode_matrices(&a.tm_c, C, bf16, d.N, along_k ? d.M : rows, along_k ? d.groups : 1, ldc, along_k ? c_stride : ldc, 32, 1))
+    return GEMM_ERR_CUDA;
   a.c = static_cast<uint16_t*>(C);
   a.offsets = offsets;
   a.status = plan->d_status;
