@@ -338,7 +338,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
   if (warp == 0 || warp == kGgQWarp || warp >= kGgOddP) {
     // ------------------------------------------------------------ copies
     const bool is_p = warp == 0 || warp == kGgOddP, odd = warp >= kGgOddP;
-    if ((!odd || (is_p ? a.p_boxes : a.q_boxes) > 1) && elect_one()) {
+    // (A second warp has a copy in every stage or in none: one that waited for stages
+    // without would be bound to nobody, and could miss that a stage was used twice.)
+    const uint32_t every = !is_p && !a.along_k ? 1u : 2u;
+    if ((!odd || (every > 1 && (is_p ? a.p_boxes : a.q_boxes) > 1)) && elect_one()) {
       const CUtensorMap* tm = is_p ? &a.tm_p : &a.tm_q;
       const CUtensorMap* tm_rest = is_p ? &a.tm_pr : &a.tm_qr;
       const uint32_t at = is_p ? 0u : kGgPBytes;
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
       const bool k_first = is_p ? !a.p_mn : !a.along_k, whole = is_p ? a.p_whole : a.q_whole;
       auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t apart, uint32_t bar, int32_t x0, int32_t k, int32_t z) {
         const int32_t stretch = whole ? x0 >> 6 : 0;
-        for (uint32_t j = odd; j < boxes; j += 2) {
+        for (uint32_t j = odd; j < boxes; j += every) {
           const int32_t x = whole ? 0 : x0 + static_cast<int32_t>(box * j);
           if constexpr (PAIR)
             tma_load_4d_pair(dst + j * apart, map, bar, k_first ? k : x, k_first ? x : k, stretch, z);
@@ -858,7 +861,6 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
     a.q_most = pair ? kGgMost : narrow;
     while (1u << a.lg_most < a.q_most) ++a.lg_most;
     a.q_box = mean >= kGgWideMean ? a.q_most / ctas : mean <= kGgNarrowMean ? kGgPiece / 2 : kGgPiece;
-    a.q_boxes = a.q_most / ctas / a.q_box;
     a.stage_bytes = kGgPBytes + a.q_most / ctas * TILE_K * 2;
     tiles = (rows / a.q_most + busy) * a.p_tiles;
   }

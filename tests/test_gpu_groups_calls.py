@@ -211,6 +211,40 @@ def test_adapter_gradients(m, sizes, rank):
 
 # ------------------------------------------------------------------ graphs, streams, repeats
 
+@pytest.mark.parametrize("kind", ["rows", "wide rows", "sums", "adapters", "adapters gathered", "adapters, two CTAs"])
+def test_many_calls_one_after_the_other(m, kind, monkeypatch):
+    """No wait runs out where copying warps have unequal work: narrow tiles of a plan for wider ones, tiles of few
+    rows, many stages a tile.  (A warp that waits for stages that it brings nothing to can miss one.)"""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    groups, n, k = (128, 1536, 2048) if "rows" in kind else (24, 520, 520) if kind == "sums" else (9, 512, 4096)
+    per = 4 if kind == "rows" else 40 if "rows" in kind else 150 if kind == "sums" else 60
+    rows = per * groups
+    x, w = _ints(1, rows, k, dtype=torch.bfloat16), _ints(2, groups, n, k, dtype=torch.bfloat16)
+    ids = [torch.randint(0, groups, (rows,), generator=g, device="cuda", dtype=torch.int32) for _ in range(4)]
+    if kind == "adapters gathered":
+        ids = [torch.where(torch.rand(rows, generator=g, device="cuda") < 0.03, i, i % 2 * 5) for i in ids]
+    offsets, order, _ = zip(*(_order(m, i.int(), groups) for i in ids))
+    if kind == "sums":
+        op, outs = m.GroupedGemmK(groups, n, k), [torch.empty(groups, n, k, dtype=torch.bfloat16, device="cuda") for _ in ids]
+        calls = [lambda i=i: op.run(x[:, :n], x, offsets[i], outs[i]) for i in range(4)]
+    elif "rows" in kind:
+        op, outs = m.GroupedGemm(groups, n, k), [torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda") for _ in ids]
+        calls = [lambda i=i: op.run(x, w, offsets[i], outs[i]) for i in range(4)]
+    else:
+        monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", "2" if "two" in kind else "1")
+        op, b = m.Adapters(groups, n, k, 16), _ints(3, groups, n, 16, dtype=torch.bfloat16, most=1)
+        base, outs = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda"), [torch.empty(rows, n, dtype=torch.bfloat16, device="cuda") for _ in ids]
+        a = _ints(4, groups, 16, k, dtype=torch.bfloat16, most=1)
+        calls = [lambda i=i: op.run(x, a, b, offsets[i], order[i] if "gathered" in kind else None, base, outs[i]) for i in range(4)]
+    for call in calls:
+        call()
+    assert op.sync_status() == m.GEMM_OK
+    once = [o.clone() for o in outs]
+    for i in range(400):
+        calls[i % 4]()
+    assert op.sync_status() == m.GEMM_OK
+    assert all(torch.equal(o, p) for o, p in zip(once, outs))
+
 def _operators(m, big):
     """Each operator on whole numbers: (its call, its output, what the output has to be for the present ids)."""
     t, groups, n, k, rank = torch.float16, 6, 264, 200, 16
