@@ -581,8 +581,17 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
       // (by fours as far as the tile has rows, or all of a box)
       const uint32_t fours = (w.count + 3) / 4, load_bytes = (a.order ? fours * 512 : t.height * 128) + t.rank16 * 16 * 128;
+      // A warp without copies passes a tile's stages over: nothing would bind it to the
+      // others, and it could miss that a stage was used twice.  (All stages are empty
+      // when a tile begins.)
+      const bool copies = a.order ? static_cast<uint32_t>(warp) < fours || warp == 0 : warp == 0;
+      if (!copies) {
+        const uint32_t to = s + static_cast<uint32_t>(kb1 - kb0);
+        phase ^= to / t.stages & 1u;
+        s = to % t.stages;
+      }
       if (elect_one()) {
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = kb0; copies && kb < kb1; ++kb) {
           if (!(ok = wait(empty(s), phase ^ 1u))) break;
           const uint32_t dst = base + s * t.stage_bytes;
           if (warp == 0) {
