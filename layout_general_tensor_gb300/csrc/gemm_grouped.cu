@@ -17,9 +17,10 @@
 // 302 to 316 us alone, 1740 to 1820 TFLOP/s, pipe busy for 89 % of the time; 362 one after the
 // other; along K, 2048 x 4096: 165 and 188); with few rows the weights' bytes (512
 // rows of 128 groups, 1536 x 2048: 114 us, 97 % of the copy's rate; 8 rows of 8
-// groups, 2048 x 4096: 20 us, of which 4 are its ends), along K those of C (1001
-// rows of 40 groups, 1000 x 2880: 61 us, a fill of C 60); between the two, rounds of
-// tiles (4000 rows of 24 groups, 3000 x 2880: 86 us, 68 by its bytes).
+// groups, 2048 x 4096: 20 us, of which 4 are its ends), along K with few rows
+// the results' way out of tensor memory (1001 rows of 40 groups, 1000 x 2880: 50 us; 23
+// without any results, 45 without copies to C, which alone would take 37); between the two,
+// rounds of tiles (4000 rows of 24 groups, 3000 x 2880: 86 us, 68 by its bytes).
 //
 // Work.  The sizes are on the device, so every CTA sums them up itself (a scan
 // over the groups' tiles in shared memory) and takes every G-th tile, G the
@@ -82,13 +83,14 @@ constexpr uint32_t kGgMost = 256;                       // N-side columns of a t
 // Rows of A in a copy: a tile's are as many copies as it has rows for, since a tile
 // much narrower than the widest is the usual one (5266 rows of 69 groups, 3976 x
 // 1144: 128 us with copies of 64 rows, 123 of 32, against 186 with one for the widest).
-// From 2048 rows a group on most tiles are full (16384 rows of one group, 4096 x 4096,
-// one after the other: 341 us with copies of 32, 333 of 128).
+// From 512 rows a group on most tiles are wide (16384 rows of 16 groups, 4096 x 4096,
+// one after the other: 377 us with copies of 32, 365 of 128; 20000 of 12, 2048 x 2048,
+// 109 and 102; 6915 of 21, 4240 x 2008: 127 of 32, 133 of 64).
 // Up to 4, one of half the size does for most (8 rows of 8 groups, 2048 x 4096, where
 // each SM's stream is the limit: 24.1 us, 21.0).
 constexpr uint32_t kGgPiece = 32;
 constexpr int64_t kGgNarrowMean = 4;
-constexpr int64_t kGgWideMean = 2048;
+constexpr int64_t kGgWideMean = 512;
 constexpr uint32_t kGgBand = 8;                         // tiles of the N side
 constexpr uint32_t kGgMaxStages = 12;
 constexpr uint32_t kGgEpiBytes = 2 * 2 * 8192;          // 32 rows of C, 128 values each, of two sets of warps, twice
