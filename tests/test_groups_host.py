@@ -259,3 +259,30 @@ def test_tiles_of_a_group_cover_its_rows_once():
         width = -(-(-(-length // tiles)) // step) * step
         ends = [min((i + 1) * width, length) for i in range(tiles)]
         assert width <= most and ends[-1] == length and (tiles - 1) * width < length
+
+
+def test_tiles_in_bands_are_each_taken_once():
+    """The order of a group's tiles (in bands of eight of the N side) names each of them once."""
+    band = 8
+    for p_tiles in (1, 2, 3, 7, 12, 32):
+        for q_tiles in (1, 2, 5, 7, 8, 9, 15, 16, 17, 40):
+            seen = set()
+            for r in range(p_tiles * q_tiles):
+                first, high = 0, q_tiles
+                if q_tiles > band:
+                    first = r // (p_tiles * band)
+                    r -= first * (p_tiles * band)
+                    high = min(band, q_tiles - first * band)
+                p = r // high
+                seen.add((p, first * band + r - p * high))
+            assert seen == {(p, q) for p in range(p_tiles) for q in range(q_tiles)}
+
+
+def test_reciprocals_of_a_band_divide_exactly():
+    """n / d as the upper half of n times 2^32 / d, rounded up: exact for d up to 8 and n below 2^29, since the product
+    is too large by less than n * d / 2^32 < 1 / d of a whole."""
+    for d in range(2, 9):
+        m = ((1 << 32) + d - 1) // d
+        for near in list(range(0, 4096)) + [k * d for k in range(1 << 10, 1 << 26, 65537)] + [(1 << 29) - 1, (1 << 29) // d * d - 1]:
+            for n in (near, max(near - 1, 0), near + 1 if near + 1 < 1 << 29 else near):
+                assert n * m >> 32 == n // d
