@@ -482,9 +482,11 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
             st_shared_v4(at + c * kGgStep + i, 0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
+        // (A pair's product is the even CTA's: the zeros are released to the cluster, which
+        // costs 1 us before the last step; 17024 rows of 121 groups, 376 x 6584, 187 to 199 us.)
         if (lane == 0) {
           if constexpr (PAIR)
-            mbar_arrive_remote(cleared_lead + 8u * b);
+            mbar_arrive_cluster(cleared_lead + 8u * b);
           else
             mbar_arrive(cleared(b));
         }
@@ -496,10 +498,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     // together in shared memory, and a copy of the box takes them to C (by single stores
     // of 256 bytes in a piece, four warps together, 1001 rows of 40 groups along K,
     // 1000 x 2880, took 61.8 us, so 57.5; of 64 bytes, a warp's own, 127 rows of 41,
-    // 920 x 7928, 217 against 177).  The arrivals here and at the cleared rows release at
-    // CTA scope: at the cluster's they wait for the stores, 2000 to 3500 cycles of a
-    // tile's 6500 (the same case 177 to 145 us, 17024 rows of 121 groups, 376 x 6584,
-    // 280 to 185).
+    // 920 x 7928, 217 against 177).  The arrivals here release at CTA scope: at the
+    // cluster's they wait for the stores, 2000 to 3500 cycles of a tile's 6500 (the same
+    // case 177 to 145 us, 17024 rows of 121 groups, 376 x 6584, 280 to 185).
     const uint32_t quad = static_cast<uint32_t>(warp & 3), set = static_cast<uint32_t>(warp - kGgEpiWarp0) / 4;
     const uint32_t half = quad >> 1, stage = base + epi_off + set * 2 * 8192u + half * 4096u;
     // Places as a copy of boxes takes them: row r at 128 r, its 16-byte pieces exchanged

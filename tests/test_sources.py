@@ -1,0 +1,22 @@
+"""CPU tests of what no run can show: rules of the memory model that the kernels' sources keep."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "layout_general_tensor_gb300", "csrc")
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def test_rows_cleared_in_a_pair_are_announced_at_cluster_scope():
+    """The odd CTA's zeros are read by a product that a thread of the even CTA issues: what announces them has to
+    release them to that CTA.  (As it runs, the weaker form has not been seen to fail.)"""
+    source = _source("gemm_grouped.cu")
+    part = source[source.index("rows of the next group\n"):source.index("- results\n")]
+    (arrival,) = re.findall(r"(\w+)\(cleared_lead", part)
+    body = _source("ptx.cuh").split(f"void {arrival}(")[1].split("\n}")[0]
+    assert re.search(r"mbarrier\.arrive\.release\.cluster\.shared::cluster", body)
