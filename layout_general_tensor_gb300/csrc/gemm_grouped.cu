@@ -498,9 +498,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     // together in shared memory, and a copy of the box takes them to C (by single stores
     // of 256 bytes in a piece, four warps together, 1001 rows of 40 groups along K,
     // 1000 x 2880, took 61.8 us, so 57.5; of 64 bytes, a warp's own, 127 rows of 41,
-    // 920 x 7928, 217 against 177).  The arrivals here release at CTA scope: at the
-    // cluster's they wait for the stores, 2000 to 3500 cycles of a tile's 6500 (the same
-    // case 177 to 145 us, 17024 rows of 121 groups, 376 x 6584, 280 to 185).
+    // 920 x 7928, 217 against 177).  The arrivals at the even CTA release nothing, since
+    // tensor memory is all that they speak of: released to the cluster they wait for the
+    // stores, 2000 to 3500 cycles of a tile's 6500 (1001 rows of 40 groups 52 us against
+    // 76, 127 of 41 128 against 192, 32768 of 8 with K = 256 and 4096 columns 69 against 96).
     const uint32_t quad = static_cast<uint32_t>(warp & 3), set = static_cast<uint32_t>(warp - kGgEpiWarp0) / 4;
     const uint32_t half = quad >> 1, stage = base + epi_off + set * 2 * 8192u + half * 4096u;
     // Places as a copy of boxes takes them: row r at 128 r, its 16-byte pieces exchanged
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) {
           if constexpr (PAIR)
-            mbar_arrive_remote(acce_lead + 8u * buf);
+            mbar_arrive_tmem_read(acce_lead + 8u * buf);
           else
             mbar_arrive(acce(buf));
         }

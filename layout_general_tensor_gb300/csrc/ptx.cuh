@@ -453,11 +453,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-// The same, releasing at CTA scope only: it says that this thread got here (its
-// loads have returned, its shared stores are behind a proxy fence), and does not wait
-// for its stores to global memory, which takes the one above 1 to 2 us.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+// The same, relaxed: for the readers of tensor memory, whose loads have returned and
+// are ordered before what the waiting thread issues by the tcgen05 fences on both sides
+// (before_thread_sync here, after_thread_sync there), for which an execution order is
+// enough.  It orders no access to shared or global memory, and so does not wait for
+// this thread's stores, which takes the one above 1 to 2 us.
+__device__ __forceinline__ void mbar_arrive_tmem_read(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {

@@ -20,3 +20,11 @@ def test_rows_cleared_in_a_pair_are_announced_at_cluster_scope():
     (arrival,) = re.findall(r"(\w+)\(cleared_lead", part)
     body = _source("ptx.cuh").split(f"void {arrival}(")[1].split("\n}")[0]
     assert re.search(r"mbarrier\.arrive\.release\.cluster\.shared::cluster", body)
+
+
+def test_arrivals_in_another_cta_have_its_scope():
+    """What is announced in another CTA's barrier has cluster scope: a release, or, where it says only that tensor
+    memory has been read (tcgen05 fences order that), a relaxed arrival."""
+    for name in sorted(os.listdir(CSRC)):
+        for scope in re.findall(r"mbarrier\.arrive(?:\.expect_tx)?((?:\.\w+)*)\.shared::cluster", _source(name)):
+            assert scope in (".release.cluster", ".relaxed.cluster"), (name, scope)
