@@ -277,10 +277,12 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_kernel(const __grid_con
     }
     return got;
   };
-  // (for a whole warp: one lane looks)
+  // (for a whole warp: one lane looks; the others' accesses are ordered behind it by the
+  // warp's barrier, which a shuffle is not)
   auto warp_wait = [&](uint32_t bar, uint32_t parity) {
     int got = 0;
     if (lane == 0) got = wait(bar, parity);
+    __syncwarp();
     return __shfl_sync(0xffffffffu, got, 0) != 0;
   };
 

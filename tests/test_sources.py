@@ -28,3 +28,11 @@ def test_arrivals_in_another_cta_have_its_scope():
     for name in sorted(os.listdir(CSRC)):
         for scope in re.findall(r"mbarrier\.arrive(?:\.expect_tx)?((?:\.\w+)*)\.shared::cluster", _source(name)):
             assert scope in (".release.cluster", ".relaxed.cluster"), (name, scope)
+
+
+def test_a_look_by_one_lane_is_passed_on_with_its_order():
+    """Where one lane of a warp waits for a barrier, the others read and write after it what the barrier announces: a
+    shuffle tells them that it has come, and only a barrier of the warp orders their accesses behind it."""
+    source = _source("gemm_grouped.cu")
+    body = source.split("auto warp_wait = ")[1].split("\n  };")[0]
+    assert body.index("lane == 0") < body.index("__syncwarp()")
