@@ -1,4 +1,12 @@
-"""Operators over groups of rows on the GPU where values are far from ordinary."""
+"""Operators over groups of rows on the GPU where values are far from ordinary:
+adapters of infinite weights, rows of which one value is infinite, products whose
+factors pass the types' ends while the result does not; sums beside rows of infinities.
+Infinities and NaN have to be where the definition in 64 bits has them.
+
+Finite results of adapters: u is off by its sum's 2^-20 sum |x a| and by its pair's 2^-16 of the
+row's largest finite value, the second sum by 2^-20 sum |u b|, the result by one fp32
+rounding (2^-23 is ample) and half a step of its type; a result below the least normal
+value by half a step there."""
 import pytest
 import torch
 
@@ -7,10 +15,82 @@ from test_gpu_groups import TD, _code, _offsets
 
 pytestmark = pytest.mark.gpu
 
+# rows of the groups, and the form: the one for few rows, the one for many with 1, 2 and 4 CTAs a tile
+CALLS = [([5, 0, 3], 0), ([90, 0, 133], 0), ([90, 0, 133], 1), ([90, 0, 133], 2), ([90, 0, 133], 4)]
+N, K = 520, 256
+
 
 @pytest.fixture(scope="module")
 def m():
     return lib()
+
+
+def _check(m, monkeypatch, form, sizes, x, a, b, base, scales=None):
+    """One call against the definition, value by value in 64 bits."""
+    monkeypatch.setenv("LGT_GEMM_ADAPTERS_FORM", str(form))
+    t, dtype = x.dtype, "f16" if x.dtype is torch.float16 else "bf16"
+    offsets, out = _offsets(sizes), torch.full_like(base, -77.0)
+    op = m.Adapters(a.shape[0], b.shape[1], x.shape[1], a.shape[1], dtype=_code(m, dtype))
+    op.run(x, a, b, offsets, None, base, out, scales=scales)
+    assert op.sync_status() == m.GEMM_OK
+    at = offsets.tolist()
+    for g in range(len(sizes)):
+        r = slice(at[g], at[g + 1])
+        if at[g] == at[g + 1]:
+            continue
+        s = scales[g].double() if scales is not None else torch.ones((), dtype=torch.float64, device="cuda")
+        u = (x[r, None].double() * a[g, None].double()).sum(-1)
+        up = b[g].double()
+        want = base[r].double() + s * (u[:, None] * up[None]).sum(-1)
+        got = out[r].double()
+        there = want.isfinite()
+        # (a finite value beyond the type's range becomes an infinity)
+        want_t = want.to(t).double()
+        there &= want_t.isfinite()
+        assert torch.equal(got.isnan(), want.isnan()), (g, (got.isnan() != want.isnan()).nonzero()[:5])
+        assert torch.equal(got[~there & ~want.isnan()], want_t[~there & ~want.isnan()]), g
+        finite = torch.where(u.isfinite(), u, 0.0)
+        off = 2.0**-20 * (x[r].double().abs() @ a[g].double().abs().nan_to_num(posinf=0.0).T) + 2.0**-16 * finite.abs().amax(-1, keepdim=True)
+        error = s.abs() * ((off + 2.0**-20 * finite.abs()) @ up.abs().nan_to_num(posinf=0.0).T)
+        half = torch.finfo(t).eps / 2
+        tolerance = error + (want.abs() + error) * (half + 2.0**-23) + torch.finfo(t).smallest_normal * half
+        assert ((got - want).abs() <= tolerance)[there].all(), (g, ((got - want).abs() / tolerance)[there].max())
+
+
+def _rows(sizes, t, g):
+    """Rows of x with one or two values of 1: each u is a value of A, which the type holds, or the sum of two."""
+    rows = sum(sizes)
+    x = torch.zeros(rows, K, dtype=t, device="cuda")
+    for i in range(2):
+        x[torch.arange(rows, device="cuda"), torch.randint(0, K, (rows,), generator=g, device="cuda")] = 1
+        if i == 0:
+            keep = x[::2].clone()
+    x[::2] = keep
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("sizes,form", CALLS)
+@pytest.mark.parametrize("rank", [8, 24, 80])
+def test_infinite_weights_of_an_adapter(m, sizes, form, dtype, rank, monkeypatch):
+    """A column of B with an infinite value gives infinities of the sign that the definition gives, and NaN where
+    u is 0 or two of them are opposed."""
+    t, groups = TD[dtype], len(sizes)
+    g = torch.Generator(device="cuda").manual_seed(rank + form)
+    x = _rows(sizes, t, g)
+    a = torch.randn(groups, rank, K, generator=g, device="cuda").to(t)
+    a[:, 1] = 0
+    a[:, 3] = (a[:, 3].float() * 2.0**-14).to(t)  # far below the others of its row
+    a[:, 4] = (a[:, 4].float() * (2.0**-24 if dtype == "f16" else 2.0**-90)).to(t)
+    a[:, 5] = (a[:, 5].float() * 2.0**8).to(t)
+    b = (torch.randn(groups, N, rank, generator=g, device="cuda") * 0.3).to(t)
+    for i in range(rank):  # of each value of u, columns where its weight is infinite
+        b[:, i * 5::rank * 5 + 1, i] = float("inf")
+        b[:, i * 5 + 2::rank * 5 + 1, i] = -float("inf")
+    b[:, 3::17, 0], b[:, 3::17, 2] = float("inf"), float("inf")
+    base = torch.randn(x.shape[0], N, generator=g, device="cuda").to(t)
+    _check(m, monkeypatch, form, sizes, x, a, b, base)
+    _check(m, monkeypatch, form, sizes, x, a, b, base, scales=torch.tensor([-2.0, 1.0, 0.5], device="cuda"))
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
