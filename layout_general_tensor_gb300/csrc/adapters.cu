@@ -94,10 +94,17 @@ struct RankPiece<1> {
   __device__ __forceinline__ uint2 step(int) const { return v; }
 };
 
+// A value's size where it has one.  (A row's power of two goes by its finite values: with
+// an infinity's, the others could pass fp16's largest and be infinite too.)
+__device__ __forceinline__ float finite_size(float x) {
+  const float size = fabsf(x);
+  return size < INFINITY ? size : 0.0f;
+}
+
 // The power of two that takes a row's largest value to [0.5, 1), and its reverse.
 __device__ __forceinline__ float2 row_power(float most) {
   const int e = static_cast<int>(__float_as_uint(most) >> 23);  // (biased; no sign)
-  const int p = e == 0 || e == 255 ? 0 : min(e - 126, 126);
+  const int p = e == 0 ? 0 : min(e - 126, 126);
   return make_float2(__uint_as_float(static_cast<uint32_t>(127 - p) << 23), __uint_as_float(static_cast<uint32_t>(127 + p) << 23));
 }
 
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
       // (past the rank are sums of what x holds times 0, which is not 0 for an infinity)
       if (c >= a.rank) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       // The row's power of two: its largest value goes to [0.5, 1).
-      float most = fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w)));
+      float most = fmaxf(fmaxf(finite_size(s.x), finite_size(s.y)), fmaxf(finite_size(s.z), finite_size(s.w)));
 #pragma unroll
       for (int o = 1; o < PER; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
       const float2 power = row_power(most);
@@ -822,7 +829,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
           for (uint32_t k = 0; k < 8; ++k) {
             // (past the rank are sums of what x holds times 0, which is not 0 for an infinity)
             if (k >= t.rank16 || static_cast<int>(4 * (piece + 4 * k)) >= a.rank) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            most = fmaxf(most, fmaxf(fmaxf(fabsf(v[k].x), fabsf(v[k].y)), fmaxf(fabsf(v[k].z), fabsf(v[k].w))));
+            most = fmaxf(most, fmaxf(fmaxf(finite_size(v[k].x), finite_size(v[k].y)), fmaxf(finite_size(v[k].z), finite_size(v[k].w))));
           }
           most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
           most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -857,7 +864,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
           tc_wait_ld_regs(v);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (static_cast<int>(c) + e < a.rank) most = fmaxf(most, fabsf(__uint_as_float(v[e])));
+            if (static_cast<int>(c) + e < a.rank) most = fmaxf(most, finite_size(__uint_as_float(v[e])));
         }
         const float2 power = row_power(most);
         for (uint32_t c = 0; c < t.rank16 * 16; c += 16) {

@@ -94,6 +94,24 @@ def test_infinite_weights_of_an_adapter(m, sizes, form, dtype, rank, monkeypatch
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("sizes,form", CALLS)
+def test_an_infinite_value_beside_large_ones(m, sizes, form, dtype, monkeypatch):
+    """One value of u is infinite, the others are finite, in fp16 above the largest that the type holds."""
+    t, groups, rank = TD[dtype], len(sizes), 16
+    g = torch.Generator(device="cuda").manual_seed(form)
+    x = torch.zeros(sum(sizes), K, dtype=t, device="cuda")
+    x[:, 0], x[:, 1] = 1, 4
+    x[::3, 0] = -1
+    x[1::4, 0] = 0  # (no number: 0 times an infinity)
+    a = torch.zeros(groups, rank, K, dtype=t, device="cuda")
+    a[:, 0, 0] = float("inf")
+    a[:, 1, 1], a[:, 2, 1] = 30000, -50000
+    b = torch.randint(-2, 3, (groups, N, rank), generator=g, device="cuda").to(t)
+    base = torch.randn(x.shape[0], N, generator=g, device="cuda").to(t)
+    _check(m, monkeypatch, form, sizes, x, a, b, base)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("mm,n", [(264, 200), (136, 520), (512, 1024)])
 def test_sums_between_groups_of_infinities(m, dtype, mm, n):
     """Pairs, where each CTA clears its part of what lies behind a group's last whole step: every second group's rows
