@@ -14,9 +14,10 @@
  * fp16 or bf16, all of one type; sums in fp32.  The first product's result u
  * goes into the second one as two values of the type, u = (hi + lo) * 2^p with p
  * the row's, so that it loses no more than 2^-16 (bf16) or 2^-21 (fp16) of the
- * row's largest finite one and cannot overflow; one rounding of out.  An infinite
- * value of x, A or B gives the infinity, or the NaN, that the formula gives.  A row
- * reaches no other row's result, whatever it holds.  Repeated calls give the same bits.
+ * row's largest finite one and cannot overflow, with the scale neither; one rounding
+ * of out.  An infinite value of x, A or B gives the infinity, or the NaN, that the
+ * formula gives.  A row reaches no other row's result, whatever it holds.  Repeated
+ * calls give the same bits.
  *
  * Errors are status codes (gemm_status_t); nothing aborts or prints.
  */

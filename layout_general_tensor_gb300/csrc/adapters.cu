@@ -24,6 +24,7 @@
 // 32 are dealt to the instruction's 8-sides so that a lane ends up with eight
 // neighbours of a row: base and out move in 16-byte pieces.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -101,11 +102,24 @@ __device__ __forceinline__ float finite_size(float x) {
   return size < INFINITY ? size : 0.0f;
 }
 
-// The power of two that takes a row's largest value to [0.5, 1), and its reverse.
-__device__ __forceinline__ float2 row_power(float most) {
+__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float(static_cast<uint32_t>(127 + n) << 23); }
+
+// The power of two that takes a row's largest value to [0.5, 1), and what the second
+// product of a row is multiplied with: the scale over that power.  Where this would pass
+// fp32's range, though with small or large weights the result does not, u takes as much
+// of it as is beyond; fp16's u, which has no room above, leaves the largest number (what
+// is not 0 then has a result that fp16 does not hold).
+template <bool BF16>
+__device__ __forceinline__ float2 row_power(float most, float scale) {
   const int e = static_cast<int>(__float_as_uint(most) >> 23);  // (biased; no sign)
-  const int p = e == 0 ? 0 : min(e - 126, 126);
-  return make_float2(__uint_as_float(static_cast<uint32_t>(127 - p) << 23), __uint_as_float(static_cast<uint32_t>(127 + p) << 23));
+  int n = e == 0 ? 0 : -min(e - 126, 126);
+  const uint32_t size = __float_as_uint(scale) & 0x7fffffffu;
+  const bool some = size != 0 && size < 0x7f800000u;
+  const int s = size >> 23 ? static_cast<int>(size >> 23) - 126 : -117 - __clz(size);  // |scale| is in [2^(s - 1), 2^s)
+  if (some) n = min(BF16 ? max(n, s - 127) : n, s + 125);
+  float factor = scale * power_of_two(-n);
+  if (!BF16 && some) factor = fminf(fmaxf(factor, -FLT_MAX), FLT_MAX);
+  return make_float2(power_of_two(n), factor);
 }
 
 template <bool BF16>
@@ -247,6 +261,7 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
     const uint32_t g = group_of(first, a.groups, tile);
     const uint32_t at = off[g] + (tile - first[g]) * C::TOK;
     const uint32_t count = min(static_cast<uint32_t>(C::TOK), off[g + 1] - at);
+    const float scale = a.scales ? a.scales[g] : 1.0f;
     if (threadIdx.x < C::TOK16) {
       int32_t r = -1;
       if (threadIdx.x < count) {
@@ -384,13 +399,13 @@ __global__ void __launch_bounds__(kAdThreads, MT * NT <= 16 ? 2 : 1) adapters_ke
       float most = fmaxf(fmaxf(finite_size(s.x), finite_size(s.y)), fmaxf(finite_size(s.z), finite_size(s.w)));
 #pragma unroll
       for (int o = 1; o < PER; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      const float2 power = row_power(most);
+      const float2 power = row_power<BF16>(most, scale);
       if (live) {
         uint32_t hi[2], lo[2];
         split_pairs<BF16, 2>({s.x, s.y, s.z, s.w}, power.x, c < a.rank && t < static_cast<int>(count), hi, lo);
         *reinterpret_cast<uint2*>(uh + t * C::UPITCH + c) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(ul + t * C::UPITCH + c) = make_uint2(lo[0], lo[1]);
-        if (c == 0) factor[t] = power.y * (a.scales ? a.scales[g] : 1.0f);
+        if (c == 0) factor[t] = power.y;
       }
     }
     __syncthreads();
@@ -762,6 +777,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
       const Tile w = tile_at(i);
       if (!(ok = warp_wait(rows_full(it & 1), it >> 1 & 1u))) break;
       const int32_t* rows = row_of + (it & 1) * kAtcRows;
+      const float scale = a.scales ? a.scales[w.g] : 1.0f;
       // The four warps of a quarter of the lanes share the rows, 32 each, or, where
       // there are fewer, the blocks of columns.
       const uint32_t by_rows = w.count > 64 ? 4u : w.count > 32 ? 2u : 1u, every = 4u / by_rows;
@@ -833,7 +849,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
           }
           most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
           most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          const float2 power = row_power(most);
+          const float2 power = row_power<BF16>(most, scale);
   #pragma unroll
           for (uint32_t k = 0; k < 8; ++k)
             if (k < t.rank16) {
@@ -844,8 +860,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
               st_shared_v2(u_hi + to, hi[0], hi[1]);
               st_shared_v2(u_lo + to, lo[0], lo[1]);
             }
-          if (piece == 0)
-            factor[add_row] = power.y * (a.scales ? a.scales[w.g] : 1.0f);
+          if (piece == 0) factor[add_row] = power.y;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -866,7 +881,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
           for (int e = 0; e < 16; ++e)
             if (static_cast<int>(c) + e < a.rank) most = fmaxf(most, finite_size(__uint_as_float(v[e])));
         }
-        const float2 power = row_power(most);
+        const float2 power = row_power<BF16>(most, scale);
         for (uint32_t c = 0; c < t.rank16 * 16; c += 16) {
           uint32_t v[16];
           tc_ld_32x32b_x16(from + c, v);
@@ -886,7 +901,7 @@ __global__ void __launch_bounds__(kAtcThreads, 1) adapters_tc_kernel(const __gri
             st_shared_v4(u_lo + to, lo[0], lo[1], lo[2], lo[3]);
           }
         }
-        factor[row] = power.y * (a.scales ? a.scales[w.g] : 1.0f);
+        factor[row] = power.y;
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();

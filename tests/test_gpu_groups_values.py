@@ -111,6 +111,36 @@ def test_an_infinite_value_beside_large_ones(m, sizes, form, dtype, monkeypatch)
     _check(m, monkeypatch, form, sizes, x, a, b, base)
 
 
+ENDS = {
+    # x, A, B, scale: the first product's and the scale's magnitudes together pass fp32's range, the result does not
+    "scaled up": ("bf16", 2.0**63, 2.0**61, 2.0**-125, 2.0**9),
+    "scaled down": ("bf16", 2.0**-60, 2.0**-58, 2.0**120, -(2.0**-30)),
+    "a scale near zero": ("bf16", 2.0**60, 2.0**40, 2.0**30, 2.0**-140),
+    "a large scale": ("bf16", 2.0**-60, 2.0**-50, 2.0**-10, 2.0**125),
+    "a scale of zero": ("bf16", 2.0**63, 2.0**61, 2.0**-125, 0.0),
+    "an infinite scale": ("bf16", 1.0, 1.0, 1.0, float("inf")),
+    "half, scaled up": ("f16", 2.0**12, 2.0**12, 2.0**-20, 2.0**115),
+    "half, scaled down": ("f16", 2.0**-12, 2.0**-10, 2.0**10, 2.0**14),
+    "half, a scale near zero": ("f16", 2.0**12, 2.0**12, 2.0**10, 2.0**-140),
+}
+
+
+@pytest.mark.parametrize("sizes,form", CALLS)
+@pytest.mark.parametrize("end", ENDS)
+def test_factors_past_the_range_of_fp32(m, sizes, form, end, monkeypatch):
+    """u, the scale and B, whose product is a moderate number, in any distribution; columns of zeros among B's give base."""
+    dtype, *size, scale = ENDS[end]
+    t, groups, rank = TD[dtype], len(sizes), 16
+    g = torch.Generator(device="cuda").manual_seed(form)
+    x = (_rows(sizes, t, g).float() * size[0]).to(t)
+    a = ((torch.rand(groups, rank, K, generator=g, device="cuda") + 0.5) * size[1]).to(t)
+    b = ((torch.rand(groups, N, rank, generator=g, device="cuda") + 0.5) * size[2]).to(t)
+    b[:, ::7] = 0
+    b[:, 1::5] *= -1
+    base = torch.randn(x.shape[0], N, generator=g, device="cuda").to(t)
+    _check(m, monkeypatch, form, sizes, x, a, b, base, scales=torch.full((groups,), scale, device="cuda"))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("mm,n", [(264, 200), (136, 520), (512, 1024)])
 def test_sums_between_groups_of_infinities(m, dtype, mm, n):
