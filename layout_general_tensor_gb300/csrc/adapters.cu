@@ -102,22 +102,25 @@ __device__ __forceinline__ float finite_size(float x) {
   return size < INFINITY ? size : 0.0f;
 }
 
-__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float(static_cast<uint32_t>(127 + n) << 23); }
+// 2^n for n from -149 to 127.
+__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float(n >= -126 ? static_cast<uint32_t>(127 + n) << 23 : 1u << (n + 149)); }
 
-// The power of two that takes a row's largest value to [0.5, 1), and what the second
+// The power of two that takes a row's largest value to [0.5, 1), for bf16 to [2^-9, 2^-8)
+// so that no sum over the rank with bf16 weights passes fp32's range, and what the second
 // product of a row is multiplied with: the scale over that power.  Where this would pass
 // fp32's range, though with small or large weights the result does not, u takes as much
 // of it as is beyond; fp16's u, which has no room above, leaves the largest number (what
 // is not 0 then has a result that fp16 does not hold).
 template <bool BF16>
 __device__ __forceinline__ float2 row_power(float most, float scale) {
-  const int e = static_cast<int>(__float_as_uint(most) >> 23);  // (biased; no sign)
-  int n = e == 0 ? 0 : -min(e - 126, 126);
+  const int e = max(static_cast<int>(__float_as_uint(most) >> 23), 1);  // (biased; no sign)
+  int n = (BF16 ? 118 : 126) - e;
   const uint32_t size = __float_as_uint(scale) & 0x7fffffffu;
   const bool some = size != 0 && size < 0x7f800000u;
   const int s = size >> 23 ? static_cast<int>(size >> 23) - 126 : -117 - __clz(size);  // |scale| is in [2^(s - 1), 2^s)
-  if (some) n = min(BF16 ? max(n, s - 127) : n, s + 125);
-  float factor = scale * power_of_two(-n);
+  if (some) n = min(BF16 ? max(n, s - 128) : n, s + 125);  // (|factor| in [2^-126, 2^128), u below 2^128)
+  const int once = min(-n, 126);
+  float factor = scale * power_of_two(once) * power_of_two(-n - once);
   if (!BF16 && some) factor = fminf(fmaxf(factor, -FLT_MAX), FLT_MAX);
   return make_float2(power_of_two(n), factor);
 }

@@ -141,6 +141,58 @@ def test_factors_past_the_range_of_fp32(m, sizes, form, end, monkeypatch):
     _check(m, monkeypatch, form, sizes, x, a, b, base, scales=torch.full((groups,), scale, device="cuda"))
 
 
+@pytest.mark.parametrize("sizes,form", CALLS)
+@pytest.mark.parametrize("rank", [16, 128])
+def test_weights_near_the_types_end(m, sizes, form, rank, monkeypatch):
+    """The sum over the rank of large weights passes fp32's range before the row's power of two brings it back."""
+    t, groups = torch.bfloat16, len(sizes)
+    g = torch.Generator(device="cuda").manual_seed(form)
+    x = (_rows(sizes, t, g).float() * 2.0**-40).to(t)
+    a = ((torch.rand(groups, rank, K, generator=g, device="cuda") + 0.5) * 2.0**-40).to(t)
+    b = ((torch.rand(groups, N, rank, generator=g, device="cuda") * 0.4 + 0.5) * 2.0**128).to(t)
+    base = torch.randn(x.shape[0], N, generator=g, device="cuda").to(t)
+    _check(m, monkeypatch, form, sizes, x, a, b, base)
+
+
+@pytest.mark.parametrize("sizes,form", CALLS)
+def test_first_products_below_the_normal_values(m, sizes, form, monkeypatch):
+    """u is less than 2^-126, where fp32 and bf16 have fewer bits: it comes in whole steps of 2^-149 here, as the sums
+    of fp32 hold them, and the second product takes them up without a further loss."""
+    t, groups, rank = torch.bfloat16, len(sizes), 16
+    g = torch.Generator(device="cuda").manual_seed(form)
+    x = torch.zeros(sum(sizes), K, dtype=t, device="cuda")
+    x[:, 5] = 2.0**-80
+    a = torch.zeros(groups, rank, K, dtype=t, device="cuda")
+    a[:, :, 5] = (torch.randint(1, 256, (groups, rank), generator=g, device="cuda").float() * 2.0**-69).to(t)
+    b = (torch.randn(groups, N, rank, generator=g, device="cuda") * 2.0**40).to(t)
+    base = torch.zeros(x.shape[0], N, dtype=t, device="cuda")
+    _check(m, monkeypatch, form, sizes, x, a, b, base, scales=torch.full((groups,), 2.0**96, device="cuda"))
+
+
+@pytest.mark.parametrize("sizes,form", CALLS)
+def test_everything_large_but_the_weights(m, sizes, form, monkeypatch):
+    """u and the scale near the end of the range, whose weights have the least values of bf16, or are 0."""
+    t, groups, rank = torch.bfloat16, len(sizes), 16
+    g = torch.Generator(device="cuda").manual_seed(form)
+    x = (_rows(sizes, t, g).float() * 2.0**63).to(t)
+    a = ((torch.rand(groups, rank, K, generator=g, device="cuda") * 0.4 + 0.5) * 2.0**63).to(t)
+    b = (torch.randint(-1, 2, (groups, N, rank), generator=g, device="cuda").double() * 2.0**-132).to(t)
+    base = torch.randn(x.shape[0], N, generator=g, device="cuda").to(t)
+    _check(m, monkeypatch, form, sizes, x, a, b, base, scales=torch.full((groups,), 1.5 * 2.0**127, device="cuda"))
+
+
+@pytest.mark.parametrize("sizes,form", CALLS)
+def test_everything_large_but_the_scale(m, sizes, form, monkeypatch):
+    """u and B near the end of the range under a scale below the normal values."""
+    t, groups, rank = torch.bfloat16, len(sizes), 16
+    g = torch.Generator(device="cuda").manual_seed(form)
+    x = (_rows(sizes, t, g).float() * 2.0**63).to(t)
+    a = ((torch.rand(groups, rank, K, generator=g, device="cuda") + 0.5) * 2.0**62).to(t)
+    b = ((torch.rand(groups, N, rank, generator=g, device="cuda") * 0.4 + 0.5) * 2.0**128).to(t)
+    base = torch.randn(x.shape[0], N, generator=g, device="cuda").to(t)
+    _check(m, monkeypatch, form, sizes, x, a, b, base, scales=torch.full((groups,), 2.0**-145, device="cuda"))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("mm,n", [(264, 200), (136, 520), (512, 1024)])
 def test_sums_between_groups_of_infinities(m, dtype, mm, n):
