@@ -4,7 +4,7 @@
       --GroupedGemm--> up --silu--> --GroupedGemm--> down --places, weights--> out
     x --Gemm--> a projection that all tokens share --Adapters--> + each request's own --> out
 
-`forward` takes tokens and each token's adapter (-1: none); `backward` the
+`forward` takes tokens and each token's adapter (-1, or no numbers at all: none); `backward` the
 gradient to its output, and gives those to x's part through the experts and to
 the experts' matrices: the products' gradient to their rows is the same operator
 with the matrices read in the other order, the one to the matrices is GroupedGemmK.
@@ -55,7 +55,7 @@ class ExpertLayer:
             self.products[m] = lgt.Gemm(lgt.make_desc(m, self.hidden, self.hidden, split_k=0))
         y = torch.empty_like(x)
         self.products[m].run(x, self.w_shared, y)
-        if self.adapters:
+        if self.adapters and adapter is not None:
             offsets, order, _ = self._order(adapter, self.adapters)
             self.own.run(x, self.a, self.b, offsets, order, y, y, scales=self.scales)
         return y

@@ -127,6 +127,22 @@ def test_the_layer_example_runs():
         assert float((got.double() - right).norm() / right.norm()) < 6 * 2.0**-8
 
 
+def test_the_layer_example_without_adapter_numbers():
+    """A layer that has adapters takes tokens without numbers as tokens of no adapter."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer_again", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    layer = ex.ExpertLayer(128, 192, 8, 2, adapters=3, rank=8)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(50, 128, generator=g, device="cuda").bfloat16()
+    out, _ = layer.forward(x)
+    same, _ = layer.forward(x, torch.full((50,), -1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(out, same)
+
+
 # ------------------------------------------------------------------ gradients
 
 @pytest.mark.parametrize("k_contig", [True, False])
