@@ -225,6 +225,49 @@ def test_adapter_gradients(m, sizes, rank):
         assert dx[r, i] == (dout[r].double() @ step).to(t)
 
 
+@pytest.mark.parametrize("sizes", [[5, 0, 40, 1], [130, 300, 0, 77]], ids=["few", "many"])
+def test_adapter_gradients_by_differences(m, sizes):
+    """f = sum(out * dout) moves by the gradients to x, A and B when one of their values moves by 1: f is linear in
+    each.  With -1, 0 and 1 for all values, 8 of them in a sum and scales of 2, u is at most 9, what is added to base
+    at most 2 * 8 * 9 (after the move), and out at most 145, which bf16 holds: all of it is exact."""
+    t, n, k, rank, groups, rows = torch.bfloat16, 72, 8, 8, len(sizes), sum(sizes)
+    x, dout, base = (_ints(i, rows, c, dtype=t, most=1) for i, c in ((1, k), (2, n), (3, n)))
+    a, b = _ints(4, groups, rank, k, dtype=t, most=1), _ints(5, groups, n, rank, dtype=t, most=1)
+    scales = torch.full((groups,), 2.0, device="cuda")
+    offsets, at = _offsets(sizes), np.concatenate([[0], np.cumsum(sizes)])
+    scaled = dout * 2
+    u, du, dx = (torch.empty(rows, c, dtype=t, device="cuda") for c in (rank, rank, k))
+    da, db = torch.empty_like(a), torch.empty_like(b)
+    m.GroupedGemm(groups, rank, k).run(x, a, offsets, u)
+    m.GroupedGemm(groups, rank, n, b_layout=m.GEMM_MN_CONTIG).run(scaled, b, offsets, du)
+    m.GroupedGemm(groups, k, rank, b_layout=m.GEMM_MN_CONTIG).run(du, a, offsets, dx)
+    m.GroupedGemmK(groups, rank, k).run(du, x, offsets, da)
+    m.GroupedGemmK(groups, n, rank).run(scaled, u, offsets, db)
+    forward = m.Adapters(groups, n, k, rank)
+
+    def f(x, a, b):
+        out = torch.empty_like(base)
+        forward.run(x, a, b, offsets, None, base, out, scales=scales)
+        return (out.double() * dout.double()).sum()
+
+    def rounded(v):  # (the gradients are rounded once; their products' sums are whole numbers, which fp32 holds)
+        return v.to(t)
+    was = f(x, a, b)
+    for r in (0, rows // 2, rows - 1):
+        moved = x.clone()
+        moved[r, r % k] += 1
+        assert rounded(f(moved, a, b) - was) == dx[r, r % k]
+    for g in range(groups):
+        for i, j in ((0, 0), (3, 5), (rank - 1, k - 1)):
+            moved = a.clone()
+            moved[g, i, j] += 1
+            assert rounded(f(x, moved, b) - was) == da[g, i, j], (g, i, j)
+        for i, j in ((0, 0), (37, 2), (n - 1, rank - 1)):
+            moved = b.clone()
+            moved[g, i, j] += 1
+            assert rounded(f(x, a, moved) - was) == db[g, i, j], (g, i, j)
+
+
 # ------------------------------------------------------------------ graphs, streams, repeats
 
 @pytest.mark.parametrize("kind", ["rows", "wide rows", "sums", "adapters", "adapters gathered", "adapters, two CTAs"])
