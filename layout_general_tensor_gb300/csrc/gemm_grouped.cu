@@ -60,6 +60,7 @@
 #include <new>
 
 #include "gemm_grouped.h"
+#include "group_tiles.h"
 #include "groups.cuh"
 #include "half_types.cuh"
 #include "kernels.h"
@@ -91,7 +92,6 @@ constexpr uint32_t kGgMost = 256;                       // N-side columns of a t
 constexpr uint32_t kGgPiece = 32;
 constexpr int64_t kGgNarrowMean = 4;
 constexpr int64_t kGgWideMean = 512;
-constexpr uint32_t kGgBand = 8;                         // tiles of the N side
 constexpr uint32_t kGgMaxStages = 12;
 constexpr uint32_t kGgEpiBytes = 2 * 2 * 8192;          // 32 rows of C, 128 values each, of two sets of warps, twice
 constexpr uint32_t kGgStep = 16 * 128;                  // a step's 16 rows of 64 values along n or m
@@ -122,7 +122,7 @@ struct GroupedArgs {
   int32_t p_whole, q_whole;   // the one copy is of several stretches
   uint32_t q_step;            // along K: what a tile's columns are a multiple of, a power of two
   uint32_t lg_most;           // along M: of q_most
-  uint32_t recip[kGgBand + 1];  // 2^32 / d, rounded up
+  uint32_t recip[kGgBand + 1];  // band_reciprocals
   uint32_t stages, stage_bytes;
   uint32_t split;  // CTAs that share a tile's K (SPLIT)
   int32_t p_mn;
@@ -168,20 +168,6 @@ struct GroupedWork {
       step_r = step - step_g * all;
     }
   }
-  // (n / d for d up to kGgBand and n below 2^29)
-  __device__ static uint32_t few(const GroupedArgs& a, uint32_t n, uint32_t d) { return d == 1 ? n : __umulhi(n, a.recip[d]); }
-  // Tile r of a group's p_tiles x q_tiles: in bands of the N side, so that those that
-  // run at once read no more of either operand than they have to.
-  __device__ static void place(const GroupedArgs& a, uint32_t r, uint32_t q_tiles, uint32_t& p, uint32_t& q) {
-    uint32_t band = 0, high = q_tiles;
-    if (q_tiles > kGgBand) {
-      band = r / (a.p_tiles * kGgBand);
-      r -= band * (a.p_tiles * kGgBand);
-      high = min(kGgBand, q_tiles - band * kGgBand);
-    }
-    p = few(a, r, high);
-    q = band * kGgBand + r - p * high;
-  }
   // (Every role asks for every tile, and short tiles take little longer than this did
   // with divisions: 1001 rows of 40 groups along K, 57.5 to 50.1 us.  There is one left
   // where a group has more than a band.)
@@ -192,7 +178,7 @@ struct GroupedWork {
     tile += step;
     if (a.along_k) {
       uint32_t p, q;
-      place(a, r, a.q_tiles, p, q);
+      tile_in_bands(a.recip, r, a.p_tiles, a.q_tiles, p, q);
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
       const uint32_t q0 = q * a.q_width, len = off[g + 1] - off[g];
@@ -211,10 +197,9 @@ struct GroupedWork {
     } else {
       const uint32_t g = group_of(first, a.groups, u);
       const uint32_t len = off[g + 1] - off[g], tiles = (len + a.q_most - 1) >> a.lg_most;
-      const uint32_t each = tiles <= kGgBand ? few(a, len + tiles - 1, tiles) : (len + tiles - 1) / tiles;
-      const uint32_t width = (each + STEP - 1) / STEP * STEP;
+      const uint32_t width = even_width(a.recip, len, tiles, STEP);
       uint32_t p, q;
-      place(a, u - first[g], tiles, p, q);
+      tile_in_bands(a.recip, u - first[g], a.p_tiles, tiles, p, q);
       t.group = static_cast<int32_t>(g);
       t.p0 = static_cast<int32_t>(p * kGgRows * GroupedCfg<PAIR>::CTAS);
       t.q0 = static_cast<int32_t>(off[g] + q * width);
@@ -819,7 +804,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   if (dev != plan->device) return GEMM_ERR_INVALID_ARG;  // (the status word is there)
 
   GroupedArgs a = {};
-  for (uint32_t i = 2; i <= kGgBand; ++i) a.recip[i] = static_cast<uint32_t>(((uint64_t{1} << 32) + i - 1) / i);
+  band_reciprocals(a.recip);
   const int64_t busy = std::min<int64_t>(d.groups, std::max<int64_t>(rows, 1));
   const int64_t mean = (rows + busy - 1) / busy;
   // Few rows a group: tiles as wide as twice the mean, so that most groups have one, and
