@@ -43,7 +43,6 @@ namespace {
 constexpr int kAdWarps = 8;
 constexpr int kAdThreads = kAdWarps * 32;
 constexpr int kAdMaxGroups = 1024;
-constexpr uint32_t kAdMaxCluster = 8;
 
 struct AdapterArgs {
   const uint16_t *x, *a, *b, *base;
@@ -1264,7 +1263,6 @@ gemm_status_t gemm_adapters_run(gemm_adapters_plan_t* plan, const void* x, int64
       height = h;
     }
   }
-  if (lg >= 0) a.ctas = 1;
   cudaError_t e;
   if (lg >= 0) {
     AdapterTcArgs t;

@@ -27,7 +27,7 @@
 // CTAs or pairs: no launch depends on a size.  Within a group the tiles of one
 // stretch of n follow each other, so that they read its weights together, in bands of
 // eight of them, so that those that run at once have no more of the rows between them
-// than the L2 holds (16384 rows of one group, 4096 x 4096: 391 us without, 341).  (Groups
+// than the L2 holds (16384 rows of one group, 4096 x 4096: 391 us without, 335).  (Groups
 // with the largest tiles first would leave small ones for the last round, but
 // few rows and many weights then meet at the end: 4000 rows of 24 groups, 3000 x
 // 2880, 85 to 88 us, and 16384 rows of 16 groups no better.)
@@ -114,7 +114,8 @@ struct GroupedArgs {
   int32_t along_k;
   int32_t n, m;           // extent of the M side; of the N side (along K)
   int32_t kb_total;       // blocks of K (along M)
-  uint32_t p_tiles, q_most;
+  uint32_t p_tiles;
+  uint32_t q_most;            // along M: rows of a tile at most
   uint32_t q_tiles, q_width;  // along K
   uint32_t q_box;             // columns of an N-side copy
   uint32_t q_chunks;          // along K: stretches of 64 columns, of each CTA
@@ -842,7 +843,6 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t* plan, const void* A, int64_t
   if (along_k) {
     a.q_tiles = static_cast<uint32_t>((d.M + kGgMost - 1) / kGgMost);
     a.q_width = static_cast<uint32_t>(up((d.M + a.q_tiles - 1) / a.q_tiles, a.q_step));
-    a.q_most = a.q_width;
     a.q_chunks = (a.q_width / ctas + 63) / 64;
     if (!q_whole) a.q_boxes = a.q_chunks;
     a.q_box = 64;
