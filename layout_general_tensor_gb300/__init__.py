@@ -839,7 +839,8 @@ class Adapters:
     order from row_groups over the rows' adapter numbers; without order (None) the rows of a group follow each
     other.  The gradients are products over the same groups: with rows in order and dout scaled, du = GroupedGemm of
     dout and B (GEMM_MN_CONTIG), dx of du and A (likewise), dA = GroupedGemmK of du and x, dB of dout and u, which is
-    GroupedGemm of x and A.  Rows of x, base and out may be strided; the tensors of a call are on the current device, the one the
+    GroupedGemm of x and A.  There u and du are rounded to the type, once and without the power of two that a row has in
+    here: less exact than this pass, and for fp16 both have to be within its range.  Rows of x, base and out may be strided; the tensors of a call are on the current device, the one the
     object was made on.  A graph needs the object that it was captured from (its status word)."""
 
     def __init__(self, groups, N, K, rank, dtype=GEMM_BF16):

@@ -6,8 +6,8 @@
 // product's result u on the chip: no workspace, one launch.  Many rows come near
 // that (16384 rows, K = N = 4096, rank 64: 76 us, 80 % of a copy's rate).  Few are a
 // chain of trips to memory, one after the other: offsets, order, rows, the joins of
-// u, results (one row 5.8 us, 60 rows of 60 adapters 8.0, 801 rows of 13 and 198 of
-// none, 3000 x 2880, 10.2).
+// u, results (one row 5.8 us, 60 rows of 60 adapters 8.1, 801 rows of 13 and 198 of
+// none, 3000 x 2880, 10.5).
 //
 // For few rows (for many: adapters_tc_kernel below) a tile is up to 8 NT rows of one
 // group, done by a cluster of 1 to 8 CTAs:

@@ -15,12 +15,12 @@
 // 1922 TFLOP/s, 1708 for long): with many rows a group the tensor pipe, and in runs
 // of many such products the power limit (16384 rows of 16 groups, 4096 x 4096:
 // 302 to 316 us alone, 1740 to 1820 TFLOP/s, pipe busy for 92 % of the time; 365 one after the
-// other; along K, 2048 x 4096: 161 and 185); with few rows the weights' bytes (512
+// other; along K, 2048 x 4096: 164 and 181); with few rows the weights' bytes (512
 // rows of 128 groups, 1536 x 2048: 114 us, 97 % of the copy's rate; 8 rows of 8
 // groups, 2048 x 4096: 20 us, of which 4 are its ends), along K with few rows
-// the results' way out of tensor memory (1001 rows of 40 groups, 1000 x 2880: 50 us; 23
-// without any results, 45 without copies to C, which alone would take 37); between the two,
-// rounds of tiles (4000 rows of 24 groups, 3000 x 2880: 86 us, 68 by its bytes).
+// the results' way out of tensor memory (1001 rows of 40 groups, 1000 x 2880: 52 us, of
+// which 2 are the release of cleared rows to a pair; 23 without any results, 45 without
+// copies to C, which alone would take 37); between the two, rounds of tiles (4000 rows of 24 groups, 3000 x 2880: 86 us, 68 by its bytes).
 //
 // Work.  The sizes are on the device, so every CTA sums them up itself (a scan
 // over the groups' tiles in shared memory) and takes every G-th tile, G the
