@@ -17,7 +17,8 @@
  * row's largest finite one and cannot overflow, with the scale neither; one rounding
  * of out.  An infinite value of x, A or B gives the infinity, or the NaN, that the
  * formula gives.  A row reaches no other row's result, whatever it holds.  Repeated
- * calls give the same bits.
+ * calls give the same bits; with another number of rows, or an order where there was
+ * none, K may be summed in other parts.
  *
  * Errors are status codes (gemm_status_t); nothing aborts or prints.
  */

@@ -15,7 +15,8 @@
  *
  * fp16 or bf16, all of one type; sums in fp32, one rounding of the result.  A
  * row or value of another group, or behind the last, reaches no result,
- * infinities and NaN included.  Repeated calls give the same bits.
+ * infinities and NaN included.  Repeated calls give the same bits; with another number
+ * of rows or groups K may be summed in parts, and so in another order.
  *
  * Errors are status codes (gemm_status_t); nothing aborts or prints.
  */

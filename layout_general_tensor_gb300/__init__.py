@@ -749,8 +749,8 @@ def row_groups(ids, offsets, order, places=None, stream=None):
     st = _binding.row_groups(ids, offsets, order, places, stream)
     if st:
         n, int32 = len(ids), _torch.int32
-        if st == -1 and len(offsets) < 2:
-            raise ValueError("gemm_row_groups: offsets holds groups + 1 values")
+        if st == -1 and not 2 <= len(offsets) <= 1025:
+            raise ValueError("gemm_row_groups: offsets holds groups + 1 values, for 1 to 1024 groups")
         _refuse("gemm_row_groups", st, ("ids", ids, (n,), int32, False), ("offsets", offsets, (len(offsets),), int32, False),
                 ("order", order, (n,), int32, False), *((("places", places, (n,), int32, False),) if places is not None else ()))
 

@@ -286,3 +286,10 @@ def test_reciprocals_of_a_band_divide_exactly():
         for near in list(range(0, 4096)) + [k * d for k in range(1 << 10, 1 << 26, 65537)] + [(1 << 29) - 1, (1 << 29) // d * d - 1]:
             for n in (near, max(near - 1, 0), near + 1 if near + 1 < 1 << 29 else near):
                 assert n * m >> 32 == n // d
+
+
+@pytest.mark.parametrize("values", [0, 1, 1026, 5000])
+def test_a_number_of_groups_that_is_refused_is_named(lib, values):
+    ids = torch.zeros(5, dtype=torch.int32)
+    with pytest.raises(ValueError, match="1 to 1024 groups"):
+        lib.row_groups(ids, torch.zeros(values, dtype=torch.int32), ids.clone())
