@@ -20,7 +20,8 @@
 // groups, 2048 x 4096: 20 us, of which 4 are its ends), along K with few rows
 // the results' way out of tensor memory (1001 rows of 40 groups, 1000 x 2880: 52 us, of
 // which 2 are the release of cleared rows to a pair; 23 without any results, 45 without
-// copies to C, which alone would take 37); between the two, rounds of tiles (4000 rows of 24 groups, 3000 x 2880: 86 us, 68 by its bytes).
+// copies to C, which alone would take 37); between the two, rounds of tiles (4000 rows of
+// 24 groups, 3000 x 2880: 86 us, 68 by its bytes).
 //
 // Work.  The sizes are on the device, so every CTA sums them up itself (a scan
 // over the groups' tiles in shared memory) and takes every G-th tile, G the
